@@ -22,6 +22,8 @@ __all__ = [
     "block_q8_matmul_nt", "ternary_bitplane_gemv", "quantize_q8_0", "q1s32_q8_gemm", "q1s32_f32_gemm",
     "matvec_q8", "matmul_q8", "matmul_q8_mma", "wq_mma_workspace_bytes", "matvec_q4g128", "matmul_q4g128",
     "matmul_q4g128_mma", "q1s32_f32_gemm_mma", "q1s32_mma_workspace_bytes",
+    "rmsnorm", "rmsnorm_q8_0", "dequantize_q8_0", "rope_table", "KVCacheQ8_0", "kv_cache_bytes", "rope_kv_append",
+    "kv_read", "attn_q8_0", "attn_workspace", "attn_workspace_bytes",
     "device_error", "version", "PROBE_KINDS", "probe_fill", "probe_read", "probe_issue", "probe_mma",
 ]
 
@@ -51,6 +53,7 @@ def lib():
             raise GQError(f"libgq.so is not built ({path}); run __graft_entry__.build()")
         L = ctypes.CDLL(path)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        LL, F, D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
         sig = {
             "gq_version": (ctypes.c_char_p, []),
             "gq_status_string": (ctypes.c_char_p, [I]),
@@ -81,6 +84,14 @@ def lib():
             "ternary_bitplane_gemv": (I, [P, P, P, P, I, I, I, P]),
             "gq_quantize_q8_0": (I, [P, I, I, P, P, P, P]),
             "q1s32_q8_gemm": (I, [P, P, P, P, P, P, I, I, I, I, P]),
+            "gq_rmsnorm": (I, [P, LL, P, LL, P, F, I, I, I, P, P, P, P, P, P, P]),
+            "gq_dequantize_q8_0": (I, [P, LL, I, P, P]),
+            "gq_kv_cache_bytes": (S, [I, I, I, I]),
+            "gq_rope_table": (I, [P, I, I, D, I, D, D, P]),
+            "gq_rope_kv_append": (I, [P, LL, P, LL, P, LL, P, LL, I, P, I, I, I, P, P, I, I, I, I, P, I, I, P]),
+            "gq_kv_read": (I, [P, I, I, I, I, P, I, I, P, P, P]),
+            "gq_attn_workspace_bytes": (S, [I, I, I, I, I, I]),
+            "gq_attn_q8_0": (I, [P, LL, P, LL, I, P, I, I, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P]),
             "gq_probe_sm_count": (I, []),
             "gq_probe_fill": (I, [P, S, ctypes.c_uint32, P]),
             "gq_probe_read": (I, [P, S, P, I, I, P]),
@@ -471,6 +482,242 @@ def q1s32_q8_gemm(signs: torch.Tensor, wscale: torch.Tensor, xd: torch.Tensor, x
     _check(lib().q1s32_q8_gemm(_ptr(signs), _ptr(wscale), _ptr(xd), _ptr(xq), _ptr(xq_mma), _ptr(y), M, N, K,
                                path, _stream()), "q1s32_q8_gemm")
     return y
+
+
+# ----------------------------------------------------------------------------- between a layer's products
+
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GQError(f"{name}: expected a CUDA tensor")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise GQError(f"{name}: expected float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor, code: int, m: int, k: int, name: str) -> int:
+    """Checks a [m, k] tensor of the call's type with contiguous rows; the distance between rows."""
+    if _type(t, name) != code:
+        raise GQError(f"{name}: expected the type of the call's input, got {t.dtype}")
+    if t.shape != (m, k) or (k > 1 and t.stride(1) != 1):
+        raise GQError(f"{name}: expected [{m}, {k}] with contiguous rows")
+    return t.stride(0) if m > 1 else k
+
+
+def _heads(t: torch.Tensor, code: int, n: int, heads: int, hd: int, name: str) -> int:
+    """Checks a [n, heads, hd] tensor whose heads are contiguous within a token; the distance between tokens."""
+    if _type(t, name) != code:
+        raise GQError(f"{name}: expected the type of the call's input, got {t.dtype}")
+    if t.shape != (n, heads, hd) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd):
+        raise GQError(f"{name}: expected [{n}, {heads}, {hd}] with a token's heads contiguous")
+    return t.stride(0) if n > 1 else heads * hd
+
+
+def _rmsnorm(x, weight, eps, residual, sum_out, y, act, d, q, op):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise GQError("x: expected a CUDA tensor [m, k]")
+    m, k = x.shape
+    code = _type(x, "x")
+    xs = _rows(x, code, m, k, "x")
+    rs = _rows(residual, code, m, k, "residual") if residual is not None else 0
+    _need(weight, torch.float32, k, "weight")
+    if sum_out is not None:
+        _need(sum_out, x.dtype, m * k, "sum_out")
+    _check(lib().gq_rmsnorm(_ptr(x), xs, _ptr(residual), rs, _ptr(weight), eps, code, m, k, _ptr(sum_out), _ptr(y),
+                            _ptr(act), _ptr(d), _ptr(q), _ptr(op), _stream()), "gq_rmsnorm")
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, sum_out: torch.Tensor | None = None):
+    """y = h * weight / sqrt(mean(h^2) + eps) of x's type, h = x + residual, x [m, k] f32, f16 or bf16 with
+    contiguous rows, weight [k] f32.  h goes to sum_out if given (it may be x or residual)."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _need(y, x.dtype, x.numel(), "out")
+    _rmsnorm(x, weight, eps, residual, sum_out, y, None, None, None, None)
+    return y
+
+
+def rmsnorm_q8_0(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+                 split: bool = False, mma_operand: bool = False, out=None, sum_out: torch.Tensor | None = None):
+    """rmsnorm with its output in Q8_0: blocks (uint8, m * k/32 * 34 bytes) as q1_q8_gemv and q1_q8_gemm take
+    them, or with split=True (d [m, k/32] int16, q [m, k] int8, operand [3, m, k] int16 or None) as
+    quantize_q8_0 gives them; `out` reuses buffers of those shapes."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] % 32:
+        raise GQError("rmsnorm_q8_0: expected x [m, k] with k a multiple of 32")
+    m, k = x.shape
+    if not split:
+        act = torch.empty(m * (k // 32) * 34, dtype=torch.uint8, device=x.device) if out is None else out
+        _need(act, torch.uint8, m * (k // 32) * 34, "out")
+        _rmsnorm(x, weight, eps, residual, sum_out, None, act, None, None, None)
+        return act
+    if out is None:
+        d = torch.empty((m, k // 32), dtype=torch.int16, device=x.device)
+        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+        op = torch.empty((3, m, k), dtype=torch.int16, device=x.device) if mma_operand else None
+    else:
+        d, q, op = out
+    _need(d, torch.int16, m * (k // 32), "d")
+    _need(q, torch.int8, m * k, "q")
+    if mma_operand:
+        _need(op, torch.int16, 3 * m * k, "op")
+    else:
+        op = None
+    _rmsnorm(x, weight, eps, residual, sum_out, None, None, d, q, op)
+    return d, q, op
+
+
+def dequantize_q8_0(act: torch.Tensor, m: int, k: int, dtype=torch.float32, out: torch.Tensor | None = None):
+    """The values of m * k/32 Q8_0 blocks (uint8, 34 bytes each) as [m, k] f32, f16 or bf16."""
+    if m < 1 or k < 32 or k % 32:
+        raise GQError("dequantize_q8_0: expected m >= 1 and k a positive multiple of 32")
+    _need(act, torch.uint8, m * (k // 32) * 34, "act")
+    y = torch.empty((m, k), dtype=dtype, device=act.device) if out is None else out
+    code = _type(y, "out")
+    _need(y, y.dtype, m * k, "out")
+    _check(lib().gq_dequantize_q8_0(_ptr(act), m * (k // 32), code, _ptr(y), _stream()), "gq_dequantize_q8_0")
+    return y
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               original: float = 0.0, device="cuda"):
+    """cos and sin of the rotary angles, [positions, rot/2, 2] f32, formed in 64 bits.  scaling: "plain", "linear",
+    "ntk" or "yarn" (which takes the `original` context length)."""
+    if scaling not in ROPE_SCALING:
+        raise GQError(f"rope_table: unknown scaling {scaling!r}")
+    t = torch.empty((max(positions, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
+    _check(lib().gq_rope_table(_ptr(t), positions, rot, base, ROPE_SCALING[scaling], factor, original, _stream()),
+           "gq_rope_table")
+    return t
+
+
+def kv_cache_bytes(pages: int, page_size: int, kv_heads: int, head_dim: int) -> int:
+    return lib().gq_kv_cache_bytes(pages, page_size, kv_heads, head_dim)
+
+
+class KVCacheQ8_0:
+    """A paged key/value cache in Q8_0 (layout: gq_kv_cache_bytes in include/gq.h).  `data`: a uint8 CUDA
+    tensor of kv_cache_bytes(...) bytes, allocated here when None."""
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, data: torch.Tensor | None = None,
+                 device="cuda"):
+        nbytes = kv_cache_bytes(pages, page_size, kv_heads, head_dim)
+        if nbytes == 0:
+            raise GQError("KVCacheQ8_0: invalid shape")
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _need(data, torch.uint8, nbytes, "data")
+        self.data, self.pages, self.page_size, self.kv_heads, self.head_dim = data, pages, page_size, kv_heads, head_dim
+
+
+def rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KVCacheQ8_0, slots: torch.Tensor,
+                   rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None):
+    """Turns q and k by rows `positions` (int32 [n]) of `rope` ([rows, rot/2, 2] f32; None: no rotation), and writes k and
+    v to `slots` (int64 [n], negative: skipped) of the cache.  q [n, q_heads, hd] (or None), k, v [n, kv_heads, hd];
+    views of one fused row serve.  Returns the turned q (q_out, which may be q)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise GQError("k: expected a CUDA tensor [n, kv_heads, head_dim]")
+    n, hkv, hd = k.shape
+    if (hkv, hd) != (cache.kv_heads, cache.head_dim):
+        raise GQError(f"k: expected {cache.kv_heads} heads of {cache.head_dim}")
+    code = _type(k, "k")
+    ks, vs = _heads(k, code, n, hkv, hd, "k"), _heads(v, code, n, hkv, hd, "v")
+    hq = qs = qos = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise GQError("q: expected a CUDA tensor [n, q_heads, head_dim]")
+        hq = q.shape[1]
+        qs = _heads(q, code, n, hq, hd, "q")
+        if q_out is None:
+            q_out = torch.empty((n, hq, hd), dtype=q.dtype, device=q.device)
+        qos = _heads(q_out, code, n, hq, hd, "q_out")
+    rows = rot = 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise GQError("rope: expected [rows, rot/2, 2]")
+        rows, rot = rope.shape[0], 2 * rope.shape[1]
+        _need(rope, torch.float32, rows * rot, "rope")
+        _need(positions, torch.int32, n, "positions")
+    _need(slots, torch.int64, n, "slots")
+    _check(lib().gq_rope_kv_append(_ptr(q), qs, _ptr(q_out if q is not None else None), qos, _ptr(k), ks, _ptr(v), vs, code,
+                                   _ptr(rope), rows, rot, 1 if interleaved else 0,
+                                   _ptr(positions if rope is not None else None), _ptr(slots), n, hq, hkv, hd,
+                                   _ptr(cache.data), cache.pages, cache.page_size, _stream()), "gq_rope_kv_append")
+    return q_out if q is not None else None
+
+
+def kv_read(cache: KVCacheQ8_0, slots: torch.Tensor, dtype=torch.float32, k_out: torch.Tensor | None = None,
+            v_out: torch.Tensor | None = None):
+    """(k, v) [n, kv_heads, head_dim]: the values of `slots` (int64 [n]; a negative one gives zeros)."""
+    n = slots.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=slots.device) if k_out is None else k_out
+    v = torch.empty(shape, dtype=k.dtype, device=slots.device) if v_out is None else v_out
+    code = _type(k, "k_out")
+    _need(slots, torch.int64, n, "slots")
+    _need(k, k.dtype, n * cache.kv_heads * cache.head_dim, "k_out")
+    _need(v, k.dtype, n * cache.kv_heads * cache.head_dim, "v_out")
+    _check(lib().gq_kv_read(_ptr(cache.data), cache.pages, cache.page_size, cache.kv_heads, cache.head_dim, _ptr(slots), n,
+                            code, _ptr(k), _ptr(v), _stream()), "gq_kv_read")
+    return k, v
+
+
+def attn_workspace_bytes(cache: KVCacheQ8_0, q_heads: int, seqs: int, max_q: int, dtype=torch.float32) -> int:
+    """Bytes of the workspace attn_q8_0 needs (0: invalid shape)."""
+    return lib().gq_attn_workspace_bytes(seqs, max_q, q_heads, cache.kv_heads, cache.head_dim, _TYPES.get(dtype, -1))
+
+
+def attn_workspace(cache: KVCacheQ8_0, q_heads: int, seqs: int, max_q: int, dtype=torch.float32) -> torch.Tensor:
+    """A workspace for attn_q8_0, to be kept between calls (calls sharing it must not overlap)."""
+    need = attn_workspace_bytes(cache, q_heads, seqs, max_q, dtype)
+    if need == 0:
+        raise GQError("attn_workspace: invalid shape")
+    return torch.empty(need, dtype=torch.uint8, device=cache.data.device)
+
+
+def attn_q8_0(q: torch.Tensor, cache: KVCacheQ8_0, block_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor,
+              max_q: int, max_kv: int, scale: float | None = None, softcap: float = 0.0,
+              tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Attention of each sequence's newest tokens (rows q_start[b]..q_start[b + 1] of q [n, q_heads, head_dim]) over its
+    kv_len[b] cached ones, themselves included; block_table [seqs, pages a sequence] int32, kv_len [seqs] and
+    q_start [seqs + 1] int32.  Among the newest tokens the mask is causal, or tree_mask[row] (int64, bit j: newest
+    token j is seen).  scale: 1 / sqrt(head_dim) when None; softcap > 0 caps the scores."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise GQError("q: expected a CUDA tensor [n, q_heads, head_dim]")
+    n, hq, hd = q.shape
+    if hd != cache.head_dim:
+        raise GQError(f"q: expected heads of {cache.head_dim}")
+    code = _type(q, "q")
+    qs = _heads(q, code, n, hq, hd, "q")
+    o = torch.empty((n, hq, hd), dtype=q.dtype, device=q.device) if out is None else out
+    os_ = _heads(o, code, n, hq, hd, "out")
+    seqs = kv_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != seqs:
+        raise GQError(f"block_table: expected [{seqs}, pages]")
+    _need(block_table, torch.int32, block_table.numel(), "block_table")
+    _need(kv_len, torch.int32, seqs, "kv_len")
+    _need(q_start, torch.int32, seqs + 1, "q_start")
+    if tree_mask is not None:
+        _need(tree_mask, torch.int64, n, "tree_mask")
+    if n == 0:
+        return o
+    need = attn_workspace_bytes(cache, hq, seqs, max_q, q.dtype)
+    if need == 0:
+        raise GQError("attn_q8_0: invalid shape")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, workspace.numel(), "workspace")
+    if workspace.numel() < need:
+        raise GQError(f"attn_q8_0: workspace holds {workspace.numel()} bytes, needs {need}")
+    _check(lib().gq_attn_q8_0(_ptr(q), qs, _ptr(o), os_, code, _ptr(cache.data), cache.pages, cache.page_size,
+                              _ptr(block_table), block_table.shape[1], _ptr(kv_len), _ptr(q_start), _ptr(tree_mask), seqs,
+                              max_q, max_kv, hq, cache.kv_heads, hd, hd ** -0.5 if scale is None else scale, softcap,
+                              _ptr(workspace), _stream()), "gq_attn_q8_0")
+    return o
 
 
 # ----------------------------------------------------------------------------- roofline probes

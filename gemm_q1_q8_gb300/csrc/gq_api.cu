@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "gq_internal.cuh"
+#include "layer_ops.cuh"
 #include "wq_mma.cuh"
 #include "w1a32_mma.cuh"
 
@@ -56,7 +57,7 @@ int gq_device_error(void) {
     if (e != cudaSuccess) return cuda_status(e) == GQ_OK ? 0 : -1;
     const unsigned v = gq::error_read_clear_q1() | gq::error_read_clear_q1_gemv() | gq::error_read_clear_ternary() | gq::error_read_clear_prefill_mma() |
                        gq::error_read_clear_wq_mma() | gq::error_read_clear_w1a32() | gq::error_read_clear_probes() |
-                       gq::error_read_clear_block_q8();
+                       gq::error_read_clear_block_q8() | gq::error_read_clear_kv() | gq::error_read_clear_attn();
     return v == ~0u ? -1 : static_cast<int>(v);
 }
 
@@ -259,6 +260,121 @@ int q1s32_q8_gemm(const uint32_t* signs, const float* wscale, const uint16_t* xd
         return cuda_status(e);
     }
     return cuda_status(gq::launch_prefill_lut4(signs, wscale, xd, xq, y, M, N, K, s));
+}
+
+// ---------------------------------------------------------------- between a layer's products
+
+static size_t type_bytes(int type) { return type == GQ_F32 ? 4 : type == GQ_F16 || type == GQ_BF16 ? 2 : 0; }
+
+static bool cache_shape(int pages, int page_size, int kv_heads, int head_dim) {
+    return pages >= 1 && page_size >= 16 && page_size <= 65536 && page_size % 16 == 0 && kv_heads >= 1 && kv_heads <= 1024 &&
+           (head_dim == 64 || head_dim == 128 || head_dim == 256) && static_cast<long long>(pages) * page_size < (1ll << 40);
+}
+
+int gq_rmsnorm(const void* x, long long x_stride, const void* residual, long long residual_stride, const float* weight,
+               float eps, int type, int m, int k, void* sum, void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op,
+               gq_stream_t stream) {
+    if (m < 1 || k < 1 || k > kMaxK || x_stride < k || (residual && residual_stride < k) || !(eps >= 0.0f))
+        return GQ_EINVAL_SHAPE;
+    if ((act || d || q || op) && k % 32 != 0) return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!b) return GQ_EUNSUPPORTED;
+    if (!x || !weight || (!sum && !y && !act && !d && !q && !op) || !d != !q || (op && !q)) return GQ_EINVAL_PTR;
+    if (!aligned(x, b) || !aligned(residual, b) || !aligned(weight, 4) || !aligned(sum, b) || !aligned(y, b) ||
+        !aligned(act, 2) || !aligned(d, 2) || !aligned(q, 16) || !aligned(op, 16))
+        return GQ_EINVAL_PTR;
+    if ((sum == x && sum && x_stride != k) || (sum && sum == residual && residual_stride != k)) return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_rmsnorm(x, x_stride, residual, residual_stride, weight, eps, type, m, k, sum, y, act, d, q,
+                                          op, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gq_dequantize_q8_0(const void* act, long long blocks, int type, void* out, gq_stream_t stream) {
+    if (blocks < 1 || blocks > (1ll << 40)) return GQ_EINVAL_SHAPE;
+    if (!type_bytes(type)) return GQ_EUNSUPPORTED;
+    if (!act || !out || !aligned(act, 2) || !aligned(out, 16)) return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_dequantize_q8_0(act, blocks, type, out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gq_kv_cache_bytes(int pages, int page_size, int kv_heads, int head_dim) {
+    if (!cache_shape(pages, page_size, kv_heads, head_dim)) return 0;
+    return static_cast<size_t>(pages) * (page_size / 16) * kv_heads * gq::kv_chunk_bytes(head_dim);
+}
+
+int gq_rope_table(float* table, int positions, int rot, double base, int scaling, double factor, double original,
+                  gq_stream_t stream) {
+    if (positions < 1 || rot < 8 || rot > 256 || rot % 8 != 0 || !(base > 1.0) || !(factor >= 1.0)) return GQ_EINVAL_SHAPE;
+    if (scaling < GQ_ROPE_PLAIN || scaling > GQ_ROPE_YARN) return GQ_EUNSUPPORTED;
+    if (scaling == GQ_ROPE_YARN && !(original >= 1.0)) return GQ_EINVAL_SHAPE;
+    if (!table || !aligned(table, 8)) return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_rope_table(table, positions, rot, base, scaling, factor, original,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gq_rope_kv_append(const void* q, long long q_stride, void* q_out, long long q_out_stride, const void* k,
+                      long long k_stride, const void* v, long long v_stride, int type, const float* rope, int rope_rows,
+                      int rot, int layout, const int32_t* positions, const int64_t* slots, int tokens, int q_heads,
+                      int kv_heads, int head_dim, void* cache, int pages, int page_size, gq_stream_t stream) {
+    if (tokens < 1 || q_heads < 0 || q_heads > 1024 || !cache_shape(pages, page_size, kv_heads, head_dim)) return GQ_EINVAL_SHAPE;
+    if (!rope) rot = 0;
+    if (rot < 0 || rot > head_dim || rot % 8 != 0 || (rot && rope_rows < 1)) return GQ_EINVAL_SHAPE;
+    const long long qw = static_cast<long long>(q_heads) * head_dim, kw = static_cast<long long>(kv_heads) * head_dim;
+    if ((q_heads && (q_stride < qw || q_out_stride < qw)) || k_stride < kw || v_stride < kw) return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!b || (layout != GQ_ROPE_HALF && layout != GQ_ROPE_INTERLEAVED)) return GQ_EUNSUPPORTED;
+    if ((q_heads && (!q || !q_out)) || !k || !v || !slots || !cache || (rot && !positions)) return GQ_EINVAL_PTR;
+    if (!aligned(k, 4 * b) || !aligned(v, 4 * b) || k_stride % 4 || v_stride % 4 || !aligned(cache, 16) ||
+        !aligned(slots, 8) || (rot && (!aligned(rope, 16) || !aligned(positions, 4))))
+        return GQ_EINVAL_PTR;
+    if (q_heads && (!aligned(q, 4 * b) || !aligned(q_out, 4 * b) || q_stride % 4 || q_out_stride % 4 ||
+                    (q == q_out && q_stride != q_out_stride)))
+        return GQ_EINVAL_PTR;
+    const gq::AppendArgs a = {q, q_out, k, v, q_stride, q_out_stride, k_stride, v_stride, rope, rope_rows, rot,
+                              layout == GQ_ROPE_INTERLEAVED, positions, slots, tokens, q_heads, kv_heads,
+                              static_cast<uint8_t*>(cache), pages, page_size};
+    return cuda_status(gq::launch_kv_append(a, type, head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gq_kv_read(const void* cache, int pages, int page_size, int kv_heads, int head_dim, const int64_t* slots, int n,
+               int type, void* k_out, void* v_out, gq_stream_t stream) {
+    if (n < 1 || !cache_shape(pages, page_size, kv_heads, head_dim)) return GQ_EINVAL_SHAPE;
+    if (!type_bytes(type)) return GQ_EUNSUPPORTED;
+    if (!cache || !slots || (!k_out && !v_out) || !aligned(cache, 16) || !aligned(slots, 8) || !aligned(k_out, 16) ||
+        !aligned(v_out, 16))
+        return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_kv_read(static_cast<const uint8_t*>(cache), pages, page_size, kv_heads, head_dim, slots, n,
+                                          type, k_out, v_out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool attn_shape(int seqs, int max_q, int q_heads, int kv_heads, int head_dim) {
+    return seqs >= 1 && seqs <= 65535 && max_q >= 1 && q_heads >= 1 && kv_heads >= 1 && kv_heads <= 1024 &&
+           q_heads % kv_heads == 0 && q_heads / kv_heads <= 64 && (head_dim == 64 || head_dim == 128 || head_dim == 256);
+}
+
+size_t gq_attn_workspace_bytes(int seqs, int max_q, int q_heads, int kv_heads, int head_dim, int type) {
+    if (!attn_shape(seqs, max_q, q_heads, kv_heads, head_dim) || !type_bytes(type)) return 0;
+    return gq::attn_workspace_bytes(seqs, max_q, q_heads, kv_heads, head_dim, type);
+}
+
+int gq_attn_q8_0(const void* q, long long q_stride, void* out, long long out_stride, int type, const void* cache, int pages,
+                 int page_size, const int32_t* table, int table_stride, const int32_t* kv_len, const int32_t* q_start,
+                 const uint64_t* tree, int seqs, int max_q, int max_kv, int q_heads, int kv_heads, int head_dim, float scale,
+                 float softcap, void* workspace, gq_stream_t stream) {
+    if (!attn_shape(seqs, max_q, q_heads, kv_heads, head_dim) || !cache_shape(pages, page_size, kv_heads, head_dim) ||
+        max_kv < 1 || (tree && max_q > 64))
+        return GQ_EINVAL_SHAPE;
+    const long long w = static_cast<long long>(q_heads) * head_dim;
+    if (q_stride < w || out_stride < w || table_stride < (max_kv - 1) / page_size + 1) return GQ_EINVAL_SHAPE;
+    if (!(scale - scale == 0.0f) || !(softcap >= 0.0f) || !(softcap - softcap == 0.0f)) return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!b) return GQ_EUNSUPPORTED;
+    if (!q || !out || !cache || !table || !kv_len || !q_start || !workspace) return GQ_EINVAL_PTR;
+    if (!aligned(q, 4 * b) || !aligned(out, 4 * b) || q_stride % 4 || out_stride % 4 || !aligned(cache, 16) ||
+        !aligned(workspace, 16) || !aligned(table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(tree, 8))
+        return GQ_EINVAL_PTR;
+    const gq::AttnArgs a = {q, out, q_stride, out_stride, static_cast<const uint8_t*>(cache), pages, page_size, table,
+                            table_stride, kv_len, q_start, tree, seqs, max_q, max_kv, q_heads, kv_heads, scale, softcap,
+                            workspace};
+    return cuda_status(gq::launch_attn(a, type, head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

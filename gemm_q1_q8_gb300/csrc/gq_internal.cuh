@@ -16,6 +16,7 @@ enum DeviceError : unsigned {
     kErrWaitTimeout = 1u,      // an mbarrier wait on the kernel's own copies exceeded ~1 s
     kErrDrainTimeout = 2u,     // after a timeout, in-flight copies did not land within ~1 s
     kErrMmaTimeout = 4u,       // an MMA/epilogue handshake exceeded ~1 s
+    kErrIndex = GQ_DEVERR_INDEX,   // an index read from device memory was out of range
 };
 // Each translation unit with kernels holds its own word (no relocatable device code needed) and
 // exposes it through GQ_ERROR_ACCESSOR(unit): gq_device_error() reads and clears them all.
@@ -37,6 +38,8 @@ unsigned error_read_clear_prefill_mma();
 unsigned error_read_clear_w1a32();
 unsigned error_read_clear_probes();
 unsigned error_read_clear_block_q8();
+unsigned error_read_clear_kv();
+unsigned error_read_clear_attn();
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;

@@ -380,6 +380,140 @@ int q1s32_q8_gemm(const uint32_t* signs_device, const float* wscale_device,
                   gq_stream_t stream);
 
 /* ============================================================================================
+ * Between a layer's products: RMS norm into Q8_0, rotary positions, a paged Q8_0 key/value cache, and
+ * attention over it.  Inputs and outputs are f32, f16 or bf16 (one type per call); every sum, norm,
+ * softmax statistic and rotation is formed in f32 whatever the type, and rounded once on the store.
+ * Kernels whose indices come from device memory check them: an index out of its range is skipped as
+ * stated at the call and sets GQ_DEVERR_INDEX in the device error word (gq_device_error).
+ * ========================================================================================== */
+
+enum gq_dtype { GQ_F32 = 0, GQ_F16 = 1, GQ_BF16 = 2 };
+
+#define GQ_DEVERR_INDEX 8   /* bit of gq_device_error(): an index read from device memory was out of range */
+
+/* RMS norm with the residual's addition, and an output in Q8_0:
+ *   h = x + r (r = 0 if residual_device is NULL), y_i = (h_i * w_i) * (1 / sqrt(sum h^2 / k + eps)).
+ *   x_device [m, k] of `type`, rows x_stride elements apart (x_stride >= k); residual_device NULL or
+ *   [m, k], rows residual_stride apart; weight_device k f32.  Any output may be NULL, not all of them:
+ *     sum_device  [m, k] of `type`, contiguous: h; it may be x_device or residual_device itself if
+ *                 those rows are contiguous (each row is read before it is written);
+ *     y_device    [m, k] of `type`, contiguous;
+ *     act_device  m * k/32 Q8_0 blocks of 34 bytes (2-byte aligned), as the Q1_0 GEMV and GEMM take them;
+ *     d_device, q_device, mma_operand_device: the split form, as gq_quantize_q8_0 writes it (both of
+ *                 d and q or neither; q and the operand 16-byte aligned; the operand only beside them).
+ *   y is quantized in f32, before any rounding to `type`, by the rule stated at gq_quantize_q8_0.  Two
+ *   calls on the same inputs give the same bits.
+ * Errors: GQ_EINVAL_SHAPE if m < 1, k < 1, k > 65536, a stride < k, or a Q8_0 output with k % 32 != 0;
+ *         GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR (elements aligned to their size, weight to 4
+ *         bytes, or no output at all); GQ_ECUDA.  eps must be >= 0 (else GQ_EINVAL_SHAPE). */
+int gq_rmsnorm(const void* x_device, long long x_stride, const void* residual_device, long long residual_stride,
+               const float* weight_device, float eps, int type, int m, int k, void* sum_device, void* y_device,
+               void* act_device, uint16_t* d_device, int8_t* q_device, uint16_t* mma_operand_device,
+               gq_stream_t stream);
+
+/* The values code * d of Q8_0 blocks (34 bytes, 2-byte aligned), `blocks` of them one after another,
+ * as 32 values of `type` each (16-byte aligned).
+ * Errors: GQ_EINVAL_SHAPE unless 1 <= blocks <= 2^40, GQ_EUNSUPPORTED for another type, GQ_EINVAL_PTR, GQ_ECUDA. */
+int gq_dequantize_q8_0(const void* act_device, long long blocks, int type, void* out_device, gq_stream_t stream);
+
+/* The key/value cache: `pages` pages of page_size token slots for kv_heads heads of head_dim; slot s is
+ * place s % page_size of page s / page_size.  Keys and values are Q8_0: per slot, head and 32 dims an
+ * f16 scale d and 32 codes q in [-127, 127] (rule: gq_quantize_q8_0; value = q * d).  A code is stored
+ * as sign bit and 7-bit magnitude.  [page][head][16 slots] is one chunk of 34 * head_dim bytes:
+ *   K codes 16 * hd | V codes 16 * hd | K scales 16 * hd/32 f16 | V scales 16 * hd/32 f16.
+ * With tok the place in the 16, d the dim, t = (tok & 7) >> 1, p = (tok & 1) + 2 * (tok >> 3), byte offsets:
+ *   K code  tok * hd + 16 * u + 4 * ((d >> 4) & 3) + (d & 3), u = 4 * (d >> 6) + ((d >> 2) & 3),
+ *           with bit 2 of u flipped where hd > 64 and tok is odd;
+ *   V code  hd = 64:  (4 p + t) * 64 + 8 * (g ^ (4 * (t >> 1))) + 4 * (d >> 5) + (d & 3),   g = (d >> 2) & 7;
+ *           hd > 64:  (4 p + t) * hd + 128 * (d >> 7) + 16 * (g ^ (2 t)) + 4 * ((d >> 5) & 3) + (d & 3);
+ *   scales  2 * ((4 t + p) * hd/32 + (d >> 5)).
+ * (A warp's 16-byte shared-memory reads of this order give its matrix fragments directly, without bank
+ * conflicts, and a token's codes stay together.)  A slot never written need not be initialised: nothing of it reaches
+ * a result.  kv_heads 1 to 1024, head_dim 64, 128 or 256, page_size a multiple of 16 up to 65536,
+ * pages * page_size < 2^40.  0 for an invalid shape. */
+size_t gq_kv_cache_bytes(int pages, int page_size, int kv_heads, int head_dim);
+
+/* Rotary frequencies scaled for long contexts (gq_rope_table). */
+enum gq_rope_scaling {
+    GQ_ROPE_PLAIN = 0,     /* f_i = base^(-2i/rot)                                                       */
+    GQ_ROPE_LINEAR = 1,    /* f_i / factor                                                               */
+    GQ_ROPE_NTK = 2,       /* base * factor^(rot / (rot - 2)) in the place of base                       */
+    GQ_ROPE_YARN = 3       /* f_i * (r_i + (1 - r_i) / factor) with r_i = 1 - clamp((i - low) / (high - low), 0, 1);
+                              low = floor(c(32)), high = ceil(c(1)), both clamped to [0, rot - 1],
+                              high = low + 0.001 where they are equal,
+                              c(n) = rot * ln(original / (2 pi n)) / (2 ln base); cos and sin are multiplied
+                              by 1 + 0.1 ln(factor)                                                       */
+};
+
+/* cos and sin of every position's rotary angles, formed in 64 bits and rounded to f32 once:
+ *   table_device [positions, rot/2, 2] f32 (8-byte aligned): cos, sin of position * f_i.
+ * Errors: GQ_EINVAL_SHAPE unless positions >= 1, rot is a multiple of 8 in [8, 256], base > 1, factor >= 1 and
+ *         (yarn) original >= 1; GQ_EUNSUPPORTED for another scaling; GQ_EINVAL_PTR; GQ_ECUDA. */
+int gq_rope_table(float* table_device, int positions, int rot, double base, int scaling, double factor,
+                  double original, gq_stream_t stream);
+
+/* Pairs that a rotation turns: element i with i + rot/2 (half), or 2i with 2i + 1 (interleaved). */
+enum gq_rope_layout { GQ_ROPE_HALF = 0, GQ_ROPE_INTERLEAVED = 1 };
+
+/* Rotary positions on the first `rot` dims of every q and k head, and the append of k and v to the cache:
+ *   (a, b) -> (a * cos - b * sin, b * cos + a * sin) for pair i of token n, cos and sin from row
+ *   positions_device[n] of rope_device ([rope_rows, rot/2, 2] f32; NULL or rot = 0: no rotation).
+ *   q_device [tokens, q_heads, head_dim] -> q_out_device of the same shape and `type` (it may be q_device
+ *   itself, with the same stride); both NULL where q_heads = 0.  k_device, v_device [tokens, kv_heads, head_dim];
+ *   heads are contiguous, tokens the given strides (in elements) apart, so that one fused q | k | v row serves.
+ *   slots_device[n] (int64): where token n goes; a negative one is not written.  Two tokens with one slot in
+ *   a call leave either's values.
+ *   A position outside [0, rope_rows) leaves that token's q_out and slot unwritten, a slot >= pages * page_size
+ *   is not written; both set GQ_DEVERR_INDEX.
+ *   k is quantized after the rotation, in f32.
+ * Errors: GQ_EINVAL_SHAPE unless tokens >= 1, q_heads in [0, 1024], a valid cache shape, rot a multiple of 8 in [0, head_dim],
+ *         strides >= the heads' width and rope_rows >= 1 with rot > 0; GQ_EUNSUPPORTED for another type
+ *         or layout; GQ_EINVAL_PTR for NULL pointers, elements or strides not aligned to 4 elements, cache or rope not
+ *         aligned to 16 bytes; GQ_ECUDA. */
+int gq_rope_kv_append(const void* q_device, long long q_stride, void* q_out_device, long long q_out_stride,
+                      const void* k_device, long long k_stride, const void* v_device, long long v_stride, int type,
+                      const float* rope_device, int rope_rows, int rot, int layout, const int32_t* positions_device,
+                      const int64_t* slots_device, int tokens, int q_heads, int kv_heads, int head_dim,
+                      void* cache_device, int pages, int page_size, gq_stream_t stream);
+
+/* Reads slots back: k_out_device, v_out_device [n, kv_heads, head_dim] of `type` (16-byte aligned; either may be
+ * NULL) = code * d.  A negative slot gives zeros; one >= pages * page_size too, and sets GQ_DEVERR_INDEX.
+ * Errors: GQ_EINVAL_SHAPE unless n >= 1 and the cache shape is valid; GQ_EUNSUPPORTED; GQ_EINVAL_PTR; GQ_ECUDA. */
+int gq_kv_read(const void* cache_device, int pages, int page_size, int kv_heads, int head_dim,
+               const int64_t* slots_device, int n, int type, void* k_out_device, void* v_out_device,
+               gq_stream_t stream);
+
+/* Attention of each sequence's newest tokens over its cached ones (themselves included: append first):
+ *   s = scale * (q . k), capped to softcap * tanh(s / softcap) where softcap > 0; o = softmax(s) . v over the
+ *   visible keys, 0 where none is visible.  Query head h reads kv head h / (q_heads / kv_heads).
+ *   Sequence b has kv_len_device[b] cached tokens, token j in place j % page_size of page
+ *   block_table_device[b * table_stride + j / page_size], and T = q_start_device[b + 1] - q_start_device[b] query tokens,
+ *   rows q_start_device[b].. of q_device and out_device ([q_start_device[seqs], q_heads, head_dim] of `type`, tokens
+ *   q_stride / out_stride elements apart).  Query i of them stands at token L - T + i.
+ *   Keys before L - T are visible to every query; of the newest T, key j is visible to query i if
+ *     tree_mask_device is NULL: j <= i (causal);
+ *     else: bit j of tree_mask_device[row of query i] is set (its drafted ancestors and itself; T <= 64).
+ *   T > L is allowed (the first queries then see nothing, and give 0), T = 0 and L = 0 too.
+ *   max_q and max_kv bound T and L of every sequence; a longer T or L, or a page index outside
+ *   [0, pages), sets GQ_DEVERR_INDEX: what is past the bound is not computed or not seen.
+ *   workspace_device: gq_attn_workspace_bytes(...) bytes, 16-byte aligned, overwritten; calls that
+ *   share it must not overlap on the GPU.  Nothing of it is kept between calls.  Results do not depend on
+ *   timing: the same inputs give the same bits.
+ * Precision: f32 queries are split into two f16 parts after a row's scaling by a power of two, so are the softmax's
+ * numerators; codes are exact; sums are in f32.  f16 and bf16 queries take one part (numerators rounded to f16).
+ * Errors: GQ_EINVAL_SHAPE unless 1 <= seqs <= 65535, max_q >= 1, max_kv >= 1, q_heads a multiple of kv_heads with
+ *         q_heads / kv_heads <= 64, a valid cache shape, strides >= q_heads * head_dim, table_stride >=
+ *         ceil(max_kv / page_size), scale finite, softcap >= 0 and finite, and max_q <= 64 with tree_mask_device;
+ *         GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR for NULL pointers, or elements and strides of q and out not
+ *         aligned to 4 elements, cache or workspace not to 16 bytes; GQ_ECUDA. */
+size_t gq_attn_workspace_bytes(int seqs, int max_q, int q_heads, int kv_heads, int head_dim, int type);  /* 0: invalid */
+int gq_attn_q8_0(const void* q_device, long long q_stride, void* out_device, long long out_stride, int type,
+                 const void* cache_device, int pages, int page_size, const int32_t* block_table_device,
+                 int table_stride, const int32_t* kv_len_device, const int32_t* q_start_device,
+                 const uint64_t* tree_mask_device, int seqs, int max_q, int max_kv, int q_heads, int kv_heads,
+                 int head_dim, float scale, float softcap, void* workspace_device, gq_stream_t stream);
+
+/* ============================================================================================
  * Roofline probes (measurement only; no hot-path entry point uses them).  The machine's own
  * ceilings, measured in the same session as the kernels whose fractions are quoted against them:
  * roofline.html's read-only bandwidth method (FILL a buffer with a non-zero pattern, then read it
