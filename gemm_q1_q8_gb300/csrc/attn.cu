@@ -5,11 +5,12 @@
 // The floor is the cache's bytes (17/16 a value) at the HBM rate; a row costs 4 flops a value, so up to some 16 rows
 // a read the matrix work hides behind the copy.
 //
-// Work: the unit is one 16-token chunk of one (sequence, kv head, row tile); the units of the whole call, in that
-// order, are cut into equal runs of consecutive units, one a thread block (one block an SM), whatever the sequences'
-// lengths.  A run's warps take its units in turn, each from its own ring of bulk copies (a chunk is one contiguous
-// copy), so nothing but the end of a row tile meets at a barrier.  A row tile that several blocks share leaves
-// partial sums in the workspace, and a second kernel joins them in block order: the result does not depend on timing.
+// Work: the unit is one 16-token chunk of one (sequence, kv head, row tile); the units of the whole call, in that order, are cut
+// into equal runs of consecutive units, one a warp of every SM, whatever the sequences' lengths.  A warp goes through its run alone: it
+// lays out a tile's queries in shared memory, takes the chunks from its own ring of bulk copies (a chunk is one contiguous copy),
+// which one more warp of the block fills (its lane w for warp w), and writes the tiles that lie in its run.  A tile that runs share leaves
+// partial sums: at the end of its run a warp's open tile meets those of the block's other warps, once; a second kernel joins what is left in
+// the order of the runs, so the result does not depend on timing.
 //
 // Tensor cores: mma.sync m16n8k16 (f32 sums) with the queries as A and 8 keys as B.  Each code is its own exact 16-bit float: sign and
 // 7-bit magnitude are the bits of the f16 subnormal magnitude * 2^-24, and of the bf16 one magnitude * 2^-133, so two codes become a
@@ -28,53 +29,69 @@ namespace gq {
 GQ_ERROR_ACCESSOR(attn)
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kBlocks = 152;                       // one thread block an SM
 constexpr float kNone = -1e30f;                    // running maximum of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int HD> __host__ __device__ constexpr int stages() { return HD == 64 ? 6 : HD == 128 ? 4 : 2; }
-// Rows of a tile, and the columns of it that meet in shared memory at a time (64 KB at most)
-template <int PARTS, int MT> __host__ __device__ constexpr int tile_rows() { return MT * 16 / PARTS; }
-template <int HD, int PARTS, int MT> __host__ __device__ constexpr int merge_cols() {
-    return tile_rows<PARTS, MT>() * HD <= 2048 ? HD : 2048 / tile_rows<PARTS, MT>();
-}
-template <int HD, int PARTS, int MT> constexpr int smem_bytes() {
-    return 1024 + kWarps * stages<HD>() * kv_chunk_bytes(HD) + kWarps * tile_rows<PARTS, MT>() * (merge_cols<HD, PARTS, MT>() + 4) * 4;
-}
+constexpr float kLift = 108.f;                     // f32 weights carry 2^108: times a scale below 2^16 and 2^kSlack they stay in f32's range
+constexpr float kSlack = 2.f;                      // a score may pass the running maximum by this much before it moves: 1.02 (16 bits: 0)
+// Rows of a tile by the parts of its operands: 16-bit queries 1; f32 2, or 3 for up to four rows
+template <int PARTS, int MT> __host__ __device__ constexpr int tile_rows() { return PARTS == 1 ? 16 * MT : PARTS == 2 ? 8 * MT : 4; }
+// Computing warps, by the registers that a warp's sums take, and the chunks of a warp's ring
+template <int HD, int MT> __host__ __device__ constexpr int warps() { return HD * MT <= 64 ? 15 : HD * MT <= 128 ? 11 : 7; }
+template <int HD, int MT> __host__ __device__ constexpr int stages() { return HD == 64 ? 4 : HD == 128 ? (MT == 1 ? 3 : 4) : 2; }
+template <int HD, int MT> __host__ __device__ constexpr int ring_bytes() { return warps<HD, MT>() * stages<HD, MT>() * kv_chunk_bytes(HD); }
+template <int HD, int MT> constexpr int smem_bytes() { return 1024 + ring_bytes<HD, MT>() + warps<HD, MT>() * MT * (HD / 16) * 512; }
+
+// The workspace: partial sums [2][runs][rows][HD] (heads, tails), their maxima and sums [2][runs][rows], and for each run the tile whose end
+// it has after an earlier run began it
+struct Head {
+    int first;             // the run that began the tile; -1: none
+    int b, at;
+};
+struct Parts {
+    float* o;
+    float2* ml;
+    Head* head;
+    int runs;
+};
 
 // One sequence's share of the work.
 struct Seq {
     int L, T, q0;          // cached tokens, query tokens, first query row
-    int groups;            // 16-token chunks
+    int units;             // of one tile
     int tiles;             // row tiles a kv head
-    __device__ __forceinline__ long long units(int kv_heads) const { return static_cast<long long>(groups) * tiles * kv_heads; }
+    __device__ __forceinline__ long long span(int kv_heads) const { return static_cast<long long>(units) * tiles * kv_heads; }
 };
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int rows) {
+// ROWS a tile
+template <int ROWS>
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     Seq s;
     s.q0 = a.q_start[b];
     s.T = a.q_start[b + 1] - s.q0;
     s.L = a.kv_len[b];
     if (s.T > a.max_q || s.L > a.max_kv) report_error(kErrIndex);
-    s.groups = (min(max(s.L, 0), a.max_kv) + kvGroup - 1) / kvGroup;
-    s.tiles = (min(max(s.T, 0), a.max_q) * (a.q_heads / a.kv_heads) + rows - 1) / rows;
+    s.units = (min(max(s.L, 0), a.max_kv) + kvGroup - 1) / kvGroup;
+    s.tiles = (min(max(s.T, 0), a.max_q) * (a.q_heads / a.kv_heads) + ROWS - 1) / ROWS;
     return s;
 }
 
 // The units of all sequences, by one warp.
-__device__ __forceinline__ long long total_units(const AttnArgs& a, int rows, int lane) {
+template <int ROWS>
+__device__ __forceinline__ long long total_units(const AttnArgs& a, int lane) {
     long long sum = 0;
-    for (int b = lane; b < a.seqs; b += 32) sum += load_seq(a, b, rows).units(a.kv_heads);
+    for (int b = lane; b < a.seqs; b += 32) sum += load_seq<ROWS>(a, b).span(a.kv_heads);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 // The sequence that holds unit w, and its first unit.
-__device__ __forceinline__ int locate(const AttnArgs& a, int rows, int lane, long long w, long long& first) {
+template <int ROWS>
+__device__ __forceinline__ int locate(const AttnArgs& a, int lane, long long w, long long& first) {
     long long before = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += 32) {
         const int b = b0 + lane;
-        const long long mine = b < a.seqs ? load_seq(a, b, rows).units(a.kv_heads) : 0;
+        const long long mine = b < a.seqs ? load_seq<ROWS>(a, b).span(a.kv_heads) : 0;
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -92,12 +109,6 @@ __device__ __forceinline__ int locate(const AttnArgs& a, int rows, int lane, lon
     first = before;
     return a.seqs;
 }
-// Units a block takes: whole rounds of its warps.
-__device__ __forceinline__ long long run_length(long long total, int blocks) {
-    const long long each = (total + blocks - 1) / blocks;
-    return (each + kWarps - 1) / kWarps * kWarps;
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -105,14 +116,22 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
 
+// c = a * b
+__device__ __forceinline__ void mma16816_set(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// c += a * b
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16816_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -129,66 +148,128 @@ __device__ __forceinline__ uint32_t pack2_bf16(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-// A row of this thread's tile: where its query is, what it sees.
+// A row of a tile, in shared memory
 struct RowInfo {
     float rs;              // score multiplier: scale * log2(e) (or scale / softcap) and the powers of two taken out
     int last;              // causal: the last visible token; -1 for a row past the end
     uint32_t bits0, bits1; // tree: visible among the newest
 };
+// Bounded wait (~1 s) that also gives up when another warp has
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > 1000000000ull) {
+            report_error(kErrWaitTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 
+// Requests the queries of m-tile mt of the tile from row tile0, and lays them out: fragments [k-step][lane], rows' multipliers and masks
 template <typename T, int HD, int PARTS, int MT>
-struct Tile {
-    static constexpr int kKs = HD / 16, kNb = HD / 32, kRowsT = tile_rows<PARTS, MT>(), kSets = PARTS == 2 ? 1 : 2;
-    uint32_t qa[MT][kKs][4];
-    float o[MT][kNb][4][4];
-    float m[MT][kSets], l[MT][kSets];
-    RowInfo row[MT][kSets];
-    int vexp;              // value scales are multiplied by 2^(15 - vexp)
+struct Queries {
+    static constexpr int kKs = HD / 16, kSets = PARTS == 1 ? 2 : 1;
+    using Raw = typename Vec4<T>::Raw;
+    Raw raw[kSets][kKs];
 
-    // Queries of rows tile0 .. as fragments, rows' multipliers and masks, empty sums
-    __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, int hk, int tile0, int lane) {
+    // The tile's row of this thread's set `set` of m-tile mt.  With three parts rows 0-3 stand twice.
+    static __device__ __forceinline__ int row_of(int mt, int set, int g) {
+        return PARTS == 1 ? 16 * mt + 8 * set + g : PARTS == 2 ? 8 * mt + g : g & 3;
+    }
+    __device__ __forceinline__ void request(const AttnArgs& a, const Seq& s, int hk, int tile0, int mt, int lane) {
         const int g = lane >> 2, t = lane & 3, group = a.q_heads / a.kv_heads;
-        const int rows = min(max(s.T, 0), a.max_q) * group;
+        const int rows = min(s.T, a.max_q) * group;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int set = 0; set < kSets; ++set) {
+            const int r = tile0 + row_of(mt, set, g);
+            const bool in = r < rows;
+            const int tok = in ? r / group : 0, h = in ? r % group : 0;
+            const T* q = static_cast<const T*>(a.q) + (s.q0 + tok) * a.q_stride + (hk * group + h) * HD;
 #pragma unroll
-            for (int set = 0; set < kSets; ++set) {
-                const int r = tile0 + mt * (16 / PARTS) + set * 8 + g;
+            for (int ks = 0; ks < kKs; ++ks) raw[set][ks] = in ? *reinterpret_cast<const Raw*>(q + 16 * ks + 4 * t) : Raw{};
+        }
+    }
+    __device__ __forceinline__ void lay(const AttnArgs& a, const Seq& s, int tile0, int mt, int lane, uint4* frag, RowInfo* info) const {
+        const int g = lane >> 2, t = lane & 3, group = a.q_heads / a.kv_heads;
+        const int rows = min(s.T, a.max_q) * group;
+        float f[kSets];
+#pragma unroll
+        for (int set = 0; set < kSets; ++set) {
+            float amax = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < kKs; ++ks) {
+                const float4 v = Vec4<T>::widen(raw[set][ks]);
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // the largest value goes to [2^14, 2^15); not finite or zero: as it is
+            const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+            const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
+            f[set] = pow2i(up);
+            if (t == 0 && (PARTS != 3 || g < 4)) {
+                const int r = tile0 + row_of(mt, set, g);
                 const bool in = r < rows;
-                const int tok = in ? r / group : 0, h = in ? r % group : 0;
-                const T* q = static_cast<const T*>(a.q) + (s.q0 + tok) * a.q_stride + (hk * group + h) * HD;
-                float4 v[kKs];
-                float amax = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < kKs; ++ks) {
-                    v[ks] = in ? load4(q + 16 * ks + 4 * t) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[ks].x), fabsf(v[ks].y)), fmaxf(fabsf(v[ks].z), fabsf(v[ks].w))));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // the largest value goes to [2^14, 2^15); not finite or zero: as it is
-                const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-                const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
-                const float f = pow2i(up);
-#pragma unroll
-                for (int ks = 0; ks < kKs; ++ks) {
-                    const float4 w = make_float4(v[ks].x * f, v[ks].y * f, v[ks].z * f, v[ks].w * f);
-                    const uint32_t h0 = pack2(w.x, w.y), h1 = pack2(w.z, w.w);
-                    qa[mt][ks][set] = h0;
-                    qa[mt][ks][2 + set] = h1;
-                    if (PARTS == 2) {
-                        const float2 x = unpack2(h0), y = unpack2(h1);
-                        qa[mt][ks][1] = pack2(w.x - x.x, w.y - x.y);
-                        qa[mt][ks][3] = pack2(w.z - y.x, w.w - y.y);
-                    }
-                }
-                RowInfo& ri = row[mt][set];
-                // 2^24 for the codes, 2^-up for the query; in two steps, each within f32's range
+                const int tok = in ? r / group : 0;
+                RowInfo ri;
+                // 2^24 for the codes, 2^-up for the query
                 ri.rs = (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) * 16777216.f * pow2i(-up);
                 ri.last = in ? s.L - s.T + tok : -1;
                 const unsigned long long bits = a.tree && in ? a.tree[s.q0 + tok] : 0ull;
                 ri.bits0 = static_cast<uint32_t>(bits);
                 ri.bits1 = static_cast<uint32_t>(bits >> 32);
+                info[row_of(mt, set, g)] = ri;
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < kKs; ++ks) {
+            uint32_t q[4];
+#pragma unroll
+            for (int set = 0; set < kSets; ++set) {
+                const float4 v = Vec4<T>::widen(raw[set][ks]);
+                const float4 w = make_float4(v.x * f[set], v.y * f[set], v.z * f[set], v.w * f[set]);
+                q[set] = pack2(w.x, w.y);
+                q[2 + set] = pack2(w.z, w.w);
+                if (PARTS > 1) {
+                    const float2 x = unpack2(q[0]), y = unpack2(q[2]);
+                    q[1] = pack2(w.x - x.x, w.y - x.y);
+                    q[3] = pack2(w.z - y.x, w.w - y.y);
+                }
+            }
+            frag[(mt * kKs + ks) * 32 + lane] = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+    }
+};
+
+// A warp's sums over its units of a tile
+template <typename T, int HD, int PARTS, int MT>
+struct Tile {
+    using Q = Queries<T, HD, PARTS, MT>;
+    static constexpr int kKs = HD / 16, kNb = HD / 32, kSets = Q::kSets;
+    float o[MT][kNb][4][4];
+    float m[MT][kSets], l[MT][kSets];
+    RowInfo row[MT][kSets];
+    int vexp;              // 16-bit queries: weights are multiplied by 2^(15 - vexp)
+
+    __device__ __forceinline__ void start(const RowInfo* info, int lane) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int set = 0; set < kSets; ++set) {
+                row[mt][set] = info[Q::row_of(mt, set, lane >> 2)];
                 m[mt][set] = kNone;
                 l[mt][set] = 0.f;
             }
@@ -202,68 +283,80 @@ struct Tile {
         vexp = -24;
     }
 
-    // One chunk of 16 tokens from j0 on.  MASKED: some of its tokens are new or past the end.
+    // Scales of this thread's four tokens (2t, 2t + 1, 2t + 8, 2t + 9), [token][block] in halves; tokens from `end` on have none
+    static __device__ __forceinline__ void load_scales(const uint8_t* p, int t, int end, uint32_t (&w)[kNb * 2]) {
+#pragma unroll
+        for (int i = 0; i < kNb / 2; ++i) *reinterpret_cast<uint4*>(w + 4 * i) = *reinterpret_cast<const uint4*>(p + t * 8 * kNb + 16 * i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (2 * t + (k & 1) + 8 * (k >> 1) >= end)
+#pragma unroll
+                for (int i = 0; i < kNb / 2; ++i) w[k * kNb / 2 + i] = 0u;
+    }
+    static __device__ __forceinline__ float scale_of(const uint32_t (&w)[kNb * 2], int k, int b) {
+        const float2 v = unpack2(w[(k * kNb + b) / 2]);
+        return b & 1 ? v.y : v.x;
+    }
+
+    // One chunk, its first token j0.  MASKED: some of its tokens are new or past the end.
     template <bool MASKED>
-    __device__ __forceinline__ void chunk(const AttnArgs& a, const Seq& s, const uint8_t* __restrict__ buf, int j0, int lane) {
+    __device__ __forceinline__ void unit(const AttnArgs& a, const Seq& s, const uint8_t* __restrict__ ch, const uint4* __restrict__ frag, int j0,
+                                         bool have, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const int len = min(s.L, a.max_kv);
-        // scales of this thread's four tokens (2t, 2t + 1, 2t + 8, 2t + 9), [token][block]
-        uint32_t ksw[kNb * 2], vsw[kNb * 2];
-#pragma unroll
-        for (int i = 0; i < kNb / 2; ++i) {
-            *reinterpret_cast<uint4*>(ksw + 4 * i) = *reinterpret_cast<const uint4*>(buf + kv_ks_offset(HD) + t * 8 * kNb + 16 * i);
-            *reinterpret_cast<uint4*>(vsw + 4 * i) = *reinterpret_cast<const uint4*>(buf + kv_vs_offset(HD) + t * 8 * kNb + 16 * i);
-        }
-        if (MASKED) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                if (j0 + 2 * t + (p & 1) + 8 * (p >> 1) >= len)
-#pragma unroll
-                    for (int i = 0; i < kNb / 2; ++i) ksw[p * kNb / 2 + i] = vsw[p * kNb / 2 + i] = 0u;
-        }
+        const int len = have ? min(s.L, a.max_kv) : 0, end = MASKED ? len - j0 : 16;
         float S[MT][2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t w[kKs];
+        {
+            uint32_t ksw[kNb * 2];
+            load_scales(ch + kv_ks_offset(HD), t, end, ksw);
 #pragma unroll
             for (int c = 0; c < kKs / 4; ++c) {
-                int u = 4 * c + t;
-                if (HD > 64) u ^= 4 * (g & 1);
-                *reinterpret_cast<uint4*>(w + 4 * c) = *reinterpret_cast<const uint4*>(buf + (8 * j + g) * HD + u * 16);
-            }
+                uint32_t w[2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[mt][j][i] = 0.f;
-#pragma unroll
-            for (int b = 0; b < kNb; ++b) {
-                const uint32_t b00 = codes2(w[2 * b], 0, 0x1100), b01 = codes2(w[2 * b], 0, 0x3322);
-                const uint32_t b10 = codes2(w[2 * b + 1], 0, 0x1100), b11 = codes2(w[2 * b + 1], 0, 0x3322);
-                float k0, k1;                                    // scales of tokens 2j and 2j + 1 of the thread's four
-                {
-                    const int i0 = 2 * j * kNb + b, i1 = i0 + kNb;
-                    k0 = f16_to_f32(i0 & 1 ? ksw[i0 / 2] >> 16 : ksw[i0 / 2] & 0xffffu);
-                    k1 = f16_to_f32(i1 & 1 ? ksw[i1 / 2] >> 16 : ksw[i1 / 2] & 0xffffu);
+                for (int j = 0; j < 2; ++j) {
+                    int at = 4 * c + t;
+                    if (HD > 64) at ^= 4 * (g & 1);
+                    *reinterpret_cast<uint4*>(w[j]) = *reinterpret_cast<const uint4*>(ch + (8 * j + g) * HD + at * 16);
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float p[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816(p, qa[mt][2 * b], b00, b01);
-                    mma16816(p, qa[mt][2 * b + 1], b10, b11);
-                    S[mt][j][0] = fmaf(k0, p[0], S[mt][j][0]);
-                    S[mt][j][1] = fmaf(k1, p[1], S[mt][j][1]);
-                    S[mt][j][2] = fmaf(k0, p[2], S[mt][j][2]);
-                    S[mt][j][3] = fmaf(k1, p[3], S[mt][j][3]);
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * c + h;
+                    uint32_t k[2][4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        k[j][0] = codes2(w[j][2 * h], 0, 0x1100);
+                        k[j][1] = codes2(w[j][2 * h], 0, 0x3322);
+                        k[j][2] = codes2(w[j][2 * h + 1], 0, 0x1100);
+                        k[j][3] = codes2(w[j][2 * h + 1], 0, 0x3322);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4 q0 = frag[(mt * kKs + 2 * b) * 32 + lane], q1 = frag[(mt * kKs + 2 * b + 1) * 32 + lane];
+                        const uint32_t a0[4] = {q0.x, q0.y, q0.z, q0.w}, a1[4] = {q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float p[4];
+                            mma16816_set(p, a0, k[j][0], k[j][1]);
+                            mma16816(p, a1, k[j][2], k[j][3]);
+                            const float k0 = scale_of(ksw, 2 * j, b), k1 = scale_of(ksw, 2 * j + 1, b);
+                            float (&x)[4] = S[mt][j];
+                            x[0] = b ? fmaf(k0, p[0], x[0]) : k0 * p[0];
+                            x[1] = b ? fmaf(k1, p[1], x[1]) : k1 * p[1];
+                            x[2] = b ? fmaf(k0, p[2], x[2]) : k0 * p[2];
+                            x[3] = b ? fmaf(k1, p[3], x[3]) : k1 * p[3];
+                        }
+                    }
                 }
             }
         }
+        uint32_t vsw[kNb * 2];
+        load_scales(ch + kv_vs_offset(HD), t, end, vsw);
         // f16 weights: the largest value scale so far sets the power of two
         if (PARTS == 1) {
             __half2 mx = *reinterpret_cast<const __half2*>(vsw);
 #pragma unroll
             for (int i = 1; i < kNb * 2; ++i) mx = __hmax2(mx, *reinterpret_cast<const __half2*>(vsw + i));
-            uint32_t u = *reinterpret_cast<const uint32_t*>(&mx);
-            int e = static_cast<int>(max((u >> 10) & 31u, (u >> 26) & 31u)) - 14;     // scale < 2^e
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(&mx);
+            int e = static_cast<int>(max((v >> 10) & 31u, (v >> 26) & 31u)) - 14;     // scale < 2^e
             if (__any_sync(0xffffffffu, e > vexp)) {
                 e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
                 e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
@@ -279,25 +372,36 @@ struct Tile {
                             for (int i = 0; i < 4; ++i) o[mt][c][x][i] *= down;
             }
         }
-        // scores to weights
+        // scores to weights, which carry the power of two 2^lift
+        const float lift = PARTS == 1 ? static_cast<float>(15 - vexp) : kLift;
+        const float lower = PARTS == 1 ? pow2i(vexp - 15) : 0x1p-108f;
         float P[MT][kSets][4];                                   // [row][token of the thread's four]
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            bool higher = false;
 #pragma unroll
-            for (int set = 0; set < kSets; ++set) {
-                const RowInfo& ri = row[mt][set];
+            for (int set = 0; set < kSets; ++set)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     float x = S[mt][p >> 1][2 * set + (p & 1)];
-                    if (PARTS == 2) x += S[mt][p >> 1][2 + (p & 1)];
-                    x *= ri.rs;
-                    if (a.softcap > 0.f) {
-                        // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones
-                        const float th = PARTS == 2 ? tanhf(x) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * x) + 1.f);
-                        x = a.softcap * kLog2e * th;
+                    if (PARTS > 1) x += S[mt][p >> 1][2 + (p & 1)];
+                    P[mt][set][p] = x * row[mt][set].rs;
+                }
+            if (a.softcap > 0.f) {
+                // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones
+#pragma unroll
+                for (int set = 0; set < kSets; ++set)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float x = P[mt][set][p];
+                        P[mt][set][p] = a.softcap * kLog2e * (PARTS > 1 ? tanhf(x) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * x) + 1.f));
                     }
-                    if (MASKED) {
+            }
+            if (MASKED) {
+#pragma unroll
+                for (int set = 0; set < kSets; ++set)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const RowInfo& ri = row[mt][set];
                         const int j = j0 + 2 * t + (p & 1) + 8 * (p >> 1);
                         const int rel = j - (s.L - s.T);
                         bool seen = ri.last >= 0 && j < len;
@@ -307,50 +411,50 @@ struct Tile {
                         } else {
                             seen = seen && j <= ri.last;
                         }
-                        if (!seen) x = -INFINITY;
+                        if (!seen) P[mt][set][p] = -INFINITY;
                     }
-                    P[mt][set][p] = x;
-                }
-                const float top = fmaxf(fmaxf(P[mt][set][0], P[mt][set][1]), fmaxf(P[mt][set][2], P[mt][set][3]));
-                higher |= top > m[mt][set];
+            }
+            float top[kSets];
+            bool higher = false;
+#pragma unroll
+            for (int set = 0; set < kSets; ++set) {
+                top[set] = fmaxf(fmaxf(P[mt][set][0], P[mt][set][1]), fmaxf(P[mt][set][2], P[mt][set][3]));
+                higher |= top[set] > m[mt][set] + (PARTS == 1 ? 0.f : kSlack);
             }
             if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
                 for (int set = 0; set < kSets; ++set) {
-                    float top = fmaxf(fmaxf(P[mt][set][0], P[mt][set][1]), fmaxf(P[mt][set][2], P[mt][set][3]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    top = fmaxf(top, m[mt][set]);
-                    const float down = ex2(m[mt][set] - top);
-                    m[mt][set] = top;
+                    float up = fmaxf(top[set], __shfl_xor_sync(0xffffffffu, top[set], 1));
+                    up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+                    up = fmaxf(up, m[mt][set]);
+                    const float down = ex2(m[mt][set] - up);
+                    m[mt][set] = up;
                     l[mt][set] *= down;
+                    // rows g and g + 8 of the accumulators; of more parts both belong to row g, or with three parts its copy
 #pragma unroll
                     for (int c = 0; c < kNb; ++c)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            o[mt][c][x][2 * set] *= down;
-                            o[mt][c][x][2 * set + 1] *= down;
-                            if (PARTS == 2) {
-                                o[mt][c][x][2] *= down;
-                                o[mt][c][x][3] *= down;
-                            }
-                        }
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int i = 0; i < (PARTS == 1 ? 2 : 4); ++i) o[mt][c][x][2 * set + i] *= down;
                 }
             }
 #pragma unroll
-            for (int set = 0; set < kSets; ++set)
+            for (int set = 0; set < kSets; ++set) {
+                const float from = m[mt][set] - lift;
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    P[mt][set][p] -= m[mt][set];
-                    P[mt][set][p] = ex2(P[mt][set][p]);
-                    l[mt][set] += P[mt][set][p];
+                    const float x = ex2(P[mt][set][p] - from);
+                    P[mt][set][p] = x;
+                    l[mt][set] = fmaf(x, lower, l[mt][set]);
                 }
+            }
         }
         // values: words [token][block], four dims each
         uint32_t w[4][kNb];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const uint8_t* r = buf + kv_v_offset(HD) + (4 * p + t) * HD;
+            const uint8_t* r = ch + kv_v_offset(HD) + (4 * p + t) * HD;
             if (HD == 64) {
                 *reinterpret_cast<uint2*>(w[p]) = *reinterpret_cast<const uint2*>(r + 8 * (g ^ (4 * (t >> 1))));
             } else {
@@ -359,15 +463,8 @@ struct Tile {
                     *reinterpret_cast<uint4*>(w[p] + 4 * h) = *reinterpret_cast<const uint4*>(r + 128 * h + 16 * (g ^ (2 * t)));
             }
         }
-        const float vf = PARTS == 2 ? 0x1p110f : pow2i(15 - vexp);
 #pragma unroll
         for (int c = 0; c < kNb; ++c) {
-            float vs[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int i = p * kNb + c;
-                vs[p] = f16_to_f32(i & 1 ? vsw[i / 2] >> 16 : vsw[i / 2] & 0xffffu) * vf;
-            }
             uint32_t pa[MT][4], low[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -376,8 +473,8 @@ struct Tile {
                     float z[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        z[p] = P[mt][set][p] * vs[p];
-                        if (MASKED && P[mt][set][p] == 0.f) z[p] = 0.f;          // whatever the masked value's scale is
+                        z[p] = P[mt][set][p] * scale_of(vsw, p, c);
+                        if (MASKED && P[mt][set][p] == 0.f) z[p] = 0.f;      // whatever the masked value's scale is
                     }
                     if (PARTS == 1) {
                         pa[mt][set] = pack2(z[0], z[1]);
@@ -386,13 +483,21 @@ struct Tile {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float x = z[2 * h], y = z[2 * h + 1];
-                            pa[mt][2 * h] = pack2_bf16(x, y);
-                            x -= __uint_as_float(pa[mt][2 * h] << 16);
-                            y -= __uint_as_float(pa[mt][2 * h] & 0xffff0000u);
-                            pa[mt][2 * h + 1] = pack2_bf16(x, y);
-                            x -= __uint_as_float(pa[mt][2 * h + 1] << 16);
-                            y -= __uint_as_float(pa[mt][2 * h + 1] & 0xffff0000u);
-                            low[mt][h] = pack2_bf16(x, y);
+                            const uint32_t hi = pack2_bf16(x, y);
+                            x -= __uint_as_float(hi << 16);
+                            y -= __uint_as_float(hi & 0xffff0000u);
+                            const uint32_t mid = pack2_bf16(x, y);
+                            x -= __uint_as_float(mid << 16);
+                            y -= __uint_as_float(mid & 0xffff0000u);
+                            const uint32_t lo = pack2_bf16(x, y);
+                            if (PARTS == 2) {
+                                pa[mt][2 * h] = hi;
+                                pa[mt][2 * h + 1] = mid;
+                                low[mt][h] = lo;
+                            } else {                          // rows 0-3 the high parts, 4-7 the middle ones, 8-11 the low ones
+                                pa[mt][2 * h] = g < 4 ? hi : mid;
+                                pa[mt][2 * h + 1] = lo;       // again in rows 12-15, which nothing reads
+                            }
                         }
                     }
                 }
@@ -406,261 +511,334 @@ struct Tile {
                         mma16816(o[mt][c][e], pa[mt], b0, b1);
                     } else {
                         mma16816_bf16(o[mt][c][e], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
-                        mma16816_bf16(o[mt][c][e], low[mt][0], 0u, low[mt][1], 0u, b0, b1);
+                        if (PARTS == 2) mma16816_bf16(o[mt][c][e], low[mt][0], 0u, low[mt][1], 0u, b0, b1);
                     }
                 }
             }
+        }
+    }
+
+    // This warp's sums of a row to dst(row), four columns at a time; `norm`: divided by the row's sum
+    template <typename F>
+    __device__ __forceinline__ void put(int lane, bool norm, F&& store) const {
+        const int g = lane >> 2, t = lane & 3;
+        // 2^133 (2^24) for the codes, and the power of two of the weights
+        const float back = PARTS == 1 ? pow2i(9 + vexp) : 0x1p25f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int set = 0; set < kSets; ++set) {
+                float sum = l[mt][set];                                  // over the four threads that share the row
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const float f = !norm ? back : sum == 0.f ? 0.f : back / sum;
+#pragma unroll
+                for (int c = 0; c < kNb; ++c) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = o[mt][c][e][2 * set + i];
+                            if (PARTS == 2 || (PARTS == 3 && g < 4)) x += o[mt][c][e][2 + i];
+                            if (PARTS == 3) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                            v[4 * i + e] = x * f;
+                        }
+                    if (PARTS != 3 || g < 4) {
+                        store(Q::row_of(mt, set, g), 32 * c + 8 * t, make_float4(v[0], v[1], v[2], v[3]), m[mt][set], sum);
+                        store(Q::row_of(mt, set, g), 32 * c + 8 * t + 4, make_float4(v[4], v[5], v[6], v[7]), m[mt][set], sum);
+                    }
+                }
+            }
+    }
+};
+
+// A place in the order of the units: unit g of tile `at` ((kv head, row tile)) of sequence b
+template <int ROWS>
+struct Place {
+    Seq s;
+    int b, at, g;
+    // On from a tile's end to the next tile
+    __device__ __forceinline__ void next_tile(const AttnArgs& a) {
+        g = 0;
+        if (++at >= s.tiles * a.kv_heads) {
+            at = 0;
+            do s = load_seq<ROWS>(a, ++b); while (s.units == 0 || s.tiles == 0);
         }
     }
 };
 
 template <typename T, int HD, int PARTS, int MT>
-__global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a, float* __restrict__ part_o, float2* __restrict__ part_ml,
-                                                               int page_shift) {
+__global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kernel(const AttnArgs a, const Parts parts, int page_shift) {
     using TileT = Tile<T, HD, PARTS, MT>;
-    constexpr int kRows = TileT::kRowsT, kNst = stages<HD>(), kChunk = kv_chunk_bytes(HD);
-    constexpr int kCols = merge_cols<HD, PARTS, MT>(), kPitch = kCols + 4;
+    using QT = typename TileT::Q;
+    constexpr int kWarps = warps<HD, MT>(), kRows = tile_rows<PARTS, MT>(), kNst = stages<HD, MT>(), kChunk = kv_chunk_bytes(HD);
+    constexpr int kFrags = MT * (HD / 16) * 32, kPitch = HD + 4;
+    static_assert(2 * kWarps * kNst * 8 <= 1024 && kWarps * kRows * kPitch * 4 <= ring_bytes<HD, MT>(), "shared memory");
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                              // [kWarps][kNst]
-    uint8_t* ring_all = smem + 1024;
-    float* merge = reinterpret_cast<float*>(ring_all + kWarps * kNst * kChunk);      // [kWarps][kRows][kPitch]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                              // [kWarps][kNst] full, [kWarps][kNst] empty
+    uint8_t* ring = smem + 1024;                                                     // [kWarps][kNst][kChunk]
+    uint4* frag_all = reinterpret_cast<uint4*>(ring + kWarps * kNst * kChunk);       // [kWarps][MT][HD / 16][32]
+    float* merge = reinterpret_cast<float*>(ring);                                   // at the end: [kWarps][kRows][kPitch]
+    __shared__ RowInfo info_all[kWarps][kRows];
     __shared__ float sm[kWarps][kRows], sl[kWarps][kRows];
+    __shared__ uint8_t have[kWarps][kNst];                                           // whether a ring slot's page exists
+    __shared__ long long open[kWarps];                                               // the first unit of the tile that a warp's run ends in, or -1
+    __shared__ volatile int abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t* bar = bars + warp * kNst;
-    uint8_t* ring = ring_all + warp * kNst * kChunk;
-    if (lane == 0)
-        for (int i = 0; i < kNst; ++i) mbar_init(&bar[i], 1);
+    if (threadIdx.x < 2 * kWarps * kNst) mbar_init(&bars[threadIdx.x], 1);
+    if (threadIdx.x == 0) abort = 0;
     fence_barrier_init();
-    __syncwarp();
+    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const long long total = total_units(a, kRows, lane);
-    const long long per = run_length(total, gridDim.x);
-    const long long w0 = per * blockIdx.x;
-    const long long count = min(total - w0, per);
-    if (count <= 0) return;
-    long long first;
-    const int b_start = locate(a, kRows, lane, w0, first);
-    Seq s = load_seq(a, b_start, kRows);
-    const int at = static_cast<int>((w0 - first) / s.groups);            // (kv head, row tile) of the first unit
-    const int g_start = static_cast<int>((w0 - first) % s.groups);
-
-    // ---- the fetching side: this warp's units warp, warp + 8, ... of the run
-    int f_b = b_start, f_at = at, f_g = g_start + warp;
-    Seq f_s = s;
+    const long long total = total_units<kRows>(a, lane);
+    const long long per = max((total + parts.runs - 1) / parts.runs, 1ll);
     const int gpp = a.page_size / kvGroup;
-    int f_page = -1, f_off = 0;
-    unsigned good = 0;                                                   // ring slots that hold a chunk
-    auto settle = [&]() {                                                // carries f_g into its tile and sequence, and looks its page up
-        while (f_g >= f_s.groups) {
-            f_g -= f_s.groups;
-            if (++f_at >= f_s.tiles * a.kv_heads) {
-                f_at = 0;
-                do f_s = load_seq(a, ++f_b, kRows); while (f_s.groups == 0 || f_s.tiles == 0);
-            }
-        }
-        const int pi = page_shift >= 0 ? f_g >> page_shift : f_g / gpp;
-        f_off = f_g - pi * gpp;
-        f_page = __ldg(a.table + static_cast<size_t>(f_b) * a.table_stride + pi);
-    };
-    long long f_u = warp;
-    if (f_u < count) settle();
-    auto fetch = [&](int slot) {                                         // requests the warp's next unit into a ring slot
-        if (f_u >= count) return;
-        const bool ok = f_page >= 0 && f_page < a.pages;
-        good = ok ? good | 1u << slot : good & ~(1u << slot);
-        if (lane == 0) {
-            if (ok) {
-                mbar_arrive_expect_tx(&bar[slot], kChunk);
-                const uint8_t* src = a.cache + ((static_cast<size_t>(f_page) * a.kv_heads + f_at / f_s.tiles) * gpp + f_off) * kChunk;
-                bulk_g2s(ring + slot * kChunk, src, kChunk, &bar[slot]);
-            } else {
-                mbar_arrive(&bar[slot]);
-                report_error(kErrIndex);
-            }
-        }
-        f_u += kWarps;
-        f_g += kWarps;
-        if (f_u < count) settle();
-    };
-    for (int i = 0; i < kNst; ++i) fetch(i);
 
-    // ---- the computing side: tile by tile, all warps together
-    TileT tile;
-    int slot = 0;
-    uint32_t phase = 0;
-    bool dead = false;
-    int dead_slot = 0;
-    uint32_t dead_phase = 0;
-    int b = b_start, c_at = at, ga = g_start;
-    for (long long done = 0; done < count;) {
-        if (c_at >= s.tiles * a.kv_heads) {
-            do s = load_seq(a, ++b, kRows); while (s.groups == 0 || s.tiles == 0);
-            c_at = 0;
+    if (warp == kWarps) {
+        // ---- the fetching warp: lane w requests the units of warp w's run into its ring
+        const long long w0 = per * (static_cast<long long>(blockIdx.x) * kWarps + lane);
+        const int count = lane < kWarps && w0 < total ? static_cast<int>(min(total - w0, per)) : 0;
+        Place<kRows> p;
+        {
+            // the block's first unit is found by the warp together; each lane goes on from there
+            const long long first_unit = per * blockIdx.x * kWarps;
+            if (first_unit >= total) return;
+            long long first;
+            p.b = locate<kRows>(a, lane, first_unit, first);
+            p.s = load_seq<kRows>(a, p.b);
+            if (count) {
+                long long rest = w0 - first;
+                while (rest >= p.s.span(a.kv_heads)) {
+                    rest -= p.s.span(a.kv_heads);
+                    p.s = load_seq<kRows>(a, ++p.b);
+                }
+                p.at = static_cast<int>(rest / p.s.units);
+                p.g = static_cast<int>(rest % p.s.units);
+            }
         }
-        const int n = static_cast<int>(min(static_cast<long long>(s.groups - ga), count - done));
-        const int turn = static_cast<int>(done) & (kWarps - 1);          // the warp that has the first of these
-        const int hk = c_at / s.tiles, tile0 = (c_at % s.tiles) * kRows;
-        const int mine = (warp - turn) & (kWarps - 1);
-        if (mine < n) {
-            tile.start(a, s, hk, tile0, lane);
-            for (int i = mine; i < n; i += kWarps) {
-                if (!dead && __any_sync(0xffffffffu, !mbar_wait(&bar[slot], phase))) {
-                    dead = true;
-                    dead_slot = slot;
-                    dead_phase = phase;
-                    if (lane == 0) report_error(kErrWaitTimeout);
-                }
-                if (!dead) {
-                    if (good >> slot & 1u) {
-                        const int j0 = (ga + i) * kvGroup;
-                        if (j0 + kvGroup > min(s.L - s.T, a.max_kv))
-                            tile.template chunk<true>(a, s, ring + slot * kChunk, j0, lane);
-                        else
-                            tile.template chunk<false>(a, s, ring + slot * kChunk, j0, lane);
+        int fetched = 0, slot = 0, page = -1, off = 0;
+        uint32_t parity = 1;                                             // of a ring's first round: nothing to wait for
+        auto look_up = [&]() {                                           // used at the next fetch, not waited for here
+            const int pi = page_shift >= 0 ? p.g >> page_shift : p.g / gpp;
+            off = p.g - pi * gpp;
+            page = __ldg(a.table + static_cast<size_t>(p.b) * a.table_stride + pi);
+        };
+        if (count) look_up();
+        uint64_t since = globaltimer_ns();
+        while (__any_sync(0xffffffffu, fetched < count)) {
+            bool did = false;
+            if (fetched < count) {
+                uint64_t* full = &bars[lane * kNst + slot];
+                if (mbar_test(full + kWarps * kNst, parity)) {
+                    const bool there = page >= 0 && page < a.pages;
+                    have[lane][slot] = there;
+                    if (there) {
+                        mbar_arrive_expect_tx(full, kChunk);
+                        bulk_g2s(ring + (lane * kNst + slot) * kChunk,
+                                 a.cache + ((static_cast<size_t>(page) * a.kv_heads + p.at / p.s.tiles) * gpp + off) * kChunk, kChunk, full);
+                    } else {
+                        report_error(kErrIndex);
+                        mbar_arrive(full);
                     }
-                    __syncwarp();
-                    fetch(slot);
+                    if (++slot == kNst) {
+                        slot = 0;
+                        parity ^= 1;
+                    }
+                    if (++fetched < count) {
+                        if (++p.g == p.s.units) p.next_tile(a);
+                        look_up();
+                    }
+                    did = true;
                 }
+            }
+            if (__any_sync(0xffffffffu, did)) {
+                since = globaltimer_ns();
+            } else {
+                __nanosleep(32);
+                if (__any_sync(0xffffffffu, abort || globaltimer_ns() - since > 2000000000ull)) break;    // a computing warp reports its own wait
+            }
+        }
+        if (abort)                                                       // copies in flight land before shared memory goes away
+            for (int i = 0; i < kNst; ++i) {
+                const int times = (fetched + kNst - 1 - i) / kNst;
+                if (times && !mbar_wait(&bars[lane * kNst + i], (times - 1) & 1)) report_error(kErrDrainTimeout);
+            }
+        return;
+    }
+
+    // ---- the computing warps: each its own run
+    const int run = blockIdx.x * kWarps + warp, group = a.q_heads / a.kv_heads;
+    const long long w0 = per * run;
+    const int count = w0 < total ? static_cast<int>(min(total - w0, per)) : 0;
+    uint4* frag = frag_all + warp * kFrags;
+    RowInfo* info = info_all[warp];
+    Head head = {-1, 0, 0};
+    long long open_at = -1;
+    if (count) {
+        TileT tile;
+        uint64_t* full = &bars[warp * kNst];
+        const uint8_t* ring_w = ring + warp * kNst * kChunk;
+        int slot = 0;
+        uint32_t phase = 0;
+        Place<kRows> p;
+        long long first;                                                 // the first unit of the tile
+        p.b = locate<kRows>(a, lane, w0, first);
+        p.s = load_seq<kRows>(a, p.b);
+        p.at = static_cast<int>((w0 - first) / p.s.units);
+        p.g = static_cast<int>((w0 - first) % p.s.units);
+        first = w0 - p.g;
+        bool ok = true;
+        for (int done = 0; ok;) {
+            const int tile0 = (p.at % p.s.tiles) * kRows, hk = p.at / p.s.tiles;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                QT q;
+                q.request(a, p.s, hk, tile0, mt, lane);
+                q.lay(a, p.s, tile0, mt, lane, frag, info);
+            }
+            __syncwarp();
+            tile.start(info, lane);
+            const int end = min(p.s.units, p.g + count - done);
+            const bool begun_here = p.g == 0;
+            // units from here on hold new tokens, or the end
+            const int old = min(p.s.L - p.s.T, a.max_kv), masked = old > 0 ? old / kvGroup : 0;
+            done += end - p.g;
+            for (int i = p.g; i < end; ++i) {
+                if (!wait_for(&full[slot], phase, &abort)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                const uint8_t* ch = ring_w + slot * kChunk;
+                if (i >= masked)
+                    tile.template unit<true>(a, p.s, ch, frag, i * kvGroup, have[warp][slot], lane);
+                else if (have[warp][slot])
+                    tile.template unit<false>(a, p.s, ch, frag, 0, true, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[kWarps * kNst + slot]);
                 if (++slot == kNst) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
-            // a row's sums in this warp: over the four threads that share it
-            const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int set = 0; set < TileT::kSets; ++set) {
-                    float l = tile.l[mt][set];
-                    l += __shfl_xor_sync(0xffffffffu, l, 1);
-                    l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    if (t == 0) {
-                        sm[warp][mt * (16 / PARTS) + set * 8 + g] = tile.m[mt][set];
-                        sl[warp][mt * (16 / PARTS) + set * 8 + g] = l;
-                    }
-                }
-        }
-        // ---- the warps' sums meet
-        const bool whole = ga == 0 && n == s.groups;                     // this block has all of the tile
-        const int live = min(n, kWarps);
-        const int group = a.q_heads / a.kv_heads;
-        const int rows = min(min(s.T, a.max_q) * group - tile0, kRows);
-        const size_t out_slot = 2 * blockIdx.x + (done == 0 && ga > 0 ? 0 : 1);
-#pragma unroll
-        for (int c0 = 0; c0 < HD; c0 += kCols) {
-            if (mine < n) {
-                // 2^133 (2^24) for the codes, and the power of two of the value scales
-                const float back = PARTS == 2 ? 0x1p23f : pow2i(9 + tile.vexp);
-                const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int set = 0; set < TileT::kSets; ++set) {
-                        float* dst = merge + (warp * kRows + mt * (16 / PARTS) + set * 8 + g) * kPitch;
-#pragma unroll
-                        for (int c = 0; c < kCols / 32; ++c) {
-                            float v[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    float x = tile.o[mt][c0 / 32 + c][e][2 * set + i];
-                                    if (PARTS == 2) x += tile.o[mt][c0 / 32 + c][e][2 + i];
-                                    v[4 * i + e] = x * back;
-                                }
-                            *reinterpret_cast<float4*>(dst + 32 * c + 8 * t) = make_float4(v[0], v[1], v[2], v[3]);
-                            *reinterpret_cast<float4*>(dst + 32 * c + 8 * t + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                        }
-                    }
+            if (!ok) break;
+            if (end == p.s.units && begun_here) {                        // all of the tile
+                const int rows = min(p.s.T, a.max_q) * group - tile0;
+                T* out = static_cast<T*>(a.out) + p.s.q0 * a.out_stride + hk * group * HD;
+                tile.put(lane, true, [&](int r, int c, float4 v, float, float) {
+                    if (r < rows) store4(out + ((tile0 + r) / group) * a.out_stride + ((tile0 + r) % group) * HD + c, v);
+                });
+            } else if (end == p.s.units) {                               // its end: for the second kernel
+                head = {static_cast<int>(first / per), p.b, p.at};
+                tile.put(lane, false, [&](int r, int c, float4 v, float m, float l) {
+                    const size_t at = static_cast<size_t>(run) * kRows + r;
+                    *reinterpret_cast<float4*>(parts.o + at * HD + c) = v;
+                    if (c == 0) parts.ml[at] = make_float2(m, l);
+                });
+            } else {
+                open_at = first;
             }
-            __syncthreads();
-            for (int i = threadIdx.x; i < kRows * (kCols / 4); i += kThreads) {
-                const int r = i / (kCols / 4), c = 4 * (i % (kCols / 4));
-                if (r >= rows) continue;
+            if (done == count) break;
+            first += p.s.units;
+            p.next_tile(a);
+        }
+        if (!ok) open_at = -1;
+        if (lane == 0) open[warp] = open_at;
+        // every warp's ring has been read: the open tiles meet there
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        if (open_at >= 0)
+            tile.put(lane, false, [&](int r, int c, float4 v, float m, float l) {
+                *reinterpret_cast<float4*>(merge + (warp * kRows + r) * kPitch + c) = v;
+                if (c == 0) {
+                    sm[warp][r] = m;
+                    sl[warp][r] = l;
+                }
+            });
+    } else {
+        if (lane == 0) open[warp] = -1;
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    }
+    if (lane == 0) parts.head[run] = head;
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    // neighbours in the same tile are joined; the sum is the tail of the first of them
+    for (int w = 0; w < kWarps;) {
+        const long long which = open[w];
+        int n = 1;
+        while (w + n < kWarps && which >= 0 && open[w + n] == which) ++n;
+        if (which >= 0)
+            for (int i = threadIdx.x; i < kRows * (HD / 4); i += kWarps * 32) {
+                const int r = i / (HD / 4), c = 4 * (i % (HD / 4));
                 float top = kNone;
-                for (int k = 0; k < live; ++k) top = fmaxf(top, sm[(turn + k) & (kWarps - 1)][r]);
+                for (int k = 0; k < n; ++k) top = fmaxf(top, sm[w + k][r]);
                 float l = 0.f;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < live; ++k) {
-                    const int wk = (turn + k) & (kWarps - 1);
-                    const float f = ex2(sm[wk][r] - top);
-                    const float4 x = *reinterpret_cast<const float4*>(merge + (wk * kRows + r) * kPitch + c);
-                    l = fmaf(f, sl[wk][r], l);
+                for (int k = 0; k < n; ++k) {
+                    const float f = ex2(sm[w + k][r] - top);
+                    const float4 x = *reinterpret_cast<const float4*>(merge + ((w + k) * kRows + r) * kPitch + c);
+                    l = fmaf(f, sl[w + k][r], l);
                     v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
                 }
-                if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    const int tok = (tile0 + r) / group, h = (tile0 + r) % group;
-                    store4(static_cast<T*>(a.out) + (s.q0 + tok) * a.out_stride + (hk * group + h) * HD + c0 + c,
-                           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                } else {
-                    *reinterpret_cast<float4*>(part_o + (out_slot * kRows + r) * HD + c0 + c) = v;
-                    if (c0 + c == 0) part_ml[out_slot * kRows + r] = make_float2(top, l);
-                }
+                const size_t at = (static_cast<size_t>(parts.runs) + blockIdx.x * kWarps + w) * kRows + r;
+                *reinterpret_cast<float4*>(parts.o + at * HD + c) = v;
+                if (c == 0) parts.ml[at] = make_float2(top, l);
             }
-            __syncthreads();
-        }
-        done += n;
-        ga = 0;
-        ++c_at;
-    }
-    if (dead) {                                                          // copies in flight land before shared memory goes away
-        for (int i = 0; i < kNst; ++i)
-            if (lane == 0 && !mbar_wait(&bar[i], dead_phase ^ (i < dead_slot ? 1u : 0u))) report_error(kErrDrainTimeout);
+        w += n;
     }
 }
 
-// Joins the partial sums of the tiles that more than one block shares, in block order.  Block (x, r): row r of the
-// tile that the boundary between runs x and x + 1 cuts, if it is that tile's first boundary.  Rows of sequences
-// without keys are written here too.
+// Joins the tiles that runs share, in the order of the runs: the tails of the blocks from the run that began the tile, and the head of the
+// run that ends it.  A warp takes a row of a run's head, four columns a lane (two of them for 256).  Rows of sequences without keys are
+// written here too.
 template <typename T, int HD, int PARTS, int MT>
-__global__ void __launch_bounds__(HD) attn_join_kernel(const AttnArgs a, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                                                      int blocks) {
-    constexpr int kRows = tile_rows<PARTS, MT>();
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const Parts parts) {
+    constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, group = a.q_heads / a.kv_heads;
-    const int r = blockIdx.y;
-    if (static_cast<int>(blockIdx.x) >= blocks - 1) {                    // the last column of blocks: outputs without keys
-        for (int b = r; b < a.seqs; b += gridDim.y) {
-            const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
-            if (a.kv_len[b] > 0) continue;
-            for (int tok = 0; tok < n; ++tok)
-                for (int h = 0; h < a.q_heads; ++h)
-                    from_f32(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + h * HD + threadIdx.x, 0.f);
-        }
-        return;
+    const int warps_all = gridDim.x * 8, me = blockIdx.x * 8 + (threadIdx.x >> 5);
+    for (int i = me; i < parts.runs * kRows; i += warps_all) {
+        const int run = i / kRows, r = i % kRows;
+        const Head head = parts.head[run];
+        if (head.first < 0) continue;
+        const Seq s = load_seq<kRows>(a, head.b);
+        const int tile0 = (head.at % s.tiles) * kRows, hk = head.at / s.tiles;
+        if (tile0 + r >= min(s.T, a.max_q) * group) continue;
+        float top = kNone, l = 0.f;
+        float4 v[kRuns];
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](size_t slot) {
+            const float2 ml = parts.ml[slot * kRows + r];
+            const float up = fmaxf(top, ml.x), f = ex2(top - up), h = ex2(ml.x - up);
+            l = fmaf(l, f, ml.y * h);
+            top = up;
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c)
+                if (lane < kLanes) {
+                    const float4 x = *reinterpret_cast<const float4*>(parts.o + (slot * kRows + r) * HD + 128 * c + 4 * lane);
+                    v[c] = make_float4(fmaf(v[c].x, f, x.x * h), fmaf(v[c].y, f, x.y * h), fmaf(v[c].z, f, x.z * h), fmaf(v[c].w, f, x.w * h));
+                }
+        };
+#pragma unroll 4
+        for (int k = head.first; k < run; k = (k / kWarps + 1) * kWarps) add(static_cast<size_t>(parts.runs) + k);
+        add(run);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(a.out) + (s.q0 + (tile0 + r) / group) * a.out_stride + (hk * group + (tile0 + r) % group) * HD;
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c)
+            if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
     }
-    const long long total = total_units(a, kRows, lane);
-    const long long per = run_length(total, blocks);
-    const int i = blockIdx.x + 1;
-    const long long w = per * i;
-    if (w >= total) return;
-    long long first;
-    const int b = locate(a, kRows, lane, w, first);
-    const Seq s = load_seq(a, b, kRows);
-    const int at = static_cast<int>((w - first) / s.groups);
-    const long long begin = first + static_cast<long long>(at) * s.groups, end = begin + s.groups;
-    if (begin >= w || begin < w - per) return;                           // not cut here, or cut earlier too
-    const int tile0 = (at % s.tiles) * kRows;
-    if (tile0 + r >= min(s.T, a.max_q) * group) return;
-    const int last = static_cast<int>((end - 1) / per);
-    float top = kNone, l = 0.f, v = 0.f;
-    for (int k = i - 1; k <= last; ++k) {
-        const size_t slot = 2 * k + (k == i - 1 ? 1 : 0);
-        const float2 ml = part_ml[slot * kRows + r];
-        const float x = part_o[(slot * kRows + r) * HD + threadIdx.x];
-        const float up = fmaxf(top, ml.x), f = ex2(top - up), h = ex2(ml.x - up);
-        l = fmaf(l, f, ml.y * h);
-        v = fmaf(v, f, x * h);
-        top = up;
+    for (int b = me; b < a.seqs; b += warps_all) {
+        if (a.kv_len[b] > 0) continue;
+        const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
+        for (int tok = 0; tok < n; ++tok)
+            for (int d = lane * 4; d < a.q_heads * HD; d += 128)
+                store4(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    const int tok = (tile0 + r) / group, h = (tile0 + r) % group, hk = at / s.tiles;
-    from_f32(static_cast<T*>(a.out) + (s.q0 + tok) * a.out_stride + (hk * group + h) * HD + threadIdx.x, l == 0.f ? 0.f : v / l);
 }
 
 template <typename K, typename... A>
@@ -680,8 +858,8 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStr
 
 template <typename T, int HD, int PARTS, int MT>
 cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
-    constexpr int kRows = tile_rows<PARTS, MT>(), smem = smem_bytes<HD, PARTS, MT>();
-    static_assert(smem <= 227 * 1024, "shared memory");
+    constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), smem = smem_bytes<HD, MT>();
+    static_assert(smem <= 220 * 1024, "shared memory");
     static bool configured = false;
     if (!configured) {
         const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<T, HD, PARTS, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -692,28 +870,50 @@ cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
     int shift = -1;
     for (int i = 0; i < 16; ++i)
         if (gpp == 1 << i) shift = i;
-    float* part_o = static_cast<float*>(a.workspace);
-    float2* part_ml = reinterpret_cast<float2*>(part_o + static_cast<size_t>(2) * kBlocks * kRows * HD);
-    const cudaError_t e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), kThreads, smem, s, a, part_o, part_ml, shift);
+    Parts parts;
+    parts.runs = kBlocks * kWarps;
+    parts.o = static_cast<float*>(a.workspace);
+    parts.ml = reinterpret_cast<float2*>(parts.o + static_cast<size_t>(2) * parts.runs * kRows * HD);
+    parts.head = reinterpret_cast<Head*>(parts.ml + static_cast<size_t>(2) * parts.runs * kRows);
+    const cudaError_t e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), (kWarps + 1) * 32, smem, s, a, parts, shift);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_join_kernel<T, HD, PARTS, MT>, dim3(kBlocks, kRows), HD, 0, s, a, part_o, part_ml, kBlocks);
+    return launch_dependent(attn_join_kernel<T, HD, PARTS, MT>, dim3(kBlocks * 2), 256, 0, s, a, parts);
+}
+template <int HD, int PARTS, int MT>
+size_t rows_bytes() {
+    const size_t runs = kBlocks * warps<HD, MT>();
+    return runs * (2 * tile_rows<PARTS, MT>() * (HD * 4 + 8) + sizeof(Head));
 }
 
 // One 16-row (8-row for f32) tile where a kv head's rows fit it, else two of them at a time (head_dim 256: the
-// accumulators leave no registers for the second).
+// accumulators leave no registers for the second).  Up to four f32 rows take all three parts of a weight in one product.
 template <typename T, int HD>
 cudaError_t rows_type(const AttnArgs& a, cudaStream_t s) {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
     const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
+    if constexpr (PARTS == 2)
+        if (rows <= 4) return rows_go<T, HD, 3, 1>(a, s);
     if constexpr (HD < 256)
         if (rows > 16 / PARTS) return rows_go<T, HD, PARTS, 2>(a, s);
     return rows_go<T, HD, PARTS, 1>(a, s);
 }
+template <typename T, int HD>
+size_t rows_type_bytes(long long rows) {
+    constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+    if constexpr (PARTS == 2)
+        if (rows <= 4) return rows_bytes<HD, 3, 1>();
+    if constexpr (HD < 256)
+        if (rows > 16 / PARTS) return rows_bytes<HD, PARTS, 2>();
+    return rows_bytes<HD, PARTS, 1>();
+}
 
 }  // namespace
 
-size_t attn_workspace_bytes(int, int, int, int, int head_dim, int) {
-    return static_cast<size_t>(2) * kBlocks * 32 * (head_dim + 2) * sizeof(float);      // 32: the largest tile's rows
+size_t attn_workspace_bytes(int, int max_q, int q_heads, int kv_heads, int head_dim, int type) {
+    const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
+    if (type == GQ_F32)
+        return head_dim == 64 ? rows_type_bytes<float, 64>(rows) : head_dim == 128 ? rows_type_bytes<float, 128>(rows) : rows_type_bytes<float, 256>(rows);
+    return head_dim == 64 ? rows_type_bytes<__half, 64>(rows) : head_dim == 128 ? rows_type_bytes<__half, 128>(rows) : rows_type_bytes<__half, 256>(rows);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
