@@ -486,6 +486,22 @@ def q1s32_q8_gemm(signs: torch.Tensor, wscale: torch.Tensor, xd: torch.Tensor, x
 
 # ----------------------------------------------------------------------------- between a layer's products
 
+# The calls of a decode step are short, so these wrappers keep their own cost low: addresses go to C as plain integers, and the stream is
+# read without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(t: torch.Tensor) -> int:
+    """The raw current stream of a tensor's device."""
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -527,8 +543,8 @@ def _rmsnorm(x, weight, eps, residual, sum_out, y, act, d, q, op):
     _need(weight, torch.float32, k, "weight")
     if sum_out is not None:
         _need(sum_out, x.dtype, m * k, "sum_out")
-    _check(lib().gq_rmsnorm(_ptr(x), xs, _ptr(residual), rs, _ptr(weight), eps, code, m, k, _ptr(sum_out), _ptr(y),
-                            _ptr(act), _ptr(d), _ptr(q), _ptr(op), _stream()), "gq_rmsnorm")
+    _check(lib().gq_rmsnorm(_at(x), xs, _at(residual), rs, _at(weight), eps, code, m, k, _at(sum_out), _at(y),
+                            _at(act), _at(d), _at(q), _at(op), _on(x)), "gq_rmsnorm")
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
@@ -578,7 +594,7 @@ def dequantize_q8_0(act: torch.Tensor, m: int, k: int, dtype=torch.float32, out:
     y = torch.empty((m, k), dtype=dtype, device=act.device) if out is None else out
     code = _type(y, "out")
     _need(y, y.dtype, m * k, "out")
-    _check(lib().gq_dequantize_q8_0(_ptr(act), m * (k // 32), code, _ptr(y), _stream()), "gq_dequantize_q8_0")
+    _check(lib().gq_dequantize_q8_0(_at(act), m * (k // 32), code, _at(y), _on(y)), "gq_dequantize_q8_0")
     return y
 
 
@@ -589,7 +605,7 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "
     if scaling not in ROPE_SCALING:
         raise GQError(f"rope_table: unknown scaling {scaling!r}")
     t = torch.empty((max(positions, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
-    _check(lib().gq_rope_table(_ptr(t), positions, rot, base, ROPE_SCALING[scaling], factor, original, _stream()),
+    _check(lib().gq_rope_table(_at(t), positions, rot, base, ROPE_SCALING[scaling], factor, original, _on(t)),
            "gq_rope_table")
     return t
 
@@ -643,10 +659,10 @@ def rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cac
         _need(rope, torch.float32, rows * rot, "rope")
         _need(positions, torch.int32, n, "positions")
     _need(slots, torch.int64, n, "slots")
-    _check(lib().gq_rope_kv_append(_ptr(q), qs, _ptr(q_out if q is not None else None), qos, _ptr(k), ks, _ptr(v), vs, code,
-                                   _ptr(rope), rows, rot, 1 if interleaved else 0,
-                                   _ptr(positions if rope is not None else None), _ptr(slots), n, hq, hkv, hd,
-                                   _ptr(cache.data), cache.pages, cache.page_size, _stream()), "gq_rope_kv_append")
+    _check(lib().gq_rope_kv_append(_at(q), qs, _at(q_out if q is not None else None), qos, _at(k), ks, _at(v), vs, code,
+                                   _at(rope), rows, rot, 1 if interleaved else 0,
+                                   _at(positions if rope is not None else None), _at(slots), n, hq, hkv, hd,
+                                   _at(cache.data), cache.pages, cache.page_size, _on(k)), "gq_rope_kv_append")
     return q_out if q is not None else None
 
 
@@ -661,8 +677,8 @@ def kv_read(cache: KVCacheQ8_0, slots: torch.Tensor, dtype=torch.float32, k_out:
     _need(slots, torch.int64, n, "slots")
     _need(k, k.dtype, n * cache.kv_heads * cache.head_dim, "k_out")
     _need(v, k.dtype, n * cache.kv_heads * cache.head_dim, "v_out")
-    _check(lib().gq_kv_read(_ptr(cache.data), cache.pages, cache.page_size, cache.kv_heads, cache.head_dim, _ptr(slots), n,
-                            code, _ptr(k), _ptr(v), _stream()), "gq_kv_read")
+    _check(lib().gq_kv_read(_at(cache.data), cache.pages, cache.page_size, cache.kv_heads, cache.head_dim, _at(slots), n,
+                            code, _at(k), _at(v), _on(k)), "gq_kv_read")
     return k, v
 
 
@@ -713,10 +729,10 @@ def attn_q8_0(q: torch.Tensor, cache: KVCacheQ8_0, block_table: torch.Tensor, kv
     _need(workspace, torch.uint8, workspace.numel(), "workspace")
     if workspace.numel() < need:
         raise GQError(f"attn_q8_0: workspace holds {workspace.numel()} bytes, needs {need}")
-    _check(lib().gq_attn_q8_0(_ptr(q), qs, _ptr(o), os_, code, _ptr(cache.data), cache.pages, cache.page_size,
-                              _ptr(block_table), block_table.shape[1], _ptr(kv_len), _ptr(q_start), _ptr(tree_mask), seqs,
+    _check(lib().gq_attn_q8_0(_at(q), qs, _at(o), os_, code, _at(cache.data), cache.pages, cache.page_size,
+                              _at(block_table), block_table.shape[1], _at(kv_len), _at(q_start), _at(tree_mask), seqs,
                               max_q, max_kv, hq, cache.kv_heads, hd, hd ** -0.5 if scale is None else scale, softcap,
-                              _ptr(workspace), _stream()), "gq_attn_q8_0")
+                              _at(workspace), _on(q)), "gq_attn_q8_0")
     return o
 
 

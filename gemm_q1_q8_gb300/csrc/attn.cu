@@ -47,13 +47,12 @@ template <int HD, int MT> constexpr int smem_bytes() { return 1024 + ring_bytes<
 // it has after an earlier run began it
 struct Head {
     int first;             // the run that began the tile; -1: none
-    int b, at;
+    int q0, tile0, rows, hk;
 };
 struct Parts {
     float* o;
     float2* ml;
     Head* head;
-    int runs;
 };
 
 // One sequence's share of the work.
@@ -76,22 +75,23 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     return s;
 }
 
-// The units of all sequences, by one warp.
+// The units of all sequences, by one warp, and up to 32 sequences' own (this lane's) for locate().
 template <int ROWS>
-__device__ __forceinline__ long long total_units(const AttnArgs& a, int lane) {
+__device__ __forceinline__ long long total_units(const AttnArgs& a, int lane, long long& mine) {
     long long sum = 0;
     for (int b = lane; b < a.seqs; b += 32) sum += load_seq<ROWS>(a, b).span(a.kv_heads);
+    mine = sum;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 // The sequence that holds unit w, and its first unit.
 template <int ROWS>
-__device__ __forceinline__ int locate(const AttnArgs& a, int lane, long long w, long long& first) {
+__device__ __forceinline__ int locate(const AttnArgs& a, int lane, long long w, long long mine, long long& first) {
     long long before = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += 32) {
         const int b = b0 + lane;
-        const long long mine = b < a.seqs ? load_seq<ROWS>(a, b).span(a.kv_heads) : 0;
+        if (a.seqs > 32) mine = b < a.seqs ? load_seq<ROWS>(a, b).span(a.kv_heads) : 0;
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -109,6 +109,17 @@ __device__ __forceinline__ int locate(const AttnArgs& a, int lane, long long w, 
     first = before;
     return a.seqs;
 }
+// x / d and x % d, in 32 bits where x allows
+__device__ __forceinline__ void div_mod(long long x, int d, int& quot, int& rest) {
+    if (x < 0x7fffffffll) {
+        quot = static_cast<int>(x) / d;
+        rest = static_cast<int>(x) - quot * d;
+    } else {
+        quot = static_cast<int>(x / d);
+        rest = static_cast<int>(x % d);
+    }
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -594,8 +605,10 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const long long total = total_units<kRows>(a, lane);
-    const long long per = max((total + parts.runs - 1) / parts.runs, 1ll);
+    long long own;
+    const long long total = total_units<kRows>(a, lane, own);
+    constexpr int kRunsAll = kBlocks * kWarps;
+    const long long per = max((total + kRunsAll - 1) / kRunsAll, 1ll);
     const int gpp = a.page_size / kvGroup;
 
     if (warp == kWarps) {
@@ -608,7 +621,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
             const long long first_unit = per * blockIdx.x * kWarps;
             if (first_unit >= total) return;
             long long first;
-            p.b = locate<kRows>(a, lane, first_unit, first);
+            p.b = locate<kRows>(a, lane, first_unit, own, first);
             p.s = load_seq<kRows>(a, p.b);
             if (count) {
                 long long rest = w0 - first;
@@ -616,8 +629,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
                     rest -= p.s.span(a.kv_heads);
                     p.s = load_seq<kRows>(a, ++p.b);
                 }
-                p.at = static_cast<int>(rest / p.s.units);
-                p.g = static_cast<int>(rest % p.s.units);
+                div_mod(rest, p.s.units, p.at, p.g);
             }
         }
         int fetched = 0, slot = 0, page = -1, off = 0;
@@ -625,7 +637,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
         auto look_up = [&]() {                                           // used at the next fetch, not waited for here
             const int pi = page_shift >= 0 ? p.g >> page_shift : p.g / gpp;
             off = p.g - pi * gpp;
-            page = __ldg(a.table + static_cast<size_t>(p.b) * a.table_stride + pi);
+            page = a.table[static_cast<size_t>(p.b) * a.table_stride + pi];
         };
         if (count) look_up();
         uint64_t since = globaltimer_ns();
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
     const int count = w0 < total ? static_cast<int>(min(total - w0, per)) : 0;
     uint4* frag = frag_all + warp * kFrags;
     RowInfo* info = info_all[warp];
-    Head head = {-1, 0, 0};
+    Head head = {-1, 0, 0, 0, 0};
     long long open_at = -1;
     if (count) {
         TileT tile;
@@ -686,10 +698,9 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
         uint32_t phase = 0;
         Place<kRows> p;
         long long first;                                                 // the first unit of the tile
-        p.b = locate<kRows>(a, lane, w0, first);
+        p.b = locate<kRows>(a, lane, w0, own, first);
         p.s = load_seq<kRows>(a, p.b);
-        p.at = static_cast<int>((w0 - first) / p.s.units);
-        p.g = static_cast<int>((w0 - first) % p.s.units);
+        div_mod(w0 - first, p.s.units, p.at, p.g);
         first = w0 - p.g;
         bool ok = true;
         for (int done = 0; ok;) {
@@ -733,7 +744,9 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
                     if (r < rows) store4(out + ((tile0 + r) / group) * a.out_stride + ((tile0 + r) % group) * HD + c, v);
                 });
             } else if (end == p.s.units) {                               // its end: for the second kernel
-                head = {static_cast<int>(first / per), p.b, p.at};
+                int begun, unused;
+                div_mod(first, static_cast<int>(per), begun, unused);
+                head = {begun, p.s.q0, tile0, min(min(p.s.T, a.max_q) * group - tile0, kRows), hk};
                 tile.put(lane, false, [&](int r, int c, float4 v, float m, float l) {
                     const size_t at = static_cast<size_t>(run) * kRows + r;
                     *reinterpret_cast<float4*>(parts.o + at * HD + c) = v;
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
                     l = fmaf(f, sl[w + k][r], l);
                     v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
                 }
-                const size_t at = (static_cast<size_t>(parts.runs) + blockIdx.x * kWarps + w) * kRows + r;
+                const size_t at = (static_cast<size_t>(kRunsAll) + blockIdx.x * kWarps + w) * kRows + r;
                 *reinterpret_cast<float4*>(parts.o + at * HD + c) = v;
                 if (c == 0) parts.ml[at] = make_float2(top, l);
             }
@@ -791,51 +804,70 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
 }
 
 // Joins the tiles that runs share, in the order of the runs: the tails of the blocks from the run that began the tile, and the head of the
-// run that ends it.  A warp takes a row of a run's head, four columns a lane (two of them for 256).  Rows of sequences without keys are
-// written here too.
+// run that ends it.  A block looks at one run, a warp at rows of its head, a lane at four columns (256: two times four).  Sixteen parts are
+// requested at once, before their weights are known.  Rows of sequences without keys are written here too.
+template <int PARTS, int MT> __host__ __device__ constexpr int join_warps() { return tile_rows<PARTS, MT>() < 8 ? tile_rows<PARTS, MT>() : 8; }
+
 template <typename T, int HD, int PARTS, int MT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const Parts parts) {
+__global__ void __launch_bounds__(join_warps<PARTS, MT>() * 32) attn_join_kernel(const AttnArgs a, const Parts parts) {
     constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1;
+    constexpr int kRunsAll = kBlocks * kWarps, kBatch = 16 / kRuns;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, group = a.q_heads / a.kv_heads;
-    const int warps_all = gridDim.x * 8, me = blockIdx.x * 8 + (threadIdx.x >> 5);
-    for (int i = me; i < parts.runs * kRows; i += warps_all) {
-        const int run = i / kRows, r = i % kRows;
-        const Head head = parts.head[run];
-        if (head.first < 0) continue;
-        const Seq s = load_seq<kRows>(a, head.b);
-        const int tile0 = (head.at % s.tiles) * kRows, hk = head.at / s.tiles;
-        if (tile0 + r >= min(s.T, a.max_q) * group) continue;
-        float top = kNone, l = 0.f;
-        float4 v[kRuns];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.kv_heads;
+    const int run = blockIdx.x;
+    const Head head = parts.head[run];
+    if (head.first >= 0)
+        for (int r = warp; r < head.rows; r += join_warps<PARTS, MT>()) {
+            // parts: the tail of the run that began the tile, those of the blocks between, the head
+            const int block0 = head.first / kWarps, n = (run + kWarps - 1) / kWarps - block0 + 1;
+            float top = kNone, l = 0.f;
+            float4 v[kRuns];
 #pragma unroll
-        for (int c = 0; c < kRuns; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](size_t slot) {
-            const float2 ml = parts.ml[slot * kRows + r];
-            const float up = fmaxf(top, ml.x), f = ex2(top - up), h = ex2(ml.x - up);
-            l = fmaf(l, f, ml.y * h);
-            top = up;
+            for (int c = 0; c < kRuns; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < n; j0 += kBatch) {
+                auto slot = [&](int j) {
+                    const size_t s = j >= n - 1 ? run : kRunsAll + (j == 0 ? head.first : (block0 + j) * kWarps);
+                    return s * kRows + r;
+                };
+                const int j = j0 + lane % kBatch;
+                const float2 ml = j < n ? parts.ml[slot(j)] : make_float2(kNone, 0.f);
+                float4 x[kBatch][kRuns];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int c = 0; c < kRuns; ++c)
+                        if (j0 + k < n) x[k][c] = *reinterpret_cast<const float4*>(parts.o + slot(j0 + k) * HD + 128 * c + 4 * (lane % kLanes));
+                float up = fmaxf(ml.x, top);
+#pragma unroll
+                for (int o = kBatch / 2; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+                const float f = ex2(ml.x - up), down = ex2(top - up);
+                float sum = f * ml.y;
+#pragma unroll
+                for (int o = kBatch / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l = fmaf(l, down, sum);
+                top = up;
+#pragma unroll
+                for (int c = 0; c < kRuns; ++c) v[c] = make_float4(v[c].x * down, v[c].y * down, v[c].z * down, v[c].w * down);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float h = __shfl_sync(0xffffffffu, f, k);
+                    if (j0 + k < n)
+#pragma unroll
+                        for (int c = 0; c < kRuns; ++c)
+                            v[c] = make_float4(fmaf(h, x[k][c].x, v[c].x), fmaf(h, x[k][c].y, v[c].y), fmaf(h, x[k][c].z, v[c].z), fmaf(h, x[k][c].w, v[c].w));
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* out = static_cast<T*>(a.out) + (head.q0 + (head.tile0 + r) / group) * a.out_stride + (head.hk * group + (head.tile0 + r) % group) * HD;
 #pragma unroll
             for (int c = 0; c < kRuns; ++c)
-                if (lane < kLanes) {
-                    const float4 x = *reinterpret_cast<const float4*>(parts.o + (slot * kRows + r) * HD + 128 * c + 4 * lane);
-                    v[c] = make_float4(fmaf(v[c].x, f, x.x * h), fmaf(v[c].y, f, x.y * h), fmaf(v[c].z, f, x.z * h), fmaf(v[c].w, f, x.w * h));
-                }
-        };
-#pragma unroll 4
-        for (int k = head.first; k < run; k = (k / kWarps + 1) * kWarps) add(static_cast<size_t>(parts.runs) + k);
-        add(run);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* out = static_cast<T*>(a.out) + (s.q0 + (tile0 + r) / group) * a.out_stride + (hk * group + (tile0 + r) % group) * HD;
-#pragma unroll
-        for (int c = 0; c < kRuns; ++c)
-            if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
-    }
-    for (int b = me; b < a.seqs; b += warps_all) {
+                if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
+        }
+    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
         if (a.kv_len[b] > 0) continue;
         const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
-        for (int tok = 0; tok < n; ++tok)
+        for (int tok = warp; tok < n; tok += join_warps<PARTS, MT>())
             for (int d = lane * 4; d < a.q_heads * HD; d += 128)
                 store4(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
     }
@@ -870,14 +902,14 @@ cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
     int shift = -1;
     for (int i = 0; i < 16; ++i)
         if (gpp == 1 << i) shift = i;
+    constexpr size_t runs = kBlocks * kWarps;
     Parts parts;
-    parts.runs = kBlocks * kWarps;
     parts.o = static_cast<float*>(a.workspace);
-    parts.ml = reinterpret_cast<float2*>(parts.o + static_cast<size_t>(2) * parts.runs * kRows * HD);
-    parts.head = reinterpret_cast<Head*>(parts.ml + static_cast<size_t>(2) * parts.runs * kRows);
+    parts.ml = reinterpret_cast<float2*>(parts.o + 2 * runs * kRows * HD);
+    parts.head = reinterpret_cast<Head*>(parts.ml + 2 * runs * kRows);
     const cudaError_t e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), (kWarps + 1) * 32, smem, s, a, parts, shift);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_join_kernel<T, HD, PARTS, MT>, dim3(kBlocks * 2), 256, 0, s, a, parts);
+    return launch_dependent(attn_join_kernel<T, HD, PARTS, MT>, dim3(kBlocks * kWarps), join_warps<PARTS, MT>() * 32, 0, s, a, parts);
 }
 template <int HD, int PARTS, int MT>
 size_t rows_bytes() {

@@ -37,140 +37,179 @@ __global__ void rope_table_kernel(float2* __restrict__ table, int positions, int
     table[n] = make_float2(static_cast<float>(c * size), static_cast<float>(s * size));
 }
 
-__device__ __forceinline__ uint32_t sign_magnitude(int c) { return c < 0 ? static_cast<uint32_t>(128 - c) : static_cast<uint32_t>(c); }
-
-// Four dims of a row, turned: v their values, row the head's row.
+// A token's angles for this thread's four dims: (cos, sin) of each of its pairs (half), or of its two (interleaved)
+struct Turn {
+    float4 z0, z1;
+    int other;             // half: distance to the pairs' other dims; 0: not turned
+    float sign;
+};
 template <typename T>
-__device__ __forceinline__ float4 turned(const AppendArgs& a, const T* row, int d, float4 v, const float2* cs) {
-    if (d >= a.rot) return v;
-    if (a.interleaved) {
-        const float4 z = *reinterpret_cast<const float4*>(cs + d / 2);
-        return make_float4(v.x * z.x - v.y * z.y, v.y * z.x + v.x * z.y, v.z * z.z - v.w * z.w, v.w * z.z + v.z * z.w);
-    }
-    const int half = a.rot / 2;
-    const bool first = d < half;
-    const float4 o = load4(row + (first ? d + half : d - half));
-    const float2* at = cs + (first ? d : d - half);
-    const float4 z0 = *reinterpret_cast<const float4*>(at), z1 = *reinterpret_cast<const float4*>(at + 2);
-    if (first)
-        return make_float4(v.x * z0.x - o.x * z0.y, v.y * z0.z - o.y * z0.w, v.z * z1.x - o.z * z1.y,
-                           v.w * z1.z - o.w * z1.w);
-    return make_float4(v.x * z0.x + o.x * z0.y, v.y * z0.z + o.y * z0.w, v.z * z1.x + o.z * z1.y, v.w * z1.z + o.w * z1.w);
+__device__ __forceinline__ float4 turned(const Turn& t, bool interleaved, float4 v, const T* p) {
+    if (t.other == 0) return v;
+    if (interleaved)
+        return make_float4(v.x * t.z0.x - v.y * t.z0.y, v.y * t.z0.x + v.x * t.z0.y, v.z * t.z0.z - v.w * t.z0.w, v.w * t.z0.z + v.z * t.z0.w);
+    // first half: a cos - b sin; second: b cos + a sin, the sign in front of an exact product
+    const float4 o = load4(p + t.other);
+    return make_float4(v.x * t.z0.x + t.sign * (o.x * t.z0.y), v.y * t.z0.z + t.sign * (o.y * t.z0.w), v.z * t.z1.x + t.sign * (o.z * t.z1.y),
+                       v.w * t.z1.z + t.sign * (o.w * t.z1.w));
 }
 
-// A warp takes 32 * 4 / HD rows (HD = 64: two; 128 and 256: one); the rows of a token are its q heads, k heads, v heads.
+// The rows of a token are its q heads, k heads, v heads.  A warp takes rows part * per .. of one token (HD = 64: two at a time), so that
+// a token's position, slot and angles are looked up once for all of them.
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
-    constexpr int kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1;
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int parts, int per) {
+    constexpr int kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kAt = 32 / kLanes, kU = 4 / kRuns;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int rows = a.q_heads + 2 * a.kv_heads;
-    const long long idx = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
-    const int l = threadIdx.x % kLanes;
-    const bool in = idx < static_cast<long long>(a.tokens) * rows;
-    const int n = in ? static_cast<int>(idx / rows) : 0;
-    int h = in ? static_cast<int>(idx % rows) : 0;
-    const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.kv_heads ? 1 : 2;
-    if (kind == 1) h -= a.q_heads;
-    if (kind == 2) h -= a.q_heads + a.kv_heads;
-    const T* row = kind == 0   ? static_cast<const T*>(a.q) + n * a.q_stride
-                   : kind == 1 ? static_cast<const T*>(a.k) + n * a.k_stride
-                               : static_cast<const T*>(a.v) + n * a.v_stride;
-    row += h * HD;
-    bool ok = in;
-    const float2* cs = nullptr;
+    const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int n = warp / parts, from = (warp % parts) * per, to = min(from + per, rows);
+    if (n >= a.tokens) return;
+    const int l = threadIdx.x % kLanes, half_warp = (threadIdx.x & 31) / kLanes;
+    long long slot = a.slots[n];
+    Turn turn[kRuns];
+#pragma unroll
+    for (int c = 0; c < kRuns; ++c) turn[c].other = 0;
     if (a.rot) {
         const int pos = a.positions[n];
         if (pos < 0 || pos >= a.rope_rows) {
-            if (in && l == 0 && h == 0) report_error(kErrIndex);
-            ok = false;
-        } else {
-            cs = reinterpret_cast<const float2*>(a.rope) + static_cast<size_t>(pos) * (a.rot / 2);
-        }
-    }
-    float4 v[kRuns];
-#pragma unroll
-    for (int c = 0; c < kRuns; ++c) {
-        const int d = c * 128 + 4 * l;
-        v[c] = load4(row + d);
-        if (kind != 2 && cs) v[c] = turned(a, row, d, v[c], cs);
-    }
-    __syncwarp();                                     // q_out may be q: every read of the row is before its writes
-    if (kind == 0 && ok) {
-        T* out = static_cast<T*>(a.q_out) + n * a.q_out_stride + h * HD;
-#pragma unroll
-        for (int c = 0; c < kRuns; ++c) store4(out + c * 128 + 4 * l, v[c]);
-    }
-    long long slot = -1;
-    if (kind != 0 && ok) {
-        slot = a.slots[n];
-        if (slot >= static_cast<long long>(a.pages) * a.page_size) {
             if (l == 0) report_error(kErrIndex);
-            slot = -1;
+            return;                                       // the token is left out
         }
+        const float2* cs = reinterpret_cast<const float2*>(a.rope) + static_cast<size_t>(pos) * (a.rot / 2);
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c) {
+            const int d = c * 128 + 4 * l, half = a.rot / 2;
+            if (d >= a.rot) continue;
+            if (a.interleaved) {
+                turn[c].other = 1;
+                turn[c].z0 = *reinterpret_cast<const float4*>(cs + d / 2);
+            } else {
+                const float2* at = cs + (d < half ? d : d - half);
+                turn[c].z0 = *reinterpret_cast<const float4*>(at);
+                turn[c].z1 = *reinterpret_cast<const float4*>(at + 2);
+                turn[c].other = d < half ? half : -half;
+                turn[c].sign = d < half ? -1.0f : 1.0f;
+            }
+        }
+    }
+    if (slot >= static_cast<long long>(a.pages) * a.page_size) {
+        if (l == 0) report_error(kErrIndex);
+        slot = -1;
     }
     const int tok = static_cast<int>(slot & (kvGroup - 1));
-    const long long page = slot / a.page_size;
-    const int place = static_cast<int>(slot - page * a.page_size);
-    uint8_t* chunk = a.cache + ((page * a.kv_heads + h) * (a.page_size / kvGroup) + place / kvGroup) * kv_chunk_bytes(HD);
+    const long long page = slot < 0 ? 0 : slot / a.page_size;
+    const int group = static_cast<int>(slot - page * a.page_size) / kvGroup, groups = a.page_size / kvGroup;
+    uint8_t* chunk0 = a.cache + (page * a.kv_heads * groups + group) * kv_chunk_bytes(HD);
+
+    for (int r0 = from; r0 < to; r0 += kAt * kU) {
+        float4 v[kU][kRuns];
 #pragma unroll
-    for (int c = 0; c < kRuns; ++c) {
-        const int d = c * 128 + 4 * l;
-        float amax = fmaxf(fmaxf(fabsf(v[c].x), fabsf(v[c].y)), fmaxf(fabsf(v[c].z), fabsf(v[c].w)));
+        for (int u = 0; u < kU; ++u) {
+            const int r = r0 + u * kAt + half_warp;
+            if (r >= to) continue;
+            const T* p = r < a.q_heads              ? static_cast<const T*>(a.q) + n * a.q_stride + r * HD
+                         : r < a.q_heads + a.kv_heads ? static_cast<const T*>(a.k) + n * a.k_stride + (r - a.q_heads) * HD
+                                                      : static_cast<const T*>(a.v) + n * a.v_stride + (r - a.q_heads - a.kv_heads) * HD;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (slot < 0) continue;                       // after the shuffles: the warp's rows may differ
-        const float dd = q8_0_scale(amax);
-        const uint32_t word = sign_magnitude(q8_0_quant(v[c].x, amax, dd)) | sign_magnitude(q8_0_quant(v[c].y, amax, dd)) << 8 |
-                              sign_magnitude(q8_0_quant(v[c].z, amax, dd)) << 16 | sign_magnitude(q8_0_quant(v[c].w, amax, dd)) << 24;
-        *reinterpret_cast<uint32_t*>(chunk + (kind == 1 ? kv_k_word<HD>(tok, d) : kv_v_word<HD>(tok, d))) = word;
-        if ((l & 7) == 0)
-            *reinterpret_cast<uint16_t*>(chunk + (kind == 1 ? kv_ks_offset(HD) : kv_vs_offset(HD)) + kv_scale<HD>(tok, d)) =
-                __half_as_ushort(__float2half_rn(dd));
+            for (int c = 0; c < kRuns; ++c) {
+                const int d = c * 128 + 4 * l;
+                v[u][c] = load4(p + d);
+                if (r < a.q_heads + a.kv_heads) v[u][c] = turned(turn[c], a.interleaved, v[u][c], p + d);
+            }
+        }
+        __syncwarp();                                     // q_out may be q: every read of a row is before its writes
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int r = r0 + u * kAt + half_warp;
+            if (r < min(to, a.q_heads)) {
+                T* out = static_cast<T*>(a.q_out) + n * a.q_out_stride + r * HD;
+#pragma unroll
+                for (int c = 0; c < kRuns; ++c) store4(out + c * 128 + 4 * l, v[u][c]);
+            }
+            if (r0 + (u + 1) * kAt <= a.q_heads) continue;               // all of the warp's rows are queries
+            const bool on = r >= a.q_heads && r < to && slot >= 0, is_k = r < a.q_heads + a.kv_heads;
+            const int h = is_k ? r - a.q_heads : r - a.q_heads - a.kv_heads;
+            uint8_t* chunk = chunk0 + static_cast<long long>(h) * groups * kv_chunk_bytes(HD);
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) {
+                const int d = c * 128 + 4 * l;
+                const float4 x = v[u][c];
+                float amax = r < to ? fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) : 0.f;
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                if (!on) continue;
+                const float dd = q8_0_scale(amax);
+                int code[4];
+                q8_0_quant4(x, amax, dd, code);
+                *reinterpret_cast<uint32_t*>(chunk + (is_k ? kv_k_word<HD>(tok, d) : kv_v_word<HD>(tok, d))) = cache_word(code);
+                if ((l & 7) == 0)
+                    *reinterpret_cast<uint16_t*>(chunk + (is_k ? kv_ks_offset(HD) : kv_vs_offset(HD)) + kv_scale<HD>(tok, d)) =
+                        __half_as_ushort(__float2half_rn(dd));
+            }
+        }
     }
 }
 
-__device__ __forceinline__ float4 code_values(uint32_t w, float d) {
-    auto one = [&](int e) {
-        const uint32_t b = (w >> (8 * e)) & 0xffu;
-        const float m = static_cast<float>(b & 127u) * d;
-        return b & 128u ? -m : m;
-    };
-    return make_float4(one(0), one(1), one(2), one(3));
-}
-
-// As the append: four dims a thread, rows of slots and kv heads; K and V of a row by the same thread.
+// A warp takes `per` heads of one slot (HD = 64: two at a time): a thread four dims of K and of V.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256)
-kv_read_kernel(const uint8_t* __restrict__ cache, long long slots_all, int page_size, int kv_heads,
-               const int64_t* __restrict__ slots, int n, T* __restrict__ k_out, T* __restrict__ v_out) {
-    constexpr int kWords = HD / 4;
+kv_read_kernel(const uint8_t* cache, long long slots_all, int page_size, int kv_heads, const int64_t* slots, int n, int parts, int per, T* k_out,
+               T* v_out) {
+    constexpr int kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kAt = 32 / kLanes, kU = 4 / kRuns;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const long long row = i / kWords;
-    if (row >= static_cast<long long>(n) * kv_heads) return;
-    const int d = 4 * static_cast<int>(i % kWords);
-    const int h = static_cast<int>(row % kv_heads);
-    const long long slot = slots[row / kv_heads];
-    float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+    const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int i = warp / parts, from = (warp % parts) * per, to = min(from + per, kv_heads);
+    if (i >= n) return;
+    const int l = threadIdx.x % kLanes, half_warp = (threadIdx.x & 31) / kLanes;
+    long long slot = slots[i];
     if (slot >= slots_all) {
-        if (d == 0 && h == 0) report_error(kErrIndex);
-    } else if (slot >= 0) {
-        const int tok = static_cast<int>(slot & (kvGroup - 1));
-        const long long page = slot / page_size;
-        const int place = static_cast<int>(slot - page * page_size);
-        const uint8_t* chunk = cache + ((page * kv_heads + h) * (page_size / kvGroup) + place / kvGroup) * kv_chunk_bytes(HD);
-        const int sc = kv_scale<HD>(tok, d);
-        if (k_out)
-            kv = code_values(*reinterpret_cast<const uint32_t*>(chunk + kv_k_word<HD>(tok, d)),
-                             f16_to_f32(*reinterpret_cast<const uint16_t*>(chunk + kv_ks_offset(HD) + sc)));
-        if (v_out)
-            vv = code_values(*reinterpret_cast<const uint32_t*>(chunk + kv_v_word<HD>(tok, d)),
-                             f16_to_f32(*reinterpret_cast<const uint16_t*>(chunk + kv_vs_offset(HD) + sc)));
+        if (l == 0) report_error(kErrIndex);
+        slot = -1;
     }
-    if (k_out) store4(k_out + row * HD + d, kv);
-    if (v_out) store4(v_out + row * HD + d, vv);
+    const int tok = static_cast<int>(slot & (kvGroup - 1));
+    const long long page = slot < 0 ? 0 : slot / page_size;
+    const int group = static_cast<int>(slot - page * page_size) / kvGroup, groups = page_size / kvGroup;
+    const uint8_t* chunk0 = cache + (page * kv_heads * groups + group) * kv_chunk_bytes(HD);
+    const size_t out0 = static_cast<size_t>(i) * kv_heads * HD;
+    for (int h0 = from; h0 < to; h0 += kAt * kU) {
+        uint32_t kw[kU][kRuns], vw[kU][kRuns], ks[kU][kRuns], vs[kU][kRuns];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) {
+                const int h = h0 + u * kAt + half_warp, d = c * 128 + 4 * l;
+                kw[u][c] = vw[u][c] = ks[u][c] = vs[u][c] = 0;
+                if (h >= to || slot < 0) continue;
+                const uint8_t* chunk = chunk0 + static_cast<long long>(h) * groups * kv_chunk_bytes(HD);
+                const int sc = kv_scale<HD>(tok, d);
+                if (k_out) {
+                    kw[u][c] = *reinterpret_cast<const uint32_t*>(chunk + kv_k_word<HD>(tok, d));
+                    ks[u][c] = *reinterpret_cast<const uint16_t*>(chunk + kv_ks_offset(HD) + sc);
+                }
+                if (v_out) {
+                    vw[u][c] = *reinterpret_cast<const uint32_t*>(chunk + kv_v_word<HD>(tok, d));
+                    vs[u][c] = *reinterpret_cast<const uint16_t*>(chunk + kv_vs_offset(HD) + sc);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) {
+                const int h = h0 + u * kAt + half_warp, d = c * 128 + 4 * l;
+                if (h >= to) continue;
+                if (k_out) store4(k_out + out0 + h * HD + d, cache_values(kw[u][c], ks[u][c]));
+                if (v_out) store4(v_out + out0 + h * HD + d, cache_values(vw[u][c], vs[u][c]));
+            }
+    }
+}
+
+// Rows of a token that a warp takes: all of them where the tokens fill the GPU (152 SMs, some 64 warps each), fewer for few tokens
+int rows_per_warp(long long tokens, int rows, int step) {
+    int per = (rows + step - 1) / step * step;
+    while (per > step && tokens * ((rows + per - 1) / per) < 152 * 64) per = (per / 2 + step - 1) / step * step;
+    return per;
 }
 
 template <typename K, typename... A>
@@ -190,16 +229,15 @@ cudaError_t launch_dependent(K kernel, long long blocks, int threads, cudaStream
 
 template <typename T, int HD>
 cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
-    const long long rows = static_cast<long long>(a.tokens) * (a.q_heads + 2 * a.kv_heads);
-    const int per = 256 / (HD == 64 ? 16 : 32);
-    return launch_dependent(kv_append_kernel<T, HD>, (rows + per - 1) / per, 256, s, a);
+    const int rows = a.q_heads + 2 * a.kv_heads, per = rows_per_warp(a.tokens, rows, HD == 64 ? 2 : 1), parts = (rows + per - 1) / per;
+    return launch_dependent(kv_append_kernel<T, HD>, (static_cast<long long>(a.tokens) * parts + 7) / 8, 256, s, a, parts, per);
 }
 template <typename T, int HD>
 cudaError_t read_go(const uint8_t* cache, int pages, int page_size, int kv_heads, const int64_t* slots, int n, void* k,
                     void* v, cudaStream_t s) {
-    const long long threads = static_cast<long long>(n) * kv_heads * (HD / 4);
-    return launch_dependent(kv_read_kernel<T, HD>, (threads + 255) / 256, 256, s, cache,
-                            static_cast<long long>(pages) * page_size, page_size, kv_heads, slots, n, static_cast<T*>(k),
+    const int per = rows_per_warp(n, kv_heads, HD == 64 ? 2 : 1), parts = (kv_heads + per - 1) / per;
+    return launch_dependent(kv_read_kernel<T, HD>, (static_cast<long long>(n) * parts + 7) / 8, 256, s, cache,
+                            static_cast<long long>(pages) * page_size, page_size, kv_heads, slots, n, parts, per, static_cast<T*>(k),
                             static_cast<T*>(v));
 }
 

@@ -55,6 +55,38 @@ __device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Four values of a block quantized by the rule of q8_0_quant (round half up of the rounded quotient x / d), without its
+// divisions: x times the reciprocal is within 2^-16 of the quotient, so where it is further than 2^-11 from a tie its nearest integer is the
+// code; the few others (and NaN) are divided.  16 instructions instead of some 80.
+__device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int (&c)[4]) {
+    const float r = dd >= 0x1p-120f ? __frcp_rn(dd) : 0.0f, magic = 12582912.0f;       // 1.5 * 2^23: the sum's low bits are the integer
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    bool far = dd >= 0x1p-120f || amax == 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float t = fmaf(x[i], r, magic);
+        c[i] = __float_as_int(t) - __float_as_int(magic);
+        far = far && fabsf(fmaf(x[i], r, magic - t)) <= 0.5f - 0x1p-11f;
+    }
+    if (!far)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = q8_0_quant(x[i], amax, dd);
+}
+
+// Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d
+__device__ __forceinline__ uint32_t cache_word(const int (&c)[4]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= static_cast<uint32_t>(c[i] < 0 ? 128 - c[i] : c[i]) << (8 * i);
+    return w;
+}
+__device__ __forceinline__ float4 cache_values(uint32_t w, uint32_t d16) {
+    const float d = f16_to_f32(d16) * 16777216.0f;                      // a code's bits as f16 are code * 2^-24
+    const uint32_t lo = __byte_perm(w, 0, 0x1100) & 0x807f807fu, hi = __byte_perm(w, 0, 0x3322) & 0x807f807fu;
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x * d, a.y * d, b.x * d, b.y * d);
+}
+
 // ---------------------------------------------------------------- the cache (layout: include/gq.h)
 constexpr int kvGroup = 16;                                             // tokens of a chunk
 __host__ __device__ constexpr int kv_chunk_bytes(int hd) { return 34 * hd; }

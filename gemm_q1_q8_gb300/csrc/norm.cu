@@ -60,9 +60,9 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
     for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float dd = q8_0_scale(amax);
     const uint16_t dbits = __half_as_ushort(__float2half_rn(dd));
-    const int c0 = q8_0_quant(y.x, amax, dd), c1 = q8_0_quant(y.y, amax, dd);
-    const int c2 = q8_0_quant(y.z, amax, dd), c3 = q8_0_quant(y.w, amax, dd);
-    const uint32_t word = (c0 & 0xff) | (c1 & 0xff) << 8 | (c2 & 0xff) << 16 | static_cast<uint32_t>(c3 & 0xff) << 24;
+    int cd[4];
+    q8_0_quant4(y, amax, dd, cd);
+    const uint32_t word = __byte_perm(__byte_perm(cd[0], cd[1], 0x0040), __byte_perm(cd[2], cd[3], 0x0040), 0x5410);
     const size_t block = row * (a.k / 32) + (i >> 5);
     if (a.act && on) {
         uint16_t* p = reinterpret_cast<uint16_t*>(a.act + block * 34);
@@ -78,8 +78,9 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
         // three bf16 parts of f16(d) * q, element u and u + 16 of the block side by side: the lane of the
         // lower half takes its partner's four
         const float ds = f16_to_f32(dbits);
-        float pv[4] = {__fmul_rn(ds, static_cast<float>(c0)), __fmul_rn(ds, static_cast<float>(c1)),
-                       __fmul_rn(ds, static_cast<float>(c2)), __fmul_rn(ds, static_cast<float>(c3))};
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pv[e] = __fmul_rn(ds, static_cast<float>(cd[e]));
         uint32_t w[3][4];
 #pragma unroll
         for (int p = 0; p < 3; ++p)
@@ -187,7 +188,7 @@ cudaError_t norm_type(const NormArgs& a, int m, cudaStream_t s) {
 
 // Eight threads a block, four values each.
 template <typename T>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ act, long long blocks, T* __restrict__ out) {
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* act, long long blocks, T* out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
