@@ -29,6 +29,7 @@ namespace gq {
 GQ_ERROR_ACCESSOR(attn)
 namespace {
 
+constexpr int kManyRows = 256;                    // rows a kv head from which attn_tiles.cu takes the call
 constexpr int kBlocks = 152;                       // one thread block an SM
 constexpr float kNone = -1e30f;                    // running maximum of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;
@@ -949,6 +950,7 @@ size_t attn_workspace_bytes(int, int max_q, int q_heads, int kv_heads, int head_
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
+    if (head_dim <= 128 && static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads) >= kManyRows) return launch_attn_tiles(a, type, head_dim, s);
     if (type == GQ_F32)
         return head_dim == 64 ? rows_type<float, 64>(a, s) : head_dim == 128 ? rows_type<float, 128>(a, s) : rows_type<float, 256>(a, s);
     if (type == GQ_F16)

@@ -1,0 +1,608 @@
+// Attention over the paged Q8_0 cache for many rows (prefill chunks): 128 rows a thread block on the 5th-generation tensor cores.
+//
+// Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
+// keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
+//
+// Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
+// thread; keys and values (B) in shared memory (128-byte swizzle), converted from the cache's codes by eight warps.  With A in tensor
+// memory a 128 x 64 x 16 MMA reads 2 KB of shared memory instead of 6, which would bound it.
+// A code is the f16 subnormal magnitude * 2^-24 (attn.cu); times 2^15 it is normal, times the scale it is the value, rounded once to f16; and
+// fma(code, scale, -value) is the exact rest: two f16 parts hold all 18 bits.  f32 queries take two parts of everything and three
+// products (high x high, low x high, high x low): 2^-22 of a term.  16-bit queries take one part: 2^-11.  Powers of two keep the parts in f16's
+// range: a row's largest query at 2^14, a tile's largest key and value scale below 1, weights at 2^11 at most before kSlack; weights below 2^-36
+// of a row's largest are rounded absolutely (the row kernel keeps them).
+//
+// Keys' and values' orders are free where they are contracted: dims stand in the order in which a 16-byte unit of the cache holds them
+// (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
+// chunks without moving single bytes.
+//
+//   warps 0-3   softmax: scores from tensor memory (a row a thread, so no shuffles), weights back to it; the running maximum moves (and the
+//               sums in tensor memory are multiplied) only where a row's scores pass it by 2^kSlack
+//   warps 4-11  keys and values of a tile, two stages
+//   warp 12     MMA issue: scores of tile i + 1 before the sums of tile i, so the tensor cores work during the softmax
+//   warp 13     bulk copies of the chunks, two stages
+#include "layer_ops.cuh"
+#include "tc_common.cuh"
+
+namespace gq {
+GQ_ERROR_ACCESSOR(attn_tiles)
+namespace {
+
+constexpr int kRows = 128, kTok = 64, kGroups = kTok / kvGroup;
+constexpr int kWarpKV = 4, kNumKV = 8, kWarpMma = 12, kThreads = 14 * 32;
+constexpr float kNone = -1e30f, kLog2e = 1.4426950408889634f;
+constexpr float kLift = 11.f, kSlack = 4.f;
+constexpr int kColS = 0, kColP = 128, kColQ = 256, kColO = 384, kTmemCols = 512;
+
+struct Info {
+    float kfactor;         // 2^e of the keys' scales
+    int vexp;              // e of the values' scales
+    int have;              // a bit for each chunk whose page exists
+    int odd;               // whether some value scale is not finite:
+    uint32_t bad[2];       // those tokens' columns
+};
+struct Bars {
+    uint64_t rawfull[2], rawfree[2], kfull[2], vfull[2], qk[2], pv[2], sfree[2], pfull[2], qfull, final_;
+    uint32_t tmem;
+    int abort;
+    int have[2];
+    Info info[4];
+};
+
+template <int HD, int PARTS> struct Smem {
+    static constexpr int kRaw = kGroups * kv_chunk_bytes(HD);             // a tile's chunks
+    static constexpr int kK = kTok * HD * 2, kV = HD * kTok * 2;          // one part of a tile's keys, values
+    static constexpr int kKat = 0, kVat = 2 * PARTS * kK, kRawAt = kVat + 2 * PARTS * kV, kBars = kRawAt + 2 * kRaw;
+    static constexpr int kAll = 1024 + kBars + sizeof(Bars);
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
+__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t codes2(uint32_t lo, uint32_t hi, uint32_t sel) { return __byte_perm(lo, hi, sel) & 0x807f807fu; }
+
+template <int N>
+__device__ __forceinline__ constexpr uint32_t idesc() {                   // D f32, A and B f16, both K-major, M = 128
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
+        "r"(desc), "r"(accumulate)
+        : "memory");
+}
+// 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 16 columns
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Column n of a tile's scores holds this token of the tile
+__device__ __forceinline__ constexpr int token_of(int n) { return (n & ~15) + 2 * (n & 3) + ((n >> 2) & 1) + 8 * ((n >> 3) & 1); }
+
+// What a tile's scales need to get near 1: the exponent e of the largest finite one (all below 2^e), by a whole warp.  `edge`: only the
+// first `end` tokens, of the chunks in `have`, count.
+template <int HD>
+__device__ __forceinline__ int scales_exponent(const uint8_t* raw, int offset, int lane, bool edge, int end, int have, bool& odd) {
+    constexpr int kWords = kvGroup * (HD / 32) / 2;                       // 32-bit words of a chunk's scales
+    uint32_t top = 0;
+    bool strange = false;
+#pragma unroll
+    for (int i = 0; i < kGroups * kWords / 32; ++i) {
+        const int at = i * 32 + lane;
+        uint32_t w = *reinterpret_cast<const uint32_t*>(raw + (at / kWords) * kv_chunk_bytes(HD) + offset + 4 * (at % kWords));
+        if (edge) {
+            const int grp = at / kWords, at4 = at % kWords / (HD / 64), t = at4 >> 2, p = at4 & 3;       // scales stand by 4 t + p
+            if (16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= end || !(have >> grp & 1)) w = 0;
+        }
+        strange = strange || ((((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0);
+        if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;                   // not finite: does not count
+        if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
+        top = max(top, max(w & 0x7c00u, (w >> 16) & 0x7c00u));
+    }
+    odd = __any_sync(0xffffffffu, strange);
+    return static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 10) - 14;
+}
+// 2^(9 - e) as the product of two f16 powers of two
+__device__ __forceinline__ void scale_factors(int e, __half2& f1, __half2& f2) {
+    const int x = 9 - e, y = x / 2;                                       // -8 <= x <= 23
+    f1 = __float2half2_rn(pow2i(y));
+    f2 = __float2half2_rn(pow2i(x - y));
+}
+
+// Eight values (four pairs) as one or two parts: 16 bytes each
+template <int PARTS>
+__device__ __forceinline__ void put8(uint8_t* dst, int part_bytes, const uint32_t (&code)[4], const __half2 (&s)[4]) {
+    const __half2 up = __float2half2_rn(32768.0f);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = __hmul2(h2(code[i]), up);
+        const __half2 v = __hmul2(x, s[i]);
+        hi[i] = u32(v);
+        if (PARTS == 2) lo[i] = u32(__hfma2(x, s[i], __hneg2(v)));
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (PARTS == 2) *reinterpret_cast<uint4*>(dst + part_bytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+template <typename T, int HD, int PARTS>
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a) {
+    using M = Smem<HD, PARTS>;
+    constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32, kAtoms = HD / 64;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = smem_align1024(smem_raw);
+    uint8_t* sk = base + M::kKat;                          // [2][PARTS][kAtoms][64 rows x 128 bytes]
+    uint8_t* sv = base + M::kVat;                          // [2][PARTS][HD rows x 128 bytes]
+    uint8_t* sraw = base + M::kRawAt;                      // [2][kGroups][chunk]
+    Bars* bars = reinterpret_cast<Bars*>(base + M::kBars);
+    volatile int* abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.z, hk = blockIdx.y, group = a.q_heads / a.kv_heads;
+    const int q0 = a.q_start[b], T_ = a.q_start[b + 1] - q0, L = a.kv_len[b];
+    if (threadIdx.x == 0 && (T_ > a.max_q || L > a.max_kv)) report_error(kErrIndex);
+    const int rows = min(T_, a.max_q) * group;
+    const int tile0 = (gridDim.x - 1 - blockIdx.x) * kRows;               // the longest first
+    if (tile0 >= rows) return;
+    const int len = min(max(L, 0), a.max_kv);
+    // keys that the last of the rows sees
+    const int seen = a.tree ? len : min(len, max(L - T_ + min(tile0 + kRows, rows) / group + (min(tile0 + kRows, rows) % group ? 1 : 0), 0));
+    const int tiles = (seen + kTok - 1) / kTok;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->rawfull[s], 1);
+            mbar_init(&bars->rawfree[s], kNumKV);
+            mbar_init(&bars->kfull[s], kNumKV);
+            mbar_init(&bars->vfull[s], kNumKV);
+            mbar_init(&bars->qk[s], 1);
+            mbar_init(&bars->pv[s], 1);
+            mbar_init(&bars->sfree[s], 4);
+            mbar_init(&bars->pfull[s], 4);
+        }
+        mbar_init(&bars->qfull, 4);
+        mbar_init(&bars->final_, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    if (warp < kWarpKV) {
+        // ---------------- softmax: row tile0 + 32 * warp + lane
+        const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const int r = tile0 + warp * 32 + lane;
+        const bool in = r < rows;
+        const int tok = in ? r / group : 0, h = in ? r % group : 0;
+        float rs;
+        {
+            const T* q = static_cast<const T*>(a.q) + (q0 + tok) * a.q_stride + (hk * group + h) * HD;
+            float amax = 0.f;
+            for (int d = 0; d < HD; d += 4) {
+                const float4 v = load4(q + d);
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            }
+            const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+            const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
+            const float f = in ? pow2i(up) : 0.f;
+            rs = (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) * pow2i(-up);
+#pragma unroll
+            for (int c = 0; c < kAtoms; ++c)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {                          // four dims: positions 4 i .. of this half of the atom
+                        const int t = 2 * half + (i >> 2), hh = (i >> 1) & 1, bb = i & 1;
+                        float4 v = load4(q + 64 * c + 32 * hh + 16 * bb + 4 * t);
+                        v = in ? make_float4(v.x * f, v.y * f, v.z * f, v.w * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
+                        hi[2 * i] = u32(x);
+                        hi[2 * i + 1] = u32(y);
+                        if (PARTS == 2) {
+                            const float2 fx = __half22float2(x), fy = __half22float2(y);
+                            lo[2 * i] = u32(__floats2half2_rn(v.x - fx.x, v.y - fx.y));
+                            lo[2 * i + 1] = u32(__floats2half2_rn(v.z - fy.x, v.w - fy.y));
+                        }
+                    }
+                    tc_st16(tl + kColQ + 32 * c + 16 * half, hi);
+                    if (PARTS == 2) tc_st16(tl + kColQ + HD / 2 + 32 * c + 16 * half, lo);
+                }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->qfull);
+        }
+        const int last = in ? L - T_ + tok : -1;
+        const unsigned long long bits = a.tree && in ? a.tree[q0 + tok] : 0ull;
+        float m = kNone, l = 0.f;
+        int vref = -24;
+        bool ok = true;
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i & 1;
+            const uint32_t par = (i >> 1) & 1;
+            // (the scores' MMAs were issued after the keys' barrier, so what stands in `info` was written before)
+            if (!wait_or_abort_sleep(&bars->qk[s], par, abort)) {
+                ok = false;
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            const Info& info = bars->info[i & 3];
+            const float x_of = rs * info.kfactor;
+            const int vexp = info.vexp, have = info.have, odd = info.odd;
+            const uint32_t bad0 = odd ? info.bad[0] : 0u, bad1 = odd ? info.bad[1] : 0u;
+            float x[kTok];
+            tc_ld32(tl + kColS + s * kTok, x);
+            tc_ld32(tl + kColS + s * kTok + 32, x + 32);
+            tc_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->sfree[s]);
+            const int j0 = i * kTok;
+            if (a.softcap > 0.f) {
+#pragma unroll
+                for (int n = 0; n < kTok; ++n) {
+                    // tanh: 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely; f32 queries take the function
+                    const float y = x[n] * x_of;
+                    x[n] = a.softcap * kLog2e * (PARTS == 2 ? tanhf(y) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f));
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < kTok; ++n) x[n] *= x_of;
+            }
+            if (j0 + kTok > min(L - T_, a.max_kv) || have != (1 << kGroups) - 1) {
+#pragma unroll
+                for (int n = 0; n < kTok; ++n) {
+                    const int j = j0 + token_of(n), rel = j - (L - T_);
+                    bool vis = last >= 0 && j < len && (have >> (n >> 4) & 1);
+                    vis = vis && (a.tree ? rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)) : j <= last);
+                    if (!vis) x[n] = -INFINITY;
+                }
+            }
+            float top = x[0];
+#pragma unroll
+            for (int n = 1; n < kTok; ++n) top = fmaxf(top, x[n]);
+            const bool move = top > m + kSlack || vexp > vref;
+            if (__any_sync(0xffffffffu, move)) {
+                const float mn = top > m + kSlack ? top : m;
+                const int vn = max(vexp, vref);
+                const float down = ex2(m - mn), downo = down * pow2i(max(vref - vn, -126));
+                l *= down;
+                m = mn;
+                vref = vn;
+                if (i > 0) {
+                    if (!wait_or_abort(&bars->pv[s ^ 1], ((i - 1) >> 1) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < HD; c += 32) {
+                        float o[32];
+                        tc_ld32(tl + kColO + c, o);
+                        tc_wait_ld();
+                        uint32_t w[32];
+#pragma unroll
+                        for (int n = 0; n < 32; ++n) w[n] = __float_as_uint(o[n] * downo);
+                        tc_st32(tl + kColO + c, w);
+                    }
+                    tc_wait_st();
+                }
+            }
+            if (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort)) {     // the weights' slot is free
+                ok = false;
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            const float from = m - kLift - static_cast<float>(vexp - vref), lower = pow2i(max(vref - vexp, 0)) * 0x1p-11f;
+            float sum = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    const float p0 = ex2(x[32 * half + 2 * n] - from), p1 = ex2(x[32 * half + 2 * n + 1] - from);
+                    sum += p0 + p1;
+                    const __half2 v = __floats2half2_rn(p0, p1);
+                    hi[n] = u32(v);
+                    if (PARTS == 2) {
+                        const float2 f = __half22float2(v);
+                        lo[n] = u32(__floats2half2_rn(p0 - f.x, p1 - f.y));
+                    }
+                }
+                const uint32_t col = tl + kColP + s * PARTS * 32 + 16 * half;
+                tc_st16(col, hi);
+                if (PARTS == 2) tc_st16(col + 32, lo);
+            }
+            l = fmaf(sum, lower, l);
+            if (odd)                                                      // a value that is not finite, seen by this row
+#pragma unroll
+                for (int n = 0; n < kTok; ++n)
+                    if (((n < 32 ? bad0 : bad1) >> (n & 31) & 1u) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->pfull[s]);
+        }
+        if (ok && tiles > 0 && !wait_or_abort(&bars->pv[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort)) ok = false;
+        __syncwarp();
+        if (ok) {
+            tc_fence_after();
+            const float back = l == 0.f || tiles == 0 ? 0.f : pow2i(vref - 11) / l;
+            T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD;
+#pragma unroll
+            for (int c = 0; c < HD; c += 32) {
+                float o[32];
+                if (tiles > 0) {
+                    tc_ld32(tl + kColO + c, o);
+                    tc_wait_ld();
+                }
+                if (in)
+#pragma unroll
+                    for (int n = 0; n < 32; n += 4)
+                        store4(out + c + n, back == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                        : make_float4(o[n] * back, o[n + 1] * back, o[n + 2] * back, o[n + 3] * back));
+            }
+        }
+    } else if (warp < kWarpMma) {
+        // ---------------- keys and values
+        const int w8 = warp - kWarpKV, dt = threadIdx.x - kWarpKV * 32;
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i & 1;
+            const uint32_t par = (i >> 1) & 1;
+            if (!wait_or_abort(&bars->rawfull[s], par, abort)) break;
+            __syncwarp();
+            const uint8_t* raw = sraw + s * M::kRaw;
+            const int have = bars->have[s], j0 = i * kTok;
+            const bool edge = j0 + kTok > len || have != (1 << kGroups) - 1;      // some of the tile's tokens do not exist
+            // keys, once the scores of the tile before the last are done
+            if (i >= 2 && !wait_or_abort(&bars->qk[s], par ^ 1, abort)) break;
+            __syncwarp();
+            bool odd;
+            {
+                const int e = scales_exponent<HD>(raw, kv_ks_offset(HD), lane, edge, len - j0, have, odd);
+                __half2 f1, f2;
+                scale_factors(e, f1, f2);
+                if (dt == 0) {
+                    bars->info[i & 3].kfactor = pow2i(e);
+                    bars->info[i & 3].have = have;
+                }
+                constexpr int kUnits = HD / 16;
+#pragma unroll
+                for (int k = 0; k < kTok * kUnits / (kNumKV * 32); ++k) {
+                    const int id = dt + k * kNumKV * 32, ta = id / kUnits, up = id % kUnits, grp = ta >> 4, tok = ta & 15;
+                    const int u = HD > 64 ? up ^ (4 * (tok & 1)) : up, c = u >> 2, t = u & 3;
+                    const int tt = (tok & 7) >> 1, p = (tok & 1) + 2 * (tok >> 3), n = 16 * grp + 4 * p + tt;
+                    const uint8_t* ch = raw + grp * kChunk;
+                    const uint4 w = *reinterpret_cast<const uint4*>(ch + tok * HD + up * 16);
+                    uint32_t sc = *reinterpret_cast<const uint32_t*>(ch + kv_ks_offset(HD) + 2 * ((4 * tt + p) * kNb + 2 * c));
+                    if (edge && (j0 + ta >= len || !(have >> grp & 1))) sc = 0;
+                    const bool swap = HD > 64 ? c & 1 : tok & 1;           // chunks of one store differ in their banks
+                    uint8_t* row = sk + s * PARTS * M::kK + c * (kTok * 128);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int hh = swap ? x ^ 1 : x;
+                        const uint32_t wa = hh ? w.z : w.x, wb = hh ? w.w : w.y;
+                        const __half2 sh = __hmul2(__hmul2(h2(__byte_perm(sc, 0, hh ? 0x3232 : 0x1010)), f1), f2);
+                        const uint32_t code[4] = {codes2(wa, 0, 0x1100), codes2(wa, 0, 0x3322), codes2(wb, 0, 0x1100), codes2(wb, 0, 0x3322)};
+                        const __half2 sa[4] = {sh, sh, sh, sh};
+                        put8<PARTS>(row + swz128(n, 2 * t + hh), M::kK, code, sa);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            // values' exponent, needed with the scores
+            const int ve = scales_exponent<HD>(raw, kv_vs_offset(HD), lane, edge, len - j0, have, odd);
+            if (dt == 0) {
+                bars->info[i & 3].vexp = ve;
+                bars->info[i & 3].odd = odd;
+            }
+            if (odd && w8 < 2) {                                          // which tokens: columns 32 w8 + lane
+                const int n = 32 * w8 + lane, grp = n >> 4, p = (n >> 2) & 3, t = n & 3;
+                bool strange = false;
+                for (int c = 0; c < kNb; ++c)
+                    strange |= (*reinterpret_cast<const uint16_t*>(raw + grp * kChunk + kv_vs_offset(HD) + 2 * ((4 * t + p) * kNb + c)) & 0x7c00) == 0x7c00;
+                const uint32_t mask = __ballot_sync(0xffffffffu, strange);
+                if (lane == 0) bars->info[i & 3].bad[w8] = mask;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->kfull[s]);
+            // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..)
+            if (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort)) break;
+            {
+                __half2 f1, f2;
+                scale_factors(ve, f1, f2);
+                const int grp = w8 >> 1, o = w8 & 1;
+                const int g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, c0 = HD == 64 ? lane & 1 : lane & 3;
+                const uint8_t* ch = raw + grp * kChunk;
+#pragma unroll
+                for (int hc = 0; hc < (HD > 128 ? HD / 128 : 1); ++hc) {
+                    const int c = c0 + 4 * hc;
+                    uint32_t w[8], sc[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int p = 2 * o + (k >> 2), t = k & 3;
+                        const uint8_t* r = ch + kv_v_offset(HD) + (4 * p + t) * HD;
+                        w[k] = *reinterpret_cast<const uint32_t*>(HD == 64 ? r + 8 * (g ^ (4 * (t >> 1))) + 4 * c : r + 128 * hc + 16 * (g ^ (2 * t)) + 4 * c0);
+                        sc[k] = *reinterpret_cast<const uint16_t*>(ch + kv_vs_offset(HD) + 2 * ((4 * t + p) * kNb + c));
+                        if (edge && (j0 + 16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= len || !(have >> grp & 1))) sc[k] = 0;
+                        if (odd && (sc[k] & 0x7c00u) == 0x7c00u) sc[k] = 0;
+                    }
+                    __half2 sh[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sh[k] = __hmul2(__hmul2(h2(sc[2 * k] | sc[2 * k + 1] << 16), f1), f2);
+                    uint8_t* dst = sv + s * PARTS * M::kV;
+#pragma unroll
+                    for (int x = 0; x < (HD == 64 ? 2 : 4); ++x) {
+                        const int e = HD == 64 ? 2 * (lane >> 4) + ((x + c0) & 1) : (x + c0) & 3;      // a store's chunks differ in their banks
+                        const uint32_t sel = 0x4400u + 0x1111u * e;
+                        const uint32_t code[4] = {codes2(w[0], w[1], sel), codes2(w[2], w[3], sel), codes2(w[4], w[5], sel), codes2(w[6], w[7], sel)};
+                        put8<PARTS>(dst + swz128(32 * c + 4 * g + e, w8), M::kV, code, sh);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars->vfull[s]);
+                mbar_arrive(&bars->rawfree[s]);
+            }
+        }
+    } else if (warp == kWarpMma) {
+        // ---------------- MMAs, by one thread
+        if (lane == 0) {
+            bool ok = tiles > 0 && wait_or_abort(&bars->qfull, 0, abort);
+            auto sums = [&](int i) {                                      // o += weights * values of tile i
+                const int s = i & 1;
+                const uint32_t par = (i >> 1) & 1;
+                if (!wait_or_abort(&bars->vfull[s], par, abort) || !wait_or_abort(&bars->pfull[s], par, abort)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(tmem + kColO, tmem + kColP + (s * PARTS + (t == 1)) * 32 + 8 * k,
+                               smem_desc(sv + (s * PARTS + (t == 2)) * M::kV + 32 * k), idesc<HD>(), i | t | k ? 1u : 0u);
+                tc_commit(&bars->pv[s]);
+                return true;
+            };
+            for (int i = 0; ok && i < tiles; ++i) {
+                const int s = i & 1;
+                const uint32_t par = (i >> 1) & 1;
+                ok = wait_or_abort(&bars->kfull[s], par, abort) && (i < 2 || wait_or_abort(&bars->sfree[s], par ^ 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k)
+                        mma_ts(tmem + kColS + s * kTok, tmem + kColQ + (t == 1) * (HD / 2) + 8 * k,
+                               smem_desc(sk + (s * PARTS + (t == 2)) * M::kK + (k >> 2) * (kTok * 128) + 32 * (k & 3)), idesc<kTok>(), t | k ? 1u : 0u);
+                tc_commit(&bars->qk[s]);
+                if (i > 0) ok = sums(i - 1);
+            }
+            if (ok) sums(tiles - 1);
+            tc_commit(&bars->final_);                                     // all MMAs issued so far complete before TMEM is freed
+        }
+    } else {
+        // ---------------- chunks of a tile: lane g one of its groups
+        const int gpp = a.page_size / kvGroup;
+        int issued = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int s = i & 1;
+            int page = -1, off = 0;
+            const int g = i * kGroups + lane;
+            const bool wanted = lane < kGroups && g * kvGroup < len;
+            if (wanted) {
+                const int pi = g / gpp;
+                off = g - pi * gpp;
+                page = a.table[static_cast<size_t>(b) * a.table_stride + pi];
+                if (page < 0 || page >= a.pages) {
+                    page = -1;
+                    report_error(kErrIndex);
+                }
+            }
+            const unsigned there = __ballot_sync(0xffffffffu, page >= 0), missing = __ballot_sync(0xffffffffu, wanted && page < 0);
+            if (i >= 2 && !wait_or_abort(&bars->rawfree[s], ((i >> 1) & 1) ^ 1, abort)) break;
+            if (lane == 0) {
+                bars->have[s] = ((1 << kGroups) - 1) & ~missing;          // chunks past the end count as there: their tokens are past the end
+                if (there) mbar_arrive_expect_tx(&bars->rawfull[s], __popc(there) * kChunk);
+                else mbar_arrive(&bars->rawfull[s]);
+            }
+            __syncwarp();
+            if (page >= 0)
+                bulk_g2s(sraw + s * M::kRaw + lane * kChunk, a.cache + ((static_cast<size_t>(page) * a.kv_heads + hk) * gpp + off) * kChunk, kChunk,
+                         &bars->rawfull[s]);
+            issued = i + 1;
+        }
+        __syncwarp();
+        if (*abort)                                                       // copies in flight land before shared memory goes away
+            for (int i = max(issued - 2, 0); i < issued; ++i)
+                if (lane == 0 && !mbar_wait(&bars->rawfull[i & 1], (i >> 1) & 1)) report_error(kErrDrainTimeout);
+    }
+
+    // ---------------- teardown
+    __syncwarp();
+    if (warp == kWarpMma) {
+        if (lane == 0 && !mbar_wait(&bars->final_, 0)) report_error(kErrMmaTimeout);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <typename T, int HD>
+cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
+    constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, smem = Smem<HD, PARTS>::kAll;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static bool configured = false;
+    if (!configured) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<T, HD, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured = true;
+    }
+    const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kRows - 1) / kRows), a.kv_heads, a.seqs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<T, HD, PARTS>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
+    if (type == GQ_F32) return head_dim == 64 ? tiles_go<float, 64>(a, s) : tiles_go<float, 128>(a, s);
+    if (type == GQ_F16) return head_dim == 64 ? tiles_go<__half, 64>(a, s) : tiles_go<__half, 128>(a, s);
+    return head_dim == 64 ? tiles_go<__nv_bfloat16, 64>(a, s) : tiles_go<__nv_bfloat16, 128>(a, s);
+}
+
+}  // namespace gq

@@ -40,6 +40,7 @@ unsigned error_read_clear_probes();
 unsigned error_read_clear_block_q8();
 unsigned error_read_clear_kv();
 unsigned error_read_clear_attn();
+unsigned error_read_clear_attn_tiles();
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;

@@ -478,3 +478,57 @@ def test_indices_out_of_range(gq, t):
     assert torch.allclose(got[:t].double(), want, rtol=1e-4, atol=1e-4)
     gq.attn_q8_0(q, f.cache, f.table, f.kv_len, start, t, L - 1)
     assert gq.device_error() == 8
+
+
+@pytest.mark.parametrize("hd,kind", [(64, "f32"), (128, "f32"), (128, "bf16")])
+def test_many_rows_infinity_and_nan_in_masked_places(gq, hd, kind):
+    """As above with rows enough for the tensor-core tiles; a row that does see the token is not finite."""
+    hq, hkv, L, t = 16, 2, 300, 64
+    f = Filled(gq, [L], hkv, hd, 16)
+    hide = 20
+    rows = [((1 << t) - 1) & ~(1 << hide) & ((1 << (i + 1)) - 1) | (1 << hide if i == 40 else 0) for i in range(t)]
+    tree = torch.tensor([r - (1 << 64) if r >> 63 else r for r in rows], dtype=torch.int64, device="cuda")
+    q, want, start = attention_check(gq, f, [t], hq, kind, tree=tree)
+    slot = torch.tensor([int(f.table[0, (L - t + hide) // 16]) * 16 + (L - t + hide) % 16], device="cuda")
+    inf = torch.full((1, hkv, hd), float("inf"), device="cuda")
+    for k in (inf, torch.ones_like(inf)):
+        gq.rope_kv_append(None, k, inf, f.cache, slot)
+        got = gq.attn_q8_0(q, f.cache, f.table, f.kv_len, start, t, L, tree_mask=tree)
+        seen = torch.arange(t, device="cuda") == 40
+        assert not torch.isfinite(got[seen]).any()
+        tol = dict(rtol=1e-4, atol=1e-5) if kind == "f32" else dict(rtol=2e-2, atol=2e-2)
+        assert torch.allclose(got[~seen].float(), want[~seen].float(), **tol)
+    assert gq.device_error() == 0
+
+
+def test_many_rows_indices_and_offsets(gq):
+    """Page indices outside the cache are not seen, in a cache of over 4 GB, with rows enough for the tensor-core tiles."""
+    hkv, hd, page, L, t, hq = 4, 128, 64, 700, 100, 16
+    pages = (5 << 30) // (page * hkv * 34 * hd // 16)
+    data = torch.empty(gq.kv_cache_bytes(pages, page, hkv, hd), dtype=torch.uint8, device="cuda")
+    f = Filled(gq, [L], hkv, hd, page, first_page=pages - 14, extra=3, data=data, pages=pages)
+    q, _, start = attention_check(gq, f, [t], hq, "f32")
+    bad = f.table.clone()
+    bad[0, 1], bad[0, 4] = f.pages, -5
+    got = gq.attn_q8_0(q, f.cache, bad, f.kv_len, start, t, L)
+    assert gq.device_error() == 8
+    keep = torch.ones(L, dtype=torch.bool, device="cuda")
+    keep[64:128], keep[256:320] = False, False
+    s = torch.einsum("qhd,lhd->qhl", q.double(), f.k[0].double().repeat_interleave(hq // hkv, 1)) * hd ** -0.5
+    hidden = (torch.arange(L, device="cuda")[None] > L - t + torch.arange(t, device="cuda")[:, None]) | ~keep[None]
+    w = torch.softmax(s.masked_fill(hidden[:, None], -np.inf), -1)
+    want = torch.einsum("qhl,lhd->qhd", w, f.v[0].double().repeat_interleave(hq // hkv, 1))
+    assert torch.allclose(got.double(), want, rtol=1e-4, atol=1e-4)
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_many_rows_scales_that_differ(gq, kind):
+    """Sequences whose later keys and values are far larger or smaller than the first, over several tiles."""
+    hkv, hd, page, L, t, hq = 1, 64, 16, 500, 70, 4
+    f = Filled(gq, [L], hkv, hd, page)
+    j = torch.arange(L, device="cuda")
+    slots = f.table[0, j // page].long() * page + j % page
+    size = torch.exp2(((j // 50) * 7 % 11 - 5).float())[:, None, None]
+    gq.rope_kv_append(None, normal(61, L, hkv, hd) * size.clamp(max=2.0), normal(62, L, hkv, hd) * size, f.cache, slots)
+    f.k[0], f.v[0] = gq.kv_read(f.cache, slots)
+    attention_check(gq, f, [t], hq, kind)
