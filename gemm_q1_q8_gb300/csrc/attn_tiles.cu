@@ -16,10 +16,11 @@
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
 // chunks without moving single bytes.
 //
-//   warps 0-3   softmax: scores from tensor memory (a row a thread, so no shuffles), weights back to it; the running maximum moves (and the
-//               sums in tensor memory are multiplied) only where a row's scores pass it by 2^kSlack
-//   warps 4-11  keys and values of a tile, two stages
-//   warp 12     MMA issue: scores of tile i + 1 before the sums of tile i, so the tensor cores work during the softmax
+//   warps 0-7   softmax, two groups that take every other tile, each with a running maximum and sums (in tensor memory) of its own, joined at
+//               the end: scores from tensor memory, a row a thread (so no shuffles), the weights into the scores' place; the maximum moves
+//               (and the sums are multiplied) only where a row's scores pass it by 2^kSlack
+//   warps 8-11  keys and values of a tile, two stages
+//   warp 12     MMA issue: the sums of tile i, then the scores of tile i + 2 into the same place
 //   warp 13     bulk copies of the chunks, two stages
 #include "layer_ops.cuh"
 #include "tc_common.cuh"
@@ -29,10 +30,10 @@ GQ_ERROR_ACCESSOR(attn_tiles)
 namespace {
 
 constexpr int kRows = 128, kTok = 64, kGroups = kTok / kvGroup;
-constexpr int kWarpKV = 4, kNumKV = 8, kWarpMma = 12, kThreads = 14 * 32;
+constexpr int kWarpKV = 8, kNumKV = 4, kWarpMma = 12, kThreads = 14 * 32;
 constexpr float kNone = -1e30f, kLog2e = 1.4426950408889634f;
 constexpr float kLift = 11.f, kSlack = 4.f;
-constexpr int kColS = 0, kColP = 128, kColQ = 256, kColO = 384, kTmemCols = 512;
+constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 
 struct Info {
     float kfactor;         // 2^e of the keys' scales
@@ -42,11 +43,13 @@ struct Info {
     uint32_t bad[2];       // those tokens' columns
 };
 struct Bars {
-    uint64_t rawfull[2], rawfree[2], kfull[2], vfull[2], qk[2], pv[2], sfree[2], pfull[2], qfull, final_;
+    uint64_t rawfull[2], rawfree[2], kfull[2], vfull[2], qk[2], pv[2], pfull[2], qfull, final_;
     uint32_t tmem;
     int abort;
     int have[2];
     Info info[4];
+    float m[2][kRows], l[2][kRows];                        // the groups' maxima and sums, at the end
+    int vref[2][kRows];
 };
 
 template <int HD, int PARTS> struct Smem {
@@ -91,6 +94,15 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float* v) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 columns of it
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -152,7 +164,7 @@ __device__ __forceinline__ void put8(uint8_t* dst, int part_bytes, const uint32_
     if (PARTS == 2) *reinterpret_cast<uint4*>(dst + part_bytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-template <typename T, int HD, int PARTS>
+template <typename T, int HD, int PARTS, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a) {
     using M = Smem<HD, PARTS>;
     constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32, kAtoms = HD / 64;
@@ -186,10 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             mbar_init(&bars->vfull[s], kNumKV);
             mbar_init(&bars->qk[s], 1);
             mbar_init(&bars->pv[s], 1);
-            mbar_init(&bars->sfree[s], 4);
             mbar_init(&bars->pfull[s], 4);
         }
-        mbar_init(&bars->qfull, 4);
+        mbar_init(&bars->qfull, 8);
         mbar_init(&bars->final_, 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -204,25 +215,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     const uint32_t tmem = bars->tmem;
 
     if (warp < kWarpKV) {
-        // ---------------- softmax: row tile0 + 32 * warp + lane
-        const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const int r = tile0 + warp * 32 + lane;
+        // ---------------- softmax: row tile0 + 32 * (warp % 4) + lane, tiles wg, wg + 2, ...
+        const int wg = warp >> 2, lr = (warp & 3) * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const int r = tile0 + lr;
         const bool in = r < rows;
         const int tok = in ? r / group : 0, h = in ? r % group : 0;
         float rs;
         {
             const T* q = static_cast<const T*>(a.q) + (q0 + tok) * a.q_stride + (hk * group + h) * HD;
             float amax = 0.f;
+#pragma unroll 8
             for (int d = 0; d < HD; d += 4) {
                 const float4 v = load4(q + d);
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
             }
             const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
             const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
-            const float f = in ? pow2i(up) : 0.f;
-            rs = (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) * pow2i(-up);
-#pragma unroll
-            for (int c = 0; c < kAtoms; ++c)
+            // the scale's sign goes into the queries, and a scale of 0 (equal weights) too: the scores' factor stays positive
+            const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
+            rs = (CAP ? size / a.softcap : size * kLog2e) * pow2i(-up);
+            if (wg < kAtoms) {
+                const int c = wg;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t hi[16], lo[16];
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     for (int i = 0; i < 8; ++i) {                          // four dims: positions 4 i .. of this half of the atom
                         const int t = 2 * half + (i >> 2), hh = (i >> 1) & 1, bb = i & 1;
                         float4 v = load4(q + 64 * c + 32 * hh + 16 * bb + 4 * t);
-                        v = in ? make_float4(v.x * f, v.y * f, v.z * f, v.w * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
                         const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
                         hi[2 * i] = u32(x);
                         hi[2 * i + 1] = u32(y);
@@ -243,104 +257,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     tc_st16(tl + kColQ + 32 * c + 16 * half, hi);
                     if (PARTS == 2) tc_st16(tl + kColQ + HD / 2 + 32 * c + 16 * half, lo);
                 }
-            tc_wait_st();
+                tc_wait_st();
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->qfull);
         }
         const int last = in ? L - T_ + tok : -1;
-        const unsigned long long bits = a.tree && in ? a.tree[q0 + tok] : 0ull;
+        const uint32_t cs = tl + kColS + wg * kTok, co = tl + kColO + wg * HD;
         float m = kNone, l = 0.f;
         int vref = -24;
         bool ok = true;
-        for (int i = 0; i < tiles; ++i) {
-            const int s = i & 1;
-            const uint32_t par = (i >> 1) & 1;
-            // (the scores' MMAs were issued after the keys' barrier, so what stands in `info` was written before)
-            if (!wait_or_abort_sleep(&bars->qk[s], par, abort)) {
+        for (int i = wg; i < tiles; i += 2) {
+            // (the scores' MMAs were issued after the keys' barrier, so what stands in `info` was written before; and after the sums of
+            // tile i - 2, so those are complete)
+            if (!wait_or_abort_sleep(&bars->qk[wg], (i >> 1) & 1, abort)) {
                 ok = false;
                 break;
             }
             __syncwarp();
             tc_fence_after();
             const Info& info = bars->info[i & 3];
-            const float x_of = rs * info.kfactor;
-            const int vexp = info.vexp, have = info.have, odd = info.odd;
-            const uint32_t bad0 = odd ? info.bad[0] : 0u, bad1 = odd ? info.bad[1] : 0u;
+            float x_of = rs * info.kfactor;
+            const int vexp = info.vexp, have = info.have;
             float x[kTok];
-            tc_ld32(tl + kColS + s * kTok, x);
-            tc_ld32(tl + kColS + s * kTok + 32, x + 32);
+            tc_ld32(cs, x);
+            tc_ld32(cs + 32, x + 32);
             tc_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->sfree[s]);
             const int j0 = i * kTok;
-            if (a.softcap > 0.f) {
+            if (CAP) {
 #pragma unroll
                 for (int n = 0; n < kTok; ++n) {
-                    // tanh: 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely; f32 queries take the function
+                    // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones
                     const float y = x[n] * x_of;
                     x[n] = a.softcap * kLog2e * (PARTS == 2 ? tanhf(y) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f));
                 }
-            } else {
-#pragma unroll
-                for (int n = 0; n < kTok; ++n) x[n] *= x_of;
+                x_of = 1.f;
             }
             if (j0 + kTok > min(L - T_, a.max_kv) || have != (1 << kGroups) - 1) {
-#pragma unroll
+                const unsigned long long bits = a.tree && in ? a.tree[q0 + tok] : 0ull;
+                uint32_t vis[2] = {0u, 0u};
+#pragma unroll 1
                 for (int n = 0; n < kTok; ++n) {
                     const int j = j0 + token_of(n), rel = j - (L - T_);
-                    bool vis = last >= 0 && j < len && (have >> (n >> 4) & 1);
-                    vis = vis && (a.tree ? rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)) : j <= last);
-                    if (!vis) x[n] = -INFINITY;
+                    const bool v = last >= 0 && j < len && (have >> (n >> 4) & 1) &&
+                                   (a.tree ? rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)) : j <= last);
+                    vis[n >> 5] |= static_cast<uint32_t>(v) << (n & 31);
                 }
+#pragma unroll
+                for (int n = 0; n < kTok; ++n)
+                    if (!(vis[n >> 5] >> (n & 31) & 1u)) x[n] = -INFINITY;
             }
             float top = x[0];
 #pragma unroll
             for (int n = 1; n < kTok; ++n) top = fmaxf(top, x[n]);
-            const bool move = top > m + kSlack || vexp > vref;
-            if (__any_sync(0xffffffffu, move)) {
+            top *= x_of;
+            if (__any_sync(0xffffffffu, top > m + kSlack || vexp > vref)) {
                 const float mn = top > m + kSlack ? top : m;
                 const int vn = max(vexp, vref);
                 const float down = ex2(m - mn), downo = down * pow2i(max(vref - vn, -126));
                 l *= down;
                 m = mn;
                 vref = vn;
-                if (i > 0) {
-                    if (!wait_or_abort(&bars->pv[s ^ 1], ((i - 1) >> 1) & 1, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    __syncwarp();
-                    tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < HD; c += 32) {
-                        float o[32];
-                        tc_ld32(tl + kColO + c, o);
+                if (i >= 2) {
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 16) {
+                        uint32_t o[16];
+                        tc_ld16(co + c, o);
                         tc_wait_ld();
-                        uint32_t w[32];
 #pragma unroll
-                        for (int n = 0; n < 32; ++n) w[n] = __float_as_uint(o[n] * downo);
-                        tc_st32(tl + kColO + c, w);
+                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * downo);
+                        tc_st16(co + c, o);
                     }
-                    tc_wait_st();
                 }
             }
-            if (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort)) {     // the weights' slot is free
-                ok = false;
-                break;
-            }
-            __syncwarp();
-            tc_fence_after();
-            const float from = m - kLift - static_cast<float>(vexp - vref), lower = pow2i(max(vref - vexp, 0)) * 0x1p-11f;
-            float sum = 0.f;
+            const float from = m - kLift - static_cast<float>(vexp - vref), lower = pow2i(vref - vexp) * 0x1p-11f;
+            float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    const float p0 = ex2(x[32 * half + 2 * n] - from), p1 = ex2(x[32 * half + 2 * n + 1] - from);
-                    sum += p0 + p1;
+                    const float p0 = ex2(fmaf(x[32 * half + 2 * n], x_of, -from)), p1 = ex2(fmaf(x[32 * half + 2 * n + 1], x_of, -from));
+                    sum0 += p0;
+                    sum1 += p1;
                     const __half2 v = __floats2half2_rn(p0, p1);
                     hi[n] = u32(v);
                     if (PARTS == 2) {
@@ -348,38 +348,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                         lo[n] = u32(__floats2half2_rn(p0 - f.x, p1 - f.y));
                     }
                 }
-                const uint32_t col = tl + kColP + s * PARTS * 32 + 16 * half;
-                tc_st16(col, hi);
-                if (PARTS == 2) tc_st16(col + 32, lo);
+                tc_st16(cs + 16 * half, hi);
+                if (PARTS == 2) tc_st16(cs + 32 + 16 * half, lo);
             }
-            l = fmaf(sum, lower, l);
-            if (odd)                                                      // a value that is not finite, seen by this row
+            l = fmaf(sum0 + sum1, lower, l);
+            if (info.odd) {                                               // a value that is not finite, seen by this row
+                const unsigned long long bad = info.bad[0] | static_cast<unsigned long long>(info.bad[1]) << 32;
 #pragma unroll
                 for (int n = 0; n < kTok; ++n)
-                    if (((n < 32 ? bad0 : bad1) >> (n & 31) & 1u) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
+                    if ((bad >> n & 1) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
+            }
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->pfull[s]);
+            if (lane == 0) mbar_arrive(&bars->pfull[wg]);
         }
-        if (ok && tiles > 0 && !wait_or_abort(&bars->pv[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort)) ok = false;
-        __syncwarp();
-        if (ok) {
+        // ---- the groups' sums meet: each group writes half of the dims
+        const int mine = (tiles + 1 - wg) >> 1;                           // this group's tiles
+        if (ok && mine > 0 && !wait_or_abort(&bars->pv[wg], (mine - 1) & 1, abort)) ok = false;
+        bars->m[wg][lr] = ok ? m : __int_as_float(0x7fc00000);
+        bars->l[wg][lr] = l;
+        bars->vref[wg][lr] = vref;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        {
             tc_fence_after();
-            const float back = l == 0.f || tiles == 0 ? 0.f : pow2i(vref - 11) / l;
-            T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD;
+            const float m0 = bars->m[0][lr], m1 = bars->m[1][lr], top = fmaxf(m0, m1), f0 = ex2(m0 - top), f1 = ex2(m1 - top);
+            const float sum = fmaf(bars->l[0][lr], f0, bars->l[1][lr] * f1), inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float a0 = f0 * pow2i(bars->vref[0][lr] - 11) * inv, a1 = f1 * pow2i(bars->vref[1][lr] - 11) * inv;
+            T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD + wg * (HD / 2);
+#pragma unroll 1
+            for (int c = 0; c < HD / 2; c += 16) {
+                uint32_t o0[16], o1[16];
+                tc_ld16(tl + kColO + wg * (HD / 2) + c, o0);
+                tc_ld16(tl + kColO + HD + wg * (HD / 2) + c, o1);
+                tc_wait_ld();
+                float v[16];
 #pragma unroll
-            for (int c = 0; c < HD; c += 32) {
-                float o[32];
-                if (tiles > 0) {
-                    tc_ld32(tl + kColO + c, o);
-                    tc_wait_ld();
+                for (int n = 0; n < 16; ++n) {                            // a group without tiles has no sums
+                    v[n] = tiles > 0 && sum != 0.f ? __uint_as_float(o0[n]) * a0 : 0.f;
+                    if (tiles > 1 && sum != 0.f) v[n] = fmaf(__uint_as_float(o1[n]), a1, v[n]);
                 }
                 if (in)
 #pragma unroll
-                    for (int n = 0; n < 32; n += 4)
-                        store4(out + c + n, back == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                        : make_float4(o[n] * back, o[n + 1] * back, o[n + 2] * back, o[n + 3] * back));
+                    for (int n = 0; n < 16; n += 4) store4(out + c + n, make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]));
             }
         }
     } else if (warp < kWarpMma) {
@@ -388,13 +399,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         for (int i = 0; i < tiles; ++i) {
             const int s = i & 1;
             const uint32_t par = (i >> 1) & 1;
-            if (!wait_or_abort(&bars->rawfull[s], par, abort)) break;
+            if (!wait_or_abort_sleep(&bars->rawfull[s], par, abort)) break;
             __syncwarp();
             const uint8_t* raw = sraw + s * M::kRaw;
             const int have = bars->have[s], j0 = i * kTok;
             const bool edge = j0 + kTok > len || have != (1 << kGroups) - 1;      // some of the tile's tokens do not exist
             // keys, once the scores of the tile before the last are done
-            if (i >= 2 && !wait_or_abort(&bars->qk[s], par ^ 1, abort)) break;
+            if (i >= 2 && !wait_or_abort_sleep(&bars->qk[s], par ^ 1, abort)) break;
             __syncwarp();
             bool odd;
             {
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     bars->info[i & 3].have = have;
                 }
                 constexpr int kUnits = HD / 16;
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < kTok * kUnits / (kNumKV * 32); ++k) {
                     const int id = dt + k * kNumKV * 32, ta = id / kUnits, up = id % kUnits, grp = ta >> 4, tok = ta & 15;
                     const int u = HD > 64 ? up ^ (4 * (tok & 1)) : up, c = u >> 2, t = u & 3;
@@ -446,23 +457,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->kfull[s]);
-            // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..)
-            if (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort)) break;
+            // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..) twice
+            if (i >= 2 && !wait_or_abort_sleep(&bars->pv[s], par ^ 1, abort)) break;
+            __syncwarp();
             {
                 __half2 f1, f2;
                 scale_factors(ve, f1, f2);
-                const int grp = w8 >> 1, o = w8 & 1;
                 const int g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, c0 = HD == 64 ? lane & 1 : lane & 3;
-                const uint8_t* ch = raw + grp * kChunk;
-#pragma unroll
-                for (int hc = 0; hc < (HD > 128 ? HD / 128 : 1); ++hc) {
-                    const int c = c0 + 4 * hc;
+#pragma unroll 1
+                for (int oct = w8; oct < kTok / 8; oct += kNumKV) {
+                    const int grp = oct >> 1, o = oct & 1, c = c0;
+                    const uint8_t* ch = raw + grp * kChunk;
                     uint32_t w[8], sc[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const int p = 2 * o + (k >> 2), t = k & 3;
                         const uint8_t* r = ch + kv_v_offset(HD) + (4 * p + t) * HD;
-                        w[k] = *reinterpret_cast<const uint32_t*>(HD == 64 ? r + 8 * (g ^ (4 * (t >> 1))) + 4 * c : r + 128 * hc + 16 * (g ^ (2 * t)) + 4 * c0);
+                        w[k] = *reinterpret_cast<const uint32_t*>(HD == 64 ? r + 8 * (g ^ (4 * (t >> 1))) + 4 * c : r + 16 * (g ^ (2 * t)) + 4 * c);
                         sc[k] = *reinterpret_cast<const uint16_t*>(ch + kv_vs_offset(HD) + 2 * ((4 * t + p) * kNb + c));
                         if (edge && (j0 + 16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= len || !(have >> grp & 1))) sc[k] = 0;
                         if (odd && (sc[k] & 0x7c00u) == 0x7c00u) sc[k] = 0;
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                         const int e = HD == 64 ? 2 * (lane >> 4) + ((x + c0) & 1) : (x + c0) & 3;      // a store's chunks differ in their banks
                         const uint32_t sel = 0x4400u + 0x1111u * e;
                         const uint32_t code[4] = {codes2(w[0], w[1], sel), codes2(w[2], w[3], sel), codes2(w[4], w[5], sel), codes2(w[6], w[7], sel)};
-                        put8<PARTS>(dst + swz128(32 * c + 4 * g + e, w8), M::kV, code, sh);
+                        put8<PARTS>(dst + swz128(32 * c + 4 * g + e, oct), M::kV, code, sh);
                     }
                 }
             }
@@ -500,16 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(tmem + kColO, tmem + kColP + (s * PARTS + (t == 1)) * 32 + 8 * k,
-                               smem_desc(sv + (s * PARTS + (t == 2)) * M::kV + 32 * k), idesc<HD>(), i | t | k ? 1u : 0u);
+                        mma_ts(tmem + kColO + s * HD, tmem + kColS + s * kTok + (t == 1) * 32 + 8 * k,
+                               smem_desc(sv + (s * PARTS + (t == 2)) * M::kV + 32 * k), idesc<HD>(), (i >> 1) | t | k ? 1u : 0u);
                 tc_commit(&bars->pv[s]);
                 return true;
             };
-            for (int i = 0; ok && i < tiles; ++i) {
+            auto scores = [&](int i) {                                    // of tile i, into the place of the weights of tile i - 2
                 const int s = i & 1;
                 const uint32_t par = (i >> 1) & 1;
-                ok = wait_or_abort(&bars->kfull[s], par, abort) && (i < 2 || wait_or_abort(&bars->sfree[s], par ^ 1, abort));
-                if (!ok) break;
+                if (!wait_or_abort(&bars->kfull[s], par, abort) || (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort))) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
@@ -518,9 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                         mma_ts(tmem + kColS + s * kTok, tmem + kColQ + (t == 1) * (HD / 2) + 8 * k,
                                smem_desc(sk + (s * PARTS + (t == 2)) * M::kK + (k >> 2) * (kTok * 128) + 32 * (k & 3)), idesc<kTok>(), t | k ? 1u : 0u);
                 tc_commit(&bars->qk[s]);
-                if (i > 0) ok = sums(i - 1);
-            }
-            if (ok) sums(tiles - 1);
+                return true;
+            };
+            ok = ok && scores(0) && (tiles < 2 || scores(1));
+            for (int i = 0; ok && i < tiles; ++i) ok = sums(i) && (i + 2 >= tiles || scores(i + 2));
             tc_commit(&bars->final_);                                     // all MMAs issued so far complete before TMEM is freed
         }
     } else {
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 }
             }
             const unsigned there = __ballot_sync(0xffffffffu, page >= 0), missing = __ballot_sync(0xffffffffu, wanted && page < 0);
-            if (i >= 2 && !wait_or_abort(&bars->rawfree[s], ((i >> 1) & 1) ^ 1, abort)) break;
+            if (i >= 2 && !wait_or_abort_sleep(&bars->rawfree[s], ((i >> 1) & 1) ^ 1, abort)) break;
             if (lane == 0) {
                 bars->have[s] = ((1 << kGroups) - 1) & ~missing;          // chunks past the end count as there: their tokens are past the end
                 if (there) mbar_arrive_expect_tx(&bars->rawfull[s], __popc(there) * kChunk);
@@ -573,13 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool CAP>
 cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, smem = Smem<HD, PARTS>::kAll;
     static_assert(smem <= 227 * 1024, "shared memory");
     static bool configured = false;
     if (!configured) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<T, HD, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<T, HD, PARTS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         configured = true;
     }
@@ -594,15 +605,21 @@ cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<T, HD, PARTS>, a);
+    return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<T, HD, PARTS, CAP>, a);
+}
+
+template <typename T>
+cudaError_t tiles_type(const AttnArgs& a, int head_dim, cudaStream_t s) {
+    if (a.softcap > 0.f) return head_dim == 64 ? tiles_go<T, 64, true>(a, s) : tiles_go<T, 128, true>(a, s);
+    return head_dim == 64 ? tiles_go<T, 64, false>(a, s) : tiles_go<T, 128, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tiles(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
-    if (type == GQ_F32) return head_dim == 64 ? tiles_go<float, 64>(a, s) : tiles_go<float, 128>(a, s);
-    if (type == GQ_F16) return head_dim == 64 ? tiles_go<__half, 64>(a, s) : tiles_go<__half, 128>(a, s);
-    return head_dim == 64 ? tiles_go<__nv_bfloat16, 64>(a, s) : tiles_go<__nv_bfloat16, 128>(a, s);
+    if (type == GQ_F32) return tiles_type<float>(a, head_dim, s);
+    if (type == GQ_F16) return tiles_type<__half>(a, head_dim, s);
+    return tiles_type<__nv_bfloat16>(a, head_dim, s);
 }
 
 }  // namespace gq
