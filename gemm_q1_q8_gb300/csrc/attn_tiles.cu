@@ -19,9 +19,10 @@
 //   warps 0-7   softmax, two groups that take every other tile, each with a running maximum and sums (in tensor memory) of its own, joined at
 //               the end: scores from tensor memory, a row a thread (so no shuffles), the weights into the scores' place; the maximum moves
 //               (and the sums are multiplied) only where a row's scores pass it by 2^kSlack
-//   warps 8-11  keys and values of a tile, two stages
-//   warp 12     MMA issue: the sums of tile i, then the scores of tile i + 2 into the same place
-//   warp 13     bulk copies of the chunks, two stages
+//   warps 8-15  keys and values of a tile, two stages
+//   warp 16     MMA issue of the scores: those of tile i + 2 into the place of the weights of tile i, once its sums are done
+//   warp 17     MMA issue of the sums
+//   warp 18     bulk copies of the chunks, two stages (warp 19 fills the last warpgroup)
 #include "layer_ops.cuh"
 #include "tc_common.cuh"
 
@@ -30,7 +31,10 @@ GQ_ERROR_ACCESSOR(attn_tiles)
 namespace {
 
 constexpr int kRows = 128, kTok = 64, kGroups = kTok / kvGroup;
-constexpr int kWarpKV = 8, kNumKV = 4, kWarpMma = 12, kThreads = 14 * 32;
+constexpr int kWarpKV = 8, kNumKV = 8, kWarpMma = 16, kThreads = 20 * 32;
+// Registers a thread of each warpgroup, out of the 5 x 96 that a launch of 640 threads has: two softmax groups, two of keys and values, one
+constexpr int kRegsSoftmax = 136, kRegsKV = 72, kRegsRest = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsKV + kRegsRest == 5 * 96, "registers");
 constexpr float kNone = -1e30f, kLog2e = 1.4426950408889634f;
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
@@ -73,10 +77,11 @@ template <int N>
 __device__ __forceinline__ constexpr uint32_t idesc() {                   // D f32, A and B f16, both K-major, M = 128
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+// One MMA, its B descriptor in halves (the low one moves by constants from MMA to MMA: little is left to issue per MMA)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t desc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-        "r"(desc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(desc), "r"(accumulate)
         : "memory");
 }
 // 32 columns of this thread's TMEM lane
@@ -119,33 +124,43 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ constexpr int token_of(int n) { return (n & ~15) + 2 * (n & 3) + ((n >> 2) & 1) + 8 * ((n >> 3) & 1); }
 
 // What a tile's scales need to get near 1: the exponent e of the largest finite one (all below 2^e), by a whole warp.  `edge`: only the
-// first `end` tokens, of the chunks in `have`, count.
+// first `end` tokens, of the chunks in `have`, count.  `odd`: some scale is not finite (its bits are above every finite one's).
 template <int HD>
-__device__ __forceinline__ int scales_exponent(const uint8_t* raw, int offset, int lane, bool edge, int end, int have, bool& odd) {
-    constexpr int kWords = kvGroup * (HD / 32) / 2;                       // 32-bit words of a chunk's scales
-    uint32_t top = 0;
-    bool strange = false;
+__device__ __forceinline__ int scales_exponent(const uint8_t* raw, int lane, bool edge, int end, int have, bool& odd) {
+    constexpr int kWords = kvGroup * (HD / 32) / 2, kPer = kGroups * kWords / 32;      // 32-bit words of a chunk's scales; a lane's
+    uint32_t w[kPer], top = 0;
 #pragma unroll
-    for (int i = 0; i < kGroups * kWords / 32; ++i) {
+    for (int i = 0; i < kPer; ++i) {
         const int at = i * 32 + lane;
-        uint32_t w = *reinterpret_cast<const uint32_t*>(raw + (at / kWords) * kv_chunk_bytes(HD) + offset + 4 * (at % kWords));
-        if (edge) {
-            const int grp = at / kWords, at4 = at % kWords / (HD / 64), t = at4 >> 2, p = at4 & 3;       // scales stand by 4 t + p
-            if (16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= end || !(have >> grp & 1)) w = 0;
-        }
-        strange = strange || ((((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0);
-        if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;                   // not finite: does not count
-        if ((w & 0x7c000000u) == 0x7c000000u) w &= 0xffffu;
-        top = max(top, max(w & 0x7c00u, (w >> 16) & 0x7c00u));
+        w[i] = *reinterpret_cast<const uint32_t*>(raw + (at / kWords) * kv_chunk_bytes(HD) + 4 * (at % kWords)) & 0x7fff7fffu;
     }
-    odd = __any_sync(0xffffffffu, strange);
-    return static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 10) - 14;
+    if (edge) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = i * 32 + lane, grp = at / kWords, at4 = at % kWords / (HD / 64), t = at4 >> 2, p = at4 & 3;       // by 4 t + p
+            if (16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= end || !(have >> grp & 1)) w[i] = 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) top = __vmaxu2(top, w[i]);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    odd = top >= 0x7c00u;
+    if (odd) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if ((w[i] & 0xffffu) < 0x7c00u) top = max(top, w[i] & 0xffffu);
+            if ((w[i] >> 16) < 0x7c00u) top = max(top, w[i] >> 16);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    return static_cast<int>(top >> 10) - 14;
 }
 // 2^(9 - e) as the product of two f16 powers of two
 __device__ __forceinline__ void scale_factors(int e, __half2& f1, __half2& f2) {
-    const int x = 9 - e, y = x / 2;                                       // -8 <= x <= 23
-    f1 = __float2half2_rn(pow2i(y));
-    f2 = __float2half2_rn(pow2i(x - y));
+    const int x = 9 - e, y = x >> 1;                                      // -7 <= x <= 23
+    f1 = h2(static_cast<uint32_t>((15 + y) << 10) * 0x10001u);
+    f2 = h2(static_cast<uint32_t>((15 + x - y) << 10) * 0x10001u);
 }
 
 // Eight values (four pairs) as one or two parts: 16 bytes each
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             mbar_init(&bars->pfull[s], 4);
         }
         mbar_init(&bars->qfull, 8);
-        mbar_init(&bars->final_, 1);
+        mbar_init(&bars->final_, 2);
         bars->abort = 0;
         fence_barrier_init();
     }
@@ -215,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     const uint32_t tmem = bars->tmem;
 
     if (warp < kWarpKV) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: row tile0 + 32 * (warp % 4) + lane, tiles wg, wg + 2, ...
         const int wg = warp >> 2, lr = (warp & 3) * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -394,8 +410,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
         }
     } else if (warp < kWarpMma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKV));
         // ---------------- keys and values
         const int w8 = warp - kWarpKV, dt = threadIdx.x - kWarpKV * 32;
+        // this thread's part of the keys: unit k_up of token k_tok (of the first kStep), as chunk 2 t (+ 1) of its row
+        constexpr int kUnits = HD / 16, kStep = kNumKV * 32 / kUnits, kUnitsPer = kTok / kStep;
+        static_assert(kStep % 16 == 0, "a unit's token has the same place in every chunk");
+        const int k_tok = dt / kUnits, k_up = dt % kUnits, k_in = k_tok & 15;
+        const int k_u = HD > 64 ? k_up ^ (4 * (k_in & 1)) : k_up, k_tt = (k_in & 7) >> 1, k_p = (k_in & 1) + 2 * (k_in >> 3);
+        const int k_src = (k_tok >> 4) * kChunk + k_in * HD + k_up * 16;
+        const int k_scale = (k_tok >> 4) * kChunk + kv_ks_offset(HD) + 2 * ((4 * k_tt + k_p) * kNb + 2 * (k_u >> 2));
+        const bool k_swap = HD > 64 ? (k_u >> 2) & 1 : k_in & 1;          // the two chunks of a unit in this order: a store's chunks differ in their banks
+        const int k_dst = (k_u >> 2) * (kTok * 128) + static_cast<int>(swz128((k_tok & ~15) + 4 * k_p + k_tt, 2 * (k_u & 3) + (k_swap ? 1 : 0)));
+        // and of the values: four dims 32 v_c + 4 v_g .. of eight tokens
+        const int v_g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, v_c = HD == 64 ? lane & 1 : lane & 3;
+        const int v_src = kv_v_offset(HD) + (w8 & 1) * 8 * HD + 4 * v_c, v_scale = kv_vs_offset(HD) + 2 * (2 * (w8 & 1) * kNb + v_c);
         for (int i = 0; i < tiles; ++i) {
             const int s = i & 1;
             const uint32_t par = (i >> 1) & 1;
@@ -407,46 +436,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             // keys, once the scores of the tile before the last are done
             if (i >= 2 && !wait_or_abort_sleep(&bars->qk[s], par ^ 1, abort)) break;
             __syncwarp();
+            // both exponents: the scores need them
             bool odd;
+            const int ve = scales_exponent<HD>(raw + kv_vs_offset(HD), lane, edge, len - j0, have, odd);
+            if (dt == 0) {
+                bars->info[i & 3].vexp = ve;
+                bars->info[i & 3].odd = odd;
+            }
             {
-                const int e = scales_exponent<HD>(raw, kv_ks_offset(HD), lane, edge, len - j0, have, odd);
+                bool kodd;
+                const int e = scales_exponent<HD>(raw + kv_ks_offset(HD), lane, edge, len - j0, have, kodd);
                 __half2 f1, f2;
                 scale_factors(e, f1, f2);
                 if (dt == 0) {
                     bars->info[i & 3].kfactor = pow2i(e);
                     bars->info[i & 3].have = have;
                 }
-                constexpr int kUnits = HD / 16;
-#pragma unroll 2
-                for (int k = 0; k < kTok * kUnits / (kNumKV * 32); ++k) {
-                    const int id = dt + k * kNumKV * 32, ta = id / kUnits, up = id % kUnits, grp = ta >> 4, tok = ta & 15;
-                    const int u = HD > 64 ? up ^ (4 * (tok & 1)) : up, c = u >> 2, t = u & 3;
-                    const int tt = (tok & 7) >> 1, p = (tok & 1) + 2 * (tok >> 3), n = 16 * grp + 4 * p + tt;
-                    const uint8_t* ch = raw + grp * kChunk;
-                    const uint4 w = *reinterpret_cast<const uint4*>(ch + tok * HD + up * 16);
-                    uint32_t sc = *reinterpret_cast<const uint32_t*>(ch + kv_ks_offset(HD) + 2 * ((4 * tt + p) * kNb + 2 * c));
-                    if (edge && (j0 + ta >= len || !(have >> grp & 1))) sc = 0;
-                    const bool swap = HD > 64 ? c & 1 : tok & 1;           // chunks of one store differ in their banks
-                    uint8_t* row = sk + s * PARTS * M::kK + c * (kTok * 128);
+                // a thread has one 16-byte unit of one token in every 128 / units tokens
+                uint4 w[kUnitsPer];
+                uint32_t sc[kUnitsPer];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int hh = swap ? x ^ 1 : x;
-                        const uint32_t wa = hh ? w.z : w.x, wb = hh ? w.w : w.y;
-                        const __half2 sh = __hmul2(__hmul2(h2(__byte_perm(sc, 0, hh ? 0x3232 : 0x1010)), f1), f2);
-                        const uint32_t code[4] = {codes2(wa, 0, 0x1100), codes2(wa, 0, 0x3322), codes2(wb, 0, 0x1100), codes2(wb, 0, 0x3322)};
-                        const __half2 sa[4] = {sh, sh, sh, sh};
-                        put8<PARTS>(row + swz128(n, 2 * t + hh), M::kK, code, sa);
-                    }
+                for (int k = 0; k < kUnitsPer; ++k) {
+                    const uint8_t* ch = raw + (kStep * k >> 4) * kChunk;
+                    w[k] = *reinterpret_cast<const uint4*>(ch + k_src);
+                    sc[k] = *reinterpret_cast<const uint32_t*>(ch + k_scale);
+                    if (edge && (j0 + k_tok + kStep * k >= len || !(have >> ((k_tok + kStep * k) >> 4) & 1))) sc[k] = 0;
+                }
+                uint8_t* dst = sk + s * PARTS * M::kK;
+#pragma unroll
+                for (int k = 0; k < kUnitsPer; ++k) {
+                    const __half2 s0 = __hmul2(__hmul2(h2(__byte_perm(sc[k], 0, k_swap ? 0x3232 : 0x1010)), f1), f2);
+                    const __half2 s1 = __hmul2(__hmul2(h2(__byte_perm(sc[k], 0, k_swap ? 0x1010 : 0x3232)), f1), f2);
+                    const uint32_t wa = k_swap ? w[k].z : w[k].x, wb = k_swap ? w[k].w : w[k].y, wc = k_swap ? w[k].x : w[k].z,
+                                   wd = k_swap ? w[k].y : w[k].w;
+                    const uint32_t ca[4] = {codes2(wa, 0, 0x1100), codes2(wa, 0, 0x3322), codes2(wb, 0, 0x1100), codes2(wb, 0, 0x3322)};
+                    const uint32_t cb[4] = {codes2(wc, 0, 0x1100), codes2(wc, 0, 0x3322), codes2(wd, 0, 0x1100), codes2(wd, 0, 0x3322)};
+                    const __half2 sa[4] = {s0, s0, s0, s0}, sb[4] = {s1, s1, s1, s1};
+                    put8<PARTS>(dst + k_dst + kStep * 128 * k, M::kK, ca, sa);
+                    put8<PARTS>(dst + (k_dst ^ 16) + kStep * 128 * k, M::kK, cb, sb);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            // values' exponent, needed with the scores
-            const int ve = scales_exponent<HD>(raw, kv_vs_offset(HD), lane, edge, len - j0, have, odd);
-            if (dt == 0) {
-                bars->info[i & 3].vexp = ve;
-                bars->info[i & 3].odd = odd;
-            }
             if (odd && w8 < 2) {                                          // which tokens: columns 32 w8 + lane
                 const int n = 32 * w8 + lane, grp = n >> 4, p = (n >> 2) & 3, t = n & 3;
                 bool strange = false;
@@ -457,37 +488,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->kfull[s]);
-            // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..) twice
+            // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..)
             if (i >= 2 && !wait_or_abort_sleep(&bars->pv[s], par ^ 1, abort)) break;
             __syncwarp();
             {
                 __half2 f1, f2;
                 scale_factors(ve, f1, f2);
-                const int g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, c0 = HD == 64 ? lane & 1 : lane & 3;
-#pragma unroll 1
-                for (int oct = w8; oct < kTok / 8; oct += kNumKV) {
-                    const int grp = oct >> 1, o = oct & 1, c = c0;
-                    const uint8_t* ch = raw + grp * kChunk;
+                uint8_t* dst = sv + s * PARTS * M::kV;
+#pragma unroll
+                for (int j = 0; j < kTok / 8 / kNumKV; ++j) {             // octets w8, w8 + kNumKV ..
+                    const uint8_t* ch = raw + ((w8 >> 1) + kNumKV / 2 * j) * kChunk;
+                    const int t0 = j0 + 16 * ((w8 >> 1) + kNumKV / 2 * j) + 8 * (w8 & 1);
                     uint32_t w[8], sc[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int p = 2 * o + (k >> 2), t = k & 3;
-                        const uint8_t* r = ch + kv_v_offset(HD) + (4 * p + t) * HD;
-                        w[k] = *reinterpret_cast<const uint32_t*>(HD == 64 ? r + 8 * (g ^ (4 * (t >> 1))) + 4 * c : r + 16 * (g ^ (2 * t)) + 4 * c);
-                        sc[k] = *reinterpret_cast<const uint16_t*>(ch + kv_vs_offset(HD) + 2 * ((4 * t + p) * kNb + c));
-                        if (edge && (j0 + 16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= len || !(have >> grp & 1))) sc[k] = 0;
-                        if (odd && (sc[k] & 0x7c00u) == 0x7c00u) sc[k] = 0;
+                    for (int k = 0; k < 8; ++k) {                         // value rows 8 o + k: p = 2 o + (k >> 2), t = k & 3
+                        const int t = k & 3;
+                        w[k] = *reinterpret_cast<const uint32_t*>(ch + v_src + (k >> 2) * 4 * HD + t * HD + (HD == 64 ? 8 * (v_g ^ (4 * (t >> 1))) : 16 * (v_g ^ (2 * t))));
+                        sc[k] = *reinterpret_cast<const uint16_t*>(ch + v_scale + 2 * (4 * t + (k >> 2)) * kNb);
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)                       // tokens 2 t + (p & 1) + 8 (p >> 1)
+                            if (t0 + 2 * (k & 3) + (k >> 2) >= len || !(have >> ((w8 >> 1) + kNumKV / 2 * j) & 1)) sc[k] = 0;
+                    }
+                    if (odd) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if ((sc[k] & 0x7c00u) == 0x7c00u) sc[k] = 0;
                     }
                     __half2 sh[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sh[k] = __hmul2(__hmul2(h2(sc[2 * k] | sc[2 * k + 1] << 16), f1), f2);
-                    uint8_t* dst = sv + s * PARTS * M::kV;
 #pragma unroll
                     for (int x = 0; x < (HD == 64 ? 2 : 4); ++x) {
-                        const int e = HD == 64 ? 2 * (lane >> 4) + ((x + c0) & 1) : (x + c0) & 3;      // a store's chunks differ in their banks
+                        const int e = HD == 64 ? 2 * (lane >> 4) + ((x + v_c) & 1) : (x + v_c) & 3;      // a store's chunks differ in their banks
                         const uint32_t sel = 0x4400u + 0x1111u * e;
                         const uint32_t code[4] = {codes2(w[0], w[1], sel), codes2(w[2], w[3], sel), codes2(w[4], w[5], sel), codes2(w[6], w[7], sel)};
-                        put8<PARTS>(dst + swz128(32 * c + 4 * g + e, oct), M::kV, code, sh);
+                        put8<PARTS>(dst + swz128(32 * v_c + 4 * v_g + e, w8 + kNumKV * j), M::kV, code, sh);
                     }
                 }
             }
@@ -498,43 +535,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 mbar_arrive(&bars->rawfree[s]);
             }
         }
-    } else if (warp == kWarpMma) {
-        // ---------------- MMAs, by one thread
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    }
+    if (warp == kWarpMma) {
+        // ---------------- scores, by one thread: of tile i into the place of the weights of tile i - 2
         if (lane == 0) {
             bool ok = tiles > 0 && wait_or_abort(&bars->qfull, 0, abort);
-            auto sums = [&](int i) {                                      // o += weights * values of tile i
+            const uint64_t desc = smem_desc(sk);
+            const uint32_t hi = static_cast<uint32_t>(desc >> 32);
+            for (int i = 0; ok && i < tiles; ++i) {
                 const int s = i & 1;
                 const uint32_t par = (i >> 1) & 1;
-                if (!wait_or_abort(&bars->vfull[s], par, abort) || !wait_or_abort(&bars->pfull[s], par, abort)) return false;
+                ok = wait_or_abort_sleep(&bars->kfull[s], par, abort) && (i < 2 || wait_or_abort_sleep(&bars->pv[s], par ^ 1, abort));
+                if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(tmem + kColO + s * HD, tmem + kColS + s * kTok + (t == 1) * 32 + 8 * k,
-                               smem_desc(sv + (s * PARTS + (t == 2)) * M::kV + 32 * k), idesc<HD>(), (i >> 1) | t | k ? 1u : 0u);
-                tc_commit(&bars->pv[s]);
-                return true;
-            };
-            auto scores = [&](int i) {                                    // of tile i, into the place of the weights of tile i - 2
-                const int s = i & 1;
-                const uint32_t par = (i >> 1) & 1;
-                if (!wait_or_abort(&bars->kfull[s], par, abort) || (i >= 2 && !wait_or_abort(&bars->pv[s], par ^ 1, abort))) return false;
-                tc_fence_after();
+                const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kK >> 4), d = tmem + kColS + s * kTok;
 #pragma unroll
                 for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
-                        mma_ts(tmem + kColS + s * kTok, tmem + kColQ + (t == 1) * (HD / 2) + 8 * k,
-                               smem_desc(sk + (s * PARTS + (t == 2)) * M::kK + (k >> 2) * (kTok * 128) + 32 * (k & 3)), idesc<kTok>(), t | k ? 1u : 0u);
+                        mma_ts(d, tmem + kColQ + (t == 1) * (HD / 2) + 8 * k, lo + (((t == 2) * M::kK + (k >> 2) * (kTok * 128) + 32 * (k & 3)) >> 4), hi,
+                               idesc<kTok>(), t | k ? 1u : 0u);
                 tc_commit(&bars->qk[s]);
-                return true;
-            };
-            ok = ok && scores(0) && (tiles < 2 || scores(1));
-            for (int i = 0; ok && i < tiles; ++i) ok = sums(i) && (i + 2 >= tiles || scores(i + 2));
+            }
             tc_commit(&bars->final_);                                     // all MMAs issued so far complete before TMEM is freed
         }
-    } else {
+    } else if (warp == kWarpMma + 1) {
+        // ---------------- sums, by one thread: o += weights * values of tile i
+        if (lane == 0) {
+            const uint64_t desc = smem_desc(sv);
+            const uint32_t hi = static_cast<uint32_t>(desc >> 32);
+            for (int i = 0; i < tiles; ++i) {
+                const int s = i & 1;
+                const uint32_t par = (i >> 1) & 1;
+                if (!wait_or_abort_sleep(&bars->vfull[s], par, abort) || !wait_or_abort_sleep(&bars->pfull[s], par, abort)) break;
+                tc_fence_after();
+                const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kV >> 4), d = tmem + kColO + s * HD, p = tmem + kColS + s * kTok;
+                const uint32_t acc = i > 1;
+#pragma unroll
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(d, p + (t == 1) * 32 + 8 * k, lo + (((t == 2) * M::kV + 32 * k) >> 4), hi, idesc<HD>(), t | k ? 1u : acc);
+                tc_commit(&bars->pv[s]);
+            }
+            tc_commit(&bars->final_);
+        }
+    } else if (warp == kWarpMma + 2) {
         // ---------------- chunks of a tile: lane g one of its groups
         const int gpp = a.page_size / kvGroup;
         int issued = 0;
