@@ -23,7 +23,7 @@
 // range: a weight of 2^-90 counts where the larger ones meet zero codes.
 // Why not tcgen05 here: its tiles are 128 rows, and B comes from shared memory only, so the codes would be
 // converted through shared memory for rows that are mostly absent.
-#include "layer_ops.cuh"
+#include "attn_join.cuh"
 
 namespace gq {
 GQ_ERROR_ACCESSOR(attn)
@@ -31,8 +31,6 @@ namespace {
 
 constexpr int kManyRows = 256;                    // rows a kv head from which attn_tiles.cu takes the call
 constexpr int kBlocks = 152;                       // one thread block an SM
-constexpr float kNone = -1e30f;                    // running maximum of a row that has seen no key
-constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr float kLift = 108.f;                     // f32 weights carry 2^108: times a scale below 2^16 and 2^kSlack they stay in f32's range
 constexpr float kSlack = 2.f;                      // a score may pass the running maximum by this much before it moves: 1.02 (16 bits: 0)
@@ -43,18 +41,6 @@ template <int HD, int MT> __host__ __device__ constexpr int warps() { return HD 
 template <int HD, int MT> __host__ __device__ constexpr int stages() { return HD == 64 ? 4 : HD == 128 ? (MT == 1 ? 3 : 4) : 2; }
 template <int HD, int MT> __host__ __device__ constexpr int ring_bytes() { return warps<HD, MT>() * stages<HD, MT>() * kv_chunk_bytes(HD); }
 template <int HD, int MT> constexpr int smem_bytes() { return 1024 + ring_bytes<HD, MT>() + warps<HD, MT>() * MT * (HD / 16) * 512; }
-
-// The workspace: partial sums [2][runs][rows][HD] (heads, tails), their maxima and sums [2][runs][rows], and for each run the tile whose end
-// it has after an earlier run began it
-struct Head {
-    int first;             // the run that began the tile; -1: none
-    int q0, tile0, rows, hk;
-};
-struct Parts {
-    float* o;
-    float2* ml;
-    Head* head;
-};
 
 // One sequence's share of the work.
 struct Seq {
@@ -110,24 +96,6 @@ __device__ __forceinline__ int locate(const AttnArgs& a, int lane, long long w, 
     first = before;
     return a.seqs;
 }
-// x / d and x % d, in 32 bits where x allows
-__device__ __forceinline__ void div_mod(long long x, int d, int& quot, int& rest) {
-    if (x < 0x7fffffffll) {
-        quot = static_cast<int>(x) / d;
-        rest = static_cast<int>(x) - quot * d;
-    } else {
-        quot = static_cast<int>(x / d);
-        rest = static_cast<int>(x % d);
-    }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
-
 // c = a * b
 __device__ __forceinline__ void mma16816_set(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm(
@@ -804,91 +772,6 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
     }
 }
 
-// Joins the tiles that runs share, in the order of the runs: the tails of the blocks from the run that began the tile, and the head of the
-// run that ends it.  A block looks at one run, a warp at rows of its head, a lane at four columns (256: two times four).  Sixteen parts are
-// requested at once, before their weights are known.  Rows of sequences without keys are written here too.
-template <int PARTS, int MT> __host__ __device__ constexpr int join_warps() { return tile_rows<PARTS, MT>() < 8 ? tile_rows<PARTS, MT>() : 8; }
-
-template <typename T, int HD, int PARTS, int MT>
-__global__ void __launch_bounds__(join_warps<PARTS, MT>() * 32) attn_join_kernel(const AttnArgs a, const Parts parts) {
-    constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1;
-    constexpr int kRunsAll = kBlocks * kWarps, kBatch = 16 / kRuns;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.kv_heads;
-    const int run = blockIdx.x;
-    const Head head = parts.head[run];
-    if (head.first >= 0)
-        for (int r = warp; r < head.rows; r += join_warps<PARTS, MT>()) {
-            // parts: the tail of the run that began the tile, those of the blocks between, the head
-            const int block0 = head.first / kWarps, n = (run + kWarps - 1) / kWarps - block0 + 1;
-            float top = kNone, l = 0.f;
-            float4 v[kRuns];
-#pragma unroll
-            for (int c = 0; c < kRuns; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j0 = 0; j0 < n; j0 += kBatch) {
-                auto slot = [&](int j) {
-                    const size_t s = j >= n - 1 ? run : kRunsAll + (j == 0 ? head.first : (block0 + j) * kWarps);
-                    return s * kRows + r;
-                };
-                const int j = j0 + lane % kBatch;
-                const float2 ml = j < n ? parts.ml[slot(j)] : make_float2(kNone, 0.f);
-                float4 x[kBatch][kRuns];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                    for (int c = 0; c < kRuns; ++c)
-                        if (j0 + k < n) x[k][c] = *reinterpret_cast<const float4*>(parts.o + slot(j0 + k) * HD + 128 * c + 4 * (lane % kLanes));
-                float up = fmaxf(ml.x, top);
-#pragma unroll
-                for (int o = kBatch / 2; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
-                const float f = ex2(ml.x - up), down = ex2(top - up);
-                float sum = f * ml.y;
-#pragma unroll
-                for (int o = kBatch / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                l = fmaf(l, down, sum);
-                top = up;
-#pragma unroll
-                for (int c = 0; c < kRuns; ++c) v[c] = make_float4(v[c].x * down, v[c].y * down, v[c].z * down, v[c].w * down);
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const float h = __shfl_sync(0xffffffffu, f, k);
-                    if (j0 + k < n)
-#pragma unroll
-                        for (int c = 0; c < kRuns; ++c)
-                            v[c] = make_float4(fmaf(h, x[k][c].x, v[c].x), fmaf(h, x[k][c].y, v[c].y), fmaf(h, x[k][c].z, v[c].z), fmaf(h, x[k][c].w, v[c].w));
-                }
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            T* out = static_cast<T*>(a.out) + (head.q0 + (head.tile0 + r) / group) * a.out_stride + (head.hk * group + (head.tile0 + r) % group) * HD;
-#pragma unroll
-            for (int c = 0; c < kRuns; ++c)
-                if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
-        }
-    for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
-        if (a.kv_len[b] > 0) continue;
-        const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
-        for (int tok = warp; tok < n; tok += join_warps<PARTS, MT>())
-            for (int d = lane * 4; d < a.q_heads * HD; d += 128)
-                store4(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
-    }
-}
-
-template <typename K, typename... A>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T, int HD, int PARTS, int MT>
 cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), smem = smem_bytes<HD, MT>();
@@ -903,19 +786,14 @@ cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
     int shift = -1;
     for (int i = 0; i < 16; ++i)
         if (gpp == 1 << i) shift = i;
-    constexpr size_t runs = kBlocks * kWarps;
-    Parts parts;
-    parts.o = static_cast<float*>(a.workspace);
-    parts.ml = reinterpret_cast<float2*>(parts.o + 2 * runs * kRows * HD);
-    parts.head = reinterpret_cast<Head*>(parts.ml + 2 * runs * kRows);
+    const Parts parts = parts_at(a.workspace, kBlocks * kWarps, kRows, HD);
     const cudaError_t e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), (kWarps + 1) * 32, smem, s, a, parts, shift);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_join_kernel<T, HD, PARTS, MT>, dim3(kBlocks * kWarps), join_warps<PARTS, MT>() * 32, 0, s, a, parts);
+    return launch_join<T, HD, kRows, kWarps>(a, parts, kBlocks * kWarps, s);
 }
 template <int HD, int PARTS, int MT>
 size_t rows_bytes() {
-    const size_t runs = kBlocks * warps<HD, MT>();
-    return runs * (2 * tile_rows<PARTS, MT>() * (HD * 4 + 8) + sizeof(Head));
+    return parts_bytes(kBlocks * warps<HD, MT>(), tile_rows<PARTS, MT>(), HD);
 }
 
 // One 16-row (8-row for f32) tile where a kv head's rows fit it, else two of them at a time (head_dim 256: the
@@ -944,6 +822,7 @@ size_t rows_type_bytes(long long rows) {
 
 size_t attn_workspace_bytes(int, int max_q, int q_heads, int kv_heads, int head_dim, int type) {
     const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
+    if (head_dim <= 128 && rows >= kManyRows) return attn_tiles_workspace_bytes(head_dim);
     if (type == GQ_F32)
         return head_dim == 64 ? rows_type_bytes<float, 64>(rows) : head_dim == 128 ? rows_type_bytes<float, 128>(rows) : rows_type_bytes<float, 256>(rows);
     return head_dim == 64 ? rows_type_bytes<__half, 64>(rows) : head_dim == 128 ? rows_type_bytes<__half, 128>(rows) : rows_type_bytes<__half, 256>(rows);

@@ -1,0 +1,144 @@
+// What the two attention kernels share: the cut of their work into runs of units, and the joining of tiles that runs share.
+//
+// A kernel's units (pieces of one tile's keys), in the order sequence, kv head, row tile, key, are cut into equal runs.  A run that begins and
+// ends a tile writes its rows; of a tile that several runs share, each leaves partial sums, and attn_join_kernel adds them in the order of the
+// runs: the result does not depend on timing.
+#pragma once
+
+#include "layer_ops.cuh"
+
+namespace gq {
+namespace {
+
+constexpr float kNone = -1e30f;                    // running maximum of a row that has seen no key
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
+
+// x / d and x % d, in 32 bits where x allows
+__device__ __forceinline__ void div_mod(long long x, int d, int& quot, int& rest) {
+    if (x < 0x7fffffffll) {
+        quot = static_cast<int>(x) / d;
+        rest = static_cast<int>(x) - quot * d;
+    } else {
+        quot = static_cast<int>(x / d);
+        rest = static_cast<int>(x % d);
+    }
+}
+
+// The workspace: partial sums [2][runs][rows][HD] (heads, tails) relative to 2^m, their m and l [2][runs][rows], and for each run the tile
+// whose end it has after an earlier run began it
+struct Head {
+    int first;             // the run that began the tile; -1: none
+    int q0, tile0, rows, hk;
+};
+struct Parts {
+    float* o;
+    float2* ml;
+    Head* head;
+};
+inline size_t parts_bytes(size_t runs, size_t rows, size_t hd) { return runs * (2 * rows * (hd * 4 + 8) + sizeof(Head)); }
+inline Parts parts_at(void* workspace, size_t runs, size_t rows, size_t hd) {
+    Parts p;
+    p.o = static_cast<float*>(workspace);
+    p.ml = reinterpret_cast<float2*>(p.o + 2 * runs * rows * hd);
+    p.head = reinterpret_cast<Head*>(p.ml + 2 * runs * rows);
+    return p;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A block looks at one run, a warp at rows of its head, a lane at four columns (256: two times four).  GROUP neighbouring runs (the warps of a
+// block) have joined their tails already: the first of them holds the sum.  Sixteen parts are requested at once, before their weights are known.
+// Rows of sequences without keys are written here too.
+template <typename T, int HD, int ROWS, int GROUP>
+__global__ void __launch_bounds__((ROWS < 8 ? ROWS : 8) * 32) attn_join_kernel(const AttnArgs a, const Parts parts, int runs) {
+    constexpr int kWarps = ROWS < 8 ? ROWS : 8, kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kBatch = 16 / kRuns;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.kv_heads;
+    const int run = blockIdx.x;
+    const Head head = parts.head[run];
+    if (head.first >= 0)
+        for (int r = warp + kWarps * blockIdx.y; r < head.rows; r += kWarps * gridDim.y) {
+            // parts: the tail of the run that began the tile, those of the groups between, the head
+            const int group0 = head.first / GROUP, n = (run + GROUP - 1) / GROUP - group0 + 1;
+            float top = kNone, l = 0.f;
+            float4 v[kRuns];
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < n; j0 += kBatch) {
+                auto slot = [&](int j) {
+                    const size_t s = j >= n - 1 ? run : runs + (j == 0 ? head.first : (group0 + j) * GROUP);
+                    return s * ROWS + r;
+                };
+                const int j = j0 + lane % kBatch;
+                const float2 ml = j < n ? parts.ml[slot(j)] : make_float2(kNone, 0.f);
+                float4 x[kBatch][kRuns];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int c = 0; c < kRuns; ++c)
+                        if (j0 + k < n) x[k][c] = *reinterpret_cast<const float4*>(parts.o + slot(j0 + k) * HD + 128 * c + 4 * (lane % kLanes));
+                float up = fmaxf(ml.x, top);
+#pragma unroll
+                for (int o = kBatch / 2; o > 0; o >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+                const float f = ex2(ml.x - up), down = ex2(top - up);
+                float sum = f * ml.y;
+#pragma unroll
+                for (int o = kBatch / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l = fmaf(l, down, sum);
+                top = up;
+#pragma unroll
+                for (int c = 0; c < kRuns; ++c) v[c] = make_float4(v[c].x * down, v[c].y * down, v[c].z * down, v[c].w * down);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float h = __shfl_sync(0xffffffffu, f, k);
+                    if (j0 + k < n)
+#pragma unroll
+                        for (int c = 0; c < kRuns; ++c)
+                            v[c] = make_float4(fmaf(h, x[k][c].x, v[c].x), fmaf(h, x[k][c].y, v[c].y), fmaf(h, x[k][c].z, v[c].z), fmaf(h, x[k][c].w, v[c].w));
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* out = static_cast<T*>(a.out) + (head.q0 + (head.tile0 + r) / group) * a.out_stride + (head.hk * group + (head.tile0 + r) % group) * HD;
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c)
+                if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
+        }
+    if (blockIdx.y == 0)
+        for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+            if (a.kv_len[b] > 0) continue;
+            const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
+            for (int tok = warp; tok < n; tok += kWarps)
+                for (int d = lane * 4; d < a.q_heads * HD; d += 128)
+                    store4(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+}
+
+template <typename T, int HD, int ROWS, int GROUP>
+cudaError_t launch_join(const AttnArgs& a, const Parts& parts, int runs, cudaStream_t s) {
+    constexpr int kWarps = ROWS < 8 ? ROWS : 8;
+    return launch_dependent(attn_join_kernel<T, HD, ROWS, GROUP>, dim3(runs, ROWS / kWarps > 4 ? 4 : 1), kWarps * 32, 0, s, a, parts, runs);
+}
+
+}  // namespace
+}  // namespace gq

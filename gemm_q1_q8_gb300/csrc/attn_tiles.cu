@@ -16,14 +16,18 @@
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
 // chunks without moving single bytes.
 //
+// Work: the key tiles of every (sequence, kv head, row tile) are cut into one equal run a thread block (attn_join.cuh), so 512 row tiles
+// leave no SM idle, and few rows over a long context use them all.
+//
 //   warps 0-7   softmax, two groups that take every other tile, each with a running maximum and sums (in tensor memory) of its own, joined at
 //               the end: scores from tensor memory, a row a thread (so no shuffles), the weights into the scores' place; the maximum moves
 //               (and the sums are multiplied) only where a row's scores pass it by 2^kSlack
 //   warps 8-15  keys and values of a tile, two stages
 //   warp 16     MMA issue of the scores: those of tile i + 2 into the place of the weights of tile i, once its sums are done
 //   warp 17     MMA issue of the sums
-//   warp 18     bulk copies of the chunks, two stages (warp 19 fills the last warpgroup)
-#include "layer_ops.cuh"
+//   warp 18     bulk copies of the chunks, two stages
+//   warp 19     the run's pieces (in a ring that the other roles read), and the exponents of a tile's scales
+#include "attn_join.cuh"
 #include "tc_common.cuh"
 
 namespace gq {
@@ -35,43 +39,30 @@ constexpr int kWarpKV = 8, kNumKV = 8, kWarpMma = 16, kThreads = 20 * 32;
 // Registers a thread of each warpgroup, out of the 5 x 96 that a launch of 640 threads has: two softmax groups, two of keys and values, one
 constexpr int kRegsSoftmax = 136, kRegsKV = 72, kRegsRest = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsKV + kRegsRest == 5 * 96, "registers");
-constexpr float kNone = -1e30f, kLog2e = 1.4426950408889634f;
+constexpr int kBlocks = 152;                               // one thread block an SM
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 
-struct Info {
-    float kfactor;         // 2^e of the keys' scales
-    int vexp;              // e of the values' scales
-    int have;              // a bit for each chunk whose page exists
-    int odd;               // whether some value scale is not finite:
-    uint32_t bad[2];       // those tokens' columns
-};
-struct Bars {
-    uint64_t rawfull[2], rawfree[2], kfull[2], vfull[2], qk[2], pv[2], pfull[2], qfull, final_;
-    uint32_t tmem;
-    int abort;
-    int have[2];
-    Info info[4];
-    float m[2][kRows], l[2][kRows];                        // the groups' maxima and sums, at the end
-    int vref[2][kRows];
-};
-
-template <int HD, int PARTS> struct Smem {
-    static constexpr int kRaw = kGroups * kv_chunk_bytes(HD);             // a tile's chunks
-    static constexpr int kK = kTok * HD * 2, kV = HD * kTok * 2;          // one part of a tile's keys, values
-    static constexpr int kKat = 0, kVat = 2 * PARTS * kK, kRawAt = kVat + 2 * PARTS * kV, kBars = kRawAt + 2 * kRaw;
-    static constexpr int kAll = 1024 + kBars + sizeof(Bars);
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t codes2(uint32_t lo, uint32_t hi, uint32_t sel) { return __byte_perm(lo, hi, sel) & 0x807f807fu; }
+
+// Bounded wait (~1 s) that also gives up when another role has.  Small, because it stands in many places and the roles' code together
+// should stay in the instruction caches.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity)) return true;
+        if (*abort) return false;
+        if (__builtin_expect(globaltimer_ns() - t0 > 1000000000ull, 0)) {
+            report_error(kErrMmaTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+}
 
 template <int N>
 __device__ __forceinline__ constexpr uint32_t idesc() {                   // D f32, A and B f16, both K-major, M = 128
@@ -122,6 +113,10 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
 
 // Column n of a tile's scores holds this token of the tile
 __device__ __forceinline__ constexpr int token_of(int n) { return (n & ~15) + 2 * (n & 3) + ((n >> 2) & 1) + 8 * ((n >> 3) & 1); }
+
+// Columns of a 16-token chunk that hold tokens 0 .. k
+__constant__ uint16_t kUpTo[16] = {0x0001, 0x0011, 0x0013, 0x0033, 0x0037, 0x0077, 0x007f, 0x00ff,
+                                   0x01ff, 0x11ff, 0x13ff, 0x33ff, 0x37ff, 0x77ff, 0x7fff, 0xffff};
 
 // What a tile's scales need to get near 1: the exponent e of the largest finite one (all below 2^e), by a whole warp.  `edge`: only the
 // first `end` tokens, of the chunks in `have`, count.  `odd`: some scale is not finite (its bits are above every finite one's).
@@ -179,13 +174,130 @@ __device__ __forceinline__ void put8(uint8_t* dst, int part_bytes, const uint32_
     if (PARTS == 2) *reinterpret_cast<uint4*>(dst + part_bytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
+// A sequence, and the key tiles of its row tiles
+struct Seq {
+    int L, T, q0, rows;    // cached tokens, query tokens, first query row, rows of a kv head
+    int len;               // visible at most
+    __device__ __forceinline__ int row_tiles() const { return (rows + kRows - 1) / kRows; }
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+    Seq s;
+    s.q0 = a.q_start[b];
+    s.T = a.q_start[b + 1] - s.q0;
+    s.L = a.kv_len[b];
+    if (s.T > a.max_q || s.L > a.max_kv) report_error(kErrIndex);
+    s.rows = min(max(s.T, 0), a.max_q) * (a.q_heads / a.kv_heads);
+    s.len = min(max(s.L, 0), a.max_kv);
+    return s;
+}
+// Key tiles that row tile rt sees; one at least, which writes zeros where there is none
+__device__ __forceinline__ int key_tiles(const AttnArgs& a, const Seq& s, int rt) {
+    const int group = a.q_heads / a.kv_heads, end = min((rt + 1) * kRows, s.rows);
+    const int seen = a.tree ? s.len : min(s.len, max(s.L - s.T + (end + group - 1) / group, 0));
+    return max((seen + kTok - 1) / kTok, 1);
+}
+// The key tiles of one kv head of a sequence, by a warp
+__device__ __forceinline__ long long head_units(const AttnArgs& a, const Seq& s, int lane) {
+    int sum = 0;
+    for (int rt = lane; rt < s.row_tiles(); rt += 32) sum += key_tiles(a, s, rt);
+    return __reduce_add_sync(0xffffffffu, sum);
+}
+
+// A block's run, piece by piece: key tiles k0 .. k1 of row tile rt of kv head hk of sequence b
+struct Piece {
+    Seq s;
+    int b, hk, rt, k0, k1, all, left;                      // left: units of the run from k0 on
+    int begun;             // the run that began the tile, of the run's first piece
+    // The first piece of a run (a whole warp together) -> whether there is one
+    __device__ __forceinline__ bool first(const AttnArgs& a, int lane) {
+        long long total = 0;
+        for (int i = 0; i < a.seqs; ++i) total += head_units(a, load_seq(a, i), lane) * a.kv_heads;
+        const long long per = max((total + kBlocks - 1) / kBlocks, 1ll), pos = per * blockIdx.x;
+        if (pos >= total) return false;
+        left = static_cast<int>(min(per, total - pos));
+        long long before = 0, units = 0;
+        for (b = 0;; ++b) {
+            s = load_seq(a, b);
+            units = head_units(a, s, lane);
+            if (before + units * a.kv_heads > pos) break;
+            before += units * a.kv_heads;
+        }
+        int rest;
+        div_mod(pos - before, static_cast<int>(units), hk, rest);
+        for (rt = 0;; rt += 32) {
+            const int mine = rt + lane < s.row_tiles() ? key_tiles(a, s, rt + lane) : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                rt += at;
+                k0 = rest - __shfl_sync(0xffffffffu, upto - mine, at);
+                break;
+            }
+            rest -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        cut(a);
+        div_mod(pos - k0, static_cast<int>(per), begun, rest);
+        return true;
+    }
+    __device__ __forceinline__ void cut(const AttnArgs& a) {
+        all = key_tiles(a, s, rt);
+        k1 = min(all, k0 + left);
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a) {
+        left -= k1 - k0;
+        if (left == 0) return false;
+        k0 = 0;
+        if (++rt >= s.row_tiles()) {
+            rt = 0;
+            if (++hk >= a.kv_heads) {
+                hk = 0;
+                do s = load_seq(a, ++b); while (s.rows == 0);
+            }
+        }
+        cut(a);
+        return true;
+    }
+};
+
+struct Info {
+    int kexp;              // e of the keys' scales
+    int vexp;              // e of the values' scales
+    int have;              // a bit for each chunk whose page exists
+    int odd;               // whether some value scale is not finite:
+    uint32_t bad[2];       // those tokens' columns
+};
+struct Bars {
+    uint64_t rawfull[2], rawfree[2], expfull[2], kfull[2], vfull[2], qk[2], pv[2], pfull[2], qfull, final_, piecefull[4], piecefree[4], meet;
+    uint32_t tmem;
+    int abort;
+    int have[2];
+    Info info[4];
+    float amax[2][kRows];                                  // of the groups' halves of the queries
+    float m[2][kRows], l[2][kRows];                        // the groups' maxima and sums, at the end
+    int vref[2][kRows];
+    Piece piece[4];                                        // a ring, filled by one warp; k1 = 0 ends it
+};
+
+template <int HD, int PARTS> struct Smem {
+    static constexpr int kRaw = kGroups * kv_chunk_bytes(HD);             // a tile's chunks
+    static constexpr int kK = kTok * HD * 2, kV = HD * kTok * 2;          // one part of a tile's keys, values
+    static constexpr int kKat = 0, kVat = 2 * PARTS * kK, kRawAt = kVat + 2 * PARTS * kV, kBars = kRawAt + 2 * kRaw;
+    static constexpr int kAll = 1024 + kBars + sizeof(Bars);
+};
+
 template <typename T, int HD, int PARTS, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a, const Parts parts) {
     using M = Smem<HD, PARTS>;
-    constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32, kAtoms = HD / 64;
+    constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_align1024(smem_raw);
-    uint8_t* sk = base + M::kKat;                          // [2][PARTS][kAtoms][64 rows x 128 bytes]
+    uint8_t* sk = base + M::kKat;                          // [2][PARTS][HD / 64][64 rows x 128 bytes]
     uint8_t* sv = base + M::kVat;                          // [2][PARTS][HD rows x 128 bytes]
     uint8_t* sraw = base + M::kRawAt;                      // [2][kGroups][chunk]
     Bars* bars = reinterpret_cast<Bars*>(base + M::kBars);
@@ -194,21 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.z, hk = blockIdx.y, group = a.q_heads / a.kv_heads;
-    const int q0 = a.q_start[b], T_ = a.q_start[b + 1] - q0, L = a.kv_len[b];
-    if (threadIdx.x == 0 && (T_ > a.max_q || L > a.max_kv)) report_error(kErrIndex);
-    const int rows = min(T_, a.max_q) * group;
-    const int tile0 = (gridDim.x - 1 - blockIdx.x) * kRows;               // the longest first
-    if (tile0 >= rows) return;
-    const int len = min(max(L, 0), a.max_kv);
-    // keys that the last of the rows sees
-    const int seen = a.tree ? len : min(len, max(L - T_ + min(tile0 + kRows, rows) / group + (min(tile0 + kRows, rows) % group ? 1 : 0), 0));
-    const int tiles = (seen + kTok - 1) / kTok;
-
+    const int group = a.q_heads / a.kv_heads;
+    if (threadIdx.x == 0) parts.head[blockIdx.x].first = -1;               // the piece that ends a shared tile says so later
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->rawfull[s], 1);
             mbar_init(&bars->rawfree[s], kNumKV);
+            mbar_init(&bars->expfull[s], 1);
             mbar_init(&bars->kfull[s], kNumKV);
             mbar_init(&bars->vfull[s], kNumKV);
             mbar_init(&bars->qk[s], 1);
@@ -216,6 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             mbar_init(&bars->pfull[s], 4);
         }
         mbar_init(&bars->qfull, 8);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars->piecefull[i], 1);
+            mbar_init(&bars->piecefree[i], 8 + kNumKV + 3);
+        }
+        mbar_init(&bars->meet, 8);
         mbar_init(&bars->final_, 2);
         bars->abort = 0;
         fence_barrier_init();
@@ -228,79 +337,112 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
+    // the run's pieces, as every role takes them: piece n is there (false: no more, or given up); this warp is done with it
+    auto take = [&](int n) { return wait_for(&bars->piecefull[n & 3], (n >> 2) & 1, abort) && bars->piece[n & 3].k1 > 0; };
+    auto done = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->piecefree[n & 3]);
+    };
 
     if (warp < kWarpKV) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------- softmax: row tile0 + 32 * (warp % 4) + lane, tiles wg, wg + 2, ...
         const int wg = warp >> 2, lr = (warp & 3) * 32 + lane;
-        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), cs = tl + kColS + wg * kTok, co = tl + kColO + wg * HD;
+        int it = 0;                                                       // tiles so far
+        bool ok = true, more = take(0);
+        // this thread's half of its row's queries, requested before the piece before it is written out: positions 4 i .. of atom c = wg
+        // (HD = 64: of half of the atom)
+        constexpr int kQ = HD / 8;                                        // runs of four dims
+        typename Vec4<T>::Raw q[kQ];
+        auto request = [&](const Piece& p) {
+            const int r = p.rt * kRows + lr, tok = r < p.s.rows ? r / group : 0, h = r < p.s.rows ? r % group : 0;
+            const T* at = static_cast<const T*>(a.q) + (p.s.q0 + tok) * a.q_stride + (p.hk * group + h) * HD;
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                const int k = HD == 64 ? i + 8 * wg : i, t = k >> 2, hh = (k >> 1) & 1, bb = k & 1;
+                q[i] = *reinterpret_cast<const typename Vec4<T>::Raw*>(at + (HD == 64 ? 0 : 64 * wg) + 32 * hh + 16 * bb + 4 * t);
+            }
+        };
+        uint32_t met = 0;
+        auto meet = [&]() {                                               // all softmax warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->meet);
+            ok = wait_for(&bars->meet, met++ & 1, abort) && ok;
+            __syncwarp();
+        };
+        if (more) request(bars->piece[0]);
+        for (int pi = 0; ok && more; ++pi) {
+        const Piece& p = bars->piece[pi & 3];
+        const int q0 = p.s.q0, hk = p.hk, tile0 = p.rt * kRows, group0 = tile0 / group;
+        // tokens that every row of the tile sees
+        const int all_see = min(p.s.L - p.s.T + (a.tree ? 0 : group0 + 1), a.max_kv);
         const int r = tile0 + lr;
-        const bool in = r < rows;
+        const bool in = r < p.s.rows;
         const int tok = in ? r / group : 0, h = in ? r % group : 0;
         float rs;
         {
-            const T* q = static_cast<const T*>(a.q) + (q0 + tok) * a.q_stride + (hk * group + h) * HD;
             float amax = 0.f;
-#pragma unroll 8
-            for (int d = 0; d < HD; d += 4) {
-                const float4 v = load4(q + d);
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                const float4 v = Vec4<T>::widen(q[i]);
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
             }
+            bars->amax[wg][lr] = amax;
+            meet();
+            amax = fmaxf(bars->amax[0][lr], bars->amax[1][lr]);
             const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
             const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
             // the scale's sign goes into the queries, and a scale of 0 (equal weights) too: the scores' factor stays positive
             const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
             rs = (CAP ? size / a.softcap : size * kLog2e) * pow2i(-up);
-            if (wg < kAtoms) {
-                const int c = wg;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t hi[16], lo[16];
+            for (int part = 0; part < kQ / 8; ++part) {
+                uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {                          // four dims: positions 4 i .. of this half of the atom
-                        const int t = 2 * half + (i >> 2), hh = (i >> 1) & 1, bb = i & 1;
-                        float4 v = load4(q + 64 * c + 32 * hh + 16 * bb + 4 * t);
-                        v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-                        const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
-                        hi[2 * i] = u32(x);
-                        hi[2 * i + 1] = u32(y);
-                        if (PARTS == 2) {
-                            const float2 fx = __half22float2(x), fy = __half22float2(y);
-                            lo[2 * i] = u32(__floats2half2_rn(v.x - fx.x, v.y - fx.y));
-                            lo[2 * i + 1] = u32(__floats2half2_rn(v.z - fy.x, v.w - fy.y));
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    float4 v = Vec4<T>::widen(q[8 * part + i]);
+                    v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                    const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
+                    hi[2 * i] = u32(x);
+                    hi[2 * i + 1] = u32(y);
+                    if (PARTS == 2) {
+                        const float2 fx = __half22float2(x), fy = __half22float2(y);
+                        lo[2 * i] = u32(__floats2half2_rn(v.x - fx.x, v.y - fx.y));
+                        lo[2 * i + 1] = u32(__floats2half2_rn(v.z - fy.x, v.w - fy.y));
                     }
-                    tc_st16(tl + kColQ + 32 * c + 16 * half, hi);
-                    if (PARTS == 2) tc_st16(tl + kColQ + HD / 2 + 32 * c + 16 * half, lo);
                 }
-                tc_wait_st();
+                const uint32_t col = tl + kColQ + 16 * (wg * (kQ / 8) + part);
+                tc_st16(col, hi);
+                if (PARTS == 2) tc_st16(col + HD / 2, lo);
             }
+            tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->qfull);
         }
-        const int last = in ? L - T_ + tok : -1;
-        const uint32_t cs = tl + kColS + wg * kTok, co = tl + kColO + wg * HD;
+        const int last = in ? p.s.L - p.s.T + tok : -1;
         float m = kNone, l = 0.f;
         int vref = -24;
-        bool ok = true;
-        for (int i = wg; i < tiles; i += 2) {
+        const int tiles = p.k1 - p.k0;
+        for (int j = (it ^ wg) & 1; ok && j < tiles; j += 2) {                  // tile it + j of all, which is in this group's place
+            const int i = it + j;
             // (the scores' MMAs were issued after the keys' barrier, so what stands in `info` was written before; and after the sums of
             // tile i - 2, so those are complete)
-            if (!wait_or_abort_sleep(&bars->qk[wg], (i >> 1) & 1, abort)) {
+            if (!wait_for(&bars->qk[wg], (i >> 1) & 1, abort)) {
                 ok = false;
                 break;
             }
             __syncwarp();
             tc_fence_after();
             const Info& info = bars->info[i & 3];
-            float x_of = rs * info.kfactor;
+            float x_of = rs * pow2i(info.kexp);
             const int vexp = info.vexp, have = info.have;
             float x[kTok];
             tc_ld32(cs, x);
             tc_ld32(cs + 32, x + 32);
             tc_wait_ld();
-            const int j0 = i * kTok;
+            const int j0 = (p.k0 + j) * kTok;
             if (CAP) {
 #pragma unroll
                 for (int n = 0; n < kTok; ++n) {
@@ -310,19 +452,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 }
                 x_of = 1.f;
             }
-            if (j0 + kTok > min(L - T_, a.max_kv) || have != (1 << kGroups) - 1) {
-                const unsigned long long bits = a.tree && in ? a.tree[q0 + tok] : 0ull;
-                uint32_t vis[2] = {0u, 0u};
+            if (j0 + kTok > all_see || have != (1 << kGroups) - 1) {
+                const int len = p.s.len, base = p.s.L - p.s.T;
+                unsigned long long vis = 0;
+                if (!a.tree) {
+                    const int upto = min(last, len - 1) - j0;             // the last visible token of the tile
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        if (upto >= 16 * g && (have >> g & 1)) vis |= static_cast<unsigned long long>(kUpTo[min(upto - 16 * g, 15)]) << (16 * g);
+                } else {
+                    const unsigned long long bits = in ? a.tree[q0 + tok] : 0ull;
 #pragma unroll 1
-                for (int n = 0; n < kTok; ++n) {
-                    const int j = j0 + token_of(n), rel = j - (L - T_);
-                    const bool v = last >= 0 && j < len && (have >> (n >> 4) & 1) &&
-                                   (a.tree ? rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)) : j <= last);
-                    vis[n >> 5] |= static_cast<uint32_t>(v) << (n & 31);
+                    for (int n = 0; n < kTok; ++n) {
+                        const int key = j0 + token_of(n), rel = key - base;
+                        const bool v = in && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
+                        vis |= static_cast<unsigned long long>(v) << n;
+                    }
                 }
+                const uint32_t vis0 = static_cast<uint32_t>(vis), vis1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
                 for (int n = 0; n < kTok; ++n)
-                    if (!(vis[n >> 5] >> (n & 31) & 1u)) x[n] = -INFINITY;
+                    if (!((n < 32 ? vis0 : vis1) >> (n & 31) & 1u)) x[n] = -INFINITY;
             }
             float top = x[0];
 #pragma unroll
@@ -335,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 l *= down;
                 m = mn;
                 vref = vn;
-                if (i >= 2) {
+                if (j >= 2) {
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 16) {
                         uint32_t o[16];
@@ -348,13 +498,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 }
             }
             const float from = m - kLift - static_cast<float>(vexp - vref), lower = pow2i(vref - vexp) * 0x1p-11f;
-            float sum0 = 0.f, sum1 = 0.f;
+            if (info.odd) {                                               // a value that is not finite, seen by this row
+                const unsigned long long bad = info.bad[0] | static_cast<unsigned long long>(info.bad[1]) << 32;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+                for (int n = 0; n < kTok; ++n)
+                    if ((bad >> n & 1) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
+            }
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {                        // (half the code)
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    const float p0 = ex2(fmaf(x[32 * half + 2 * n], x_of, -from)), p1 = ex2(fmaf(x[32 * half + 2 * n + 1], x_of, -from));
+                    const float p0 = ex2(fmaf(x[2 * n], x_of, -from)), p1 = ex2(fmaf(x[2 * n + 1], x_of, -from));
                     sum0 += p0;
                     sum1 += p1;
                     const __half2 v = __floats2half2_rn(p0, p1);
@@ -366,32 +522,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 }
                 tc_st16(cs + 16 * half, hi);
                 if (PARTS == 2) tc_st16(cs + 32 + 16 * half, lo);
+#pragma unroll
+                for (int n = 0; n < 32; ++n) x[n] = x[32 + n];
             }
             l = fmaf(sum0 + sum1, lower, l);
-            if (info.odd) {                                               // a value that is not finite, seen by this row
-                const unsigned long long bad = info.bad[0] | static_cast<unsigned long long>(info.bad[1]) << 32;
-#pragma unroll
-                for (int n = 0; n < kTok; ++n)
-                    if ((bad >> n & 1) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
-            }
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->pfull[wg]);
         }
-        // ---- the groups' sums meet: each group writes half of the dims
-        const int mine = (tiles + 1 - wg) >> 1;                           // this group's tiles
-        if (ok && mine > 0 && !wait_or_abort(&bars->pv[wg], (mine - 1) & 1, abort)) ok = false;
-        bars->m[wg][lr] = ok ? m : __int_as_float(0x7fc00000);
-        bars->l[wg][lr] = l;
+        // ---- the groups' sums meet: each group takes half of the dims
+        it += tiles;
+        const int e0 = (it - 1 - ((it - 1 ^ wg) & 1));                    // this group's last tile, if it had one of the piece
+        if (ok && e0 >= it - tiles && !wait_for(&bars->pv[wg], (e0 >> 1) & 1, abort)) ok = false;
+        const bool has = e0 >= it - tiles;
+        more = take(pi + 1);
+        if (more) request(bars->piece[(pi + 1) & 3]);
+        bars->m[wg][lr] = !ok ? __int_as_float(0x7fc00000) : has ? m : kNone;
+        bars->l[wg][lr] = has ? l : 0.f;
         bars->vref[wg][lr] = vref;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        meet();
         {
             tc_fence_after();
             const float m0 = bars->m[0][lr], m1 = bars->m[1][lr], top = fmaxf(m0, m1), f0 = ex2(m0 - top), f1 = ex2(m1 - top);
-            const float sum = fmaf(bars->l[0][lr], f0, bars->l[1][lr] * f1), inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float sum = fmaf(bars->l[0][lr], f0, bars->l[1][lr] * f1);
+            const bool has0 = tiles > 1 || !((it - 1) & 1), has1 = tiles > 1 || ((it - 1) & 1);      // a group without tiles has no sums
+            const bool whole = p.k0 == 0 && p.k1 == p.all, head = p.k1 == p.all;
+            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
             const float a0 = f0 * pow2i(bars->vref[0][lr] - 11) * inv, a1 = f1 * pow2i(bars->vref[1][lr] - 11) * inv;
             T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD + wg * (HD / 2);
+            const size_t slot = (static_cast<size_t>(head ? 0 : kBlocks) + blockIdx.x) * kRows + lr;
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 16) {
                 uint32_t o0[16], o1[16];
@@ -400,14 +560,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 tc_wait_ld();
                 float v[16];
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {                            // a group without tiles has no sums
-                    v[n] = tiles > 0 && sum != 0.f ? __uint_as_float(o0[n]) * a0 : 0.f;
-                    if (tiles > 1 && sum != 0.f) v[n] = fmaf(__uint_as_float(o1[n]), a1, v[n]);
+                for (int n = 0; n < 16; ++n) {
+                    v[n] = has0 && sum != 0.f ? __uint_as_float(o0[n]) * a0 : 0.f;
+                    if (has1 && sum != 0.f) v[n] = fmaf(__uint_as_float(o1[n]), a1, v[n]);
                 }
                 if (in)
 #pragma unroll
-                    for (int n = 0; n < 16; n += 4) store4(out + c + n, make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]));
+                    for (int n = 0; n < 16; n += 4) {
+                        const float4 x = make_float4(v[n], v[n + 1], v[n + 2], v[n + 3]);
+                        if (whole) store4(out + c + n, x);
+                        else *reinterpret_cast<float4*>(parts.o + slot * HD + wg * (HD / 2) + c + n) = x;
+                    }
             }
+            if (!whole && wg == 0) parts.ml[slot] = make_float2(top, sum);
+            if (head && !whole && threadIdx.x == 0) {                     // (only the run's first piece can be one)
+                parts.head[blockIdx.x] = {p.begun, q0, tile0, min(p.s.rows - tile0, kRows), hk};
+            }
+        }
+        tc_fence_before();
+        meet();                                                           // the sums have been read: the next piece's may begin
+        tc_fence_after();
+        done(pi);
         }
     } else if (warp < kWarpMma) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKV));
@@ -425,33 +598,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         // and of the values: four dims 32 v_c + 4 v_g .. of eight tokens
         const int v_g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, v_c = HD == 64 ? lane & 1 : lane & 3;
         const int v_src = kv_v_offset(HD) + (w8 & 1) * 8 * HD + 4 * v_c, v_scale = kv_vs_offset(HD) + 2 * (2 * (w8 & 1) * kNb + v_c);
-        for (int i = 0; i < tiles; ++i) {
+        int i = 0;                                                        // tiles so far
+        bool ok = true;
+        for (int pi = 0; ok && take(pi); done(pi), ++pi)
+        for (int kt = bars->piece[pi & 3].k0; kt < bars->piece[pi & 3].k1; ++kt, ++i) {
             const int s = i & 1;
             const uint32_t par = (i >> 1) & 1;
-            if (!wait_or_abort_sleep(&bars->rawfull[s], par, abort)) break;
+            ok = wait_for(&bars->expfull[s], par, abort) && wait_for(&bars->rawfull[s], par, abort);
+            if (!ok) break;
             __syncwarp();
             const uint8_t* raw = sraw + s * M::kRaw;
-            const int have = bars->have[s], j0 = i * kTok;
+            const Info& info = bars->info[i & 3];
+            const int have = info.have, j0 = kt * kTok, len = bars->piece[pi & 3].s.len, ve = info.vexp;
+            const bool odd = info.odd;
             const bool edge = j0 + kTok > len || have != (1 << kGroups) - 1;      // some of the tile's tokens do not exist
             // keys, once the scores of the tile before the last are done
-            if (i >= 2 && !wait_or_abort_sleep(&bars->qk[s], par ^ 1, abort)) break;
+            if (i >= 2 && !(ok = wait_for(&bars->qk[s], par ^ 1, abort))) break;
             __syncwarp();
-            // both exponents: the scores need them
-            bool odd;
-            const int ve = scales_exponent<HD>(raw + kv_vs_offset(HD), lane, edge, len - j0, have, odd);
-            if (dt == 0) {
-                bars->info[i & 3].vexp = ve;
-                bars->info[i & 3].odd = odd;
-            }
             {
-                bool kodd;
-                const int e = scales_exponent<HD>(raw + kv_ks_offset(HD), lane, edge, len - j0, have, kodd);
                 __half2 f1, f2;
-                scale_factors(e, f1, f2);
-                if (dt == 0) {
-                    bars->info[i & 3].kfactor = pow2i(e);
-                    bars->info[i & 3].have = have;
-                }
+                scale_factors(info.kexp, f1, f2);
                 // a thread has one 16-byte unit of one token in every 128 / units tokens
                 uint4 w[kUnitsPer];
                 uint32_t sc[kUnitsPer];
@@ -478,18 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (odd && w8 < 2) {                                          // which tokens: columns 32 w8 + lane
-                const int n = 32 * w8 + lane, grp = n >> 4, p = (n >> 2) & 3, t = n & 3;
-                bool strange = false;
-                for (int c = 0; c < kNb; ++c)
-                    strange |= (*reinterpret_cast<const uint16_t*>(raw + grp * kChunk + kv_vs_offset(HD) + 2 * ((4 * t + p) * kNb + c)) & 0x7c00) == 0x7c00;
-                const uint32_t mask = __ballot_sync(0xffffffffu, strange);
-                if (lane == 0) bars->info[i & 3].bad[w8] = mask;
-            }
-            __syncwarp();
             if (lane == 0) mbar_arrive(&bars->kfull[s]);
             // values, once the sums of the tile before the last are done: this warp eight tokens (value rows 8 o ..)
-            if (i >= 2 && !wait_or_abort_sleep(&bars->pv[s], par ^ 1, abort)) break;
+            if (i >= 2 && !(ok = wait_for(&bars->pv[s], par ^ 1, abort))) break;
             __syncwarp();
             {
                 __half2 f1, f2;
@@ -541,22 +698,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     if (warp == kWarpMma) {
         // ---------------- scores, by one thread: of tile i into the place of the weights of tile i - 2
         if (lane == 0) {
-            bool ok = tiles > 0 && wait_or_abort(&bars->qfull, 0, abort);
+            bool ok = true;
             const uint64_t desc = smem_desc(sk);
             const uint32_t hi = static_cast<uint32_t>(desc >> 32);
-            for (int i = 0; ok && i < tiles; ++i) {
+            int i = 0;                                                    // tiles so far
+            for (int pi = 0; ok && take(pi); mbar_arrive(&bars->piecefree[pi & 3]), ++pi)
+            for (int k0 = bars->piece[pi & 3].k0, k1 = bars->piece[pi & 3].k1, kt = k0; kt < k1; ++kt, ++i) {
                 const int s = i & 1;
                 const uint32_t par = (i >> 1) & 1;
-                ok = wait_or_abort_sleep(&bars->kfull[s], par, abort) && (i < 2 || wait_or_abort_sleep(&bars->pv[s], par ^ 1, abort));
+                ok = (kt > k0 || wait_for(&bars->qfull, pi & 1, abort)) && wait_for(&bars->kfull[s], par, abort) &&
+                     (i < 2 || wait_for(&bars->pv[s], par ^ 1, abort));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kK >> 4), d = tmem + kColS + s * kTok;
-#pragma unroll
-                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
+#pragma unroll 1
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t) {          // high x high, low x high, high x low
+                    const uint32_t q = tmem + kColQ + (t == 1 ? HD / 2 : 0), k0 = lo + (t == 2 ? M::kK >> 4 : 0);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
-                        mma_ts(d, tmem + kColQ + (t == 1) * (HD / 2) + 8 * k, lo + (((t == 2) * M::kK + (k >> 2) * (kTok * 128) + 32 * (k & 3)) >> 4), hi,
-                               idesc<kTok>(), t | k ? 1u : 0u);
+                        mma_ts(d, q + 8 * k, k0 + (((k >> 2) * (kTok * 128) + 32 * (k & 3)) >> 4), hi, idesc<kTok>(), k ? 1u : t);
+                }
                 tc_commit(&bars->qk[s]);
             }
             tc_commit(&bars->final_);                                     // all MMAs issued so far complete before TMEM is freed
@@ -566,18 +727,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         if (lane == 0) {
             const uint64_t desc = smem_desc(sv);
             const uint32_t hi = static_cast<uint32_t>(desc >> 32);
-            for (int i = 0; i < tiles; ++i) {
+            int i = 0;                                                    // tiles so far
+            bool ok = true;
+            for (int pi = 0; ok && take(pi); mbar_arrive(&bars->piecefree[pi & 3]), ++pi)
+            for (int k0 = bars->piece[pi & 3].k0, k1 = bars->piece[pi & 3].k1, kt = k0; kt < k1; ++kt, ++i) {
                 const int s = i & 1;
                 const uint32_t par = (i >> 1) & 1;
-                if (!wait_or_abort_sleep(&bars->vfull[s], par, abort) || !wait_or_abort_sleep(&bars->pfull[s], par, abort)) break;
+                ok = wait_for(&bars->vfull[s], par, abort) && wait_for(&bars->pfull[s], par, abort);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kV >> 4), d = tmem + kColO + s * HD, p = tmem + kColS + s * kTok;
-                const uint32_t acc = i > 1;
+                const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kV >> 4), d = tmem + kColO + s * HD, w = tmem + kColS + s * kTok;
+                const uint32_t acc = kt > k0 + 1;                       // a group's first tile of a piece begins its sums
+#pragma unroll 1
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t) {
+                    const uint32_t w0 = w + (t == 1 ? 32 : 0), v0 = lo + (t == 2 ? M::kV >> 4 : 0);
 #pragma unroll
-                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t)
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(d, p + (t == 1) * 32 + 8 * k, lo + (((t == 2) * M::kV + 32 * k) >> 4), hi, idesc<HD>(), t | k ? 1u : acc);
+                    for (int k = 0; k < kTok / 16; ++k) mma_ts(d, w0 + 8 * k, v0 + (32 * k >> 4), hi, idesc<HD>(), k || t ? 1u : acc);
+                }
                 tc_commit(&bars->pv[s]);
             }
             tc_commit(&bars->final_);
@@ -585,23 +751,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     } else if (warp == kWarpMma + 2) {
         // ---------------- chunks of a tile: lane g one of its groups
         const int gpp = a.page_size / kvGroup;
-        int issued = 0;
-        for (int i = 0; i < tiles; ++i) {
+        int i = 0;                                                        // tiles so far
+        bool ok = true;
+        for (int pi = 0; ok && take(pi); done(pi), ++pi)
+        for (int kt = bars->piece[pi & 3].k0; kt < bars->piece[pi & 3].k1; ++kt, ++i) {
+            const Piece& p = bars->piece[pi & 3];
             const int s = i & 1;
             int page = -1, off = 0;
-            const int g = i * kGroups + lane;
-            const bool wanted = lane < kGroups && g * kvGroup < len;
+            const int g = kt * kGroups + lane;
+            const bool wanted = lane < kGroups && g * kvGroup < p.s.len;
             if (wanted) {
                 const int pi = g / gpp;
                 off = g - pi * gpp;
-                page = a.table[static_cast<size_t>(b) * a.table_stride + pi];
+                page = a.table[static_cast<size_t>(p.b) * a.table_stride + pi];
                 if (page < 0 || page >= a.pages) {
                     page = -1;
                     report_error(kErrIndex);
                 }
             }
             const unsigned there = __ballot_sync(0xffffffffu, page >= 0), missing = __ballot_sync(0xffffffffu, wanted && page < 0);
-            if (i >= 2 && !wait_or_abort_sleep(&bars->rawfree[s], ((i >> 1) & 1) ^ 1, abort)) break;
+            if (i >= 2 && !(ok = wait_for(&bars->rawfree[s], ((i >> 1) & 1) ^ 1, abort))) break;
+            __syncwarp();
             if (lane == 0) {
                 bars->have[s] = ((1 << kGroups) - 1) & ~missing;          // chunks past the end count as there: their tokens are past the end
                 if (there) mbar_arrive_expect_tx(&bars->rawfull[s], __popc(there) * kChunk);
@@ -609,14 +779,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             __syncwarp();
             if (page >= 0)
-                bulk_g2s(sraw + s * M::kRaw + lane * kChunk, a.cache + ((static_cast<size_t>(page) * a.kv_heads + hk) * gpp + off) * kChunk, kChunk,
+                bulk_g2s(sraw + s * M::kRaw + lane * kChunk, a.cache + ((static_cast<size_t>(page) * a.kv_heads + p.hk) * gpp + off) * kChunk, kChunk,
                          &bars->rawfull[s]);
-            issued = i + 1;
         }
         __syncwarp();
         if (*abort)                                                       // copies in flight land before shared memory goes away
-            for (int i = max(issued - 2, 0); i < issued; ++i)
-                if (lane == 0 && !mbar_wait(&bars->rawfull[i & 1], (i >> 1) & 1)) report_error(kErrDrainTimeout);
+            for (int k = max(i - 2, 0); k < i; ++k)
+                if (lane == 0 && !mbar_wait(&bars->rawfull[k & 1], (k >> 1) & 1)) report_error(kErrDrainTimeout);
+    } else if (warp == kWarpMma + 3) {
+        // ---------------- the run's pieces, a piece ahead, and the exponents of a tile's scales
+        Piece now, then;
+        int i = 0, pi = 0;                                                // tiles so far, pieces
+        bool more = then.first(a, lane), ok = true;
+        auto publish = [&](int n) {                                       // `then`, or the end
+            if (n >= 4 && !wait_for(&bars->piecefree[n & 3], ((n >> 2) & 1) ^ 1, abort)) ok = false;
+            __syncwarp();
+            if (lane == 0) {
+                if (!more) then.k1 = 0;
+                bars->piece[n & 3] = then;
+                mbar_arrive(&bars->piecefull[n & 3]);
+            }
+        };
+        publish(0);
+        while (ok && more) {
+        now = then;
+        more = then.next(a);
+        publish(++pi);
+        for (int kt = now.k0; ok && kt < now.k1; ++kt, ++i) {
+            const int s = i & 1;
+            if (!(ok = wait_for(&bars->rawfull[s], (i >> 1) & 1, abort))) break;
+            __syncwarp();
+            const uint8_t* raw = sraw + s * M::kRaw;
+            const int have = bars->have[s], left = now.s.len - kt * kTok;
+            const bool edge = left < kTok || have != (1 << kGroups) - 1;
+            bool odd = false;
+            int ke = 0, ve = 0;
+#pragma unroll 1
+            for (int what = 0; what < 2; ++what) {                        // keys, then values
+                ke = ve;
+                ve = scales_exponent<HD>(raw + (what ? kv_vs_offset(HD) : kv_ks_offset(HD)), lane, edge, left, have, odd);
+            }
+            Info& info = bars->info[i & 3];
+            if (odd)                                                      // which tokens: columns lane, 32 + lane
+                for (int half = 0; half < 2; ++half) {
+                    const int n = 32 * half + lane, grp = n >> 4, pp = (n >> 2) & 3, t = n & 3;
+                    bool strange = false;
+                    for (int c = 0; c < kNb; ++c)
+                        strange |= (*reinterpret_cast<const uint16_t*>(raw + grp * kChunk + kv_vs_offset(HD) + 2 * ((4 * t + pp) * kNb + c)) & 0x7c00) == 0x7c00;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, strange);
+                    if (lane == 0) info.bad[half] = mask;
+                }
+            if (lane == 0) {
+                info.kexp = ke;
+                info.vexp = ve;
+                info.have = have;
+                info.odd = odd;
+                mbar_arrive(&bars->expfull[s]);
+            }
+        }
+        }
     }
 
     // ---------------- teardown
@@ -642,18 +863,10 @@ cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         configured = true;
     }
-    const long long rows = static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kRows - 1) / kRows), a.kv_heads, a.seqs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<T, HD, PARTS, CAP>, a);
+    const Parts parts = parts_at(a.workspace, kBlocks, kRows, HD);
+    const cudaError_t e = launch_dependent(attn_tiles_kernel<T, HD, PARTS, CAP>, dim3(kBlocks), kThreads, smem, s, a, parts);
+    if (e != cudaSuccess) return e;
+    return launch_join<T, HD, kRows, 1>(a, parts, kBlocks, s);
 }
 
 template <typename T>
@@ -663,6 +876,8 @@ cudaError_t tiles_type(const AttnArgs& a, int head_dim, cudaStream_t s) {
 }
 
 }  // namespace
+
+size_t attn_tiles_workspace_bytes(int head_dim) { return parts_bytes(kBlocks, kRows, head_dim); }
 
 cudaError_t launch_attn_tiles(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
     if (type == GQ_F32) return tiles_type<float>(a, head_dim, s);
