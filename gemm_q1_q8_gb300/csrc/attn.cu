@@ -29,7 +29,11 @@ namespace gq {
 GQ_ERROR_ACCESSOR(attn)
 namespace {
 
-constexpr int kManyRows = 256;                    // rows a kv head from which attn_tiles.cu takes the call
+// Rows a kv head (max_q tokens times its query heads) from which attn_tiles.cu takes the call.  32 query and 8 kv heads of 128, 8 sequences of
+// 8192 tokens, this kernel against that one: f32 64 rows 221 / 125 us, 256 rows 826 / 235; bf16 64 rows 115 / 84, 128 rows 204 / 92, 16 rows
+// 47 / 79.  16 bits: from one full 128-row tile, since max_q only bounds the rows (8 ragged trees of 27 to 99 rows: 44 / 52 us).  f32: from
+// two tiles only, because up to there a weight below 2^-36 of the largest still counts here.
+constexpr int many_rows(int type) { return type == GQ_F32 ? 256 : 128; }
 constexpr int kBlocks = 152;                       // one thread block an SM
 
 constexpr float kLift = 108.f;                     // f32 weights carry 2^108: times a scale below 2^16 and 2^kSlack they stay in f32's range
@@ -822,14 +826,14 @@ size_t rows_type_bytes(long long rows) {
 
 size_t attn_workspace_bytes(int, int max_q, int q_heads, int kv_heads, int head_dim, int type) {
     const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-    if (head_dim <= 128 && rows >= kManyRows) return attn_tiles_workspace_bytes(head_dim);
+    if (head_dim <= 128 && rows >= many_rows(type)) return attn_tiles_workspace_bytes(head_dim);
     if (type == GQ_F32)
         return head_dim == 64 ? rows_type_bytes<float, 64>(rows) : head_dim == 128 ? rows_type_bytes<float, 128>(rows) : rows_type_bytes<float, 256>(rows);
     return head_dim == 64 ? rows_type_bytes<__half, 64>(rows) : head_dim == 128 ? rows_type_bytes<__half, 128>(rows) : rows_type_bytes<__half, 256>(rows);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
-    if (head_dim <= 128 && static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads) >= kManyRows) return launch_attn_tiles(a, type, head_dim, s);
+    if (head_dim <= 128 && static_cast<long long>(a.max_q) * (a.q_heads / a.kv_heads) >= many_rows(type)) return launch_attn_tiles(a, type, head_dim, s);
     if (type == GQ_F32)
         return head_dim == 64 ? rows_type<float, 64>(a, s) : head_dim == 128 ? rows_type<float, 128>(a, s) : rows_type<float, 256>(a, s);
     if (type == GQ_F16)

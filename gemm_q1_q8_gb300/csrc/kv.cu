@@ -40,23 +40,24 @@ __global__ void rope_table_kernel(float2* __restrict__ table, int positions, int
 // A token's angles for this thread's four dims: (cos, sin) of each of its pairs (half), or of its two (interleaved)
 struct Turn {
     float4 z0, z1;
-    int other;             // half: distance to the pairs' other dims; 0: not turned
+    int other;             // half: distance to the pairs' other dims (0: these dims are not turned)
     float sign;
+    bool on;
 };
-template <typename T>
-__device__ __forceinline__ float4 turned(const Turn& t, bool interleaved, float4 v, const T* p) {
-    if (t.other == 0) return v;
-    if (interleaved)
+// MODE 1: half, o the pairs' other dims; 2: interleaved
+template <int MODE>
+__device__ __forceinline__ float4 turned(const Turn& t, float4 v, float4 o) {
+    if (MODE == 2)
         return make_float4(v.x * t.z0.x - v.y * t.z0.y, v.y * t.z0.x + v.x * t.z0.y, v.z * t.z0.z - v.w * t.z0.w, v.w * t.z0.z + v.z * t.z0.w);
     // first half: a cos - b sin; second: b cos + a sin, the sign in front of an exact product
-    const float4 o = load4(p + t.other);
     return make_float4(v.x * t.z0.x + t.sign * (o.x * t.z0.y), v.y * t.z0.z + t.sign * (o.y * t.z0.w), v.z * t.z1.x + t.sign * (o.z * t.z1.y),
                        v.w * t.z1.z + t.sign * (o.w * t.z1.w));
 }
 
 // The rows of a token are its q heads, k heads, v heads.  A warp takes rows part * per .. of one token (HD = 64: two at a time), so that
 // a token's position, slot and angles are looked up once for all of them.
-template <typename T, int HD>
+// Every load of a step is issued before any branch on what its rows are (8192 tokens of 32 + 2 x 8 heads with them in branches: 110 us, without 97).
+template <typename T, int HD, int MODE>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int parts, int per) {
     constexpr int kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kAt = 32 / kLanes, kU = 4 / kRuns;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -69,8 +70,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     long long slot = a.slots[n];
     Turn turn[kRuns];
 #pragma unroll
-    for (int c = 0; c < kRuns; ++c) turn[c].other = 0;
-    if (a.rot) {
+    for (int c = 0; c < kRuns; ++c) {
+        turn[c].other = 0;
+        turn[c].on = false;
+    }
+    if (MODE) {
         const int pos = a.positions[n];
         if (pos < 0 || pos >= a.rope_rows) {
             if (l == 0) report_error(kErrIndex);
@@ -81,8 +85,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
         for (int c = 0; c < kRuns; ++c) {
             const int d = c * 128 + 4 * l, half = a.rot / 2;
             if (d >= a.rot) continue;
-            if (a.interleaved) {
-                turn[c].other = 1;
+            turn[c].on = true;
+            if (MODE == 2) {
                 turn[c].z0 = *reinterpret_cast<const float4*>(cs + d / 2);
             } else {
                 const float2* at = cs + (d < half ? d : d - half);
@@ -103,21 +107,28 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     uint8_t* chunk0 = a.cache + (page * a.kv_heads * groups + group) * kv_chunk_bytes(HD);
 
     for (int r0 = from; r0 < to; r0 += kAt * kU) {
-        float4 v[kU][kRuns];
+        float4 v[kU][kRuns], o[kU][kRuns];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int r = r0 + u * kAt + half_warp;
-            if (r >= to) continue;
-            const T* p = r < a.q_heads              ? static_cast<const T*>(a.q) + n * a.q_stride + r * HD
-                         : r < a.q_heads + a.kv_heads ? static_cast<const T*>(a.k) + n * a.k_stride + (r - a.q_heads) * HD
-                                                      : static_cast<const T*>(a.v) + n * a.v_stride + (r - a.q_heads - a.kv_heads) * HD;
+            const int r = min(r0 + u * kAt + half_warp, to - 1);          // past the end: the last row again, which nothing is done with
+            const bool is_q = r < a.q_heads, is_k = r < a.q_heads + a.kv_heads;
+            const T* p = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) + n * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) +
+                         (r - (is_q ? 0 : is_k ? a.q_heads : a.q_heads + a.kv_heads)) * HD;
 #pragma unroll
             for (int c = 0; c < kRuns; ++c) {
-                const int d = c * 128 + 4 * l;
-                v[u][c] = load4(p + d);
-                if (r < a.q_heads + a.kv_heads) v[u][c] = turned(turn[c], a.interleaved, v[u][c], p + d);
+                v[u][c] = load4(p + c * 128 + 4 * l);
+                if (MODE == 1) o[u][c] = load4(p + c * 128 + 4 * l + turn[c].other);
             }
         }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int c = 0; c < kRuns; ++c)
+                if (MODE) {
+                    const float4 x = turned<MODE>(turn[c], v[u][c], o[u][c]);
+                    const bool on = turn[c].on && r0 + u * kAt + half_warp < a.q_heads + a.kv_heads;
+                    v[u][c] = make_float4(on ? x.x : v[u][c].x, on ? x.y : v[u][c].y, on ? x.z : v[u][c].z, on ? x.w : v[u][c].w);
+                }
         __syncwarp();                                     // q_out may be q: every read of a row is before its writes
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -135,11 +146,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
             for (int c = 0; c < kRuns; ++c) {
                 const int d = c * 128 + 4 * l;
                 const float4 x = v[u][c];
-                float amax = r < to ? fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) : 0.f;
+                float amax = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
                 for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 if (!on) continue;
-                const float dd = q8_0_scale(amax);
+                const float dd = q8_0_scale_fast(amax);
                 int code[4];
                 q8_0_quant4(x, amax, dd, code);
                 *reinterpret_cast<uint32_t*>(chunk + (is_k ? kv_k_word<HD>(tok, d) : kv_v_word<HD>(tok, d))) = cache_word(code);
@@ -230,7 +241,10 @@ cudaError_t launch_dependent(K kernel, long long blocks, int threads, cudaStream
 template <typename T, int HD>
 cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
     const int rows = a.q_heads + 2 * a.kv_heads, per = rows_per_warp(a.tokens, rows, HD == 64 ? 2 : 1), parts = (rows + per - 1) / per;
-    return launch_dependent(kv_append_kernel<T, HD>, (static_cast<long long>(a.tokens) * parts + 7) / 8, 256, s, a, parts, per);
+    const long long blocks = (static_cast<long long>(a.tokens) * parts + 7) / 8;
+    if (a.rot == 0) return launch_dependent(kv_append_kernel<T, HD, 0>, blocks, 256, s, a, parts, per);
+    return a.interleaved ? launch_dependent(kv_append_kernel<T, HD, 2>, blocks, 256, s, a, parts, per)
+                         : launch_dependent(kv_append_kernel<T, HD, 1>, blocks, 256, s, a, parts, per);
 }
 template <typename T, int HD>
 cudaError_t read_go(const uint8_t* cache, int pages, int page_size, int kv_heads, const int64_t* slots, int n, void* k,

@@ -55,11 +55,23 @@ __device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// amax / 127 rounded to nearest, as q8_0_scale has it: the product with the rounded reciprocal, corrected by its exact remainder (division by a
+// divisor known in advance: Brisebarre, Muller and Raina, IEEE Trans. Computers 53, 2004; equal to the division for each of the 2^23
+// mantissas); where a step could leave f32's normal range, the division itself.  It is 3 instructions of every thread: 8192 rows of 4096
+// normed 96 -> 93 us, 8192 tokens appended 97 -> 93 us.
+__device__ __forceinline__ float q8_0_scale_fast(float amax) {
+    if (!(amax >= 0x1p-90f && amax <= 0x1p126f)) return q8_0_scale(amax);
+    const float r = 1.0f / 127.0f, q = __fmul_rn(amax, r);
+    return __fmaf_rn(__fmaf_rn(-127.0f, q, amax), r, q);
+}
 // Four values of a block quantized by the rule of q8_0_quant (round half up of the rounded quotient x / d), without its
-// divisions: x times the reciprocal is within 2^-16 of the quotient, so where it is further than 2^-11 from a tie its nearest integer is the
+// divisions: x times the approximate reciprocal is within 2^-14 of the quotient, so where it is further than 2^-11 from a tie its nearest integer is the
 // code; the few others (and NaN) are divided.  16 instructions instead of some 80.
 __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int (&c)[4]) {
-    const float r = dd >= 0x1p-120f ? __frcp_rn(dd) : 0.0f, magic = 12582912.0f;       // 1.5 * 2^23: the sum's low bits are the integer
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(dd));
+    if (!(dd >= 0x1p-120f)) r = 0.0f;
+    const float magic = 12582912.0f;                                    // 1.5 * 2^23: the sum's low bits are the integer
     const float x[4] = {v.x, v.y, v.z, v.w};
     bool far = dd >= 0x1p-120f || amax == 0.0f;
 #pragma unroll

@@ -110,3 +110,14 @@ def test_binding_refuses_host_tensors():
         gq.KVCacheQ8_0(1, 17, 1, 64)
     with pytest.raises(gq.GQError):
         gq.rope_table(4, 64, scaling="other", device="cpu")
+
+
+def test_scale_by_product_is_the_division():
+    """A block's scale is amax / 127 rounded: the kernels' product, corrected by its exact remainder, for every mantissa."""
+    import numpy as np
+    a = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(127 << 23)).view(np.float32)
+    r = np.float32(1) / np.float32(127)
+    q = a * r
+    rem = (a.astype(np.float64) - 127.0 * q.astype(np.float64)).astype(np.float32)          # exact
+    fixed = (rem.astype(np.longdouble) * np.longdouble(r) + q.astype(np.longdouble)).astype(np.float32)
+    assert np.array_equal(fixed, a / np.float32(127))
