@@ -66,19 +66,26 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStr
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// A block looks at one run, a warp at rows of its head, a lane at four columns (256: two times four).  GROUP neighbouring runs (the warps of a
-// block) have joined their tails already: the first of them holds the sum.  Sixteen parts are requested at once, before their weights are known.
-// Rows of sequences without keys are written here too.
+// A block looks at GROUP neighbouring runs (the warps of a block of the first kernel) with the blocks of its column, a warp takes rows of their
+// heads, a lane four columns (256: two times four).  The group has joined its tails already: the first of a tile's holds the sum.  Sixteen
+// (eight) parts are requested at once, before their weights are known.  Rows of sequences without keys are written here too.
+// It is bound by latency, three dependent loads: with a block for each run, most of them without a head, it was its own eleven waves of blocks.
 template <typename T, int HD, int ROWS, int GROUP>
-__global__ void __launch_bounds__((ROWS < 8 ? ROWS : 8) * 32) attn_join_kernel(const AttnArgs a, const Parts parts, int runs) {
-    constexpr int kWarps = ROWS < 8 ? ROWS : 8, kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kBatch = 16 / kRuns;
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const Parts parts, int runs) {
+    constexpr int kWarps = 8, kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kBatch = (ROWS > 8 ? 8 : 16) / kRuns;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.q_heads / a.kv_heads;
-    const int run = blockIdx.x;
-    const Head head = parts.head[run];
-    if (head.first >= 0)
-        for (int r = warp + kWarps * blockIdx.y; r < head.rows; r += kWarps * gridDim.y) {
+    const int run0 = blockIdx.x * GROUP;
+    unsigned heads = __ballot_sync(0xffffffffu, lane < GROUP && run0 + lane < runs && parts.head[min(run0 + lane, runs - 1)].first >= 0);
+    // the rows of the heads one after another: this warp's are warp + kWarps * blockIdx.y and every kWarps * gridDim.y further
+    for (int at = warp + kWarps * blockIdx.y; heads; at -= ROWS, heads &= heads - 1) {
+        const int run = run0 + __ffs(heads) - 1;
+        if (at >= ROWS) continue;
+        const Head head = parts.head[run];
+        for (; at < ROWS; at += kWarps * gridDim.y) {
+            const int r = at;
+            if (r >= head.rows) continue;
             // parts: the tail of the run that began the tile, those of the groups between, the head
             const int group0 = head.first / GROUP, n = (run + GROUP - 1) / GROUP - group0 + 1;
             float top = kNone, l = 0.f;
@@ -124,6 +131,7 @@ __global__ void __launch_bounds__((ROWS < 8 ? ROWS : 8) * 32) attn_join_kernel(c
             for (int c = 0; c < kRuns; ++c)
                 if (lane < kLanes) store4(out + 128 * c + 4 * lane, make_float4(v[c].x * inv, v[c].y * inv, v[c].z * inv, v[c].w * inv));
         }
+    }
     if (blockIdx.y == 0)
         for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
             if (a.kv_len[b] > 0) continue;
@@ -136,8 +144,8 @@ __global__ void __launch_bounds__((ROWS < 8 ? ROWS : 8) * 32) attn_join_kernel(c
 
 template <typename T, int HD, int ROWS, int GROUP>
 cudaError_t launch_join(const AttnArgs& a, const Parts& parts, int runs, cudaStream_t s) {
-    constexpr int kWarps = ROWS < 8 ? ROWS : 8;
-    return launch_dependent(attn_join_kernel<T, HD, ROWS, GROUP>, dim3(runs, ROWS / kWarps > 4 ? 4 : 1), kWarps * 32, 0, s, a, parts, runs);
+    constexpr int kBlocksUp = ROWS > 16 ? 8 : 4;
+    return launch_dependent(attn_join_kernel<T, HD, ROWS, GROUP>, dim3((runs + GROUP - 1) / GROUP, kBlocksUp), 256, 0, s, a, parts, runs);
 }
 
 }  // namespace
