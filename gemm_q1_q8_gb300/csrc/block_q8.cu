@@ -211,7 +211,7 @@ __host__ __device__ constexpr int rw_rows() { return MT == 1 ? 7 : 4; }
 
 template <int MT>
 __global__ void __launch_bounds__(kRwWarps * 32)
-block_q8_rowwarp_kernel(const float* __restrict__ x, const uint32_t* __restrict__ quants,
+block_q8_rowwarp_kernel(const float* x, const uint32_t* __restrict__ quants,
                         const float* __restrict__ scales, float* __restrict__ y, int m, int k, int n) {
     constexpr int R = rw_rows<MT>();
     __shared__ float ps[kRwWarps][R][33];           // a warp's rounded block products, odd stride
@@ -248,7 +248,7 @@ block_q8_rowwarp_kernel(const float* __restrict__ x, const uint32_t* __restrict_
                                                                static_cast<size_t>(live ? b : 0) * 32);
 #pragma unroll
             for (int q4 = 0; q4 < 8; ++q4) {
-                const float4 a = __ldg(xp + q4);
+                const float4 a = xp[q4];           // a plain load: a read-only one may be moved above the wait
                 xv[u][4 * q4] = a.x; xv[u][4 * q4 + 1] = a.y; xv[u][4 * q4 + 2] = a.z; xv[u][4 * q4 + 3] = a.w;
             }
         }
@@ -385,9 +385,10 @@ block_q8_pair_kernel(const float* __restrict__ x, const uint32_t* __restrict__ q
 
 // Stages the tile's activations x[m0 .. m0 + MT)[0 .. k) into xs as [k][MT] (x[m0 + r][kk] at
 // kk*MT + r; rows past m as zeros): sixteen independent 16-byte loads per thread in flight when x
-// is 16-byte aligned (item i = 4 consecutive k of row i % MT), else single floats.
+// is 16-byte aligned (item i = 4 consecutive k of row i % MT), else single floats.  Plain loads of a
+// pointer that is not __restrict__: read-only loads may be moved above a wait for the preceding grids.
 template <int MT, int THREADS>
-__device__ __forceinline__ void stage_x(float* xs, const float* __restrict__ x, int m, int m0, int k) {
+__device__ __forceinline__ void stage_x(float* xs, const float* x, int m, int m0, int k) {
     if ((reinterpret_cast<uintptr_t>(x) & 15) == 0) {
         const int items = MT * k / 4;
         for (int i0 = threadIdx.x; i0 < items; i0 += 16 * THREADS) {
@@ -397,7 +398,7 @@ __device__ __forceinline__ void stage_x(float* xs, const float* __restrict__ x, 
                 const int i = i0 + u * THREADS;
                 const int r = i % MT, k4 = i / MT;
                 v[u] = (i < items && m0 + r < m)
-                           ? __ldg(reinterpret_cast<const float4*>(x + static_cast<size_t>(m0 + r) * k) + k4)
+                           ? reinterpret_cast<const float4*>(x + static_cast<size_t>(m0 + r) * k)[k4]
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
@@ -421,7 +422,7 @@ __device__ __forceinline__ void stage_x(float* xs, const float* __restrict__ x, 
             for (int u = 0; u < 8; ++u) {
                 const int e = e0 + u * THREADS;
                 const int kk = e / MT, r = e % MT;
-                v[u] = (e < total && m0 + r < m) ? __ldg(x + static_cast<size_t>(m0 + r) * k + kk) : 0.0f;
+                v[u] = (e < total && m0 + r < m) ? x[static_cast<size_t>(m0 + r) * k + kk] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -447,7 +448,7 @@ constexpr size_t kStSmemMax = 200 * 1024;
 
 template <int MT, int W = kStWarps, int D = kStDepth>
 __global__ void __launch_bounds__(W * 32)
-block_q8_strip_kernel(const float* __restrict__ x, const uint32_t* __restrict__ quants,
+block_q8_strip_kernel(const float* x, const uint32_t* __restrict__ quants,
                       const float* __restrict__ scales, float* __restrict__ y, int m, int k, int n) {
     extern __shared__ __align__(16) float smem_f[];          // [k][MT]: x[m0 + r][kk] at kk*MT + r
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -551,7 +552,7 @@ __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_
 
 template <int MT, int S, int W = kTmWarps>
 __global__ void __launch_bounds__(W * 32)
-block_q8_tma_kernel(const __grid_constant__ CUtensorMap tm, const float* __restrict__ x,
+block_q8_tma_kernel(const __grid_constant__ CUtensorMap tm, const float* x,
                     const float* __restrict__ scales, float* __restrict__ y, int m, int k, int n) {
     static_assert(S % 2 == 0, "blocks are summed in pairs");
     extern __shared__ __align__(16) uint8_t smem_raw[];

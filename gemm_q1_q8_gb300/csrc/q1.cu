@@ -60,6 +60,7 @@ __global__ void q1_pack_kernel(const uint8_t* __restrict__ raw, int rows, int nb
 // at once, loads its first weights (which no preceding launch of this library writes) and only
 // then waits for the preceding grids before it reads the activation or writes y.  In a stream of
 // GEMVs (a decode step) the next matrix's weights are in flight while the current one finishes.
+// `act` is not __restrict__: as read-only data its loads may be moved above the wait.
 // --------------------------------------------------------------------------------------------
 constexpr int kSmallWarps = 16;
 constexpr int kSmallPass = 2 * kSmallWarps;   // blocks per pass through shared memory
@@ -68,7 +69,7 @@ constexpr int kSmallPass = 2 * kSmallWarps;   // blocks per pass through shared 
 // registers so that two thread blocks share an SM; 4 for longer rows)
 template <int ACT, int J>   // ACT: GQ_ACT_Q8_0 or GQ_ACT_F32
 __global__ void __launch_bounds__(kSmallWarps * 32)
-q1_gemv_small_kernel(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ act, float* __restrict__ y,
+q1_gemv_small_kernel(const uint8_t* __restrict__ packed, const uint8_t* act, float* __restrict__ y,
                      int rows, int nb) {
     __shared__ __align__(16) float4 s_ab[kSmallPass][2][32];            // ab of (block, row): two float4
     __shared__ float s_d0[kSmallPass][32];

@@ -30,7 +30,7 @@ constexpr int kTabStride = 17;
 constexpr int kRowPad = kRawHalves + 2;         // 37 words per staged row: the rows' reads hit distinct banks
 
 __global__ void __launch_bounds__(kRawStep * 32)
-q1_gemv_raw_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ act, float* __restrict__ y,
+q1_gemv_raw_kernel(const uint16_t* __restrict__ w, const uint16_t* act, float* __restrict__ y,
                    int rows, int nb) {
     __shared__ __align__(4) uint16_t s_w[kRawRows][kRowPad];
     __shared__ float s_tab[kRawStep][32 * kTabStride];
@@ -70,7 +70,7 @@ q1_gemv_raw_kernel(const uint16_t* __restrict__ w, const uint16_t* __restrict__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     load_w(0);                                                      // weights: before the wait
     asm volatile("griddepcontrol.wait;" ::: "memory");              // the activations are ready
-    load_a(0);
+    load_a(0);                                                      // act is not __restrict__: read-only loads may pass the wait
 
     for (int b0 = 0; b0 < nb; b0 += kRawStep) {
         const int nbs = min(kRawStep, nb - b0);

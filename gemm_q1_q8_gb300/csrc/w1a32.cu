@@ -150,7 +150,8 @@ __device__ __forceinline__ void sts_vec(FVec<T>* p, const float (&v)[T]) {
 
 // The four activations x[32 b + 4 g .. + 3] of one token.
 __device__ __forceinline__ float4 ldg_x4(const float* x, size_t m, int K, int b, int g) {
-    return __ldg(reinterpret_cast<const float4*>(x + m * static_cast<size_t>(K) + static_cast<size_t>(b) * 32 + 4 * g));
+    // a plain load: a read-only one may be moved above a kernel's wait for the preceding grids
+    return *reinterpret_cast<const float4*>(x + m * static_cast<size_t>(K) + static_cast<size_t>(b) * 32 + 4 * g);
 }
 
 // A group's table is padded by one entry, so the builders' stores (one table per lane) hit
@@ -387,7 +388,7 @@ __device__ __forceinline__ void pd_reduce_store(const float* part, int t, int la
 
 __global__ void __launch_bounds__(kPdWarps * 32, 1)
 lut4_decode_persistent_kernel(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmW,
-                              const float* __restrict__ x, float* __restrict__ y, int N, int K) {
+                              const float* x, float* __restrict__ y, int N, int K) {
     extern __shared__ __align__(1024) uint8_t psm1[];
     uint8_t* base = smem_align1024(psm1);
     const int nbk = K / 32;

@@ -99,7 +99,7 @@ __device__ __forceinline__ void decode16x2(const uint32_t (&wd)[BITS == 8 ? 4 : 
 // then reduced by halving exchanges (lane l ends with value (l >> (5 - log2 V)) of the V = 8T).
 template <int BITS, int T>
 __global__ void __launch_bounds__(kGvWarps * 32, T == 1 ? 3 : 1)   // one token: 3 blocks per SM, one wave
-wq_gemv_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, const float* __restrict__ x,
+wq_gemv_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, const float* x,
                float* __restrict__ y, int N, int K, int Tn) {
     constexpr int R = 32 / T;                     // rows per thread block
     constexpr int V = 8 * T;                      // values per lane per row batch
@@ -149,7 +149,7 @@ wq_gemv_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, 
                     const float4* xp = reinterpret_cast<const float4*>(x + static_cast<size_t>(min(u, Tn - 1)) * K + k0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float4 a = __ldg(xp + q);
+                        const float4 a = xp[q];           // a plain load: a read-only one may be moved above the wait
                         xv[u][2 * q] = make_float2(a.x, a.y);
                         xv[u][2 * q + 1] = make_float2(a.z, a.w);
                     }
@@ -217,7 +217,7 @@ wq_gemv_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, 
 constexpr int kG4Chunk = 1024;
 constexpr int kG4Rows = 48;                        // rows per thread block, three batches of 16
 __global__ void __launch_bounds__(kGvWarps * 32, 2)   // two blocks per SM: 14,336 rows in one wave
-wq4_gemv1_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, const float* __restrict__ x,
+wq4_gemv1_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale, const float* x,
                  float* __restrict__ y, int N, int K) {
     constexpr int R = kG4Rows;
     __shared__ float part[4][R];
@@ -257,7 +257,7 @@ wq4_gemv1_kernel(const uint32_t* __restrict__ w, const float* __restrict__ scale
                     float2 xv[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float4 a = __ldg(xp + 4 * hh + q);
+                        const float4 a = xp[4 * hh + q];  // a plain load, see wq_gemv_kernel
                         xv[2 * q] = make_float2(a.x, a.y);
                         xv[2 * q + 1] = make_float2(a.z, a.w);
                     }
