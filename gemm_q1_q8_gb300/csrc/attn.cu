@@ -210,7 +210,7 @@ struct Queries {
                 const int tok = in ? r / group : 0;
                 RowInfo ri;
                 // 2^24 for the codes, 2^-up for the query
-                ri.rs = (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) * 16777216.f * pow2i(-up);
+                ri.rs = (a.softcap <= 0.f ? a.scale * kLog2e : a.scale / a.softcap * (PARTS > 1 ? 1.f : 2.f * kLog2e)) * 16777216.f * pow2i(-up);
                 ri.last = in ? s.L - s.T + tok : -1;
                 const unsigned long long bits = a.tree && in ? a.tree[s.q0 + tok] : 0ull;
                 ri.bits0 = static_cast<uint32_t>(bits);
@@ -371,13 +371,14 @@ struct Tile {
                     P[mt][set][p] = x * row[mt][set].rs;
                 }
             if (a.softcap > 0.f) {
-                // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones
+                // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
+                const float cap = a.softcap * kLog2e;
 #pragma unroll
                 for (int set = 0; set < kSets; ++set)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const float x = P[mt][set][p];
-                        P[mt][set][p] = a.softcap * kLog2e * (PARTS > 1 ? tanhf(x) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * x) + 1.f));
+                        P[mt][set][p] = PARTS > 1 ? cap * tanhf(x) : fmaf(-2.f * cap, rcp(ex2(x) + 1.f), cap);
                     }
             }
             if (MASKED) {

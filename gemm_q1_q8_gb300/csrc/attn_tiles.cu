@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
             // the scale's sign goes into the queries, and a scale of 0 (equal weights) too: the scores' factor stays positive
             const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
-            rs = (CAP ? size / a.softcap : size * kLog2e) * pow2i(-up);
+            rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * pow2i(-up);
 #pragma unroll
             for (int part = 0; part < kQ / 8; ++part) {
                 uint32_t hi[16], lo[16];
@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (CAP) {
 #pragma unroll
                 for (int n = 0; n < kTok; ++n) {
-                    // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones
+                    // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
                     const float y = x[n] * x_of;
-                    x[n] = a.softcap * kLog2e * (PARTS == 2 ? tanhf(y) : 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f));
+                    x[n] = PARTS == 2 ? a.softcap * kLog2e * tanhf(y) : fmaf(-2.f * kLog2e * a.softcap, rcp(ex2(y) + 1.f), a.softcap * kLog2e);
                 }
                 x_of = 1.f;
             }

@@ -54,9 +54,23 @@ __device__ __forceinline__ float4 turned(const Turn& t, float4 v, float4 o) {
                        v.w * t.z1.z + t.sign * (o.w * t.z1.w));
 }
 
+// A slot's page and its 16-token group there, in 32 bits where they allow
+__device__ __forceinline__ void page_group(long long slot, int groups, long long& page, int& group) {
+    const long long g = slot / kvGroup;
+    if (g < 0x7fffffffll) {
+        page = static_cast<int>(g) / groups;
+        group = static_cast<int>(g) - static_cast<int>(page) * groups;
+    } else {
+        page = g / groups;
+        group = static_cast<int>(g - page * groups);
+    }
+}
+
 // The rows of a token are its q heads, k heads, v heads.  A warp takes rows part * per .. of one token (HD = 64: two at a time), so that
 // a token's position, slot and angles are looked up once for all of them.
-// Every load of a step is issued before any branch on what its rows are (8192 tokens of 32 + 2 x 8 heads with them in branches: 110 us, without 97).
+// Every load of a step is issued before any branch on what its rows are, the first step's before the token's position and slot are known.
+// Bound by HBM for many tokens (8192 of 32 + 2 x 8 heads of 128 in f32, with the read of what was written: 84 us, 72% of the measured rate; with the
+// loads in branches 110 us, behind the look-ups 93 us), by the chain of loads for few.
 template <typename T, int HD, int MODE>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int parts, int per) {
     constexpr int kLanes = HD == 64 ? 16 : 32, kRuns = HD == 256 ? 2 : 1, kAt = 32 / kLanes, kU = 4 / kRuns;
@@ -68,46 +82,17 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
     if (n >= a.tokens) return;
     const int l = threadIdx.x % kLanes, half_warp = (threadIdx.x & 31) / kLanes;
     long long slot = a.slots[n];
+    const int pos = MODE ? a.positions[n] : 0;
     Turn turn[kRuns];
 #pragma unroll
     for (int c = 0; c < kRuns; ++c) {
-        turn[c].other = 0;
-        turn[c].on = false;
+        const int d = c * 128 + 4 * l, half = a.rot / 2;
+        turn[c].on = MODE && d < a.rot;
+        turn[c].other = MODE == 1 && turn[c].on ? (d < half ? half : -half) : 0;
+        turn[c].sign = d < half ? -1.0f : 1.0f;
     }
-    if (MODE) {
-        const int pos = a.positions[n];
-        if (pos < 0 || pos >= a.rope_rows) {
-            if (l == 0) report_error(kErrIndex);
-            return;                                       // the token is left out
-        }
-        const float2* cs = reinterpret_cast<const float2*>(a.rope) + static_cast<size_t>(pos) * (a.rot / 2);
-#pragma unroll
-        for (int c = 0; c < kRuns; ++c) {
-            const int d = c * 128 + 4 * l, half = a.rot / 2;
-            if (d >= a.rot) continue;
-            turn[c].on = true;
-            if (MODE == 2) {
-                turn[c].z0 = *reinterpret_cast<const float4*>(cs + d / 2);
-            } else {
-                const float2* at = cs + (d < half ? d : d - half);
-                turn[c].z0 = *reinterpret_cast<const float4*>(at);
-                turn[c].z1 = *reinterpret_cast<const float4*>(at + 2);
-                turn[c].other = d < half ? half : -half;
-                turn[c].sign = d < half ? -1.0f : 1.0f;
-            }
-        }
-    }
-    if (slot >= static_cast<long long>(a.pages) * a.page_size) {
-        if (l == 0) report_error(kErrIndex);
-        slot = -1;
-    }
-    const int tok = static_cast<int>(slot & (kvGroup - 1));
-    const long long page = slot < 0 ? 0 : slot / a.page_size;
-    const int group = static_cast<int>(slot - page * a.page_size) / kvGroup, groups = a.page_size / kvGroup;
-    uint8_t* chunk0 = a.cache + (page * a.kv_heads * groups + group) * kv_chunk_bytes(HD);
-
-    for (int r0 = from; r0 < to; r0 += kAt * kU) {
-        float4 v[kU][kRuns], o[kU][kRuns];
+    float4 v[kU][kRuns], o[kU][kRuns];
+    auto load = [&](int r0) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int r = min(r0 + u * kAt + half_warp, to - 1);          // past the end: the last row again, which nothing is done with
@@ -120,6 +105,39 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
                 if (MODE == 1) o[u][c] = load4(p + c * 128 + 4 * l + turn[c].other);
             }
         }
+    };
+    load(from);                                           // before what the token's position and slot lead to
+    if (MODE) {
+        if (pos < 0 || pos >= a.rope_rows) {
+            if (l == 0) report_error(kErrIndex);
+            return;                                       // the token is left out
+        }
+        const float2* cs = reinterpret_cast<const float2*>(a.rope) + static_cast<size_t>(pos) * (a.rot / 2);
+#pragma unroll
+        for (int c = 0; c < kRuns; ++c) {
+            const int d = c * 128 + 4 * l, half = a.rot / 2;
+            if (!turn[c].on) continue;
+            if (MODE == 2) {
+                turn[c].z0 = *reinterpret_cast<const float4*>(cs + d / 2);
+            } else {
+                const float2* at = cs + (d < half ? d : d - half);
+                turn[c].z0 = *reinterpret_cast<const float4*>(at);
+                turn[c].z1 = *reinterpret_cast<const float4*>(at + 2);
+            }
+        }
+    }
+    if (slot >= static_cast<long long>(a.pages) * a.page_size) {
+        if (l == 0) report_error(kErrIndex);
+        slot = -1;
+    }
+    const int tok = static_cast<int>(slot & (kvGroup - 1)), groups = a.page_size / kvGroup;
+    long long page;
+    int group;
+    page_group(slot < 0 ? 0 : slot, groups, page, group);
+    uint8_t* chunk0 = a.cache + (page * a.kv_heads * groups + group) * kv_chunk_bytes(HD);
+
+    for (int r0 = from; r0 < to; r0 += kAt * kU) {
+        if (r0 > from) load(r0);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -179,9 +197,10 @@ kv_read_kernel(const uint8_t* cache, long long slots_all, int page_size, int kv_
         if (l == 0) report_error(kErrIndex);
         slot = -1;
     }
-    const int tok = static_cast<int>(slot & (kvGroup - 1));
-    const long long page = slot < 0 ? 0 : slot / page_size;
-    const int group = static_cast<int>(slot - page * page_size) / kvGroup, groups = page_size / kvGroup;
+    const int tok = static_cast<int>(slot & (kvGroup - 1)), groups = page_size / kvGroup;
+    long long page;
+    int group;
+    page_group(slot < 0 ? 0 : slot, groups, page, group);
     const uint8_t* chunk0 = cache + (page * kv_heads * groups + group) * kv_chunk_bytes(HD);
     const size_t out0 = static_cast<size_t>(i) * kv_heads * HD;
     for (int h0 = from; h0 < to; h0 += kAt * kU) {
@@ -216,10 +235,11 @@ kv_read_kernel(const uint8_t* cache, long long slots_all, int page_size, int kv_
     }
 }
 
-// Rows of a token that a warp takes: all of them where the tokens fill the GPU (152 SMs, some 64 warps each), fewer for few tokens
-int rows_per_warp(long long tokens, int rows, int step) {
+// Rows of a token that a warp takes: all of them where the tokens fill the GPU (152 SMs, some 64 warps each), fewer for few tokens.  Below the
+// `full` rows that it requests at once only while half as many warps are missing (2219 tokens of 25 heads of 64: 11.5 -> 10.6 us with the read)
+int rows_per_warp(long long tokens, int rows, int step, int full) {
     int per = (rows + step - 1) / step * step;
-    while (per > step && tokens * ((rows + per - 1) / per) < 152 * 64) per = (per / 2 + step - 1) / step * step;
+    while (per > step && tokens * ((rows + per - 1) / per) < 152 * (per > full ? 64 : 32)) per = (per / 2 + step - 1) / step * step;
     return per;
 }
 
@@ -240,7 +260,7 @@ cudaError_t launch_dependent(K kernel, long long blocks, int threads, cudaStream
 
 template <typename T, int HD>
 cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
-    const int rows = a.q_heads + 2 * a.kv_heads, per = rows_per_warp(a.tokens, rows, HD == 64 ? 2 : 1), parts = (rows + per - 1) / per;
+    const int rows = a.q_heads + 2 * a.kv_heads, per = rows_per_warp(a.tokens, rows, HD == 64 ? 2 : 1, HD == 64 ? 8 : HD == 128 ? 4 : 2), parts = (rows + per - 1) / per;
     const long long blocks = (static_cast<long long>(a.tokens) * parts + 7) / 8;
     if (a.rot == 0) return launch_dependent(kv_append_kernel<T, HD, 0>, blocks, 256, s, a, parts, per);
     return a.interleaved ? launch_dependent(kv_append_kernel<T, HD, 2>, blocks, 256, s, a, parts, per)
@@ -249,7 +269,7 @@ cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
 template <typename T, int HD>
 cudaError_t read_go(const uint8_t* cache, int pages, int page_size, int kv_heads, const int64_t* slots, int n, void* k,
                     void* v, cudaStream_t s) {
-    const int per = rows_per_warp(n, kv_heads, HD == 64 ? 2 : 1), parts = (kv_heads + per - 1) / per;
+    const int per = rows_per_warp(n, kv_heads, HD == 64 ? 2 : 1, HD == 64 ? 8 : HD == 128 ? 4 : 2), parts = (kv_heads + per - 1) / per;
     return launch_dependent(kv_read_kernel<T, HD>, (static_cast<long long>(n) * parts + 7) / 8, 256, s, cache,
                             static_cast<long long>(pages) * page_size, page_size, kv_heads, slots, n, parts, per, static_cast<T*>(k),
                             static_cast<T*>(v));
