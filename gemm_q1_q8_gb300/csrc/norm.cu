@@ -2,8 +2,9 @@
 //
 // h = x + r; y = h * rstd * w, rstd = 1 / sqrt(sum h^2 / k + eps); y quantized per 32 values as the library's
 // quantizer does.  One pass over x and r: a thread block per row keeps h in registers between the sum and
-// the outputs, so a value is read once and written once (5 to 13 bytes moved a value, 7 flops and one
-// division: bound by HBM for many rows, by one load round trip and one barrier for one).
+// the outputs, so a value is read once and written once (5 to 13 bytes moved a value, 7 flops and a quantization).  Bound by HBM
+// for many rows (8192 f32 rows of 4096 with residual and sum, and the read back of their blocks: 93 us, 86% of the measured rate), by
+// two dependent round trips and two barriers for one (2560 values, with the read back: 3.2 us).
 #include "layer_ops.cuh"
 
 namespace gq {
@@ -101,8 +102,8 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
 
 // NV: four-value chunks a thread keeps in registers; a longer row's remaining chunks are read again
 // (through L2) for the outputs.  VEC: rows and outputs allow four-value accesses.
-template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+template <typename T, int NV, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) rmsnorm_kernel(const NormArgs a) {
     __shared__ float part[32];
     const int tid = threadIdx.x, nt = blockDim.x;
     const size_t row = blockIdx.x;
@@ -165,8 +166,12 @@ cudaError_t norm_go(const NormArgs& a, int m, int nt, bool vec, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return vec ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<T, NV, true>, a)
-               : cudaLaunchKernelEx(&cfg, rmsnorm_kernel<T, NV, false>, a);
+    // 40 registers let three blocks of 512 threads share an SM (bf16, 8192 rows of 4096: 60.6 -> 54.4 us, 777 of 6912 with the read back
+    // 16.6 -> 15.6); where two a SM hold all rows they only cost loads in flight (300 of 8192: 5.7 -> 7.5), and f32 rows would spill
+    // (8192 of 4096: 93 -> 102)
+    if constexpr (NV == 4 && sizeof(T) == 2)
+        if (vec && nt <= 512 && m > 2 * 152) return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<T, NV, true, 512>, a);
+    return vec ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<T, NV, true, 1024>, a) : cudaLaunchKernelEx(&cfg, rmsnorm_kernel<T, NV, false, 1024>, a);
 }
 
 template <typename T>
