@@ -827,7 +827,7 @@ size_t rows_type_bytes(long long rows) {
 
 size_t attn_workspace_bytes(int, int max_q, int q_heads, int kv_heads, int head_dim, int type) {
     const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-    if (head_dim <= 128 && rows >= many_rows(type)) return attn_tiles_workspace_bytes(head_dim);
+    if (head_dim <= 128 && rows >= many_rows(type)) return attn_tiles_workspace_bytes(head_dim, type);
     if (type == GQ_F32)
         return head_dim == 64 ? rows_type_bytes<float, 64>(rows) : head_dim == 128 ? rows_type_bytes<float, 128>(rows) : rows_type_bytes<float, 256>(rows);
     return head_dim == 64 ? rows_type_bytes<__half, 64>(rows) : head_dim == 128 ? rows_type_bytes<__half, 128>(rows) : rows_type_bytes<__half, 256>(rows);

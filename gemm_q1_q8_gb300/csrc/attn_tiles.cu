@@ -2,6 +2,9 @@
 //
 // Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
 // keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
+// Measured (2048 queries of 32 heads of 128 over 8192 tokens, 8 kv heads): f32 581 us (296 TFLOP/s of the formula, 890 of MMAs; 274 us at the
+// measured rate), bf16 335 us.  A 64-token score MMA takes two thirds of a 128-token one's time, so a tile's MMAs take 1920 cycles in f32, the
+// issue slots of the softmax and of the conversions some 2400, and a tile about 3500: what is left between them is waiting in their chain.
 //
 // Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
 // thread; keys and values (B) in shared memory (128-byte swizzle), converted from the cache's codes by eight warps.  With A in tensor
@@ -42,6 +45,11 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsKV + kRegsRest == 5 * 96, "registers")
 constexpr int kBlocks = 152;                               // one thread block an SM
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
+// f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
+// always towards zero, 12 times a tile: over 8192 tokens (64 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
+// 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543.
+// 16 bits (4 MMAs a tile) lose half of f16's last place at 600,000 tokens: not drained (the code alone would cost 4-6%, by its registers).
+constexpr int kDrain = 8;
 
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
@@ -280,6 +288,7 @@ struct Bars {
     Info info[4];
     float amax[2][kRows];                                  // of the groups' halves of the queries
     float m[2][kRows], l[2][kRows];                        // the groups' maxima and sums, at the end
+    float kept[2][kRows];                                  // and the factor of the sums that left tensor memory
     int vref[2][kRows];
     Piece piece[4];                                        // a ring, filled by one warp; k1 = 0 ends it
 };
@@ -292,7 +301,7 @@ template <int HD, int PARTS> struct Smem {
 };
 
 template <typename T, int HD, int PARTS, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a, const Parts parts) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a, const Parts parts, float4* kept) {
     using M = Smem<HD, PARTS>;
     constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -422,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (lane == 0) mbar_arrive(&bars->qfull);
         }
         const int last = in ? p.s.L - p.s.T + tok : -1;
-        float m = kNone, l = 0.f;
-        int vref = -24;
+        float m = kNone, l = 0.f, m_kept = 0.f;                               // (m_kept, v_kept: what the drained sums are relative to)
+        int vref = -24, v_kept = 0;
         const int tiles = p.k1 - p.k0;
         for (int j = (it ^ wg) & 1; ok && j < tiles; j += 2) {                  // tile it + j of all, which is in this group's place
             const int i = it + j;
@@ -435,6 +444,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             __syncwarp();
             tc_fence_after();
+            const bool drain = PARTS == 2 && j >= 2 && (j >> 1) % kDrain == 0;
+            if (drain) {
+                const bool first = j < 4 * kDrain;
+                const float f = ex2(m_kept - m) * pow2i(max(v_kept - vref, -126));
+                float4* at = kept + (blockIdx.x * 2 + wg) * (HD / 4) * kRows + lr;
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                    uint32_t o[16];
+                    float4 before[4];
+                    tc_ld16(co + c, o);
+                    if (!first)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) before[n] = at[(c / 4 + n) * kRows];
+                    tc_wait_ld();
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        float4 v = make_float4(__uint_as_float(o[4 * n]), __uint_as_float(o[4 * n + 1]), __uint_as_float(o[4 * n + 2]), __uint_as_float(o[4 * n + 3]));
+                        if (!first) v = make_float4(fmaf(before[n].x, f, v.x), fmaf(before[n].y, f, v.y), fmaf(before[n].z, f, v.z), fmaf(before[n].w, f, v.w));
+                        at[(c / 4 + n) * kRows] = v;
+                    }
+                }
+                m_kept = m;
+                v_kept = vref;
+            }
             const Info& info = bars->info[i & 3];
             float x_of = rs * pow2i(info.kexp);
             const int vexp = info.vexp, have = info.have;
@@ -485,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 l *= down;
                 m = mn;
                 vref = vn;
-                if (j >= 2) {
+                if (j >= 2 && !drain) {
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 16) {
                         uint32_t o[16];
@@ -541,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         bars->m[wg][lr] = !ok ? __int_as_float(0x7fc00000) : has ? m : kNone;
         bars->l[wg][lr] = has ? l : 0.f;
         bars->vref[wg][lr] = vref;
+        if (PARTS == 2) bars->kept[wg][lr] = ex2(m_kept - m) * pow2i(max(v_kept - vref, -126));
         meet();
         {
             tc_fence_after();
@@ -551,6 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
             const float a0 = f0 * pow2i(bars->vref[0][lr] - 11) * inv, a1 = f1 * pow2i(bars->vref[1][lr] - 11) * inv;
             T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD + wg * (HD / 2);
+            // whether a group's sums have been drained: it had more than kDrain tiles, every other one from its first on
+            const int begin0 = (it - tiles) & 1;
+            const bool kept0 = PARTS == 2 && (tiles - begin0 + 1) / 2 > kDrain, kept1 = PARTS == 2 && (tiles - (begin0 ^ 1) + 1) / 2 > kDrain;
             const size_t slot = (static_cast<size_t>(head ? 0 : kBlocks) + blockIdx.x) * kRows + lr;
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 16) {
@@ -558,6 +595,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 tc_ld16(tl + kColO + wg * (HD / 2) + c, o0);
                 tc_ld16(tl + kColO + HD + wg * (HD / 2) + c, o1);
                 tc_wait_ld();
+                auto add_kept = [&](uint32_t* o, int g) {
+                    const float f = bars->kept[g][lr];
+                    const float4* at = kept + (blockIdx.x * 2 + g) * (HD / 4) * kRows + lr;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float4 k = at[((wg * (HD / 2) + c) / 4 + n) * kRows];
+                        o[4 * n] = __float_as_uint(fmaf(k.x, f, __uint_as_float(o[4 * n])));
+                        o[4 * n + 1] = __float_as_uint(fmaf(k.y, f, __uint_as_float(o[4 * n + 1])));
+                        o[4 * n + 2] = __float_as_uint(fmaf(k.z, f, __uint_as_float(o[4 * n + 2])));
+                        o[4 * n + 3] = __float_as_uint(fmaf(k.w, f, __uint_as_float(o[4 * n + 3])));
+                    }
+                };
+                if (kept0) add_kept(o0, 0);
+                if (kept1) add_kept(o1, 1);
                 float v[16];
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
@@ -712,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 tc_fence_after();
                 const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kK >> 4), d = tmem + kColS + s * kTok;
 #pragma unroll 1
-                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t) {          // high x high, low x high, high x low
-                    const uint32_t q = tmem + kColQ + (t == 1 ? HD / 2 : 0), k0 = lo + (t == 2 ? M::kK >> 4 : 0);
+                for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t) {          // low x high, high x low, high x high: small sums lose less (kDrain)
+                    const uint32_t q = tmem + kColQ + (PARTS == 2 && t == 0 ? HD / 2 : 0), k0 = lo + (t == 1 ? M::kK >> 4 : 0);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
                         mma_ts(d, q + 8 * k, k0 + (((k >> 2) * (kTok * 128) + 32 * (k & 3)) >> 4), hi, idesc<kTok>(), k ? 1u : t);
@@ -737,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t lo = static_cast<uint32_t>(desc) + s * (PARTS * M::kV >> 4), d = tmem + kColO + s * HD, w = tmem + kColS + s * kTok;
-                const uint32_t acc = kt > k0 + 1;                       // a group's first tile of a piece begins its sums
+                // a group's first tile of a piece begins its sums, and the first after they were drained
+                const uint32_t acc = PARTS == 2 ? ((kt - k0) >> 1) % kDrain != 0 : kt > k0 + 1;
 #pragma unroll 1
                 for (int t = 0; t < (PARTS == 2 ? 3 : 1); ++t) {
                     const uint32_t w0 = w + (t == 1 ? 32 : 0), v0 = lo + (t == 2 ? M::kV >> 4 : 0);
@@ -853,6 +905,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+// The workspace: the joining kernel's, then f32's drained sums [block][group][HD / 4][row] of four columns
+size_t kept_at(int hd) { return (parts_bytes(kBlocks, kRows, hd) + 255) / 256 * 256; }
+
 template <typename T, int HD, bool CAP>
 cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, smem = Smem<HD, PARTS>::kAll;
@@ -864,7 +919,8 @@ cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
         configured = true;
     }
     const Parts parts = parts_at(a.workspace, kBlocks, kRows, HD);
-    const cudaError_t e = launch_dependent(attn_tiles_kernel<T, HD, PARTS, CAP>, dim3(kBlocks), kThreads, smem, s, a, parts);
+    float4* kept = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + kept_at(HD));
+    const cudaError_t e = launch_dependent(attn_tiles_kernel<T, HD, PARTS, CAP>, dim3(kBlocks), kThreads, smem, s, a, parts, kept);
     if (e != cudaSuccess) return e;
     return launch_join<T, HD, kRows, 1>(a, parts, kBlocks, s);
 }
@@ -877,7 +933,9 @@ cudaError_t tiles_type(const AttnArgs& a, int head_dim, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_tiles_workspace_bytes(int head_dim) { return parts_bytes(kBlocks, kRows, head_dim); }
+size_t attn_tiles_workspace_bytes(int head_dim, int type) {
+    return type == GQ_F32 ? kept_at(head_dim) + static_cast<size_t>(kBlocks) * 2 * kRows * head_dim * 4 : parts_bytes(kBlocks, kRows, head_dim);
+}
 
 cudaError_t launch_attn_tiles(const AttnArgs& a, int type, int head_dim, cudaStream_t s) {
     if (type == GQ_F32) return tiles_type<float>(a, head_dim, s);

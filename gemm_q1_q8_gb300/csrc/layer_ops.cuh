@@ -160,7 +160,7 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(int seqs, int max_q, int q_heads, int kv_heads, int head_dim, int type);
 cudaError_t launch_attn(const AttnArgs& a, int type, int head_dim, cudaStream_t s);
-size_t attn_tiles_workspace_bytes(int head_dim);
+size_t attn_tiles_workspace_bytes(int head_dim, int type);
 cudaError_t launch_attn_tiles(const AttnArgs& a, int type, int head_dim, cudaStream_t s);   // head_dim 64 or 128
 
 }  // namespace gq

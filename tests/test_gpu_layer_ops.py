@@ -532,3 +532,17 @@ def test_many_rows_scales_that_differ(gq, kind):
     gq.rope_kv_append(None, normal(61, L, hkv, hd) * size.clamp(max=2.0), normal(62, L, hkv, hd) * size, f.cache, slots)
     f.k[0], f.v[0] = gq.kv_read(f.cache, slots)
     attention_check(gq, f, [t], hq, kind)
+
+
+@pytest.mark.parametrize("hd,kind,scale,cap", [(64, "f32", None, 0.0), (64, "f32", 1.0, 0.0), (128, "f32", None, 20.0), (64, "bf16", None, 0.0)])
+def test_many_rows_over_long_contexts(gq, hd, kind, scale, cap):
+    """Runs of so many tiles that f32 sums leave tensor memory several times, also where the maxima move late (large scores)."""
+    t, L, heads = 511, 17001, 8
+    f = Filled(gq, [L], heads, hd, 64)
+    q, o, _ = attention_check(gq, f, [t], heads, kind, scale=scale, cap=cap)
+    if kind == "f32" and scale is None and cap == 0.0:
+        s = torch.einsum("qhd,lhd->hql", q.double(), f.k[0].double()) * hd ** -0.5
+        w = torch.softmax(s.masked_fill(torch.arange(L, device="cuda")[None] > L - t + torch.arange(t, device="cuda")[:, None], -np.inf), -1)
+        want = torch.einsum("hql,lhd->qhd", w, f.v[0].double())
+        # sums of 96 products of 16, each truncated by up to 2^-23 of a sum that grows (a quarter of it on the average), the scores' 24 likewise
+        assert (o.double() - want).norm() <= (96 / 4 + 24 / 4 + 8) * 2.0 ** -23 * want.norm()
