@@ -3,8 +3,9 @@
 // Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
 // keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
 // Measured (2048 queries of 32 heads of 128 over 8192 tokens, 8 kv heads): f32 581 us (296 TFLOP/s of the formula, 890 of MMAs; 274 us at the
-// measured rate), bf16 335 us.  A 64-token score MMA takes two thirds of a 128-token one's time, so a tile's MMAs take 1920 cycles in f32, the
-// issue slots of the softmax and of the conversions some 2400, and a tile about 3500: what is left between them is waiting in their chain.
+// measured rate), bf16 335 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
+// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 2830, of which a scheduler
+// issues in 1240: the rest is the chain scores - softmax - sums at the pieces' ends, and the drains below.
 //
 // Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
 // thread; keys and values (B) in shared memory (128-byte swizzle), converted from the cache's codes by eight warps.  With A in tensor
