@@ -2,10 +2,10 @@
 //
 // Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
 // keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
-// Measured (2048 queries of 32 heads of 128 over 8192 tokens, 8 kv heads): f32 581 us (296 TFLOP/s of the formula, 890 of MMAs; 274 us at the
+// Measured (2048 queries of 32 heads of 128 over 6144 tokens with them, 8 kv heads): f32 581 us (296 TFLOP/s of the formula, 890 of MMAs; 274 us at the
 // measured rate), bf16 335 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
-// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 2830, of which a scheduler
-// issues in 1240: the rest is the chain scores - softmax - sums at the pieces' ends, and the drains below.
+// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 3950, of which a scheduler
+// issues in 1730: the rest is the chain scores - softmax - sums, the pieces' ends, and the drains below.
 //
 // Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
 // thread; keys and values (B) in shared memory (128-byte swizzle), converted from the cache's codes by eight warps.  With A in tensor
@@ -47,9 +47,9 @@ constexpr int kBlocks = 152;                               // one thread block a
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 // f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
-// always towards zero, 12 times a tile: over 8192 tokens (64 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
+// always towards zero, 12 times a tile: over 6144 tokens (48 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
 // 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543.
-// 16 bits (4 MMAs a tile) lose half of f16's last place at 600,000 tokens: not drained (the code alone would cost 4-6%, by its registers).
+// 16 bits (4 MMAs a tile) lose half of f16's last place at some 400,000 tokens: not drained (the code alone would cost 4-6%, by its registers).
 constexpr int kDrain = 8;
 
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
