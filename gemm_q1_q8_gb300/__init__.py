@@ -92,6 +92,7 @@ def lib():
             "gq_kv_read": (I, [P, I, I, I, I, P, I, I, P, P, P]),
             "gq_attn_workspace_bytes": (S, [I, I, I, I, I, I]),
             "gq_attn_q8_0": (I, [P, LL, P, LL, I, P, I, I, P, I, P, P, P, I, I, I, I, I, I, F, F, P, P]),
+            "gq_attn_q8_0_bounded": (I, [P, LL, P, LL, I, P, I, I, P, I, P, P, P, I, I, I, I, I, I, I, F, F, P, P]),
             "gq_probe_sm_count": (I, []),
             "gq_probe_fill": (I, [P, S, ctypes.c_uint32, P]),
             "gq_probe_read": (I, [P, S, P, I, I, P]),
@@ -701,7 +702,8 @@ def attn_q8_0(q: torch.Tensor, cache: KVCacheQ8_0, block_table: torch.Tensor, kv
     """Attention of each sequence's newest tokens (rows q_start[b]..q_start[b + 1] of q [n, q_heads, head_dim]) over its
     kv_len[b] cached ones, themselves included; block_table [seqs, pages a sequence] int32, kv_len [seqs] and
     q_start [seqs + 1] int32.  Among the newest tokens the mask is causal, or tree_mask[row] (int64, bit j: newest
-    token j is seen).  scale: 1 / sqrt(head_dim) when None; softcap > 0 caps the scores."""
+    token j is seen).  scale: 1 / sqrt(head_dim) when None; softcap > 0 caps the scores.  Row numbers outside q are left
+    out, and set the device error word."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise GQError("q: expected a CUDA tensor [n, q_heads, head_dim]")
     n, hq, hd = q.shape
@@ -729,10 +731,10 @@ def attn_q8_0(q: torch.Tensor, cache: KVCacheQ8_0, block_table: torch.Tensor, kv
     _need(workspace, torch.uint8, workspace.numel(), "workspace")
     if workspace.numel() < need:
         raise GQError(f"attn_q8_0: workspace holds {workspace.numel()} bytes, needs {need}")
-    _check(lib().gq_attn_q8_0(_at(q), qs, _at(o), os_, code, _at(cache.data), cache.pages, cache.page_size,
-                              _at(block_table), block_table.shape[1], _at(kv_len), _at(q_start), _at(tree_mask), seqs,
-                              max_q, max_kv, hq, cache.kv_heads, hd, hd ** -0.5 if scale is None else scale, softcap,
-                              _at(workspace), _on(q)), "gq_attn_q8_0")
+    _check(lib().gq_attn_q8_0_bounded(_at(q), qs, _at(o), os_, code, _at(cache.data), cache.pages, cache.page_size,
+                                      _at(block_table), block_table.shape[1], _at(kv_len), _at(q_start), _at(tree_mask), n,
+                                      seqs, max_q, max_kv, hq, cache.kv_heads, hd, hd ** -0.5 if scale is None else scale,
+                                      softcap, _at(workspace), _on(q)), "gq_attn_q8_0_bounded")
     return o
 
 

@@ -53,6 +53,7 @@ template <int HD, int MT> constexpr int smem_bytes() { return 1024 + ring_bytes<
 // One sequence's share of the work.
 struct Seq {
     int L, T, q0;          // cached tokens, query tokens, first query row
+    int rows;              // that are computed, of a kv head
     int units;             // of one tile
     int tiles;             // row tiles a kv head
     __device__ __forceinline__ long long span(int kv_heads) const { return static_cast<long long>(units) * tiles * kv_heads; }
@@ -61,12 +62,14 @@ struct Seq {
 template <int ROWS>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     Seq s;
-    s.q0 = a.q_start[b];
-    s.T = a.q_start[b + 1] - s.q0;
+    const QueryRows q = query_rows(a, b);
+    s.q0 = q.q0;
+    s.T = q.T;
     s.L = a.kv_len[b];
-    if (s.T > a.max_q || s.L > a.max_kv) report_error(kErrIndex);
+    if (s.L > a.max_kv) report_error(kErrIndex);
+    s.rows = q.tokens * (a.q_heads / a.kv_heads);
     s.units = (min(max(s.L, 0), a.max_kv) + kvGroup - 1) / kvGroup;
-    s.tiles = (min(max(s.T, 0), a.max_q) * (a.q_heads / a.kv_heads) + ROWS - 1) / ROWS;
+    s.tiles = (s.rows + ROWS - 1) / ROWS;
     return s;
 }
 
@@ -179,11 +182,10 @@ struct Queries {
     }
     __device__ __forceinline__ void request(const AttnArgs& a, const Seq& s, int hk, int tile0, int mt, int lane) {
         const int g = lane >> 2, t = lane & 3, group = a.q_heads / a.kv_heads;
-        const int rows = min(s.T, a.max_q) * group;
 #pragma unroll
         for (int set = 0; set < kSets; ++set) {
             const int r = tile0 + row_of(mt, set, g);
-            const bool in = r < rows;
+            const bool in = r < s.rows;
             const int tok = in ? r / group : 0, h = in ? r % group : 0;
             const T* q = static_cast<const T*>(a.q) + (s.q0 + tok) * a.q_stride + (hk * group + h) * HD;
 #pragma unroll
@@ -192,7 +194,6 @@ struct Queries {
     }
     __device__ __forceinline__ void lay(const AttnArgs& a, const Seq& s, int tile0, int mt, int lane, uint4* frag, RowInfo* info) const {
         const int g = lane >> 2, t = lane & 3, group = a.q_heads / a.kv_heads;
-        const int rows = min(s.T, a.max_q) * group;
         float f[kSets];
 #pragma unroll
         for (int set = 0; set < kSets; ++set) {
@@ -210,7 +211,7 @@ struct Queries {
             f[set] = pow2i(up);
             if (t == 0 && (PARTS != 3 || g < 4)) {
                 const int r = tile0 + row_of(mt, set, g);
-                const bool in = r < rows;
+                const bool in = r < s.rows;
                 const int tok = in ? r / group : 0;
                 RowInfo ri;
                 // 2^24 for the codes, 2^-up for the query
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
             }
             if (!ok) break;
             if (end == p.s.units && begun_here) {                        // all of the tile
-                const int rows = min(p.s.T, a.max_q) * group - tile0;
+                const int rows = p.s.rows - tile0;
                 T* out = static_cast<T*>(a.out) + p.s.q0 * a.out_stride + hk * group * HD;
                 tile.put(lane, true, [&](int r, int c, float4 v, float, float) {
                     if (r < rows) store4(out + ((tile0 + r) / group) * a.out_stride + ((tile0 + r) % group) * HD + c, v);
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
             } else if (end == p.s.units) {                               // its end: for the second kernel
                 int begun, unused;
                 div_mod(first, static_cast<int>(per), begun, unused);
-                head = {begun, p.s.q0, tile0, min(min(p.s.T, a.max_q) * group - tile0, kRows), hk};
+                head = {begun, p.s.q0, tile0, min(p.s.rows - tile0, kRows), hk};
                 tile.put(lane, false, [&](int r, int c, float4 v, float m, float l) {
                     const size_t at = static_cast<size_t>(run) * kRows + r;
                     *reinterpret_cast<float4*>(parts.o + at * HD + c) = v;

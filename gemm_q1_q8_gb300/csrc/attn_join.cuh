@@ -25,6 +25,27 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
 
+// The query rows of sequence b.  q_start comes from device memory: rows outside [0, a.rows) are neither read nor written.
+struct QueryRows {
+    int q0, T;             // first row, query tokens
+    int tokens;            // those that are computed: at most max_q of them, and their rows exist
+};
+__device__ __forceinline__ QueryRows query_rows(const AttnArgs& a, int b) {
+    const int limit = a.rows >= 0 ? a.rows : a.q_start[a.seqs];
+    QueryRows r;
+    r.q0 = a.q_start[b];
+    const int end = a.q_start[b + 1];
+    if (r.q0 < 0 || end < r.q0 || end > limit) report_error(kErrIndex);
+    if (r.q0 < 0 || end < r.q0 || r.q0 >= limit) {
+        r.q0 = r.T = r.tokens = 0;
+        return r;
+    }
+    r.T = end - r.q0;
+    if (r.T > a.max_q) report_error(kErrIndex);
+    r.tokens = min(min(r.T, a.max_q), limit - r.q0);
+    return r;
+}
+
 // x / d and x % d, in 32 bits where x allows
 __device__ __forceinline__ void div_mod(long long x, int d, int& quot, int& rest) {
     if (x < 0x7fffffffll) {
@@ -140,10 +161,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
     if (blockIdx.y == 0)
         for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
             if (a.kv_len[b] > 0) continue;
-            const int q0 = a.q_start[b], n = min(a.q_start[b + 1] - q0, a.max_q);
-            for (int tok = warp; tok < n; tok += kWarps)
+            const QueryRows rows = query_rows(a, b);
+            for (int tok = warp; tok < rows.tokens; tok += kWarps)
                 for (int d = lane * 4; d < a.q_heads * HD; d += 128)
-                    store4(static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
+                    store4(static_cast<T*>(a.out) + (rows.q0 + tok) * a.out_stride + d, make_float4(0.f, 0.f, 0.f, 0.f));
         }
 }
 

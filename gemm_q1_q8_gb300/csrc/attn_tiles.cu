@@ -191,11 +191,12 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     Seq s;
-    s.q0 = a.q_start[b];
-    s.T = a.q_start[b + 1] - s.q0;
+    const QueryRows q = query_rows(a, b);
+    s.q0 = q.q0;
+    s.T = q.T;
     s.L = a.kv_len[b];
-    if (s.T > a.max_q || s.L > a.max_kv) report_error(kErrIndex);
-    s.rows = min(max(s.T, 0), a.max_q) * (a.q_heads / a.kv_heads);
+    if (s.L > a.max_kv) report_error(kErrIndex);
+    s.rows = q.tokens * (a.q_heads / a.kv_heads);
     s.len = min(max(s.L, 0), a.max_kv);
     return s;
 }

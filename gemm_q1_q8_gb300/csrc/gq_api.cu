@@ -356,10 +356,10 @@ size_t gq_attn_workspace_bytes(int seqs, int max_q, int q_heads, int kv_heads, i
     return gq::attn_workspace_bytes(seqs, max_q, q_heads, kv_heads, head_dim, type);
 }
 
-int gq_attn_q8_0(const void* q, long long q_stride, void* out, long long out_stride, int type, const void* cache, int pages,
-                 int page_size, const int32_t* table, int table_stride, const int32_t* kv_len, const int32_t* q_start,
-                 const uint64_t* tree, int seqs, int max_q, int max_kv, int q_heads, int kv_heads, int head_dim, float scale,
-                 float softcap, void* workspace, gq_stream_t stream) {
+static int attn_call(const void* q, long long q_stride, void* out, long long out_stride, int type, const void* cache, int pages,
+                     int page_size, const int32_t* table, int table_stride, const int32_t* kv_len, const int32_t* q_start,
+                     const uint64_t* tree, int rows, int seqs, int max_q, int max_kv, int q_heads, int kv_heads, int head_dim,
+                     float scale, float softcap, void* workspace, gq_stream_t stream) {
     if (!attn_shape(seqs, max_q, q_heads, kv_heads, head_dim) || !cache_shape(pages, page_size, kv_heads, head_dim) ||
         max_kv < 1 || (tree && max_q > 64))
         return GQ_EINVAL_SHAPE;
@@ -373,9 +373,26 @@ int gq_attn_q8_0(const void* q, long long q_stride, void* out, long long out_str
         !aligned(workspace, 16) || !aligned(table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(tree, 8))
         return GQ_EINVAL_PTR;
     const gq::AttnArgs a = {q, out, q_stride, out_stride, static_cast<const uint8_t*>(cache), pages, page_size, table,
-                            table_stride, kv_len, q_start, tree, seqs, max_q, max_kv, q_heads, kv_heads, scale, softcap,
+                            table_stride, kv_len, q_start, tree, rows, seqs, max_q, max_kv, q_heads, kv_heads, scale, softcap,
                             workspace};
     return cuda_status(gq::launch_attn(a, type, head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gq_attn_q8_0(const void* q, long long q_stride, void* out, long long out_stride, int type, const void* cache, int pages,
+                 int page_size, const int32_t* table, int table_stride, const int32_t* kv_len, const int32_t* q_start,
+                 const uint64_t* tree, int seqs, int max_q, int max_kv, int q_heads, int kv_heads, int head_dim, float scale,
+                 float softcap, void* workspace, gq_stream_t stream) {
+    return attn_call(q, q_stride, out, out_stride, type, cache, pages, page_size, table, table_stride, kv_len, q_start, tree, -1, seqs,
+                     max_q, max_kv, q_heads, kv_heads, head_dim, scale, softcap, workspace, stream);
+}
+
+int gq_attn_q8_0_bounded(const void* q, long long q_stride, void* out, long long out_stride, int type, const void* cache,
+                         int pages, int page_size, const int32_t* table, int table_stride, const int32_t* kv_len,
+                         const int32_t* q_start, const uint64_t* tree, int rows, int seqs, int max_q, int max_kv, int q_heads,
+                         int kv_heads, int head_dim, float scale, float softcap, void* workspace, gq_stream_t stream) {
+    if (rows < 0) return GQ_EINVAL_SHAPE;
+    return attn_call(q, q_stride, out, out_stride, type, cache, pages, page_size, table, table_stride, kv_len, q_start, tree, rows,
+                     seqs, max_q, max_kv, q_heads, kv_heads, head_dim, scale, softcap, workspace, stream);
 }
 
 }  // extern "C"

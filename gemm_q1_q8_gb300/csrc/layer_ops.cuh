@@ -154,6 +154,7 @@ struct AttnArgs {
     const int32_t* kv_len;
     const int32_t* q_start;
     const uint64_t* tree;
+    int rows;              // of q and out; negative: q_start[seqs]
     int seqs, max_q, max_kv, q_heads, kv_heads;
     float scale, softcap;
     void* workspace;

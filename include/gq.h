@@ -496,6 +496,10 @@ int gq_kv_read(const void* cache_device, int pages, int page_size, int kv_heads,
  *   T > L is allowed (the first queries then see nothing, and give 0), T = 0 and L = 0 too.
  *   max_q and max_kv bound T and L of every sequence; a longer T or L, or a page index outside
  *   [0, pages), sets GQ_DEVERR_INDEX: what is past the bound is not computed or not seen.
+ *   Row numbers are checked against [0, rows): gq_attn_q8_0_bounded is told how many rows q_device, out_device and
+ *   tree_mask_device have, gq_attn_q8_0 takes q_start_device[seqs] for it (which must then be right).  A sequence that begins
+ *   outside, or ends before it begins, is left out, of one that ends past it the rows inside are computed (each at its place
+ *   L - T + i); both set GQ_DEVERR_INDEX.
  *   workspace_device: gq_attn_workspace_bytes(...) bytes, 16-byte aligned, overwritten; calls that
  *   share it must not overlap on the GPU.  Nothing of it is kept between calls.  Results do not depend on
  *   timing: the same inputs give the same bits.
@@ -515,6 +519,13 @@ int gq_attn_q8_0(const void* q_device, long long q_stride, void* out_device, lon
                  int table_stride, const int32_t* kv_len_device, const int32_t* q_start_device,
                  const uint64_t* tree_mask_device, int seqs, int max_q, int max_kv, int q_heads, int kv_heads,
                  int head_dim, float scale, float softcap, void* workspace_device, gq_stream_t stream);
+/* gq_attn_q8_0 with the number of rows given.  Errors: also GQ_EINVAL_SHAPE if rows < 0. */
+int gq_attn_q8_0_bounded(const void* q_device, long long q_stride, void* out_device, long long out_stride, int type,
+                         const void* cache_device, int pages, int page_size, const int32_t* block_table_device,
+                         int table_stride, const int32_t* kv_len_device, const int32_t* q_start_device,
+                         const uint64_t* tree_mask_device, int rows, int seqs, int max_q, int max_kv, int q_heads,
+                         int kv_heads, int head_dim, float scale, float softcap, void* workspace_device,
+                         gq_stream_t stream);
 
 /* ============================================================================================
  * Roofline probes (measurement only; no hot-path entry point uses them).  The machine's own

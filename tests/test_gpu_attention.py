@@ -1,0 +1,104 @@
+"""Attention over the Q8_0 cache where it can go wrong: row numbers outside the call, against the calls they leave whole."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def gq():
+    need_gpu()
+    import gemm_q1_q8_gb300 as m
+    return m
+
+
+def normal(seed, *shape):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape, dtype=np.float32)).cuda()
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def cached(gq, keys, values, page=16):
+    """A cache of one sequence per (keys, values) [L, heads, hd], its block table, and the values it holds."""
+    hkv, hd = keys[0].shape[1:]
+    need = [-(-len(k) // page) for k in keys]
+    cache = gq.KVCacheQ8_0(sum(need), page, hkv, hd)
+    table = torch.full((len(keys), max(need)), -1, dtype=torch.int32, device="cuda")
+    held, first = [], 0
+    for b, (k, v) in enumerate(zip(keys, values)):
+        table[b, :need[b]] = torch.arange(first, first + need[b], device="cuda")
+        slots = first * page + torch.arange(len(k), device="cuda")
+        gq.rope_kv_append(None, k, v, cache, slots)
+        held.append(gq.kv_read(cache, slots))
+        first += need[b]
+    return cache, table, held
+
+
+INDEX_ERROR = 8                                                    # GQ_DEVERR_INDEX
+
+
+@pytest.mark.parametrize("hd,heads,t,kind", [(128, 2, 6, "f32"), (64, 2, 12, "bf16"), (64, 4, 40, "bf16"), (256, 2, 20, "f32"), (128, 8, 90, "f32"),
+                                             (64, 8, 90, "bf16")])
+def test_row_numbers_outside_the_call(gq, hd, heads, t, kind):
+    """Sequences that begin before the rows or past them, end before they begin, or end past the rows.  q and out lie inside larger
+    tensors; what is around them stays as it was."""
+    L = [200, 130, 140, 0, 150]
+    cache, table, _ = cached(gq, [normal(i, max(n, 1), 1, hd) for i, n in enumerate(L)], [normal(9 + i, max(n, 1), 1, hd) for i, n in enumerate(L)])
+    kv_len = i32(*L)
+    pad, n = 2 * t, 2 * t + 5                                     # the call's rows: pad .. pad + n of the tensors
+    big = normal(20, n + 2 * pad, heads, hd).to(TYPES[kind])
+    q = big[pad:pad + n]
+    # what each leaves whole: (sequence, first row, last row)
+    for start, whole in (((-t, t, 2 * t, 0, t, t), [(1, t, 2 * t), (3, 0, t)]), ((0, t, n + t, n + 2 * t, n, n), [(0, 0, t), (1, t, n)])):
+        out = torch.full_like(big, 7.0)
+        gq.attn_q8_0(q, cache, table, kv_len, i32(*start), 3 * t, 200, out=out[pad:pad + n])
+        assert gq.device_error() == INDEX_ERROR
+        assert torch.all(out[:pad] == 7) and torch.all(out[pad + n:] == 7)
+        got, written = out[pad:pad + n], torch.zeros(n, dtype=torch.bool, device="cuda")
+        for b, lo, hi in whole:
+            written[lo:hi] = True
+            T = start[b + 1] - start[b]
+            alone = torch.zeros(T, heads, hd, dtype=q.dtype, device="cuda")
+            alone[:hi - lo] = q[lo:hi]
+            want = gq.attn_q8_0(alone, cache, table[b:b + 1].contiguous(), kv_len[b:b + 1].contiguous(), i32(0, T), 3 * t, 200)
+            tol = dict(rtol=1e-4, atol=1e-5) if kind == "f32" else dict(rtol=2e-2, atol=2e-2)
+            assert torch.allclose(got[lo:hi].float(), want[:hi - lo].float(), **tol), (b, lo, hi)
+        assert torch.all(got[~written] == 7) and gq.device_error() == 0
+
+
+def test_rows_of_the_plain_entry_are_those_of_q_start(gq):
+    """gq_attn_q8_0 takes q_start's last element as the number of rows: an earlier one past it, or a negative one, is left out."""
+    hd, heads, L = 64, 2, 40
+    cache, table, _ = cached(gq, [normal(1, L, 1, hd)] * 3, [normal(2, L, 1, hd)] * 3)
+    q = normal(3, 12, heads, hd)
+    out = torch.full_like(q, 7.0)
+    kv_len = i32(L, L, L)
+    work = gq.attn_workspace(cache, heads, 3, 4)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+
+    def call(start, rows=None):
+        args = [p(q[4:]), heads * hd, p(out[4:]), heads * hd, 0, p(cache.data), cache.pages, cache.page_size, p(table), table.shape[1], p(kv_len),
+                p(start), None, 3, 4, L, heads, 1, hd, hd ** -0.5, 0.0, p(work), stream]
+        if rows is None:
+            return gq.lib().gq_attn_q8_0(*args)
+        return gq.lib().gq_attn_q8_0_bounded(*args[:13], rows, *args[13:])
+
+    start = i32(-4, 0, 4, 3)                                      # three rows: -4 .. -1 are not theirs, of the third's none is left
+    assert call(start) == 0 and gq.device_error() == INDEX_ERROR
+    assert torch.all(out[:4] == 7) and torch.all(out[7:] == 7)
+    want = gq.attn_q8_0(q[4:8].contiguous(), cache, table[1:2].contiguous(), i32(L), i32(0, 4), 4, L)
+    assert torch.allclose(out[4:7], want[:3], rtol=1e-5, atol=1e-6)
+    assert call(start, -1) == 1
+    out.fill_(7.0)
+    assert call(i32(0, 4, 8, 8), 2) == 0 and gq.device_error() == INDEX_ERROR
+    assert torch.allclose(out[4:6], want[:2], rtol=1e-5, atol=1e-6) and torch.all(out[6:] == 7) and torch.all(out[:4] == 7)
