@@ -786,18 +786,15 @@ template <typename T, int HD, int PARTS, int MT>
 cudaError_t rows_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int kRows = tile_rows<PARTS, MT>(), kWarps = warps<HD, MT>(), smem = smem_bytes<HD, MT>();
     static_assert(smem <= 220 * 1024, "shared memory");
-    static bool configured = false;
-    if (!configured) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<T, HD, PARTS, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = allow_smem(attn_rows_kernel<T, HD, PARTS, MT>, smem, raised);
+    if (e != cudaSuccess) return e;
     const int gpp = a.page_size / kvGroup;
     int shift = -1;
     for (int i = 0; i < 16; ++i)
         if (gpp == 1 << i) shift = i;
     const Parts parts = parts_at(a.workspace, kBlocks * kWarps, kRows, HD);
-    const cudaError_t e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), (kWarps + 1) * 32, smem, s, a, parts, shift);
+    e = launch_dependent(attn_rows_kernel<T, HD, PARTS, MT>, dim3(kBlocks), (kWarps + 1) * 32, smem, s, a, parts, shift);
     if (e != cudaSuccess) return e;
     return launch_join<T, HD, kRows, kWarps>(a, parts, kBlocks * kWarps, s);
 }

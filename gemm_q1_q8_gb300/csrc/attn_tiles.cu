@@ -914,15 +914,12 @@ template <typename T, int HD, bool CAP>
 cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, smem = Smem<HD, PARTS>::kAll;
     static_assert(smem <= 227 * 1024, "shared memory");
-    static bool configured = false;
-    if (!configured) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<T, HD, PARTS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = allow_smem(attn_tiles_kernel<T, HD, PARTS, CAP>, smem, raised);
+    if (e != cudaSuccess) return e;
     const Parts parts = parts_at(a.workspace, kBlocks, kRows, HD);
     float4* kept = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + kept_at(HD));
-    const cudaError_t e = launch_dependent(attn_tiles_kernel<T, HD, PARTS, CAP>, dim3(kBlocks), kThreads, smem, s, a, parts, kept);
+    e = launch_dependent(attn_tiles_kernel<T, HD, PARTS, CAP>, dim3(kBlocks), kThreads, smem, s, a, parts, kept);
     if (e != cudaSuccess) return e;
     return launch_join<T, HD, kRows, 1>(a, parts, kBlocks, s);
 }

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gq.h"
 
 namespace gq {
@@ -41,6 +43,19 @@ unsigned error_read_clear_block_q8();
 unsigned error_read_clear_kv();
 unsigned error_read_clear_attn();
 unsigned error_read_clear_attn_tiles();
+
+// Raises a kernel's limit of dynamic shared memory, once on each device (the limit belongs to the device; `done` is the kernel's own word).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;          // further devices raise it every time
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
