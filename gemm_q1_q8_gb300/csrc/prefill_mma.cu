@@ -361,13 +361,9 @@ cudaError_t launch_prefill_mma(const uint32_t* signs, const float* ws, const uin
     const size_t smem = 1024 + static_cast<size_t>(kStagesM) * kPlanes * kTileB + ((sizeof(Bars) + 15) & ~size_t(15)) +
                         static_cast<size_t>(kWSlots) * 2 * BM * sizeof(float);
     if (smem > 227 * 1024) return cudaErrorNotSupported;
-    static size_t configured = 0;
-    if (smem > configured) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        configured = smem;
-    }
+    static std::atomic<uint64_t> raised{0};
+    const cudaError_t e = allow_smem(prefill_mma_kernel, smem, raised);
+    if (e != cudaSuccess) return e;
     const dim3 grid((N + BM - 1) / BM, (M + BN - 1) / BN);
     prefill_mma_kernel<<<grid, kThreads, smem, s>>>(tmB, signs, ws, y, M, N, K);
     return cudaGetLastError();

@@ -6,6 +6,7 @@
 static int current;
 static struct { const void* func; int device, bytes; } raised[256];
 static int count;
+static cudaError_t last;
 
 void fake_set_device(int d) { current = d; }
 int fake_raised(void) { return count; }
@@ -25,7 +26,7 @@ static cudaError_t launch(const void* func, size_t bytes) {
     int limit = 48 * 1024;
     for (int i = 0; i < count; ++i)
         if (raised[i].func == func && raised[i].device == current) limit = raised[i].bytes;
-    return bytes <= (size_t)limit ? cudaSuccess : cudaErrorInvalidValue;
+    return last = bytes <= (size_t)limit ? cudaSuccess : cudaErrorInvalidValue;
 }
 cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* func, void** args) {
     (void)args;
@@ -35,7 +36,11 @@ cudaError_t CUDARTAPI cudaLaunchKernel(const void* func, dim3 grid, dim3 block, 
     (void)grid, (void)block, (void)args, (void)s;
     return launch(func, bytes);
 }
-cudaError_t CUDARTAPI cudaGetLastError(void) { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaGetLastError(void) {
+    const cudaError_t e = last;
+    last = cudaSuccess;
+    return e;
+}
 
 static int encode(void) { return 0; }                    /* a tensor map: any arguments, success */
 cudaError_t CUDARTAPI cudaGetDriverEntryPointByVersion(const char* name, void** fn, unsigned version, unsigned long long flags,

@@ -50,6 +50,7 @@ def attn(type, max_q, hd, cap):
     return lib.gq_attn_q8_0(X, w, X, w, type, X, 9, 64, X, 4, X, X, None, 2, max_q, 256, 4, 2, hd, F(0.1), F(cap), X, None)
 calls = {
     "attn": lambda: [attn(t, q, hd, cap) for t in (0, 1, 2) for q in (1, 3, 40, 300) for hd in (64, 128, 256) for cap in (0.0, 5.0)],
+    "prefill": lambda: [lib.q1s32_q8_gemm(X, X, X, X, X, X, M, 300, 256, 3, None) for M in (64, 333)],
 }[call]
 for device in (0, 1, 0, 3, 1):
     fake.fake_set_device(device)
@@ -62,7 +63,7 @@ assert fake.fake_raised() == raised, "raised again where it had been"
 """
 
 
-@pytest.mark.parametrize("call", ["attn"])
+@pytest.mark.parametrize("call", ["attn", "prefill"])
 def test_on_every_device_of_a_process(fake_runtime, call):
     """The shared-memory limit belongs to the device: each device's first call raises it, and no later one again."""
     from gemm_q1_q8_gb300 import build
