@@ -32,9 +32,14 @@ cudaError_t CUDARTAPI cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const voi
     (void)args;
     return launch(func, c->dynamicSmemBytes);
 }
-cudaError_t CUDARTAPI cudaLaunchKernel(const void* func, dim3 grid, dim3 block, void** args, size_t bytes, cudaStream_t s) {
+/* what a <<< >>> launch calls */
+cudaError_t CUDARTAPI __cudaGetKernel(cudaKernel_t* kernel, const void* func) {
+    *kernel = (cudaKernel_t)func;
+    return cudaSuccess;
+}
+cudaError_t CUDARTAPI __cudaLaunchKernel(cudaKernel_t kernel, dim3 grid, dim3 block, void** args, size_t bytes, cudaStream_t s) {
     (void)grid, (void)block, (void)args, (void)s;
-    return launch(func, bytes);
+    return launch((const void*)kernel, bytes);
 }
 cudaError_t CUDARTAPI cudaGetLastError(void) {
     const cudaError_t e = last;
