@@ -40,7 +40,7 @@ namespace {
 constexpr int many_rows(int type) { return type == GQ_F32 ? 256 : 128; }
 constexpr int kBlocks = 152;                       // one thread block an SM
 
-constexpr float kLift = 108.f;                     // f32 weights carry 2^108: times a scale below 2^16 and 2^kSlack they stay in f32's range
+constexpr float kLift = 0x1p108f;                  // f32 weights are multiplied by it: times a scale below 2^16 and 2^kSlack they stay in f32's range
 constexpr float kSlack = 2.f;                      // a score may pass the running maximum by this much before it moves: 1.02 (16 bits: 0)
 // Rows of a tile by the parts of its operands: 16-bit queries 1; f32 2, or 3 for up to four rows
 template <int PARTS, int MT> __host__ __device__ constexpr int tile_rows() { return PARTS == 1 ? 16 * MT : PARTS == 2 ? 8 * MT : 4; }
@@ -361,9 +361,9 @@ struct Tile {
                             for (int i = 0; i < 4; ++i) o[mt][c][x][i] *= down;
             }
         }
-        // scores to weights, which carry the power of two 2^lift
-        const float lift = PARTS == 1 ? static_cast<float>(15 - vexp) : kLift;
-        const float lower = PARTS == 1 ? pow2i(vexp - 15) : 0x1p-108f;
+        // scores to weights, which carry a power of two: 16 bits in the exponent's argument, f32 as a factor (an argument near 108 would have
+        // steps of 2^-17)
+        const float lift = static_cast<float>(15 - vexp), lower = pow2i(vexp - 15);
         float P[MT][kSets][4];                                   // [row][token of the thread's four]
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -431,12 +431,12 @@ struct Tile {
             }
 #pragma unroll
             for (int set = 0; set < kSets; ++set) {
-                const float from = m[mt][set] - lift;
+                const float from = PARTS == 1 ? m[mt][set] - lift : m[mt][set];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     const float x = ex2(P[mt][set][p] - from);
-                    P[mt][set][p] = x;
-                    l[mt][set] = fmaf(x, lower, l[mt][set]);
+                    P[mt][set][p] = PARTS == 1 ? x : x * kLift;
+                    l[mt][set] = PARTS == 1 ? fmaf(x, lower, l[mt][set]) : l[mt][set] + x;
                 }
             }
         }

@@ -1,4 +1,5 @@
-"""Attention over the Q8_0 cache where it can go wrong: row numbers outside the call, against the calls they leave whole."""
+"""Attention over the Q8_0 cache where it can go wrong, against the formula in 64 bits: row numbers outside the call, and the precision of f32
+queries."""
 import ctypes
 
 import numpy as np
@@ -102,3 +103,39 @@ def test_rows_of_the_plain_entry_are_those_of_q_start(gq):
     out.fill_(7.0)
     assert call(i32(0, 4, 8, 8), 2) == 0 and gq.device_error() == INDEX_ERROR
     assert torch.allclose(out[4:6], want[:2], rtol=1e-5, atol=1e-6) and torch.all(out[6:] == 7) and torch.all(out[:4] == 7)
+
+
+def exact(q, k, v, scale, seen=None, cap=0.0):
+    """o and sum w |v| of one sequence in 64 bits: q [T, heads, hd], k, v [L, kv heads, hd], seen [T, L] (None: causal)."""
+    T, L, group = len(q), len(k), q.shape[1] // k.shape[1]
+    k, v = k.double().repeat_interleave(group, 1), v.double().repeat_interleave(group, 1)
+    s = torch.einsum("thd,lhd->htl", q.double(), k) * scale
+    if cap:
+        s = cap * torch.tanh(s / cap)
+    if seen is None:
+        seen = torch.arange(L, device="cuda")[None] <= L - T + torch.arange(T, device="cuda")[:, None]
+    w = torch.softmax(s.masked_fill(~seen[None], -torch.inf), -1)
+    return torch.einsum("htl,lhd->thd", w, v), torch.einsum("htl,lhd->thd", w, v.abs())
+
+
+def attend(gq, q, cache, table, L, **kw):
+    T = len(q)
+    o = gq.attn_q8_0(q, cache, table, i32(L), i32(0, T), T, L, **kw)
+    assert gq.device_error() == 0
+    return o
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("heads", [4, 8, 64])
+@pytest.mark.parametrize("L", [2, 5, 40])
+def test_f32_weights_of_small_scores(gq, hd, heads, L):
+    """Scores near 0, so that what is left of the error is the exponentials' and the sums': few units of f32's last place."""
+    k, v, q = normal(1, L, 1, hd), normal(2, L, 1, hd), 0.005 * normal(3, 1, heads, hd)
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    o = attend(gq, q, cache, table, L)
+    want, big = exact(q, k, v, hd ** -0.5)
+    size = torch.einsum("thd,lhd->thl", q.abs(), k.abs().expand(-1, heads, -1)).amax(-1, keepdim=True) * hd ** -0.5
+    # a score's products of 22 bits and sums (as large scores have it); two exponentials of 2^-22; a sum's matrix products, truncated, two for every 16
+    # keys; a weight times its scale, and its three parts; the sum's division and product
+    rel = 2 * size.double() * 2.0 ** -19 + 2 * 2.0 ** -22 + (L / 16 + 1) * 2 * 2.0 ** -23 + 2.0 ** -23 + 3 * 2.0 ** -24
+    assert torch.all((o.double() - want).abs() <= rel * big), float(((o.double() - want).abs() / big).max())
