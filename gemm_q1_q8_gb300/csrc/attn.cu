@@ -500,8 +500,14 @@ struct Tile {
                     if (PARTS == 1) {
                         mma16816(o[mt][c][e], pa[mt], b0, b1);
                     } else {
-                        mma16816_bf16(o[mt][c][e], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
-                        if (PARTS == 2) mma16816_bf16(o[mt][c][e], low[mt][0], 0u, low[mt][1], 0u, b0, b1);
+                        // an MMA truncates the sum that it adds to, always towards zero, so the chunks' sums are added outside: a mean loss of 7.2e-6 of
+                        // the result after 512 chunks is gone, for 106.3 -> 110.8 us of 32 ragged sequences (with the low rows left in the MMA, whose
+                        // registers then move, 121)
+                        float z[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (PARTS == 2) mma16816_bf16(z, low[mt][0], 0u, low[mt][1], 0u, b0, b1);
+                        mma16816_bf16(z, pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[mt][c][e][i] += z[i];
                     }
                 }
             }

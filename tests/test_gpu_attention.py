@@ -139,3 +139,22 @@ def test_f32_weights_of_small_scores(gq, hd, heads, L):
     # keys; a weight times its scale, and its three parts; the sum's division and product
     rel = 2 * size.double() * 2.0 ** -19 + 2 * 2.0 ** -22 + (L / 16 + 1) * 2 * 2.0 ** -23 + 2.0 ** -23 + 3 * 2.0 ** -24
     assert torch.all((o.double() - want).abs() <= rel * big), float(((o.double() - want).abs() / big).max())
+
+
+@pytest.mark.parametrize("hd,heads,hkv,seqs,T,L", [(128, 16, 4, 64, 1, 16384), (64, 32, 4, 64, 1, 16384), (128, 16, 1, 16, 8, 8192), (256, 8, 1, 1, 1024, 8192)])
+def test_f32_sums_over_long_runs(gq, hd, heads, hkv, seqs, T, L):
+    """Many rows over the same pages, so that a warp adds hundreds of chunks.  Equal weights and positive values: what each addition loses has one
+    sign if it is truncated, and none if it is rounded."""
+    k, v = normal(1, L, hkv, hd), 1 + normal(2, L, hkv, hd).abs()
+    cache, table, [(k, v)] = cached(gq, [k], [v], page=64)
+    q = torch.zeros(seqs * T, heads, hd, device="cuda")
+    o = gq.attn_q8_0(q, cache, table.expand(seqs, -1).contiguous(), i32(*[L] * seqs), i32(*[T * b for b in range(seqs + 1)]), T, L)
+    assert gq.device_error() == 0
+    mean = v.double().cumsum(0)[L - T:] / (L - T + 1 + torch.arange(T, device="cuda"))[:, None, None]
+    want = mean.repeat_interleave(heads // hkv, 1).repeat(seqs, 1, 1)
+    rel = (o.double() - want) / want
+    # a chunk's two matrix products, truncated (2^-23 each of a sum that is rounded besides), and the division; rounded additions of a run's at most
+    # L / 16 chunks, 2^-24 at most of a sum that grows: a third of them all, by their square root
+    bias = 2 * 2.0 ** -23 + 2 * 2.0 ** -24
+    assert abs(float(rel.mean())) <= bias, float(rel.mean())
+    assert float(rel.square().mean().sqrt()) <= bias + 2.0 ** -24 * (L / 16 / 3) ** 0.5, float(rel.square().mean().sqrt())
