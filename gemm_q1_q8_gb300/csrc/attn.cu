@@ -20,8 +20,10 @@
 // 7-bit magnitude are the bits of the f16 subnormal magnitude * 2^-24, and of the bf16 one magnitude * 2^-133, so two codes become a
 // register with one byte permute and one mask, and no conversion.  S: each 32-dim block has its own accumulator, multiplied by the
 // key's scale in f32.  O: the weight times the value's scale is A, and the codes are B.
-// 16-bit queries: one f16 part of each, 16 rows a tile, powers of two keeping A near the top of f16's range (a row's largest query value,
-// and the largest value scale seen so far, go to 2^14..2^15): a rounding costs 2^-12 of the value, or 2^-40 of the largest.
+// 16-bit queries: one f16 part of each, 16 rows a tile, powers of two keeping A near the top of f16's range: a row's largest query value goes
+// to 2^14..2^15, and so does its largest product of a weight and the exponent e of that token's largest value scale (below 2^e), because the
+// running maximum is that of s + e.  A rounding costs 2^-12 of the product, or 2^-40 of the largest that the row has seen; hidden tokens
+// and those of no weight do not count, whatever their scales are.
 // f32 queries: 8 rows a tile; A has the high f16 part of the queries in its rows 0-7 and the rest in rows 8-15 (22 bits together); both halves
 // of a row end in one thread, which adds them.  The weights take three bf16 parts (24 bits, the third in a product of its own) for f32's
 // range: a weight of 2^-90 counts where the larger ones meet zero codes.
@@ -251,7 +253,6 @@ struct Tile {
     float o[MT][kNb][4][4];
     float m[MT][kSets], l[MT][kSets];
     RowInfo row[MT][kSets];
-    int vexp;              // 16-bit queries: weights are multiplied by 2^(15 - vexp)
 
     __device__ __forceinline__ void start(const RowInfo* info, int lane) {
 #pragma unroll
@@ -269,7 +270,6 @@ struct Tile {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][c][e][i] = 0.f;
         }
-        vexp = -24;
     }
 
     // Scales of this thread's four tokens (2t, 2t + 1, 2t + 8, 2t + 9), [token][block] in halves; tokens from `end` on have none
@@ -339,31 +339,19 @@ struct Tile {
         }
         uint32_t vsw[kNb * 2];
         load_scales(ch + kv_vs_offset(HD), t, end, vsw);
-        // f16 weights: the largest value scale so far sets the power of two
+        // 16 bits: the exponent of each token's largest value scale
+        float vexp[4];
         if (PARTS == 1) {
-            __half2 mx = *reinterpret_cast<const __half2*>(vsw);
 #pragma unroll
-            for (int i = 1; i < kNb * 2; ++i) mx = __hmax2(mx, *reinterpret_cast<const __half2*>(vsw + i));
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(&mx);
-            int e = static_cast<int>(max((v >> 10) & 31u, (v >> 26) & 31u)) - 14;     // scale < 2^e
-            if (__any_sync(0xffffffffu, e > vexp)) {
-                e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-                e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-                const float down = pow2i(vexp - e);
-                vexp = e;
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v = vsw[k * kNb / 2] & 0x7fff7fffu;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int c = 0; c < kNb; ++c)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) o[mt][c][x][i] *= down;
+                for (int i = 1; i < kNb / 2; ++i) v = __vmaxu2(v, vsw[k * kNb / 2 + i] & 0x7fff7fffu);
+                vexp[k] = static_cast<float>(static_cast<int>(max(v & 0xffffu, v >> 16) >> 10) - 14);
             }
         }
-        // scores to weights, which carry a power of two: 16 bits in the exponent's argument, f32 as a factor (an argument near 108 would have
+        // scores to weights, which carry a power of two: 16 bits 2^15 in the exponent's argument, f32 as a factor (an argument near 108 would have
         // steps of 2^-17)
-        const float lift = static_cast<float>(15 - vexp), lower = pow2i(vexp - 15);
         float P[MT][kSets][4];                                   // [row][token of the thread's four]
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -408,7 +396,10 @@ struct Tile {
             bool higher = false;
 #pragma unroll
             for (int set = 0; set < kSets; ++set) {
-                top[set] = fmaxf(fmaxf(P[mt][set][0], P[mt][set][1]), fmaxf(P[mt][set][2], P[mt][set][3]));
+                if (PARTS == 1)
+                    top[set] = fmaxf(fmaxf(P[mt][set][0] + vexp[0], P[mt][set][1] + vexp[1]), fmaxf(P[mt][set][2] + vexp[2], P[mt][set][3] + vexp[3]));
+                else
+                    top[set] = fmaxf(fmaxf(P[mt][set][0], P[mt][set][1]), fmaxf(P[mt][set][2], P[mt][set][3]));
                 higher |= top[set] > m[mt][set] + (PARTS == 1 ? 0.f : kSlack);
             }
             if (__any_sync(0xffffffffu, higher)) {
@@ -431,12 +422,12 @@ struct Tile {
             }
 #pragma unroll
             for (int set = 0; set < kSets; ++set) {
-                const float from = PARTS == 1 ? m[mt][set] - lift : m[mt][set];
+                const float from = PARTS == 1 ? m[mt][set] - 15.f : m[mt][set];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     const float x = ex2(P[mt][set][p] - from);
                     P[mt][set][p] = PARTS == 1 ? x : x * kLift;
-                    l[mt][set] = PARTS == 1 ? fmaf(x, lower, l[mt][set]) : l[mt][set] + x;
+                    l[mt][set] = PARTS == 1 ? fmaf(x, 0x1p-15f, l[mt][set]) : l[mt][set] + x;
                 }
             }
         }
@@ -519,7 +510,7 @@ struct Tile {
     __device__ __forceinline__ void put(int lane, bool norm, F&& store) const {
         const int g = lane >> 2, t = lane & 3;
         // 2^133 (2^24) for the codes, and the power of two of the weights
-        const float back = PARTS == 1 ? pow2i(9 + vexp) : 0x1p25f;
+        constexpr float back = PARTS == 1 ? 0x1p9f : 0x1p25f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

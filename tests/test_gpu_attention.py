@@ -158,3 +158,56 @@ def test_f32_sums_over_long_runs(gq, hd, heads, hkv, seqs, T, L):
     bias = 2 * 2.0 ** -23 + 2 * 2.0 ** -24
     assert abs(float(rel.mean())) <= bias, float(rel.mean())
     assert float(rel.square().mean().sqrt()) <= bias + 2.0 ** -24 * (L / 16 / 3) ** 0.5, float(rel.square().mean().sqrt())
+
+
+ROUND = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"f32": 0.0, "f16": 2.0 ** -25, "bf16": 0.0}               # half the distance of f16's subnormals
+
+
+def bound(kind, size, L, big, want):
+    """Of an output's error, `size` the largest sum |q k| of a score that its row sees.  A score: products of 22-bit (f32) or 11-bit parts, sums in f32; a
+    weight: the score's error twice, the exponential's and its own rounding; the sums over L keys; the output's rounding."""
+    if kind == "f32":
+        rel = 2 * size * 2.0 ** -19 + 2.0 ** -18 + (L / 16 + 64) * 2.0 ** -23
+    else:
+        rel = 2 * size * 2.0 ** -10 + 3 * 2.0 ** -11 + 2.0 ** -18 + (L / 16 + 64) * 2.0 ** -23
+    return rel * big + ROUND[kind] * want.abs() + 2 * TINY[kind]
+
+
+def one_large_value(gq, kind, spread, where, hd, T, heads, at=10):
+    """One token's values (and keys) are 2^spread times the others'; every row either gives it a weight of some 2^-100 or does not see it."""
+    L = 333
+    base = 2.0 ** (-6 if kind == "f16" else -12 if spread <= 32 else -17)      # (block scales of 2^-22, the smallest but two)
+    k, v, q = normal(1, L, 1, hd), base * normal(2, L, 1, hd), 0.5 * normal(3, T, heads, hd)
+    tree = None
+    seen = torch.arange(L, device="cuda")[None] <= L - T + torch.arange(T, device="cuda")[:, None]
+    if where == "hidden":
+        at = L - T                                                # the first of the newest tokens
+        k[at] *= 2.0 ** (spread // 2)
+        seen[:, at] = False
+        tree = torch.tensor([((2 << i) - 1) & ~1 for i in range(T)], dtype=torch.int64, device="cuda")
+    else:
+        q[..., 0] = q[..., 0].abs() + 8
+        k[..., 0] = 0
+        k[at] = 0
+        k[at, :, 0] = -200.0
+    v[at] *= 2.0 ** spread
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = q.to(TYPES[kind])
+    o = attend(gq, q, cache, table, L, tree_mask=tree)
+    want, big = exact(q, k, v, hd ** -0.5, seen=seen)
+    size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
+    if where != "hidden":
+        seen = seen.clone()
+        seen[:, at] = False                                       # its weight is nothing, whatever its score's error is
+    size = size.masked_fill(~seen[:, None], 0).amax(-1, keepdim=True)
+    err = (o.double() - want).abs() / bound(kind, size, L, big, want)
+    assert torch.all(err <= 1), float(err.max())
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("T,heads", [(1, 4), (1, 8), (5, 8)])
+@pytest.mark.parametrize("where", ["hidden", "faint"])
+@pytest.mark.parametrize("kind,spread", [("f32", 32), ("f32", 38), ("f16", 21), ("bf16", 24), ("bf16", 32), ("bf16", 38)])
+def test_one_large_value_few_rows(gq, kind, spread, where, hd, T, heads):
+    one_large_value(gq, kind, spread, where, hd, T, heads)
