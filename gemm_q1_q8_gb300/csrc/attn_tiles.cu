@@ -12,9 +12,16 @@
 // memory a 128 x 64 x 16 MMA reads 2 KB of shared memory instead of 6, which would bound it.
 // A code is the f16 subnormal magnitude * 2^-24 (attn.cu); times 2^15 it is normal, times the scale it is the value, rounded once to f16; and
 // fma(code, scale, -value) is the exact rest: two f16 parts hold all 18 bits.  f32 queries take two parts of everything and three
-// products (high x high, low x high, high x low): 2^-22 of a term.  16-bit queries take one part: 2^-11.  Powers of two keep the parts in f16's
-// range: a row's largest query at 2^14, a tile's largest key and value scale below 1, weights at 2^11 at most before kSlack; weights below 2^-36
-// of a row's largest are rounded absolutely (the row kernel keeps them).
+// products (high x high, low x high, high x low): 2^-22 of a term.  16-bit queries take one part: 2^-11.
+//
+// Powers of two keep the parts in f16's range.  A row's largest query goes to 2^14, its largest weight to 2^11 (2^15 before its maximum moves; a weight
+// is off by up to 2^-36 of it besides its bits, the row kernel keeps the faint ones).  A tile's keys are divided by 2^e, e the exponent of its
+// largest scale, its values by 2^ref, ref at most kAbove more than theirs; the sums are relative to ref and move with it, up or down, so what one tile
+// holds takes nothing of another's range.  Within a tile the tokens' exponents may differ by kNear: a key or value is then off by up to 2^-22 of its
+// token's largest besides its bits.  Where they differ by more, each token is divided by its own 2^e, which comes back on its column of scores and
+// in its weights, and each row's sums are relative to the largest product of a weight and 2^e that it sees (wide_tile): a token that a row does
+// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 596 us
+// (f32 below), 333 -> 346 (bf16); a call whose every tile is wide takes some 1.5 times as long.
 //
 // Keys' and values' orders are free where they are contracted: dims stand in the order in which a 16-byte unit of the cache holds them
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
@@ -45,6 +52,7 @@ constexpr int kRegsSoftmax = 136, kRegsKV = 72, kRegsRest = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsKV + kRegsRest == 5 * 96, "registers");
 constexpr int kBlocks = 152;                               // one thread block an SM
 constexpr float kLift = 11.f, kSlack = 4.f;
+constexpr int kNear = 12, kAbove = 3;              // how far the exponents of a tile's tokens may differ, and ref be above the values'
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 // f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
 // always towards zero, 12 times a tile: over 6144 tokens (48 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
@@ -127,44 +135,37 @@ __device__ __forceinline__ constexpr int token_of(int n) { return (n & ~15) + 2 
 __constant__ uint16_t kUpTo[16] = {0x0001, 0x0011, 0x0013, 0x0033, 0x0037, 0x0077, 0x007f, 0x00ff,
                                    0x01ff, 0x11ff, 0x13ff, 0x33ff, 0x37ff, 0x77ff, 0x7fff, 0xffff};
 
-// What a tile's scales need to get near 1: the exponent e of the largest finite one (all below 2^e), by a whole warp.  `edge`: only the
-// first `end` tokens, of the chunks in `have`, count.  `odd`: some scale is not finite (its bits are above every finite one's).
+// The exponents e of the scales of this lane's two tokens, columns lane and 32 + lane: the finite ones are below 2^e (-14 where all are subnormal or
+// 0).  -> that of the tile, also of tokens that are not `there`.  strange: the columns with a scale that is not finite.
 template <int HD>
-__device__ __forceinline__ int scales_exponent(const uint8_t* raw, int lane, bool edge, int end, int have, bool& odd) {
-    constexpr int kWords = kvGroup * (HD / 32) / 2, kPer = kGroups * kWords / 32;      // 32-bit words of a chunk's scales; a lane's
-    uint32_t w[kPer], top = 0;
+__device__ __forceinline__ int scale_exponents(const uint8_t* raw, int lane, const bool (&there)[2], int (&e)[2], uint32_t (&strange)[2]) {
+    constexpr int kNb = HD / 32;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int at = i * 32 + lane;
-        w[i] = *reinterpret_cast<const uint32_t*>(raw + (at / kWords) * kv_chunk_bytes(HD) + 4 * (at % kWords)) & 0x7fff7fffu;
-    }
-    if (edge) {
+    for (int half = 0; half < 2; ++half) {
+        const int n = 32 * half + lane;
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(raw + (n >> 4) * kv_chunk_bytes(HD) + 2 * (4 * (n & 3) + ((n >> 2) & 3)) * kNb);
+        uint32_t largest = 0;
+        bool odd = false;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = i * 32 + lane, grp = at / kWords, at4 = at % kWords / (HD / 64), t = at4 >> 2, p = at4 & 3;       // by 4 t + p
-            if (16 * grp + 2 * t + (p & 1) + 8 * (p >> 1) >= end || !(have >> grp & 1)) w[i] = 0;
+        for (int i = 0; i < kNb / 2; ++i) {
+            const uint32_t w = there[half] ? at[i] & 0x7fff7fffu : 0u, lo = w & 0xffffu, hi = w >> 16;
+            odd |= lo >= 0x7c00u || hi >= 0x7c00u;
+            largest = max(largest, max(lo < 0x7c00u ? lo : 0u, hi < 0x7c00u ? hi : 0u));
         }
+        e[half] = static_cast<int>(largest >> 10) - 14;
+        strange[half] = __ballot_sync(0xffffffffu, odd);
     }
+    const int top = __reduce_max_sync(0xffffffffu, max(e[0], e[1]));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) top = __vmaxu2(top, w[i]);
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-    odd = top >= 0x7c00u;
-    if (odd) {
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if ((w[i] & 0xffffu) < 0x7c00u) top = max(top, w[i] & 0xffffu);
-            if ((w[i] >> 16) < 0x7c00u) top = max(top, w[i] >> 16);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-    }
-    return static_cast<int>(top >> 10) - 14;
+    for (int half = 0; half < 2; ++half)
+        if (!there[half]) e[half] = top;
+    return top;
 }
-// 2^(9 - e) as the product of two f16 powers of two
-__device__ __forceinline__ void scale_factors(int e, __half2& f1, __half2& f2) {
-    const int x = 9 - e, y = x >> 1;                                      // -7 <= x <= 23
-    f1 = h2(static_cast<uint32_t>((15 + y) << 10) * 0x10001u);
-    f2 = h2(static_cast<uint32_t>((15 + x - y) << 10) * 0x10001u);
+// 2^(15 - e) as the product of two f16 powers of two (a scale below 2^e goes below 2^15, and with code * 2^-9 a value below 2^13)
+__device__ __forceinline__ void scale_factors(int e, uint32_t& f1, uint32_t& f2) {
+    const int x = 15 - e, y = x >> 1;                                     // -4 <= x <= 29
+    f1 = (15 + y) << 10;
+    f2 = (15 + x - y) << 10;
 }
 
 // Eight values (four pairs) as one or two parts: 16 bytes each
@@ -276,9 +277,11 @@ struct Piece {
 };
 
 struct Info {
-    int kexp;              // e of the keys' scales
-    int vexp;              // e of the values' scales
-    int have;              // a bit for each chunk whose page exists
+    uint2 kf[kTok];        // two factors (f16, twice) of a key's scales, by column (token)
+    uint16_t vf[2][kTok];  // two of a value's
+    // e of the keys, what the values were divided by, a bit for each chunk whose page exists, and whether each token was divided by its own 2^e:
+    alignas(16) int4 tile;
+    signed char ke[kTok], ve[kTok];                        // those
     int odd;               // whether some value scale is not finite:
     uint32_t bad[2];       // those tokens' columns
 };
@@ -287,13 +290,98 @@ struct Bars {
     uint32_t tmem;
     int abort;
     int have[2];
-    Info info[4];
+    alignas(16) Info info[4];
     float amax[2][kRows];                                  // of the groups' halves of the queries
     float m[2][kRows], l[2][kRows];                        // the groups' maxima and sums, at the end
     float kept[2][kRows];                                  // and the factor of the sums that left tensor memory
-    int vref[2][kRows];
+    int ref[2][kRows];
     Piece piece[4];                                        // a ring, filled by one warp; k1 = 0 ends it
 };
+
+// A row's softmax state: running maximum, sum relative to it, and the exponent that its sums of values are relative to
+struct RowState {
+    float m, l;
+    int ref;
+};
+// Which tokens of a tile from key j0 on a row sees
+struct Sees {
+    int j0, last, len, base;                               // last: causal, the last visible token (-1: none)
+    const uint64_t* mask;                                  // tree: the row's mask (NULL: causal)
+};
+// A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.
+// Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
+template <int HD, int PARTS, bool CAP>
+__device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info* info, float rs, float softcap, Sees sees, RowState row, bool sums) {
+    float top = -INFINITY, top_e = -INFINITY;
+    uint32_t y[16];
+    const unsigned long long bits = sees.mask ? *sees.mask : 0ull, bad = info->bad[0] | static_cast<unsigned long long>(info->bad[1]) << 32;
+#pragma unroll 1
+    for (int c = 0; c < kTok; c += 16) {
+        tc_ld16(cs + c, y);
+        tc_wait_ld();
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            float v = __uint_as_float(y[n]) * (rs * pow2i(info->ke[c + n]));
+            if (CAP) v = PARTS == 2 ? softcap * kLog2e * tanhf(v) : fmaf(-2.f * kLog2e * softcap, rcp(ex2(v) + 1.f), softcap * kLog2e);
+            const int key = sees.j0 + token_of(c + n), rel = key - sees.base;
+            bool seen = sees.last >= 0 && key < sees.len && (info->tile.z >> (c >> 4) & 1);
+            seen = seen && (sees.mask ? rel < 0 || (rel < 64 && (bits >> (rel & 63) & 1)) : key <= sees.last);
+            if (!seen) v = -INFINITY;
+            if (seen && (bad >> (c + n) & 1)) row.l = __int_as_float(0x7fc00000);
+            top = fmaxf(top, v);
+            top_e = fmaxf(top_e, v + static_cast<float>(info->ve[c + n]));
+            y[n] = __float_as_uint(v);
+        }
+        tc_st16(cs + c, y);
+    }
+    tc_wait_st();
+    const float m = top > row.m + kSlack ? top : row.m;
+    const int ref = static_cast<int>(fminf(fmaxf(ceilf(top_e - m), -16.f), 32.f));       // (no token at all, or scores that are not finite)
+    const float down = ex2(row.m - m), downo = down * pow2i(row.ref - ref);
+    if (sums)
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 16) {
+            tc_ld16(co + c, y);
+            tc_wait_ld();
+#pragma unroll
+            for (int n = 0; n < 16; ++n) y[n] = __float_as_uint(__uint_as_float(y[n]) * downo);
+            tc_st16(co + c, y);
+        }
+    // the weights' first half takes the first quarter of the scores' place, and of the third (their low parts): the second half is read before
+    uint32_t z[32];
+    tc_ld16(cs + 32, z);
+    tc_ld16(cs + 48, z + 16);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+        if (half == 0) {
+            tc_ld16(cs, w);
+            tc_ld16(cs + 16, w + 16);
+        } else {
+#pragma unroll
+            for (int n = 0; n < 32; ++n) w[n] = z[n];
+        }
+        tc_wait_ld();
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            const float x0 = __uint_as_float(w[2 * n]) - m, x1 = __uint_as_float(w[2 * n + 1]) - m;
+            sum += ex2(x0) + ex2(x1);
+            const float p0 = ex2(x0 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n] - ref)));
+            const float p1 = ex2(x1 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n + 1] - ref)));
+            const __half2 v = __floats2half2_rn(p0, p1);
+            hi[n] = u32(v);
+            if (PARTS == 2) {
+                const float2 f = __half22float2(v);
+                lo[n] = u32(__floats2half2_rn(p0 - f.x, p1 - f.y));
+            }
+        }
+        tc_st16(cs + 16 * half, hi);
+        if (PARTS == 2) tc_st16(cs + 32 + 16 * half, lo);
+    }
+    return {m, fmaf(row.l, down, sum), ref};
+}
 
 template <int HD, int PARTS> struct Smem {
     static constexpr int kRaw = kGroups * kv_chunk_bytes(HD);             // a tile's chunks
@@ -406,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;
             // the scale's sign goes into the queries, and a scale of 0 (equal weights) too: the scores' factor stays positive
             const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
-            rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * pow2i(-up);
+            rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * 0x1p-6f * pow2i(-up);    // 2^6 of the keys
 #pragma unroll
             for (int part = 0; part < kQ / 8; ++part) {
                 uint32_t hi[16], lo[16];
@@ -433,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (lane == 0) mbar_arrive(&bars->qfull);
         }
         const int last = in ? p.s.L - p.s.T + tok : -1;
-        float m = kNone, l = 0.f, m_kept = 0.f;                               // (m_kept, v_kept: what the drained sums are relative to)
-        int vref = -24, v_kept = 0;
+        float m = kNone, l = 0.f, m_kept = 0.f;                               // (m_kept, ref_kept: what the drained sums are relative to)
+        int ref = 0, ref_kept = 0;
         const int tiles = p.k1 - p.k0;
         for (int j = (it ^ wg) & 1; ok && j < tiles; j += 2) {                  // tile it + j of all, which is in this group's place
             const int i = it + j;
@@ -449,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const bool drain = PARTS == 2 && j >= 2 && (j >> 1) % kDrain == 0;
             if (drain) {
                 const bool first = j < 4 * kDrain;
-                const float f = ex2(m_kept - m) * pow2i(max(v_kept - vref, -126));
+                const float f = ex2(m_kept - m) * pow2i(ref_kept - ref);
                 float4* at = kept + (blockIdx.x * 2 + wg) * (HD / 4) * kRows + lr;
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 16) {
@@ -468,99 +556,111 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     }
                 }
                 m_kept = m;
-                v_kept = vref;
+                ref_kept = ref;
             }
             const Info& info = bars->info[i & 3];
-            float x_of = rs * pow2i(info.kexp);
-            const int vexp = info.vexp, have = info.have;
+            const int4 tile = info.tile;
+            const int have = tile.z, j0 = (p.k0 + j) * kTok;
             float x[kTok];
-            tc_ld32(cs, x);
-            tc_ld32(cs + 32, x + 32);
-            tc_wait_ld();
-            const int j0 = (p.k0 + j) * kTok;
-            if (CAP) {
+            auto load = [&]() {
+                tc_ld32(cs, x);
+                tc_ld32(cs + 32, x + 32);
+                tc_wait_ld();
+            };
+            if (!CAP) load();                                             // (capped scores: their code is better without them in registers here)
+            if (__builtin_expect(tile.w, 0)) {
+                const RowState row = wide_tile<HD, PARTS, CAP>(cs, co, &info, rs, a.softcap,
+                                                               {j0, in && a.tree ? 0 : last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
+                                                               {m, l, ref}, j >= 2 && !drain);
+                m = row.m;
+                l = row.l;
+                ref = row.ref;
+            } else {
+                float x_of = rs * pow2i(tile.x);
+                const int vn = tile.y;
+                if (CAP) {
+                    load();
 #pragma unroll
-                for (int n = 0; n < kTok; ++n) {
-                    // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
-                    const float y = x[n] * x_of;
-                    x[n] = PARTS == 2 ? a.softcap * kLog2e * tanhf(y) : fmaf(-2.f * kLog2e * a.softcap, rcp(ex2(y) + 1.f), a.softcap * kLog2e);
-                }
-                x_of = 1.f;
-            }
-            if (j0 + kTok > all_see || have != (1 << kGroups) - 1) {
-                const int len = p.s.len, base = p.s.L - p.s.T;
-                unsigned long long vis = 0;
-                if (!a.tree) {
-                    const int upto = min(last, len - 1) - j0;             // the last visible token of the tile
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        if (upto >= 16 * g && (have >> g & 1)) vis |= static_cast<unsigned long long>(kUpTo[min(upto - 16 * g, 15)]) << (16 * g);
-                } else {
-                    const unsigned long long bits = in ? a.tree[q0 + tok] : 0ull;
-#pragma unroll 1
                     for (int n = 0; n < kTok; ++n) {
-                        const int key = j0 + token_of(n), rel = key - base;
-                        const bool v = in && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
-                        vis |= static_cast<unsigned long long>(v) << n;
+                        // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
+                        const float y = x[n] * x_of;
+                        x[n] = PARTS == 2 ? a.softcap * kLog2e * tanhf(y) : fmaf(-2.f * kLog2e * a.softcap, rcp(ex2(y) + 1.f), a.softcap * kLog2e);
                     }
+                    x_of = 1.f;
                 }
-                const uint32_t vis0 = static_cast<uint32_t>(vis), vis1 = static_cast<uint32_t>(vis >> 32);
+                if (j0 + kTok > all_see || have != (1 << kGroups) - 1) {
+                    const int len = p.s.len, base = p.s.L - p.s.T;
+                    unsigned long long vis = 0;
+                    if (!a.tree) {
+                        const int upto = min(last, len - 1) - j0;             // the last visible token of the tile
 #pragma unroll
-                for (int n = 0; n < kTok; ++n)
-                    if (!((n < 32 ? vis0 : vis1) >> (n & 31) & 1u)) x[n] = -INFINITY;
-            }
-            float top = x[0];
-#pragma unroll
-            for (int n = 1; n < kTok; ++n) top = fmaxf(top, x[n]);
-            top *= x_of;
-            if (__any_sync(0xffffffffu, top > m + kSlack || vexp > vref)) {
-                const float mn = top > m + kSlack ? top : m;
-                const int vn = max(vexp, vref);
-                const float down = ex2(m - mn), downo = down * pow2i(max(vref - vn, -126));
-                l *= down;
-                m = mn;
-                vref = vn;
-                if (j >= 2 && !drain) {
+                        for (int g = 0; g < kGroups; ++g)
+                            if (upto >= 16 * g && (have >> g & 1)) vis |= static_cast<unsigned long long>(kUpTo[min(upto - 16 * g, 15)]) << (16 * g);
+                    } else {
+                        const unsigned long long bits = in ? a.tree[q0 + tok] : 0ull;
 #pragma unroll 1
-                    for (int c = 0; c < HD; c += 16) {
-                        uint32_t o[16];
-                        tc_ld16(co + c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * downo);
-                        tc_st16(co + c, o);
+                        for (int n = 0; n < kTok; ++n) {
+                            const int key = j0 + token_of(n), rel = key - base;
+                            const bool v = in && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
+                            vis |= static_cast<unsigned long long>(v) << n;
+                        }
                     }
-                }
-            }
-            const float from = m - kLift - static_cast<float>(vexp - vref), lower = pow2i(vref - vexp) * 0x1p-11f;
-            if (info.odd) {                                               // a value that is not finite, seen by this row
-                const unsigned long long bad = info.bad[0] | static_cast<unsigned long long>(info.bad[1]) << 32;
+                    const uint32_t vis0 = static_cast<uint32_t>(vis), vis1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-                for (int n = 0; n < kTok; ++n)
-                    if ((bad >> n & 1) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
-            }
-            float sum0 = 0.f, sum1 = 0.f;
+                    for (int n = 0; n < kTok; ++n)
+                        if (!((n < 32 ? vis0 : vis1) >> (n & 31) & 1u)) x[n] = -INFINITY;
+                }
+                float top = x[0];
+#pragma unroll
+                for (int n = 1; n < kTok; ++n) top = fmaxf(top, x[n]);
+                top *= x_of;
+                if (__any_sync(0xffffffffu, top > m + kSlack || vn != ref)) {
+                    const float mn = top > m + kSlack ? top : m, down = ex2(m - mn), downo = down * pow2i(ref - vn);
+                    l *= down;
+                    m = mn;
+                    ref = vn;
+                    if (j >= 2 && !drain) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {                        // (half the code)
-                uint32_t hi[16], lo[16];
+                        for (int c = 0; c < HD; c += 16) {
+                            uint32_t o[16];
+                            tc_ld16(co + c, o);
+                            tc_wait_ld();
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    const float p0 = ex2(fmaf(x[2 * n], x_of, -from)), p1 = ex2(fmaf(x[2 * n + 1], x_of, -from));
-                    sum0 += p0;
-                    sum1 += p1;
-                    const __half2 v = __floats2half2_rn(p0, p1);
-                    hi[n] = u32(v);
-                    if (PARTS == 2) {
-                        const float2 f = __half22float2(v);
-                        lo[n] = u32(__floats2half2_rn(p0 - f.x, p1 - f.y));
+                            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * downo);
+                            tc_st16(co + c, o);
+                        }
                     }
                 }
-                tc_st16(cs + 16 * half, hi);
-                if (PARTS == 2) tc_st16(cs + 32 + 16 * half, lo);
+                const float from = m - kLift;
+                if (info.odd) {                                               // a value that is not finite, seen by this row
+                    const unsigned long long bad = info.bad[0] | static_cast<unsigned long long>(info.bad[1]) << 32;
 #pragma unroll
-                for (int n = 0; n < 32; ++n) x[n] = x[32 + n];
+                    for (int n = 0; n < kTok; ++n)
+                        if ((bad >> n & 1) && x[n] > -INFINITY) l = __int_as_float(0x7fc00000);
+                }
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {                        // (half the code)
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) {
+                        const float p0 = ex2(fmaf(x[2 * n], x_of, -from)), p1 = ex2(fmaf(x[2 * n + 1], x_of, -from));
+                        sum0 += p0;
+                        sum1 += p1;
+                        const __half2 v = __floats2half2_rn(p0, p1);
+                        hi[n] = u32(v);
+                        if (PARTS == 2) {
+                            const float2 g = __half22float2(v);
+                            lo[n] = u32(__floats2half2_rn(p0 - g.x, p1 - g.y));
+                        }
+                    }
+                    tc_st16(cs + 16 * half, hi);
+                    if (PARTS == 2) tc_st16(cs + 32 + 16 * half, lo);
+#pragma unroll
+                    for (int n = 0; n < 32; ++n) x[n] = x[32 + n];
+                }
+                l = fmaf(sum0 + sum1, 0x1p-11f, l);
             }
-            l = fmaf(sum0 + sum1, lower, l);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -575,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         if (more) request(bars->piece[(pi + 1) & 3]);
         bars->m[wg][lr] = !ok ? __int_as_float(0x7fc00000) : has ? m : kNone;
         bars->l[wg][lr] = has ? l : 0.f;
-        bars->vref[wg][lr] = vref;
-        if (PARTS == 2) bars->kept[wg][lr] = ex2(m_kept - m) * pow2i(max(v_kept - vref, -126));
+        bars->ref[wg][lr] = ref;
+        if (PARTS == 2) bars->kept[wg][lr] = ex2(m_kept - m) * pow2i(ref_kept - ref);
         meet();
         {
             tc_fence_after();
@@ -585,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const bool has0 = tiles > 1 || !((it - 1) & 1), has1 = tiles > 1 || ((it - 1) & 1);      // a group without tiles has no sums
             const bool whole = p.k0 == 0 && p.k1 == p.all, head = p.k1 == p.all;
             const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            const float a0 = f0 * pow2i(bars->vref[0][lr] - 11) * inv, a1 = f1 * pow2i(bars->vref[1][lr] - 11) * inv;
+            const float a0 = f0 * pow2i(bars->ref[0][lr] - 17) * inv, a1 = f1 * pow2i(bars->ref[1][lr] - 17) * inv;    // 2^11 of the weights, 2^6 of the values
             T* out = static_cast<T*>(a.out) + (q0 + tok) * a.out_stride + (hk * group + h) * HD + wg * (HD / 2);
             // whether a group's sums have been drained: it had more than kDrain tiles, every other one from its first on
             const int begin0 = (it - tiles) & 1;
@@ -647,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         const int k_src = (k_tok >> 4) * kChunk + k_in * HD + k_up * 16;
         const int k_scale = (k_tok >> 4) * kChunk + kv_ks_offset(HD) + 2 * ((4 * k_tt + k_p) * kNb + 2 * (k_u >> 2));
         const bool k_swap = HD > 64 ? (k_u >> 2) & 1 : k_in & 1;          // the two chunks of a unit in this order: a store's chunks differ in their banks
-        const int k_dst = (k_u >> 2) * (kTok * 128) + static_cast<int>(swz128((k_tok & ~15) + 4 * k_p + k_tt, 2 * (k_u & 3) + (k_swap ? 1 : 0)));
+        const int k_col = (k_tok & ~15) + 4 * k_p + k_tt;
+        const int k_dst = (k_u >> 2) * (kTok * 128) + static_cast<int>(swz128(k_col, 2 * (k_u & 3) + (k_swap ? 1 : 0)));
         // and of the values: four dims 32 v_c + 4 v_g .. of eight tokens
         const int v_g = HD == 64 ? (lane >> 1) & 7 : lane >> 2, v_c = HD == 64 ? lane & 1 : lane & 3;
         const int v_src = kv_v_offset(HD) + (w8 & 1) * 8 * HD + 4 * v_c, v_scale = kv_vs_offset(HD) + 2 * (2 * (w8 & 1) * kNb + v_c);
@@ -662,15 +763,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             __syncwarp();
             const uint8_t* raw = sraw + s * M::kRaw;
             const Info& info = bars->info[i & 3];
-            const int have = info.have, j0 = kt * kTok, len = bars->piece[pi & 3].s.len, ve = info.vexp;
+            const int have = info.tile.z, j0 = kt * kTok, len = bars->piece[pi & 3].s.len;
             const bool odd = info.odd;
             const bool edge = j0 + kTok > len || have != (1 << kGroups) - 1;      // some of the tile's tokens do not exist
             // keys, once the scores of the tile before the last are done
             if (i >= 2 && !(ok = wait_for(&bars->qk[s], par ^ 1, abort))) break;
             __syncwarp();
             {
-                __half2 f1, f2;
-                scale_factors(info.kexp, f1, f2);
                 // a thread has one 16-byte unit of one token in every 128 / units tokens
                 uint4 w[kUnitsPer];
                 uint32_t sc[kUnitsPer];
@@ -681,11 +780,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     sc[k] = *reinterpret_cast<const uint32_t*>(ch + k_scale);
                     if (edge && (j0 + k_tok + kStep * k >= len || !(have >> ((k_tok + kStep * k) >> 4) & 1))) sc[k] = 0;
                 }
+#pragma unroll
+                for (int k = 0; k < kUnitsPer; ++k) {
+                    const uint2 f = info.kf[k_col + kStep * k];
+                    sc[k] = u32(__hmul2(__hmul2(h2(sc[k]), h2(f.x)), h2(f.y)));
+                }
                 uint8_t* dst = sk + s * PARTS * M::kK;
 #pragma unroll
                 for (int k = 0; k < kUnitsPer; ++k) {
-                    const __half2 s0 = __hmul2(__hmul2(h2(__byte_perm(sc[k], 0, k_swap ? 0x3232 : 0x1010)), f1), f2);
-                    const __half2 s1 = __hmul2(__hmul2(h2(__byte_perm(sc[k], 0, k_swap ? 0x1010 : 0x3232)), f1), f2);
+                    const __half2 s0 = h2(__byte_perm(sc[k], 0, k_swap ? 0x3232 : 0x1010)), s1 = h2(__byte_perm(sc[k], 0, k_swap ? 0x1010 : 0x3232));
                     const uint32_t wa = k_swap ? w[k].z : w[k].x, wb = k_swap ? w[k].w : w[k].y, wc = k_swap ? w[k].x : w[k].z,
                                    wd = k_swap ? w[k].y : w[k].w;
                     const uint32_t ca[4] = {codes2(wa, 0, 0x1100), codes2(wa, 0, 0x3322), codes2(wb, 0, 0x1100), codes2(wb, 0, 0x3322)};
@@ -702,8 +805,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (i >= 2 && !(ok = wait_for(&bars->pv[s], par ^ 1, abort))) break;
             __syncwarp();
             {
-                __half2 f1, f2;
-                scale_factors(ve, f1, f2);
                 uint8_t* dst = sv + s * PARTS * M::kV;
 #pragma unroll
                 for (int j = 0; j < kTok / 8 / kNumKV; ++j) {             // octets w8, w8 + kNumKV ..
@@ -728,7 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                     }
                     __half2 sh[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sh[k] = __hmul2(__hmul2(h2(sc[2 * k] | sc[2 * k + 1] << 16), f1), f2);
+                    for (int k = 0; k < 4; ++k) sh[k] = h2(sc[2 * k] | sc[2 * k + 1] << 16);
+                    const uint4 f1 = *reinterpret_cast<const uint4*>(info.vf[0] + 8 * (w8 + kNumKV * j)), f2 = *reinterpret_cast<const uint4*>(info.vf[1] + 8 * (w8 + kNumKV * j));
+                    sh[0] = __hmul2(__hmul2(sh[0], h2(f1.x)), h2(f2.x));
+                    sh[1] = __hmul2(__hmul2(sh[1], h2(f1.y)), h2(f2.y));
+                    sh[2] = __hmul2(__hmul2(sh[2], h2(f1.z)), h2(f2.z));
+                    sh[3] = __hmul2(__hmul2(sh[3], h2(f1.w)), h2(f2.w));
 #pragma unroll
                     for (int x = 0; x < (HD == 64 ? 2 : 4); ++x) {
                         const int e = HD == 64 ? 2 * (lane >> 4) + ((x + v_c) & 1) : (x + v_c) & 3;      // a store's chunks differ in their banks
@@ -843,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
     } else if (warp == kWarpMma + 3) {
         // ---------------- the run's pieces, a piece ahead, and the exponents of a tile's scales
         Piece now, then;
-        int i = 0, pi = 0;                                                // tiles so far, pieces
+        int i = 0, pi = 0, ref = -14;                                     // tiles so far, pieces, what values are divided by
         bool more = then.first(a, lane), ok = true;
         auto publish = [&](int n) {                                       // `then`, or the end
             if (n >= 4 && !wait_for(&bars->piecefree[n & 3], ((n >> 2) & 1) ^ 1, abort)) ok = false;
@@ -865,29 +971,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             __syncwarp();
             const uint8_t* raw = sraw + s * M::kRaw;
             const int have = bars->have[s], left = now.s.len - kt * kTok;
-            const bool edge = left < kTok || have != (1 << kGroups) - 1;
-            bool odd = false;
-            int ke = 0, ve = 0;
-#pragma unroll 1
-            for (int what = 0; what < 2; ++what) {                        // keys, then values
-                ke = ve;
-                ve = scales_exponent<HD>(raw + (what ? kv_vs_offset(HD) : kv_ks_offset(HD)), lane, edge, left, have, odd);
-            }
             Info& info = bars->info[i & 3];
-            if (odd)                                                      // which tokens: columns lane, 32 + lane
-                for (int half = 0; half < 2; ++half) {
-                    const int n = 32 * half + lane, grp = n >> 4, pp = (n >> 2) & 3, t = n & 3;
-                    bool strange = false;
-                    for (int c = 0; c < kNb; ++c)
-                        strange |= (*reinterpret_cast<const uint16_t*>(raw + grp * kChunk + kv_vs_offset(HD) + 2 * ((4 * t + pp) * kNb + c)) & 0x7c00) == 0x7c00;
-                    const uint32_t mask = __ballot_sync(0xffffffffu, strange);
-                    if (lane == 0) info.bad[half] = mask;
-                }
+            uint32_t bad[2];
+            int ke[2], ve[2];
+            bool there[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = 32 * half + lane;
+                there[half] = token_of(n) < left && (have >> (n >> 4) & 1);
+            }
+            const int kexp = scale_exponents<HD>(raw + kv_ks_offset(HD), lane, there, ke, bad);
+            const int vexp = scale_exponents<HD>(raw + kv_vs_offset(HD), lane, there, ve, bad);
+            const bool wide = __any_sync(0xffffffffu, kexp - min(ke[0], ke[1]) > kNear || vexp - min(ve[0], ve[1]) > kNear);
+            if (vexp > ref || vexp < ref - kAbove) ref = vexp;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = 32 * half + lane;
+                uint32_t f1, f2;
+                scale_factors(wide ? ke[half] : kexp, f1, f2);
+                info.kf[n] = make_uint2(f1 * 0x10001u, f2 * 0x10001u);
+                scale_factors(wide ? ve[half] : ref, f1, f2);
+                info.vf[0][n] = static_cast<uint16_t>(f1);
+                info.vf[1][n] = static_cast<uint16_t>(f2);
+                info.ke[n] = static_cast<signed char>(ke[half]);
+                info.ve[n] = static_cast<signed char>(ve[half]);
+            }
+            __syncwarp();
             if (lane == 0) {
-                info.kexp = ke;
-                info.vexp = ve;
-                info.have = have;
-                info.odd = odd;
+                info.tile = make_int4(kexp, ref, have, wide);
+                info.odd = bad[0] | bad[1];
+                info.bad[0] = bad[0];
+                info.bad[1] = bad[1];
                 mbar_arrive(&bars->expfull[s]);
             }
         }

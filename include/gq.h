@@ -504,10 +504,13 @@ int gq_kv_read(const void* cache_device, int pages, int page_size, int kv_heads,
  *   share it must not overlap on the GPU.  Nothing of it is kept between calls.  Results do not depend on
  *   timing: the same inputs give the same bits.
  * Precision: sums and statistics are in f32, codes are exact.  f32 queries take two f16 parts after a row's scaling by a
- * power of two, and the softmax's numerators three bf16 parts; f16 and bf16 queries take one f16 part of both.  From 256
- * (f32) or 128 (f16, bf16) rows a kv head on (max_q * q_heads / kv_heads; head_dim 64 and 128) keys, values and numerators
- * take two f16 parts (one): numerators below 2^-36 of a row's largest are then rounded absolutely, and a row that sees a
- * value whose scale is not finite is NaN.
+ * power of two, and the softmax's numerators three bf16 parts; f16 and bf16 queries take one f16 part of both, the numerators
+ * times the values' scales (off by up to 2^-40 of a row's largest such product besides their 11 bits).  From 256 (f32) or 128
+ * (f16, bf16) rows a kv head on (max_q * q_heads / kv_heads; head_dim 64 and 128) keys, values and numerators take two f16 parts
+ * (one): a numerator is off by up to 2^-36 of its row's largest besides its 22 (11) bits, a key or value by 2^-22 of its token's
+ * largest, and a row that sees a value whose scale is not finite is NaN.  Where the scales of 64 neighbouring tokens differ by
+ * more than 2^12, 2^-36 is of the row's largest product of a numerator and its token's largest scale.  What a token that a row does
+ * not see holds does not matter to any of this.
  * Errors: GQ_EINVAL_SHAPE unless 1 <= seqs <= 65535, max_q >= 1, max_kv >= 1, q_heads a multiple of kv_heads with
  *         q_heads / kv_heads <= 64, a valid cache shape, strides >= q_heads * head_dim, table_stride >=
  *         ceil(max_kv / page_size), scale finite, softcap >= 0 and finite, and max_q <= 64 with tree_mask_device;

@@ -1,5 +1,5 @@
-"""Attention over the Q8_0 cache where it can go wrong, against the formula in 64 bits: row numbers outside the call, and the precision of f32
-queries."""
+"""Attention over the Q8_0 cache where it can go wrong, against the formula in 64 bits: row numbers outside the call, precision, and values of very
+different sizes."""
 import ctypes
 
 import numpy as np
@@ -174,7 +174,7 @@ def bound(kind, size, L, big, want):
     return rel * big + ROUND[kind] * want.abs() + 2 * TINY[kind]
 
 
-def one_large_value(gq, kind, spread, where, hd, T, heads, at=10):
+def one_large_value(gq, kind, spread, where, hd, T, heads, at=10, cap=0.0):
     """One token's values (and keys) are 2^spread times the others'; every row either gives it a weight of some 2^-100 or does not see it."""
     L = 333
     base = 2.0 ** (-6 if kind == "f16" else -12 if spread <= 32 else -17)      # (block scales of 2^-22, the smallest but two)
@@ -194,8 +194,8 @@ def one_large_value(gq, kind, spread, where, hd, T, heads, at=10):
     v[at] *= 2.0 ** spread
     cache, table, [(k, v)] = cached(gq, [k], [v])
     q = q.to(TYPES[kind])
-    o = attend(gq, q, cache, table, L, tree_mask=tree)
-    want, big = exact(q, k, v, hd ** -0.5, seen=seen)
+    o = attend(gq, q, cache, table, L, tree_mask=tree, softcap=cap)
+    want, big = exact(q, k, v, hd ** -0.5, seen=seen, cap=cap)
     size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
     if where != "hidden":
         seen = seen.clone()
@@ -211,3 +211,70 @@ def one_large_value(gq, kind, spread, where, hd, T, heads, at=10):
 @pytest.mark.parametrize("kind,spread", [("f32", 32), ("f32", 38), ("f16", 21), ("bf16", 24), ("bf16", 32), ("bf16", 38)])
 def test_one_large_value_few_rows(gq, kind, spread, where, hd, T, heads):
     one_large_value(gq, kind, spread, where, hd, T, heads)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("where", ["hidden", "faint", "faint and late"])
+@pytest.mark.parametrize("kind,spread", [("f32", 3), ("f32", 16), ("f32", 24), ("f32", 32), ("f16", 21), ("bf16", 24), ("bf16", 32), ("bf16", 38)])
+def test_one_large_value_many_rows(gq, kind, spread, where, hd, cap):
+    """As above with rows enough for the tensor-core tiles: keys and values of a tile share an exponent only where their own are near."""
+    one_large_value(gq, kind, spread, where, hd, 40, 8, at=292 if where == "faint and late" else 10, cap=cap)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("kind,spread", [("f32", 4), ("f32", 14), ("f16", 14), ("bf16", 20)])
+def test_many_rows_blocks_of_different_sizes(gq, kind, spread, hd):
+    """Every token's first 32 values are 2^spread times the others', its keys by turns; the tokens themselves differ too."""
+    L, T, heads = 300, 40, 8
+    size = torch.exp2(torch.arange(L, device="cuda") * 5 % 7 - 3.0)[:, None, None]
+    k, v, q = 0.1 * normal(1, L, 1, hd), 2.0 ** -8 * size * normal(2, L, 1, hd), normal(3, T, heads, hd)
+    v[..., :32] *= 2.0 ** spread
+    k[::2, :, 32:] *= 2.0 ** -spread
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = q.to(TYPES[kind])
+    o = attend(gq, q, cache, table, L)
+    want, big = exact(q, k, v, hd ** -0.5)
+    size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
+    err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
+    assert torch.all(err <= 1), float(err.max())
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_many_rows_tiles_of_different_sizes(gq, kind, hd):
+    """Runs of 64 tokens whose values are by turns 2^-12 to 2^10 of the others': the large ones' weights are nothing, so that what is left is the small
+    ones', after sums that have gone up and down with them (f32: some of them have left tensor memory)."""
+    L, T, heads = 64 * 44 + 7, 40, 8
+    run = torch.arange(L, device="cuda") // 64
+    power = torch.tensor([0, -4, 10, 0, 3, -12, 0, 8], device="cuda")[run % 8]
+    k, v, q = normal(1, L, 1, hd), torch.exp2(power - 3.0)[:, None, None] * normal(2, L, 1, hd), 0.5 * normal(3, T, heads, hd)
+    q[..., 0] = q[..., 0].abs() + 8
+    k[..., 0] = torch.where(power <= 0, 0.0, -100.0)[:, None]
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = q.to(TYPES[kind])
+    o = attend(gq, q, cache, table, L)
+    want, big = exact(q, k, v, hd ** -0.5)
+    faint = (power > 0)[None, None]
+    size = (torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5).masked_fill(faint, 0)
+    err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
+    assert torch.all(err <= 1), float(err.max())
+
+
+@pytest.mark.parametrize("spread", [9, 11, 12, 13, 14, 18])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_many_rows_around_the_limit_of_a_tile(gq, kind, spread):
+    """Tokens' keys and values that differ by about as much as a tile's may share an exponent, all of them with weight; the last tile is not full."""
+    L, T, heads, hd = 1000, 40, 8, 128
+    j = torch.arange(L, device="cuda")
+    large = (j % 7 == 3)[:, None, None]
+    k, v, q = 0.1 * normal(1, L, 1, hd), normal(2, L, 1, hd), normal(3, T, heads, hd)
+    k, v = torch.where(large, k, k * 2.0 ** -spread), torch.where(large, v * 2.0 ** -spread, v)
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = q.to(TYPES[kind])
+    for cap in (0.0, 20.0):
+        o = attend(gq, q, cache, table, L, softcap=cap)
+        want, big = exact(q, k, v, hd ** -0.5, cap=cap)
+        size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
+        err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
+        assert torch.all(err <= 1), float(err.max())
