@@ -392,7 +392,8 @@ enum gq_dtype { GQ_F32 = 0, GQ_F16 = 1, GQ_BF16 = 2 };
 #define GQ_DEVERR_INDEX 8   /* bit of gq_device_error(): an index read from device memory was out of range */
 
 /* RMS norm with the residual's addition, and an output in Q8_0:
- *   h = x + r (r = 0 if residual_device is NULL), y_i = (h_i * w_i) * (1 / sqrt(sum h^2 / k + eps)).
+ *   h = x + r (r = 0 if residual_device is NULL), y_i = (h_i * (1 / sqrt(sum h^2 / k + eps))) * w_i, each step
+ *   rounded to f32 (the sum's order is not stated).
  *   x_device [m, k] of `type`, rows x_stride elements apart (x_stride >= k); residual_device NULL or
  *   [m, k], rows residual_stride apart; weight_device k f32.  Any output may be NULL, not all of them:
  *     sum_device  [m, k] of `type`, contiguous: h; it may be x_device or residual_device itself if
