@@ -634,7 +634,7 @@ def rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cac
                    rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
                    q_out: torch.Tensor | None = None):
     """Turns q and k by rows `positions` (int32 [n]) of `rope` ([rows, rot/2, 2] f32; None: no rotation), and writes k and
-    v to `slots` (int64 [n], negative: skipped) of the cache.  q [n, q_heads, hd] (or None), k, v [n, kv_heads, hd];
+    v to `slots` (int64 [n], negative: skipped; no two tokens with one slot) of the cache.  q [n, q_heads, hd] (or None), k, v [n, kv_heads, hd];
     views of one fused row serve.  Returns the turned q (q_out, which may be q)."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise GQError("k: expected a CUDA tensor [n, kv_heads, head_dim]")

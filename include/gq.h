@@ -463,7 +463,8 @@ enum gq_rope_layout { GQ_ROPE_HALF = 0, GQ_ROPE_INTERLEAVED = 1 };
  *   itself, with the same stride); both NULL where q_heads = 0.  k_device, v_device [tokens, kv_heads, head_dim];
  *   heads are contiguous, tokens the given strides (in elements) apart, so that one fused q | k | v row serves.
  *   slots_device[n] (int64): where token n goes; a negative one is not written.  Two tokens with one slot in
- *   a call leave either's values.
+ *   a call leave that slot unspecified: words of both may be mixed there, a code of one beside a scale of the other, and not
+ *   the same ones every time.  Other slots are as they should be.
  *   A position outside [0, rope_rows) leaves that token's q_out and slot unwritten, a slot >= pages * page_size
  *   is not written; both set GQ_DEVERR_INDEX.
  *   k is quantized after the rotation, in f32.

@@ -278,3 +278,19 @@ def test_many_rows_around_the_limit_of_a_tile(gq, kind, spread):
         size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
         err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
         assert torch.all(err <= 1), float(err.max())
+
+
+def test_two_tokens_with_one_slot(gq):
+    """Of a slot that two tokens of a call name nothing is promised; all others hold their token."""
+    n, hkv, hd = 500, 4, 128
+    k, v = normal(1, n, hkv, hd), normal(2, n, hkv, hd)
+    a, b = gq.KVCacheQ8_0(32, 16, hkv, hd), gq.KVCacheQ8_0(32, 16, hkv, hd)
+    slots = torch.arange(n, device="cuda")
+    gq.rope_kv_append(None, k, v, a, slots)
+    twice = slots.clone()
+    twice[300] = 17
+    gq.rope_kv_append(None, k, v, b, twice)
+    others = slots[(slots != 17) & (slots != 300)]
+    for x, y in zip(gq.kv_read(a, others), gq.kv_read(b, others)):
+        assert torch.equal(x, y)
+    assert gq.device_error() == 0
