@@ -364,15 +364,18 @@ struct Tile {
                     P[mt][set][p] = x * row[mt][set].rs;
                 }
             if (a.softcap > 0.f) {
-                // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
                 const float cap = a.softcap * kLog2e;
+                if (PARTS == 1 && a.softcap > kCapNear) {
 #pragma unroll
-                for (int set = 0; set < kSets; ++set)
+                    for (int set = 0; set < kSets; ++set)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const float x = P[mt][set][p];
-                        P[mt][set][p] = PARTS > 1 ? cap * tanhf(x) : fmaf(-2.f * cap, rcp(ex2(x) + 1.f), cap);
-                    }
+                        for (int p = 0; p < 4; ++p) P[mt][set][p] = capped16<true>(P[mt][set][p], cap);
+                } else {
+#pragma unroll
+                    for (int set = 0; set < kSets; ++set)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) P[mt][set][p] = PARTS > 1 ? cap * tanhf(P[mt][set][p]) : capped16<false>(P[mt][set][p], cap);
+                }
             }
             if (MASKED) {
 #pragma unroll

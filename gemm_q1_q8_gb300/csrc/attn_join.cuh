@@ -25,6 +25,18 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }    // -126 <= e <= 127
 
+// A capped score times log2 e, cap * tanh(y), for 16-bit queries; x = 2 y log2 e.  1 - 2 / (e^2y + 1) is off by some 2^-22 absolutely, which a cap above
+// kCapNear makes felt.  ANY takes every cap: below |y| = 1/4 the series of tanh (off by 2^-21 of itself).
+constexpr float kCapNear = 512.f;
+template <bool ANY>
+__device__ __forceinline__ float capped16(float x, float cap) {
+    const float far = fmaf(-2.f * cap, rcp(ex2(x) + 1.f), cap);
+    if (!ANY) return far;
+    const float y = x * 0.34657359f, z = y * y;
+    const float series = cap * y * fmaf(z, fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+    return fabsf(y) < 0.25f ? series : far;
+}
+
 // The query rows of sequence b.  q_start comes from device memory: rows outside [0, a.rows) are neither read nor written.
 struct QueryRows {
     int q0, T;             // first row, query tokens

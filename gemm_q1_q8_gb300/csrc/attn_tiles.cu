@@ -298,6 +298,12 @@ struct Bars {
     Piece piece[4];                                        // a ring, filled by one warp; k1 = 0 ends it
 };
 
+// A capped score; CAP 2: 16-bit queries, any cap
+template <int PARTS, int CAP>
+__device__ __forceinline__ float capped(float x, float cap) {
+    return PARTS == 2 ? cap * tanhf(x) : capped16<CAP == 2>(x, cap);
+}
+
 // A row's softmax state: running maximum, sum relative to it, and the exponent that its sums of values are relative to
 struct RowState {
     float m, l;
@@ -310,7 +316,7 @@ struct Sees {
 };
 // A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.
 // Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
-template <int HD, int PARTS, bool CAP>
+template <int HD, int PARTS, int CAP>
 __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info* info, float rs, float softcap, Sees sees, RowState row, bool sums) {
     float top = -INFINITY, top_e = -INFINITY;
     uint32_t y[16];
@@ -322,7 +328,7 @@ __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info*
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
             float v = __uint_as_float(y[n]) * (rs * pow2i(info->ke[c + n]));
-            if (CAP) v = PARTS == 2 ? softcap * kLog2e * tanhf(v) : fmaf(-2.f * kLog2e * softcap, rcp(ex2(v) + 1.f), softcap * kLog2e);
+            if (CAP) v = capped<PARTS, CAP>(v, softcap * kLog2e);
             const int key = sees.j0 + token_of(c + n), rel = key - sees.base;
             bool seen = sees.last >= 0 && key < sees.len && (info->tile.z >> (c >> 4) & 1);
             seen = seen && (sees.mask ? rel < 0 || (rel < 64 && (bits >> (rel & 63) & 1)) : key <= sees.last);
@@ -390,7 +396,7 @@ template <int HD, int PARTS> struct Smem {
     static constexpr int kAll = 1024 + kBars + sizeof(Bars);
 };
 
-template <typename T, int HD, int PARTS, bool CAP>
+template <typename T, int HD, int PARTS, int CAP>
 __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs a, const Parts parts, float4* kept) {
     using M = Smem<HD, PARTS>;
     constexpr int kChunk = kv_chunk_bytes(HD), kNb = HD / 32;
@@ -581,11 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 if (CAP) {
                     load();
 #pragma unroll
-                    for (int n = 0; n < kTok; ++n) {
-                        // tanh in f32 for f32 queries; 1 - 2 / (e^2x + 1), off by some 2^-23 absolutely, for 16-bit ones (their multiplier holds the 2 log2 e)
-                        const float y = x[n] * x_of;
-                        x[n] = PARTS == 2 ? a.softcap * kLog2e * tanhf(y) : fmaf(-2.f * kLog2e * a.softcap, rcp(ex2(y) + 1.f), a.softcap * kLog2e);
-                    }
+                    for (int n = 0; n < kTok; ++n) x[n] = capped<PARTS, CAP>(x[n] * x_of, a.softcap * kLog2e);
                     x_of = 1.f;
                 }
                 if (j0 + kTok > all_see || have != (1 << kGroups) - 1) {
@@ -1024,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
 // The workspace: the joining kernel's, then f32's drained sums [block][group][HD / 4][row] of four columns
 size_t kept_at(int hd) { return (parts_bytes(kBlocks, kRows, hd) + 255) / 256 * 256; }
 
-template <typename T, int HD, bool CAP>
+template <typename T, int HD, int CAP>
 cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, smem = Smem<HD, PARTS>::kAll;
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -1040,8 +1042,10 @@ cudaError_t tiles_go(const AttnArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t tiles_type(const AttnArgs& a, int head_dim, cudaStream_t s) {
-    if (a.softcap > 0.f) return head_dim == 64 ? tiles_go<T, 64, true>(a, s) : tiles_go<T, 128, true>(a, s);
-    return head_dim == 64 ? tiles_go<T, 64, false>(a, s) : tiles_go<T, 128, false>(a, s);
+    if constexpr (sizeof(T) == 2)
+        if (a.softcap > kCapNear) return head_dim == 64 ? tiles_go<T, 64, 2>(a, s) : tiles_go<T, 128, 2>(a, s);
+    if (a.softcap > 0.f) return head_dim == 64 ? tiles_go<T, 64, 1>(a, s) : tiles_go<T, 128, 1>(a, s);
+    return head_dim == 64 ? tiles_go<T, 64, 0>(a, s) : tiles_go<T, 128, 0>(a, s);
 }
 
 }  // namespace

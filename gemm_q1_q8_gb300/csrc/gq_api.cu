@@ -372,6 +372,10 @@ static int attn_call(const void* q, long long q_stride, void* out, long long out
     if (!aligned(q, 4 * b) || !aligned(out, 4 * b) || q_stride % 4 || out_stride % 4 || !aligned(cache, 16) ||
         !aligned(workspace, 16) || !aligned(table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(tree, 8))
         return GQ_EINVAL_PTR;
+    // a cap that no score comes near is none, and below the other bound all weights are equal in f32: products of either with the scale could
+    // leave f32's range
+    if (softcap > 1e20f) softcap = 0.0f;
+    if (softcap > 0.0f && softcap < 1e-30f) softcap = 1e-30f;
     const gq::AttnArgs a = {q, out, q_stride, out_stride, static_cast<const uint8_t*>(cache), pages, page_size, table,
                             table_stride, kv_len, q_start, tree, rows, seqs, max_q, max_kv, q_heads, kv_heads, scale, softcap,
                             workspace};

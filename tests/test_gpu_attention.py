@@ -294,3 +294,18 @@ def test_two_tokens_with_one_slot(gq):
     for x, y in zip(gq.kv_read(a, others), gq.kv_read(b, others)):
         assert torch.equal(x, y)
     assert gq.device_error() == 0
+
+
+@pytest.mark.parametrize("hd,T,heads", [(128, 1, 8), (64, 4, 8), (256, 5, 8), (128, 40, 8), (64, 40, 8)])
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cap", [3e-38, 400.0, 600.0, 3e4, 1e6, 1e9, 3e38])
+def test_caps_of_any_size(gq, kind, cap, hd, T, heads):
+    """A cap that is large beside the scores leaves them as they are, however large it is; a tiny one makes all weights equal."""
+    L = 200
+    cache, table, [(k, v)] = cached(gq, [normal(1, L, 1, hd)], [normal(2, L, 1, hd)])
+    q = normal(3, T, heads, hd).to(TYPES[kind])
+    o = attend(gq, q, cache, table, L, softcap=cap)
+    want, big = exact(q, k, v, hd ** -0.5, cap=cap)
+    size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
+    err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
+    assert torch.all(err <= 1), float(err.max())
