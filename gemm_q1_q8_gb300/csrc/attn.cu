@@ -216,8 +216,9 @@ struct Queries {
                 const bool in = r < s.rows;
                 const int tok = in ? r / group : 0;
                 RowInfo ri;
-                // 2^24 for the codes, 2^-up for the query
-                ri.rs = (a.softcap <= 0.f ? a.scale * kLog2e : a.scale / a.softcap * (PARTS > 1 ? 1.f : 2.f * kLog2e)) * 16777216.f * pow2i(-up);
+                // 2^24 for the codes, 2^-up for the query; finite for queries near f32's largest value too, whose scores stay in their order
+                const float rs = (a.softcap <= 0.f ? a.scale * kLog2e : a.scale / a.softcap * (PARTS > 1 ? 1.f : 2.f * kLog2e)) * 16777216.f * pow2i(-up);
+                ri.rs = fminf(fmaxf(rs, -0x1p127f), 0x1p127f);
                 ri.last = in ? s.L - s.T + tok : -1;
                 const unsigned long long bits = a.tree && in ? a.tree[s.q0 + tok] : 0ull;
                 ri.bits0 = static_cast<uint32_t>(bits);

@@ -10,7 +10,7 @@
 namespace gq {
 namespace {
 
-constexpr float kNone = -1e30f;                    // running maximum of a row that has seen no key
+constexpr float kNone = -3e38f;                    // running maximum of a row that has seen no key, below every finite score
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {

@@ -279,7 +279,7 @@ struct Piece {
 struct Info {
     uint2 kf[kTok];        // two factors (f16, twice) of a key's scales, by column (token)
     uint16_t vf[2][kTok];  // two of a value's
-    // e of the keys, what the values were divided by, a bit for each chunk whose page exists, and whether each token was divided by its own 2^e:
+    // e of the keys, ref of the values, a bit for each chunk whose page exists, and whether each token was divided by its own 2^e instead:
     alignas(16) int4 tile;
     signed char ke[kTok], ve[kTok];                        // those
     int odd;               // whether some value scale is not finite:
@@ -314,12 +314,16 @@ struct Sees {
     int j0, last, len, base;                               // last: causal, the last visible token (-1: none)
     const uint64_t* mask;                                  // tree: the row's mask (NULL: causal)
 };
-// A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.
-// Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
+// A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.  Also one
+// with scores beyond 2^20: the common way subtracts the maximum from products that are not rounded, as the maximum was, and past 2^24 the
+// difference counts.  Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
 template <int HD, int PARTS, int CAP>
 __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info* info, float rs, float softcap, Sees sees, RowState row, bool sums) {
     float top = -INFINITY, top_e = -INFINITY;
     uint32_t y[16];
+    const int4 tile = info->tile;
+    auto ke = [&](int n) { return tile.w ? info->ke[n] : tile.x; };
+    auto ve = [&](int n) { return tile.w ? info->ve[n] : tile.y; };
     const unsigned long long bits = sees.mask ? *sees.mask : 0ull, bad = info->bad[0] | static_cast<unsigned long long>(info->bad[1]) << 32;
 #pragma unroll 1
     for (int c = 0; c < kTok; c += 16) {
@@ -327,15 +331,15 @@ __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info*
         tc_wait_ld();
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-            float v = __uint_as_float(y[n]) * (rs * pow2i(info->ke[c + n]));
+            float v = __uint_as_float(y[n]) * (rs * pow2i(ke(c + n)));
             if (CAP) v = capped<PARTS, CAP>(v, softcap * kLog2e);
             const int key = sees.j0 + token_of(c + n), rel = key - sees.base;
-            bool seen = sees.last >= 0 && key < sees.len && (info->tile.z >> (c >> 4) & 1);
+            bool seen = sees.last >= 0 && key < sees.len && (tile.z >> (c >> 4) & 1);
             seen = seen && (sees.mask ? rel < 0 || (rel < 64 && (bits >> (rel & 63) & 1)) : key <= sees.last);
             if (!seen) v = -INFINITY;
             if (seen && (bad >> (c + n) & 1)) row.l = __int_as_float(0x7fc00000);
             top = fmaxf(top, v);
-            top_e = fmaxf(top_e, v + static_cast<float>(info->ve[c + n]));
+            top_e = fmaxf(top_e, v + static_cast<float>(ve(c + n)));
             y[n] = __float_as_uint(v);
         }
         tc_st16(cs + c, y);
@@ -374,8 +378,8 @@ __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info*
         for (int n = 0; n < 16; ++n) {
             const float x0 = __uint_as_float(w[2 * n]) - m, x1 = __uint_as_float(w[2 * n + 1]) - m;
             sum += ex2(x0) + ex2(x1);
-            const float p0 = ex2(x0 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n] - ref)));
-            const float p1 = ex2(x1 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n + 1] - ref)));
+            const float p0 = ex2(x0 + (kLift + static_cast<float>(ve(32 * half + 2 * n) - ref)));
+            const float p1 = ex2(x1 + (kLift + static_cast<float>(ve(32 * half + 2 * n + 1) - ref)));
             const __half2 v = __floats2half2_rn(p0, p1);
             hi[n] = u32(v);
             if (PARTS == 2) {
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         const bool in = r < p.s.rows;
         const int tok = in ? r / group : 0, h = in ? r % group : 0;
         float rs;
+        int far = 99;
         {
             float amax = 0.f;
 #pragma unroll
@@ -501,6 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             // the scale's sign goes into the queries, and a scale of 0 (equal weights) too: the scores' factor stays positive
             const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
             rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * 0x1p-6f * pow2i(-up);    // 2^6 of the keys
+            rs = fminf(fmaxf(rs, 0x1p-100f), 0x1p107f);                   // times a scale's power of two neither 0 nor infinite, for queries of any size
+            // the keys' exponent up to which no row's score here is beyond 2^20 (products of 2^15 and 2^13, 2^7 of them); the common way wants that
+            if (!CAP) far = -16 - (static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(rs)) >> 23) - 127);
 #pragma unroll
             for (int part = 0; part < kQ / 8; ++part) {
                 uint32_t hi[16], lo[16];
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 tc_wait_ld();
             };
             if (!CAP) load();                                             // (capped scores: their code is better without them in registers here)
-            if (__builtin_expect(tile.w, 0)) {
+            if (__builtin_expect(tile.w || tile.x > far, 0)) {
                 const RowState row = wide_tile<HD, PARTS, CAP>(cs, co, &info, rs, a.softcap,
                                                                {j0, in && a.tree ? 0 : last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
                                                                {m, l, ref}, j >= 2 && !drain);

@@ -309,3 +309,22 @@ def test_caps_of_any_size(gq, kind, cap, hd, T, heads):
     size = torch.einsum("thd,lhd->thl", q.double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
     err = (o.double() - want).abs() / bound(kind, size.amax(-1, keepdim=True), L, big, want)
     assert torch.all(err <= 1), float(err.max())
+
+
+@pytest.mark.parametrize("hd,T,heads", [(128, 1, 4), (128, 1, 8), (64, 4, 8), (256, 5, 8), (128, 40, 8), (64, 40, 8)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("size,scale,cap", [(-1e33, 1.0, 0.0), (-1e36, 0.1, 0.0), (1e36, 0.1, 0.0), (1e37, 0.01, 0.0), (1e-37, 1e-4, 0.0), (1e-30, 1e-20, 0.0),
+                                            (1e37, 0.01, 50.0), (1e-37, 1e-4, 50.0)])
+def test_queries_near_the_ends_of_the_range(gq, size, scale, cap, kind, hd, T, heads):
+    """Equal keys have equal weights, however large, small or negative the scores are (the largest ones' scores are finite); small keys besides."""
+    L = 200
+    for key in (1.0, 2.0 ** -14):
+        if abs(size) < 1:
+            key *= 2.0 ** -9                                      # the smallest block scales
+        cache, table, [(k, v)] = cached(gq, [torch.full((L, 1, hd), key, device="cuda")], [normal(2, L, 1, hd)])
+        q = torch.full((T, heads, hd), size, device="cuda").to(TYPES[kind])
+        o = attend(gq, q, cache, table, L, scale=scale, softcap=cap)
+        want = (v.double().cumsum(0)[L - T:] / (L - T + 1 + torch.arange(T, device="cuda"))[:, None, None]).expand(T, heads, hd)
+        big = (v.double().abs().cumsum(0)[L - T:] / (L - T + 1 + torch.arange(T, device="cuda"))[:, None, None]).expand(T, heads, hd)
+        err = (o.double() - want).abs() / bound(kind, 0.0, L, big, want)
+        assert torch.all(err <= 1), float(err.max())
