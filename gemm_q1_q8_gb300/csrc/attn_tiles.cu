@@ -20,8 +20,8 @@
 // holds takes nothing of another's range.  Within a tile the tokens' exponents may differ by kNear: a key or value is then off by up to 2^-22 of its
 // token's largest besides its bits.  Where they differ by more, each token is divided by its own 2^e, which comes back on its column of scores and
 // in its weights, and each row's sums are relative to the largest product of a weight and 2^e that it sees (wide_tile): a token that a row does
-// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 596 us
-// (f32 below), 333 -> 346 (bf16); a call whose every tile is wide takes some 1.5 times as long.
+// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 599 us
+// (f32 below), 333 -> 345 (bf16); a call whose every tile is wide takes some 1.5 times as long.
 //
 // Keys' and values' orders are free where they are contracted: dims stand in the order in which a 16-byte unit of the cache holds them
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
@@ -53,6 +53,7 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsKV + kRegsRest == 5 * 96, "registers")
 constexpr int kBlocks = 152;                               // one thread block an SM
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr int kNear = 12, kAbove = 3;              // how far the exponents of a tile's tokens may differ, and ref be above the values'
+constexpr int kOwn = 100;                          // in the place of a tile's exponent: each token has its own
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 // f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
 // always towards zero, 12 times a tile: over 6144 tokens (48 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
@@ -279,7 +280,8 @@ struct Piece {
 struct Info {
     uint2 kf[kTok];        // two factors (f16, twice) of a key's scales, by column (token)
     uint16_t vf[2][kTok];  // two of a value's
-    // e of the keys, ref of the values, a bit for each chunk whose page exists, and whether each token was divided by its own 2^e instead:
+    // e of the keys, ref of the values, a bit for each chunk whose page exists, and whether each token was divided by its own 2^e instead (then
+    // kOwn for that of the keys):
     alignas(16) int4 tile;
     signed char ke[kTok], ve[kTok];                        // those
     int odd;               // whether some value scale is not finite:
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
         const bool in = r < p.s.rows;
         const int tok = in ? r / group : 0, h = in ? r % group : 0;
         float rs;
-        int far = 99;
+        int far = kOwn - 1;
         {
             float amax = 0.f;
 #pragma unroll
@@ -581,8 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                 tc_ld32(cs + 32, x + 32);
                 tc_wait_ld();
             };
-            if (!CAP) load();                                             // (capped scores: their code is better without them in registers here)
-            if (__builtin_expect(tile.w || tile.x > far, 0)) {
+            constexpr bool kEarly = !CAP && !(PARTS == 2 && HD == 128);   // (these spill more with the scores in registers at the branch: 606 against 599 us)
+            if (kEarly) load();
+            if (__builtin_expect(tile.x > far, 0)) {
                 const RowState row = wide_tile<HD, PARTS, CAP>(cs, co, &info, rs, a.softcap,
                                                                {j0, in && a.tree ? 0 : last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
                                                                {m, l, ref}, j >= 2 && !drain);
@@ -592,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             } else {
                 float x_of = rs * pow2i(tile.x);
                 const int vn = tile.y;
+                if (!kEarly) load();
                 if (CAP) {
-                    load();
 #pragma unroll
                     for (int n = 0; n < kTok; ++n) x[n] = capped<PARTS, CAP>(x[n] * x_of, a.softcap * kLog2e);
                     x_of = 1.f;
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             }
             __syncwarp();
             if (lane == 0) {
-                info.tile = make_int4(kexp, ref, have, wide);
+                info.tile = make_int4(wide ? kOwn : kexp, ref, have, wide);
                 info.odd = bad[0] | bad[1];
                 info.bad[0] = bad[0];
                 info.bad[1] = bad[1];
