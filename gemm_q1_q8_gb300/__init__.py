@@ -606,6 +606,7 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "
     if scaling not in ROPE_SCALING:
         raise GQError(f"rope_table: unknown scaling {scaling!r}")
     t = torch.empty((max(positions, 0), max(rot, 0) // 2, 2), dtype=torch.float32, device=device)
+    _need(t, torch.float32, t.numel(), "device")
     _check(lib().gq_rope_table(_at(t), positions, rot, base, ROPE_SCALING[scaling], factor, original, _on(t)),
            "gq_rope_table")
     return t

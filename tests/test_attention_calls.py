@@ -70,3 +70,10 @@ def test_on_every_device_of_a_process(fake_runtime, call):
     r = subprocess.run([sys.executable, "-c", ON_DEVICES, fake_runtime, build.LIB, call], env=dict(os.environ, LD_PRELOAD=fake_runtime),
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_rope_table_on_the_host_is_refused():
+    """A kernel is never given a host address."""
+    import gemm_q1_q8_gb300 as gq
+    with pytest.raises(gq.GQError, match="expected a CUDA tensor"):
+        gq.rope_table(4, 64, device="cpu")
