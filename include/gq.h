@@ -496,6 +496,7 @@ int gq_kv_read(const void* cache_device, int pages, int page_size, int kv_heads,
  *     tree_mask_device is NULL: j <= i (causal);
  *     else: bit j of tree_mask_device[row of query i] is set (its drafted ancestors and itself; T <= 64).
  *   T > L is allowed (the first queries then see nothing, and give 0), T = 0 and L = 0 too.
+ *   T * (q_heads / kv_heads) * L of a sequence stays below 2^44.
  *   max_q and max_kv bound T and L of every sequence; a longer T or L, or a page index outside
  *   [0, pages), sets GQ_DEVERR_INDEX: what is past the bound is not computed or not seen.
  *   Row numbers are checked against [0, rows): gq_attn_q8_0_bounded is told how many rows q_device, out_device and
