@@ -44,6 +44,11 @@ constexpr int kBlocks = 152;                       // one thread block an SM
 
 constexpr float kLift = 0x1p108f;                  // f32 weights are multiplied by it: times a scale below 2^16 and 2^kSlack they stay in f32's range
 constexpr float kSlack = 2.f;                      // a score may pass the running maximum by this much before it moves: 1.02 (16 bits: 0)
+// f32: chunks after which a tile's sums leave the registers, for the workspace.  An MMA truncates the sum that it adds to, always towards zero: 1024
+// queries of 256 over 8192 tokens lost 6.7e-6 of the result, in plain f32 its error is 1.2e-6.  Every 16 / 32 / 64 chunks 2.7 / 2.1 / 2.0e-7 are lost at any
+// length, for 110.9 / 109.1 / 108.2 us of 32 ragged sequences instead of 106.3 (each chunk's sums added outside the MMA: 110.8, and 8 sequences of 64
+// rows 248 instead of 214 us).
+constexpr int kDrain = 64;
 // Rows of a tile by the parts of its operands: 16-bit queries 1; f32 2, or 3 for up to four rows
 template <int PARTS, int MT> __host__ __device__ constexpr int tile_rows() { return PARTS == 1 ? 16 * MT : PARTS == 2 ? 8 * MT : 4; }
 // Computing warps, by the registers that a warp's sums take, and the chunks of a warp's ring
@@ -250,12 +255,20 @@ struct Queries {
 template <typename T, int HD, int PARTS, int MT>
 struct Tile {
     using Q = Queries<T, HD, PARTS, MT>;
-    static constexpr int kKs = HD / 16, kNb = HD / 32, kSets = Q::kSets;
+    static constexpr int kKs = HD / 16, kNb = HD / 32, kSets = Q::kSets, kKeepers = PARTS == 3 ? 16 : 32;
+    static constexpr float kEmpty = INFINITY;
     float o[MT][kNb][4][4];
     float m[MT][kSets], l[MT][kSets];
     RowInfo row[MT][kSets];
+    // f32: what left the registers, relative to 2^m_kept, this thread's part of the run's place in the workspace
+    float4* kept;
+    float m_kept[MT];
 
     __device__ __forceinline__ void start(const RowInfo* info, int lane) {
+        if (PARTS > 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) m_kept[mt] = kEmpty;
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -495,17 +508,58 @@ struct Tile {
                     if (PARTS == 1) {
                         mma16816(o[mt][c][e], pa[mt], b0, b1);
                     } else {
-                        // an MMA truncates the sum that it adds to, always towards zero, so the chunks' sums are added outside: a mean loss of 7.2e-6 of
-                        // the result after 512 chunks is gone, for 106.3 -> 110.8 us of 32 ragged sequences (with the low rows left in the MMA, whose
-                        // registers then move, 121)
-                        float z[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (PARTS == 2) mma16816_bf16(z, low[mt][0], 0u, low[mt][1], 0u, b0, b1);
-                        mma16816_bf16(z, pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[mt][c][e][i] += z[i];
+                        mma16816_bf16(o[mt][c][e], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b0, b1);
+                        if (PARTS == 2) mma16816_bf16(o[mt][c][e], low[mt][0], 0u, low[mt][1], 0u, b0, b1);
                     }
                 }
             }
+        }
+    }
+
+    // The two float4 of block c: columns 8t .. and 8t + 4 .. of the row, its parts added
+    __device__ __forceinline__ void sums(int mt, int c, int set, int g, float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = o[mt][c][e][2 * set + i];
+                if (PARTS == 2 || (PARTS == 3 && g < 4)) x += o[mt][c][e][2 + i];
+                if (PARTS == 3) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                v[4 * i + e] = x;
+            }
+    }
+    __device__ __forceinline__ void add_kept(int mt, int c, float f, float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 k = kept[((mt * kNb + c) * 2 + i) * kKeepers];
+            v[4 * i] = fmaf(k.x, f, v[4 * i]);
+            v[4 * i + 1] = fmaf(k.y, f, v[4 * i + 1]);
+            v[4 * i + 2] = fmaf(k.z, f, v[4 * i + 2]);
+            v[4 * i + 3] = fmaf(k.w, f, v[4 * i + 3]);
+        }
+    }
+    // f32: the sums go to the workspace
+    __device__ __forceinline__ void drain(int lane) {
+        const int g = lane >> 2;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const bool before = m_kept[mt] != kEmpty;
+            const float f = ex2(m_kept[mt] - m[mt][0]);
+#pragma unroll
+            for (int c = 0; c < kNb; ++c) {
+                float v[8];
+                sums(mt, c, 0, g, v);
+                if (lane < kKeepers) {
+                    if (before) add_kept(mt, c, f, v);
+                    kept[(mt * kNb + c) * 2 * kKeepers] = make_float4(v[0], v[1], v[2], v[3]);
+                    kept[((mt * kNb + c) * 2 + 1) * kKeepers] = make_float4(v[4], v[5], v[6], v[7]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][c][e][i] = 0.f;
+            }
+            m_kept[mt] = m[mt][0];
         }
     }
 
@@ -526,15 +580,11 @@ struct Tile {
 #pragma unroll
                 for (int c = 0; c < kNb; ++c) {
                     float v[8];
+                    sums(mt, c, set, g, v);
+                    if (PARTS > 1)
+                        if (m_kept[mt] != kEmpty && lane < kKeepers) add_kept(mt, c, ex2(m_kept[mt] - m[mt][set]), v);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x = o[mt][c][e][2 * set + i];
-                            if (PARTS == 2 || (PARTS == 3 && g < 4)) x += o[mt][c][e][2 + i];
-                            if (PARTS == 3) x += __shfl_xor_sync(0xffffffffu, x, 16);
-                            v[4 * i + e] = x * f;
-                        }
+                    for (int i = 0; i < 8; ++i) v[i] *= f;
                     if (PARTS != 3 || g < 4) {
                         store(Q::row_of(mt, set, g), 32 * c + 8 * t, make_float4(v[0], v[1], v[2], v[3]), m[mt][set], sum);
                         store(Q::row_of(mt, set, g), 32 * c + 8 * t + 4, make_float4(v[4], v[5], v[6], v[7]), m[mt][set], sum);
@@ -672,6 +722,8 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
     long long open_at = -1;
     if (count) {
         TileT tile;
+        // until the block's warps meet, the place of the run's tail is free for its own sums
+        if (PARTS > 1) tile.kept = reinterpret_cast<float4*>(parts.o + (static_cast<size_t>(kRunsAll) + run) * kRows * HD) + lane;
         uint64_t* full = &bars[warp * kNst];
         const uint8_t* ring_w = ring + warp * kNst * kChunk;
         int slot = 0;
@@ -698,23 +750,27 @@ __global__ void __launch_bounds__((warps<HD, MT>() + 1) * 32, 1) attn_rows_kerne
             // units from here on hold new tokens, or the end
             const int old = min(p.s.L - p.s.T, a.max_kv), masked = old > 0 ? old / kvGroup : 0;
             done += end - p.g;
-            for (int i = p.g; i < end; ++i) {
-                if (!wait_for(&full[slot], phase, &abort)) {
-                    ok = false;
-                    break;
+            for (int i = p.g, until;;) {
+                for (until = PARTS > 1 ? min(end, i + kDrain) : end; i < until; ++i) {
+                    if (!wait_for(&full[slot], phase, &abort)) {
+                        ok = false;
+                        break;
+                    }
+                    __syncwarp();
+                    const uint8_t* ch = ring_w + slot * kChunk;
+                    if (i >= masked)
+                        tile.template unit<true>(a, p.s, ch, frag, i * kvGroup, have[warp][slot], lane);
+                    else if (have[warp][slot])
+                        tile.template unit<false>(a, p.s, ch, frag, 0, true, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[kWarps * kNst + slot]);
+                    if (++slot == kNst) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
-                __syncwarp();
-                const uint8_t* ch = ring_w + slot * kChunk;
-                if (i >= masked)
-                    tile.template unit<true>(a, p.s, ch, frag, i * kvGroup, have[warp][slot], lane);
-                else if (have[warp][slot])
-                    tile.template unit<false>(a, p.s, ch, frag, 0, true, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[kWarps * kNst + slot]);
-                if (++slot == kNst) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                if (PARTS == 1 || !ok || i >= end) break;
+                tile.drain(lane);
             }
             if (!ok) break;
             if (end == p.s.units && begun_here) {                        // all of the tile

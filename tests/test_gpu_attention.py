@@ -328,3 +328,17 @@ def test_queries_near_the_ends_of_the_range(gq, size, scale, cap, kind, hd, T, h
         big = (v.double().abs().cumsum(0)[L - T:] / (L - T + 1 + torch.arange(T, device="cuda"))[:, None, None]).expand(T, heads, hd)
         err = (o.double() - want).abs() / bound(kind, 0.0, L, big, want)
         assert torch.all(err <= 1), float(err.max())
+
+
+def test_f32_error_over_long_runs(gq):
+    """As above with weights that differ: no loss to one side beyond what plain f32 has of either."""
+    T, L, heads, hd = 1024, 8192, 8, 256
+    k, v = 0.1 * normal(1, L, 1, hd), 1 + normal(2, L, 1, hd).abs()
+    cache, table, [(k, v)] = cached(gq, [k], [v], page=64)
+    q = normal(3, T, heads, hd)
+    o = attend(gq, q, cache, table, L)
+    want, _ = exact(q, k, v, hd ** -0.5)
+    # 64 chunks of two products, each truncated by 2^-24 on the average of a sum that grows, half of it on the average; the scores' 32 products likewise, of
+    # scores below 1/8
+    rel = (o.double() - want) / want
+    assert abs(float(rel.mean())) <= 64 * 2.0 ** -24 / 2 / 2 + 2.0 ** -24 and float(rel.square().mean().sqrt()) <= 64 * 2.0 ** -24 / 2
