@@ -5,9 +5,9 @@
 // The floor is the cache's bytes (17/16 a value) at the HBM rate; a row costs 4 flops a value, so up to some 16 rows
 // a read the matrix work hides behind the copy.
 //
-// Measured: one f32 token of 20 heads over 4096 tokens 11.6 us (latency: a chain of waits, ring, join); 32 f32 tokens over ragged 501 to 32768 tokens, 559 MB
-// of cache, 106 us (5.3 TB/s, 78% of the measured copy; a scheduler issues in 54% of its cycles, 490 instructions a chunk); 8 bf16 trees of 9 to 33 tokens
-// over 1111 to 9000 tokens 34 us (issue and latency: 490 instructions a chunk and 32 rows at 11 warps an SM, the cap's exponentials among them).
+// Measured: one f32 token of 20 heads over 4096 tokens 11.8 us (latency: a chain of waits, ring, join); 32 f32 tokens over ragged 501 to 32768 tokens, 559 MB
+// of cache, 108 us (5.2 TB/s, 76% of the measured copy; a scheduler issues in 55% of its cycles, 490 instructions a chunk); 8 bf16 trees of 9 to 33 tokens
+// over 1111 to 9000 tokens 35 us (issue and latency: 490 instructions a chunk and 32 rows at 11 warps an SM, the cap's exponentials among them).
 //
 // Work: the unit is one 16-token chunk of one (sequence, kv head, row tile); the units of the whole call, in that order, are cut
 // into equal runs of consecutive units, one a warp of every SM, whatever the sequences' lengths.  A warp goes through its run alone: it
@@ -36,8 +36,8 @@ GQ_ERROR_ACCESSOR(attn)
 namespace {
 
 // Rows a kv head (max_q tokens times its query heads) from which attn_tiles.cu takes the call.  32 query and 8 kv heads of 128, 8 sequences of
-// 8192 tokens, this kernel against that one: f32 64 rows 214 / 130 us, 256 rows 820 / 246; bf16 64 rows 108 / 84, 128 rows 200 / 91, 16 rows
-// 39 / 79.  16 bits: from one full 128-row tile, since max_q only bounds the rows (8 ragged trees of 27 to 99 rows: 34 / 52 us).  f32: from
+// 8192 tokens, this kernel against that one: f32 64 rows 214 / 136 us, 256 rows 805 / 249; bf16 64 rows 105 / 83, 128 rows 191 / 90, 16 rows
+// 39 / 79.  16 bits: from one full 128-row tile, since max_q only bounds the rows (8 ragged trees of 27 to 99 rows: 35 / 45 us).  f32: from
 // two tiles only, because up to there a weight below 2^-36 of the largest still counts here.
 constexpr int many_rows(int type) { return type == GQ_F32 ? 256 : 128; }
 constexpr int kBlocks = 152;                       // one thread block an SM
