@@ -2,9 +2,9 @@
 //
 // Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
 // keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
-// Measured (2048 queries of 32 heads of 128 over 6144 tokens with them, 8 kv heads): f32 598 us (287 TFLOP/s of the formula, 862 of MMAs; 274 us at the
-// measured rate), bf16 345 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
-// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 4070, of which a scheduler
+// Measured (2048 queries of 32 heads of 128 over 6144 tokens with them, 8 kv heads): f32 596 us (288 TFLOP/s of the formula, 864 of MMAs; 274 us at the
+// measured rate), bf16 341 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
+// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 4050, of which a scheduler
 // issues in 1710: the rest is the chain scores - softmax - sums, the pieces' ends, and the drains below.
 //
 // Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
@@ -20,8 +20,8 @@
 // holds takes nothing of another's range.  Within a tile the tokens' exponents may differ by kNear: a key or value is then off by up to 2^-22 of its
 // token's largest besides its bits.  Where they differ by more, each token is divided by its own 2^e, which comes back on its column of scores and
 // in its weights, and each row's sums are relative to the largest product of a weight and 2^e that it sees (wide_tile): a token that a row does
-// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 598 us
-// (f32 below), 333 -> 345 (bf16); with every other tile wide the f32 chunk takes 850.
+// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 596 us
+// (f32 below), 333 -> 341 (bf16); with every other tile wide the f32 chunk takes 850.
 //
 // Keys' and values' orders are free where they are contracted: dims stand in the order in which a 16-byte unit of the cache holds them
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
@@ -57,7 +57,7 @@ constexpr int kOwn = 100;                          // in the place of a tile's e
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 // f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
 // always towards zero, 12 times a tile: over 6144 tokens (48 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
-// 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543 (every 8 tiles 598 us since, see above).
+// 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543 (every 8 tiles 596 us since, see above).
 // 16 bits (4 MMAs a tile) lose half of f16's last place at some 400,000 tokens: not drained (the code alone would cost 4-6%, by its registers).
 constexpr int kDrain = 8;
 
@@ -510,7 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * 0x1p-6f * pow2i(-up);    // 2^6 of the keys
             rs = fminf(fmaxf(rs, 0x1p-100f), 0x1p107f);                   // times a scale's power of two neither 0 nor infinite, for queries of any size
             // the keys' exponent up to which no row's score here is beyond 2^20 (products of 2^15 and 2^13, 2^7 of them); the common way wants that
-            if (!CAP) far = -16 - (static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(rs)) >> 23) - 127);
+            // (rows of zeros, rows past the end among them, have no scores, and those that are not finite no order)
+            if (!CAP) {
+                const uint32_t most = __reduce_max_sync(0xffffffffu, amax > 0.f && e < 128 ? __float_as_uint(rs) : 0u);
+                far = min(-16 - (static_cast<int>(most >> 23) - 127), kOwn - 1);
+            }
 #pragma unroll
             for (int part = 0; part < kQ / 8; ++part) {
                 uint32_t hi[16], lo[16];
