@@ -313,7 +313,7 @@ struct RowState {
 };
 // Which tokens of a tile from key j0 on a row sees
 struct Sees {
-    int j0, last, len, base;                               // last: causal, the last visible token (-1: none)
+    int j0, last, len, base;                               // last: the row's own place (negative: it sees nothing)
     const uint64_t* mask;                                  // tree: the row's mask (NULL: causal)
 };
 // A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.  Also one
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (kEarly) load();
             if (__builtin_expect(tile.x > far, 0)) {
                 const RowState row = wide_tile<HD, PARTS, CAP>(cs, co, &info, rs, a.softcap,
-                                                               {j0, in && a.tree ? 0 : last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
+                                                               {j0, last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
                                                                {m, l, ref}, j >= 2 && !drain);
                 m = row.m;
                 l = row.l;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
 #pragma unroll 1
                         for (int n = 0; n < kTok; ++n) {
                             const int key = j0 + token_of(n), rel = key - base;
-                            const bool v = in && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
+                            const bool v = last >= 0 && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
                             vis |= static_cast<unsigned long long>(v) << n;
                         }
                     }

@@ -342,3 +342,19 @@ def test_f32_error_over_long_runs(gq):
     # scores below 1/8
     rel = (o.double() - want) / want
     assert abs(float(rel.mean())) <= 64 * 2.0 ** -24 / 2 / 2 + 2.0 ** -24 and float(rel.square().mean().sqrt()) <= 64 * 2.0 ** -24 / 2
+
+
+@pytest.mark.parametrize("hd,T,heads", [(128, 4, 1), (64, 5, 8), (256, 40, 8), (128, 40, 8), (64, 64, 8)])
+@pytest.mark.parametrize("kind,spread", [("f32", 0), ("bf16", 0), ("f32", 20)])
+def test_tree_of_more_tokens_than_are_cached(gq, kind, spread, hd, T, heads):
+    """The queries before the first cached token see nothing, whatever their masks say."""
+    L = T - 3
+    k, v = normal(1, L, 1, hd), normal(2, L, 1, hd)
+    v[L // 2] *= 2.0 ** -spread
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = normal(3, T, heads, hd).to(TYPES[kind])
+    o = attend(gq, q, cache, table, L, tree_mask=torch.full((T,), -1, dtype=torch.int64, device="cuda"))
+    assert torch.all(o[:3] == 0)
+    want, big = exact(q[3:], k, v, hd ** -0.5, seen=torch.ones(T - 3, L, dtype=torch.bool, device="cuda"))
+    size = torch.einsum("thd,lhd->thl", q[3:].double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
+    assert torch.all((o[3:].double() - want).abs() <= bound(kind, size.amax(-1, keepdim=True), L, big, want))
