@@ -70,7 +70,8 @@ __device__ __forceinline__ void div_mod(long long x, int d, int& quot, int& rest
 }
 
 // The workspace: partial sums [2][runs][rows][HD] (heads, tails) relative to 2^m, their m and l [2][runs][rows], and for each run the tile
-// whose end it has after an earlier run began it
+// whose end it has after an earlier run began it.  (The row kernel's f32 sums that leave the registers stand in their own run's tail, until its
+// block's open tiles meet.)
 struct Head {
     int first;             // the run that began the tile; -1: none
     int q0, tile0, rows, hk;

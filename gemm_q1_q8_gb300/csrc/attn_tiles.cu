@@ -2,9 +2,9 @@
 //
 // Mathematics as attn.cu: s = scale * q.k, o = sum 2^(s - m) v / sum 2^(s - m), rows (token * group + head) of one kv head, one pass over the
 // keys in tiles of 64.  Bound: the tensor cores, 4 * hd flops a visible pair (three times that for f32), and the softmax's exponentials.
-// Measured (2048 queries of 32 heads of 128 over 6144 tokens with them, 8 kv heads): f32 596 us (288 TFLOP/s of the formula, 864 of MMAs; 274 us at the
-// measured rate), bf16 341 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
-// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 4050, of which a scheduler
+// Measured (2048 queries of 32 heads of 128 over 6144 tokens with them, 8 kv heads): f32 603 us (285 TFLOP/s of the formula, 855 of MMAs; 274 us at the
+// measured rate), bf16 343 us.  A 64-token score MMA holds the tensor core for 48 cycles, a 128-token one for 64, so a tile's MMAs take 1920 cycles
+// in f32 (128-token tiles would need 1536, and tensor memory that the queries and sums fill); a tile takes 4100, of which a scheduler
 // issues in 1710: the rest is the chain scores - softmax - sums, the pieces' ends, and the drains below.
 //
 // Operands (kind::f16, f32 sums): the queries (A) and the weights (A) lie in tensor memory, written there by the softmax's threads, a row a
@@ -20,8 +20,8 @@
 // holds takes nothing of another's range.  Within a tile the tokens' exponents may differ by kNear: a key or value is then off by up to 2^-22 of its
 // token's largest besides its bits.  Where they differ by more, each token is divided by its own 2^e, which comes back on its column of scores and
 // in its weights, and each row's sums are relative to the largest product of a weight and 2^e that it sees (wide_tile): a token that a row does
-// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 596 us
-// (f32 below), 333 -> 341 (bf16); with every other tile wide the f32 chunk takes 850.
+// not see, or that has no weight there, takes nothing of the others' range either, whatever its scale is.  The common way pays for that with 581 -> 603 us
+// (f32 below), 333 -> 343 (bf16); with every other tile wide the chunk takes 706 (414).
 //
 // Keys' and values' orders are free where they are contracted: dims stand in the order in which a 16-byte unit of the cache holds them
 // (the queries' too), tokens in the order of the cache's value rows (the score columns too), so both conversions go from words to 16-byte
@@ -57,7 +57,7 @@ constexpr int kOwn = 100;                          // in the place of a tile's e
 constexpr int kColS = 0, kColQ = 128, kColO = 256, kTmemCols = 512;        // scores (weights) 2 x 64, queries 128, sums 2 x 128
 // f32: a group's sums leave tensor memory every kDrain of its tiles, for f32 sums in the workspace.  An MMA truncates the sum that it adds to,
 // always towards zero, 12 times a tile: over 6144 tokens (48 tiles a group) the result lost 9.8e-6 of itself, against 1.7e-6 in plain f32.  Every
-// 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543 (every 8 tiles 596 us since, see above).
+// 4 / 8 / 16 tiles, with the small products of the scores first: 1.5e-6 / 2.3e-6 / 3.8e-6, at any length, for 619 / 581 / 563 us instead of 543 (every 8 tiles 603 us since, see above).
 // 16 bits (4 MMAs a tile) lose half of f16's last place at some 400,000 tokens: not drained (the code alone would cost 4-6%, by its registers).
 constexpr int kDrain = 8;
 
@@ -317,31 +317,42 @@ struct Sees {
     const uint64_t* mask;                                  // tree: the row's mask (NULL: causal)
 };
 // A tile whose tokens have exponents of their own, from its scores to its weights, as the common way does it below, with the e of each column.  Also one
-// with scores beyond 2^20: the common way subtracts the maximum from products that are not rounded, as the maximum was, and past 2^24 the
-// difference counts.  Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
+// whose scores may pass 2^23: the common way subtracts the maximum from products that are not rounded, as the maximum was, and up to there the
+// difference is 1/2 at most.  Sixteen columns at a time, and not inlined: the common way keeps its registers and its code small.
 template <int HD, int PARTS, int CAP>
 __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info* info, float rs, float softcap, Sees sees, RowState row, bool sums) {
     float top = -INFINITY, top_e = -INFINITY;
     uint32_t y[16];
     const int4 tile = info->tile;
-    auto ke = [&](int n) { return tile.w ? info->ke[n] : tile.x; };
-    auto ve = [&](int n) { return tile.w ? info->ve[n] : tile.y; };
-    const unsigned long long bits = sees.mask ? *sees.mask : 0ull, bad = info->bad[0] | static_cast<unsigned long long>(info->bad[1]) << 32;
+    const unsigned long long bad = info->bad[0] | static_cast<unsigned long long>(info->bad[1]) << 32;
+    unsigned long long vis = 0;                            // the columns that the row sees
+    if (!sees.mask) {
+        const int upto = min(sees.last, sees.len - 1) - sees.j0;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            if (upto >= 16 * g && (tile.z >> g & 1)) vis |= static_cast<unsigned long long>(kUpTo[min(upto - 16 * g, 15)]) << (16 * g);
+    } else {
+        const unsigned long long bits = *sees.mask;
+#pragma unroll 1
+        for (int n = 0; n < kTok; ++n) {
+            const int key = sees.j0 + token_of(n), rel = key - sees.base;
+            const bool v = key < sees.len && (tile.z >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && (bits >> (rel & 63) & 1)));
+            vis |= static_cast<unsigned long long>(v) << n;
+        }
+    }
+    if (vis & bad) row.l = __int_as_float(0x7fc00000);
 #pragma unroll 1
     for (int c = 0; c < kTok; c += 16) {
         tc_ld16(cs + c, y);
         tc_wait_ld();
+        const uint32_t now = static_cast<uint32_t>(vis >> c);
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-            float v = __uint_as_float(y[n]) * (rs * pow2i(ke(c + n)));
+            float v = __uint_as_float(y[n]) * (rs * pow2i(info->ke[c + n]));
             if (CAP) v = capped<PARTS, CAP>(v, softcap * kLog2e);
-            const int key = sees.j0 + token_of(c + n), rel = key - sees.base;
-            bool seen = sees.last >= 0 && key < sees.len && (tile.z >> (c >> 4) & 1);
-            seen = seen && (sees.mask ? rel < 0 || (rel < 64 && (bits >> (rel & 63) & 1)) : key <= sees.last);
-            if (!seen) v = -INFINITY;
-            if (seen && (bad >> (c + n) & 1)) row.l = __int_as_float(0x7fc00000);
+            if (!(now >> n & 1)) v = -INFINITY;
             top = fmaxf(top, v);
-            top_e = fmaxf(top_e, v + static_cast<float>(ve(c + n)));
+            top_e = fmaxf(top_e, v + static_cast<float>(info->ve[c + n]));
             y[n] = __float_as_uint(v);
         }
         tc_st16(cs + c, y);
@@ -380,8 +391,8 @@ __device__ __noinline__ RowState wide_tile(uint32_t cs, uint32_t co, const Info*
         for (int n = 0; n < 16; ++n) {
             const float x0 = __uint_as_float(w[2 * n]) - m, x1 = __uint_as_float(w[2 * n + 1]) - m;
             sum += ex2(x0) + ex2(x1);
-            const float p0 = ex2(x0 + (kLift + static_cast<float>(ve(32 * half + 2 * n) - ref)));
-            const float p1 = ex2(x1 + (kLift + static_cast<float>(ve(32 * half + 2 * n + 1) - ref)));
+            const float p0 = ex2(x0 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n] - ref)));
+            const float p1 = ex2(x1 + (kLift + static_cast<float>(info->ve[32 * half + 2 * n + 1] - ref)));
             const __half2 v = __floats2half2_rn(p0, p1);
             hi[n] = u32(v);
             if (PARTS == 2) {
@@ -509,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             const float f = !in || a.scale == 0.f ? 0.f : copysignf(pow2i(up), a.scale), size = a.scale == 0.f ? 1.f : fabsf(a.scale);
             rs = (!CAP ? size * kLog2e : size / a.softcap * (PARTS == 2 ? 1.f : 2.f * kLog2e)) * 0x1p-6f * pow2i(-up);    // 2^6 of the keys
             rs = fminf(fmaxf(rs, 0x1p-100f), 0x1p107f);                   // times a scale's power of two neither 0 nor infinite, for queries of any size
-            // the keys' exponent up to which no row's score here is beyond 2^20 (products of 2^15 and 2^13, 2^7 of them); the common way wants that
+            // the keys' exponent up to which no row's score here is beyond 2^23 (products of 2^15 and 2^13, 2^7 of them); the common way wants that
             // (rows of zeros, rows past the end among them, have no scores, and those that are not finite no order)
             if (!CAP) {
                 const uint32_t most = __reduce_max_sync(0xffffffffu, amax > 0.f && e < 128 ? __float_as_uint(rs) : 0u);
-                far = min(-16 - (static_cast<int>(most >> 23) - 127), kOwn - 1);
+                far = min(-13 - (static_cast<int>(most >> 23) - 127), kOwn - 1);
             }
 #pragma unroll
             for (int part = 0; part < kQ / 8; ++part) {
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
             if (kEarly) load();
             if (__builtin_expect(tile.x > far, 0)) {
                 const RowState row = wide_tile<HD, PARTS, CAP>(cs, co, &info, rs, a.softcap,
-                                                               {j0, last, p.s.len, p.s.L - p.s.T, in && a.tree ? a.tree + q0 + tok : nullptr},
+                                                               {j0, last, p.s.len, p.s.L - p.s.T, last >= 0 && a.tree ? a.tree + q0 + tok : nullptr},
                                                                {m, l, ref}, j >= 2 && !drain);
                 m = row.m;
                 l = row.l;
@@ -614,11 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
                         for (int g = 0; g < kGroups; ++g)
                             if (upto >= 16 * g && (have >> g & 1)) vis |= static_cast<unsigned long long>(kUpTo[min(upto - 16 * g, 15)]) << (16 * g);
                     } else {
-                        const unsigned long long bits = in ? a.tree[q0 + tok] : 0ull;
+                        const unsigned long long bits = last >= 0 ? a.tree[q0 + tok] : 0ull;
 #pragma unroll 1
                         for (int n = 0; n < kTok; ++n) {
                             const int key = j0 + token_of(n), rel = key - base;
-                            const bool v = last >= 0 && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
+                            const bool v = in && key < len && (have >> (n >> 4) & 1) && (rel < 0 || (rel < 64 && ((bits >> (rel & 63)) & 1)));
                             vis |= static_cast<unsigned long long>(v) << n;
                         }
                     }
@@ -1004,14 +1015,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnArgs 
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int n = 32 * half + lane;
+                const int kn = wide ? ke[half] : kexp, vn = wide ? ve[half] : ref;
                 uint32_t f1, f2;
-                scale_factors(wide ? ke[half] : kexp, f1, f2);
+                scale_factors(kn, f1, f2);
                 info.kf[n] = make_uint2(f1 * 0x10001u, f2 * 0x10001u);
-                scale_factors(wide ? ve[half] : ref, f1, f2);
+                scale_factors(vn, f1, f2);
                 info.vf[0][n] = static_cast<uint16_t>(f1);
                 info.vf[1][n] = static_cast<uint16_t>(f2);
-                info.ke[n] = static_cast<signed char>(ke[half]);
-                info.ve[n] = static_cast<signed char>(ve[half]);
+                info.ke[n] = static_cast<signed char>(kn);
+                info.ve[n] = static_cast<signed char>(vn);
             }
             __syncwarp();
             if (lane == 0) {

@@ -358,3 +358,23 @@ def test_tree_of_more_tokens_than_are_cached(gq, kind, spread, hd, T, heads):
     want, big = exact(q[3:], k, v, hd ** -0.5, seen=torch.ones(T - 3, L, dtype=torch.bool, device="cuda"))
     size = torch.einsum("thd,lhd->thl", q[3:].double().abs(), k.double().abs().expand(-1, heads, -1)) * hd ** -0.5
     assert torch.all((o[3:].double() - want).abs() <= bound(kind, size.amax(-1, keepdim=True), L, big, want))
+
+
+@pytest.mark.parametrize("power", [17, 19, 20, 21, 22, 23, 24, 25, 27, 40])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_scores_beyond_what_f32_resolves(gq, kind, power):
+    """Two keys by turns, whose scores are some 2^power apart or equal: of equal ones each has its share, the lower ones have none.  Causal rows see from none
+    to all of the high ones of the last tile."""
+    L, T, heads, hd = 300, 40, 8, 128
+    high = torch.arange(L, device="cuda") % 3 == 1
+    k = torch.where(high[:, None, None], 0.75, -0.5) * torch.ones(L, 1, hd, device="cuda")
+    v = normal(2, L, 1, hd)
+    cache, table, [(k, v)] = cached(gq, [k], [v])
+    q = torch.full((T, heads, hd), 1.37 * 2.0 ** power / hd, device="cuda").to(TYPES[kind])
+    for scale in (1.0, -1.0):
+        o = attend(gq, q, cache, table, L, scale=scale)
+        some = high if scale > 0 else ~high
+        seen = (torch.arange(L, device="cuda")[None] <= L - T + torch.arange(T, device="cuda")[:, None]) & some[None]
+        w = seen.double() / seen.sum(-1, keepdim=True)
+        want, big = (torch.einsum("tl,lhd->thd", w, x.double()).expand(T, heads, hd) for x in (v, v.abs()))
+        assert torch.all((o.double() - want).abs() <= bound(kind, 0.0, L, big, want))
