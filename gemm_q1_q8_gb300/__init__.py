@@ -7,6 +7,7 @@ CPU or PyTorch fallback, and a missing library is an error.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -24,6 +25,8 @@ __all__ = [
     "matmul_q4g128_mma", "q1s32_f32_gemm_mma", "q1s32_mma_workspace_bytes",
     "rmsnorm", "rmsnorm_q8_0", "dequantize_q8_0", "rope_table", "KVCacheQ8_0", "kv_cache_bytes", "rope_kv_append",
     "kv_read", "attn_q8_0", "attn_workspace", "attn_workspace_bytes",
+    "rmsnorm_block", "rmsnorm_block_q8_0", "FUNCTIONS", "q1_q8_linear", "q1_q8_glu", "q1_q8_linear_workspace",
+    "q1_q8_linear_workspace_bytes", "LogProbs", "logprobs", "logprobs_workspace", "logprobs_workspace_bytes",
     "device_error", "version", "PROBE_KINDS", "probe_fill", "probe_read", "probe_issue", "probe_mma",
 ]
 
@@ -85,6 +88,12 @@ def lib():
             "gq_quantize_q8_0": (I, [P, I, I, P, P, P, P]),
             "q1s32_q8_gemm": (I, [P, P, P, P, P, P, I, I, I, I, P]),
             "gq_rmsnorm": (I, [P, LL, P, LL, P, F, I, I, I, P, P, P, P, P, P, P]),
+            "gq_rmsnorm_block": (I, [P, LL, P, LL, P, P, LL, F, F, P, F, I, I, I, P, P, P, P, P, P, P]),
+            "gq_q1_q8_linear_workspace_bytes": (S, [I, I, I, I]),
+            "q1_q8_linear": (I, [P, P, I, I, I, P, I, P, LL, I, P, LL, P, P, P]),
+            "q1_q8_glu": (I, [P, P, P, I, I, I, P, P, I, I, P, LL, P, P, P]),
+            "gq_logprobs_workspace_bytes": (S, [I, I, I]),
+            "gq_logprobs": (I, [P, LL, I, I, I, F, P, P, P, I, P, P, P, P]),
             "gq_dequantize_q8_0": (I, [P, LL, I, P, P]),
             "gq_kv_cache_bytes": (S, [I, I, I, I]),
             "gq_rope_table": (I, [P, I, I, D, I, D, D, P]),
@@ -585,6 +594,201 @@ def rmsnorm_q8_0(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
         op = None
     _rmsnorm(x, weight, eps, residual, sum_out, None, None, d, q, op)
     return d, q, op
+
+
+def _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, y, act, d, q, op):
+    m, k = x.shape
+    code = _type(x, "x")
+    xs, bs = _rows(x, code, m, k, "x"), _rows(block, code, m, k, "block")
+    gs = 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2) or (gate.dim() == 2 and gate.shape[0] not in (1, m)):
+            raise GQError(f"gate: expected [{k}] or [{m}, {k}]")
+        one = gate.dim() == 1 or gate.shape[0] == 1
+        row = _rows(gate.view(1, -1) if gate.dim() == 1 else gate, code, 1 if one else m, k, "gate")
+        gs = 0 if one else row
+    _need(weight, torch.float32, k, "weight")
+    if post_weight is not None:
+        _need(post_weight, torch.float32, k, "post_weight")
+    if sum_out is not None:
+        _need(sum_out, x.dtype, m * k, "sum_out")
+    _one_device(x, block=block, weight=weight, post_weight=post_weight, gate=gate, sum_out=sum_out, out=y if y is not None else act if act is not None else q)
+    _check(lib().gq_rmsnorm_block(_at(block), bs, _at(x), xs, _at(post_weight), _at(gate), gs, block_scale, residual_scale, _at(weight),
+                                  eps, code, m, k, _at(sum_out), _at(y), _at(act), _at(d), _at(q), _at(op), _on(x)), "gq_rmsnorm_block")
+
+
+def _one_device(first: torch.Tensor, **others):
+    """Refuses tensors of another device than the call's first."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise GQError(f"{name}: expected a tensor on {first.device}, got {t.device}")
+
+
+def rmsnorm_block(block: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, post_weight: torch.Tensor | None = None, eps: float = 1e-5,
+                  gate: torch.Tensor | None = None, block_scale: float = 1.0, residual_scale: float = 1.0,
+                  out: torch.Tensor | None = None, sum_out: torch.Tensor | None = None):
+    """The norm after a block, its gate, the residual's addition and the norm before the next block: h = residual_scale * x +
+    block_scale * (gate * n), n = block / sqrt(mean(block^2) + eps) * post_weight (None: block itself), and h / sqrt(mean(h^2) + eps) *
+    weight.  block, x [m, k] of one type with contiguous rows, gate [k] or [m, k] of that type, weights [k] f32.  h goes to sum_out if
+    given (it may be x or block)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise GQError("x: expected a CUDA tensor [m, k]")
+    _type(x, "x")
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _need(y, x.dtype, x.numel(), "out")
+    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, y, None, None, None, None)
+    return y
+
+
+def rmsnorm_block_q8_0(block: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, post_weight: torch.Tensor | None = None,
+                       eps: float = 1e-5, gate: torch.Tensor | None = None, block_scale: float = 1.0, residual_scale: float = 1.0,
+                       split: bool = False, mma_operand: bool = False, out=None, sum_out: torch.Tensor | None = None):
+    """rmsnorm_block with its output in Q8_0, in the forms of rmsnorm_q8_0."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] % 32:
+        raise GQError("rmsnorm_block_q8_0: expected x [m, k] with k a multiple of 32")
+    _type(x, "x")
+    m, k = x.shape
+    act = d = q = op = None
+    if not split:
+        act = torch.empty(m * (k // 32) * 34, dtype=torch.uint8, device=x.device) if out is None else out
+        _need(act, torch.uint8, m * (k // 32) * 34, "out")
+    else:
+        if out is None:
+            d = torch.empty((m, k // 32), dtype=torch.int16, device=x.device)
+            q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+            op = torch.empty((3, m, k), dtype=torch.int16, device=x.device) if mma_operand else None
+        else:
+            d, q, op = out
+        _need(d, torch.int16, m * (k // 32), "d")
+        _need(q, torch.int8, m * k, "q")
+        if mma_operand:
+            _need(op, torch.int16, 3 * m * k, "op")
+        else:
+            op = None
+    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, None, act, d, q, op)
+    return act if not split else (d, q, op)
+
+
+FUNCTIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+def q1_q8_linear_workspace_bytes(rows: int, n: int, cols: int, dtype=torch.float32) -> int:
+    """Bytes of the workspace q1_q8_linear and q1_q8_glu need for these sizes (0: invalid)."""
+    return lib().gq_q1_q8_linear_workspace_bytes(rows, n, cols, _TYPES.get(dtype, -1))
+
+
+def q1_q8_linear_workspace(rows: int, n: int, cols: int, dtype=torch.float32, device="cuda") -> torch.Tensor:
+    """A workspace for q1_q8_linear or q1_q8_glu, to be kept between calls (calls sharing it must not overlap)."""
+    need = q1_q8_linear_workspace_bytes(rows, n, cols, dtype)
+    if need == 0:
+        raise GQError("q1_q8_linear_workspace: invalid shape")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _linear(name, packed, act, rows, n, cols, biases, function, dtype, q8_0, out, workspace):
+    """What both products check; (function code, type code, y, its stride, blocks, workspace, biases)."""
+    if function not in FUNCTIONS:
+        raise GQError(f"{name}: unknown activation {function!r}")
+    code = _TYPES.get(dtype)
+    if code is None:
+        raise GQError(f"{name}: expected float32, float16 or bfloat16, got {dtype}")
+    nbytes = q1_0_packed_bytes(rows, n)
+    need = q1_q8_linear_workspace_bytes(rows, n, cols, dtype)
+    if nbytes == 0 or need == 0 or (q8_0 and rows % 32):
+        raise GQError(f"{name}: invalid shape")
+    _need(act, torch.uint8, cols * (n // 32) * 34, "act")
+    for p in packed:
+        _need(p, torch.uint8, nbytes, "packed")
+    for b in biases:
+        if b is not None:
+            _need(b, torch.float32, rows, "bias")
+    y = blocks = None
+    ys = rows
+    if q8_0:
+        blocks = torch.empty(cols * (rows // 32) * 34, dtype=torch.uint8, device=act.device) if out is None else out
+        _need(blocks, torch.uint8, cols * (rows // 32) * 34, "out")
+    else:
+        y = torch.empty((cols, rows), dtype=dtype, device=act.device) if out is None else out
+        ys = _rows(y, code, cols, rows, "out")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=act.device)
+    _need(workspace, torch.uint8, workspace.numel(), "workspace")
+    if workspace.numel() < need:
+        raise GQError(f"{name}: workspace holds {workspace.numel()} bytes, needs {need}")
+    _one_device(act, packed=packed[0], packed_up=packed[-1], bias=biases[0], bias_up=biases[-1], out=y if blocks is None else blocks, workspace=workspace)
+    return FUNCTIONS[function], code, y, ys, blocks, workspace
+
+
+def q1_q8_linear(packed: torch.Tensor, act: torch.Tensor, rows: int, n: int, cols: int, bias: torch.Tensor | None = None,
+                 activation: str = "none", residual: torch.Tensor | None = None, dtype=torch.float32, q8_0: bool = False,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """activation(w . a + bias) + residual for a packed rows x n Q1_0 matrix and `cols` Q8_0 vectors (uint8, cols * n/32 * 34 bytes), from
+    one decoded token to long prompts: y [cols, rows] of dtype (f32, f16 or bf16), or with q8_0=True its Q8_0 blocks (uint8, rows a
+    multiple of 32).  activation: a name of FUNCTIONS; bias [rows] f32; residual [cols, rows] of dtype with contiguous rows, which out may be."""
+    fn, code, y, ys, blocks, work = _linear("q1_q8_linear", (packed,), act, rows, n, cols, (bias,), activation, dtype, q8_0, out, workspace)
+    rs = _rows(residual, code, cols, rows, "residual") if residual is not None else 0
+    _one_device(act, residual=residual)
+    _check(lib().q1_q8_linear(_at(packed), _at(act), rows, n, cols, _at(bias), fn, _at(residual), rs, code, _at(y), ys, _at(blocks),
+                              _at(work), _on(act)), "q1_q8_linear")
+    return y if blocks is None else blocks
+
+
+def q1_q8_glu(packed_gate: torch.Tensor, packed_up: torch.Tensor, act: torch.Tensor, rows: int, n: int, cols: int,
+              activation: str = "silu", bias_gate: torch.Tensor | None = None, bias_up: torch.Tensor | None = None, dtype=torch.float32,
+              q8_0: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """activation(w_gate . a + bias_gate) * (w_up . a + bias_up): the gated pair of a feed-forward block, outputs as q1_q8_linear's."""
+    fn, code, y, ys, blocks, work = _linear("q1_q8_glu", (packed_gate, packed_up), act, rows, n, cols, (bias_gate, bias_up), activation,
+                                            dtype, q8_0, out, workspace)
+    _check(lib().q1_q8_glu(_at(packed_gate), _at(packed_up), _at(act), rows, n, cols, _at(bias_gate), _at(bias_up), fn, code, _at(y),
+                           ys, _at(blocks), _at(work), _on(act)), "q1_q8_glu")
+    return y if blocks is None else blocks
+
+
+LogProbs = collections.namedtuple("LogProbs", "logprob entropy top_ids top_logprobs")
+
+
+def logprobs_workspace_bytes(m: int, vocab: int, top: int = 0) -> int:
+    """Bytes of the workspace logprobs needs (0: invalid sizes)."""
+    return lib().gq_logprobs_workspace_bytes(m, vocab, top)
+
+
+def logprobs_workspace(m: int, vocab: int, top: int = 0, device="cuda") -> torch.Tensor:
+    """A workspace for logprobs, to be kept between calls (calls sharing it must not overlap)."""
+    need = logprobs_workspace_bytes(m, vocab, top)
+    if need == 0:
+        raise GQError("logprobs_workspace: invalid shape")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, scale: float = 1.0, entropy: bool = True,
+             workspace: torch.Tensor | None = None) -> LogProbs:
+    """Of each row of logits [m, vocab] (f32, f16 or bf16, contiguous rows), with p = softmax(scale * logits): the log probability of
+    tokens[i] (int64 [m]; a negative one gives 0), the entropy of p, and the `top` largest logits (at most 32) with their log
+    probabilities, largest first, equal ones by index.  What is not asked for is None."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise GQError("logits: expected a CUDA tensor [m, vocab]")
+    code = _type(logits, "logits")
+    m, vocab = logits.shape
+    stride = _rows(logits, code, m, vocab, "logits")
+    if tokens is not None:
+        _need(tokens, torch.int64, m, "tokens")
+    need = logprobs_workspace_bytes(m, vocab, top)
+    if need == 0 or (tokens is None and not entropy and top == 0):
+        raise GQError("logprobs: invalid shape, or nothing asked for")
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    lp = torch.empty(m, **f32) if tokens is not None else None
+    h = torch.empty(m, **f32) if entropy else None
+    ids = torch.empty((m, top), dtype=torch.int64, device=logits.device) if top else None
+    best = torch.empty((m, top), **f32) if top else None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    _need(workspace, torch.uint8, workspace.numel(), "workspace")
+    if workspace.numel() < need:
+        raise GQError(f"logprobs: workspace holds {workspace.numel()} bytes, needs {need}")
+    _one_device(logits, tokens=tokens, workspace=workspace)
+    _check(lib().gq_logprobs(_at(logits), stride, code, m, vocab, scale, _at(tokens), _at(lp), _at(h), top, _at(ids), _at(best),
+                             _at(workspace), _on(logits)), "gq_logprobs")
+    return LogProbs(lp, h, ids, best)
 
 
 def dequantize_q8_0(act: torch.Tensor, m: int, k: int, dtype=torch.float32, out: torch.Tensor | None = None):

@@ -1,10 +1,12 @@
 // The C ABI of libgq: argument validation on the host, then one launch on the caller's stream.
 // Nothing here allocates device memory or synchronizes, except gq_device_error().
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "gq_internal.cuh"
 #include "layer_ops.cuh"
+#include "linear.cuh"
 #include "wq_mma.cuh"
 #include "w1a32_mma.cuh"
 
@@ -58,7 +60,7 @@ int gq_device_error(void) {
     const unsigned v = gq::error_read_clear_q1() | gq::error_read_clear_q1_gemv() | gq::error_read_clear_ternary() | gq::error_read_clear_prefill_mma() |
                        gq::error_read_clear_wq_mma() | gq::error_read_clear_w1a32() | gq::error_read_clear_probes() |
                        gq::error_read_clear_block_q8() | gq::error_read_clear_kv() | gq::error_read_clear_attn() |
-                       gq::error_read_clear_attn_tiles();
+                       gq::error_read_clear_attn_tiles() | gq::error_read_clear_logprobs();
     return v == ~0u ? -1 : static_cast<int>(v);
 }
 
@@ -272,6 +274,26 @@ static bool cache_shape(int pages, int page_size, int kv_heads, int head_dim) {
            (head_dim == 64 || head_dim == 128 || head_dim == 256) && static_cast<long long>(pages) * page_size < (1ll << 40);
 }
 
+static bool logprob_shape(int m, int vocab, int top) {
+    return m >= 1 && m <= 1 << 24 && vocab >= 1 && vocab <= 1 << 20 && top >= 0 && top <= 32 && top <= vocab;
+}
+
+constexpr int kMaxCols = 1 << 20;
+
+static int linear_call(const gq::LinearArgs& a, bool pair, gq_stream_t stream) {
+    if (a.rows < 1 || a.n < 128 || a.n % 128 != 0 || a.n > gq::kMaxN || a.cols < 1 || a.cols > kMaxCols || (a.blocks && a.rows % 32 != 0) ||
+        (a.y && a.y_stride < a.rows) || (a.residual && a.residual_stride < a.rows))
+        return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(a.type);
+    if (!b || a.function < GQ_FN_NONE || a.function > GQ_FN_GELU_TANH) return GQ_EUNSUPPORTED;
+    if (!a.w[0] || !a.w[1] || !a.act || (!a.y && !a.blocks) || !a.workspace) return GQ_EINVAL_PTR;
+    if (!aligned(a.w[0], 16) || !aligned(a.w[1], 16) || !aligned(a.act, 2) || !aligned(a.bias[0], 4) || !aligned(a.bias[1], 4) ||
+        !aligned(a.residual, b) || !aligned(a.y, b) || !aligned(a.blocks, 2) || !aligned(a.workspace, 16))
+        return GQ_EINVAL_PTR;
+    if (a.y && a.y == a.residual && a.y_stride != a.residual_stride) return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_linear(a, pair, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int gq_rmsnorm(const void* x, long long x_stride, const void* residual, long long residual_stride, const float* weight,
                float eps, int type, int m, int k, void* sum, void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op,
                gq_stream_t stream) {
@@ -287,6 +309,67 @@ int gq_rmsnorm(const void* x, long long x_stride, const void* residual, long lon
     if ((sum == x && sum && x_stride != k) || (sum && sum == residual && residual_stride != k)) return GQ_EINVAL_PTR;
     return cuda_status(gq::launch_rmsnorm(x, x_stride, residual, residual_stride, weight, eps, type, m, k, sum, y, act, d, q,
                                           op, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int gq_rmsnorm_block(const void* block, long long block_stride, const void* x, long long x_stride, const float* post_weight,
+                     const void* gate, long long gate_stride, float block_scale, float residual_scale, const float* weight,
+                     float eps, int type, int m, int k, void* sum, void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op,
+                     gq_stream_t stream) {
+    if (m < 1 || k < 1 || k > kMaxK || block_stride < k || x_stride < k || (gate && gate_stride != 0 && gate_stride < k) ||
+        !(eps >= 0.0f) || !std::isfinite(block_scale) || !std::isfinite(residual_scale))
+        return GQ_EINVAL_SHAPE;
+    if ((act || d || q || op) && k % 32 != 0) return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!b) return GQ_EUNSUPPORTED;
+    if (!block || !x || !weight || (!sum && !y && !act && !d && !q && !op) || !d != !q || (op && !q)) return GQ_EINVAL_PTR;
+    if (!aligned(block, b) || !aligned(x, b) || !aligned(gate, b) || !aligned(weight, 4) || !aligned(post_weight, 4) ||
+        !aligned(sum, b) || !aligned(y, b) || !aligned(act, 2) || !aligned(d, 2) || !aligned(q, 16) || !aligned(op, 16))
+        return GQ_EINVAL_PTR;
+    if (sum && ((sum == x && x_stride != k) || (sum == block && block_stride != k) || sum == gate)) return GQ_EINVAL_PTR;
+    return cuda_status(gq::launch_block_norm(block, block_stride, x, x_stride, post_weight, gate, gate_stride, block_scale,
+                                             residual_scale, weight, eps, type, m, k, sum, y, act, d, q, op,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gq_logprobs_workspace_bytes(int m, int vocab, int top) {
+    return logprob_shape(m, vocab, top) ? gq::logprobs_workspace_bytes(m, vocab, top) : 0;
+}
+
+int gq_logprobs(const void* logits, long long stride, int type, int m, int vocab, float scale, const int64_t* tokens, float* logprob,
+                float* entropy, int top, int64_t* top_ids, float* top_logprobs, void* workspace, gq_stream_t stream) {
+    if (!logprob_shape(m, vocab, top) || stride < vocab || !std::isfinite(scale) || !(scale > 0.0f)) return GQ_EINVAL_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!b) return GQ_EUNSUPPORTED;
+    if (!logits || !tokens != !logprob || (!logprob && !entropy && top == 0) || (top > 0 && (!top_ids || !top_logprobs)) || !workspace)
+        return GQ_EINVAL_PTR;
+    if (!aligned(logits, b) || !aligned(tokens, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(workspace, 16) ||
+        (top > 0 && (!aligned(top_ids, 8) || !aligned(top_logprobs, 4))))
+        return GQ_EINVAL_PTR;
+    const gq::LogprobArgs a = {logits, stride, m, vocab, top, scale, tokens, logprob, entropy, top_logprobs, top_ids, workspace};
+    return cuda_status(gq::launch_logprobs(a, type, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type) {
+    if (rows < 1 || n < 128 || n % 128 != 0 || n > gq::kMaxN || cols < 1 || cols > kMaxCols || !type_bytes(type)) return 0;
+    return gq::linear_workspace_bytes(rows, n, cols, type);
+}
+
+int q1_q8_linear(const void* packed_w, const void* act, int rows, int n, int cols, const float* bias, int function,
+                 const void* residual, long long residual_stride, int type, void* y, long long y_stride, void* blocks,
+                 void* workspace, gq_stream_t stream) {
+    const gq::LinearArgs a = {{static_cast<const uint8_t*>(packed_w), static_cast<const uint8_t*>(packed_w)}, static_cast<const uint8_t*>(act),
+                              {bias, bias}, rows, n, cols, function, type, residual, residual_stride, y, y_stride,
+                              static_cast<uint8_t*>(blocks), workspace};
+    return linear_call(a, false, stream);
+}
+
+int q1_q8_glu(const void* packed_gate, const void* packed_up, const void* act, int rows, int n, int cols, const float* bias_gate,
+              const float* bias_up, int function, int type, void* y, long long y_stride, void* blocks, void* workspace,
+              gq_stream_t stream) {
+    const gq::LinearArgs a = {{static_cast<const uint8_t*>(packed_gate), static_cast<const uint8_t*>(packed_up)}, static_cast<const uint8_t*>(act),
+                              {bias_gate, bias_up}, rows, n, cols, function, type, nullptr, 0, y, y_stride,
+                              static_cast<uint8_t*>(blocks), workspace};
+    return linear_call(a, true, stream);
 }
 
 int gq_dequantize_q8_0(const void* act, long long blocks, int type, void* out, gq_stream_t stream) {

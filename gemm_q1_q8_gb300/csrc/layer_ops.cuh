@@ -85,6 +85,16 @@ __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int 
         for (int i = 0; i < 4; ++i) c[i] = q8_0_quant(x[i], amax, dd);
 }
 
+// One value by the same rule.
+__device__ __forceinline__ int q8_0_quant1(float v, float amax, float dd) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(dd));
+    if (!(dd >= 0x1p-120f)) r = 0.0f;
+    const float magic = 12582912.0f, t = fmaf(v, r, magic);
+    const bool far = (dd >= 0x1p-120f || amax == 0.0f) && fabsf(fmaf(v, r, magic - t)) <= 0.5f - 0x1p-11f;
+    return far ? __float_as_int(t) - __float_as_int(magic) : q8_0_quant(v, amax, dd);
+}
+
 // Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d
 __device__ __forceinline__ uint32_t cache_word(const int (&c)[4]) {
     uint32_t w = 0;
@@ -125,6 +135,21 @@ template <int HD> __device__ __forceinline__ int kv_scale(int tok, int d) {
 cudaError_t launch_rmsnorm(const void* x, long long xs, const void* r, long long rs, const float* w, float eps, int type,
                            int m, int k, void* h, void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op,
                            cudaStream_t s);
+cudaError_t launch_block_norm(const void* block, long long bs, const void* x, long long xs, const float* post, const void* gate, long long gs,
+                              float block_scale, float residual_scale, const float* w, float eps, int type, int m, int k, void* h,
+                              void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op, cudaStream_t s);
+struct LogprobArgs {
+    const void* x;
+    long long stride;
+    int m, vocab, top;
+    float scale;
+    const int64_t* tokens;
+    float* logprob; float* entropy; float* top_values;
+    int64_t* top_ids;
+    void* workspace;
+};
+size_t logprobs_workspace_bytes(int m, int vocab, int top);
+cudaError_t launch_logprobs(const LogprobArgs& a, int type, cudaStream_t s);
 cudaError_t launch_dequantize_q8_0(const void* act, long long blocks, int type, void* out, cudaStream_t s);
 cudaError_t launch_rope_table(float* table, int positions, int rot, double base, int scaling, double factor,
                               double original, cudaStream_t s);

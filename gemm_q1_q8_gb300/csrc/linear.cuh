@@ -1,0 +1,88 @@
+// Q1_0 products with an epilogue: what the kernel for few tokens (linear.cu) and the one for many (linear_tiles.cu) share.
+//
+//   z[c, r] = sum_b d0[r, b] * sum_k d1[c, 4b + k] * sum_t (+-1) q   (+ bias[r])
+//   linear:  y = act(z) (+ residual[c, r]);      pair: y = act(z_gate) * z_up
+//
+// Both kernels take +-d0 as f16 matrix operands, made from the sign bits by two logic operations a pair, and the activations as
+// pv = d1 * q * 2^-e, e one power of two a token: pv has at most 18 significant bits, so two f16 parts hold it exactly while it is
+// not below 2^-20 of the token's largest (then it is off by at most 2^-39 of that).  f32, f16 and Q8_0 results take both
+// parts; a bf16 result (8 bits) takes one, off by 2^-12 of each value.  Products are exact in f32, sums are f32; the tensor
+// cores truncate the sum that they add to, so it goes to registers every few blocks of 128 (a chain of n steps costs n / 3 * 2^-23).
+#pragma once
+
+#include "layer_ops.cuh"
+
+namespace gq {
+
+struct LinearArgs {
+    const uint8_t* w[2];               // packed Q1_0; the pair: gate, up
+    const uint8_t* act;                // Q8_0 blocks
+    const float* bias[2];
+    int rows, n, cols;
+    int function;                      // gq_function
+    int type;
+    const void* residual;
+    long long residual_stride;
+    void* y;
+    long long y_stride;
+    uint8_t* blocks;                   // Q8_0 output
+    void* workspace;
+};
+
+cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s);
+size_t linear_workspace_bytes(int rows, int n, int cols, int type);
+
+namespace {
+
+// f16 parts that an activation takes
+__host__ __device__ __forceinline__ int linear_parts(const LinearArgs& a) { return a.type == GQ_BF16 && !a.blocks ? 1 : 2; }
+
+__device__ __forceinline__ float bend(float z, int function) {
+    switch (function) {
+        case GQ_FN_RELU: return z < 0.f ? 0.f : z;                               // NaN stays
+        case GQ_FN_RELU2: z = z < 0.f ? 0.f : z; return z * z;
+        case GQ_FN_SILU: return __fdividef(z, 1.f + __expf(-z));
+        case GQ_FN_GELU: return 0.5f * z * erfcf(z * -0.70710678f);              // no cancellation below zero
+        case GQ_FN_GELU_TANH: return __fdividef(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));   // z * sigmoid(2u)
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float load_typed(const void* p, size_t i, int type) {
+    if (type == GQ_F32) return static_cast<const float*>(p)[i];
+    if (type == GQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_typed(void* p, size_t i, int type, float v) {
+    if (type == GQ_F32) static_cast<float*>(p)[i] = v;
+    else if (type == GQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// A warp's 32 values (one a lane: 32 neighbouring rows of one token) as a Q8_0 block, by the library's rule.  A NaN gives a NaN scale.
+__device__ __forceinline__ void store_block(uint8_t* block, float v, int lane) {
+    const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v))));
+    const float dd = q8_0_scale_fast(amax);
+    const int code = q8_0_quant1(v, amax, dd);
+    if (lane == 0) *reinterpret_cast<uint16_t*>(block) = __half_as_ushort(__float2half_rn(dd));
+    block[2 + lane] = static_cast<uint8_t>(code);
+}
+
+// The power of two that a token's values are multiplied by, 2^(7 - E) for scales below 2^(E + 1) (f16 bits without sign):
+// codes times scales are then below 2^15, and it is undone after the sums.
+__device__ __forceinline__ int token_shift(uint32_t largest) {
+    const int e = static_cast<int>(largest >> 10);                               // 31: not finite, whatever comes
+    if (e) return 7 - (e - 15);
+    return 7 - (largest ? -24 + (31 - __clz(largest)) : -24);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Two f16 parts of a value
+__device__ __forceinline__ void two_parts(float v, uint16_t& hi, uint16_t& lo) {
+    const __half h = __float2half_rn(v);
+    hi = __half_as_ushort(h);
+    lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+}
+
+}  // namespace
+}  // namespace gq

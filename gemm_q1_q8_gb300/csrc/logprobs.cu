@@ -1,0 +1,385 @@
+// Log probabilities of given tokens, the entropy and the best alternatives of rows of logits.
+//
+//   p = softmax(scale * x);  logprob = scale * (x[token] - M) - ln s,  H = ln s - (sum e^t t) / s,
+//   with M = max x, t = scale * (x - M), s = sum e^t.
+// A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps a running maximum and the two sums a
+// thread (rescaled where a step of loads raises the maximum).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
+// k-th largest logit from below, and a search over the bits of an order-preserving key finds it by 16 block-wide counts.  Only the threads whose maximum
+// reaches the bound (about k of 512) have their logits read once more, from L2, by a warp together.  Equal values go by
+// the lower index: where too many share the bound (masked rows), they are taken in the order of their index.
+// Parts are joined by a second kernel in their order.  Bound by HBM for many rows, by two launches and the
+// searches' barriers for one.
+#include "layer_ops.cuh"
+
+namespace gq {
+GQ_ERROR_ACCESSOR(logprobs)
+
+namespace {
+
+constexpr int kThreads = 512, kJoinThreads = 256;
+constexpr int kMaxTop = 32, kMaxPart = 65536, kMaxSplits = 64;
+constexpr int kFound = 4096;                      // candidates: 31 threads of kMaxPart / kThreads logits fit
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float d;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+    return d;
+}
+
+// Values in the order of unsigned numbers: both zeros alike, NaN above all, 0 below all
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    if (x != x) return ~0u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    if (key == ~0u) return __uint_as_float(0x7fffffffu);
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return static_cast<uint64_t>(key) << 32 | (0xffffffffu - index); }
+
+// m: the largest logit (at least the lowest number); s = sum 2^t, u = sum 2^t t, t = c (x - m)
+struct Sums { float m, s, u; };
+
+__device__ __forceinline__ void rescale(Sums& a, float m, float c) {
+    const float d = max_nan(c * (a.m - m), -1e4f), f = exp2_fast(d);
+    a.u = fmaf(a.s, d, a.u) * f;
+    a.s *= f;
+    a.m = m;
+}
+__device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
+    const float m = max_nan(a.m, b.m);
+    rescale(a, m, c);
+    rescale(b, m, c);
+    return {m, a.s + b.s, a.u + b.u};
+}
+__device__ __forceinline__ Sums shuffled(const Sums& a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.u, o)};
+}
+__device__ __forceinline__ void add(Sums& a, float x, float c) {
+    const float t = max_nan(c * (x - a.m), -1e4f), e = exp2_fast(t);               // -inf: no weight, and no 0 * inf
+    a.s += e;
+    a.u = fmaf(e, t, a.u);
+}
+
+// 16 bytes of logits
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int W = 4;
+    static __device__ __forceinline__ void get(const uint4& r, float (&v)[4]) {
+        v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int W = 8;
+    static __device__ __forceinline__ void get(const uint4& r, float (&v)[8]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Vec<__half> {
+    static constexpr int W = 8;
+    static __device__ __forceinline__ void get(const uint4& r, float (&v)[8]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+};
+
+__device__ __forceinline__ float logprob_of(float x, const Sums& a, float scale) {
+    if (a.s == 0.f) return x != x ? x : __uint_as_float(0xff800000u);              // nothing has any weight
+    return scale * (x - a.m) - logf(a.s);
+}
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, const Sums& t) {
+    if (a.entropy) a.entropy[row] = t.s == 0.f ? 0.f : logf(t.s) - t.u / t.s * kLn2;
+    if (a.logprob) {
+        const int64_t tok = a.tokens[row];
+        float r = 0.f;
+        if (tok >= a.vocab) {
+            r = __uint_as_float(0x7fffffffu);
+            report_error(kErrIndex);
+        } else if (tok >= 0) r = logprob_of(to_f32(static_cast<const T*>(a.x)[row * a.stride + tok]), t, a.scale);
+        a.logprob[row] = r;
+    }
+}
+
+// The workspace of rows in parts: Sums (as float4) and `top` entries of each part
+__host__ __device__ __forceinline__ float4* part_sums(void* w) { return static_cast<float4*>(w); }
+__device__ __forceinline__ uint64_t* part_best(void* w, size_t parts) { return reinterpret_cast<uint64_t*>(static_cast<float4*>(w) + parts); }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs a, int splits, int part) {
+    constexpr int W = Vec<T>::W, UN = 4;
+    __shared__ uint64_t found[kFound];
+    __shared__ Sums warp_sums[kThreads / 32];
+    __shared__ int count, warp_counts[kThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const size_t row = blockIdx.x / splits;
+    const int split = blockIdx.x % splits, v0 = split * part, n = max(0, min(part, a.vocab - v0));
+    const T* x = static_cast<const T*>(a.x) + row * a.stride + v0;
+    const int k = a.top;
+    const float c = a.scale * kLog2e;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // whole vectors, and up to 7 logits on either side of them, one a thread
+    const int head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)));
+    const int vecs = (n - head) / W, tail = n - head - vecs * W;
+    const int extra = tid < head ? tid : tid >= 32 && tid - 32 < tail ? head + vecs * W + tid - 32 : -1;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    const float none = __uint_as_float(0xff800000u);
+    float top = none;                                                             // the thread's largest
+    Sums t = {kLowest, 0.f, 0.f};
+    if (extra >= 0) {
+        top = to_f32(x[extra]);
+        t.m = max_nan(top, kLowest);
+        add(t, top, c);
+    }
+    for (int v = tid; v < vecs; v += UN * kThreads) {
+        uint4 r[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+            if (v + i * kThreads < vecs) r[i] = xv[v + i * kThreads];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            if (v + i * kThreads >= vecs) break;
+            float f[W];
+            Vec<T>::get(r[i], f);
+            float m = f[0];
+#pragma unroll
+            for (int j = 1; j < W; ++j) m = max_nan(m, f[j]);
+            top = max_nan(top, m);
+            rescale(t, max_nan(t.m, m), c);
+#pragma unroll
+            for (int j = 0; j < W; ++j) add(t, f[j], c);
+        }
+    }
+    const uint32_t mine = key_of(top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
+    if (lane == 0) warp_sums[warp] = t;
+    if (tid == 0) count = 0;
+    __syncthreads();
+    t = lane < kThreads / 32 ? warp_sums[lane] : Sums{kLowest, 0.f, 0.f};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
+    t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0), __shfl_sync(0xffffffffu, t.u, 0)};
+    if (tid == 0) {
+        if (splits == 1) finish_row<T>(a, row, t);
+        else part_sums(a.workspace)[blockIdx.x] = make_float4(t.m, t.s, t.u, 0.f);
+    }
+    if (k == 0) return;
+
+    // bound: the largest number that k threads' maxima reach, in its upper 16 bits, or exactly
+    uint32_t bound = 0;
+    auto search = [&](int from, int to, int q) {
+        for (int b = from; b >= to; --b) {
+            const uint32_t try_ = bound | 1u << b;
+            const int reach = __syncthreads_count(mine >= try_);
+            if (reach >= k) {
+                bound = try_;
+                q = reach;
+            }
+        }
+        return q;
+    };
+    // entries of the threads that reach the bound, of logits at least `least`
+    auto gather = [&](uint32_t least) {
+        for (unsigned left = __ballot_sync(0xffffffffu, mine >= least); left; left &= left - 1) {
+            const int other = warp * 32 + __ffs(left) - 1;
+            for (int v = other + lane * kThreads; v < vecs; v += 32 * kThreads) {
+                float f[W];
+                Vec<T>::get(xv[v], f);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const uint32_t key = key_of(f[j]);
+                    if (key >= least) {
+                        const int at = atomicAdd(&count, 1);
+                        if (at < kFound) found[at] = entry(key, v0 + head + v * W + j);
+                    }
+                }
+            }
+        }
+        if (extra >= 0) {
+            const uint32_t key = key_of(to_f32(x[extra]));
+            if (key >= least) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kFound) found[at] = entry(key, v0 + extra);
+            }
+        }
+        __syncthreads();
+        return count;
+    };
+    const int few = 2 * k + 16;
+    int have = kFound + 1;
+    int reach = search(31, 16, kThreads);
+    if (reach <= few) have = gather(bound);
+    if (have > kFound) {
+        // too many near the bound: the exact one
+        __syncthreads();
+        if (tid == 0) count = 0;
+        reach = search(15, 0, reach);                                                    // its barriers stand between the zero and the entries
+        have = kFound + 1;
+        if (reach <= few) have = gather(bound);
+        if (have > kFound) {
+            // logits above the bound lie with fewer than k threads; of those at the bound the first few, in their order
+            __syncthreads();
+            if (tid == 0) count = 0;
+            __syncthreads();
+            have = bound == ~0u ? 0 : gather(bound + 1);
+            int need = k - have;
+            for (int at = 0; at < n && need > 0; at += kThreads) {
+                const bool is = at + tid < n && key_of(to_f32(x[at + tid])) == bound;
+                const unsigned who = __ballot_sync(0xffffffffu, is);
+                if (lane == 0) warp_counts[warp] = __popc(who);
+                __syncthreads();
+                int before = __popc(who & ((1u << lane) - 1)), all = 0;
+                for (int w = 0; w < kThreads / 32; ++w) {
+                    if (w < warp) before += warp_counts[w];
+                    all += warp_counts[w];
+                }
+                if (is && before < need) found[have + before] = entry(bound, v0 + at + tid);
+                have += min(all, need);
+                need -= min(all, need);
+                __syncthreads();
+            }
+        }
+    }
+    // the place of each among them
+    for (int i = tid; i < have; i += kThreads) {
+        const uint64_t e = found[i];
+        int rank = 0;
+        for (int j = 0; j < have; ++j) rank += found[j] > e;
+        if (rank < k) {
+            if (splits == 1) {
+                a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
+                a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
+            } else part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + rank] = e;
+        }
+    }
+    // a part of fewer logits
+    if (splits > 1 && tid >= have && tid < k) part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + tid] = 0;
+}
+
+// One block a row: its parts' sums in their order, and the best of the parts' best.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const LogprobArgs a, int splits) {
+    constexpr int PER = kMaxSplits * kMaxTop / kJoinThreads;
+    __shared__ uint64_t found[kMaxSplits * kMaxTop];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const size_t row = blockIdx.x, parts = static_cast<size_t>(gridDim.x) * splits;
+    const int k = a.top;
+    const float c = a.scale * kLog2e;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float4* sums = part_sums(a.workspace) + row * splits;
+    Sums t = {kLowest, 0.f, 0.f};
+    for (int i = lane; i < splits; i += 32) {
+        const float4 p = sums[i];
+        t = joined(t, Sums{p.x, p.y, p.z}, c);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
+    t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0), __shfl_sync(0xffffffffu, t.u, 0)};
+    if (tid == 0) {
+        finish_row<T>(a, row, t);
+        count = 0;
+    }
+    if (k == 0) return;
+    const uint64_t* best = part_best(a.workspace, parts) + row * splits * k;
+    uint64_t mine[PER], top = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        mine[i] = tid + i * kJoinThreads < splits * k ? best[tid + i * kJoinThreads] : 0;
+        top = max(top, mine[i]);
+    }
+    // as above, over entries, which are all different: with all their bits, k threads reach the bound
+    uint64_t bound = 0;
+    int reach = kJoinThreads;
+    for (int b = 63; b >= 0; --b) {
+        if (b == 47 && reach <= 2 * k + 16) break;
+        const uint64_t try_ = bound | 1ull << b;
+        const int q = __syncthreads_count(top >= try_);
+        if (q >= k) {
+            bound = try_;
+            reach = q;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (mine[i] && mine[i] >= bound) found[atomicAdd(&count, 1)] = mine[i];
+    __syncthreads();
+    const int have = count;
+    for (int i = tid; i < have; i += kJoinThreads) {
+        const uint64_t e = found[i];
+        int rank = 0;
+        for (int j = 0; j < have; ++j) rank += found[j] > e;
+        if (rank < k) {
+            a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
+            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
+        }
+    }
+}
+
+// Parts of a row: enough for two blocks an SM, of at least 2048 logits each where they need not be smaller than kMaxPart
+int splits_of(int m, int vocab) {
+    const int least = (vocab + kMaxPart - 1) / kMaxPart, want = m < 2 * 152 ? 2 * 152 / m : 1;
+    const int most = vocab / 2048 > 1 ? vocab / 2048 : 1;
+    const int s = want < most ? want : most;
+    return s < least ? least : s > kMaxSplits ? kMaxSplits : s;
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, unsigned grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T>
+cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
+    const int splits = splits_of(a.m, a.vocab), part = (a.vocab + splits - 1) / splits;
+    const cudaError_t e = launch(logprobs_kernel<T>, static_cast<unsigned>(a.m) * splits, kThreads, s, a, splits, part);
+    if (e != cudaSuccess || splits == 1) return e;
+    return launch(logprobs_join_kernel<T>, static_cast<unsigned>(a.m), kJoinThreads, s, a, splits);
+}
+
+}  // namespace
+
+size_t logprobs_workspace_bytes(int m, int vocab, int top) {
+    const size_t splits = splits_of(m, vocab);
+    return splits == 1 ? 16 : static_cast<size_t>(m) * splits * (16 + 8 * static_cast<size_t>(top));
+}
+
+cudaError_t launch_logprobs(const LogprobArgs& a, int type, cudaStream_t s) {
+    if (type == GQ_F32) return logprobs_type<float>(a, s);
+    if (type == GQ_F16) return logprobs_type<__half>(a, s);
+    return logprobs_type<__nv_bfloat16>(a, s);
+}
+
+}  // namespace gq

@@ -188,6 +188,130 @@ cudaError_t norm_type(const NormArgs& a, int m, cudaStream_t s) {
     return norm_go<T, 8>(a, m, threads(8) < 1024 ? threads(8) : 1024, vec, s);
 }
 
+// --------------------------------------------------------------------------------------------
+// The norm after a block, its gate, the residual's addition and the norm before the next block:
+//   n = y * rstd(y) * post (or y);  h = residual_scale * x + block_scale * (gate * n);  z = h * rstd(h) * w
+// One pass as above with two sums a row: y and then h stay in registers.  Bytes: y, x and the gate once, h and z once.
+// --------------------------------------------------------------------------------------------
+struct BlockNormArgs {
+    NormArgs n;                                       // x: the stream, h, y, act, ...: the outputs; r unused
+    const void* block; long long bs;
+    const float* post;
+    const void* gate; long long gs;
+    float block_scale, residual_scale;
+};
+
+__device__ __forceinline__ float row_sum(float s, float* part, int tid, int nt) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((tid & 31) == 0) part[tid >> 5] = s;
+    __syncthreads();
+    s = (tid & 31) < nt / 32 ? part[tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+// in the norm's orders above: values in registers, and those read again
+__device__ __forceinline__ float squares(float4 v, float s) { return fmaf(v.w, v.w, fmaf(v.z, v.z, fmaf(v.y, v.y, fmaf(v.x, v.x, s)))); }
+__device__ __forceinline__ float squares_again(float4 v, float s) { return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s)))); }
+
+template <typename T, int NV, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_kernel(const BlockNormArgs b) {
+    __shared__ float part[2][32];
+    const NormArgs& a = b.n;
+    const int tid = threadIdx.x, nt = blockDim.x, k = a.k;
+    const size_t row = blockIdx.x;
+    const T* xr = static_cast<const T*>(a.x) + row * a.xs;
+    const T* yr = static_cast<const T*>(b.block) + row * b.bs;
+    const T* gr = b.gate ? static_cast<const T*>(b.gate) + row * b.gs : nullptr;
+    const int chunks = ((k + 3) / 4 + nt - 1) / nt;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    float4 v[NV], x[NV];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) v[c] = load_row4<T, VEC>(yr, 4 * (c * nt + tid), k);
+#pragma unroll
+    for (int c = 0; c < NV; ++c) x[c] = load_row4<T, VEC>(xr, 4 * (c * nt + tid), k);
+    float rstd = 1.f;
+    if (b.post) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) s = squares(v[c], s);
+        for (int c = NV; c < chunks; ++c) s = squares_again(load_row4<T, VEC>(yr, 4 * (c * nt + tid), k), s);
+        s = row_sum(s, part[0], tid, nt);
+        rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
+    }
+    // h of four values
+    auto join = [&](int i, float4 y, float4 x) {
+        if (b.post) {
+            const float4 w = load_row4<float, VEC>(b.post, i, k);
+            y = make_float4(y.x * rstd * w.x, y.y * rstd * w.y, y.z * rstd * w.z, y.w * rstd * w.w);
+        }
+        if (gr) {
+            const float4 g = load_row4<T, VEC>(gr, i, k);
+            y = make_float4(g.x * y.x, g.y * y.y, g.z * y.z, g.w * y.w);
+        }
+        const float p = b.residual_scale, q = b.block_scale;
+        return make_float4(p * x.x + q * y.x, p * x.y + q * y.y, p * x.z + q * y.z, p * x.w + q * y.w);
+    };
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        v[c] = join(4 * (c * nt + tid), v[c], x[c]);
+        s = squares(v[c], s);
+    }
+    for (int c = NV; c < chunks; ++c) {
+        const int i = 4 * (c * nt + tid);
+        s = squares_again(join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k)), s);
+    }
+    s = row_sum(s, part[1], tid, nt);
+    const float rstd2 = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
+
+    auto emit = [&](int i, float4 h) {
+        if (a.h) store_row4<T, VEC>(static_cast<T*>(a.h) + row * k, i, k, h);
+        const float4 w = load_row4<float, VEC>(a.w, i, k);
+        const float4 z = make_float4(h.x * rstd2 * w.x, h.y * rstd2 * w.y, h.z * rstd2 * w.z, h.w * rstd2 * w.w);
+        if (a.y) store_row4<T, VEC>(static_cast<T*>(a.y) + row * k, i, k, z);
+        if (a.act || a.q) quantize4(a, row, i, i < k, z);
+    };
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+        if (c < chunks) emit(4 * (c * nt + tid), v[c]);
+    for (int c = NV; c < chunks; ++c) {
+        const int i = 4 * (c * nt + tid);
+        emit(i, join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k)));
+    }
+}
+
+template <typename T, int NV>
+cudaError_t block_norm_go(const BlockNormArgs& b, int m, int nt, bool vec, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(m);
+    cfg.blockDim = dim3(nt);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return vec ? cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, true, 1024>, b) : cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, false, 1024>, b);
+}
+
+template <typename T>
+cudaError_t block_norm_type(const BlockNormArgs& b, int m, cudaStream_t s) {
+    const NormArgs& a = b.n;
+    auto al = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const size_t n = 4 * sizeof(T);
+    const bool vec = a.k % 4 == 0 && a.xs % 4 == 0 && b.bs % 4 == 0 && (!b.gate || b.gs % 4 == 0) && al(a.x, n) && al(b.block, n) &&
+                     al(b.gate, n) && al(a.h, n) && al(a.y, n) && al(a.w, 16) && al(b.post, 16);
+    const int k4 = (a.k + 3) / 4;
+    auto threads = [&](int nv) { return ((k4 + nv - 1) / nv + 31) / 32 * 32; };
+    if (m <= 152 && threads(1) <= 1024) return block_norm_go<T, 1>(b, m, threads(1), vec, s);
+    if (threads(4) <= 1024) return block_norm_go<T, 4>(b, m, threads(4), vec, s);
+    return block_norm_go<T, 8>(b, m, threads(8) < 1024 ? threads(8) : 1024, vec, s);
+}
+
 // Eight threads a block, four values each.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* act, long long blocks, T* out) {
@@ -230,6 +354,16 @@ cudaError_t launch_rmsnorm(const void* x, long long xs, const void* r, long long
     if (type == GQ_F32) return norm_type<float>(a, m, s);
     if (type == GQ_F16) return norm_type<__half>(a, m, s);
     return norm_type<__nv_bfloat16>(a, m, s);
+}
+
+cudaError_t launch_block_norm(const void* block, long long bs, const void* x, long long xs, const float* post, const void* gate, long long gs,
+                              float block_scale, float residual_scale, const float* w, float eps, int type, int m, int k, void* h,
+                              void* y, void* act, uint16_t* d, int8_t* q, uint16_t* op, cudaStream_t s) {
+    const BlockNormArgs b = {{x, nullptr, w, xs, 0, eps, k, h, y, static_cast<uint8_t*>(act), d, q, op, static_cast<size_t>(m) * k},
+                             block, bs, post, gate, gs, block_scale, residual_scale};
+    if (type == GQ_F32) return block_norm_type<float>(b, m, s);
+    if (type == GQ_F16) return block_norm_type<__half>(b, m, s);
+    return block_norm_type<__nv_bfloat16>(b, m, s);
 }
 
 cudaError_t launch_dequantize_q8_0(const void* act, long long blocks, int type, void* out, cudaStream_t s) {

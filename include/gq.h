@@ -412,6 +412,75 @@ int gq_rmsnorm(const void* x_device, long long x_stride, const void* residual_de
                void* act_device, uint16_t* d_device, int8_t* q_device, uint16_t* mma_operand_device,
                gq_stream_t stream);
 
+/* The norm after a block, the block's gate, the residual stream's addition and the norm before the next block, in one pass:
+ *   n = y * (1 / sqrt(sum y^2 / k + eps)) * post_weight   (post_weight NULL: n = y),
+ *   h = residual_scale * x + block_scale * (gate * n)     (gate NULL: 1),
+ *   z = h * (1 / sqrt(sum h^2 / k + eps)) * weight,        each step rounded to f32.
+ *   block_device [m, k] of `type`: y, what the block gave; x_device [m, k]: the stream; rows block_stride and x_stride elements apart;
+ *   gate_device NULL or [m, k] of `type`, rows gate_stride apart, 0: one row for all; post_weight_device (or NULL) and weight_device k f32.
+ *   Outputs as gq_rmsnorm's: sum_device receives h (it may be x_device or block_device itself if those rows are contiguous), the others z.
+ *   Two calls on the same inputs give the same bits.
+ * Errors: as gq_rmsnorm; GQ_EINVAL_SHAPE for scales that are not finite too, GQ_EINVAL_PTR where sum_device is gate_device. */
+int gq_rmsnorm_block(const void* block_device, long long block_stride, const void* x_device, long long x_stride,
+                     const float* post_weight_device, const void* gate_device, long long gate_stride, float block_scale,
+                     float residual_scale, const float* weight_device, float eps, int type, int m, int k, void* sum_device,
+                     void* y_device, void* act_device, uint16_t* d_device, int8_t* q_device, uint16_t* mma_operand_device,
+                     gq_stream_t stream);
+
+/* Functions of an epilogue. */
+enum gq_function {
+    GQ_FN_NONE = 0,
+    GQ_FN_RELU = 1,        /* max(z, 0)                                                      */
+    GQ_FN_RELU2 = 2,       /* max(z, 0)^2                                                    */
+    GQ_FN_SILU = 3,        /* z / (1 + e^-z)                                                 */
+    GQ_FN_GELU = 4,        /* z * (1 + erf(z / sqrt 2)) / 2                                  */
+    GQ_FN_GELU_TANH = 5    /* z * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2            */
+};
+
+/* Q1_0 products over `cols` Q8_0 activation vectors with an epilogue, from one decoded token to long prompts.
+ *   z[c, r] = sum over the row's Q1_0 blocks i of d0 * sum over k of d1 * (sum of +-q over the 32)   (as q1_q8_gemm defines it, without
+ *             its order of roundings; -128 is negated to 128 here) + bias[r];
+ *   q1_q8_linear: y[c, r] = function(z[c, r]) + residual[c, r];
+ *   q1_q8_glu:    y[c, r] = function(z_gate[c, r]) * z_up[c, r]   (a gated feed-forward block up to its down product).
+ *   packed_*_device from gq_q1_0_pack(rows, n), finite scales; act_device: cols * n/32 Q8_0 blocks, vector after vector (2-byte aligned);
+ *   bias*_device NULL or rows f32; residual_device NULL or [cols, rows] of `type`, rows residual_stride elements apart.
+ *   Outputs, either may be NULL: y_device [cols, rows] of `type`, rows y_stride elements apart (it may be residual_device with the same
+ *   stride); blocks_device cols * rows/32 Q8_0 blocks, as the products and gq_dequantize_q8_0 take them, quantized in f32 by
+ *   the rule stated at gq_quantize_q8_0 (a block with a NaN has a NaN scale).
+ *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's sizes and type (both calls take the same), 16-byte aligned,
+ *   overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
+ * Precision: activations are exact where they are not below 2^-20 of their vector's largest (there: off by at most 2^-39 of it); where
+ *   the only output is bf16 they are rounded to 12 bits.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 128
+ *   weights, of 512 for bf16), everything after them f32, rounded once.  The same inputs give the same bits.  A vector with a scale that is not finite gives no numbers,
+ *   and leaves the others as they are.
+ * Errors: GQ_EINVAL_SHAPE if rows < 1, n < 128, n % 128 != 0, n > 2^20, cols < 1, cols > 2^20, a stride < rows or blocks_device with
+ *         rows % 32 != 0; GQ_EUNSUPPORTED for another type or function; GQ_EINVAL_PTR for NULL or misaligned pointers (packed weights
+ *         and workspace 16 bytes, others their elements), no output, or y_device = residual_device with another stride; GQ_ECUDA. */
+size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type);   /* 0 for invalid sizes */
+int q1_q8_linear(const void* packed_w_device, const void* act_device, int rows, int n, int cols, const float* bias_device,
+                 int function, const void* residual_device, long long residual_stride, int type, void* y_device,
+                 long long y_stride, void* blocks_device, void* workspace_device, gq_stream_t stream);
+int q1_q8_glu(const void* packed_gate_device, const void* packed_up_device, const void* act_device, int rows, int n, int cols,
+              const float* bias_gate_device, const float* bias_up_device, int function, int type, void* y_device,
+              long long y_stride, void* blocks_device, void* workspace_device, gq_stream_t stream);
+
+/* What a decoder answers: of each row of logits, with p = softmax(scale * x) in f32,
+ *   logprob_device[i] = ln p of token tokens_device[i] (int64; a negative one: 0; one >= vocab: NaN, and GQ_DEVERR_INDEX is set);
+ *   entropy_device[i] = -sum p ln p;
+ *   top_ids_device[i, j], top_logprobs_device[i, j], j < top: the largest logits, largest first, of equal ones (as stored; -0 is 0) the
+ *   lower index first, and their ln p.
+ *   logits_device [m, vocab] of `type`, rows `stride` elements apart, any alignment of the rows.  scale is 1 / temperature.  tokens and
+ *   logprob both or neither; entropy may be NULL.  A logit of -inf has no weight; a row of nothing else gives -inf for every token and
+ *   entropy 0.  A row with NaN or +inf gives NaN (its alternatives in order, NaN first).
+ *   workspace_device: gq_logprobs_workspace_bytes(m, vocab, top) bytes, 16-byte aligned, overwritten; calls that share it must not overlap
+ *   on the GPU.  The same inputs give the same bits.
+ * Errors: GQ_EINVAL_SHAPE unless 1 <= m <= 2^24, 1 <= vocab <= 2^20, 0 <= top <= min(32, vocab), stride >= vocab, scale positive and
+ *         finite; GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR for NULL or misaligned pointers or no output; GQ_ECUDA. */
+size_t gq_logprobs_workspace_bytes(int m, int vocab, int top);   /* 0 for invalid sizes */
+int gq_logprobs(const void* logits_device, long long stride, int type, int m, int vocab, float scale, const int64_t* tokens_device,
+                float* logprob_device, float* entropy_device, int top, int64_t* top_ids_device, float* top_logprobs_device,
+                void* workspace_device, gq_stream_t stream);
+
 /* The values code * d of Q8_0 blocks (34 bytes, 2-byte aligned), `blocks` of them one after another,
  * as 32 values of `type` each (16-byte aligned).
  * Errors: GQ_EINVAL_SHAPE unless 1 <= blocks <= 2^40, GQ_EUNSUPPORTED for another type, GQ_EINVAL_PTR, GQ_ECUDA. */
