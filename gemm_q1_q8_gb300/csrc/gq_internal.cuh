@@ -44,6 +44,7 @@ unsigned error_read_clear_kv();
 unsigned error_read_clear_attn();
 unsigned error_read_clear_attn_tiles();
 unsigned error_read_clear_logprobs();
+unsigned error_read_clear_linear_tiles();
 
 // Raises a kernel's limit of dynamic shared memory, once on each device (the limit belongs to the device; `done` is the kernel's own word).
 template <typename K>

@@ -236,17 +236,27 @@ cudaError_t rows_tokens(const LinearArgs& a, cudaStream_t s) {
     const int columns = a.cols * PARTS;
     if (columns <= 8) return rows_go<1, PARTS, PAIR>(a, s);
     if (columns <= 16) return rows_go<2, PARTS, PAIR>(a, s);
-    if (columns <= 32) return rows_go<4, PARTS, PAIR>(a, s);
-    return rows_go<8, PARTS, PAIR>(a, s);
+    return rows_go<4, PARTS, PAIR>(a, s);
 }
 
 }  // namespace
 
+// From this many columns on (tokens times parts) the tiles take over
+constexpr int kRowColumns = 32;
+
 cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s) {
-    if (linear_parts(a) == 1) return pair ? rows_tokens<1, true>(a, s) : rows_tokens<1, false>(a, s);
+    const int parts = linear_parts(a);
+    if (a.cols * parts > kRowColumns) return launch_linear_tiles(a, pair, s);
+    if (parts == 1) return pair ? rows_tokens<1, true>(a, s) : rows_tokens<1, false>(a, s);
     return pair ? rows_tokens<2, true>(a, s) : rows_tokens<2, false>(a, s);
 }
 
-size_t linear_workspace_bytes(int, int, int, int) { return 16; }
+size_t linear_workspace_bytes(int rows, int n, int cols, int type) {
+    // bf16 may take one part or, with Q8_0 outputs, two
+    size_t need = 16;
+    for (int parts = type == GQ_BF16 ? 1 : 2; parts <= 2; ++parts)
+        if (static_cast<long long>(cols) * parts > kRowColumns) need = std::max(need, linear_tiles_workspace_bytes(rows, n, cols, parts));
+    return need;
+}
 
 }  // namespace gq

@@ -10,6 +10,8 @@
 // cores truncate the sum that they add to, so it goes to registers every few blocks of 128 (a chain of n steps costs n / 3 * 2^-23).
 #pragma once
 
+#include <algorithm>
+
 #include "layer_ops.cuh"
 
 namespace gq {
@@ -31,6 +33,8 @@ struct LinearArgs {
 
 cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s);
 size_t linear_workspace_bytes(int rows, int n, int cols, int type);
+cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s);
+size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts);
 
 namespace {
 
@@ -45,6 +49,21 @@ __device__ __forceinline__ float bend(float z, int function) {
         case GQ_FN_GELU: return 0.5f * z * erfcf(z * -0.70710678f);              // no cancellation below zero
         case GQ_FN_GELU_TANH: return __fdividef(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));   // z * sigmoid(2u)
         default: return z;
+    }
+}
+
+// The same of several values: one branch, and their chains beside one another
+template <int N>
+__device__ __forceinline__ void bend_all(float (&z)[N], int function) {
+    switch (function) {
+#define GQ_BEND(f) case f: _Pragma("unroll") for (int i = 0; i < N; ++i) z[i] = bend(z[i], f); break
+        GQ_BEND(GQ_FN_RELU);
+        GQ_BEND(GQ_FN_RELU2);
+        GQ_BEND(GQ_FN_SILU);
+        GQ_BEND(GQ_FN_GELU);
+        GQ_BEND(GQ_FN_GELU_TANH);
+#undef GQ_BEND
+        default: break;
     }
 }
 

@@ -1,0 +1,524 @@
+// Q1_0 products with an epilogue, many tokens: tcgen05 (kind::f16), weights as +-d0 in tensor memory.
+//
+// A first kernel writes the activations' f16 parts (linear.cuh) once, in the order in which a sign word's bits become pairs.  A tile of the second
+// is two 128-row matrices (gate and up of a pair, or two neighbouring row tiles) by BN tokens, so that a copied activation meets 256 rows.
+// Roles of a thread block (one an SM, tiles in turn):
+//   warp 0: MMAs.  A stage is 64 of n: four steps of 16 for each part, first one matrix, then the other.
+//   warp 1: TMA copies of the stage's parts (128-byte swizzle)
+//   warps 4-7: weights.  A thread has one row of each matrix; two words of signs become 32 registers of +-d0 pairs by a shift and a logic
+//              operation each, and go to the stage's slot of tensor memory (the operand A), so shared memory is read for B alone
+//   warps 8-15: sums.  A round is 128 of n (512 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so it
+//              leaves tensor memory after each round and is added in registers; one matrix is drained while the other's MMAs run.  Behind the
+//              last round the function, the residual, the conversion and the stores, while the next tile's MMAs start.
+// Tensor memory: 2 x 128 columns of sums, 4 stages x 64 columns of weights.  Where the tiles are fewer than the SMs, n is cut into equal
+// shares, whose sums a third kernel adds in order before the epilogue.
+#include "linear.cuh"
+#include "tc_common.cuh"
+
+namespace gq {
+GQ_ERROR_ACCESSOR(linear_tiles)
+
+namespace {
+
+constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
+constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
+constexpr int kSlotB = 2 * 128 * BK * 2;                                   // two parts of up to 128 tokens
+constexpr int kWarpA0 = 4, kWarpE0 = 8, kEWarps = 8, kThreads = 512;
+constexpr int kRegsSums = 168, kRegsRest = 88;                             // 8 warps each: 65536 registers in all
+static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
+static_assert((kRegsSums + kRegsRest) * 256 <= 65536, "registers");
+
+struct Bars {
+    uint64_t full[kStages];            // four weight warps, the copy's expect_tx and its bytes
+    uint64_t done[kStages];            // the stage's MMAs are complete
+    uint64_t accfull[2], accempty[2];  // a matrix's round is complete; drained
+    uint64_t final_;
+    int last_copy[kStages];            // the last copy into each slot, -1: none
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Plan {
+    int row_tiles, tok_tiles, splits, units, rounds_stages, parts, pad_rows;
+    const float* scale;                // a token's power of two, undone after the sums
+    float* partial;                    // [split][matrix][token][pad_rows], splits > 1
+};
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {     // 32 lanes x 16 columns
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A unit's tile and its stages [k0, k1)
+struct Unit { int row_tile, tok0, split, k0, k1; };
+template <int BN>
+__device__ __forceinline__ Unit unit_of(const Plan& p, int u, int nb) {
+    const int split = u % p.splits, tile = u / p.splits;
+    Unit r;
+    r.row_tile = tile % p.row_tiles;
+    r.tok0 = tile / p.row_tiles * BN;
+    r.split = split;
+    r.k0 = 2 * static_cast<int>(static_cast<long long>(nb) * split / p.splits);
+    r.k1 = 2 * static_cast<int>(static_cast<long long>(nb) * (split + 1) / p.splits);
+    return r;
+}
+
+// What is left to do with the sums of one row (a lane) and up to N neighbouring tokens
+template <bool PAIR, int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, float (&y)[N], const float (&z1)[N], int row, size_t tok, int count, int lane) {
+    const bool there = row < a.rows;
+    float r[N];
+    if (!PAIR && a.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = there && i < count ? load_typed(a.residual, (tok + i) * a.residual_stride + row, a.type) : 0.f;
+    }
+    bend_all(y, a.function);
+    if (PAIR) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] *= z1[i];
+    } else if (a.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] += r[i];
+    }
+    if (a.y && there) {
+        const size_t at = tok * a.y_stride + row;
+        if (a.type == GQ_F32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) if (i < count) static_cast<float*>(a.y)[at + i * a.y_stride] = y[i];
+        } else if (a.type == GQ_F16) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) if (i < count) static_cast<__half*>(a.y)[at + i * a.y_stride] = __float2half_rn(y[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) if (i < count) static_cast<__nv_bfloat16*>(a.y)[at + i * a.y_stride] = __float2bfloat16_rn(y[i]);
+        }
+    }
+    if (a.blocks && __shfl_sync(0xffffffffu, there, 0)) {
+        uint8_t* block = a.blocks + (tok * (a.rows / 32) + row / 32) * 34;
+#pragma unroll
+        for (int i = 0; i < N; ++i) if (i < count) store_block(block + static_cast<size_t>(i) * (a.rows / 32) * 34, y[i], lane);
+    }
+}
+
+template <int BN, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_constant__ CUtensorMap tmB, const LinearArgs a, const Plan plan) {
+    constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);   // f32 += f16 x f16
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sB = smem_align1024(smem_raw);                                // [kStages][part][BN rows of 128 bytes]
+    Bars* bars = reinterpret_cast<Bars*>(sB + kStages * kSlotB);
+    volatile int* abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nb = a.n / 128, parts = plan.parts, round = plan.rounds_stages;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars->full[s], 5);
+            mbar_init(&bars->done[s], 1);
+            bars->last_copy[s] = -1;
+        }
+        for (int m = 0; m < 2; ++m) {
+            mbar_init(&bars->accfull[m], 1);
+            mbar_init(&bars->accempty[m], kEWarps);
+        }
+        mbar_init(&bars->final_, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp >= kWarpE0) {
+        // ---------------- sums
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        constexpr int NC = BN / 2;                                         // columns of this warp, of each matrix
+        const int q = warp & 3, h = (warp - kWarpE0) >> 2;
+        const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * NC);
+        uint32_t turn = 0;                                                 // rounds so far
+        bool ok = true;
+        for (int u = blockIdx.x; u < plan.units && ok; u += gridDim.x) {
+            const Unit w = unit_of<BN>(plan, u, nb);
+            float acc[2][NC];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < NC; ++i) acc[m][i] = 0.f;
+            for (int k = w.k0; k < w.k1 && ok; k += round, ++turn) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    if (!wait_or_abort_sleep(&bars->accfull[m], turn & 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < NC; c += 16) {
+                        uint32_t v[16];
+                        ld16(at + static_cast<uint32_t>(m * kDCols + c), v);
+                        wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[m][c + i] += __uint_as_float(v[i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->accempty[m]);
+                }
+            }
+            if (!ok) break;
+            const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
+            const int tok0 = w.tok0 + h * NC;
+            if (plan.splits > 1) {
+                float* to = plan.partial + (static_cast<size_t>(w.split) * (PAIR ? 2 : 1) * a.cols + tok0) * plan.pad_rows;
+                const size_t second = PAIR ? static_cast<size_t>(a.cols) * plan.pad_rows : 0;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    if (tok0 + i >= a.cols) break;
+                    to[static_cast<size_t>(i) * plan.pad_rows + row0] = acc[0][i];
+                    if (PAIR || row1 < plan.pad_rows) to[second + static_cast<size_t>(i) * plan.pad_rows + row1] = acc[1][i];
+                }
+                continue;
+            }
+            const float b0 = a.bias[0] && row0 < a.rows ? a.bias[0][row0] : 0.f, b1 = a.bias[1] && row1 < a.rows ? a.bias[1][row1] : 0.f;
+            // eight tokens at a time, in a loop: unrolled whole it does not fit the instruction cache (4096 tokens, 14336 x 4096, bf16:
+            // 2074 us).  The registers of a step are chosen by selects.
+#pragma unroll 1
+            for (int c = 0; c < NC; c += 8) {
+                const int tok = tok0 + c, count = a.cols - tok;
+                if (count <= 0) break;
+                float z0[8], z1[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s = i < count ? plan.scale[tok + i] : 0.f;
+                    float v0 = acc[0][i], v1 = acc[1][i];
+#pragma unroll
+                    for (int o = 8; o < NC; o += 8) {
+                        v0 = c == o ? acc[0][o + i] : v0;
+                        v1 = c == o ? acc[1][o + i] : v1;
+                    }
+                    z0[i] = fmaf(v0, s, b0);                               // the product is exact
+                    z1[i] = fmaf(v1, s, b1);
+                }
+                finish<PAIR>(a, z0, z1, row0, tok, count, lane);
+                if (!PAIR) finish<PAIR>(a, z1, z1, row1, tok, count, lane);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == 0) {
+            // ---------------- MMAs
+            if (lane == 0) {
+                uint32_t g = 0, turn = 0;
+                bool live = true;
+                for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
+                    const Unit w = unit_of<BN>(plan, u, nb);
+                    for (int k = w.k0, r = 0; k < w.k1 && live; ++k, ++g) {
+                        const int s = g % kStages;
+                        if (!wait_or_abort(&bars->full[s], (g / kStages) & 1u, abort)) {
+                            live = false;
+                            break;
+                        }
+                        const bool first = r == 0, last = r == round - 1 || k == w.k1 - 1;
+                        const uint64_t bdesc = smem_desc(sB + s * kSlotB);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            if (first && turn > 0 && !wait_or_abort(&bars->accempty[m], (turn - 1) & 1u, abort)) {
+                                live = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t d = tmem + static_cast<uint32_t>(m * kDCols), av = tmem + static_cast<uint32_t>(kA0 + (2 * s + m) * kACols);
+                            for (int p = 0; p < parts; ++p)
+#pragma unroll
+                                for (int j = 0; j < BK / 16; ++j)
+                                    mma_ts(d, av + static_cast<uint32_t>(j * 8), bdesc + static_cast<uint64_t>((p * BN * 128 + j * 32) >> 4), kIdesc,
+                                           first && p == 0 && j == 0 ? 0u : 1u);
+                            if (last) tc_commit(&bars->accfull[m]);
+                        }
+                        if (live) tc_commit(&bars->done[s]);
+                        r = last ? 0 : r + 1;
+                        turn += last;
+                    }
+                }
+                tc_commit(&bars->final_);
+            }
+        } else if (warp == 1) {
+            // ---------------- copies of the activations
+            if (lane == 0) {
+                prefetch_tmap(&tmB);
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                uint32_t g = 0;
+                bool live = true;
+                for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
+                    const Unit w = unit_of<BN>(plan, u, nb);
+                    for (int k = w.k0; k < w.k1; ++k, ++g) {
+                        const int s = g % kStages;
+                        if (g >= kStages && !wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort)) {
+                            live = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bars->full[s], static_cast<uint32_t>(parts * BN * 128));
+                        for (int p = 0; p < parts; ++p)
+                            tma_load_2d(sB + s * kSlotB + p * BN * 128, &tmB, k * BK, p * a.cols + w.tok0, &bars->full[s]);
+                        bars->last_copy[s] = static_cast<int>(g);
+                    }
+                }
+            }
+        } else if (warp >= kWarpA0) {
+            // ---------------- weights
+            const int r = (warp & 3) * 32 + lane;
+            const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kA0;
+            const int tiles = (a.rows + BM - 1) / BM;
+            uint32_t g = 0;
+            bool live = true;
+            for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
+                const Unit w = unit_of<BN>(plan, u, nb);
+                const uint8_t* src[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    src[m] = a.w[m] + static_cast<size_t>(PAIR ? w.row_tile : min(2 * w.row_tile + m, tiles - 1)) * nb * kChunkBytes;
+                uint4 bits[2];
+                uint32_t d0[2];
+                auto load = [&](int b) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint8_t* ch = src[m] + static_cast<size_t>(b) * kChunkBytes;
+                        bits[m] = *reinterpret_cast<const uint4*>(ch + r * 16);
+                        d0[m] = *reinterpret_cast<const uint16_t*>(ch + BM * 16 + r * 2);
+                    }
+                };
+                load(w.k0 / 2);
+                for (int k = w.k0; k < w.k1 && live; k += 2) {
+                    uint4 now[2];
+                    uint32_t neg[2];                                       // a clear bit gives -d0
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        now[m] = bits[m];
+                        neg[m] = (d0[m] * 0x00010001u) ^ 0x80008000u;
+                    }
+                    if (k + 2 < w.k1) load(k / 2 + 1);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half, ++g) {
+                        const int s = g % kStages;
+                        if (g >= kStages && !wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort)) {
+                            live = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t w2[2] = {half ? now[m].z : now[m].x, half ? now[m].w : now[m].y};
+                            uint32_t av[32];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int p = 0; p < 16; ++p) av[16 * i + p] = ((w2[i] << (15 - p)) & 0x80008000u) ^ neg[m];
+                            tc_st32(at + static_cast<uint32_t>((2 * s + m) * kACols), av);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->full[s]);
+                    }
+                }
+            }
+        }
+    }
+
+    // ---------------- teardown
+    __syncwarp();
+    if (warp == 0) {
+        if (lane == 0 && !mbar_wait(&bars->final_, 0)) report_error(kErrMmaTimeout);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 32 && *abort) {
+        // an aborted block may hold copies that no MMA waited for
+        for (int s = 0; s < kStages; ++s) {
+            const int g = bars->last_copy[s];
+            if (g >= 0 && !mbar_wait(&bars->full[s], static_cast<uint32_t>(g / kStages) & 1u)) report_error(kErrDrainTimeout);
+        }
+    }
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    __syncthreads();
+}
+
+// The f16 parts [part][token][n] of the activations, and each token's power of two.  One block a token.  In a 32-block, place 2 p + i holds
+// element 4 (p % 8) + p / 8 + 2 i, as bits p and p + 16 of a packed sign word.
+constexpr int kSplitThreads = 256;
+__global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const uint8_t* act, int nb32, int cols, int parts, uint32_t* out, float* scale) {
+    __shared__ uint32_t largest[kSplitThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const size_t tok = blockIdx.x;
+    const uint8_t* p = act + tok * nb32 * 34;
+    uint32_t top = 0;
+    for (int b = threadIdx.x; b < nb32; b += kSplitThreads) top = max(top, *reinterpret_cast<const uint16_t*>(p + static_cast<size_t>(b) * 34) & 0x7fffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSplitThreads / 32; ++i) top = max(top, largest[i]);
+    const int shift = token_shift(top);
+    if (threadIdx.x == 0) scale[tok] = pow2(-shift);
+    uint32_t* row = out + tok * nb32 * 16;
+    const size_t second = static_cast<size_t>(cols) * nb32 * 16;
+    for (int i = threadIdx.x; i < nb32 * 8; i += kSplitThreads) {
+        const uint16_t* blk = reinterpret_cast<const uint16_t*>(p + static_cast<size_t>(i >> 3) * 34);
+        const int l = i & 7;
+        const float d = f16_to_f32(blk[0]) * pow2(shift);
+        const uint32_t lo = blk[1 + 2 * l], hi = blk[2 + 2 * l];
+        const float v[4] = {d * static_cast<float>(static_cast<int8_t>(lo & 0xff)), d * static_cast<float>(static_cast<int8_t>(lo >> 8)),
+                            d * static_cast<float>(static_cast<int8_t>(hi & 0xff)), d * static_cast<float>(static_cast<int8_t>(hi >> 8))};
+        uint16_t h[4], low[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) two_parts(v[e], h[e], low[e]);
+        uint32_t* to = row + static_cast<size_t>(i >> 3) * 16 + l;
+        to[0] = h[0] | static_cast<uint32_t>(h[2]) << 16;
+        to[8] = h[1] | static_cast<uint32_t>(h[3]) << 16;
+        if (parts == 2) {
+            to[second] = low[0] | static_cast<uint32_t>(low[2]) << 16;
+            to[second + 8] = low[1] | static_cast<uint32_t>(low[3]) << 16;
+        }
+    }
+}
+
+// The shares' sums in order, and the epilogue.  A warp has 32 rows of a token.
+template <bool PAIR>
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const Plan plan) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, groups = (a.rows + 31) / 32;
+    const long long id = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+    if (id >= static_cast<long long>(groups) * a.cols) return;
+    const size_t tok = id / groups;
+    const int row = static_cast<int>(id % groups) * 32 + lane;
+    const size_t matrix = static_cast<size_t>(a.cols) * plan.pad_rows;
+    const float* from = plan.partial + tok * plan.pad_rows + row;
+    float z0 = 0.f, z1 = 0.f;
+    for (int s = 0; s < plan.splits; ++s) {
+        z0 += from[(PAIR ? 2 : 1) * s * matrix];
+        if (PAIR) z1 += from[(2 * s + 1) * matrix];
+    }
+    const float sc = plan.scale[tok];
+    const bool there = row < a.rows;
+    float y[1] = {fmaf(z0, sc, a.bias[0] && there ? a.bias[0][row] : 0.f)};
+    const float up[1] = {fmaf(z1, sc, PAIR && a.bias[1] && there ? a.bias[1][row] : 0.f)};
+    finish<PAIR>(a, y, up, row, tok, 1, lane);
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kSMs = 152;
+
+struct Shape { int bn; Plan p; };
+// Tokens a tile and shares of n.  An MMA of 128, 96 or 64 tokens takes 64, 48 or 46 cycles: the tile whose waves take the fewest is taken.  Where
+// the tiles of one wave leave SMs idle, n is cut into shares of at least two blocks.
+Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
+    const int tiles = (rows + BM - 1) / BM;
+    Shape best = {};
+    long long least = -1;
+    for (int bn : {128, 96, 64}) {
+        Plan p = {};
+        p.row_tiles = pair ? tiles : (tiles + 1) / 2;
+        p.tok_tiles = (cols + bn - 1) / bn;
+        const long long all = static_cast<long long>(p.row_tiles) * p.tok_tiles;
+        const int nb = n / 128;
+        p.splits = 1;
+        if (all < kSMs) p.splits = std::max(1, std::min<int>(kSMs / static_cast<int>(all), nb / 2));
+        const long long units = all * p.splits, waves = (units + kSMs - 1) / kSMs;
+        const long long cost = waves * ((nb + p.splits - 1) / p.splits) * (bn == 128 ? 64 : bn == 96 ? 48 : 46);
+        if (least < 0 || cost < least) {
+            least = cost;
+            p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
+            p.parts = parts;
+            p.rounds_stages = parts == 2 ? 2 : 8;
+            p.pad_rows = tiles * BM;
+            best = {bn, p};
+        }
+    }
+    return best;
+}
+
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
+size_t parts_bytes(int n, int cols) { return up(static_cast<size_t>(2) * cols * n * 2); }
+
+template <int BN, bool PAIR>
+cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cudaStream_t s) {
+    CUtensorMap tmB;
+    if (!make_tmap_2d(&tmB, parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, static_cast<uint64_t>(a.n), static_cast<uint64_t>(p.parts) * a.cols,
+                      static_cast<uint64_t>(a.n) * 2, BK, BN, true))
+        return cudaErrorInvalidValue;
+    constexpr size_t smem = 1024 + static_cast<size_t>(kStages) * kSlotB + sizeof(Bars);
+    static std::atomic<uint64_t> raised{0};
+    cudaError_t e = allow_smem(linear_tiles_kernel<BN, PAIR>, smem, raised);
+    if (e != cudaSuccess) return e;
+    e = launch(linear_tiles_kernel<BN, PAIR>, static_cast<unsigned>(std::min(p.units, kSMs)), kThreads, smem, s, tmB, a, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const long long warps = static_cast<long long>((a.rows + 31) / 32) * a.cols;
+    return launch(linear_join_kernel<PAIR>, static_cast<unsigned>((warps + 7) / 8), 256, 0, s, a, p);
+}
+
+}  // namespace
+
+size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts) {
+    size_t partial = 0;
+    for (int pair = 0; pair < 2; ++pair) {
+        const Plan p = shape_of(rows, n, cols, parts, pair).p;
+        if (p.splits > 1) partial = std::max(partial, static_cast<size_t>(p.splits) * (pair ? 2 : 1) * cols * p.pad_rows * 4);
+    }
+    return parts_bytes(n, cols) + up(static_cast<size_t>(cols) * 4) + partial;
+}
+
+cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s) {
+    Shape t = shape_of(a.rows, a.n, a.cols, linear_parts(a), pair);
+    uint8_t* work = static_cast<uint8_t*>(a.workspace);
+    float* scale = reinterpret_cast<float*>(work + parts_bytes(a.n, a.cols));
+    t.p.scale = scale;
+    t.p.partial = reinterpret_cast<float*>(work + parts_bytes(a.n, a.cols) + up(static_cast<size_t>(a.cols) * 4));
+    const cudaError_t e = launch(linear_split_kernel, static_cast<unsigned>(a.cols), kSplitThreads, 0, s, a.act, a.n / 32, a.cols, t.p.parts,
+                                 reinterpret_cast<uint32_t*>(work), scale);
+    if (e != cudaSuccess) return e;
+    if (pair) return t.bn == 128 ? tiles_go<128, true>(a, t.p, work, s) : t.bn == 96 ? tiles_go<96, true>(a, t.p, work, s) : tiles_go<64, true>(a, t.p, work, s);
+    return t.bn == 128 ? tiles_go<128, false>(a, t.p, work, s) : t.bn == 96 ? tiles_go<96, false>(a, t.p, work, s) : tiles_go<64, false>(a, t.p, work, s);
+}
+
+}  // namespace gq
