@@ -3,8 +3,8 @@
 // A first kernel writes the activations' f16 parts (linear.cuh) once, in the order in which a sign word's bits become pairs.  A tile of the second
 // is two 128-row matrices (gate and up of a pair, or two neighbouring row tiles) by BN tokens, so that a copied activation meets 256 rows.
 // Roles of a thread block (one an SM, tiles in turn):
-//   warp 0: MMAs.  A stage is 64 of n: four steps of 16 for each part, first one matrix, then the other.
-//   warp 1: TMA copies of the stage's parts (128-byte swizzle)
+//   warps 0, 1: MMAs, a warp for each matrix.  A stage is 64 of n: four steps of 16 for each part.
+//   warp 2: TMA copies of the stage's parts (128-byte swizzle)
 //   warps 4-7: weights.  A thread has one row of each matrix; two words of signs become 32 registers of +-d0 pairs by a shift and a logic
 //              operation each, and go to the stage's slot of tensor memory (the operand A), so shared memory is read for B alone
 //   warps 8-15: sums.  A round is 128 of n (512 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so it
@@ -22,35 +22,49 @@ namespace {
 
 constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
 constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
-constexpr int kSlotB = 2 * 128 * BK * 2;                                   // two parts of up to 128 tokens
+constexpr int kTileB = 128 * BK * 2, kTilesB = 12;                         // a part of up to 128 tokens; room for 6 or 12 stages
 constexpr int kWarpA0 = 4, kWarpE0 = 8, kEWarps = 8, kThreads = 512;
 constexpr int kRegsSums = 168, kRegsRest = 88;                             // 8 warps each: 65536 registers in all
 static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
 static_assert((kRegsSums + kRegsRest) * 256 <= 65536, "registers");
 
 struct Bars {
-    uint64_t full[kStages];            // four weight warps, the copy's expect_tx and its bytes
-    uint64_t done[kStages];            // the stage's MMAs are complete
+    uint64_t full[kStages];            // four weight warps
+    uint64_t done[kStages];            // both matrices' MMAs of the stage are complete: its weights' slot is free
+    uint64_t bfull[kTilesB];           // the copy's expect_tx and its bytes
+    uint64_t bdone[kTilesB];           // as done, of the copy's slot
     uint64_t accfull[2], accempty[2];  // a matrix's round is complete; drained
     uint64_t final_;
-    int last_copy[kStages];            // the last copy into each slot, -1: none
+    int last_copy[kTilesB];            // the last copy into each slot, -1: none
     uint32_t tmem_base;
     int abort;
 };
 
 struct Plan {
-    int row_tiles, tok_tiles, splits, units, rounds_stages, parts, pad_rows;
+    int row_tiles, tok_tiles, splits, units, round, parts, pad_rows;
     const float* scale;                // a token's power of two, undone after the sums
     float* partial;                    // [split][matrix][token][pad_rows], splits > 1
 };
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Issued by the one lane whose `leader` is set, with the whole warp on the way: descriptors then stay in uniform registers (from a branch of one
+// lane an issue took 130 cycles: 4096 tokens, 14336 x 4096, bf16: 937 us)
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {     // 32 lanes x 16 columns
     asm volatile(
@@ -118,23 +132,27 @@ template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_constant__ CUtensorMap tmB, const LinearArgs a, const Plan plan) {
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);   // f32 += f16 x f16
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* sB = smem_align1024(smem_raw);                                // [kStages][part][BN rows of 128 bytes]
-    Bars* bars = reinterpret_cast<Bars*>(sB + kStages * kSlotB);
+    uint8_t* sB = smem_align1024(smem_raw);                                // [stage][part][BN rows of 128 bytes]
+    Bars* bars = reinterpret_cast<Bars*>(sB + kTilesB * kTileB);
     volatile int* abort = &bars->abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nb = a.n / 128, parts = plan.parts, round = plan.rounds_stages;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int nb = a.n / 128, parts = plan.parts, slots = kTilesB / parts, half_round = plan.round / 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 5);
-            mbar_init(&bars->done[s], 1);
+            mbar_init(&bars->full[s], 4);
+            mbar_init(&bars->done[s], 2);
+        }
+        for (int s = 0; s < kTilesB; ++s) {
+            mbar_init(&bars->bfull[s], 1);
+            mbar_init(&bars->bdone[s], 2);
             bars->last_copy[s] = -1;
         }
         for (int m = 0; m < 2; ++m) {
             mbar_init(&bars->accfull[m], 1);
             mbar_init(&bars->accempty[m], kEWarps);
         }
-        mbar_init(&bars->final_, 1);
+        mbar_init(&bars->final_, 2);
         bars->abort = 0;
         fence_barrier_init();
     }
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= kWarpE0) {
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
         constexpr int NC = BN / 2;                                         // columns of this warp, of each matrix
         const int q = warp & 3, h = (warp - kWarpE0) >> 2;
         const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * NC);
-        uint32_t turn = 0;                                                 // rounds so far
+        uint32_t turn[2] = {0, 0};                                         // rounds of each matrix so far
         bool ok = true;
         for (int u = blockIdx.x; u < plan.units && ok; u += gridDim.x) {
             const Unit w = unit_of<BN>(plan, u, nb);
@@ -166,27 +184,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < NC; ++i) acc[m][i] = 0.f;
-            for (int k = w.k0; k < w.k1 && ok; k += round, ++turn) {
+            auto drain = [&](int m, float (&sum)[NC]) {
+                ok = __all_sync(0xffffffffu, ok && wait_or_abort_sleep(&bars->accfull[m], turn[m] & 1u, abort));
+                if (!ok) return;
+                ++turn[m];
+                tc_fence_after();
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    if (!wait_or_abort_sleep(&bars->accfull[m], turn & 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int c = 0; c < NC; c += 16) {
+                    uint32_t v[16];
+                    ld16(at + static_cast<uint32_t>(m * kDCols + c), v);
+                    wait_ld();
 #pragma unroll
-                    for (int c = 0; c < NC; c += 16) {
-                        uint32_t v[16];
-                        ld16(at + static_cast<uint32_t>(m * kDCols + c), v);
-                        wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[m][c + i] += __uint_as_float(v[i]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->accempty[m]);
+                    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->accempty[m]);
+            };
+            // the second matrix's rounds end in the middle of the first one's
+            for (int k = half_round; k < w.k1 - w.k0; k += 2 * half_round) {
+                drain(1, acc[1]);
+                if (k + half_round < w.k1 - w.k0) drain(0, acc[0]);
             }
+            drain(0, acc[0]);
+            drain(1, acc[1]);
             if (!ok) break;
             const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
             const int tok0 = w.tok0 + h * NC;
@@ -227,62 +248,76 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == 0) {
-            // ---------------- MMAs
-            if (lane == 0) {
-                uint32_t g = 0, turn = 0;
-                bool live = true;
-                for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
-                    const Unit w = unit_of<BN>(plan, u, nb);
-                    for (int k = w.k0, r = 0; k < w.k1 && live; ++k, ++g) {
-                        const int s = g % kStages;
-                        if (!wait_or_abort(&bars->full[s], (g / kStages) & 1u, abort)) {
-                            live = false;
-                            break;
-                        }
-                        const bool first = r == 0, last = r == round - 1 || k == w.k1 - 1;
-                        const uint64_t bdesc = smem_desc(sB + s * kSlotB);
+        if (warp < 2) {
+            // ---------------- MMAs: an issuer for each matrix
+            const int m = warp;
+            const uint32_t leader = elect_one();
+            const uint32_t d = tmem + static_cast<uint32_t>(m * kDCols);
+            uint32_t g = 0, turn = 0, slot = 0, lap = 0;                   // lap: times around the copies' ring
+            bool live = true;
+            for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
+                const Unit w = unit_of<BN>(plan, u, nb);
+                int r = m * half_round;                                    // stages of the round
+                bool first = true;
+                for (int k = w.k0; k < w.k1; ++k, ++g) {
+                    const int s = g % kStages;
+                    const bool last = r == 2 * half_round - 1 || k == w.k1 - 1;
+                    const bool ready = wait_or_abort(&bars->bfull[slot], lap & 1u, abort) && wait_or_abort(&bars->full[s], (g / kStages) & 1u, abort) &&
+                                       (!first || turn == 0 || wait_or_abort(&bars->accempty[m], (turn - 1) & 1u, abort));
+                    if (!__all_sync(0xffffffffu, ready)) {
+                        live = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t bdesc = smem_desc(sB + slot * parts * kTileB);
+                    const uint32_t av = tmem + static_cast<uint32_t>(kA0 + (2 * s + m) * kACols);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            if (first && turn > 0 && !wait_or_abort(&bars->accempty[m], (turn - 1) & 1u, abort)) {
-                                live = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t d = tmem + static_cast<uint32_t>(m * kDCols), av = tmem + static_cast<uint32_t>(kA0 + (2 * s + m) * kACols);
-                            for (int p = 0; p < parts; ++p)
+                    for (int p = 0; p < 2; ++p) {
+                        if (p == parts) break;
 #pragma unroll
-                                for (int j = 0; j < BK / 16; ++j)
-                                    mma_ts(d, av + static_cast<uint32_t>(j * 8), bdesc + static_cast<uint64_t>((p * BN * 128 + j * 32) >> 4), kIdesc,
-                                           first && p == 0 && j == 0 ? 0u : 1u);
-                            if (last) tc_commit(&bars->accfull[m]);
-                        }
-                        if (live) tc_commit(&bars->done[s]);
-                        r = last ? 0 : r + 1;
-                        turn += last;
+                        for (int j = 0; j < BK / 16; ++j)
+                            mma_ts(leader, d, av + static_cast<uint32_t>(j * 8), bdesc + static_cast<uint64_t>((p * kTileB + j * 32) >> 4), kIdesc,
+                                   first && p == 0 && j == 0 ? 0u : 1u);
+                    }
+                    if (leader) {
+                        if (last) tc_commit(&bars->accfull[m]);
+                        tc_commit(&bars->done[s]);
+                        tc_commit(&bars->bdone[slot]);
+                    }
+                    __syncwarp();
+                    first = last;
+                    r = last ? 0 : r + 1;
+                    turn += last;
+                    if (++slot == slots) {
+                        slot = 0;
+                        ++lap;
                     }
                 }
-                tc_commit(&bars->final_);
             }
-        } else if (warp == 1) {
+            if (leader) tc_commit(&bars->final_);
+            __syncwarp();
+        } else if (warp == 2) {
             // ---------------- copies of the activations
             if (lane == 0) {
                 prefetch_tmap(&tmB);
                 asm volatile("griddepcontrol.wait;" ::: "memory");
-                uint32_t g = 0;
+                int slot = 0, lap = 0;
                 bool live = true;
                 for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
                     const Unit w = unit_of<BN>(plan, u, nb);
-                    for (int k = w.k0; k < w.k1; ++k, ++g) {
-                        const int s = g % kStages;
-                        if (g >= kStages && !wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort)) {
+                    for (int k = w.k0; k < w.k1; ++k) {
+                        if (lap > 0 && !wait_or_abort(&bars->bdone[slot], (lap - 1) & 1u, abort)) {
                             live = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&bars->full[s], static_cast<uint32_t>(parts * BN * 128));
+                        mbar_arrive_expect_tx(&bars->bfull[slot], static_cast<uint32_t>(parts * BN * 128));
                         for (int p = 0; p < parts; ++p)
-                            tma_load_2d(sB + s * kSlotB + p * BN * 128, &tmB, k * BK, p * a.cols + w.tok0, &bars->full[s]);
-                        bars->last_copy[s] = static_cast<int>(g);
+                            tma_load_2d(sB + (slot * parts + p) * kTileB, &tmB, k * BK, p * a.cols + w.tok0, &bars->bfull[slot]);
+                        bars->last_copy[slot] = lap;
+                        if (++slot == slots) {
+                            slot = 0;
+                            ++lap;
+                        }
                     }
                 }
             }
@@ -322,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
 #pragma unroll
                     for (int half = 0; half < 2; ++half, ++g) {
                         const int s = g % kStages;
-                        if (g >= kStages && !wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort)) {
+                        if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                             live = false;
                             break;
                         }
@@ -356,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 32 && *abort) {
+    if (threadIdx.x == 64 && *abort) {
         // an aborted block may hold copies that no MMA waited for
-        for (int s = 0; s < kStages; ++s) {
-            const int g = bars->last_copy[s];
-            if (g >= 0 && !mbar_wait(&bars->full[s], static_cast<uint32_t>(g / kStages) & 1u)) report_error(kErrDrainTimeout);
+        for (int s = 0; s < kTilesB; ++s) {
+            const int lap = bars->last_copy[s];
+            if (lap >= 0 && !mbar_wait(&bars->bfull[s], static_cast<uint32_t>(lap) & 1u)) report_error(kErrDrainTimeout);
         }
     }
     if (warp == 0)
@@ -470,7 +505,7 @@ Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
             least = cost;
             p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
             p.parts = parts;
-            p.rounds_stages = parts == 2 ? 2 : 8;
+            p.round = parts == 2 ? 2 : 1024;
             p.pad_rows = tiles * BM;
             best = {bn, p};
         }
@@ -487,7 +522,7 @@ cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cuda
     if (!make_tmap_2d(&tmB, parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, static_cast<uint64_t>(a.n), static_cast<uint64_t>(p.parts) * a.cols,
                       static_cast<uint64_t>(a.n) * 2, BK, BN, true))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = 1024 + static_cast<size_t>(kStages) * kSlotB + sizeof(Bars);
+    constexpr size_t smem = 1024 + static_cast<size_t>(kTilesB) * kTileB + sizeof(Bars);
     static std::atomic<uint64_t> raised{0};
     cudaError_t e = allow_smem(linear_tiles_kernel<BN, PAIR>, smem, raised);
     if (e != cudaSuccess) return e;
