@@ -24,7 +24,7 @@ constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
 constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
 constexpr int kTileB = 128 * BK * 2, kTilesB = 12;                         // a part of up to 128 tokens; room for 6 or 12 stages
 constexpr int kWarpA0 = 4, kWarpE0 = 8, kEWarps = 8, kThreads = 512;
-constexpr int kRegsSums = 168, kRegsRest = 88;                             // 8 warps each: 65536 registers in all
+constexpr int kRegsSums = 176, kRegsRest = 80;                             // 8 warps each: 65536 registers in all
 static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
 static_assert((kRegsSums + kRegsRest) * 256 <= 65536, "registers");
 
@@ -505,7 +505,7 @@ Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
             least = cost;
             p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
             p.parts = parts;
-            p.round = parts == 2 ? 2 : 1024;
+            p.round = parts == 2 ? 4 : 1024;
             p.pad_rows = tiles * BM;
             best = {bn, p};
         }
