@@ -5,9 +5,9 @@
 // Roles of a thread block (one an SM, tiles in turn):
 //   warps 0, 1: MMAs, a warp for each matrix.  A stage is 64 of n: four steps of 16 for each part.
 //   warp 2: TMA copies of the stage's parts (128-byte swizzle)
-//   warps 4-7: weights.  A thread has one row of each matrix; two words of signs become 32 registers of +-d0 pairs by a shift and a logic
+//   warps 4-11: weights.  A thread has a row of one matrix; two words of signs become 32 registers of +-d0 pairs by a shift and a logic
 //              operation each, and go to the stage's slot of tensor memory (the operand A), so shared memory is read for B alone
-//   warps 8-15: sums.  A round is 128 of n (512 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so it
+//   warps 12-19: sums.  A round is 128 of n (512 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so it
 //              leaves tensor memory after each round and is added in registers; one matrix is drained while the other's MMAs run.  Behind the
 //              last round the function, the residual, the conversion and the stores, while the next tile's MMAs start.
 // Tensor memory: 2 x 128 columns of sums, 4 stages x 64 columns of weights.  Where the tiles are fewer than the SMs, n is cut into equal
@@ -23,13 +23,13 @@ namespace {
 constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
 constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
 constexpr int kTileB = 128 * BK * 2, kTilesB = 12;                         // a part of up to 128 tokens; room for 6 or 12 stages
-constexpr int kWarpA0 = 4, kWarpE0 = 8, kEWarps = 8, kThreads = 512;
-constexpr int kRegsSums = 176, kRegsRest = 80;                             // 8 warps each: 65536 registers in all
+constexpr int kWarpA0 = 4, kWarpE0 = 12, kEWarps = 8, kThreads = 640;
+constexpr int kRegs = 96, kRegsSums = 168, kRegsRest = 48;                 // a thread's at launch, of 8 warps, of the other 12
 static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
-static_assert((kRegsSums + kRegsRest) * 256 <= 65536, "registers");
+static_assert(kRegsSums * 256 + kRegsRest * 384 <= kRegs * kThreads && kRegs * kThreads <= 65536, "registers");
 
 struct Bars {
-    uint64_t full[kStages];            // four weight warps
+    uint64_t full[kStages];            // eight weight warps
     uint64_t done[kStages];            // both matrices' MMAs of the stage are complete: its weights' slot is free
     uint64_t bfull[kTilesB];           // the copy's expect_tx and its bytes
     uint64_t bdone[kTilesB];           // as done, of the copy's slot
@@ -57,6 +57,14 @@ __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, 
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
+__device__ __forceinline__ void tma_load(uint32_t leader, void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(leader)
+        : "memory");
+}
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile(
@@ -73,6 +81,14 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {     //
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -140,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 4);
+            mbar_init(&bars->full[s], 8);
             mbar_init(&bars->done[s], 2);
         }
         for (int s = 0; s < kTilesB; ++s) {
@@ -189,13 +205,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 if (!ok) return;
                 ++turn[m];
                 tc_fence_after();
+                constexpr int AT_ONCE = NC == 48 ? 48 : 32;                // columns whose loads are in flight together
 #pragma unroll
-                for (int c = 0; c < NC; c += 16) {
-                    uint32_t v[16];
-                    ld16(at + static_cast<uint32_t>(m * kDCols + c), v);
+                for (int c = 0; c < NC; c += AT_ONCE) {
+                    uint32_t v[AT_ONCE / 16][16];
+#pragma unroll
+                    for (int o = 0; o < AT_ONCE / 16; ++o) ld16(at + static_cast<uint32_t>(m * kDCols + c + 16 * o), v[o]);
                     wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+                    for (int i = 0; i < AT_ONCE; ++i) sum[c + i] += __uint_as_float(v[i / 16][i % 16]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -298,87 +316,79 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- copies of the activations
-            if (lane == 0) {
-                prefetch_tmap(&tmB);
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                int slot = 0, lap = 0;
-                bool live = true;
-                for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
-                    const Unit w = unit_of<BN>(plan, u, nb);
-                    for (int k = w.k0; k < w.k1; ++k) {
-                        if (lap > 0 && !wait_or_abort(&bars->bdone[slot], (lap - 1) & 1u, abort)) {
-                            live = false;
-                            break;
-                        }
+            const uint32_t leader = elect_one();
+            if (leader) prefetch_tmap(&tmB);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int slot = 0, lap = 0;
+            bool live = true;
+            for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
+                const Unit w = unit_of<BN>(plan, u, nb);
+                for (int k = w.k0; k < w.k1; ++k) {
+                    if (lap > 0 && !__all_sync(0xffffffffu, wait_or_abort(&bars->bdone[slot], (lap - 1) & 1u, abort))) {
+                        live = false;
+                        break;
+                    }
+                    if (leader) {
                         mbar_arrive_expect_tx(&bars->bfull[slot], static_cast<uint32_t>(parts * BN * 128));
-                        for (int p = 0; p < parts; ++p)
-                            tma_load_2d(sB + (slot * parts + p) * kTileB, &tmB, k * BK, p * a.cols + w.tok0, &bars->bfull[slot]);
                         bars->last_copy[slot] = lap;
-                        if (++slot == slots) {
-                            slot = 0;
-                            ++lap;
-                        }
+                    }
+                    __syncwarp();
+                    for (int p = 0; p < parts; ++p)
+                        tma_load(leader, sB + (slot * parts + p) * kTileB, &tmB, k * BK, p * a.cols + w.tok0, &bars->bfull[slot]);
+                    if (++slot == slots) {
+                        slot = 0;
+                        ++lap;
                     }
                 }
             }
         } else if (warp >= kWarpA0) {
-            // ---------------- weights
-            const int r = (warp & 3) * 32 + lane;
-            const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kA0;
+            // ---------------- weights: four warps for each matrix
+            const int r = (warp & 3) * 32 + lane, m = (warp - kWarpA0) >> 2;
+            const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(kA0 + m * kACols);
             const int tiles = (a.rows + BM - 1) / BM;
+            auto arrive = [&](uint32_t g) {                                // the weights of stage g are there
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->full[g % kStages]);
+            };
             uint32_t g = 0;
             bool live = true;
             for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
                 const Unit w = unit_of<BN>(plan, u, nb);
-                const uint8_t* src[2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    src[m] = a.w[m] + static_cast<size_t>(PAIR ? w.row_tile : min(2 * w.row_tile + m, tiles - 1)) * nb * kChunkBytes;
-                uint4 bits[2];
-                uint32_t d0[2];
-                auto load = [&](int b) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint8_t* ch = src[m] + static_cast<size_t>(b) * kChunkBytes;
-                        bits[m] = *reinterpret_cast<const uint4*>(ch + r * 16);
-                        d0[m] = *reinterpret_cast<const uint16_t*>(ch + BM * 16 + r * 2);
-                    }
-                };
-                load(w.k0 / 2);
+                const uint8_t* src = (m ? a.w[1] : a.w[0]) + static_cast<size_t>(PAIR ? w.row_tile : min(2 * w.row_tile + m, tiles - 1)) * nb * kChunkBytes +
+                                     static_cast<size_t>(w.k0 / 2) * kChunkBytes;
+                uint4 bits = *reinterpret_cast<const uint4*>(src + r * 16);
+                uint32_t d0 = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
                 for (int k = w.k0; k < w.k1 && live; k += 2) {
-                    uint4 now[2];
-                    uint32_t neg[2];                                       // a clear bit gives -d0
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        now[m] = bits[m];
-                        neg[m] = (d0[m] * 0x00010001u) ^ 0x80008000u;
+                    const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w}, neg = (d0 * 0x00010001u) ^ 0x80008000u;   // a clear bit gives -d0
+                    src += kChunkBytes;
+                    if (k + 2 < w.k1) {
+                        bits = *reinterpret_cast<const uint4*>(src + r * 16);
+                        d0 = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
                     }
-                    if (k + 2 < w.k1) load(k / 2 + 1);
 #pragma unroll
                     for (int half = 0; half < 2; ++half, ++g) {
                         const int s = g % kStages;
+                        uint32_t av[16];
+                        auto expand = [&](uint32_t word) {
+#pragma unroll
+                            for (int p = 0; p < 16; ++p) av[p] = ((word << (15 - p)) & 0x80008000u) ^ neg;
+                        };
+                        expand(words[2 * half]);
+                        if (g > 0) arrive(g - 1);                          // the stores of the stage before went on meanwhile
                         if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                             live = false;
                             break;
                         }
                         tc_fence_after();
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint32_t w2[2] = {half ? now[m].z : now[m].x, half ? now[m].w : now[m].y};
-                            uint32_t av[32];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int p = 0; p < 16; ++p) av[16 * i + p] = ((w2[i] << (15 - p)) & 0x80008000u) ^ neg[m];
-                            tc_st32(at + static_cast<uint32_t>((2 * s + m) * kACols), av);
-                        }
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->full[s]);
+                        st16(at + static_cast<uint32_t>(2 * s * kACols), av);
+                        expand(words[2 * half + 1]);
+                        st16(at + static_cast<uint32_t>(2 * s * kACols + 16), av);
                     }
                 }
             }
+            if (live && g > 0) arrive(g - 1);
         }
     }
 
