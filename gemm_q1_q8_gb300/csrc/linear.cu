@@ -206,7 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_rows_kernel(const LinearAr
         if (PAIR) y *= z[MT - 1];
         if (a.residual && there) y += load_typed(a.residual, tok * a.residual_stride + row, a.type);
         if (a.y && there) store_typed(a.y, tok * a.y_stride + row, a.type, y);
-        if (a.blocks && row0 < a.rows) store_block(a.blocks + (tok * (a.rows / 32) + row0 / 32) * 34, y, lane);
+        if (a.blocks && row0 < a.rows) {
+            const float v[1] = {y};
+            store_blocks(a.blocks + (tok * (a.rows / 32) + row0 / 32) * 34, 0, v, 1, lane);
+        }
     }
 }
 

@@ -78,13 +78,31 @@ __device__ __forceinline__ void store_typed(void* p, size_t i, int type, float v
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// A warp's 32 values (one a lane: 32 neighbouring rows of one token) as a Q8_0 block, by the library's rule.  A NaN gives a NaN scale.
-__device__ __forceinline__ void store_block(uint8_t* block, float v, int lane) {
-    const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v))));
-    const float dd = q8_0_scale_fast(amax);
-    const int code = q8_0_quant1(v, amax, dd);
-    if (lane == 0) *reinterpret_cast<uint16_t*>(block) = __half_as_ushort(__float2half_rn(dd));
-    block[2 + lane] = static_cast<uint8_t>(code);
+// Q8_0 blocks of a warp's values, one a lane (32 neighbouring rows of a token), of up to N neighbouring tokens `step` bytes apart, by the
+// library's rule.  A NaN gives a NaN scale.  The tokens' chains run beside one another.
+template <int N>
+__device__ __forceinline__ void store_blocks(uint8_t* block, size_t step, const float (&v)[N], int count, int lane) {
+    float amax[N], dd[N];
+    int code[N];
+    bool far = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) amax[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v[i]))));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        dd[i] = q8_0_scale_fast(amax[i]);
+        bool sure;
+        code[i] = q8_0_code_near(v[i], amax[i], dd[i], sure);
+        far = far && sure;
+    }
+    if (!far)
+#pragma unroll
+        for (int i = 0; i < N; ++i) code[i] = q8_0_quant(v[i], amax[i], dd[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < count) {
+            if (lane == 0) *reinterpret_cast<uint16_t*>(block + i * step) = __half_as_ushort(__float2half_rn(dd[i]));
+            block[i * step + 2 + lane] = static_cast<uint8_t>(code[i]);
+        }
 }
 
 // The power of two that a token's values are multiplied by, 2^(7 - E) for scales below 2^(E + 1) (f16 bits without sign):

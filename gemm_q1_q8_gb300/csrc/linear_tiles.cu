@@ -108,21 +108,23 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, int u, int nb) {
 }
 
 // What is left to do with the sums of one row (a lane) and up to N neighbouring tokens
-template <bool PAIR, int N>
-__device__ __forceinline__ void finish(const LinearArgs& a, float (&y)[N], const float (&z1)[N], int row, size_t tok, int count, int lane) {
-    const bool there = row < a.rows;
-    float r[N];
-    if (!PAIR && a.residual) {
+template <int N>
+__device__ __forceinline__ void load_residual(const LinearArgs& a, float (&r)[N], int row, size_t tok, int count) {
+    const bool there = a.residual && row < a.rows;
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = there && i < count ? load_typed(a.residual, (tok + i) * a.residual_stride + row, a.type) : 0.f;
-    }
+    for (int i = 0; i < N; ++i) r[i] = there && i < count ? load_typed(a.residual, (tok + i) * a.residual_stride + row, a.type) : 0.f;
+}
+// `other`: the pair's second factor, or what is added
+template <bool PAIR, int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, float (&y)[N], const float (&other)[N], int row, size_t tok, int count, int lane) {
+    const bool there = row < a.rows;
     bend_all(y, a.function);
     if (PAIR) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] *= z1[i];
+        for (int i = 0; i < N; ++i) y[i] *= other[i];
     } else if (a.residual) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] += r[i];
+        for (int i = 0; i < N; ++i) y[i] += other[i];
     }
     if (a.y && there) {
         const size_t at = tok * a.y_stride + row;
@@ -138,9 +140,8 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&y)[N], const
         }
     }
     if (a.blocks && __shfl_sync(0xffffffffu, there, 0)) {
-        uint8_t* block = a.blocks + (tok * (a.rows / 32) + row / 32) * 34;
-#pragma unroll
-        for (int i = 0; i < N; ++i) if (i < count) store_block(block + static_cast<size_t>(i) * (a.rows / 32) * 34, y[i], lane);
+        const size_t step = static_cast<size_t>(a.rows / 32) * 34;
+        store_blocks(a.blocks + tok * step + row / 32 * 34, step, y, count, lane);
     }
 }
 
@@ -195,6 +196,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
         bool ok = true;
         for (int u = blockIdx.x; u < plan.units && ok; u += gridDim.x) {
             const Unit w = unit_of<BN>(plan, u, nb);
+            const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
+            const int tok0 = w.tok0 + h * NC;
+            // what the epilogue needs, loaded before the sums come: a column's power of two is with lane column % 32
+            float b0 = 0.f, b1 = 0.f, scales[(NC + 31) / 32];
+            if (plan.splits == 1) {
+                if (a.bias[0] && row0 < a.rows) b0 = a.bias[0][row0];
+                if (a.bias[1] && row1 < a.rows) b1 = a.bias[1][row1];
+#pragma unroll
+                for (int i = 0; i < (NC + 31) / 32; ++i) scales[i] = tok0 + 32 * i + lane < a.cols ? plan.scale[tok0 + 32 * i + lane] : 0.f;
+            }
             float acc[2][NC];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 if (!ok) return;
                 ++turn[m];
                 tc_fence_after();
-                constexpr int AT_ONCE = NC == 48 ? 48 : 32;                // columns whose loads are in flight together
+                constexpr int AT_ONCE = NC == 48 ? 48 : 16;                // columns whose loads are in flight together
 #pragma unroll
                 for (int c = 0; c < NC; c += AT_ONCE) {
                     uint32_t v[AT_ONCE / 16][16];
@@ -227,8 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             drain(0, acc[0]);
             drain(1, acc[1]);
             if (!ok) break;
-            const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
-            const int tok0 = w.tok0 + h * NC;
             if (plan.splits > 1) {
                 float* to = plan.partial + (static_cast<size_t>(w.split) * (PAIR ? 2 : 1) * a.cols + tok0) * plan.pad_rows;
                 const size_t second = PAIR ? static_cast<size_t>(a.cols) * plan.pad_rows : 0;
@@ -240,17 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 }
                 continue;
             }
-            const float b0 = a.bias[0] && row0 < a.rows ? a.bias[0][row0] : 0.f, b1 = a.bias[1] && row1 < a.rows ? a.bias[1][row1] : 0.f;
             // eight tokens at a time, in a loop: unrolled whole it does not fit the instruction cache (4096 tokens, 14336 x 4096, bf16:
             // 2074 us).  The registers of a step are chosen by selects.
 #pragma unroll 1
             for (int c = 0; c < NC; c += 8) {
                 const int tok = tok0 + c, count = a.cols - tok;
                 if (count <= 0) break;
-                float z0[8], z1[8];
+                float z0[8], z1[8], r0[8], r1[8];
+                if (!PAIR) {
+                    load_residual(a, r0, row0, tok, count);
+                    load_residual(a, r1, row1, tok, count);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float s = i < count ? plan.scale[tok + i] : 0.f;
+                    const float s = __shfl_sync(0xffffffffu, NC > 32 && c >= 32 ? scales[(NC + 31) / 32 - 1] : scales[0], (c + i) & 31);
                     float v0 = acc[0][i], v1 = acc[1][i];
 #pragma unroll
                     for (int o = 8; o < NC; o += 8) {
@@ -260,8 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     z0[i] = fmaf(v0, s, b0);                               // the product is exact
                     z1[i] = fmaf(v1, s, b1);
                 }
-                finish<PAIR>(a, z0, z1, row0, tok, count, lane);
-                if (!PAIR) finish<PAIR>(a, z1, z1, row1, tok, count, lane);
+                if constexpr (PAIR) {
+                    finish<true>(a, z0, z1, row0, tok, count, lane);
+                } else {
+                    finish<false>(a, z0, r0, row0, tok, count, lane);
+                    finish<false>(a, z1, r1, row1, tok, count, lane);
+                }
             }
         }
     } else {
@@ -473,8 +489,10 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, co
     const float sc = plan.scale[tok];
     const bool there = row < a.rows;
     float y[1] = {fmaf(z0, sc, a.bias[0] && there ? a.bias[0][row] : 0.f)};
-    const float up[1] = {fmaf(z1, sc, PAIR && a.bias[1] && there ? a.bias[1][row] : 0.f)};
-    finish<PAIR>(a, y, up, row, tok, 1, lane);
+    float other[1];
+    if (PAIR) other[0] = fmaf(z1, sc, a.bias[1] && there ? a.bias[1][row] : 0.f);
+    else load_residual(a, other, row, tok, 1);
+    finish<PAIR>(a, y, other, row, tok, 1, lane);
 }
 
 template <typename K, typename... A>
