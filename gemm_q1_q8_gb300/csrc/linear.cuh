@@ -41,13 +41,20 @@ namespace {
 // f16 parts that an activation takes
 __host__ __device__ __forceinline__ int linear_parts(const LinearArgs& a) { return a.type == GQ_BF16 && !a.blocks ? 1 : 2; }
 
+// 1 / (1 + e^-v); the exponential of 2^-v log2(e) and the reciprocal are off by two units each, and give 0 below 2^-126
+__device__ __forceinline__ float sigmoid_of(float v) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 __device__ __forceinline__ float bend(float z, int function) {
     switch (function) {
         case GQ_FN_RELU: return z < 0.f ? 0.f : z;                               // NaN stays
         case GQ_FN_RELU2: z = z < 0.f ? 0.f : z; return z * z;
-        case GQ_FN_SILU: return __fdividef(z, 1.f + __expf(-z));
+        case GQ_FN_SILU: return z * sigmoid_of(z);
         case GQ_FN_GELU: return 0.5f * z * erfcf(z * -0.70710678f);              // no cancellation below zero
-        case GQ_FN_GELU_TANH: return __fdividef(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));   // z * sigmoid(2u)
+        case GQ_FN_GELU_TANH: return z * sigmoid_of(1.5957691f * fmaf(0.044715f * z * z, z, z));
         default: return z;
     }
 }
@@ -97,12 +104,13 @@ __device__ __forceinline__ void store_blocks(uint8_t* block, size_t step, const 
     if (!far)
 #pragma unroll
         for (int i = 0; i < N; ++i) code[i] = q8_0_quant(v[i], amax[i], dd[i]);
+    float mine = dd[0];                                                          // lane i stores the i-th scale
+#pragma unroll
+    for (int i = 1; i < N; ++i) mine = lane == i ? dd[i] : mine;
+    if (lane < (N < count ? N : count)) *reinterpret_cast<uint16_t*>(block + lane * step) = __half_as_ushort(__float2half_rn(mine));
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (i < count) {
-            if (lane == 0) *reinterpret_cast<uint16_t*>(block + i * step) = __half_as_ushort(__float2half_rn(dd[i]));
-            block[i * step + 2 + lane] = static_cast<uint8_t>(code[i]);
-        }
+        if (i < count) block[i * step + 2 + lane] = static_cast<uint8_t>(code[i]);
 }
 
 // The power of two that a token's values are multiplied by, 2^(7 - E) for scales below 2^(E + 1) (f16 bits without sign):

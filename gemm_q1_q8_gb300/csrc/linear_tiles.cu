@@ -199,12 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
             const int tok0 = w.tok0 + h * NC;
             // what the epilogue needs, loaded before the sums come: a column's power of two is with lane column % 32
-            float b0 = 0.f, b1 = 0.f, scales[(NC + 31) / 32];
+            float b0 = 0.f, b1 = 0.f, scales = 0.f, scales2 = 0.f;
             if (plan.splits == 1) {
                 if (a.bias[0] && row0 < a.rows) b0 = a.bias[0][row0];
                 if (a.bias[1] && row1 < a.rows) b1 = a.bias[1][row1];
-#pragma unroll
-                for (int i = 0; i < (NC + 31) / 32; ++i) scales[i] = tok0 + 32 * i + lane < a.cols ? plan.scale[tok0 + 32 * i + lane] : 0.f;
+                if (tok0 + lane < a.cols) scales = plan.scale[tok0 + lane];
+                const int second = NC / 2 + ((lane - NC / 2) & 31);        // the second half's columns, around 32
+                if (second < NC && tok0 + second < a.cols) scales2 = plan.scale[tok0 + second];
             }
             float acc[2][NC];
 #pragma unroll
@@ -249,35 +250,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 }
                 continue;
             }
-            // eight tokens at a time, in a loop: unrolled whole it does not fit the instruction cache (4096 tokens, 14336 x 4096, bf16:
-            // 2074 us).  The registers of a step are chosen by selects.
+            // Eight tokens at a time, and the warp's columns in two halves by the same code: unrolled whole it does not fit the instruction
+            // cache (4096 tokens, 14336 x 4096, bf16, first form of this kernel: 2074 us against 1251), and choosing a step's registers by selects
+            // costs as many instructions as the epilogue.
 #pragma unroll 1
-            for (int c = 0; c < NC; c += 8) {
-                const int tok = tok0 + c, count = a.cols - tok;
-                if (count <= 0) break;
-                float z0[8], z1[8], r0[8], r1[8];
-                if (!PAIR) {
-                    load_residual(a, r0, row0, tok, count);
-                    load_residual(a, r1, row1, tok, count);
-                }
+            for (int half = 0; half < 2; ++half) {
+                constexpr int HC = NC / 2;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = __shfl_sync(0xffffffffu, NC > 32 && c >= 32 ? scales[(NC + 31) / 32 - 1] : scales[0], (c + i) & 31);
-                    float v0 = acc[0][i], v1 = acc[1][i];
+                for (int c = 0; c < HC; c += 8) {
+                    const int tok = tok0 + half * HC + c, count = a.cols - tok;
+                    if (count > 0) {
+                        float z0[8], z1[8], r0[8], r1[8];
+                        if (!PAIR) {
+                            load_residual(a, r0, row0, tok, count);
+                            load_residual(a, r1, row1, tok, count);
+                        }
 #pragma unroll
-                    for (int o = 8; o < NC; o += 8) {
-                        v0 = c == o ? acc[0][o + i] : v0;
-                        v1 = c == o ? acc[1][o + i] : v1;
+                        for (int i = 0; i < 8; ++i) {
+                            const float s = __shfl_sync(0xffffffffu, scales, (half * HC + c + i) & 31);
+                            z0[i] = fmaf(acc[0][c + i], s, b0);            // the product is exact
+                            z1[i] = fmaf(acc[1][c + i], s, b1);
+                        }
+                        if constexpr (PAIR) {
+                            finish<true>(a, z0, z1, row0, tok, count, lane);
+                        } else {
+                            finish<false>(a, z0, r0, row0, tok, count, lane);
+                            finish<false>(a, z1, r1, row1, tok, count, lane);
+                        }
                     }
-                    z0[i] = fmaf(v0, s, b0);                               // the product is exact
-                    z1[i] = fmaf(v1, s, b1);
                 }
-                if constexpr (PAIR) {
-                    finish<true>(a, z0, z1, row0, tok, count, lane);
-                } else {
-                    finish<false>(a, z0, r0, row0, tok, count, lane);
-                    finish<false>(a, z1, r1, row1, tok, count, lane);
+#pragma unroll
+                for (int i = 0; i < HC; ++i) {
+                    acc[0][i] = acc[0][HC + i];
+                    acc[1][i] = acc[1][HC + i];
                 }
+                scales = scales2;
             }
         }
     } else {
@@ -296,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 for (int k = w.k0; k < w.k1; ++k, ++g) {
                     const int s = g % kStages;
                     const bool last = r == 2 * half_round - 1 || k == w.k1 - 1;
-                    const bool ready = wait_or_abort(&bars->bfull[slot], lap & 1u, abort) && wait_or_abort(&bars->full[s], (g / kStages) & 1u, abort) &&
-                                       (!first || turn == 0 || wait_or_abort(&bars->accempty[m], (turn - 1) & 1u, abort));
+                    const bool ready = wait_or_abort_sleep(&bars->bfull[slot], lap & 1u, abort) && wait_or_abort_sleep(&bars->full[s], (g / kStages) & 1u, abort) &&
+                                       (!first || turn == 0 || wait_or_abort_sleep(&bars->accempty[m], (turn - 1) & 1u, abort));
                     if (!__all_sync(0xffffffffu, ready)) {
                         live = false;
                         break;
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
                 const Unit w = unit_of<BN>(plan, u, nb);
                 for (int k = w.k0; k < w.k1; ++k) {
-                    if (lap > 0 && !__all_sync(0xffffffffu, wait_or_abort(&bars->bdone[slot], (lap - 1) & 1u, abort))) {
+                    if (lap > 0 && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->bdone[slot], (lap - 1) & 1u, abort))) {
                         live = false;
                         break;
                     }
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                         };
                         expand(words[2 * half]);
                         if (g > 0) arrive(g - 1);                          // the stores of the stage before went on meanwhile
-                        if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
+                        if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                             live = false;
                             break;
                         }
