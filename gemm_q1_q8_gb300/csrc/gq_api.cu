@@ -292,7 +292,9 @@ static int linear_call(const gq::LinearArgs& a, bool pair, gq_stream_t stream) {
         !aligned(a.residual, b) || !aligned(a.y, b) || !aligned(a.blocks, 2) || !aligned(a.workspace, 16))
         return GQ_EINVAL_PTR;
     if (a.y && a.y == a.residual && a.y_stride != a.residual_stride) return GQ_EINVAL_PTR;
-    return cuda_status(gq::launch_linear(a, pair, reinterpret_cast<cudaStream_t>(stream)));
+    gq::LinearArgs v = a;
+    v.vec = a.rows % 4 == 0 && a.y_stride % 4 == 0 && a.residual_stride % 4 == 0 && aligned(a.y, 4 * b) && aligned(a.residual, 4 * b);
+    return cuda_status(gq::launch_linear(v, pair, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int gq_rmsnorm(const void* x, long long x_stride, const void* residual, long long residual_stride, const float* weight,
@@ -360,7 +362,7 @@ int q1_q8_linear(const void* packed_w, const void* act, int rows, int n, int col
                  void* workspace, gq_stream_t stream) {
     const gq::LinearArgs a = {{static_cast<const uint8_t*>(packed_w), static_cast<const uint8_t*>(packed_w)}, static_cast<const uint8_t*>(act),
                               {bias, bias}, rows, n, cols, function, type, residual, residual_stride, y, y_stride,
-                              static_cast<uint8_t*>(blocks), workspace};
+                              static_cast<uint8_t*>(blocks), workspace, false};
     return linear_call(a, false, stream);
 }
 
@@ -369,7 +371,7 @@ int q1_q8_glu(const void* packed_gate, const void* packed_up, const void* act, i
               gq_stream_t stream) {
     const gq::LinearArgs a = {{static_cast<const uint8_t*>(packed_gate), static_cast<const uint8_t*>(packed_up)}, static_cast<const uint8_t*>(act),
                               {bias_gate, bias_up}, rows, n, cols, function, type, nullptr, 0, y, y_stride,
-                              static_cast<uint8_t*>(blocks), workspace};
+                              static_cast<uint8_t*>(blocks), workspace, false};
     return linear_call(a, true, stream);
 }
 

@@ -85,16 +85,6 @@ __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int 
         for (int i = 0; i < 4; ++i) c[i] = q8_0_quant(x[i], amax, dd);
 }
 
-// One value by the same rule: its code where `sure` is set afterwards, elsewhere q8_0_quant gives it.
-__device__ __forceinline__ int q8_0_code_near(float v, float amax, float dd, bool& sure) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(dd));
-    if (!(dd >= 0x1p-120f)) r = 0.0f;
-    const float magic = 12582912.0f, t = fmaf(v, r, magic);
-    sure = (dd >= 0x1p-120f || amax == 0.0f) && fabsf(fmaf(v, r, magic - t)) <= 0.5f - 0x1p-11f;
-    return __float_as_int(t) - __float_as_int(magic);
-}
-
 // Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d
 __device__ __forceinline__ uint32_t cache_word(const int (&c)[4]) {
     uint32_t w = 0;

@@ -187,29 +187,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_rows_kernel(const LinearAr
                 }
             }
     __syncthreads();
-    const int row = row0 + lane;
-    const bool there = row < a.rows;
-    float bias[MT];
+    // four tokens a warp, four rows a lane
+    const int row = row0 + 4 * (lane & 7);
+    float bias[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) bias[m] = a.bias[m] && there ? a.bias[m][row] : 0.f;
-    for (int tk = warp; tk < toks; tk += kWarps) {
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[m][i] = a.bias[m] && row + i < a.rows ? a.bias[m][row + i] : 0.f;
+    for (int t0 = 4 * warp; t0 < toks; t0 += 4 * kWarps) {
+        const int tk = t0 + (lane >> 3);
+        const bool on = tk < toks;
         const size_t tok = tok0 + tk;
-        float z[MT];
+        float other[4], z[MT][4];
+        if (!PAIR) load_four(a, other, row, tok, on);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            float v = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on)
 #pragma unroll
-            for (int q = 0; q < kShares; ++q) v += red[((m * kShares + q) * TOK + tk) * 32 + lane];
-            z[m] = v * pow2(-token_shift(largest[tk])) + bias[m];
+                for (int q = 0; q < kShares; ++q) {
+                    const float4 p = *reinterpret_cast<const float4*>(red + ((m * kShares + q) * TOK + tk) * 32 + 4 * (lane & 7));
+                    v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+                }
+            const float s = on ? pow2(-token_shift(largest[tk])) : 0.f;          // the product is exact
+            z[m][0] = fmaf(v.x, s, bias[m][0]);
+            z[m][1] = fmaf(v.y, s, bias[m][1]);
+            z[m][2] = fmaf(v.z, s, bias[m][2]);
+            z[m][3] = fmaf(v.w, s, bias[m][3]);
         }
-        float y = bend(z[0], a.function);
-        if (PAIR) y *= z[MT - 1];
-        if (a.residual && there) y += load_typed(a.residual, tok * a.residual_stride + row, a.type);
-        if (a.y && there) store_typed(a.y, tok * a.y_stride + row, a.type, y);
-        if (a.blocks && row0 < a.rows) {
-            const float v[1] = {y};
-            store_blocks(a.blocks + (tok * (a.rows / 32) + row0 / 32) * 34, 0, v, 1, lane);
-        }
+        finish_fours<PAIR, 1>(a, z[0], PAIR ? z[MT - 1] : other, row, static_cast<int>(tok), a.cols, lane);
     }
 }
 

@@ -29,6 +29,7 @@ struct LinearArgs {
     long long y_stride;
     uint8_t* blocks;                   // Q8_0 output
     void* workspace;
+    bool vec;                          // y and residual allow four values at once
 };
 
 cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s);
@@ -85,32 +86,72 @@ __device__ __forceinline__ void store_typed(void* p, size_t i, int type, float v
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// Q8_0 blocks of a warp's values, one a lane (32 neighbouring rows of a token), of up to N neighbouring tokens `step` bytes apart, by the
-// library's rule.  A NaN gives a NaN scale.  The tokens' chains run beside one another.
-template <int N>
-__device__ __forceinline__ void store_blocks(uint8_t* block, size_t step, const float (&v)[N], int count, int lane) {
-    float amax[N], dd[N];
-    int code[N];
-    bool far = true;
+// The epilogue of four neighbouring rows (`row` the first) of a token: eight neighbouring lanes hold a 32-row block, and all of a warp take
+// part.  `other`: the pair's second factor, or what is added.
+__device__ __forceinline__ void load_four(const LinearArgs& a, float* r, int row, size_t tok, bool on) {
+    if (!on || !a.residual) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) amax[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v[i]))));
+        for (int i = 0; i < 4; ++i) r[i] = 0.f;
+    } else if (a.vec && row < a.rows) {
+        const size_t at = tok * a.residual_stride + row;
+        const float4 v = a.type == GQ_F32   ? load4(static_cast<const float*>(a.residual) + at)
+                         : a.type == GQ_F16 ? load4(static_cast<const __half*>(a.residual) + at)
+                                            : load4(static_cast<const __nv_bfloat16*>(a.residual) + at);
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        dd[i] = q8_0_scale_fast(amax[i]);
-        bool sure;
-        code[i] = q8_0_code_near(v[i], amax[i], dd[i], sure);
-        far = far && sure;
+        for (int i = 0; i < 4; ++i) r[i] = row + i < a.rows ? load_typed(a.residual, tok * a.residual_stride + row + i, a.type) : 0.f;
     }
-    if (!far)
+}
+// G tokens a lane, tok, tok + 4, ..., of which those below `end` exist: their chains run beside one another.
+template <bool PAIR, int G>
+__device__ __forceinline__ void finish_fours(const LinearArgs& a, float (&y)[4 * G], const float (&other)[4 * G], int row, int tok, int end, int lane) {
+    bend_all(y, a.function);
 #pragma unroll
-        for (int i = 0; i < N; ++i) code[i] = q8_0_quant(v[i], amax[i], dd[i]);
-    float mine = dd[0];                                                          // lane i stores the i-th scale
+    for (int i = 0; i < 4 * G; ++i) y[i] = PAIR ? y[i] * other[i] : a.residual ? y[i] + other[i] : y[i];
+    if (a.y) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) mine = lane == i ? dd[i] : mine;
-    if (lane < (N < count ? N : count)) *reinterpret_cast<uint16_t*>(block + lane * step) = __half_as_ushort(__float2half_rn(mine));
+        for (int g = 0; g < G; ++g) {
+            if (tok + 4 * g >= end) continue;
+            const size_t at = static_cast<size_t>(tok + 4 * g) * a.y_stride + row;
+            if (a.vec && row < a.rows) {
+                const float4 v = make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
+                if (a.type == GQ_F32) store4(static_cast<float*>(a.y) + at, v);
+                else if (a.type == GQ_F16) store4(static_cast<__half*>(a.y) + at, v);
+                else store4(static_cast<__nv_bfloat16*>(a.y) + at, v);
+            } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < count) block[i * step + 2 + lane] = static_cast<uint8_t>(code[i]);
+                for (int i = 0; i < 4; ++i) if (row + i < a.rows) store_typed(a.y, at + i, a.type, y[4 * g + i]);
+            }
+        }
+    }
+    if (a.blocks) {
+        uint32_t top[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float* v = y + 4 * g;
+            top[g] = __float_as_uint(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+            const float sum = (v[0] + v[1]) + (v[2] + v[3]);
+            if (sum != sum) top[g] = 0x7fffffffu;                                 // a NaN, or infinities that make one
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int g = 0; g < G; ++g) top[g] = max(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));   // as bits: NaN above all
+        const int sub = lane & 7;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float amax = __uint_as_float(top[g]), dd = q8_0_scale_fast(amax);
+            int c[4];
+            q8_0_quant4(make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), amax, dd, c);
+            if (tok + 4 * g < end && row < a.rows) {
+                uint16_t* p = reinterpret_cast<uint16_t*>(a.blocks + (static_cast<size_t>(tok + 4 * g) * (a.rows / 32) + row / 32) * 34);
+                if (sub == 0) p[0] = __half_as_ushort(__float2half_rn(dd));
+                p[1 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[0], c[1], 0x0040));
+                p[2 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[2], c[3], 0x0040));
+            }
+        }
+    }
 }
 
 // The power of two that a token's values are multiplied by, 2^(7 - E) for scales below 2^(E + 1) (f16 bits without sign):

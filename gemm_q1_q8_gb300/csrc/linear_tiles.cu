@@ -22,7 +22,8 @@ namespace {
 
 constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
 constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
-constexpr int kTileB = 128 * BK * 2, kTilesB = 12;                         // a part of up to 128 tokens; room for 6 or 12 stages
+constexpr int kTileB = 128 * BK * 2, kTilesB = 10;                         // a part of up to 128 tokens; room for 5 or 10 stages
+constexpr int kStaged = 2 * 32 * 32 * 4;                                   // of a sums warp: half its columns of both matrices
 constexpr int kWarpA0 = 4, kWarpE0 = 12, kEWarps = 8, kThreads = 640;
 constexpr int kRegs = 96, kRegsSums = 168, kRegsRest = 48;                 // a thread's at launch, of 8 warps, of the other 12
 static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
@@ -107,50 +108,13 @@ __device__ __forceinline__ Unit unit_of(const Plan& p, int u, int nb) {
     return r;
 }
 
-// What is left to do with the sums of one row (a lane) and up to N neighbouring tokens
-template <int N>
-__device__ __forceinline__ void load_residual(const LinearArgs& a, float (&r)[N], int row, size_t tok, int count) {
-    const bool there = a.residual && row < a.rows;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = there && i < count ? load_typed(a.residual, (tok + i) * a.residual_stride + row, a.type) : 0.f;
-}
-// `other`: the pair's second factor, or what is added
-template <bool PAIR, int N>
-__device__ __forceinline__ void finish(const LinearArgs& a, float (&y)[N], const float (&other)[N], int row, size_t tok, int count, int lane) {
-    const bool there = row < a.rows;
-    bend_all(y, a.function);
-    if (PAIR) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] *= other[i];
-    } else if (a.residual) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] += other[i];
-    }
-    if (a.y && there) {
-        const size_t at = tok * a.y_stride + row;
-        if (a.type == GQ_F32) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) if (i < count) static_cast<float*>(a.y)[at + i * a.y_stride] = y[i];
-        } else if (a.type == GQ_F16) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) if (i < count) static_cast<__half*>(a.y)[at + i * a.y_stride] = __float2half_rn(y[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) if (i < count) static_cast<__nv_bfloat16*>(a.y)[at + i * a.y_stride] = __float2bfloat16_rn(y[i]);
-        }
-    }
-    if (a.blocks && __shfl_sync(0xffffffffu, there, 0)) {
-        const size_t step = static_cast<size_t>(a.rows / 32) * 34;
-        store_blocks(a.blocks + tok * step + row / 32 * 34, step, y, count, lane);
-    }
-}
-
 template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_constant__ CUtensorMap tmB, const LinearArgs a, const Plan plan) {
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);   // f32 += f16 x f16
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sB = smem_align1024(smem_raw);                                // [stage][part][BN rows of 128 bytes]
-    Bars* bars = reinterpret_cast<Bars*>(sB + kTilesB * kTileB);
+    uint8_t* staged = sB + kTilesB * kTileB;                               // [sums warp][matrix][column][32 rows] f32
+    Bars* bars = reinterpret_cast<Bars*>(staged + kEWarps * kStaged);
     volatile int* abort = &bars->abort;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int nb = a.n / 128, parts = plan.parts, slots = kTilesB / parts, half_round = plan.round / 2;
@@ -196,17 +160,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
         bool ok = true;
         for (int u = blockIdx.x; u < plan.units && ok; u += gridDim.x) {
             const Unit w = unit_of<BN>(plan, u, nb);
-            const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32 + lane, row1 = PAIR ? row0 : row0 + BM;
+            const int row0 = (PAIR ? w.row_tile : 2 * w.row_tile) * BM + q * 32, row1 = PAIR ? row0 : row0 + BM;
             const int tok0 = w.tok0 + h * NC;
-            // what the epilogue needs, loaded before the sums come: a column's power of two is with lane column % 32
-            float b0 = 0.f, b1 = 0.f, scales = 0.f, scales2 = 0.f;
-            if (plan.splits == 1) {
-                if (a.bias[0] && row0 < a.rows) b0 = a.bias[0][row0];
-                if (a.bias[1] && row1 < a.rows) b1 = a.bias[1][row1];
-                if (tok0 + lane < a.cols) scales = plan.scale[tok0 + lane];
-                const int second = NC / 2 + ((lane - NC / 2) & 31);        // the second half's columns, around 32
-                if (second < NC && tok0 + second < a.cols) scales2 = plan.scale[tok0 + second];
+            // what the epilogue needs is loaded before the sums come: a column's power of two is with lane column % 32
+            const int sub = lane & 7, r0 = row0 + 4 * sub, r1 = row1 + 4 * sub;
+            float b0[4], b1[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                b0[i] = a.bias[0] && r0 + i < a.rows ? a.bias[0][r0 + i] : 0.f;
+                b1[i] = a.bias[1] && r1 + i < a.rows ? a.bias[1][r1 + i] : 0.f;
             }
+            const int second = NC / 2 + ((lane - NC / 2) & 31);            // the second half's columns
+            const float scales = tok0 + lane < a.cols ? plan.scale[tok0 + lane] : 0.f;
+            const float scales2 = second < NC && tok0 + second < a.cols ? plan.scale[tok0 + second] : 0.f;
             float acc[2][NC];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -245,46 +211,57 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     if (tok0 + i >= a.cols) break;
-                    to[static_cast<size_t>(i) * plan.pad_rows + row0] = acc[0][i];
-                    if (PAIR || row1 < plan.pad_rows) to[second + static_cast<size_t>(i) * plan.pad_rows + row1] = acc[1][i];
+                    to[static_cast<size_t>(i) * plan.pad_rows + row0 + lane] = acc[0][i];
+                    if (PAIR || row1 < plan.pad_rows) to[second + static_cast<size_t>(i) * plan.pad_rows + row1 + lane] = acc[1][i];
                 }
                 continue;
             }
-            // Eight tokens at a time, and the warp's columns in two halves by the same code: unrolled whole it does not fit the instruction
-            // cache (4096 tokens, 14336 x 4096, bf16, first form of this kernel: 2074 us against 1251), and choosing a step's registers by selects
-            // costs as many instructions as the epilogue.
+            // Through shared memory, in two halves, to four rows a lane and four tokens a step: a loop that fits the instruction cache, with a third of
+            // the instructions that a row a lane takes.  (Unrolled over registers: 517 tokens of the 6912 x 2560 pair in f32 to Q8_0, 22,000
+            // of a tile's 62,000 cycles went into this.)
+            constexpr int HC = NC / 2;
+            float* own = reinterpret_cast<float*>(staged + (warp - kWarpE0) * kStaged);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                constexpr int HC = NC / 2;
-#pragma unroll
-                for (int c = 0; c < HC; c += 8) {
-                    const int tok = tok0 + half * HC + c, count = a.cols - tok;
-                    if (count > 0) {
-                        float z0[8], z1[8], r0[8], r1[8];
-                        if (!PAIR) {
-                            load_residual(a, r0, row0, tok, count);
-                            load_residual(a, r1, row1, tok, count);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float s = __shfl_sync(0xffffffffu, scales, (half * HC + c + i) & 31);
-                            z0[i] = fmaf(acc[0][c + i], s, b0);            // the product is exact
-                            z1[i] = fmaf(acc[1][c + i], s, b1);
-                        }
-                        if constexpr (PAIR) {
-                            finish<true>(a, z0, z1, row0, tok, count, lane);
-                        } else {
-                            finish<false>(a, z0, r0, row0, tok, count, lane);
-                            finish<false>(a, z1, r1, row1, tok, count, lane);
-                        }
-                    }
-                }
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < HC; ++i) {
+                    own[i * 32 + lane] = acc[0][i];
+                    own[(HC + i) * 32 + lane] = acc[1][i];
                     acc[0][i] = acc[0][HC + i];
                     acc[1][i] = acc[1][HC + i];
                 }
-                scales = scales2;
+                __syncwarp();
+                constexpr int G = HC % 16 == 0 ? 4 : 2;
+#pragma unroll 1
+                for (int c = lane >> 3; c < HC; c += 4 * G) {
+                    const int tok = tok0 + half * HC + c;
+                    float other[4 * G], z0[4 * G], z1[4 * G], more[4 * G];
+                    if (!PAIR)
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            load_four(a, other + 4 * g, r0, tok + 4 * g, tok + 4 * g < a.cols);
+                            load_four(a, more + 4 * g, r1, tok + 4 * g, tok + 4 * g < a.cols);
+                        }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float s = __shfl_sync(0xffffffffu, half ? scales2 : scales, (half * HC + c + 4 * g) & 31);
+                        const float4 u = *reinterpret_cast<const float4*>(own + (c + 4 * g) * 32 + 4 * sub);
+                        const float4 v = *reinterpret_cast<const float4*>(own + (HC + c + 4 * g) * 32 + 4 * sub);
+                        const float u4[4] = {u.x, u.y, u.z, u.w}, v4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            z0[4 * g + i] = fmaf(u4[i], s, b0[i]);         // the products are exact
+                            z1[4 * g + i] = fmaf(v4[i], s, b1[i]);
+                        }
+                    }
+                    if constexpr (PAIR) {
+                        finish_fours<true, G>(a, z0, z1, r0, tok, a.cols, lane);
+                    } else {
+                        finish_fours<false, G>(a, z0, other, r0, tok, a.cols, lane);
+                        finish_fours<false, G>(a, z1, more, r1, tok, a.cols, lane);
+                    }
+                }
             }
         }
     } else {
@@ -476,30 +453,39 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const uint8
     }
 }
 
-// The shares' sums in order, and the epilogue.  A warp has 32 rows of a token.
+// The shares' sums in order, and the epilogue.  A warp has 32 rows of four tokens.
 template <bool PAIR>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearArgs a, const Plan plan) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, groups = (a.rows + 31) / 32;
+    const int lane = threadIdx.x & 31, groups = (a.rows + 31) / 32, quads = (a.cols + 3) / 4;
     const long long id = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    if (id >= static_cast<long long>(groups) * a.cols) return;
-    const size_t tok = id / groups;
-    const int row = static_cast<int>(id % groups) * 32 + lane;
+    if (id >= static_cast<long long>(groups) * quads) return;
+    const int tok = static_cast<int>(id / groups) * 4 + (lane >> 3), row = static_cast<int>(id % groups) * 32 + 4 * (lane & 7);
+    const bool on = tok < a.cols;
     const size_t matrix = static_cast<size_t>(a.cols) * plan.pad_rows;
-    const float* from = plan.partial + tok * plan.pad_rows + row;
-    float z0 = 0.f, z1 = 0.f;
+    const float* from = plan.partial + static_cast<size_t>(on ? tok : 0) * plan.pad_rows + row;
+    float other[4], y[4];
+    if (!PAIR) load_four(a, other, row, tok, on);
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 4
     for (int s = 0; s < plan.splits; ++s) {
-        z0 += from[(PAIR ? 2 : 1) * s * matrix];
-        if (PAIR) z1 += from[(2 * s + 1) * matrix];
+        const float4 p = *reinterpret_cast<const float4*>(from + (PAIR ? 2 : 1) * s * matrix);
+        u = make_float4(u.x + p.x, u.y + p.y, u.z + p.z, u.w + p.w);
+        if (PAIR) {
+            const float4 o = *reinterpret_cast<const float4*>(from + (2 * s + 1) * matrix);
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
     }
-    const float sc = plan.scale[tok];
-    const bool there = row < a.rows;
-    float y[1] = {fmaf(z0, sc, a.bias[0] && there ? a.bias[0][row] : 0.f)};
-    float other[1];
-    if (PAIR) other[0] = fmaf(z1, sc, a.bias[1] && there ? a.bias[1][row] : 0.f);
-    else load_residual(a, other, row, tok, 1);
-    finish<PAIR>(a, y, other, row, tok, 1, lane);
+    const float sc = on ? plan.scale[tok] : 0.f;
+    const float z0[4] = {u.x, u.y, u.z, u.w}, z1[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool there = row + i < a.rows;
+        y[i] = fmaf(z0[i], sc, a.bias[0] && there ? a.bias[0][row + i] : 0.f);
+        if (PAIR) other[i] = fmaf(z1[i], sc, a.bias[1] && there ? a.bias[1][row + i] : 0.f);
+    }
+    finish_fours<PAIR, 1>(a, y, other, row, tok, a.cols, lane);
 }
 
 template <typename K, typename... A>
@@ -557,13 +543,13 @@ cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cuda
     if (!make_tmap_2d(&tmB, parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, static_cast<uint64_t>(a.n), static_cast<uint64_t>(p.parts) * a.cols,
                       static_cast<uint64_t>(a.n) * 2, BK, BN, true))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = 1024 + static_cast<size_t>(kTilesB) * kTileB + sizeof(Bars);
+    constexpr size_t smem = 1024 + static_cast<size_t>(kTilesB) * kTileB + kEWarps * kStaged + sizeof(Bars);
     static std::atomic<uint64_t> raised{0};
     cudaError_t e = allow_smem(linear_tiles_kernel<BN, PAIR>, smem, raised);
     if (e != cudaSuccess) return e;
     e = launch(linear_tiles_kernel<BN, PAIR>, static_cast<unsigned>(std::min(p.units, kSMs)), kThreads, smem, s, tmB, a, p);
     if (e != cudaSuccess || p.splits == 1) return e;
-    const long long warps = static_cast<long long>((a.rows + 31) / 32) * a.cols;
+    const long long warps = static_cast<long long>((a.rows + 31) / 32) * ((a.cols + 3) / 4);
     return launch(linear_join_kernel<PAIR>, static_cast<unsigned>((warps + 7) / 8), 256, 0, s, a, p);
 }
 
