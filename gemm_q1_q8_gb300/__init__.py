@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -598,30 +599,44 @@ def rmsnorm_q8_0(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
 
 def _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, y, act, d, q, op):
     m, k = x.shape
-    code = _type(x, "x")
+    code, dev = _type(x, "x"), x.get_device()
     xs, bs = _rows(x, code, m, k, "x"), _rows(block, code, m, k, "block")
-    gs = 0
+    gs, gp = 0, None
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2) or (gate.dim() == 2 and gate.shape[0] not in (1, m)):
             raise GQError(f"gate: expected [{k}] or [{m}, {k}]")
         one = gate.dim() == 1 or gate.shape[0] == 1
         row = _rows(gate.view(1, -1) if gate.dim() == 1 else gate, code, 1 if one else m, k, "gate")
-        gs = 0 if one else row
-    _need(weight, torch.float32, k, "weight")
-    if post_weight is not None:
-        _need(post_weight, torch.float32, k, "post_weight")
-    if sum_out is not None:
-        _need(sum_out, x.dtype, m * k, "sum_out")
-    _one_device(x, block=block, weight=weight, post_weight=post_weight, gate=gate, sum_out=sum_out, out=y if y is not None else act if act is not None else q)
-    _check(lib().gq_rmsnorm_block(_at(block), bs, _at(x), xs, _at(post_weight), _at(gate), gs, block_scale, residual_scale, _at(weight),
-                                  eps, code, m, k, _at(sum_out), _at(y), _at(act), _at(d), _at(q), _at(op), _on(x)), "gq_rmsnorm_block")
+        gs, gp = 0 if one else row, _same_device(gate, dev, "gate")
+    wp = _is(weight, torch.float32, k, dev, "weight")
+    pp = _is(post_weight, torch.float32, k, dev, "post_weight") if post_weight is not None else None
+    hp = _is(sum_out, x.dtype, m * k, dev, "sum_out") if sum_out is not None else None
+    _launched(x, dev, lib().gq_rmsnorm_block, "gq_rmsnorm_block", _same_device(block, dev, "block"), bs, x.data_ptr(), xs, pp, gp, gs,
+              block_scale, residual_scale, wp, eps, code, m, k, hp, y, act, d, q, op)
 
 
-def _one_device(first: torch.Tensor, **others):
-    """Refuses tensors of another device than the call's first."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise GQError(f"{name}: expected a tensor on {first.device}, got {t.device}")
+def _is(t, dtype, numel: int, dev: int, name: str) -> int:
+    """Checks a contiguous tensor of a dtype, a number of elements and the call's device; its address.  _need, in one go where all is well."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, dtype, numel, name)
+    raise GQError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+
+
+def _launched(t: torch.Tensor, dev: int, fn, name: str, *args):
+    """Calls a C entry point on the current stream of t's device (index dev), which is made the current one for it."""
+    if torch._C._cuda_getDevice() == dev:
+        _check(fn(*args, _on(t)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _on(t)), name)
+
+
+def _same_device(t, dev: int, name: str) -> int:
+    """Refuses a tensor of another device than the call's; its address."""
+    if t.get_device() != dev:
+        raise GQError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+    return t.data_ptr()
 
 
 def rmsnorm_block(block: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, post_weight: torch.Tensor | None = None, eps: float = 1e-5,
@@ -635,8 +650,8 @@ def rmsnorm_block(block: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, po
         raise GQError("x: expected a CUDA tensor [m, k]")
     _type(x, "x")
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    _need(y, x.dtype, x.numel(), "out")
-    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, y, None, None, None, None)
+    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out,
+                   _is(y, x.dtype, x.numel(), x.get_device(), "out"), None, None, None, None)
     return y
 
 
@@ -647,26 +662,24 @@ def rmsnorm_block_q8_0(block: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] % 32:
         raise GQError("rmsnorm_block_q8_0: expected x [m, k] with k a multiple of 32")
     _type(x, "x")
-    m, k = x.shape
-    act = d = q = op = None
+    (m, k), dev = x.shape, x.get_device()
     if not split:
         act = torch.empty(m * (k // 32) * 34, dtype=torch.uint8, device=x.device) if out is None else out
-        _need(act, torch.uint8, m * (k // 32) * 34, "out")
+        _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, None,
+                       _is(act, torch.uint8, m * (k // 32) * 34, dev, "out"), None, None, None)
+        return act
+    if out is None:
+        d = torch.empty((m, k // 32), dtype=torch.int16, device=x.device)
+        q = torch.empty((m, k), dtype=torch.int8, device=x.device)
+        op = torch.empty((3, m, k), dtype=torch.int16, device=x.device) if mma_operand else None
     else:
-        if out is None:
-            d = torch.empty((m, k // 32), dtype=torch.int16, device=x.device)
-            q = torch.empty((m, k), dtype=torch.int8, device=x.device)
-            op = torch.empty((3, m, k), dtype=torch.int16, device=x.device) if mma_operand else None
-        else:
-            d, q, op = out
-        _need(d, torch.int16, m * (k // 32), "d")
-        _need(q, torch.int8, m * k, "q")
-        if mma_operand:
-            _need(op, torch.int16, 3 * m * k, "op")
-        else:
-            op = None
-    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, None, act, d, q, op)
-    return act if not split else (d, q, op)
+        d, q, op = out
+    if not mma_operand:
+        op = None
+    _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, None, None,
+                   _is(d, torch.int16, m * (k // 32), dev, "d"), _is(q, torch.int8, m * k, dev, "q"),
+                   _is(op, torch.int16, 3 * m * k, dev, "op") if mma_operand else None)
+    return d, q, op
 
 
 FUNCTIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
@@ -685,38 +698,39 @@ def q1_q8_linear_workspace(rows: int, n: int, cols: int, dtype=torch.float32, de
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 
-def _linear(name, packed, act, rows, n, cols, biases, function, dtype, q8_0, out, workspace):
-    """What both products check; (function code, type code, y, its stride, blocks, workspace, biases)."""
-    if function not in FUNCTIONS:
+@functools.lru_cache(maxsize=4096)
+def _linear_sizes(rows: int, n: int, cols: int, code: int):
+    return q1_0_packed_bytes(rows, n), lib().gq_q1_q8_linear_workspace_bytes(rows, n, cols, code)
+
+
+def _linear(name, act, rows, n, cols, function, dtype, q8_0, out, workspace):
+    """What both products check: (function code, type code, device, packed bytes, out, addresses of act, y, its stride, of blocks and workspace)."""
+    fn, code = FUNCTIONS.get(function), _TYPES.get(dtype)
+    if fn is None:
         raise GQError(f"{name}: unknown activation {function!r}")
-    code = _TYPES.get(dtype)
     if code is None:
         raise GQError(f"{name}: expected float32, float16 or bfloat16, got {dtype}")
-    nbytes = q1_0_packed_bytes(rows, n)
-    need = q1_q8_linear_workspace_bytes(rows, n, cols, dtype)
+    nbytes, need = _linear_sizes(rows, n, cols, code)
     if nbytes == 0 or need == 0 or (q8_0 and rows % 32):
         raise GQError(f"{name}: invalid shape")
-    _need(act, torch.uint8, cols * (n // 32) * 34, "act")
-    for p in packed:
-        _need(p, torch.uint8, nbytes, "packed")
-    for b in biases:
-        if b is not None:
-            _need(b, torch.float32, rows, "bias")
+    if not isinstance(act, torch.Tensor) or not act.is_cuda:
+        raise GQError("act: expected a CUDA tensor")
+    dev = act.get_device()
+    ap = _is(act, torch.uint8, cols * (n // 32) * 34, dev, "act")
     y = blocks = None
     ys = rows
     if q8_0:
-        blocks = torch.empty(cols * (rows // 32) * 34, dtype=torch.uint8, device=act.device) if out is None else out
-        _need(blocks, torch.uint8, cols * (rows // 32) * 34, "out")
+        out = torch.empty(cols * (rows // 32) * 34, dtype=torch.uint8, device=act.device) if out is None else out
+        blocks = _is(out, torch.uint8, cols * (rows // 32) * 34, dev, "out")
     else:
-        y = torch.empty((cols, rows), dtype=dtype, device=act.device) if out is None else out
-        ys = _rows(y, code, cols, rows, "out")
+        out = torch.empty((cols, rows), dtype=dtype, device=act.device) if out is None else out
+        ys = _rows(out, code, cols, rows, "out")
+        y = _same_device(out, dev, "out")
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=act.device)
-    _need(workspace, torch.uint8, workspace.numel(), "workspace")
-    if workspace.numel() < need:
-        raise GQError(f"{name}: workspace holds {workspace.numel()} bytes, needs {need}")
-    _one_device(act, packed=packed[0], packed_up=packed[-1], bias=biases[0], bias_up=biases[-1], out=y if blocks is None else blocks, workspace=workspace)
-    return FUNCTIONS[function], code, y, ys, blocks, workspace
+    elif not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
+        raise GQError(f"{name}: expected a workspace of at least {need} bytes")
+    return fn, code, dev, nbytes, out, ap, y, ys, blocks, _is(workspace, torch.uint8, workspace.numel(), dev, "workspace")
 
 
 def q1_q8_linear(packed: torch.Tensor, act: torch.Tensor, rows: int, n: int, cols: int, bias: torch.Tensor | None = None,
@@ -725,23 +739,26 @@ def q1_q8_linear(packed: torch.Tensor, act: torch.Tensor, rows: int, n: int, col
     """activation(w . a + bias) + residual for a packed rows x n Q1_0 matrix and `cols` Q8_0 vectors (uint8, cols * n/32 * 34 bytes), from
     one decoded token to long prompts: y [cols, rows] of dtype (f32, f16 or bf16), or with q8_0=True its Q8_0 blocks (uint8, rows a
     multiple of 32).  activation: a name of FUNCTIONS; bias [rows] f32; residual [cols, rows] of dtype with contiguous rows, which out may be."""
-    fn, code, y, ys, blocks, work = _linear("q1_q8_linear", (packed,), act, rows, n, cols, (bias,), activation, dtype, q8_0, out, workspace)
-    rs = _rows(residual, code, cols, rows, "residual") if residual is not None else 0
-    _one_device(act, residual=residual)
-    _check(lib().q1_q8_linear(_at(packed), _at(act), rows, n, cols, _at(bias), fn, _at(residual), rs, code, _at(y), ys, _at(blocks),
-                              _at(work), _on(act)), "q1_q8_linear")
-    return y if blocks is None else blocks
+    fn, code, dev, nbytes, out, ap, y, ys, blocks, work = _linear("q1_q8_linear", act, rows, n, cols, activation, dtype, q8_0, out, workspace)
+    rs, rp = 0, None
+    if residual is not None:
+        rs = _rows(residual, code, cols, rows, "residual")
+        rp = _same_device(residual, dev, "residual")
+    _launched(act, dev, lib().q1_q8_linear, "q1_q8_linear", _is(packed, torch.uint8, nbytes, dev, "packed"), ap, rows, n, cols,
+              _is(bias, torch.float32, rows, dev, "bias") if bias is not None else None, fn, rp, rs, code, y, ys, blocks, work)
+    return out
 
 
 def q1_q8_glu(packed_gate: torch.Tensor, packed_up: torch.Tensor, act: torch.Tensor, rows: int, n: int, cols: int,
               activation: str = "silu", bias_gate: torch.Tensor | None = None, bias_up: torch.Tensor | None = None, dtype=torch.float32,
               q8_0: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """activation(w_gate . a + bias_gate) * (w_up . a + bias_up): the gated pair of a feed-forward block, outputs as q1_q8_linear's."""
-    fn, code, y, ys, blocks, work = _linear("q1_q8_glu", (packed_gate, packed_up), act, rows, n, cols, (bias_gate, bias_up), activation,
-                                            dtype, q8_0, out, workspace)
-    _check(lib().q1_q8_glu(_at(packed_gate), _at(packed_up), _at(act), rows, n, cols, _at(bias_gate), _at(bias_up), fn, code, _at(y),
-                           ys, _at(blocks), _at(work), _on(act)), "q1_q8_glu")
-    return y if blocks is None else blocks
+    fn, code, dev, nbytes, out, ap, y, ys, blocks, work = _linear("q1_q8_glu", act, rows, n, cols, activation, dtype, q8_0, out, workspace)
+    _launched(act, dev, lib().q1_q8_glu, "q1_q8_glu", _is(packed_gate, torch.uint8, nbytes, dev, "packed_gate"),
+              _is(packed_up, torch.uint8, nbytes, dev, "packed_up"), ap, rows, n, cols,
+              _is(bias_gate, torch.float32, rows, dev, "bias_gate") if bias_gate is not None else None,
+              _is(bias_up, torch.float32, rows, dev, "bias_up") if bias_up is not None else None, fn, code, y, ys, blocks, work)
+    return out
 
 
 LogProbs = collections.namedtuple("LogProbs", "logprob entropy top_ids top_logprobs")
@@ -750,6 +767,9 @@ LogProbs = collections.namedtuple("LogProbs", "logprob entropy top_ids top_logpr
 def logprobs_workspace_bytes(m: int, vocab: int, top: int = 0) -> int:
     """Bytes of the workspace logprobs needs (0: invalid sizes)."""
     return lib().gq_logprobs_workspace_bytes(m, vocab, top)
+
+
+_logprobs_bytes = functools.lru_cache(maxsize=4096)(logprobs_workspace_bytes)
 
 
 def logprobs_workspace(m: int, vocab: int, top: int = 0, device="cuda") -> torch.Tensor:
@@ -767,27 +787,28 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int 
     probabilities, largest first, equal ones by index.  What is not asked for is None."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise GQError("logits: expected a CUDA tensor [m, vocab]")
-    code = _type(logits, "logits")
-    m, vocab = logits.shape
+    code, dev, (m, vocab) = _type(logits, "logits"), logits.get_device(), logits.shape
     stride = _rows(logits, code, m, vocab, "logits")
-    if tokens is not None:
-        _need(tokens, torch.int64, m, "tokens")
-    need = logprobs_workspace_bytes(m, vocab, top)
+    need = _logprobs_bytes(m, vocab, top)
     if need == 0 or (tokens is None and not entropy and top == 0):
         raise GQError("logprobs: invalid shape, or nothing asked for")
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    lp = torch.empty(m, **f32) if tokens is not None else None
-    h = torch.empty(m, **f32) if entropy else None
-    ids = torch.empty((m, top), dtype=torch.int64, device=logits.device) if top else None
-    best = torch.empty((m, top), **f32) if top else None
+    where, f32 = logits.device, torch.float32
+    lp = h = ids = best = tp = None
+    if tokens is not None:
+        tp = _is(tokens, torch.int64, m, dev, "tokens")
+        lp = torch.empty(m, dtype=f32, device=where)
+    if entropy:
+        h = torch.empty(m, dtype=f32, device=where)
+    if top:
+        ids = torch.empty((m, top), dtype=torch.int64, device=where)
+        best = torch.empty((m, top), dtype=f32, device=where)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
-    _need(workspace, torch.uint8, workspace.numel(), "workspace")
-    if workspace.numel() < need:
-        raise GQError(f"logprobs: workspace holds {workspace.numel()} bytes, needs {need}")
-    _one_device(logits, tokens=tokens, workspace=workspace)
-    _check(lib().gq_logprobs(_at(logits), stride, code, m, vocab, scale, _at(tokens), _at(lp), _at(h), top, _at(ids), _at(best),
-                             _at(workspace), _on(logits)), "gq_logprobs")
+        workspace = torch.empty(need, dtype=torch.uint8, device=where)
+    elif not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
+        raise GQError(f"logprobs: expected a workspace of at least {need} bytes")
+    wp = _is(workspace, torch.uint8, workspace.numel(), dev, "workspace")
+    _launched(logits, dev, lib().gq_logprobs, "gq_logprobs", logits.data_ptr(), stride, code, m, vocab, scale, tp, _at(lp), _at(h), top,
+              _at(ids), _at(best), wp)
     return LogProbs(lp, h, ids, best)
 
 

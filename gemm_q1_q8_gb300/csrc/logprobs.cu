@@ -124,8 +124,8 @@ __host__ __device__ __forceinline__ float4* part_sums(void* w) { return static_c
 __device__ __forceinline__ uint64_t* part_best(void* w, size_t parts) { return reinterpret_cast<uint64_t*>(static_cast<float4*>(w) + parts); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs a, int splits, int part) {
-    constexpr int W = Vec<T>::W, UN = 4;
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
+    constexpr int W = Vec<T>::W, UN = 2;
     __shared__ uint64_t found[kFound];
     __shared__ Sums warp_sums[kThreads / 32];
     __shared__ int count, warp_counts[kThreads / 32];
@@ -165,9 +165,20 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
 #pragma unroll
             for (int j = 1; j < W; ++j) m = max_nan(m, f[j]);
             top = max_nan(top, m);
-            rescale(t, max_nan(t.m, m), c);
+            if (!(m <= t.m)) rescale(t, max_nan(t.m, m), c);               // rare after the first steps
+            // two sums side by side, packed
+            const float2 low = make_float2(-t.m, -t.m), cc = make_float2(c, c);
+            float2 s2 = make_float2(0.f, 0.f), u2 = s2;
 #pragma unroll
-            for (int j = 0; j < W; ++j) add(t, f[j], c);
+            for (int j = 0; j < W; j += 2) {
+                float2 d = fmul2(fadd2(make_float2(f[j], f[j + 1]), low), cc);
+                d = make_float2(max_nan(d.x, -1e4f), max_nan(d.y, -1e4f)); // -inf: no weight, and no 0 * inf
+                const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+                s2 = fadd2(s2, e);
+                u2 = ffma2(e, d, u2);
+            }
+            t.s += s2.x + s2.y;
+            t.u += u2.x + u2.y;
         }
     }
     const uint32_t mine = key_of(top);
@@ -228,7 +239,16 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LogprobArgs
     };
     const int few = 2 * k + 16;
     int have = kFound + 1;
-    int reach = search(31, 16, kThreads);
+    int reach;
+    if (k == 1) {
+        // the largest: that of the sums, but for rows of nothing above -inf
+        bound = key_of(t.m);
+        reach = __syncthreads_count(mine >= bound);
+        if (reach == 0) {
+            bound = 0;
+            reach = search(31, 16, kThreads);
+        }
+    } else reach = search(31, 16, kThreads);
     if (reach <= few) have = gather(bound);
     if (have > kFound) {
         // too many near the bound: the exact one
@@ -339,9 +359,9 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const Logpr
     }
 }
 
-// Parts of a row: enough for two blocks an SM, of at least 2048 logits each where they need not be smaller than kMaxPart
+// Parts of a row: enough for three blocks an SM, of at least 2048 logits each where they need not be smaller than kMaxPart
 int splits_of(int m, int vocab) {
-    const int least = (vocab + kMaxPart - 1) / kMaxPart, want = m < 2 * 152 ? 2 * 152 / m : 1;
+    const int least = (vocab + kMaxPart - 1) / kMaxPart, want = m < 3 * 152 ? 3 * 152 / m : 1;
     const int most = vocab / 2048 > 1 ? vocab / 2048 : 1;
     const int s = want < most ? want : most;
     return s < least ? least : s > kMaxSplits ? kMaxSplits : s;

@@ -201,6 +201,21 @@ struct BlockNormArgs {
     float block_scale, residual_scale;
 };
 
+// Four values of a row as they are stored, or in f32 where they cannot be loaded together
+template <typename T, bool VEC> struct Kept {
+    float4 v;
+    __device__ __forceinline__ void load(const T* row, int i, int k) { v = load_row4<T, VEC>(row, i, k); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <typename T> struct Kept<T, true> {
+    typename Vec4<T>::Raw r;
+    __device__ __forceinline__ void load(const T* row, int i, int k) {
+        r = typename Vec4<T>::Raw{};
+        if (i < k) r = *reinterpret_cast<const typename Vec4<T>::Raw*>(row + i);
+    }
+    __device__ __forceinline__ float4 get() const { return Vec4<T>::widen(r); }
+};
+
 __device__ __forceinline__ float row_sum(float s, float* part, int tid, int nt) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -228,11 +243,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    float4 v[NV], x[NV];
+    // all of a row's loads before the first sum, x and the gate kept as they are stored: behind the barriers a load costs its whole round
+    // trip (8192 bf16 rows of 4096 with a gate for each, and the blocks' read back: 131 -> 91 us)
+    float4 v[NV];
+    Kept<T, VEC> x[NV], g[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) v[c] = load_row4<T, VEC>(yr, 4 * (c * nt + tid), k);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) x[c] = load_row4<T, VEC>(xr, 4 * (c * nt + tid), k);
+    for (int c = 0; c < NV; ++c) x[c].load(xr, 4 * (c * nt + tid), k);
+    if (gr)
+#pragma unroll
+        for (int c = 0; c < NV; ++c) g[c].load(gr, 4 * (c * nt + tid), k);
     float rstd = 1.f;
     if (b.post) {
         float s = 0.f;
@@ -243,27 +264,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
         rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
     }
     // h of four values
-    auto join = [&](int i, float4 y, float4 x) {
+    auto join = [&](int i, float4 y, float4 x, float4 g) {
         if (b.post) {
             const float4 w = load_row4<float, VEC>(b.post, i, k);
             y = make_float4(y.x * rstd * w.x, y.y * rstd * w.y, y.z * rstd * w.z, y.w * rstd * w.w);
         }
-        if (gr) {
-            const float4 g = load_row4<T, VEC>(gr, i, k);
-            y = make_float4(g.x * y.x, g.y * y.y, g.z * y.z, g.w * y.w);
-        }
+        if (gr) y = make_float4(g.x * y.x, g.y * y.y, g.z * y.z, g.w * y.w);
         const float p = b.residual_scale, q = b.block_scale;
         return make_float4(p * x.x + q * y.x, p * x.y + q * y.y, p * x.z + q * y.z, p * x.w + q * y.w);
+    };
+    auto again = [&](int i) {
+        return join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k), gr ? load_row4<T, VEC>(gr, i, k) : make_float4(0.f, 0.f, 0.f, 0.f));
     };
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        v[c] = join(4 * (c * nt + tid), v[c], x[c]);
+        v[c] = join(4 * (c * nt + tid), v[c], x[c].get(), g[c].get());
         s = squares(v[c], s);
     }
     for (int c = NV; c < chunks; ++c) {
         const int i = 4 * (c * nt + tid);
-        s = squares_again(join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k)), s);
+        s = squares_again(again(i), s);
     }
     s = row_sum(s, part[1], tid, nt);
     const float rstd2 = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
@@ -280,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
         if (c < chunks) emit(4 * (c * nt + tid), v[c]);
     for (int c = NV; c < chunks; ++c) {
         const int i = 4 * (c * nt + tid);
-        emit(i, join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k)));
+        emit(i, again(i));
     }
 }
 
