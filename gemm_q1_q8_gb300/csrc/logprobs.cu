@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, the entropy and the best alternatives of rows of logits.
 //
-//   p = softmax(scale * x);  logprob = scale * (x[token] - M) - ln s,  H = ln s - (sum e^t t) / s,
-//   with M = max x, t = scale * (x - M), s = sum e^t.
+//   p = softmax(scale * x);  in powers of two, c = scale * log2(e), t = c (x - max x), s = sum 2^t:
+//   logprob = (t[token] - log2 s) ln 2,  H = (log2 s - (sum 2^t t) / s) ln 2.
 // A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps a running maximum and the two sums a
 // thread (rescaled where a step of loads raises the maximum).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
 // k-th largest logit from below, and a search over the bits of an order-preserving key finds it by 16 block-wide counts.  Only the threads whose maximum
@@ -45,40 +45,55 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 __device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return static_cast<uint64_t>(key) << 32 | (0xffffffffu - index); }
 
-// m: the largest logit (at least the lowest number); s = sum 2^t, u = sum 2^t t, t = c (x - m)
+// s = sum 2^t, u = sum 2^t t, m the largest logit.  Near: t = c x - r with r = c m rounded, one fma, while |r| < 2^20 (r is then off by at most
+// 1/32, the same in every term).  Far: t = c (x - m), for rows whose largest logit is further out, summed once more.
 struct Sums { float m, s, u; };
+constexpr float kNear = 1048576.f;
+__device__ __forceinline__ bool is_far(float m, float c) { return !(fabsf(c * m) < kNear); }
+__device__ __forceinline__ float floor_of(float c) { return -1.0001f * kNear / c; }            // a first m that is far
 
-__device__ __forceinline__ void rescale(Sums& a, float m, float c) {
-    const float d = max_nan(c * (a.m - m), -1e4f), f = exp2_fast(d);
+__device__ __forceinline__ float power(float x, float m, float c, bool far) { return max_nan(far ? c * (x - m) : fmaf(c, x, -(c * m)), -1e4f); }
+__device__ __forceinline__ void rescale(Sums& a, float m, float c, bool far) {
+    const float d = max_nan(far ? c * (a.m - m) : c * a.m - c * m, -1e4f), f = exp2_fast(d);
     a.u = fmaf(a.s, d, a.u) * f;
     a.s *= f;
     a.m = m;
 }
-__device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
-    const float m = max_nan(a.m, b.m);
-    rescale(a, m, c);
-    rescale(b, m, c);
-    return {m, a.s + b.s, a.u + b.u};
-}
-__device__ __forceinline__ Sums shuffled(const Sums& a, int o) {
-    return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.u, o)};
-}
-__device__ __forceinline__ void add(Sums& a, float x, float c) {
-    const float t = max_nan(c * (x - a.m), -1e4f), e = exp2_fast(t);               // -inf: no weight, and no 0 * inf
+__device__ __forceinline__ void add(Sums& a, float x, float c, bool far) {
+    const float t = power(x, a.m, c, far), e = exp2_fast(t);                       // -inf: no weight, and no 0 * inf
     a.s += e;
     a.u = fmaf(e, t, a.u);
+}
+// The sums of a warp's lanes, or of a group's of N: the maximum first, so that each is rescaled once
+template <int N>
+__device__ __forceinline__ Sums of_lanes(Sums t, float c, bool far) {
+    float m = t.m;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    rescale(t, m, c, far);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
+        t.u += __shfl_xor_sync(0xffffffffu, t.u, o);
+    }
+    return t;
 }
 
 // 16 bytes of logits
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int W = 4;
+    static __device__ __forceinline__ float one(const uint4& r, int j) { return __uint_as_float(j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w); }
     static __device__ __forceinline__ void get(const uint4& r, float (&v)[4]) {
         v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int W = 8;
+    static __device__ __forceinline__ float one(const uint4& r, int j) {
+        const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+        return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    }
     static __device__ __forceinline__ void get(const uint4& r, float (&v)[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -90,6 +105,10 @@ template <> struct Vec<__nv_bfloat16> {
 };
 template <> struct Vec<__half> {
     static constexpr int W = 8;
+    static __device__ __forceinline__ float one(const uint4& r, int j) {
+        const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(j & 1 ? w >> 16 : w)));
+    }
     static __device__ __forceinline__ void get(const uint4& r, float (&v)[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -101,20 +120,21 @@ template <> struct Vec<__half> {
     }
 };
 
-__device__ __forceinline__ float logprob_of(float x, const Sums& a, float scale) {
+__device__ __forceinline__ float logprob_of(float x, const Sums& a, float scale, float c) {
     if (a.s == 0.f) return x != x ? x : __uint_as_float(0xff800000u);              // nothing has any weight
-    return scale * (x - a.m) - logf(a.s);
+    if (is_far(a.m, c) || is_far(x, c)) return scale * (x - a.m) - log2f(a.s) * kLn2;       // beside 2^20 the rounding of r is nothing
+    return (fmaf(c, x, -(c * a.m)) - log2f(a.s)) * kLn2;
 }
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, const Sums& t) {
-    if (a.entropy) a.entropy[row] = t.s == 0.f ? 0.f : logf(t.s) - t.u / t.s * kLn2;
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, const Sums& t, float c) {
+    if (a.entropy) a.entropy[row] = t.s == 0.f ? 0.f : (log2f(t.s) - t.u / t.s) * kLn2;
     if (a.logprob) {
         const int64_t tok = a.tokens[row];
         float r = 0.f;
         if (tok >= a.vocab) {
             r = __uint_as_float(0x7fffffffu);
             report_error(kErrIndex);
-        } else if (tok >= 0) r = logprob_of(to_f32(static_cast<const T*>(a.x)[row * a.stride + tok]), t, a.scale);
+        } else if (tok >= 0) r = logprob_of(to_f32(static_cast<const T*>(a.x)[row * a.stride + tok]), t, a.scale, c);
         a.logprob[row] = r;
     }
 }
@@ -145,54 +165,65 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
     const float none = __uint_as_float(0xff800000u);
     float top = none;                                                             // the thread's largest
-    Sums t = {kLowest, 0.f, 0.f};
-    if (extra >= 0) {
-        top = to_f32(x[extra]);
-        t.m = max_nan(top, kLowest);
-        add(t, top, c);
-    }
-    for (int v = tid; v < vecs; v += UN * kThreads) {
-        uint4 r[UN];
-#pragma unroll
-        for (int i = 0; i < UN; ++i)
-            if (v + i * kThreads < vecs) r[i] = xv[v + i * kThreads];
-#pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            if (v + i * kThreads >= vecs) break;
-            float f[W];
-            Vec<T>::get(r[i], f);
-            float m = f[0];
-#pragma unroll
-            for (int j = 1; j < W; ++j) m = max_nan(m, f[j]);
-            top = max_nan(top, m);
-            if (!(m <= t.m)) rescale(t, max_nan(t.m, m), c);               // rare after the first steps
-            // two sums side by side, packed
-            const float2 low = make_float2(-t.m, -t.m), cc = make_float2(c, c);
-            float2 s2 = make_float2(0.f, 0.f), u2 = s2;
-#pragma unroll
-            for (int j = 0; j < W; j += 2) {
-                float2 d = fmul2(fadd2(make_float2(f[j], f[j + 1]), low), cc);
-                d = make_float2(max_nan(d.x, -1e4f), max_nan(d.y, -1e4f)); // -inf: no weight, and no 0 * inf
-                const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
-                s2 = fadd2(s2, e);
-                u2 = ffma2(e, d, u2);
-            }
-            t.s += s2.x + s2.y;
-            t.u += u2.x + u2.y;
+    Sums t;
+    auto stream = [&](bool far) {
+        const float least = far ? kLowest : max_nan(floor_of(c), kLowest);
+        t = {least, 0.f, 0.f};
+        if (extra >= 0) {
+            const float f = to_f32(x[extra]);
+            top = max_nan(top, f);
+            t.m = max_nan(f, least);
+            add(t, f, c, far);
         }
+        for (int v = tid; v < vecs; v += UN * kThreads) {
+            uint4 r[UN];
+#pragma unroll
+            for (int i = 0; i < UN; ++i)
+                if (v + i * kThreads < vecs) r[i] = xv[v + i * kThreads];
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                if (v + i * kThreads >= vecs) break;
+                float f[W];
+                Vec<T>::get(r[i], f);
+                float m = f[0];
+#pragma unroll
+                for (int j = 1; j < W; ++j) m = max_nan(m, f[j]);
+                top = max_nan(top, m);
+                if (!(m <= t.m)) rescale(t, max_nan(t.m, m), c, far);      // rare after the first steps
+                if (far) {
+#pragma unroll 1
+                    for (int j = 0; j < W; ++j) add(t, Vec<T>::one(r[i], j), c, true);
+                    continue;
+                }
+                // two sums side by side, packed
+                const float low = -(c * t.m);
+                float2 s2 = make_float2(0.f, 0.f), u2 = s2;
+#pragma unroll
+                for (int j = 0; j < W; j += 2) {
+                    float2 d = ffma2(make_float2(c, c), make_float2(f[j], f[j + 1]), make_float2(low, low));
+                    d = make_float2(max_nan(d.x, -1e4f), max_nan(d.y, -1e4f));     // -inf: no weight, and no 0 * inf
+                    const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+                    s2 = fadd2(s2, e);
+                    u2 = ffma2(e, d, u2);
+                }
+                t.s += s2.x + s2.y;
+                t.u += u2.x + u2.y;
+            }
+        }
+        t = of_lanes<32>(t, c, far);
+        if (lane == 0) warp_sums[warp] = t;
+        if (tid == 0) count = 0;
+        __syncthreads();
+        t = of_lanes<kThreads / 32>(warp_sums[lane % (kThreads / 32)], c, far);
+    };
+    stream(false);
+    if (is_far(t.m, c)) {                                                  // the same in every thread
+        __syncthreads();
+        stream(true);
     }
     const uint32_t mine = key_of(top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
-    if (lane == 0) warp_sums[warp] = t;
-    if (tid == 0) count = 0;
-    __syncthreads();
-    t = lane < kThreads / 32 ? warp_sums[lane] : Sums{kLowest, 0.f, 0.f};
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
-    t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0), __shfl_sync(0xffffffffu, t.u, 0)};
     if (tid == 0) {
-        if (splits == 1) finish_row<T>(a, row, t);
+        if (splits == 1) finish_row<T>(a, row, t, c);
         else part_sums(a.workspace)[blockIdx.x] = make_float4(t.m, t.s, t.u, 0.f);
     }
     if (k == 0) return;
@@ -241,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
     int have = kFound + 1;
     int reach;
     if (k == 1) {
-        // the largest: that of the sums, but for rows of nothing above -inf
+        // the largest: that of the sums, but for parts of nothing above -inf
         bound = key_of(t.m);
         reach = __syncthreads_count(mine >= bound);
         if (reach == 0) {
@@ -289,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
         if (rank < k) {
             if (splits == 1) {
                 a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
-                a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
+                a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
             } else part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + rank] = e;
         }
     }
@@ -310,16 +341,22 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const Logpr
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float4* sums = part_sums(a.workspace) + row * splits;
-    Sums t = {kLowest, 0.f, 0.f};
+    float most = kLowest;
+    for (int i = lane; i < splits; i += 32) most = max_nan(most, sums[i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const bool far = is_far(most, c);
+    Sums t = {most, 0.f, 0.f};
     for (int i = lane; i < splits; i += 32) {
         const float4 p = sums[i];
-        t = joined(t, Sums{p.x, p.y, p.z}, c);
+        // a near part's terms are relative to its rounded r
+        const float d = max_nan(power(p.x, most, c, far) - (is_far(p.x, c) ? 0.f : fmaf(c, p.x, -(c * p.x))), -1e4f), f = exp2_fast(d);
+        t.u += fmaf(p.y, d, p.z) * f;
+        t.s += p.y * f;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t = joined(t, shuffled(t, o), c);
-    t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0), __shfl_sync(0xffffffffu, t.u, 0)};
+    t = of_lanes<32>(t, c, far);
     if (tid == 0) {
-        finish_row<T>(a, row, t);
+        finish_row<T>(a, row, t, c);
         count = 0;
     }
     if (k == 0) return;
@@ -354,7 +391,7 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const Logpr
         for (int j = 0; j < have; ++j) rank += found[j] > e;
         if (rank < k) {
             a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
-            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
+            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
         }
     }
 }

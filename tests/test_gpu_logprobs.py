@@ -77,6 +77,16 @@ def test_temperatures(gq, scale):
     check(gq, normal(2, 400, 3001, 0.5), 4, scale=scale)
 
 
+@pytest.mark.parametrize("m", [2, 460])
+@pytest.mark.parametrize("first,size", [(7e5, 3.0), (-7e5, 3.0), (7.3e5, 30.0), (-7.26842e5, 5.0), (1e9, 1e3), (-1e9, 1e3), (0.0, 1e30), (0.0, 1e37), (3.3e38, 1e32),
+                                        (-3.39e38, 1e31)])
+def test_logits_far_from_zero(gq, m, first, size):
+    """Whatever their size, up to the type's; 7.268e5 is where the form of the sums changes, in parts of a row before others."""
+    x = (first + normal(4, m, 9001, size).double()).clamp(-3.4e38, 3.4e38).float()
+    x[:, :4500] -= 6 * size if abs(first) > 1e5 and size < 1e3 else 0
+    check(gq, x, 6)
+
+
 @pytest.mark.parametrize("m", [2, 400])
 @pytest.mark.parametrize("top", [1, 5, 32])
 def test_ties_go_by_index(gq, m, top):
