@@ -5,7 +5,7 @@
 // A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps a running maximum and the two sums a
 // thread (rescaled where a step of loads raises the maximum).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
 // k-th largest logit from below, and a search over the bits of an order-preserving key finds it by 16 block-wide counts.  Only the threads whose maximum
-// reaches the bound (about k of 512) have their logits read once more, from L2, by a warp together.  Equal values go by
+// reaches the bound (about k) have their logits read once more, from L2, by a warp together.  Equal values go by
 // the lower index: where too many share the bound (masked rows), they are taken in the order of their index.
 // Parts are joined by a second kernel in their order.  Bound by HBM for many rows, by two launches and the
 // searches' barriers for one.
@@ -16,9 +16,9 @@ GQ_ERROR_ACCESSOR(logprobs)
 
 namespace {
 
-constexpr int kThreads = 512, kJoinThreads = 256;
+constexpr int kJoinThreads = 256;
 constexpr int kMaxTop = 32, kMaxPart = 65536, kMaxSplits = 64;
-constexpr int kFound = 4096;                      // candidates: 31 threads of kMaxPart / kThreads logits fit
+constexpr int kFound = 2048;                      // candidates
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
@@ -45,7 +45,7 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 __device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return static_cast<uint64_t>(key) << 32 | (0xffffffffu - index); }
 
-// s = sum 2^t, u = sum 2^t t, m the largest logit.  Near: t = c x - r with r = c m rounded, one fma, while |r| < 2^20 (r is then off by at most
+// s = sum 2^t, u = sum 2^t t, m the largest logit or one near it.  Near: t = c x - r with r = c m rounded, one fma, while |r| < 2^20 (r is then off by at most
 // 1/32, the same in every term).  Far: t = c (x - m), for rows whose largest logit is further out, summed once more.
 struct Sums { float m, s, u; };
 constexpr float kNear = 1048576.f;
@@ -83,6 +83,9 @@ __device__ __forceinline__ Sums of_lanes(Sums t, float c, bool far) {
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int W = 4;
+    static __device__ __forceinline__ float largest(const uint4& r) {
+        return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+    }
     static __device__ __forceinline__ float one(const uint4& r, int j) { return __uint_as_float(j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w); }
     static __device__ __forceinline__ void get(const uint4& r, float (&v)[4]) {
         v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
@@ -90,6 +93,13 @@ template <> struct Vec<float> {
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int W = 8;
+    static __device__ __forceinline__ float largest(const uint4& r) {             // in packed maxima
+        uint32_t m, n;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
     static __device__ __forceinline__ float one(const uint4& r, int j) {
         const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
         return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
@@ -105,6 +115,13 @@ template <> struct Vec<__nv_bfloat16> {
 };
 template <> struct Vec<__half> {
     static constexpr int W = 8;
+    static __device__ __forceinline__ float largest(const uint4& r) {             // in packed maxima
+        uint32_t m, n;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+        return max_nan(__half2float(__ushort_as_half(static_cast<unsigned short>(m))), __half2float(__ushort_as_half(static_cast<unsigned short>(m >> 16))));
+    }
     static __device__ __forceinline__ float one(const uint4& r, int j) {
         const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
         return __half2float(__ushort_as_half(static_cast<unsigned short>(j & 1 ? w >> 16 : w)));
@@ -143,15 +160,16 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, con
 __host__ __device__ __forceinline__ float4* part_sums(void* w) { return static_cast<float4*>(w); }
 __device__ __forceinline__ uint64_t* part_best(void* w, size_t parts) { return reinterpret_cast<uint64_t*>(static_cast<float4*>(w) + parts); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
-    constexpr int W = Vec<T>::W, UN = 2;
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
+    constexpr int W = Vec<T>::W, UN = kThreads == 128 ? 3 : 2;
     __shared__ uint64_t found[kFound];
     __shared__ Sums warp_sums[kThreads / 32];
     __shared__ int count, warp_counts[kThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const size_t row = blockIdx.x / splits;
-    const int split = blockIdx.x % splits, v0 = split * part, n = max(0, min(part, a.vocab - v0));
+    const unsigned row32 = splits == 1 ? blockIdx.x : blockIdx.x / splits;
+    const size_t row = row32;
+    const int split = blockIdx.x - row32 * splits, v0 = split * part, n = max(0, min(part, a.vocab - v0));
     const T* x = static_cast<const T*>(a.x) + row * a.stride + v0;
     const int k = a.top;
     const float c = a.scale * kLog2e;
@@ -169,10 +187,11 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
     auto stream = [&](bool far) {
         const float least = far ? kLowest : max_nan(floor_of(c), kLowest);
         t = {least, 0.f, 0.f};
+        bool hidden = false;
         if (extra >= 0) {
             const float f = to_f32(x[extra]);
             top = max_nan(top, f);
-            t.m = max_nan(f, least);
+            if (f > least) t.m = f;
             add(t, f, c, far);
         }
         for (int v = tid; v < vecs; v += UN * kThreads) {
@@ -183,28 +202,42 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
 #pragma unroll
             for (int i = 0; i < UN; ++i) {
                 if (v + i * kThreads >= vecs) break;
-                float f[W];
-                Vec<T>::get(r[i], f);
-                float m = f[0];
-#pragma unroll
-                for (int j = 1; j < W; ++j) m = max_nan(m, f[j]);
+                const float m = Vec<T>::largest(r[i]);
                 top = max_nan(top, m);
-                if (!(m <= t.m)) rescale(t, max_nan(t.m, m), c, far);      // rare after the first steps
+                // a thread's m stays until a logit is 2^60 times its weight: were it the running maximum, one of a warp's 32 would rise at almost
+                // every one of a row's few steps
+                if ((far ? c * (m - t.m) : fmaf(c, m, -(c * t.m))) > 60.f) rescale(t, m, c, far);
                 if (far) {
 #pragma unroll 1
                     for (int j = 0; j < W; ++j) add(t, Vec<T>::one(r[i], j), c, true);
                     continue;
                 }
                 // two sums side by side, packed
-                const float low = -(c * t.m);
+                float f[W];
+                Vec<T>::get(r[i], f);
+                const float2 low = make_float2(-(c * t.m), -(c * t.m)), cc = make_float2(c, c);
                 float2 s2 = make_float2(0.f, 0.f), u2 = s2;
+                if (!hidden) {
 #pragma unroll
-                for (int j = 0; j < W; j += 2) {
-                    float2 d = ffma2(make_float2(c, c), make_float2(f[j], f[j + 1]), make_float2(low, low));
-                    d = make_float2(max_nan(d.x, -1e4f), max_nan(d.y, -1e4f));     // -inf: no weight, and no 0 * inf
-                    const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
-                    s2 = fadd2(s2, e);
-                    u2 = ffma2(e, d, u2);
+                    for (int j = 0; j < W; j += 2) {
+                        const float2 d = ffma2(cc, make_float2(f[j], f[j + 1]), low);
+                        const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+                        s2 = fadd2(s2, e);
+                        u2 = ffma2(e, d, u2);
+                    }
+                    hidden = u2.x + u2.y != u2.x + u2.y;                   // 0 * inf
+                }
+                if (hidden) {
+                    // a logit of -inf has no weight; rows with one take this way from there on
+                    s2 = u2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < W; j += 2) {
+                        float2 d = ffma2(cc, make_float2(f[j], f[j + 1]), low);
+                        d = make_float2(max_nan(d.x, -1e4f), max_nan(d.y, -1e4f));
+                        const float2 e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+                        s2 = fadd2(s2, e);
+                        u2 = ffma2(e, d, u2);
+                    }
                 }
                 t.s += s2.x + s2.y;
                 t.u += u2.x + u2.y;
@@ -269,16 +302,16 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
         return count;
     };
     const int few = 2 * k + 16;
+    uint64_t kept = 0;
     int have = kFound + 1;
     int reach;
     if (k == 1) {
-        // the largest: that of the sums, but for parts of nothing above -inf
-        bound = key_of(t.m);
+        __shared__ uint32_t largest[kThreads / 32];
+        bound = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) largest[warp] = bound;
+        __syncthreads();
+        bound = __reduce_max_sync(0xffffffffu, largest[lane % (kThreads / 32)]);
         reach = __syncthreads_count(mine >= bound);
-        if (reach == 0) {
-            bound = 0;
-            reach = search(31, 16, kThreads);
-        }
     } else reach = search(31, 16, kThreads);
     if (reach <= few) have = gather(bound);
     if (have > kFound) {
@@ -289,11 +322,35 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const LogprobArgs
         have = kFound + 1;
         if (reach <= few) have = gather(bound);
         if (have > kFound) {
-            // logits above the bound lie with fewer than k threads; of those at the bound the first few, in their order
+            // of the logits at the bound the first few, in their order, behind those above it
             __syncthreads();
             if (tid == 0) count = 0;
             __syncthreads();
             have = bound == ~0u ? 0 : gather(bound + 1);
+            if (have > kFound) {
+                // too many above it with fewer than k threads: one after another, each the largest below the one before
+                uint64_t below = ~0ull;
+                for (have = 0; have < k; ++have) {
+                    uint64_t best = 0;
+                    for (int i = tid; i < n; i += kThreads) {
+                        const uint64_t e = entry(key_of(to_f32(x[i])), v0 + i);
+                        if (e < below && e > best) best = e;
+                    }
+                    __syncthreads();
+                    found[tid] = best;
+                    __syncthreads();
+                    for (int o = kThreads / 2; o > 0; o >>= 1) {
+                        if (tid < o) found[tid] = max(found[tid], found[tid + o]);
+                        __syncthreads();
+                    }
+                    below = found[0];
+                    if (tid == have) kept = below;
+                    if (below == 0) break;
+                }
+                __syncthreads();
+                if (tid < have) found[tid] = kept;
+                __syncthreads();
+            }
             int need = k - have;
             for (int at = 0; at < n && need > 0; at += kThreads) {
                 const bool is = at + tid < n && key_of(to_f32(x[at + tid])) == bound;
@@ -421,7 +478,11 @@ cudaError_t launch(K kernel, unsigned grid, int threads, cudaStream_t s, A... ar
 template <typename T>
 cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
     const int splits = splits_of(a.m, a.vocab), part = (a.vocab + splits - 1) / splits;
-    const cudaError_t e = launch(logprobs_kernel<T>, static_cast<unsigned>(a.m) * splits, kThreads, s, a, splits, part);
+    const unsigned blocks = static_cast<unsigned>(a.m) * splits;
+    // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us); few: the most
+    // loads in flight for each.
+    const cudaError_t e = blocks >= 152 * 8 ? launch(logprobs_kernel<T, 128>, blocks, 128, s, a, splits, part)
+                                            : launch(logprobs_kernel<T, 512>, blocks, 512, s, a, splits, part);
     if (e != cudaSuccess || splits == 1) return e;
     return launch(logprobs_join_kernel<T>, static_cast<unsigned>(a.m), kJoinThreads, s, a, splits);
 }

@@ -25,7 +25,7 @@ def gq():
 def exact(x, tokens, top, scale):
     lp = torch.log_softmax(scale * x.double(), -1)
     h = -torch.where(lp == -math.inf, 0.0, lp.exp() * lp).sum(-1)
-    order = torch.sort(x.float().cpu(), dim=-1, descending=True, stable=True).indices[:, :top].cuda()
+    order = torch.sort(x.float(), dim=-1, descending=True, stable=True).indices[:, :top]
     return lp.gather(1, tokens[:, None]).squeeze(1), h, order, lp.gather(1, order)
 
 
@@ -57,7 +57,7 @@ def normal(seed, m, vocab, size=3.0):
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("m,vocab,top", [
     (1, 1, 1), (1, 2, 2), (3, 7, 5), (2, 33, 32), (5, 511, 0), (4, 513, 1), (2, 4095, 32), (1, 49152, 20), (3, 49153, 5), (40, 5000, 10),
-    (305, 1000, 7), (310, 8191, 32), (7, 128256, 20), (2, 200001, 32), (1, 1 << 20, 32), (306, 70000, 3)])
+    (305, 1000, 7), (310, 8191, 32), (7, 128256, 20), (2, 200001, 32), (1, 1 << 20, 32), (306, 70000, 3), (1216, 4099, 5), (1300, 999, 32), (2000, 12000, 1)])
 def test_values(gq, m, vocab, top, kind):
     check(gq, normal(m + vocab, m, vocab).to(TYPES[kind]), top)
 
@@ -87,7 +87,17 @@ def test_logits_far_from_zero(gq, m, first, size):
     check(gq, x, 6)
 
 
-@pytest.mark.parametrize("m", [2, 400])
+@pytest.mark.parametrize("m,vocab,threads", [(400, 65536, 512), (1300, 20000, 128)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_more_candidates_than_fit(gq, m, vocab, threads, kind):
+    """Thousands of a row's logits with fewer threads than alternatives are asked for, above the others' maxima."""
+    x = normal(11, m, vocab, 0.25).abs().to(TYPES[kind])
+    width = 4 if kind == "f32" else 8
+    x[:, torch.arange(vocab, device="cuda") // width % threads >= 24] = 0
+    check(gq, x, 32)
+
+
+@pytest.mark.parametrize("m", [2, 400, 1300])
 @pytest.mark.parametrize("top", [1, 5, 32])
 def test_ties_go_by_index(gq, m, top):
     """Equal logits everywhere, two values, a few values, both zeros, and sorted rows (the best ones all with one thread's neighbours)."""
@@ -109,7 +119,7 @@ def test_ties_go_by_index(gq, m, top):
     check(gq, near, top)
 
 
-@pytest.mark.parametrize("m,vocab", [(1, 49152), (3, 999), (330, 5001)])
+@pytest.mark.parametrize("m,vocab", [(1, 49152), (3, 999), (330, 5001), (1300, 3001)])
 @pytest.mark.parametrize("left", [0, 1, 3, 40])
 def test_masked_rows(gq, m, vocab, left):
     """-inf, or the type's lowest value, but for `left` logits of a row."""
@@ -127,7 +137,7 @@ def test_masked_rows(gq, m, vocab, left):
             assert torch.equal(r.top_ids, torch.arange(5, device="cuda").repeat(m, 1))
 
 
-@pytest.mark.parametrize("m", [3, 400])
+@pytest.mark.parametrize("m", [3, 400, 1300])
 def test_rows_with_nan_or_infinity(gq, m):
     """They give NaN, their alternatives in order (NaN first), and the other rows what they would."""
     x = normal(6, m, 6000)
@@ -147,7 +157,7 @@ def test_rows_with_nan_or_infinity(gq, m):
 def test_given_tokens(gq):
     """Negative ones count for nothing; one past the vocabulary gives NaN and an error."""
     assert gq.device_error() == 0
-    for m in (4, 500):
+    for m in (4, 500, 1300):
         x = normal(7, m, 2000)
         tokens = torch.full((m,), 5, dtype=torch.int64, device="cuda")
         tokens[1], tokens[2] = -100, 1999
