@@ -21,8 +21,9 @@ struct NormArgs {
     size_t plane;                                     // m * k: the operand's plane stride
 };
 
-template <typename T, bool VEC>
+template <typename T, int VEC>
 __device__ __forceinline__ float4 load_row4(const T* row, int i, int k) {
+    if (VEC == 2) return load4(row + i);             // inside the row
     if (VEC) return i < k ? load4(row + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 v;
     v.x = i < k ? to_f32(row[i]) : 0.f;
@@ -31,10 +32,10 @@ __device__ __forceinline__ float4 load_row4(const T* row, int i, int k) {
     v.w = i + 3 < k ? to_f32(row[i + 3]) : 0.f;
     return v;
 }
-template <typename T, bool VEC>
+template <typename T, int VEC>
 __device__ __forceinline__ void store_row4(T* row, int i, int k, float4 v) {
     if (VEC) {
-        if (i < k) store4(row + i, v);
+        if (VEC == 2 || i < k) store4(row + i, v);
         return;
     }
     if (i < k) from_f32(row + i, v.x);
@@ -202,18 +203,23 @@ struct BlockNormArgs {
 };
 
 // Four values of a row as they are stored, or in f32 where they cannot be loaded together
-template <typename T, bool VEC> struct Kept {
+template <typename T, int VEC> struct Kept {
     float4 v;
     __device__ __forceinline__ void load(const T* row, int i, int k) { v = load_row4<T, VEC>(row, i, k); }
     __device__ __forceinline__ float4 get() const { return v; }
 };
-template <typename T> struct Kept<T, true> {
+template <typename T> struct KeptRaw {
     typename Vec4<T>::Raw r;
-    __device__ __forceinline__ void load(const T* row, int i, int k) {
-        r = typename Vec4<T>::Raw{};
-        if (i < k) r = *reinterpret_cast<const typename Vec4<T>::Raw*>(row + i);
-    }
     __device__ __forceinline__ float4 get() const { return Vec4<T>::widen(r); }
+};
+template <typename T> struct Kept<T, 1> : KeptRaw<T> {
+    __device__ __forceinline__ void load(const T* row, int i, int k) {
+        this->r = typename Vec4<T>::Raw{};
+        if (i < k) this->r = *reinterpret_cast<const typename Vec4<T>::Raw*>(row + i);
+    }
+};
+template <typename T> struct Kept<T, 2> : KeptRaw<T> {
+    __device__ __forceinline__ void load(const T* row, int i, int) { this->r = *reinterpret_cast<const typename Vec4<T>::Raw*>(row + i); }
 };
 
 __device__ __forceinline__ float row_sum(float s, float* part, int tid, int nt) {
@@ -230,8 +236,8 @@ __device__ __forceinline__ float row_sum(float s, float* part, int tid, int nt) 
 __device__ __forceinline__ float squares(float4 v, float s) { return fmaf(v.w, v.w, fmaf(v.z, v.z, fmaf(v.y, v.y, fmaf(v.x, v.x, s)))); }
 __device__ __forceinline__ float squares_again(float4 v, float s) { return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s)))); }
 
-template <typename T, int NV, bool VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_kernel(const BlockNormArgs b) {
+template <typename T, int NV, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_kernel(const BlockNormArgs b) {
     __shared__ float part[2][32];
     const NormArgs& a = b.n;
     const int tid = threadIdx.x, nt = blockDim.x, k = a.k;
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // all of a row's loads before the first sum, x and the gate kept as they are stored: behind the barriers a load costs its whole round
-    // trip (8192 bf16 rows of 4096 with a gate for each, and the blocks' read back: 131 -> 91 us)
+    // trip (8192 bf16 rows of 4096 with a gate for each, and the blocks' read back: 131 -> 109 us)
     float4 v[NV];
     Kept<T, VEC> x[NV], g[NV];
 #pragma unroll
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) s = squares(v[c], s);
-        for (int c = NV; c < chunks; ++c) s = squares_again(load_row4<T, VEC>(yr, 4 * (c * nt + tid), k), s);
+        if (VEC < 2) for (int c = NV; c < chunks; ++c) s = squares_again(load_row4<T, VEC>(yr, 4 * (c * nt + tid), k), s);
         s = row_sum(s, part[0], tid, nt);
         rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
     }
@@ -294,11 +300,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) block_norm_ke
         const float4 w = load_row4<float, VEC>(a.w, i, k);
         const float4 z = make_float4(h.x * rstd2 * w.x, h.y * rstd2 * w.y, h.z * rstd2 * w.z, h.w * rstd2 * w.w);
         if (a.y) store_row4<T, VEC>(static_cast<T*>(a.y) + row * k, i, k, z);
-        if (a.act || a.q) quantize4(a, row, i, i < k, z);
+        if (a.act || a.q) quantize4(a, row, i, VEC == 2 || i < k, z);
     };
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-        if (c < chunks) emit(4 * (c * nt + tid), v[c]);
+        if (VEC == 2 || c < chunks) emit(4 * (c * nt + tid), v[c]);
     for (int c = NV; c < chunks; ++c) {
         const int i = 4 * (c * nt + tid);
         emit(i, again(i));
@@ -316,7 +322,10 @@ cudaError_t block_norm_go(const BlockNormArgs& b, int m, int nt, bool vec, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return vec ? cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, true, 1024>, b) : cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, false, 1024>, b);
+    // rows that fill their threads need no checks of bounds, and four blocks of 256 threads an SM then hold enough loads (the same case 109 -> 97 us;
+    // three of them 109, 128 threads a row of 8 chunks 107)
+    if (vec && nt <= 256 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 256>, b);
+    return vec ? cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 1, 1024>, b) : cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 0, 1024>, b);
 }
 
 template <typename T>
