@@ -346,11 +346,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             const int r = (warp & 3) * 32 + lane, m = (warp - kWarpA0) >> 2;
             const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(kA0 + m * kACols);
             const int tiles = (a.rows + BM - 1) / BM;
-            auto arrive = [&](uint32_t g) {                                // the weights of stage g are there
+            auto arrive = [&](uint32_t g) {                                // the weights of stages g and g + 1 are there
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->full[g % kStages]);
+                if (lane == 0) {
+                    mbar_arrive(&bars->full[g % kStages]);
+                    mbar_arrive(&bars->full[(g + 1) % kStages]);
+                }
             };
             uint32_t g = 0;
             bool live = true;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                             for (int p = 0; p < 16; ++p) av[p] = ((word << (15 - p)) & 0x80008000u) ^ neg;
                         };
                         expand(words[2 * half]);
-                        if (g > 0) arrive(g - 1);                          // the stores of the stage before went on meanwhile
+                        if (half == 0 && g > 0) arrive(g - 2);             // the stores of the block before went on meanwhile
                         if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                             live = false;
                             break;
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     }
                 }
             }
-            if (live && g > 0) arrive(g - 1);
+            if (live && g > 0) arrive(g - 2);
         }
     }
 
