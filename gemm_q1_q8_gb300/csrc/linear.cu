@@ -1,7 +1,7 @@
 // Q1_0 products with an epilogue, few tokens (one decoded token to a batch): mma.sync, weights straight from memory.
 //
-// A thread block holds 32 rows (of both matrices of a pair) and 8 * NT tokens.  Its 16 warps are two groups of 16 rows by eight shares
-// of the 128-blocks.  Signs become +-d0 as f16 by a shift and a logic operation a pair, codes are f16 as they are, so two
+// A thread block holds 32 rows (of both matrices of a pair) and 8 * NT tokens.  Its 16 (8) warps are two groups of 16 rows by eight (four) shares
+// of the 128-blocks; the smaller block, of which an SM holds two, where the larger would come in two waves.  Signs become +-d0 as f16 by a shift and a logic operation a pair, codes are f16 as they are, so two
 // m16n8k16 products give the 32-block sums d0 * sum(+-q) exactly; they are multiplied by the token's scale and added in f32 registers.  In a word,
 // lane t of a row's four takes the bit pairs 4 t .. 4 t + 3 (bits p and p + 16 are one register): weights need no shuffles and no
 // shared memory.  Codes are written to shared memory once for a segment of the blocks, in the order of the lanes' 16-byte reads.
@@ -12,7 +12,7 @@
 namespace gq {
 namespace {
 
-constexpr int kWarps = 16, kShares = 8, kThreads = kWarps * 32, kBlockRows = 32;
+constexpr int kBlockRows = 32;
 
 // d = a . b (from zero), then d += a . b
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -24,17 +24,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // What a lane loads of a 128-block: the words of rows g and g + 8, and their scales
 struct Piece { uint4 w[2]; uint32_t d[2]; };
 
-// Codes of a 128-block and 8 tokens: 2 KB, in [sub-block][lane][register]; and its scales, [sub-block][token]
-__host__ __device__ constexpr int block_bytes(int nt) { return nt * (2048 + 4 * 8 * 4); }
-// Blocks of a segment: up to 208 KB, a multiple of the shares
-__host__ __device__ constexpr int most_blocks(int nt) { return nt == 8 ? 8 : 96 / nt; }
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
-template <int NT, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) linear_rows_kernel(const LinearArgs a, int segment) {
+// Of a 128-block and 8 tokens: codes in [sub-block][lane][register], 2 KB; scales, [sub-block][token]; the tokens' bytes
+__host__ __device__ constexpr int block_bytes(int nt) { return nt * (2048 + 4 * 8 * 4 + 8 * 136); }
+// Blocks of a segment: up to 209 KB, a multiple of the shares
+__host__ __device__ constexpr int most_blocks(int nt) { return nt == 8 ? 8 : 64 / nt; }
+
+template <int NT, bool PAIR, int kShares>
+__global__ void __launch_bounds__(64 * kShares, 8 / kShares) linear_rows_kernel(const LinearArgs a, int segment) {
+    constexpr int kWarps = 2 * kShares, kThreads = 32 * kWarps;
     constexpr int MT = PAIR ? 2 : 1, TOK = 8 * NT, U = NT * MT <= 2 ? 3 : NT * MT <= 4 ? 2 : 1;
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t* codes = reinterpret_cast<uint32_t*>(smem);                        // [segment][NT][4][32 lanes][4]
     float* scales = reinterpret_cast<float*>(smem + static_cast<size_t>(segment) * NT * 2048);      // [segment][4][TOK]
+    uint8_t* raw = smem + static_cast<size_t>(segment) * NT * (2048 + 128);     // [TOK][segment][136 bytes]
     float* red = reinterpret_cast<float*>(smem);                                // afterwards: [MT][kShares][TOK][32 rows]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int group = warp & 1, share = warp >> 1;
@@ -74,18 +80,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_rows_kernel(const LinearAr
     for (int s0 = 0; s0 < nb; s0 += segment) {
         const int blocks = min(segment, nb - s0);
         if (s0) __syncthreads();
+        // The tokens' bytes of the segment to shared memory, all on their way at once: a 128-block has 17 words of 8 bytes.  (Each 4 codes loaded where
+        // they are converted, by 2-byte loads: 8 tokens over 6912, 12.0 us.)
+        const bool staged = (reinterpret_cast<uintptr_t>(a.act) & 7) == 0;
+        const uint32_t words = blocks * 17, word_magic = 0xffffffffu / words + 1;
+        if (staged) {
+            for (uint32_t i = tid; i < toks * words; i += kThreads) {
+                const uint32_t tk = toks == 1 ? 0 : __umulhi(i, word_magic), e = i - tk * words;
+                cp_async8(raw + (tk * segment * 17 + e) * 8, a.act + (tok0 + tk) * row_bytes + static_cast<size_t>(s0) * 136 + e * 8);
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+        }
         // an item: four codes 4 l .. 4 l + 3 of a token's 32-block: the pairs (4 l, 4 l + 2) and (4 l + 1, 4 l + 3).  Columns of tokens that
         // do not exist stay as they are: a column's sums are its own.
-        const int items = toks * blocks * 32, per = blocks * 32;
-#pragma unroll 4
-        for (int i = tid; i < items; i += kThreads) {
-            const int tk = NT == 1 && toks == 1 ? 0 : i / per, e = i - tk * per, l = e & 7, s = e >> 3, b = s >> 2, k = s & 3;
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.act + static_cast<size_t>(tok0 + tk) * row_bytes + static_cast<size_t>(4 * s0 + s) * 34);
+        const uint32_t per = blocks * 32, magic = 0xffffffffu / per + 1;      // quotients are exact below 2^20
+#pragma unroll 2
+        for (uint32_t i = tid; i < toks * per; i += kThreads) {
+            const uint32_t tk = toks == 1 ? 0 : __umulhi(i, magic), e = i - tk * per, l = e & 7, s = e >> 3, b = s >> 2, k = s & 3;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(staged ? raw + tk * segment * 136 + s * 34
+                                                                         : a.act + (tok0 + tk) * row_bytes + static_cast<size_t>(4 * s0 + s) * 34);
             const uint32_t lo = p[1 + 2 * l], hi = p[2 + 2 * l], w = (lo | hi << 16) ^ 0x80808080u;       // code + 128
             const uint32_t even = __byte_perm(w, 0x64646464u, 0x4240), odd = __byte_perm(w, 0x64646464u, 0x4341);   // 1024 + that, as f16
             const __half2 bias = __half2half2(__ushort_as_half(0x6480));                                  // 1152
             const __half2 v0 = __hsub2(*reinterpret_cast<const __half2*>(&even), bias), v1 = __hsub2(*reinterpret_cast<const __half2*>(&odd), bias);
-            uint32_t* to = codes + (static_cast<size_t>((b * NT + (tk >> 3)) * 4 + k) * 32 + (tk & 7) * 4 + (l >> 2)) * 4 + (l & 3);
+            uint32_t* to = codes + ((b * NT + (tk >> 3)) * 4 + k) * 128 + ((tk & 7) * 4 + (l >> 2)) * 4 + (l & 3);
             to[0] = *reinterpret_cast<const uint32_t*>(&v0);
             to[2 * 4] = *reinterpret_cast<const uint32_t*>(&v1);
             if (l == 0) scales[s * TOK + tk] = f16_to_f32(p[0]);
@@ -172,18 +191,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_rows_kernel(const LinearAr
     }
 }
 
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, int kShares>
 cudaError_t rows_go(const LinearArgs& a, cudaStream_t s) {
-    constexpr int MT = PAIR ? 2 : 1, TOK = 8 * NT;
-    const int nb = (a.n / 128 + kShares - 1) / kShares * kShares, segment = nb < most_blocks(NT) ? nb : most_blocks(NT);
+    constexpr int MT = PAIR ? 2 : 1, TOK = 8 * NT, most_segment = most_blocks(NT) * kShares / 8 / kShares * kShares;
+    const int nb = (a.n / 128 + kShares - 1) / kShares * kShares, segment = nb < most_segment ? nb : most_segment;
     const size_t sum = static_cast<size_t>(MT) * kShares * TOK * 32 * 4, operand = static_cast<size_t>(segment) * block_bytes(NT);
-    const size_t smem = sum > operand ? sum : operand, most = std::max(sum, static_cast<size_t>(most_blocks(NT)) * block_bytes(NT));
+    const size_t smem = sum > operand ? sum : operand, most = std::max(sum, static_cast<size_t>(most_segment) * block_bytes(NT));
     static std::atomic<uint64_t> raised{0};
-    const cudaError_t e = allow_smem(linear_rows_kernel<NT, PAIR>, most, raised);
+    const cudaError_t e = allow_smem(linear_rows_kernel<NT, PAIR, kShares>, most, raised);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.rows + kBlockRows - 1) / kBlockRows, (a.cols + TOK - 1) / TOK);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(64 * kShares);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -191,32 +210,40 @@ cudaError_t rows_go(const LinearArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_rows_kernel<NT, PAIR>, a, segment);
+    return cudaLaunchKernelEx(&cfg, linear_rows_kernel<NT, PAIR, kShares>, a, segment);
 }
 
 template <bool PAIR>
-cudaError_t rows_tokens(const LinearArgs& a, cudaStream_t s) {
-    if (a.cols <= 8) return rows_go<1, PAIR>(a, s);
-    if (a.cols <= 16) return rows_go<2, PAIR>(a, s);
-    if (a.cols <= 32) return rows_go<4, PAIR>(a, s);
-    return rows_go<8, PAIR>(a, s);
+cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
+    const bool small = (a.rows + kBlockRows - 1) / kBlockRows > 152;
+    if (a.cols <= 8) return small ? rows_go<1, PAIR, 4>(a, s) : rows_go<1, PAIR, 8>(a, s);
+    if (a.cols <= 16) return small ? rows_go<2, PAIR, 4>(a, s) : rows_go<2, PAIR, 8>(a, s);
+    return rows_go<4, PAIR, 8>(a, s);
 }
 
 }  // namespace
 
-// Up to this many tokens the rows' kernel
-constexpr int kRowTokens = 32;
+// Up to 32 tokens the rows' kernel may be taken, where it is the faster one by its cost (linear_tiles.cu has the tiles'): fitted to 1 to 32 tokens of
+// 400 x 1024, 2560 x 2560, 2560 x 6912 and 14336 x 8192 and the pairs of 6912 x 2560 and 14336 x 4096, in microseconds.
+bool linear_by_rows(int rows, int n, int cols, bool pair, int parts) {
+    if (cols > 32) return false;
+    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+    const float waves = static_cast<float>(((rows + kBlockRows - 1) / kBlockRows + 151) / 152);
+    const float us = 1.7f + waves * (0.5f + n * 1e-3f * (0.25f + 0.08f * cols + (pair ? 0.7f : 0.25f) * nt));
+    return us < linear_tiles_us(rows, n, cols, parts, pair);
+}
 
 cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s) {
-    if (a.cols > kRowTokens) return launch_linear_tiles(a, pair, s);
-    return pair ? rows_tokens<true>(a, s) : rows_tokens<false>(a, s);
+    if (!linear_by_rows(a.rows, a.n, a.cols, pair, linear_parts(a))) return launch_linear_tiles(a, pair, s);
+    return pair ? launch_linear_rows<true>(a, s) : launch_linear_rows<false>(a, s);
 }
 
 size_t linear_workspace_bytes(int rows, int n, int cols, int type) {
-    if (cols <= kRowTokens) return 16;
-    // bf16 may take one part or, with Q8_0 outputs, two
-    size_t need = linear_tiles_workspace_bytes(rows, n, cols, 2);
-    if (type == GQ_BF16) need = std::max(need, linear_tiles_workspace_bytes(rows, n, cols, 1));
+    // for either call; bf16 may take one part or, with Q8_0 outputs, two
+    size_t need = 16;
+    for (int pair = 0; pair < 2; ++pair)
+        for (int parts = type == GQ_BF16 ? 1 : 2; parts <= 2; ++parts)
+            if (!linear_by_rows(rows, n, cols, pair, parts)) need = std::max(need, linear_tiles_workspace_bytes(rows, n, cols, parts, pair));
     return need;
 }
 

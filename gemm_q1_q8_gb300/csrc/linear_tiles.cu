@@ -22,7 +22,7 @@ namespace {
 
 constexpr int BM = 128, BK = 64, kStages = 4, kTmemCols = 512;
 constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a stage's slot: kACols for each matrix
-constexpr int kTileB = 128 * BK * 2, kTilesB = 10;                         // a part of up to 128 tokens; room for 5 or 10 stages
+constexpr int kTileB = 128 * BK * 2;                                       // a part of up to 128 tokens; a stage has two
 constexpr int kStaged = 2 * 32 * 32 * 4;                                   // of a sums warp: half its columns of both matrices
 constexpr int kWarpA0 = 4, kWarpE0 = 12, kEWarps = 8, kThreads = 640;
 constexpr int kRegs = 96, kRegsSums = 168, kRegsRest = 48;                 // a thread's at launch, of 8 warps, of the other 12
@@ -30,13 +30,11 @@ static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
 static_assert(kRegsSums * 256 + kRegsRest * 384 <= kRegs * kThreads && kRegs * kThreads <= 65536, "registers");
 
 struct Bars {
-    uint64_t full[kStages];            // eight weight warps
-    uint64_t done[kStages];            // both matrices' MMAs of the stage are complete: its weights' slot is free
-    uint64_t bfull[kTilesB];           // the copy's expect_tx and its bytes
-    uint64_t bdone[kTilesB];           // as done, of the copy's slot
+    uint64_t full[kStages];            // eight weight warps, the copy's expect_tx and its bytes
+    uint64_t done[kStages];            // both matrices' MMAs of the stage are complete: its slots are free
     uint64_t accfull[2], accempty[2];  // a matrix's round is complete; drained
     uint64_t final_;
-    int last_copy[kTilesB];            // the last copy into each slot, -1: none
+    int last_copy[kStages];            // the last copy into each slot, -1: none
     uint32_t tmem_base;
     int abort;
 };
@@ -113,20 +111,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
     constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);   // f32 += f16 x f16
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sB = smem_align1024(smem_raw);                                // [stage][part][BN rows of 128 bytes]
-    uint8_t* staged = sB + kTilesB * kTileB;                               // [sums warp][matrix][column][32 rows] f32
+    uint8_t* staged = sB + kStages * 2 * kTileB;                               // [sums warp][matrix][column][32 rows] f32
     Bars* bars = reinterpret_cast<Bars*>(staged + kEWarps * kStaged);
     volatile int* abort = &bars->abort;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const int nb = a.n / 128, parts = plan.parts, slots = kTilesB / parts, half_round = plan.round / 2;
+    const int nb = a.n / 128, parts = plan.parts, half_round = plan.round / 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 8);
+            mbar_init(&bars->full[s], 9);
             mbar_init(&bars->done[s], 2);
-        }
-        for (int s = 0; s < kTilesB; ++s) {
-            mbar_init(&bars->bfull[s], 1);
-            mbar_init(&bars->bdone[s], 2);
             bars->last_copy[s] = -1;
         }
         for (int m = 0; m < 2; ++m) {
@@ -271,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             const int m = warp;
             const uint32_t leader = elect_one();
             const uint32_t d = tmem + static_cast<uint32_t>(m * kDCols);
-            uint32_t g = 0, turn = 0, slot = 0, lap = 0;                   // lap: times around the copies' ring
+            uint32_t g = 0, turn = 0;
             bool live = true;
             for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
                 const Unit w = unit_of<BN>(plan, u, nb);
@@ -280,14 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 for (int k = w.k0; k < w.k1; ++k, ++g) {
                     const int s = g % kStages;
                     const bool last = r == 2 * half_round - 1 || k == w.k1 - 1;
-                    const bool ready = wait_or_abort_sleep(&bars->bfull[slot], lap & 1u, abort) && wait_or_abort_sleep(&bars->full[s], (g / kStages) & 1u, abort) &&
+                    const bool ready = wait_or_abort_sleep(&bars->full[s], (g / kStages) & 1u, abort) &&
                                        (!first || turn == 0 || wait_or_abort_sleep(&bars->accempty[m], (turn - 1) & 1u, abort));
                     if (!__all_sync(0xffffffffu, ready)) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t bdesc = smem_desc(sB + slot * parts * kTileB);
+                    const uint64_t bdesc = smem_desc(sB + s * 2 * kTileB);
                     const uint32_t av = tmem + static_cast<uint32_t>(kA0 + (2 * s + m) * kACols);
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
@@ -300,16 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     if (leader) {
                         if (last) tc_commit(&bars->accfull[m]);
                         tc_commit(&bars->done[s]);
-                        tc_commit(&bars->bdone[slot]);
                     }
                     __syncwarp();
                     first = last;
                     r = last ? 0 : r + 1;
                     turn += last;
-                    if (++slot == slots) {
-                        slot = 0;
-                        ++lap;
-                    }
                 }
             }
             if (leader) tc_commit(&bars->final_);
@@ -319,26 +308,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
             const uint32_t leader = elect_one();
             if (leader) prefetch_tmap(&tmB);
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            int slot = 0, lap = 0;
+            uint32_t g = 0;
             bool live = true;
             for (int u = blockIdx.x; u < plan.units && live; u += gridDim.x) {
                 const Unit w = unit_of<BN>(plan, u, nb);
-                for (int k = w.k0; k < w.k1; ++k) {
-                    if (lap > 0 && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->bdone[slot], (lap - 1) & 1u, abort))) {
+                for (int k = w.k0; k < w.k1; ++k, ++g) {
+                    const int s = g % kStages;
+                    if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                         live = false;
                         break;
                     }
                     if (leader) {
-                        mbar_arrive_expect_tx(&bars->bfull[slot], static_cast<uint32_t>(parts * BN * 128));
-                        bars->last_copy[slot] = lap;
+                        mbar_arrive_expect_tx(&bars->full[s], static_cast<uint32_t>(parts * BN * 128));
+                        bars->last_copy[s] = static_cast<int>(g);
                     }
                     __syncwarp();
                     for (int p = 0; p < parts; ++p)
-                        tma_load(leader, sB + (slot * parts + p) * kTileB, &tmB, k * BK, p * a.cols + w.tok0, &bars->bfull[slot]);
-                    if (++slot == slots) {
-                        slot = 0;
-                        ++lap;
-                    }
+                        tma_load(leader, sB + (s * 2 + p) * kTileB, &tmB, k * BK, p * a.cols + w.tok0, &bars->full[s]);
                 }
             }
         } else if (warp >= kWarpA0) {
@@ -361,15 +347,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 const Unit w = unit_of<BN>(plan, u, nb);
                 const uint8_t* src = (m ? a.w[1] : a.w[0]) + static_cast<size_t>(PAIR ? w.row_tile : min(2 * w.row_tile + m, tiles - 1)) * nb * kChunkBytes +
                                      static_cast<size_t>(w.k0 / 2) * kChunkBytes;
-                uint4 bits = *reinterpret_cast<const uint4*>(src + r * 16);
-                uint32_t d0 = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
-                for (int k = w.k0; k < w.k1 && live; k += 2) {
-                    const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w}, neg = (d0 * 0x00010001u) ^ 0x80008000u;   // a clear bit gives -d0
+                // blocks loaded three ahead: a block's MMAs take 370 to 2000 cycles, a load up to 1000
+                uint4 bits[3];
+                uint32_t d0[3];
+                auto load = [&](int i) {
+                    bits[i] = *reinterpret_cast<const uint4*>(src + r * 16);
+                    d0[i] = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
                     src += kChunkBytes;
-                    if (k + 2 < w.k1) {
-                        bits = *reinterpret_cast<const uint4*>(src + r * 16);
-                        d0 = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
-                    }
+                };
+                int ahead = w.k0;
+#pragma unroll
+                for (int i = 0; i < 3; ++i, ahead += 2)
+                    if (ahead < w.k1) load(i);
+                for (int k = w.k0; k < w.k1 && live; k += 2, ahead += 2) {
+                    const uint32_t words[4] = {bits[0].x, bits[0].y, bits[0].z, bits[0].w}, neg = (d0[0] * 0x00010001u) ^ 0x80008000u;   // a clear bit gives -d0
+                    bits[0] = bits[1], bits[1] = bits[2];
+                    d0[0] = d0[1], d0[1] = d0[2];
+                    if (ahead < w.k1) load(2);
 #pragma unroll
                     for (int half = 0; half < 2; ++half, ++g) {
                         const int s = g % kStages;
@@ -406,9 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
     tc_fence_after();
     if (threadIdx.x == 64 && *abort) {
         // an aborted block may hold copies that no MMA waited for
-        for (int s = 0; s < kTilesB; ++s) {
-            const int lap = bars->last_copy[s];
-            if (lap >= 0 && !mbar_wait(&bars->bfull[s], static_cast<uint32_t>(lap) & 1u)) report_error(kErrDrainTimeout);
+        for (int s = 0; s < kStages; ++s) {
+            const int g = bars->last_copy[s];
+            if (g >= 0 && !mbar_wait(&bars->full[s], static_cast<uint32_t>(g / kStages) & 1u)) report_error(kErrDrainTimeout);
         }
     }
     if (warp == 0)
@@ -508,30 +502,35 @@ cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, cudaStream
 
 constexpr int kSMs = 152;
 
-struct Shape { int bn; Plan p; };
-// Tokens a tile and shares of n.  An MMA of 128, 96 or 64 tokens takes 64, 48 or 46 cycles: the tile whose waves take the fewest is taken.  Where
-// the tiles of one wave leave SMs idle, n is cut into shares of at least two blocks.
+struct Shape { int bn; Plan p; float us; };
+// Tokens a tile and shares of n, by their cost in microseconds, fitted to calls of 16 to 500 tokens (2560 x 2560, 2560 x 6912, pairs of 6912 x 2560 and
+// 14336 x 4096): what a tile takes once (start, epilogue), its stages (two parts: the MMAs; one: the weights' way into tensor memory), more
+// tiles an SM, and the shares' sums written and read again.
 Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
-    const int tiles = (rows + BM - 1) / BM;
+    const int tiles = (rows + BM - 1) / BM, nb = n / 128;
     Shape best = {};
-    long long least = -1;
-    for (int bn : {128, 96, 64}) {
-        Plan p = {};
-        p.row_tiles = pair ? tiles : (tiles + 1) / 2;
-        p.tok_tiles = (cols + bn - 1) / bn;
-        const long long all = static_cast<long long>(p.row_tiles) * p.tok_tiles;
-        const int nb = n / 128;
-        p.splits = 1;
-        if (all < kSMs) p.splits = std::max(1, std::min<int>(kSMs / static_cast<int>(all), nb / 2));
-        const long long units = all * p.splits, waves = (units + kSMs - 1) / kSMs;
-        const long long cost = waves * ((nb + p.splits - 1) / p.splits) * (bn == 128 ? 64 : bn == 96 ? 48 : 46);
-        if (least < 0 || cost < least) {
-            least = cost;
-            p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
-            p.parts = parts;
-            p.round = parts == 2 ? 4 : 1024;
-            p.pad_rows = tiles * BM;
-            best = {bn, p};
+    for (int i = 0; i < 3; ++i) {
+        const int bn = i == 0 ? 128 : i == 1 ? 96 : 64;
+        const float once = i == 0 ? 11.5f : i == 1 ? 9.3f : 7.5f, stage = parts == 1 ? 0.3f : i == 0 ? 0.57f : i == 1 ? 0.45f : 0.35f;
+        const int row_tiles = pair ? tiles : (tiles + 1) / 2, tok_tiles = (cols + bn - 1) / bn;
+        const long long all = static_cast<long long>(row_tiles) * tok_tiles;
+        for (int splits = 1; splits <= 16 && splits <= std::max(1, nb / 2); ++splits) {
+            const long long units = all * splits, waves = (units + kSMs - 1) / kSMs;
+            if (splits > 1 && units > kSMs) break;                         // shares are for SMs that would be idle
+            const float sums = splits == 1 ? 0.f : 0.2f + static_cast<float>(splits) * cols * rows * (pair ? 2 : 1) * 4 * (1 / 2.4e6f);
+            const float us = once + waves * 2 * ((nb + splits - 1) / splits) * stage + (waves - 1) * (once - 5) * 0.5f + sums;
+            if (best.bn == 0 || us < best.us) {
+                Plan p = {};
+                p.row_tiles = row_tiles;
+                p.tok_tiles = tok_tiles;
+                p.splits = splits;
+                p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
+                p.parts = parts;
+                // two parts: 256 of n, 32 steps; one (bf16): 65536
+                p.round = parts == 2 ? 4 : 1024;
+                p.pad_rows = tiles * BM;
+                best = {bn, p, us};
+            }
         }
     }
     return best;
@@ -546,7 +545,7 @@ cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cuda
     if (!make_tmap_2d(&tmB, parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, static_cast<uint64_t>(a.n), static_cast<uint64_t>(p.parts) * a.cols,
                       static_cast<uint64_t>(a.n) * 2, BK, BN, true))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = 1024 + static_cast<size_t>(kTilesB) * kTileB + kEWarps * kStaged + sizeof(Bars);
+    constexpr size_t smem = 1024 + static_cast<size_t>(kStages) * 2 * kTileB + kEWarps * kStaged + sizeof(Bars);
     static std::atomic<uint64_t> raised{0};
     cudaError_t e = allow_smem(linear_tiles_kernel<BN, PAIR>, smem, raised);
     if (e != cudaSuccess) return e;
@@ -558,14 +557,13 @@ cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cuda
 
 }  // namespace
 
-size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts) {
-    size_t partial = 0;
-    for (int pair = 0; pair < 2; ++pair) {
-        const Plan p = shape_of(rows, n, cols, parts, pair).p;
-        if (p.splits > 1) partial = std::max(partial, static_cast<size_t>(p.splits) * (pair ? 2 : 1) * cols * p.pad_rows * 4);
-    }
+size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts, bool pair) {
+    const Plan p = shape_of(rows, n, cols, parts, pair).p;
+    const size_t partial = p.splits > 1 ? static_cast<size_t>(p.splits) * (pair ? 2 : 1) * cols * p.pad_rows * 4 : 0;
     return parts_bytes(n, cols) + up(static_cast<size_t>(cols) * 4) + partial;
 }
+
+float linear_tiles_us(int rows, int n, int cols, int parts, bool pair) { return shape_of(rows, n, cols, parts, pair).us; }
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s) {
     Shape t = shape_of(a.rows, a.n, a.cols, linear_parts(a), pair);
