@@ -97,3 +97,47 @@ def test_binding_refuses_host_tensors():
                  lambda: gq.q1_q8_linear(None, None, 33, 128, 1, q8_0=True)):
         with pytest.raises(gq.GQError):
             call()
+
+
+ON_DEVICES = """
+import ctypes, sys
+fake, lib = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+X, LL = ctypes.c_void_p(0x1000), ctypes.c_longlong
+def calls():
+    for rows, n in ((64, 256), (2560, 6912), (14336, 4096), (6400, 16384)):
+        for m in (1, 9, 30, 64, 97, 400, 4096):
+            for t in (0, 2):
+                yield lib.q1_q8_linear(X, X, rows, n, m, None, 0, None, LL(0), t, X, LL(rows), None, X, None)
+                yield lib.q1_q8_glu(X, X, X, rows, n, m, None, None, 3, t, None, LL(0), X, X, None)
+for device in (0, 1, 0, 3, 1):
+    fake.fake_set_device(device)
+    assert not any(calls()), (device, list(calls()))
+raised = fake.fake_raised()
+for device in (0, 1, 3):
+    fake.fake_set_device(device)
+    assert not any(calls())
+assert fake.fake_raised() == raised, "raised again where it had been"
+"""
+
+
+def test_products_on_every_device_of_a_process(L, tmp_path):
+    """The shared-memory limit belongs to the device: each device's first call raises it, and no later one again."""
+    import os
+    import subprocess
+    import sys
+
+    from gemm_q1_q8_gb300 import build
+    so, here = str(tmp_path / "libfake.so"), os.path.dirname(os.path.abspath(__file__))
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc()))), "include")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-I", include, "-o", so, os.path.join(here, "fake_cudart.c")], check=True)
+    r = subprocess.run([sys.executable, "-c", ON_DEVICES, so, build.LIB], env=dict(os.environ, LD_PRELOAD=so), capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_workspaces_hold_what_calls_take(L):
+    """The size for a call's sizes and type serves both products, whatever their outputs: at least the activations' parts where tokens are many."""
+    for rows, n in ((64, 256), (2560, 2560), (14336, 4096)):
+        sizes = [L.gq_q1_q8_linear_workspace_bytes(rows, n, m, t) for t in (0, 1, 2) for m in (1, 40, 500)]
+        assert all(s > 0 and s % 16 == 0 for s in sizes)
+        assert L.gq_q1_q8_linear_workspace_bytes(rows, n, 500, 0) >= 2 * 500 * n * 2 + 500 * 4
+        assert L.gq_q1_q8_linear_workspace_bytes(rows, n, 500, 2) >= L.gq_q1_q8_linear_workspace_bytes(rows, n, 500, 0)
