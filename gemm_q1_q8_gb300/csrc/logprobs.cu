@@ -2,13 +2,15 @@
 //
 //   p = softmax(scale * x);  in powers of two, c = scale * log2(e), t = c (x - max x), s = sum 2^t:
 //   logprob = (t[token] - log2 s) ln 2,  H = (log2 s - (sum 2^t t) / s) ln 2.
-// A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps a running maximum and the two sums a
-// thread (rescaled where a step of loads raises the maximum).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
+// A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps the largest and the two sums a
+// thread (relative to one of its logits, exchanged where another is far above it).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
 // k-th largest logit from below, and a search over the bits of an order-preserving key finds it by 16 block-wide counts.  Only the threads whose maximum
 // reaches the bound (about k) have their logits read once more, from L2, by a warp together.  Equal values go by
 // the lower index: where too many share the bound (masked rows), they are taken in the order of their index.
-// Parts are joined by a second kernel in their order.  Bound by HBM for many rows, by two launches and the
+// Parts are joined in their order: within a cluster, or by a second kernel.  Bound by HBM for many rows, by round trips and the
 // searches' barriers for one.
+#include <algorithm>
+
 #include "layer_ops.cuh"
 
 namespace gq {
@@ -17,7 +19,7 @@ GQ_ERROR_ACCESSOR(logprobs)
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kMaxTop = 32, kMaxPart = 65536, kMaxSplits = 64;
+constexpr int kMaxTop = 32, kMaxSplits = 64;
 constexpr int kFound = 2048;                      // candidates
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
@@ -160,12 +162,85 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, con
 __host__ __device__ __forceinline__ float4* part_sums(void* w) { return static_cast<float4*>(w); }
 __device__ __forceinline__ uint64_t* part_best(void* w, size_t parts) { return reinterpret_cast<uint64_t*>(static_cast<float4*>(w) + parts); }
 
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
+// A row's parts: their sums in their order, and the best of the parts' best.  By a whole block; sums_of(i) and best_of(i) give part i's sums and the
+// i-th of all parts' entries.
+template <typename T, int kThreads, int kEntries, typename S, typename B>
+__device__ __forceinline__ void join_row(const LogprobArgs& a, size_t row, int splits, float c, uint64_t* found, int* count, S sums_of, B best_of) {
+    constexpr int PER = (kEntries + kThreads - 1) / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, k = a.top;
+    float most = kLowest;
+    for (int i = lane; i < splits; i += 32) most = max_nan(most, sums_of(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const bool far = is_far(most, c);
+    Sums t = {most, 0.f, 0.f};
+    for (int i = lane; i < splits; i += 32) {
+        const float4 p = sums_of(i);
+        // a near part's terms are relative to its rounded r
+        const float d = max_nan(power(p.x, most, c, far) - (is_far(p.x, c) ? 0.f : fmaf(c, p.x, -(c * p.x))), -1e4f), f = exp2_fast(d);
+        t.u += fmaf(p.y, d, p.z) * f;
+        t.s += p.y * f;
+    }
+    t = of_lanes<32>(t, c, far);
+    if (tid == 0) {
+        finish_row<T>(a, row, t, c);
+        *count = 0;
+    }
+    if (k == 0) return;
+    uint64_t mine[PER], top = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        mine[i] = tid + i * kThreads < splits * k ? best_of(tid + i * kThreads) : 0;
+        top = max(top, mine[i]);
+    }
+    // as for a part's threads, over entries, which are all different: with all their bits, k threads reach the bound
+    uint64_t bound = 0;
+    int reach = kThreads;
+    for (int b = 63; b >= 0; --b) {
+        if (b == 47 && reach <= 2 * k + 16) break;
+        const uint64_t try_ = bound | 1ull << b;
+        const int q = __syncthreads_count(top >= try_);
+        if (q >= k) {
+            bound = try_;
+            reach = q;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (mine[i] && mine[i] >= bound) found[atomicAdd(count, 1)] = mine[i];
+    __syncthreads();
+    const int have = *count;
+    for (int i = tid; i < have; i += kThreads) {
+        const uint64_t e = found[i];
+        int rank = 0;
+        for (int j = 0; j < have; ++j) rank += found[j] > e;
+        if (rank < k) {
+            a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
+            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
+        }
+    }
+}
+
+// Shared memory of another block of the cluster
+__device__ __forceinline__ uint32_t peer(const void* p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CLUSTER > 1: so many blocks, the parts of a row, are a cluster, whose first joins them
+template <typename T, int kThreads, int CLUSTER>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ? 2 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
     constexpr int W = Vec<T>::W, UN = kThreads == 128 ? 3 : 2;
     __shared__ uint64_t found[kFound];
     __shared__ Sums warp_sums[kThreads / 32];
     __shared__ int count, warp_counts[kThreads / 32];
+    __shared__ float4 own_sums;                                            // a cluster's part
+    __shared__ uint64_t own_best[kMaxTop];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned row32 = splits == 1 ? blockIdx.x : blockIdx.x / splits;
     const size_t row = row32;
@@ -256,10 +331,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 3) logprobs_k
     }
     const uint32_t mine = key_of(top);
     if (tid == 0) {
-        if (splits == 1) finish_row<T>(a, row, t, c);
+        if (CLUSTER > 1) own_sums = make_float4(t.m, t.s, t.u, 0.f);
+        else if (splits == 1) finish_row<T>(a, row, t, c);
         else part_sums(a.workspace)[blockIdx.x] = make_float4(t.m, t.s, t.u, 0.f);
     }
-    if (k == 0) return;
+    auto join = [&] {
+        if (CLUSTER == 1) return;
+        cluster_sync();
+        if (split == 0)
+            join_row<T, kThreads, CLUSTER * kMaxTop>(a, row, CLUSTER, c, found, &count, [&](int i) {
+                float4 v;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer(&own_sums, i)));
+                return v;
+            }, [&](int i) {
+                uint64_t v;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(own_best + i % k, i / k)));
+                return v;
+            });
+        cluster_sync();                                                    // a block's shared memory is there until the first has read it
+    };
+    if (k == 0) {
+        join();
+        return;
+    }
 
     // bound: the largest number that k threads' maxima reach, in its upper 16 bits, or exactly
     uint32_t bound = 0;
@@ -375,123 +469,85 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 3) logprobs_k
         int rank = 0;
         for (int j = 0; j < have; ++j) rank += found[j] > e;
         if (rank < k) {
-            if (splits == 1) {
+            if (CLUSTER > 1) own_best[rank] = e;
+            else if (splits == 1) {
                 a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
                 a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
             } else part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + rank] = e;
         }
     }
     // a part of fewer logits
-    if (splits > 1 && tid >= have && tid < k) part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + tid] = 0;
+    if (splits > 1 && tid >= have && tid < k) {
+        if (CLUSTER > 1) own_best[tid] = 0;
+        else part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + tid] = 0;
+    }
+    join();
 }
 
-// One block a row: its parts' sums in their order, and the best of the parts' best.
+// One block a row, where its parts went through the workspace.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const LogprobArgs a, int splits) {
-    constexpr int PER = kMaxSplits * kMaxTop / kJoinThreads;
     __shared__ uint64_t found[kMaxSplits * kMaxTop];
     __shared__ int count;
-    const int tid = threadIdx.x, lane = tid & 31;
     const size_t row = blockIdx.x, parts = static_cast<size_t>(gridDim.x) * splits;
-    const int k = a.top;
-    const float c = a.scale * kLog2e;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float4* sums = part_sums(a.workspace) + row * splits;
-    float most = kLowest;
-    for (int i = lane; i < splits; i += 32) most = max_nan(most, sums[i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const bool far = is_far(most, c);
-    Sums t = {most, 0.f, 0.f};
-    for (int i = lane; i < splits; i += 32) {
-        const float4 p = sums[i];
-        // a near part's terms are relative to its rounded r
-        const float d = max_nan(power(p.x, most, c, far) - (is_far(p.x, c) ? 0.f : fmaf(c, p.x, -(c * p.x))), -1e4f), f = exp2_fast(d);
-        t.u += fmaf(p.y, d, p.z) * f;
-        t.s += p.y * f;
-    }
-    t = of_lanes<32>(t, c, far);
-    if (tid == 0) {
-        finish_row<T>(a, row, t, c);
-        count = 0;
-    }
-    if (k == 0) return;
-    const uint64_t* best = part_best(a.workspace, parts) + row * splits * k;
-    uint64_t mine[PER], top = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        mine[i] = tid + i * kJoinThreads < splits * k ? best[tid + i * kJoinThreads] : 0;
-        top = max(top, mine[i]);
-    }
-    // as above, over entries, which are all different: with all their bits, k threads reach the bound
-    uint64_t bound = 0;
-    int reach = kJoinThreads;
-    for (int b = 63; b >= 0; --b) {
-        if (b == 47 && reach <= 2 * k + 16) break;
-        const uint64_t try_ = bound | 1ull << b;
-        const int q = __syncthreads_count(top >= try_);
-        if (q >= k) {
-            bound = try_;
-            reach = q;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (mine[i] && mine[i] >= bound) found[atomicAdd(&count, 1)] = mine[i];
-    __syncthreads();
-    const int have = count;
-    for (int i = tid; i < have; i += kJoinThreads) {
-        const uint64_t e = found[i];
-        int rank = 0;
-        for (int j = 0; j < have; ++j) rank += found[j] > e;
-        if (rank < k) {
-            a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
-            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
-        }
-    }
+    const uint64_t* best = part_best(a.workspace, parts) + row * splits * a.top;
+    join_row<T, kJoinThreads, kMaxSplits * kMaxTop>(a, row, splits, a.scale * kLog2e, found, &count, [&](int i) { return sums[i]; },
+                                                    [&](int i) { return best[i]; });
 }
 
-// Parts of a row: enough for three blocks an SM, of at least 2048 logits each where they need not be smaller than kMaxPart
-int splits_of(int m, int vocab) {
-    const int least = (vocab + kMaxPart - 1) / kMaxPart, want = m < 3 * 152 ? 3 * 152 / m : 1;
-    const int most = vocab / 2048 > 1 ? vocab / 2048 : 1;
-    const int s = want < most ? want : most;
-    return s < least ? least : s > kMaxSplits ? kMaxSplits : s;
+// Parts of a row, each a block: up to two blocks an SM, of at least 2048 logits.  Up to eight are a cluster and joined there (one launch instead of two: one row of
+// 49152 called from Python 22.7 -> 18.8 us); more, through the workspace, where eight would have long ways of their own on a GPU that is mostly idle.
+struct Parts { int splits; bool cluster; };
+Parts parts_of(int m, int vocab) {
+    int n = 8;
+    while (n > 1 && (m > 2 * 152 / n || vocab / n < 2048)) n /= 2;
+    if (n < 8 || vocab <= 8 * 32768 || m > 9) return {n, n > 1};
+    return {std::min(kMaxSplits, std::min(3 * 152 / m, vocab / 16384)), false};
 }
 
 template <typename K, typename... A>
-cudaError_t launch(K kernel, unsigned grid, int threads, cudaStream_t s, A... args) {
+cudaError_t launch(K kernel, unsigned grid, int threads, int cluster, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename T>
 cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
-    const int splits = splits_of(a.m, a.vocab), part = (a.vocab + splits - 1) / splits;
-    const unsigned blocks = static_cast<unsigned>(a.m) * splits;
+    const Parts p = parts_of(a.m, a.vocab);
+    const int part = (a.vocab + p.splits - 1) / p.splits;
+    const unsigned blocks = static_cast<unsigned>(a.m) * p.splits;
+    if (p.cluster) {
+        if (p.splits == 8) return launch(logprobs_kernel<T, 512, 8>, blocks, 512, 8, s, a, 8, part);
+        if (p.splits == 4) return launch(logprobs_kernel<T, 512, 4>, blocks, 512, 4, s, a, 4, part);
+        return launch(logprobs_kernel<T, 512, 2>, blocks, 512, 2, s, a, 2, part);
+    }
     // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us); few: the most
     // loads in flight for each.
-    const cudaError_t e = blocks >= 152 * 8 ? launch(logprobs_kernel<T, 128>, blocks, 128, s, a, splits, part)
-                                            : launch(logprobs_kernel<T, 512>, blocks, 512, s, a, splits, part);
-    if (e != cudaSuccess || splits == 1) return e;
-    return launch(logprobs_join_kernel<T>, static_cast<unsigned>(a.m), kJoinThreads, s, a, splits);
+    const cudaError_t e = blocks >= 152 * 8 ? launch(logprobs_kernel<T, 128, 1>, blocks, 128, 1, s, a, p.splits, part)
+                                            : launch(logprobs_kernel<T, 512, 1>, blocks, 512, 1, s, a, p.splits, part);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch(logprobs_join_kernel<T>, static_cast<unsigned>(a.m), kJoinThreads, 1, s, a, p.splits);
 }
 
 }  // namespace
 
 size_t logprobs_workspace_bytes(int m, int vocab, int top) {
-    const size_t splits = splits_of(m, vocab);
-    return splits == 1 ? 16 : static_cast<size_t>(m) * splits * (16 + 8 * static_cast<size_t>(top));
+    const Parts p = parts_of(m, vocab);
+    return p.splits == 1 || p.cluster ? 16 : static_cast<size_t>(m) * p.splits * (16 + 8 * static_cast<size_t>(top));
 }
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int type, cudaStream_t s) {

@@ -192,6 +192,7 @@ cudaError_t norm_type(const NormArgs& a, int m, cudaStream_t s) {
 // --------------------------------------------------------------------------------------------
 // The norm after a block, its gate, the residual's addition and the norm before the next block:
 //   n = y * rstd(y) * post (or y);  h = residual_scale * x + block_scale * (gate * n);  z = h * rstd(h) * w
+// (formed as h = fma(residual_scale, x, y * (block_scale * rstd) * post * gate), a rounding a step).
 // One pass as above with two sums a row: y and then h stay in registers.  Bytes: y, x and the gate once, h and z once.
 // --------------------------------------------------------------------------------------------
 struct BlockNormArgs {
@@ -260,24 +261,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_ke
     if (gr)
 #pragma unroll
         for (int c = 0; c < NV; ++c) g[c].load(gr, 4 * (c * nt + tid), k);
-    float rstd = 1.f;
+    float factor = b.block_scale;                                          // and the first norm's
     if (b.post) {
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) s = squares(v[c], s);
         if (VEC < 2) for (int c = NV; c < chunks; ++c) s = squares_again(load_row4<T, VEC>(yr, 4 * (c * nt + tid), k), s);
         s = row_sum(s, part[0], tid, nt);
-        rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
+        factor *= __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
     }
     // h of four values
     auto join = [&](int i, float4 y, float4 x, float4 g) {
+        y = make_float4(y.x * factor, y.y * factor, y.z * factor, y.w * factor);
         if (b.post) {
             const float4 w = load_row4<float, VEC>(b.post, i, k);
-            y = make_float4(y.x * rstd * w.x, y.y * rstd * w.y, y.z * rstd * w.z, y.w * rstd * w.w);
+            y = make_float4(y.x * w.x, y.y * w.y, y.z * w.z, y.w * w.w);
         }
         if (gr) y = make_float4(g.x * y.x, g.y * y.y, g.z * y.z, g.w * y.w);
-        const float p = b.residual_scale, q = b.block_scale;
-        return make_float4(p * x.x + q * y.x, p * x.y + q * y.y, p * x.z + q * y.z, p * x.w + q * y.w);
+        const float p = b.residual_scale;
+        return make_float4(fmaf(p, x.x, y.x), fmaf(p, x.y, y.y), fmaf(p, x.z, y.z), fmaf(p, x.w, y.w));
     };
     auto again = [&](int i) {
         return join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k), gr ? load_row4<T, VEC>(gr, i, k) : make_float4(0.f, 0.f, 0.f, 0.f));
@@ -347,16 +349,31 @@ template <typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* act, long long blocks, T* out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the loads of four steps before their stores, which the compiler would keep in order (8192 rows of 4096 to f16: 22.4 -> 17.1 us)
+    constexpr int U = 4;
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < blocks * 8; i += step) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(act + (i >> 3) * 34);
-        const int sub = static_cast<int>(i & 7);
-        const float d = f16_to_f32(p[0]);
-        const uint32_t lo = p[1 + 2 * sub], hi = p[2 + 2 * sub];
-        store4(out + i * 4, make_float4(d * static_cast<float>(static_cast<int8_t>(lo & 0xff)),
-                                        d * static_cast<float>(static_cast<int8_t>(lo >> 8)),
-                                        d * static_cast<float>(static_cast<int8_t>(hi & 0xff)),
-                                        d * static_cast<float>(static_cast<int8_t>(hi >> 8))));
+    for (long long i0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i0 < blocks * 8; i0 += U * step) {
+        uint32_t d16[U], lo[U], hi[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step;
+            if (i >= blocks * 8) break;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(act + (i >> 3) * 34);
+            const int sub = static_cast<int>(i & 7);
+            d16[u] = p[0];
+            lo[u] = p[1 + 2 * sub];
+            hi[u] = p[2 + 2 * sub];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = i0 + u * step;
+            if (i >= blocks * 8) break;
+            const float d = f16_to_f32(d16[u]);
+            store4(out + i * 4, make_float4(d * static_cast<float>(static_cast<int8_t>(lo[u] & 0xff)),
+                                            d * static_cast<float>(static_cast<int8_t>(lo[u] >> 8)),
+                                            d * static_cast<float>(static_cast<int8_t>(hi[u] & 0xff)),
+                                            d * static_cast<float>(static_cast<int8_t>(hi[u] >> 8))));
+        }
     }
 }
 

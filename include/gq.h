@@ -415,7 +415,7 @@ int gq_rmsnorm(const void* x_device, long long x_stride, const void* residual_de
 /* The norm after a block, the block's gate, the residual stream's addition and the norm before the next block, in one pass:
  *   n = y * (1 / sqrt(sum y^2 / k + eps)) * post_weight   (post_weight NULL: n = y),
  *   h = residual_scale * x + block_scale * (gate * n)     (gate NULL: 1),
- *   z = h * (1 / sqrt(sum h^2 / k + eps)) * weight,        each step rounded to f32.
+ *   z = h * (1 / sqrt(sum h^2 / k + eps)) * weight,        in f32, n's factors in another order (block_scale with the root first).
  *   block_device [m, k] of `type`: y, what the block gave; x_device [m, k]: the stream; rows block_stride and x_stride elements apart;
  *   gate_device NULL or [m, k] of `type`, rows gate_stride apart, 0: one row for all; post_weight_device (or NULL) and weight_device k f32.
  *   Outputs as gq_rmsnorm's: sum_device receives h (it may be x_device or block_device itself if those rows are contiguous), the others z.

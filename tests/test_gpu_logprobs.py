@@ -77,17 +77,17 @@ def test_temperatures(gq, scale):
     check(gq, normal(2, 400, 3001, 0.5), 4, scale=scale)
 
 
-@pytest.mark.parametrize("m", [2, 460])
+@pytest.mark.parametrize("m,vocab", [(2, 9001), (460, 9001), (1, 300001)])
 @pytest.mark.parametrize("first,size", [(7e5, 3.0), (-7e5, 3.0), (7.3e5, 30.0), (-7.26842e5, 5.0), (1e9, 1e3), (-1e9, 1e3), (0.0, 1e30), (0.0, 1e37), (3.3e38, 1e32),
                                         (-3.39e38, 1e31)])
-def test_logits_far_from_zero(gq, m, first, size):
+def test_logits_far_from_zero(gq, m, vocab, first, size):
     """Whatever their size, up to the type's; 7.268e5 is where the form of the sums changes, in parts of a row before others."""
-    x = (first + normal(4, m, 9001, size).double()).clamp(-3.4e38, 3.4e38).float()
-    x[:, :4500] -= 6 * size if abs(first) > 1e5 and size < 1e3 else 0
+    x = (first + normal(4, m, vocab, size).double()).clamp(-3.4e38, 3.4e38).float()
+    x[:, :vocab // 2] -= 6 * size if abs(first) > 1e5 and size < 1e3 else 0
     check(gq, x, 6)
 
 
-@pytest.mark.parametrize("m,vocab,threads", [(400, 65536, 512), (1300, 20000, 128)])
+@pytest.mark.parametrize("m,vocab,threads", [(400, 65536, 512), (1300, 20000, 128), (2, 500000, 512)])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_more_candidates_than_fit(gq, m, vocab, threads, kind):
     """Thousands of a row's logits with fewer threads than alternatives are asked for, above the others' maxima."""
@@ -119,7 +119,7 @@ def test_ties_go_by_index(gq, m, top):
     check(gq, near, top)
 
 
-@pytest.mark.parametrize("m,vocab", [(1, 49152), (3, 999), (330, 5001), (1300, 3001)])
+@pytest.mark.parametrize("m,vocab", [(1, 49152), (3, 999), (330, 5001), (1300, 3001), (2, 300001)])
 @pytest.mark.parametrize("left", [0, 1, 3, 40])
 def test_masked_rows(gq, m, vocab, left):
     """-inf, or the type's lowest value, but for `left` logits of a row."""
