@@ -279,10 +279,10 @@ static bool logprob_shape(int m, int vocab, int top) {
     return m >= 1 && m <= 1 << 24 && vocab >= 1 && vocab <= 1 << 20 && top >= 0 && top <= 32 && top <= vocab;
 }
 
-constexpr int kMaxCols = 1 << 20;
+constexpr int kMaxCols = 1 << 20, kMaxRows = 1 << 30;
 
 static int linear_call(const gq::LinearArgs& a, bool pair, gq_stream_t stream) {
-    if (a.rows < 1 || a.n < 128 || a.n % 128 != 0 || a.n > gq::kMaxN || a.cols < 1 || a.cols > kMaxCols || (a.blocks && a.rows % 32 != 0) ||
+    if (a.rows < 1 || a.rows > kMaxRows || a.n < 128 || a.n % 128 != 0 || a.n > gq::kMaxN || a.cols < 1 || a.cols > kMaxCols || (a.blocks && a.rows % 32 != 0) ||
         (a.y && a.y_stride < a.rows) || (a.residual && a.residual_stride < a.rows))
         return GQ_EINVAL_SHAPE;
     const size_t b = type_bytes(a.type);
@@ -340,7 +340,7 @@ size_t gq_logprobs_workspace_bytes(int m, int vocab, int top) {
 
 int gq_logprobs(const void* logits, long long stride, int type, int m, int vocab, float scale, const int64_t* tokens, float* logprob,
                 float* entropy, int top, int64_t* top_ids, float* top_logprobs, void* workspace, gq_stream_t stream) {
-    if (!logprob_shape(m, vocab, top) || stride < vocab || !std::isfinite(scale) || !(scale > 0.0f)) return GQ_EINVAL_SHAPE;
+    if (!logprob_shape(m, vocab, top) || stride < vocab || !(scale > 0.0f && scale <= 1e30f)) return GQ_EINVAL_SHAPE;
     const size_t b = type_bytes(type);
     if (!b) return GQ_EUNSUPPORTED;
     if (!logits || !tokens != !logprob || (!logprob && !entropy && top == 0) || (top > 0 && (!top_ids || !top_logprobs)) || !workspace)
@@ -353,7 +353,7 @@ int gq_logprobs(const void* logits, long long stride, int type, int m, int vocab
 }
 
 size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type) {
-    if (rows < 1 || n < 128 || n % 128 != 0 || n > gq::kMaxN || cols < 1 || cols > kMaxCols || !type_bytes(type)) return 0;
+    if (rows < 1 || rows > kMaxRows || n < 128 || n % 128 != 0 || n > gq::kMaxN || cols < 1 || cols > kMaxCols || !type_bytes(type)) return 0;
     return gq::linear_workspace_bytes(rows, n, cols, type);
 }
 

@@ -449,12 +449,13 @@ enum gq_function {
  *   the rule stated at gq_quantize_q8_0 (a block with a NaN has a NaN scale).
  *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's sizes and type (both calls take the same), 16-byte aligned,
  *   overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
- * Precision: activations are exact where they are not below 2^-20 of their vector's largest (there: off by at most 2^-39 of it); where
- *   the only output is bf16 they are rounded to 12 bits.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 128
- *   weights, of 512 for bf16), everything after them f32, rounded once.  The same inputs give the same bits.  A vector with a scale that is not finite gives no numbers,
- *   and leaves the others as they are.
- * Errors: GQ_EINVAL_SHAPE if rows < 1, n < 128, n % 128 != 0, n > 2^20, cols < 1, cols > 2^20, a stride < rows or blocks_device with
- *         rows % 32 != 0; GQ_EUNSUPPORTED for another type or function; GQ_EINVAL_PTR for NULL or misaligned pointers (packed weights
+ * Precision: up to 32 tokens a kernel may be taken whose 32-block sums are exact.  The other, for more, holds activations in f16 parts: exact
+ *   where they are not below 2^-20 of 128 times their vector's largest scale (there: off by at most 2^-39 of it); rounded to 12 bits where the only
+ *   output is bf16.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 256 weights, of 65536 for bf16), everything after them
+ *   f32, rounded once.  The same inputs give the same bits.  A vector with a scale that is not finite gives no numbers, and leaves the others as
+ *   they are.
+ * Errors: GQ_EINVAL_SHAPE if rows < 1, rows > 2^30, n < 128, n % 128 != 0, n > 2^20, cols < 1, cols > 2^20, a stride < rows or
+ *         blocks_device with rows % 32 != 0; GQ_EUNSUPPORTED for another type or function; GQ_EINVAL_PTR for NULL or misaligned pointers (packed weights
  *         and workspace 16 bytes, others their elements), no output, or y_device = residual_device with another stride; GQ_ECUDA. */
 size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type);   /* 0 for invalid sizes */
 int q1_q8_linear(const void* packed_w_device, const void* act_device, int rows, int n, int cols, const float* bias_device,
@@ -474,8 +475,8 @@ int q1_q8_glu(const void* packed_gate_device, const void* packed_up_device, cons
  *   entropy 0.  A row with NaN or +inf gives NaN (its alternatives in order, NaN first).
  *   workspace_device: gq_logprobs_workspace_bytes(m, vocab, top) bytes, 16-byte aligned, overwritten; calls that share it must not overlap
  *   on the GPU.  The same inputs give the same bits.
- * Errors: GQ_EINVAL_SHAPE unless 1 <= m <= 2^24, 1 <= vocab <= 2^20, 0 <= top <= min(32, vocab), stride >= vocab, scale positive and
- *         finite; GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR for NULL or misaligned pointers or no output; GQ_ECUDA. */
+ * Errors: GQ_EINVAL_SHAPE unless 1 <= m <= 2^24, 1 <= vocab <= 2^20, 0 <= top <= min(32, vocab), stride >= vocab, 0 < scale <=
+ *         1e30; GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR for NULL or misaligned pointers or no output; GQ_ECUDA. */
 size_t gq_logprobs_workspace_bytes(int m, int vocab, int top);   /* 0 for invalid sizes */
 int gq_logprobs(const void* logits_device, long long stride, int type, int m, int vocab, float scale, const int64_t* tokens_device,
                 float* logprob_device, float* entropy_device, int top, int64_t* top_ids_device, float* top_logprobs_device,

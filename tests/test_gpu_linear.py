@@ -1,8 +1,8 @@
 """Q1_0 products with an epilogue (q1_q8_linear, q1_q8_glu) against the formula in 64 bits.
 
 Bounds (u = 2^-24, A = sum |d0 d1 q| of a result): products are exact and a part of an activation is lost only below 2^-39 of its vector's
-largest.  A tensor-core step is taken to be off by two units (its truncated sum); a chain has at most 16 steps before it is added
-in f32 (64 where the result is bf16), and there are at most n / 128 + 8 such additions.  A bf16 result takes activations rounded to 2^-12."""
+largest.  A tensor-core step is taken to be off by two units (its truncated sum); a chain has at most 32 steps before it is added
+in f32 (n / 16 where the result is bf16), and there are at most n / 32 + 8 such additions.  A bf16 result takes activations rounded to 2^-12."""
 import math
 
 import numpy as np
@@ -54,9 +54,9 @@ def activations(seed, m, n, wide=False):
 def product(x, w, bias, one_part):
     """(z, the bound of its error)."""
     z, a = x @ w.T, x.abs() @ w.abs().T
-    nb = x.shape[1] // 128
-    chain = 64 if one_part else 16
-    tol = (2 * chain + nb + 8) * U * a + 2.0 ** -39 * x.abs().amax(-1, keepdim=True) * w.abs().sum(-1)
+    n = x.shape[1]
+    chain = n // 16 if one_part else 32
+    tol = (2 * chain + n // 32 + 8) * U * a + 2.0 ** -39 * x.abs().amax(-1, keepdim=True) * w.abs().sum(-1)
     if one_part:
         tol = tol + 2.0 ** -12 * a
     if bias is not None:
@@ -158,6 +158,21 @@ def test_scales_of_any_size(gq, m):
 
 
 @pytest.mark.parametrize("m", [3, 150])
+def test_weights_of_small_scales(gq, m):
+    """Scales that are f16 subnormals count in full."""
+    rows, n = 130, 640
+    rng = np.random.default_rng(1)
+    raw = rng.integers(0, 256, (rows, n // 128, 18), dtype=np.uint8)
+    d = rng.integers(1, 40, (rows, n // 128, 1)).astype(np.uint16)          # multiples of 2^-24
+    raw[..., :2] = d.view(np.uint8)
+    bits = np.unpackbits(raw[..., 2:], axis=-1, bitorder="little").astype(np.float64)
+    wv = torch.from_numpy(((2 * bits - 1) * d * 2.0 ** -24).reshape(rows, n)).cuda()
+    w = gq.q1_0_pack(torch.from_numpy(raw.reshape(-1)).cuda(), rows, n)
+    act, x = activations(2, m, n)
+    check(gq.q1_q8_linear(w, act, rows, n, m), *product(x, wv, None, False), "f32")
+
+
+@pytest.mark.parametrize("m", [3, 150])
 def test_a_vector_that_is_not_finite(gq, m):
     rows, n = 64, 512
     w, _ = weights(gq, 7, rows, n)
@@ -192,6 +207,18 @@ def test_strides_and_in_place(gq, m, kind):
     wb, _ = weights(gq, 11, 128, n)
     got = gq.q1_q8_linear(wb, act, 128, n, m, q8_0=True, out=room[:-64])
     assert torch.equal(got, gq.q1_q8_linear(wb, act, 128, n, m, q8_0=True)) and torch.all(room[-64:] == 9)
+
+
+@pytest.mark.parametrize("m,rows,n", [(1, 64, 512), (7, 300, 1280), (20, 96, 256), (50, 640, 2560)])
+def test_activations_of_any_alignment(gq, m, rows, n):
+    w, _ = weights(gq, 3, rows, n)
+    act, _ = activations(4, m, n)
+    want = gq.q1_q8_linear(w, act, rows, n, m)
+    for shift in (2, 4, 6):
+        room = torch.empty(act.numel() + 8, dtype=torch.uint8, device="cuda")
+        moved = room[shift:shift + act.numel()]
+        moved.copy_(act)
+        assert torch.equal(gq.q1_q8_linear(w, moved, rows, n, m), want)
 
 
 def test_both_outputs_through_the_c_abi(gq):

@@ -28,7 +28,7 @@ def glu(L, **k):
     return L.q1_q8_glu(*a.values(), N)
 
 
-SIZES = [(dict(rows=0), 1), (dict(n=0), 1), (dict(n=200), 1), (dict(n=(1 << 20) + 128), 1), (dict(cols=0), 1), (dict(cols=(1 << 20) + 1), 1),
+SIZES = [(dict(rows=0), 1), (dict(rows=(1 << 30) + 1, ys=1 << 31, blocks=N), 1), (dict(n=0), 1), (dict(n=200), 1), (dict(n=(1 << 20) + 128), 1), (dict(cols=0), 1), (dict(cols=(1 << 20) + 1), 1),
          (dict(ys=63), 1), (dict(rows=33, blocks=X), 1), (dict(type=3), 3), (dict(fn=-1), 3), (dict(fn=6), 3), (dict(act=N), 2), (dict(act=O1), 2),
          (dict(y=N, blocks=N), 2), (dict(y=O2), 2), (dict(y=O1, type=2), 2), (dict(blocks=O1), 2), (dict(work=N), 2), (dict(work=O8), 2)]
 
@@ -67,7 +67,7 @@ def logprobs(L, **k):
 
 @pytest.mark.parametrize("change,expect", [
     (dict(m=0), 1), (dict(m=(1 << 24) + 1), 1), (dict(v=0), 1), (dict(v=(1 << 20) + 1, s=1 << 21), 1), (dict(s=99), 1), (dict(top=-1), 1), (dict(top=33), 1),
-    (dict(v=4), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(type=4), 3),
+    (dict(v=4), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=1.1e30), 1), (dict(type=4), 3),
     (dict(x=N), 2), (dict(x=O2), 2), (dict(x=O1, type=1), 2), (dict(tok=N), 2), (dict(lp=N), 2), (dict(tok=N, lp=N, h=N, top=0), 2),
     (dict(ids=N), 2), (dict(best=N), 2), (dict(tok=ctypes.c_void_p(0x1004)), 2), (dict(ids=ctypes.c_void_p(0x1004)), 2), (dict(best=O2), 2),
     (dict(lp=O2), 2), (dict(h=O2), 2), (dict(work=N), 2), (dict(work=O8), 2)])
