@@ -3,11 +3,11 @@
 //   z[c, r] = sum_b d0[r, b] * sum_k d1[c, 4b + k] * sum_t (+-1) q   (+ bias[r])
 //   linear:  y = act(z) (+ residual[c, r]);      pair: y = act(z_gate) * z_up
 //
-// Both kernels take +-d0 as f16 matrix operands, made from the sign bits by two logic operations a pair, and the activations as
-// pv = d1 * q * 2^-e, e one power of two a token: pv has at most 18 significant bits, so two f16 parts hold it exactly while it is
-// not below 2^-20 of the token's largest (then it is off by at most 2^-39 of that).  f32, f16 and Q8_0 results take both
-// parts; a bf16 result (8 bits) takes one, off by 2^-12 of each value.  Products are exact in f32, sums are f32; the tensor
-// cores truncate the sum that they add to, so it goes to registers every few blocks of 128 (a chain of n steps costs n / 3 * 2^-23).
+// Both kernels take +-d0 as f16 matrix operands, made from the sign bits by two logic operations a pair.  The one for few tokens takes the codes
+// as they are and multiplies the sums of 32 by d1.  The one for many takes pv = d1 * q * 2^-e, e one power of two a token: pv has at
+// most 18 significant bits, so two f16 parts hold it exactly while it is not below 2^-20 of 128 times the token's largest scale (then it is off
+// by at most 2^-39 of that).  f32, f16 and Q8_0 results take both parts; a bf16 result (8 bits) takes one, off by 2^-12 of each value.
+// Products are exact in f32, sums are f32; the tensor cores truncate the sum that they add to, so it goes to registers every 128 of n.
 #pragma once
 
 #include <algorithm>

@@ -7,9 +7,11 @@
 //   warp 2: TMA copies of the stage's parts (128-byte swizzle)
 //   warps 4-11: weights.  A thread has a row of one matrix; two words of signs become 32 registers of +-d0 pairs by a shift and a logic
 //              operation each, and go to the stage's slot of tensor memory (the operand A), so shared memory is read for B alone
-//   warps 12-19: sums.  A round is 128 of n (512 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so it
-//              leaves tensor memory after each round and is added in registers; one matrix is drained while the other's MMAs run.  Behind the
-//              last round the function, the residual, the conversion and the stores, while the next tile's MMAs start.
+//   warps 12-19: sums.  A round is 128 of n (65536 where one part is taken: bf16 results): the tensor cores truncate the sum that they add to, so
+//              it leaves tensor memory after each round and is added in registers; the rounds of the two matrices are staggered, so one
+//              is drained while the other's MMAs run.  The small parts of a round come first, while its sum is small: 1.0e-7 of the
+//              result over 6912 (large and small by stages: 1.9e-7, in rounds of 256 3.1e-7; f32 products by cuBLAS 6.8e-7).  Behind the last
+//              round the function, the residual, the conversion and the stores, while the next tile's MMAs start.
 // Tensor memory: 2 x 128 columns of sums, 4 stages x 64 columns of weights.  Where the tiles are fewer than the SMs, n is cut into equal
 // shares, whose sums a third kernel adds in order before the epilogue.
 #include "linear.cuh"
@@ -25,7 +27,7 @@ constexpr int kDCols = 128, kA0 = 2 * kDCols, kACols = BK / 2;            // a s
 constexpr int kTileB = 128 * BK * 2;                                       // a part of up to 128 tokens; a stage has two
 constexpr int kStaged = 2 * 32 * 32 * 4;                                   // of a sums warp: half its columns of both matrices
 constexpr int kWarpA0 = 4, kWarpE0 = 12, kEWarps = 8, kThreads = 640;
-constexpr int kRegs = 96, kRegsSums = 168, kRegsRest = 48;                 // a thread's at launch, of 8 warps, of the other 12
+constexpr int kRegs = 96, kRegsSums = 176, kRegsRest = 40;                 // a thread's at launch, of 8 warps, of the other 12
 static_assert(kA0 + kStages * 2 * kACols <= kTmemCols, "TMEM columns");
 static_assert(kRegsSums * 256 + kRegsRest * 384 <= kRegs * kThreads && kRegs * kThreads <= 65536, "registers");
 
@@ -192,12 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
 #pragma unroll
                     for (int o = 0; o < AT_ONCE / 16; ++o) ld16(at + static_cast<uint32_t>(m * kDCols + c + 16 * o), v[o]);
                     wait_ld();
+                    if (c + AT_ONCE == NC) {                               // read: the next round may begin
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->accempty[m]);
+                    }
 #pragma unroll
                     for (int i = 0; i < AT_ONCE; ++i) sum[c + i] += __uint_as_float(v[i / 16][i % 16]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->accempty[m]);
             };
             // the second matrix's rounds end in the middle of the first one's
             for (int k = half_round; k < w.k1 - w.k0; k += 2 * half_round) {
@@ -279,34 +283,43 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 const Unit w = unit_of<BN>(plan, u, nb);
                 int r = m * half_round;                                    // stages of the round
                 bool first = true;
-                for (int k = w.k0; k < w.k1; ++k, ++g) {
-                    const int s = g % kStages;
-                    const bool last = r == 2 * half_round - 1 || k == w.k1 - 1;
-                    const bool ready = wait_or_abort_sleep(&bars->full[s], (g / kStages) & 1u, abort) &&
-                                       (!first || turn == 0 || wait_or_abort_sleep(&bars->accempty[m], (turn - 1) & 1u, abort));
+                for (int k = w.k0; k < w.k1;) {
+                    // up to two stages of a round, the small parts of both first
+                    const int here = parts == 2 && r < 2 * half_round - 1 && k < w.k1 - 1 ? 2 : 1;
+                    const int s[2] = {static_cast<int>(g % kStages), static_cast<int>((g + 1) % kStages)};
+                    bool ready = wait_or_abort_sleep(&bars->full[s[0]], (g / kStages) & 1u, abort);
+                    if (here == 2) ready = ready && wait_or_abort_sleep(&bars->full[s[1]], ((g + 1) / kStages) & 1u, abort);
+                    ready = ready && (!first || turn == 0 || wait_or_abort_sleep(&bars->accempty[m], (turn - 1) & 1u, abort));
                     if (!__all_sync(0xffffffffu, ready)) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t bdesc = smem_desc(sB + s * 2 * kTileB);
-                    const uint32_t av = tmem + static_cast<uint32_t>(kA0 + (2 * s + m) * kACols);
+                    const bool last = r + here == 2 * half_round || k + here == w.k1;
+                    bool fresh = first;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        if (p == parts) break;
+                    for (int p = 1; p >= 0; --p) {
+                        if (p == 1 && parts == 1) continue;
 #pragma unroll
-                        for (int j = 0; j < BK / 16; ++j)
-                            mma_ts(leader, d, av + static_cast<uint32_t>(j * 8), bdesc + static_cast<uint64_t>((p * kTileB + j * 32) >> 4), kIdesc,
-                                   first && p == 0 && j == 0 ? 0u : 1u);
+                        for (int i = 0; i < 2; ++i) {
+                            if (i == here) break;
+                            const uint64_t bdesc = smem_desc(sB + s[i] * 2 * kTileB);
+                            const uint32_t av = tmem + static_cast<uint32_t>(kA0 + (2 * s[i] + m) * kACols);
+#pragma unroll
+                            for (int j = 0; j < BK / 16; ++j) {
+                                mma_ts(leader, d, av + static_cast<uint32_t>(j * 8), bdesc + static_cast<uint64_t>((p * kTileB + j * 32) >> 4), kIdesc, fresh ? 0u : 1u);
+                                fresh = false;
+                            }
+                            if (p == 0 && leader) tc_commit(&bars->done[s[i]]);
+                        }
                     }
-                    if (leader) {
-                        if (last) tc_commit(&bars->accfull[m]);
-                        tc_commit(&bars->done[s]);
-                    }
+                    if (last && leader) tc_commit(&bars->accfull[m]);
                     __syncwarp();
                     first = last;
-                    r = last ? 0 : r + 1;
+                    r = last ? 0 : r + here;
                     turn += last;
+                    k += here;
+                    g += here;
                 }
             }
             if (leader) tc_commit(&bars->final_);
@@ -346,23 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 const Unit w = unit_of<BN>(plan, u, nb);
                 const uint8_t* src = (m ? a.w[1] : a.w[0]) + static_cast<size_t>(PAIR ? w.row_tile : min(2 * w.row_tile + m, tiles - 1)) * nb * kChunkBytes +
                                      static_cast<size_t>(w.k0 / 2) * kChunkBytes;
-                // blocks loaded three ahead: a block's MMAs take 370 to 2000 cycles, a load up to 1000
-                uint4 bits[3];
-                uint32_t d0[3];
-                auto load = [&](int i) {
-                    bits[i] = *reinterpret_cast<const uint4*>(src + r * 16);
-                    d0[i] = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
+                uint4 bits;
+                uint32_t d0;
+                auto load = [&] {
+                    bits = *reinterpret_cast<const uint4*>(src + r * 16);
+                    d0 = *reinterpret_cast<const uint16_t*>(src + BM * 16 + r * 2);
                     src += kChunkBytes;
                 };
-                int ahead = w.k0;
-#pragma unroll
-                for (int i = 0; i < 3; ++i, ahead += 2)
-                    if (ahead < w.k1) load(i);
-                for (int k = w.k0; k < w.k1 && live; k += 2, ahead += 2) {
-                    const uint32_t words[4] = {bits[0].x, bits[0].y, bits[0].z, bits[0].w}, neg = (d0[0] * 0x00010001u) ^ 0x80008000u;   // a clear bit gives -d0
-                    bits[0] = bits[1], bits[1] = bits[2];
-                    d0[0] = d0[1], d0[1] = d0[2];
-                    if (ahead < w.k1) load(2);
+                load();
+                for (int k = w.k0; k < w.k1 && live; k += 2) {
+                    const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w}, neg = (d0 * 0x00010001u) ^ 0x80008000u;   // a clear bit gives -d0
+                    if (k + 2 < w.k1) load();
 #pragma unroll
                     for (int half = 0; half < 2; ++half, ++g) {
                         const int s = g % kStages;
@@ -529,8 +536,8 @@ Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
                 p.splits = splits;
                 p.units = static_cast<int>(std::min<long long>(units, 0x7fffffff));
                 p.parts = parts;
-                // two parts: 256 of n, 32 steps; one (bf16): 65536
-                p.round = parts == 2 ? 4 : 1024;
+                // two parts: 128 of n, 16 steps; one (bf16): 65536
+                p.round = parts == 2 ? 2 : 1024;
                 p.pad_rows = tiles * BM;
                 best = {bn, p, us};
             }

@@ -451,7 +451,7 @@ enum gq_function {
  *   overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
  * Precision: up to 32 tokens a kernel may be taken whose 32-block sums are exact.  The other, for more, holds activations in f16 parts: exact
  *   where they are not below 2^-20 of 128 times their vector's largest scale (there: off by at most 2^-39 of it); rounded to 12 bits where the only
- *   output is bf16.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 256 weights, of 65536 for bf16), everything after them
+ *   output is bf16.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 128 weights, of 65536 for bf16), everything after them
  *   f32, rounded once.  The same inputs give the same bits.  A vector with a scale that is not finite gives no numbers, and leaves the others as
  *   they are.
  * Errors: GQ_EINVAL_SHAPE if rows < 1, rows > 2^30, n < 128, n % 128 != 0, n > 2^20, cols < 1, cols > 2^20, a stride < rows or

@@ -1,7 +1,7 @@
 """Q1_0 products with an epilogue (q1_q8_linear, q1_q8_glu) against the formula in 64 bits.
 
 Bounds (u = 2^-24, A = sum |d0 d1 q| of a result): products are exact and a part of an activation is lost only below 2^-39 of its vector's
-largest.  A tensor-core step is taken to be off by two units (its truncated sum); a chain has at most 32 steps before it is added
+largest.  A tensor-core step is taken to be off by two units (its truncated sum); a chain has at most 16 steps before it is added
 in f32 (n / 16 where the result is bf16), and there are at most n / 32 + 8 such additions.  A bf16 result takes activations rounded to 2^-12."""
 import math
 
@@ -55,7 +55,7 @@ def product(x, w, bias, one_part):
     """(z, the bound of its error)."""
     z, a = x @ w.T, x.abs() @ w.abs().T
     n = x.shape[1]
-    chain = n // 16 if one_part else 32
+    chain = n // 16 if one_part else 16
     tol = (2 * chain + n // 32 + 8) * U * a + 2.0 ** -39 * x.abs().amax(-1, keepdim=True) * w.abs().sum(-1)
     if one_part:
         tol = tol + 2.0 ** -12 * a
