@@ -598,21 +598,22 @@ def rmsnorm_q8_0(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resid
 
 
 def _rmsnorm_block(block, x, weight, post_weight, eps, gate, block_scale, residual_scale, sum_out, y, act, d, q, op):
-    m, k = x.shape
-    code, dev = _type(x, "x"), x.get_device()
-    xs, bs = _rows(x, code, m, k, "x"), _rows(block, code, m, k, "block")
+    (m, k), dtype, dev = x.shape, x.dtype, x.get_device()
+    xp, xs = _matrix(x, dtype, m, k, dev, "x")
+    bp, bs = _matrix(block, dtype, m, k, dev, "block")
     gs, gp = 0, None
     if gate is not None:
         if not isinstance(gate, torch.Tensor) or gate.dim() not in (1, 2) or (gate.dim() == 2 and gate.shape[0] not in (1, m)):
             raise GQError(f"gate: expected [{k}] or [{m}, {k}]")
         one = gate.dim() == 1 or gate.shape[0] == 1
-        row = _rows(gate.view(1, -1) if gate.dim() == 1 else gate, code, 1 if one else m, k, "gate")
-        gs, gp = 0 if one else row, _same_device(gate, dev, "gate")
+        gp, gs = _matrix(gate.view(1, -1) if gate.dim() == 1 else gate, dtype, 1 if one else m, k, dev, "gate")
+        if one:
+            gs = 0
     wp = _is(weight, torch.float32, k, dev, "weight")
     pp = _is(post_weight, torch.float32, k, dev, "post_weight") if post_weight is not None else None
-    hp = _is(sum_out, x.dtype, m * k, dev, "sum_out") if sum_out is not None else None
-    _launched(x, dev, lib().gq_rmsnorm_block, "gq_rmsnorm_block", _same_device(block, dev, "block"), bs, x.data_ptr(), xs, pp, gp, gs,
-              block_scale, residual_scale, wp, eps, code, m, k, hp, y, act, d, q, op)
+    hp = _is(sum_out, dtype, m * k, dev, "sum_out") if sum_out is not None else None
+    _launched(x, dev, lib().gq_rmsnorm_block, "gq_rmsnorm_block", bp, bs, xp, xs, pp, gp, gs, block_scale, residual_scale, wp, eps,
+              _TYPES[dtype], m, k, hp, y, act, d, q, op)
 
 
 def _is(t, dtype, numel: int, dev: int, name: str) -> int:
@@ -621,6 +622,14 @@ def _is(t, dtype, numel: int, dev: int, name: str) -> int:
         return t.data_ptr()
     _need(t, dtype, numel, name)
     raise GQError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+
+
+def _matrix(t, dtype, m: int, k: int, dev: int, name: str):
+    """Checks a [m, k] tensor of a dtype and the call's device with contiguous rows; its address, and the distance between rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == (m, k):
+        return t.data_ptr(), k
+    stride = _rows(t, _TYPES[dtype], m, k, name)
+    return _same_device(t, dev, name), stride
 
 
 def _launched(t: torch.Tensor, dev: int, fn, name: str, *args):
@@ -724,8 +733,7 @@ def _linear(name, act, rows, n, cols, function, dtype, q8_0, out, workspace):
         blocks = _is(out, torch.uint8, cols * (rows // 32) * 34, dev, "out")
     else:
         out = torch.empty((cols, rows), dtype=dtype, device=act.device) if out is None else out
-        ys = _rows(out, code, cols, rows, "out")
-        y = _same_device(out, dev, "out")
+        y, ys = _matrix(out, dtype, cols, rows, dev, "out")
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=act.device)
     elif not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
@@ -742,8 +750,7 @@ def q1_q8_linear(packed: torch.Tensor, act: torch.Tensor, rows: int, n: int, col
     fn, code, dev, nbytes, out, ap, y, ys, blocks, work = _linear("q1_q8_linear", act, rows, n, cols, activation, dtype, q8_0, out, workspace)
     rs, rp = 0, None
     if residual is not None:
-        rs = _rows(residual, code, cols, rows, "residual")
-        rp = _same_device(residual, dev, "residual")
+        rp, rs = _matrix(residual, dtype, cols, rows, dev, "residual")
     _launched(act, dev, lib().q1_q8_linear, "q1_q8_linear", _is(packed, torch.uint8, nbytes, dev, "packed"), ap, rows, n, cols,
               _is(bias, torch.float32, rows, dev, "bias") if bias is not None else None, fn, rp, rs, code, y, ys, blocks, work)
     return out
@@ -788,7 +795,7 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int 
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise GQError("logits: expected a CUDA tensor [m, vocab]")
     code, dev, (m, vocab) = _type(logits, "logits"), logits.get_device(), logits.shape
-    stride = _rows(logits, code, m, vocab, "logits")
+    xp, stride = _matrix(logits, logits.dtype, m, vocab, dev, "logits")
     need = _logprobs_bytes(m, vocab, top)
     if need == 0 or (tokens is None and not entropy and top == 0):
         raise GQError("logprobs: invalid shape, or nothing asked for")
@@ -807,7 +814,7 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int 
     elif not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
         raise GQError(f"logprobs: expected a workspace of at least {need} bytes")
     wp = _is(workspace, torch.uint8, workspace.numel(), dev, "workspace")
-    _launched(logits, dev, lib().gq_logprobs, "gq_logprobs", logits.data_ptr(), stride, code, m, vocab, scale, tp, _at(lp), _at(h), top,
+    _launched(logits, dev, lib().gq_logprobs, "gq_logprobs", xp, stride, code, m, vocab, scale, tp, _at(lp), _at(h), top,
               _at(ids), _at(best), wp)
     return LogProbs(lp, h, ids, best)
 

@@ -227,6 +227,7 @@ cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
 // 400 x 1024, 2560 x 2560, 2560 x 6912 and 14336 x 8192 and the pairs of 6912 x 2560 and 14336 x 4096, in microseconds.
 bool linear_by_rows(int rows, int n, int cols, bool pair, int parts) {
     if (cols > 32) return false;
+    if (cols <= 4) return true;                                               // at every size that was measured
     const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
     const float waves = static_cast<float>(((rows + kBlockRows - 1) / kBlockRows + 151) / 152);
     const float us = 1.7f + waves * (0.5f + n * 1e-3f * (0.25f + 0.08f * cols + (pair ? 0.7f : 0.25f) * nt));
