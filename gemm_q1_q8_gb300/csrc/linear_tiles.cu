@@ -1,7 +1,7 @@
 // Q1_0 products with an epilogue, many tokens: tcgen05 (kind::f16), weights as +-d0 in tensor memory.
 //
 // A first kernel writes the activations' f16 parts (linear.cuh) once, in the order in which a sign word's bits become pairs.  A tile of the second
-// is two 128-row matrices (gate and up of a pair, or two neighbouring row tiles) by BN tokens, so that a copied activation meets 256 rows.
+// is two 128-row matrices (gate and up of a pair, or two neighbouring row tiles) by 64 to 128 tokens, so that a copied activation meets 256 rows.
 // Roles of a thread block (one an SM, tiles in turn):
 //   warps 0, 1: MMAs, a warp for each matrix.  A stage is 64 of n: four steps of 16 for each part.
 //   warp 2: TMA copies of the stage's parts (128-byte swizzle)
@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t elect_one() {
         : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {     // 32 lanes x 16 columns
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t* r) {     // 32 lanes x 16 columns
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -83,6 +83,12 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {     //
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {            // 32 lanes x 8 columns
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -187,20 +193,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                 if (!ok) return;
                 ++turn[m];
                 tc_fence_after();
-                constexpr int AT_ONCE = NC == 48 ? 48 : 16;                // columns whose loads are in flight together
+                constexpr int AT_ONCE = NC <= 48 ? NC : 16;                // columns whose loads are in flight together
 #pragma unroll
                 for (int c = 0; c < NC; c += AT_ONCE) {
-                    uint32_t v[AT_ONCE / 16][16];
+                    uint32_t v[AT_ONCE];
 #pragma unroll
-                    for (int o = 0; o < AT_ONCE / 16; ++o) ld16(at + static_cast<uint32_t>(m * kDCols + c + 16 * o), v[o]);
+                    for (int o = 0; o < AT_ONCE && c + o < NC; o += 16) {
+                        if (o + 16 <= AT_ONCE && c + o + 16 <= NC) ld16(at + static_cast<uint32_t>(m * kDCols + c + o), v + o);
+                        else ld8(at + static_cast<uint32_t>(m * kDCols + c + o), v + o);
+                    }
                     wait_ld();
-                    if (c + AT_ONCE == NC) {                               // read: the next round may begin
+                    if (c + AT_ONCE >= NC) {                               // read: the next round may begin
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars->accempty[m]);
                     }
 #pragma unroll
-                    for (int i = 0; i < AT_ONCE; ++i) sum[c + i] += __uint_as_float(v[i / 16][i % 16]);
+                    for (int i = 0; i < AT_ONCE; ++i)
+                        if (c + i < NC) sum[c + i] += __uint_as_float(v[i]);
                 }
             };
             // the second matrix's rounds end in the middle of the first one's
@@ -238,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     acc[1][i] = acc[1][HC + i];
                 }
                 __syncwarp();
-                constexpr int G = HC % 16 == 0 ? 4 : 2;
+                constexpr int G = HC % 16 == 0 ? 4 : HC % 8 == 0 ? 2 : 1;
 #pragma unroll 1
                 for (int c = lane >> 3; c < HC; c += 4 * G) {
                     const int tok = tok0 + half * HC + c;
@@ -513,15 +523,18 @@ cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, cudaStream
 constexpr int kSMs = 152;
 
 struct Shape { int bn; Plan p; float us; };
-// Tokens a tile and shares of n, by their cost in microseconds, fitted to calls of 16 to 500 tokens (2560 x 2560, 2560 x 6912, pairs of 6912 x 2560 and
+struct Tile { int tokens; float once[2], stage[2]; };                      // once: linear, pair; a stage: of one part, of two
+// Tokens a tile and shares of n, by their cost in microseconds, fitted to calls of 16 to 517 tokens (2560 x 2560, 2560 x 6912, pairs of 6912 x 2560 and
 // 14336 x 4096): what a tile takes once (start, epilogue), its stages (two parts: the MMAs; one: the weights' way into tensor memory), more
 // tiles an SM, and the shares' sums written and read again.
 Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
     const int tiles = (rows + BM - 1) / BM, nb = n / 128;
     Shape best = {};
-    for (int i = 0; i < 3; ++i) {
-        const int bn = i == 0 ? 128 : i == 1 ? 96 : 64;
-        const float once = i == 0 ? 11.5f : i == 1 ? 9.3f : 7.5f, stage = parts == 1 ? 0.3f : i == 0 ? 0.57f : i == 1 ? 0.45f : 0.35f;
+    static constexpr Tile kTiles[] = {{128, {13.6f, 8.9f}, {0.278f, 0.541f}}, {112, {10.7f, 9.0f}, {0.255f, 0.476f}}, {96, {10.1f, 7.9f}, {0.272f, 0.412f}},
+                                      {80, {9.0f, 8.4f}, {0.256f, 0.354f}}, {64, {7.7f, 6.5f}, {0.278f, 0.346f}}};
+    for (const Tile& tile : kTiles) {
+        const int bn = tile.tokens;
+        const float once = tile.once[pair], stage = tile.stage[parts - 1];
         const int row_tiles = pair ? tiles : (tiles + 1) / 2, tok_tiles = (cols + bn - 1) / bn;
         const long long all = static_cast<long long>(row_tiles) * tok_tiles;
         for (int splits = 1; splits <= 16 && splits <= std::max(1, nb / 2); ++splits) {
@@ -565,6 +578,17 @@ cudaError_t tiles_go(const LinearArgs& a, const Plan& p, const void* parts, cuda
     return launch(linear_join_kernel<PAIR>, static_cast<unsigned>((warps + 7) / 8), 256, 0, s, a, p);
 }
 
+template <bool PAIR>
+cudaError_t tiles_by(const Shape& t, const LinearArgs& a, const void* parts, cudaStream_t s) {
+    switch (t.bn) {
+        case 128: return tiles_go<128, PAIR>(a, t.p, parts, s);
+        case 112: return tiles_go<112, PAIR>(a, t.p, parts, s);
+        case 96: return tiles_go<96, PAIR>(a, t.p, parts, s);
+        case 80: return tiles_go<80, PAIR>(a, t.p, parts, s);
+        default: return tiles_go<64, PAIR>(a, t.p, parts, s);
+    }
+}
+
 }  // namespace
 
 size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts, bool pair) {
@@ -584,8 +608,7 @@ cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s) 
     const cudaError_t e = launch(linear_split_kernel, static_cast<unsigned>(a.cols), kSplitThreads, 0, s, a.act, a.n / 32, a.cols, t.p.parts,
                                  reinterpret_cast<uint32_t*>(work), scale);
     if (e != cudaSuccess) return e;
-    if (pair) return t.bn == 128 ? tiles_go<128, true>(a, t.p, work, s) : t.bn == 96 ? tiles_go<96, true>(a, t.p, work, s) : tiles_go<64, true>(a, t.p, work, s);
-    return t.bn == 128 ? tiles_go<128, false>(a, t.p, work, s) : t.bn == 96 ? tiles_go<96, false>(a, t.p, work, s) : tiles_go<64, false>(a, t.p, work, s);
+    return pair ? tiles_by<true>(t, a, work, s) : tiles_by<false>(t, a, work, s);
 }
 
 }  // namespace gq
