@@ -235,7 +235,7 @@ __device__ __forceinline__ void cluster_sync() {
 // CLUSTER > 1: so many blocks, the parts of a row, are a cluster, whose first joins them
 template <typename T, int kThreads, int CLUSTER>
 __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ? 2 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
-    constexpr int W = Vec<T>::W, UN = kThreads == 128 ? 3 : 2;
+    constexpr int W = Vec<T>::W, UN = 2;
     __shared__ uint64_t found[kFound];
     __shared__ Sums warp_sums[kThreads / 32];
     __shared__ int count, warp_counts[kThreads / 32];
@@ -269,11 +269,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ?
             if (f > least) t.m = f;
             add(t, f, c, far);
         }
-        for (int v = tid; v < vecs; v += UN * kThreads) {
-            uint4 r[UN];
+        uint4 r[UN], ahead[UN];                                            // a step's loads and the next one's
 #pragma unroll
-            for (int i = 0; i < UN; ++i)
-                if (v + i * kThreads < vecs) r[i] = xv[v + i * kThreads];
+        for (int i = 0; i < UN; ++i)
+            if (tid + i * kThreads < vecs) ahead[i] = xv[tid + i * kThreads];
+        for (int v = tid; v < vecs; v += UN * kThreads) {
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                r[i] = ahead[i];
+                if (v + (UN + i) * kThreads < vecs) ahead[i] = xv[v + (UN + i) * kThreads];
+            }
 #pragma unroll
             for (int i = 0; i < UN; ++i) {
                 if (v + i * kThreads >= vecs) break;
@@ -535,7 +540,7 @@ cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
         if (p.splits == 4) return launch(logprobs_kernel<T, 512, 4>, blocks, 512, 4, s, a, 4, part);
         return launch(logprobs_kernel<T, 512, 2>, blocks, 512, 2, s, a, 2, part);
     }
-    // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us); few: the most
+    // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us; with a step's loads ahead 75); few: the most
     // loads in flight for each.
     const cudaError_t e = blocks >= 152 * 8 ? launch(logprobs_kernel<T, 128, 1>, blocks, 128, 1, s, a, p.splits, part)
                                             : launch(logprobs_kernel<T, 512, 1>, blocks, 512, 1, s, a, p.splits, part);
