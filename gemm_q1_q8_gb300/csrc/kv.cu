@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int 
                 if (!on) continue;
                 const float dd = q8_0_scale_fast(amax);
                 int code[4];
-                q8_0_quant4(x, amax, dd, code);
+                q8_0_quant4<false>(x, amax, dd, code);
                 *reinterpret_cast<uint32_t*>(chunk + (is_k ? kv_k_word<HD>(tok, d) : kv_v_word<HD>(tok, d))) = cache_word(code);
                 if ((l & 7) == 0)
                     *reinterpret_cast<uint16_t*>(chunk + (is_k ? kv_ks_offset(HD) : kv_vs_offset(HD)) + kv_scale<HD>(tok, d)) =

@@ -65,24 +65,32 @@ __device__ __forceinline__ float q8_0_scale_fast(float amax) {
     return __fmaf_rn(__fmaf_rn(-127.0f, q, amax), r, q);
 }
 // Four values of a block quantized by the rule of q8_0_quant (round half up of the rounded quotient x / d), without its
-// divisions: x times the approximate reciprocal is within 2^-14 of the quotient, so where it is further than 2^-11 from a tie its nearest integer is the
-// code; the few others (and NaN) are divided.  16 instructions instead of some 80.
+// divisions: the approximate reciprocal is off by at most 2^-23 of itself, so x times it is within 127 * 2^-23 < 2^-16 of the quotient, whose rounding
+// moves it by at most 2^-18: where it is further than 2^-14 from a tie its nearest integer is the code; the few others (and NaN) are divided (of 128
+// values that a warp quantizes at once one in 64 times; with 2^-11 one in 8).  16 instructions instead of some 80.
+// BYTES: only the codes' low bytes are meant.
+template <bool BYTES>
 __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int (&c)[4]) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(dd));
     if (!(dd >= 0x1p-120f)) r = 0.0f;
-    const float magic = 12582912.0f;                                    // 1.5 * 2^23: the sum's low bits are the integer
-    const float x[4] = {v.x, v.y, v.z, v.w};
+    const float2 magic = make_float2(12582912.0f, 12582912.0f);         // 1.5 * 2^23: the sum's low bits are the integer
+    const float2 rr = make_float2(r, r), minus = make_float2(-1.0f, -1.0f);
     bool far = dd >= 0x1p-120f || amax == 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float t = fmaf(x[i], r, magic);
-        c[i] = __float_as_int(t) - __float_as_int(magic);
-        far = far && fabsf(fmaf(x[i], r, magic - t)) <= 0.5f - 0x1p-11f;
+    for (int i = 0; i < 4; i += 2) {
+        const float2 x = i ? make_float2(v.z, v.w) : make_float2(v.x, v.y), t = ffma2(x, rr, magic);
+        const float2 rest = ffma2(x, rr, ffma2(t, minus, magic));
+        c[i] = __float_as_int(t.x) - (BYTES ? 0 : __float_as_int(magic.x));
+        c[i + 1] = __float_as_int(t.y) - (BYTES ? 0 : __float_as_int(magic.x));
+        far = far && fabsf(rest.x) <= 0.5f - 0x1p-14f && fabsf(rest.y) <= 0.5f - 0x1p-14f;
     }
-    if (!far)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = q8_0_quant(x[i], amax, dd);
+    if (!far) {
+        c[0] = q8_0_quant(v.x, amax, dd);
+        c[1] = q8_0_quant(v.y, amax, dd);
+        c[2] = q8_0_quant(v.z, amax, dd);
+        c[3] = q8_0_quant(v.w, amax, dd);
+    }
 }
 
 // Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d

@@ -144,7 +144,7 @@ __device__ __forceinline__ void finish_fours(const LinearArgs& a, float (&y)[4 *
         for (int g = 0; g < G; ++g) {
             const float amax = __uint_as_float(top[g]), dd = q8_0_scale_fast(amax);
             int c[4];
-            q8_0_quant4(make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), amax, dd, c);
+            q8_0_quant4<true>(make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), amax, dd, c);
             if (tok + 4 * g < end && row < a.rows) {
                 uint16_t* p = reinterpret_cast<uint16_t*>(a.blocks + (static_cast<size_t>(tok + 4 * g) * (a.rows / 32) + row / 32) * 34);
                 if (sub == 0) p[0] = __half_as_ushort(__float2half_rn(dd));

@@ -63,7 +63,7 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
     const float dd = q8_0_scale_fast(amax);
     const uint16_t dbits = __half_as_ushort(__float2half_rn(dd));
     int cd[4];
-    q8_0_quant4(y, amax, dd, cd);
+    q8_0_quant4<true>(y, amax, dd, cd);
     const uint32_t word = __byte_perm(__byte_perm(cd[0], cd[1], 0x0040), __byte_perm(cd[2], cd[3], 0x0040), 0x5410);
     const size_t block = row * (a.k / 32) + (i >> 5);
     if (a.act && on) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
         const float ds = f16_to_f32(dbits);
         float pv[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pv[e] = __fmul_rn(ds, static_cast<float>(cd[e]));
+        for (int e = 0; e < 4; ++e) pv[e] = __fmul_rn(ds, static_cast<float>(static_cast<int8_t>(cd[e])));
         uint32_t w[3][4];
 #pragma unroll
         for (int p = 0; p < 3; ++p)
@@ -272,14 +272,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_ke
     }
     // h of four values
     auto join = [&](int i, float4 y, float4 x, float4 g) {
-        y = make_float4(y.x * factor, y.y * factor, y.z * factor, y.w * factor);
+        const float2 f = make_float2(factor, factor), p = make_float2(b.residual_scale, b.residual_scale);
+        float2 lo = fmul2(make_float2(y.x, y.y), f), hi = fmul2(make_float2(y.z, y.w), f);
         if (b.post) {
             const float4 w = load_row4<float, VEC>(b.post, i, k);
-            y = make_float4(y.x * w.x, y.y * w.y, y.z * w.z, y.w * w.w);
+            lo = fmul2(lo, make_float2(w.x, w.y)), hi = fmul2(hi, make_float2(w.z, w.w));
         }
-        if (gr) y = make_float4(g.x * y.x, g.y * y.y, g.z * y.z, g.w * y.w);
-        const float p = b.residual_scale;
-        return make_float4(fmaf(p, x.x, y.x), fmaf(p, x.y, y.y), fmaf(p, x.z, y.z), fmaf(p, x.w, y.w));
+        if (gr) lo = fmul2(make_float2(g.x, g.y), lo), hi = fmul2(make_float2(g.z, g.w), hi);
+        lo = ffma2(p, make_float2(x.x, x.y), lo), hi = ffma2(p, make_float2(x.z, x.w), hi);
+        return make_float4(lo.x, lo.y, hi.x, hi.y);
     };
     auto again = [&](int i) {
         return join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k), gr ? load_row4<T, VEC>(gr, i, k) : make_float4(0.f, 0.f, 0.f, 0.f));
@@ -300,7 +301,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_ke
     auto emit = [&](int i, float4 h) {
         if (a.h) store_row4<T, VEC>(static_cast<T*>(a.h) + row * k, i, k, h);
         const float4 w = load_row4<float, VEC>(a.w, i, k);
-        const float4 z = make_float4(h.x * rstd2 * w.x, h.y * rstd2 * w.y, h.z * rstd2 * w.z, h.w * rstd2 * w.w);
+        const float2 f = make_float2(rstd2, rstd2);
+        const float2 lo = fmul2(fmul2(make_float2(h.x, h.y), f), make_float2(w.x, w.y)), hi = fmul2(fmul2(make_float2(h.z, h.w), f), make_float2(w.z, w.w));
+        const float4 z = make_float4(lo.x, lo.y, hi.x, hi.y);
         if (a.y) store_row4<T, VEC>(static_cast<T*>(a.y) + row * k, i, k, z);
         if (a.act || a.q) quantize4(a, row, i, VEC == 2 || i < k, z);
     };

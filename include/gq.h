@@ -14,7 +14,7 @@
  *    an error, not a dropped tail.
  *  - After GQ_ECUDA, gq_last_cuda_error() returns the cudaError_t of the failed launch (per
  *    calling thread).
- *  - Decode kernels are launched as programmatic dependents of the work before them on the stream:
+ *  - Decode kernels and the products with an epilogue are launched as programmatic dependents of the work before them on the stream:
  *    they may start, and read their weights, before that work has finished, and they wait for it
  *    before they read an activation or write an output.  Weights must therefore not be written by
  *    the immediately preceding launch on the stream if that launch signals programmatic completion
