@@ -68,15 +68,15 @@ __device__ __forceinline__ float q8_0_scale_fast(float amax) {
 // divisions: the approximate reciprocal is off by at most 2^-23 of itself, so x times it is within 127 * 2^-23 < 2^-16 of the quotient, whose rounding
 // moves it by at most 2^-18: where it is further than 2^-14 from a tie its nearest integer is the code; the few others (and NaN) are divided (of 128
 // values that a warp quantizes at once one in 64 times; with 2^-11 one in 8).  16 instructions instead of some 80.
-// BYTES: only the codes' low bytes are meant.
+// BYTES: only the codes' low bytes are meant.  q8_0_codes: false where they have to be divided; zero: the block is.
 template <bool BYTES>
-__device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int (&c)[4]) {
+__device__ __forceinline__ bool q8_0_codes(float4 v, float dd, bool zero, int (&c)[4]) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(dd));
     if (!(dd >= 0x1p-120f)) r = 0.0f;
     const float2 magic = make_float2(12582912.0f, 12582912.0f);         // 1.5 * 2^23: the sum's low bits are the integer
     const float2 rr = make_float2(r, r), minus = make_float2(-1.0f, -1.0f);
-    bool far = dd >= 0x1p-120f || amax == 0.0f;
+    bool far = dd >= 0x1p-120f || zero;
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         const float2 x = i ? make_float2(v.z, v.w) : make_float2(v.x, v.y), t = ffma2(x, rr, magic);
@@ -85,12 +85,15 @@ __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int 
         c[i + 1] = __float_as_int(t.y) - (BYTES ? 0 : __float_as_int(magic.x));
         far = far && fabsf(rest.x) <= 0.5f - 0x1p-14f && fabsf(rest.y) <= 0.5f - 0x1p-14f;
     }
-    if (!far) {
-        c[0] = q8_0_quant(v.x, amax, dd);
-        c[1] = q8_0_quant(v.y, amax, dd);
-        c[2] = q8_0_quant(v.z, amax, dd);
-        c[3] = q8_0_quant(v.w, amax, dd);
-    }
+    return far;
+}
+template <bool BYTES>
+__device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int (&c)[4]) {
+    if (q8_0_codes<BYTES>(v, dd, amax == 0.0f, c)) return;
+    c[0] = q8_0_quant(v.x, amax, dd);
+    c[1] = q8_0_quant(v.y, amax, dd);
+    c[2] = q8_0_quant(v.z, amax, dd);
+    c[3] = q8_0_quant(v.w, amax, dd);
 }
 
 // Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d

@@ -101,6 +101,58 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
     }
 }
 
+// The same of four chunks, i, i + step, ..., of which those below `end` are there, without the operand.  Their chains run beside one another, and of a
+// block's eight lanes two have the scale of each chunk (the maxima meet in halves, quarters and eighths of the lanes), which the others
+// get from them: 4 + 4 shuffles and one scale instead of 12 and four.
+__device__ __forceinline__ void quantize16(const NormArgs& a, size_t row, int i, int step, int end, const float4 (&y)[4]) {
+    const int lane = threadIdx.x & 31, sub = lane & 7;
+    float m[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(fabsf(y[c].x), fabsf(y[c].y)), fmaxf(fabsf(y[c].z), fabsf(y[c].w)));
+    const bool upper = sub & 4, odd = sub & 2;
+    const float m0 = fmaxf(upper ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, upper ? m[0] : m[2], 4));
+    const float m1 = fmaxf(upper ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, upper ? m[1] : m[3], 4));
+    float amax = fmaxf(odd ? m1 : m0, __shfl_xor_sync(0xffffffffu, odd ? m0 : m1, 2));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const float dd = q8_0_scale_fast(amax);                                // of chunk sub / 2
+    const size_t block = row * (a.k / 32) + (i >> 5), apart = step >> 5;
+    if (!(sub & 1) && i + (sub >> 1) * step < end) {
+        const uint16_t bits = __half_as_ushort(__float2half_rn(dd));
+        const size_t mine = block + (sub >> 1) * apart;
+        if (a.act) *reinterpret_cast<uint16_t*>(a.act + mine * 34) = bits;
+        if (a.q) a.d[mine] = bits;
+    }
+    const float sent = amax == 0.0f ? -0.0f : dd;                          // blocks of zeros apart from those whose scale is below f32's range
+    int cd[4][4];
+    bool far[4];
+    float d[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d[c] = __shfl_sync(0xffffffffu, sent, (lane & 24) | 2 * c);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) far[c] = q8_0_codes<true>(y[c], d[c], __float_as_uint(d[c]) == 0x80000000u, cd[c]);
+    if (!(far[0] && far[1] && far[2] && far[3]))
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (!far[c]) {
+                cd[c][0] = q8_0_quant(y[c].x, 1.0f, d[c]);
+                cd[c][1] = q8_0_quant(y[c].y, 1.0f, d[c]);
+                cd[c][2] = q8_0_quant(y[c].z, 1.0f, d[c]);
+                cd[c][3] = q8_0_quant(y[c].w, 1.0f, d[c]);
+            }
+    uint16_t* p = reinterpret_cast<uint16_t*>(a.act + block * 34) + 1 + 2 * sub;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (i + c * step >= end) break;
+        const uint32_t lo = __byte_perm(cd[c][0], cd[c][1], 0x0040), hi = __byte_perm(cd[c][2], cd[c][3], 0x0040);
+        if (a.act) {
+            p[0] = static_cast<uint16_t>(lo);
+            p[1] = static_cast<uint16_t>(hi);
+            p += apart * 17;
+        }
+        if (a.q) *reinterpret_cast<uint32_t*>(a.q + (block + c * apart) * 32 + 4 * sub) = __byte_perm(lo, hi, 0x5410);
+    }
+}
+
 // NV: four-value chunks a thread keeps in registers; a longer row's remaining chunks are read again
 // (through L2) for the outputs.  VEC: rows and outputs allow four-value accesses.
 template <typename T, int NV, bool VEC, int THREADS>
@@ -237,6 +289,41 @@ __device__ __forceinline__ float row_sum(float s, float* part, int tid, int nt) 
 __device__ __forceinline__ float squares(float4 v, float s) { return fmaf(v.w, v.w, fmaf(v.z, v.z, fmaf(v.y, v.y, fmaf(v.x, v.x, s)))); }
 __device__ __forceinline__ float squares_again(float4 v, float s) { return fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, s)))); }
 
+__device__ __forceinline__ float root_of(float s, const NormArgs& a) {
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(a.k)) + a.eps));
+}
+
+// h of four values; factor: block_scale times the first norm's root
+__device__ __forceinline__ float4 join_block(const BlockNormArgs& b, float factor, float4 y, float4 post, float4 x, float4 g) {
+    const float2 f = make_float2(factor, factor), p = make_float2(b.residual_scale, b.residual_scale);
+    float2 lo = fmul2(make_float2(y.x, y.y), f), hi = fmul2(make_float2(y.z, y.w), f);
+    if (b.post) lo = fmul2(lo, make_float2(post.x, post.y)), hi = fmul2(hi, make_float2(post.z, post.w));
+    if (b.gate) lo = fmul2(make_float2(g.x, g.y), lo), hi = fmul2(make_float2(g.z, g.w), hi);
+    lo = ffma2(p, make_float2(x.x, x.y), lo), hi = ffma2(p, make_float2(x.z, x.w), hi);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+// h and z of four values; z
+template <typename T, int VEC>
+__device__ __forceinline__ float4 emit_block(const NormArgs& a, size_t row, int i, float rstd, float4 h, float4 w) {
+    if (a.h) store_row4<T, VEC>(static_cast<T*>(a.h) + row * a.k, i, a.k, h);
+    const float2 f = make_float2(rstd, rstd);
+    const float2 lo = fmul2(fmul2(make_float2(h.x, h.y), f), make_float2(w.x, w.y)), hi = fmul2(fmul2(make_float2(h.z, h.w), f), make_float2(w.z, w.w));
+    const float4 z = make_float4(lo.x, lo.y, hi.x, hi.y);
+    if (a.y) store_row4<T, VEC>(static_cast<T*>(a.y) + row * a.k, i, a.k, z);
+    return z;
+}
+// Of a thread's four chunks
+template <typename T, int VEC, typename W>
+__device__ __forceinline__ void emit_four(const NormArgs& a, size_t row, int i, int step, float rstd, float4 (&v)[4], W weight) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = emit_block<T, VEC>(a, row, i + c * step, rstd, v[c], weight(c));
+    const int end = VEC == 2 ? 0x7fffffff : a.k;
+    if (a.op) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) quantize4(a, row, i + c * step, i + c * step < end, v[c]);
+    } else if (a.act || a.q) quantize16(a, row, i, step, end, v);
+}
+
 template <typename T, int NV, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_kernel(const BlockNormArgs b) {
     __shared__ float part[2][32];
@@ -268,27 +355,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_ke
         for (int c = 0; c < NV; ++c) s = squares(v[c], s);
         if (VEC < 2) for (int c = NV; c < chunks; ++c) s = squares_again(load_row4<T, VEC>(yr, 4 * (c * nt + tid), k), s);
         s = row_sum(s, part[0], tid, nt);
-        factor *= __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
+        factor *= root_of(s, a);
     }
-    // h of four values
-    auto join = [&](int i, float4 y, float4 x, float4 g) {
-        const float2 f = make_float2(factor, factor), p = make_float2(b.residual_scale, b.residual_scale);
-        float2 lo = fmul2(make_float2(y.x, y.y), f), hi = fmul2(make_float2(y.z, y.w), f);
-        if (b.post) {
-            const float4 w = load_row4<float, VEC>(b.post, i, k);
-            lo = fmul2(lo, make_float2(w.x, w.y)), hi = fmul2(hi, make_float2(w.z, w.w));
-        }
-        if (gr) lo = fmul2(make_float2(g.x, g.y), lo), hi = fmul2(make_float2(g.z, g.w), hi);
-        lo = ffma2(p, make_float2(x.x, x.y), lo), hi = ffma2(p, make_float2(x.z, x.w), hi);
-        return make_float4(lo.x, lo.y, hi.x, hi.y);
-    };
+    auto post = [&](int i) { return b.post ? load_row4<float, VEC>(b.post, i, k) : make_float4(0.f, 0.f, 0.f, 0.f); };
     auto again = [&](int i) {
-        return join(i, load_row4<T, VEC>(yr, i, k), load_row4<T, VEC>(xr, i, k), gr ? load_row4<T, VEC>(gr, i, k) : make_float4(0.f, 0.f, 0.f, 0.f));
+        return join_block(b, factor, load_row4<T, VEC>(yr, i, k), post(i), load_row4<T, VEC>(xr, i, k),
+                          gr ? load_row4<T, VEC>(gr, i, k) : make_float4(0.f, 0.f, 0.f, 0.f));
     };
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        v[c] = join(4 * (c * nt + tid), v[c], x[c].get(), g[c].get());
+        v[c] = join_block(b, factor, v[c], post(4 * (c * nt + tid)), x[c].get(), g[c].get());
         s = squares(v[c], s);
     }
     for (int c = NV; c < chunks; ++c) {
@@ -296,15 +373,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_ke
         s = squares_again(again(i), s);
     }
     s = row_sum(s, part[1], tid, nt);
-    const float rstd2 = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, static_cast<float>(k)) + a.eps));
+    const float rstd2 = root_of(s, a);
 
+    if constexpr (NV == 4) {
+        emit_four<T, VEC>(a, row, 4 * tid, 4 * nt, rstd2, v, [&](int c) { return load_row4<float, VEC>(a.w, 4 * (c * nt + tid), k); });
+        return;
+    }
     auto emit = [&](int i, float4 h) {
-        if (a.h) store_row4<T, VEC>(static_cast<T*>(a.h) + row * k, i, k, h);
-        const float4 w = load_row4<float, VEC>(a.w, i, k);
-        const float2 f = make_float2(rstd2, rstd2);
-        const float2 lo = fmul2(fmul2(make_float2(h.x, h.y), f), make_float2(w.x, w.y)), hi = fmul2(fmul2(make_float2(h.z, h.w), f), make_float2(w.z, w.w));
-        const float4 z = make_float4(lo.x, lo.y, hi.x, hi.y);
-        if (a.y) store_row4<T, VEC>(static_cast<T*>(a.y) + row * k, i, k, z);
+        const float4 z = emit_block<T, VEC>(a, row, i, rstd2, h, load_row4<float, VEC>(a.w, i, k));
         if (a.act || a.q) quantize4(a, row, i, VEC == 2 || i < k, z);
     };
 #pragma unroll
