@@ -96,6 +96,36 @@ __device__ __forceinline__ void q8_0_quant4(float4 v, float amax, float dd, int 
     c[3] = q8_0_quant(v.w, amax, dd);
 }
 
+// Four blocks' codes (low bytes), eight lanes a block, each lane with four values y[c] of block c and their largest magnitude m[c]: the maxima (by `most`) meet in
+// halves, quarters and eighths of the lanes, so that two lanes have each scale, which the others get from them: 4 + 4 shuffles and one scale
+// instead of 12 and four, and four chains beside one another.  Returns the scale of block (lane % 8) / 2.
+template <typename F>
+__device__ __forceinline__ float q8_0_four(const float4 (&y)[4], const float (&m)[4], F most, int (&cd)[4][4]) {
+    const int lane = threadIdx.x & 31;
+    const bool upper = lane & 4, odd = lane & 2;
+    const float m0 = most(upper ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, upper ? m[0] : m[2], 4));
+    const float m1 = most(upper ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, upper ? m[1] : m[3], 4));
+    float amax = most(odd ? m1 : m0, __shfl_xor_sync(0xffffffffu, odd ? m0 : m1, 2));
+    amax = most(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const float dd = q8_0_scale_fast(amax), sent = amax == 0.0f ? -0.0f : dd;       // blocks of zeros apart from those whose scale is below f32's range
+    float d[4];
+    bool far[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d[c] = __shfl_sync(0xffffffffu, sent, (lane & 24) | 2 * c);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) far[c] = q8_0_codes<true>(y[c], d[c], __float_as_uint(d[c]) == 0x80000000u, cd[c]);
+    if (!(far[0] && far[1] && far[2] && far[3]))
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (!far[c]) {
+                cd[c][0] = q8_0_quant(y[c].x, 1.0f, d[c]);
+                cd[c][1] = q8_0_quant(y[c].y, 1.0f, d[c]);
+                cd[c][2] = q8_0_quant(y[c].z, 1.0f, d[c]);
+                cd[c][3] = q8_0_quant(y[c].w, 1.0f, d[c]);
+            }
+    return dd;
+}
+
 // Codes in the cache: sign bit and magnitude; four of them as a word, and a word's values times d
 __device__ __forceinline__ uint32_t cache_word(const int (&c)[4]) {
     uint32_t w = 0;

@@ -135,21 +135,41 @@ __device__ __forceinline__ void finish_fours(const LinearArgs& a, float (&y)[4 *
             const float sum = (v[0] + v[1]) + (v[2] + v[3]);
             if (sum != sum) top[g] = 0x7fffffffu;                                 // a NaN, or infinities that make one
         }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-            for (int g = 0; g < G; ++g) top[g] = max(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));   // as bits: NaN above all
         const int sub = lane & 7;
+        auto block = [&](int t) { return reinterpret_cast<uint16_t*>(a.blocks + (static_cast<size_t>(t) * (a.rows / 32) + row / 32) * 34); };
+        if constexpr (G == 4) {
+            float4 v[4];
+            float m[4];
+            int c[4][4];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float amax = __uint_as_float(top[g]), dd = q8_0_scale_fast(amax);
-            int c[4];
-            q8_0_quant4<true>(make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), amax, dd, c);
-            if (tok + 4 * g < end && row < a.rows) {
-                uint16_t* p = reinterpret_cast<uint16_t*>(a.blocks + (static_cast<size_t>(tok + 4 * g) * (a.rows / 32) + row / 32) * 34);
-                if (sub == 0) p[0] = __half_as_ushort(__float2half_rn(dd));
-                p[1 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[0], c[1], 0x0040));
-                p[2 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[2], c[3], 0x0040));
+            for (int g = 0; g < 4; ++g) v[g] = make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), m[g] = __uint_as_float(top[g]);
+            const float dd = q8_0_four(v, m, [](float p, float q) { return __uint_as_float(max(__float_as_uint(p), __float_as_uint(q))); }, c);
+            if (row < a.rows) {
+                if (!(sub & 1) && tok + 2 * sub < end) block(tok + 2 * sub)[0] = __half_as_ushort(__float2half_rn(dd));
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (tok + 4 * g >= end) break;
+                    uint16_t* p = block(tok + 4 * g) + 1 + 2 * sub;
+                    p[0] = static_cast<uint16_t>(__byte_perm(c[g][0], c[g][1], 0x0040));
+                    p[1] = static_cast<uint16_t>(__byte_perm(c[g][2], c[g][3], 0x0040));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int g = 0; g < G; ++g) top[g] = max(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));   // as bits: NaN above all
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float amax = __uint_as_float(top[g]), dd = q8_0_scale_fast(amax);
+                int c[4];
+                q8_0_quant4<true>(make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]), amax, dd, c);
+                if (tok + 4 * g < end && row < a.rows) {
+                    uint16_t* p = block(tok + 4 * g);
+                    if (sub == 0) p[0] = __half_as_ushort(__float2half_rn(dd));
+                    p[1 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[0], c[1], 0x0040));
+                    p[2 + 2 * sub] = static_cast<uint16_t>(__byte_perm(c[2], c[3], 0x0040));
+                }
             }
         }
     }

@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     acc[1][i] = acc[1][HC + i];
                 }
                 __syncwarp();
-                constexpr int G = HC % 16 == 0 ? 4 : HC % 8 == 0 ? 2 : 1;
+                constexpr int G = HC % 16 == 0 || HC % 16 == 12 ? 4 : 2;   // steps of 16 or 8 tokens, the last one's up to four too many without effect
+                const int end = min(a.cols, tok0 + (half + 1) * HC);
 #pragma unroll 1
                 for (int c = lane >> 3; c < HC; c += 4 * G) {
                     const int tok = tok0 + half * HC + c;
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                     if (!PAIR)
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
-                            load_four(a, other + 4 * g, r0, tok + 4 * g, tok + 4 * g < a.cols);
-                            load_four(a, more + 4 * g, r1, tok + 4 * g, tok + 4 * g < a.cols);
+                            load_four(a, other + 4 * g, r0, tok + 4 * g, tok + 4 * g < end);
+                            load_four(a, more + 4 * g, r1, tok + 4 * g, tok + 4 * g < end);
                         }
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
@@ -272,10 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                         }
                     }
                     if constexpr (PAIR) {
-                        finish_fours<true, G>(a, z0, z1, r0, tok, a.cols, lane);
+                        finish_fours<true, G>(a, z0, z1, r0, tok, end, lane);
                     } else {
-                        finish_fours<false, G>(a, z0, other, r0, tok, a.cols, lane);
-                        finish_fours<false, G>(a, z1, more, r1, tok, a.cols, lane);
+                        finish_fours<false, G>(a, z0, other, r0, tok, end, lane);
+                        finish_fours<false, G>(a, z1, more, r1, tok, end, lane);
                     }
                 }
             }

@@ -101,20 +101,14 @@ __device__ __forceinline__ void quantize4(const NormArgs& a, size_t row, int i, 
     }
 }
 
-// The same of four chunks, i, i + step, ..., of which those below `end` are there, without the operand.  Their chains run beside one another, and of a
-// block's eight lanes two have the scale of each chunk (the maxima meet in halves, quarters and eighths of the lanes), which the others
-// get from them: 4 + 4 shuffles and one scale instead of 12 and four.
+// The same of four chunks, i, i + step, ..., of which those below `end` are there, without the operand
 __device__ __forceinline__ void quantize16(const NormArgs& a, size_t row, int i, int step, int end, const float4 (&y)[4]) {
-    const int lane = threadIdx.x & 31, sub = lane & 7;
+    const int sub = threadIdx.x & 7;
     float m[4];
+    int cd[4][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) m[c] = fmaxf(fmaxf(fabsf(y[c].x), fabsf(y[c].y)), fmaxf(fabsf(y[c].z), fabsf(y[c].w)));
-    const bool upper = sub & 4, odd = sub & 2;
-    const float m0 = fmaxf(upper ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, upper ? m[0] : m[2], 4));
-    const float m1 = fmaxf(upper ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, upper ? m[1] : m[3], 4));
-    float amax = fmaxf(odd ? m1 : m0, __shfl_xor_sync(0xffffffffu, odd ? m0 : m1, 2));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const float dd = q8_0_scale_fast(amax);                                // of chunk sub / 2
+    const float dd = q8_0_four(y, m, [](float u, float v) { return fmaxf(u, v); }, cd);
     const size_t block = row * (a.k / 32) + (i >> 5), apart = step >> 5;
     if (!(sub & 1) && i + (sub >> 1) * step < end) {
         const uint16_t bits = __half_as_ushort(__float2half_rn(dd));
@@ -122,23 +116,6 @@ __device__ __forceinline__ void quantize16(const NormArgs& a, size_t row, int i,
         if (a.act) *reinterpret_cast<uint16_t*>(a.act + mine * 34) = bits;
         if (a.q) a.d[mine] = bits;
     }
-    const float sent = amax == 0.0f ? -0.0f : dd;                          // blocks of zeros apart from those whose scale is below f32's range
-    int cd[4][4];
-    bool far[4];
-    float d[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) d[c] = __shfl_sync(0xffffffffu, sent, (lane & 24) | 2 * c);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) far[c] = q8_0_codes<true>(y[c], d[c], __float_as_uint(d[c]) == 0x80000000u, cd[c]);
-    if (!(far[0] && far[1] && far[2] && far[3]))
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (!far[c]) {
-                cd[c][0] = q8_0_quant(y[c].x, 1.0f, d[c]);
-                cd[c][1] = q8_0_quant(y[c].y, 1.0f, d[c]);
-                cd[c][2] = q8_0_quant(y[c].z, 1.0f, d[c]);
-                cd[c][3] = q8_0_quant(y[c].w, 1.0f, d[c]);
-            }
     uint16_t* p = reinterpret_cast<uint16_t*>(a.act + block * 34) + 1 + 2 * sub;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -325,7 +302,7 @@ __device__ __forceinline__ void emit_four(const NormArgs& a, size_t row, int i, 
 }
 
 template <typename T, int NV, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) block_norm_kernel(const BlockNormArgs b) {
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : THREADS == 512 ? 2 : 1) block_norm_kernel(const BlockNormArgs b) {
     __shared__ float part[2][32];
     const NormArgs& a = b.n;
     const int tid = threadIdx.x, nt = blockDim.x, k = a.k;
@@ -406,6 +383,8 @@ cudaError_t block_norm_go(const BlockNormArgs& b, int m, int nt, bool vec, cudaS
     // rows that fill their threads need no checks of bounds, and four blocks of 256 threads an SM then hold enough loads (the same case 109 -> 97 us;
     // three of them 109, 128 threads a row of 8 chunks 107)
     if (vec && nt <= 256 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 256>, b);
+    if constexpr (NV == 4)
+        if (vec && nt <= 512 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 512>, b);
     return vec ? cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 1, 1024>, b) : cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 0, 1024>, b);
 }
 
