@@ -129,6 +129,28 @@ def test_glu_values(gq, m, rows, n, kind):
     check(y, a * b, ta * b.abs() + a.abs() * tb + ta * tb, kind)
 
 
+def hard_blocks(count, seed=0):
+    """`count` values, a multiple of 32, in blocks of ties, of zeros and of sizes over f32's range, in an order that mixes them."""
+    rng = np.random.default_rng(seed)
+    ties = np.concatenate([[127.0], np.arange(31) - 14.5])                # with a scale of one
+    kinds = [ties * 2.0 ** e for e in (0, -100, -119, -121, -126, -133, 118)] + [np.zeros(32), np.where(np.arange(32) % 3, 0.0, -0.0), 2.0 ** -149 * np.arange(32.0)]
+    kinds += [rng.standard_normal(32) * 10.0 ** e for e in (-30, -5, 0, 5, 30)] + [np.where(np.arange(32) == 7, 3e38, 1.0)]
+    return torch.from_numpy(np.concatenate([kinds[i] for i in rng.integers(0, len(kinds), count // 32)]).astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("m", [1, 20, 40, 70, 90, 105, 130, 517])
+def test_blocks_of_hard_values(gq, m):
+    """Activations of zeros leave the bias: ties, zeros and scales out of f16's and f32's normal range, as quantize_q8_0 has them."""
+    rows, n = 6912, 256
+    w, _ = weights(gq, 1, rows, n)
+    act = torch.zeros(m * n // 32 * 34, dtype=torch.uint8, device="cuda")
+    bias = hard_blocks(rows, m)
+    d, q, _ = gq.quantize_q8_0(bias[None].contiguous())
+    blocks = gq.q1_q8_linear(w, act, rows, n, m, bias=bias, q8_0=True).view(m, rows // 32, 34)
+    assert torch.equal(blocks[..., :2].contiguous().view(torch.int16)[..., 0], d.view(1, -1).expand(m, -1))
+    assert torch.equal(blocks[..., 2:].contiguous().view(torch.int8).reshape(m, -1), q.view(1, -1).expand(m, -1))
+
+
 @pytest.mark.parametrize("pair", [False, True])
 @pytest.mark.parametrize("m,rows,n", [(1, 32, 128), (3, 160, 2560), (20, 96, 256), (70, 416, 640), (300, 128, 1152)])
 def test_blocks_are_the_quantizer_on_the_values(gq, m, rows, n, pair):

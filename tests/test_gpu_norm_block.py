@@ -10,7 +10,7 @@ import torch
 
 import workloads as wl
 from tests.gpu_util import need_gpu
-from tests.test_gpu_linear import activations, product, weights
+from tests.test_gpu_linear import activations, hard_blocks, product, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -48,7 +48,7 @@ def exact(y, x, w, post, gate, beta, alpha, eps):
 @pytest.mark.parametrize("m,k,kind,gated", [
     (1, 1, "f32", "row"), (1, 2560, "f32", "none"), (3, 33, "f32", "token"), (5, 31, "bf16", "row"), (2, 4098, "f16", "token"),
     (200, 4096, "f32", "none"), (160, 6912, "bf16", "token"), (153, 960, "f16", "row"), (2, 65536, "f32", "token"),
-    (1, 40001, "f16", "token"), (333, 96, "f32", "row"), (1000, 16384, "bf16", "none")])
+    (1, 40001, "f16", "token"), (333, 96, "f32", "row"), (1000, 16384, "bf16", "none"), (160, 5120, "f32", "row"), (154, 8192, "bf16", "token")])
 def test_values(gq, m, k, kind, gated, post):
     t = TYPES[kind]
     y, x = normal(1, m, k).to(t), (3 * normal(2, m, k)).to(t)
@@ -67,7 +67,7 @@ def test_values(gq, m, k, kind, gated, post):
     assert torch.all((z.double() - want).abs() <= tz + ROUND[kind] * (want.abs() + tz) + TINY[kind])
 
 
-@pytest.mark.parametrize("m,k,kind", [(1, 2560, "f32"), (7, 32, "f32"), (300, 4096, "bf16"), (2, 40960, "f16"), (170, 6912, "f32")])
+@pytest.mark.parametrize("m,k,kind", [(1, 2560, "f32"), (7, 32, "f32"), (300, 4096, "bf16"), (2, 40960, "f16"), (170, 6912, "f32"), (156, 5120, "f16"), (155, 8192, "bf16")])
 def test_q8_0_is_the_quantizer_on_the_norm(gq, m, k, kind):
     t = TYPES[kind]
     y, x, g = normal(1, m, k).to(t), normal(2, m, k).to(t), normal(3, m, k).to(t)
@@ -82,6 +82,23 @@ def test_q8_0_is_the_quantizer_on_the_norm(gq, m, k, kind):
     blocks = act.view(-1, 34)
     assert torch.equal(blocks[:, :2].contiguous().view(torch.int16).flatten(), d.flatten())
     assert torch.equal(blocks[:, 2:].contiguous().view(torch.int8).flatten(), q.flatten())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("m,k", [(2, 4096), (200, 4096), (153, 960), (160, 5120), (154, 8192), (153, 6912), (153, 16384), (2, 65536)])
+def test_blocks_of_hard_values(gq, m, k, kind):
+    """A stream of ones leaves the weight: ties, zeros and scales out of f16's and f32's normal range, as quantize_q8_0 has them."""
+    w = hard_blocks(k, m)
+    one, zero = torch.ones(m, k, device="cuda", dtype=TYPES[kind]), torch.zeros(m, k, device="cuda", dtype=TYPES[kind])
+    d, q, op = gq.quantize_q8_0(w[None].contiguous(), mma_operand=True)
+    d, q = d.view(1, -1).expand(m, -1), q.view(1, -1).expand(m, -1)
+    blocks = gq.rmsnorm_block_q8_0(zero, one, w, eps=0.0).view(m, k // 32, 34)
+    assert torch.equal(blocks[..., :2].contiguous().view(torch.int16)[..., 0], d)
+    assert torch.equal(blocks[..., 2:].contiguous().view(torch.int8).reshape(m, k), q)
+    for operand in (False, True):
+        d2, q2, op2 = gq.rmsnorm_block_q8_0(zero, one, w, eps=0.0, split=True, mma_operand=operand)
+        assert torch.equal(d2, d) and torch.equal(q2, q)
+        assert not operand or torch.equal(op2.view(3, m, k), op.view(3, 1, k).expand(3, m, k))
 
 
 @pytest.mark.parametrize("m,k", [(3, 1024), (400, 1024), (2, 65536)])
