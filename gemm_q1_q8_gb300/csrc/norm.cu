@@ -223,6 +223,8 @@ cudaError_t norm_type(const NormArgs& a, int m, cudaStream_t s) {
 //   n = y * rstd(y) * post (or y);  h = residual_scale * x + block_scale * (gate * n);  z = h * rstd(h) * w
 // (formed as h = fma(residual_scale, x, y * (block_scale * rstd) * post * gate), a rounding a step).
 // One pass as above with two sums a row: y and then h stay in registers.  Bytes: y, x and the gate once, h and z once.
+// Bound by HBM for f32 rows (8192 x 4096 with a gate for each, h and the blocks out: 86 us, 6.6 TB/s), by the instructions and the chain of a row's loads,
+// two sums and outputs for 16 bits (56 us, 5.4 TB/s; with the read back 78 us).  A thread's four chunks are quantized together: 84.5 -> 77.6 us.
 // --------------------------------------------------------------------------------------------
 struct BlockNormArgs {
     NormArgs n;                                       // x: the stream, h, y, act, ...: the outputs; r unused
@@ -380,8 +382,8 @@ cudaError_t block_norm_go(const BlockNormArgs& b, int m, int nt, bool vec, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // rows that fill their threads need no checks of bounds, and four blocks of 256 threads an SM then hold enough loads (the same case 109 -> 97 us;
-    // three of them 109, 128 threads a row of 8 chunks 107)
+    // rows that fill their threads need no checks of bounds, and four blocks of 256 threads an SM (two of 512) then hold enough loads (the same case
+    // 109 -> 97 us; three of them 109, 128 threads a row of 8 chunks 107; 8192 x 5120 without the read back 79 -> 73 us)
     if (vec && nt <= 256 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 256>, b);
     if constexpr (NV == 4)
         if (vec && nt <= 512 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 512>, b);
