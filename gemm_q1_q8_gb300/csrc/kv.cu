@@ -69,7 +69,7 @@ __device__ __forceinline__ void page_group(long long slot, int groups, long long
 // The rows of a token are its q heads, k heads, v heads.  A warp takes rows part * per .. of one token (HD = 64: two at a time), so that
 // a token's position, slot and angles are looked up once for all of them.
 // Every load of a step is issued before any branch on what its rows are, the first step's before the token's position and slot are known.
-// Bound by HBM for many tokens (8192 of 32 + 2 x 8 heads of 128 in f32, with the read of what was written: 84 us, 72% of the measured rate; with the
+// Bound by HBM for many tokens (8192 of 32 + 2 x 8 heads of 128 in f32, with the read of what was written: 80 us, 76% of the measured rate; with the
 // loads in branches 110 us, behind the look-ups 93 us), by the chain of loads for few.
 template <typename T, int HD, int MODE>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a, int parts, int per) {

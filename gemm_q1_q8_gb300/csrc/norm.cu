@@ -3,7 +3,7 @@
 // h = x + r; y = h * rstd * w, rstd = 1 / sqrt(sum h^2 / k + eps); y quantized per 32 values as the library's
 // quantizer does.  One pass over x and r: a thread block per row keeps h in registers between the sum and
 // the outputs, so a value is read once and written once (5 to 13 bytes moved a value, 7 flops and a quantization).  Bound by HBM
-// for many rows (8192 f32 rows of 4096 with residual and sum, and the read back of their blocks: 93 us, 86% of the measured rate), by
+// for many rows (8192 f32 rows of 4096 with residual and sum, and the read back of their blocks: 87 us, 92% of the measured rate), by
 // two dependent round trips and two barriers for one (2560 values, with the read back: 3.2 us).
 #include "layer_ops.cuh"
 
