@@ -85,8 +85,11 @@ __device__ __forceinline__ Sums of_lanes(Sums t, float c, bool far) {
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int W = 4;
-    static __device__ __forceinline__ float largest(const uint4& r) {
-        return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)), max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&r)[N]) {
+        float m = max_nan(max_nan(__uint_as_float(r[0].x), __uint_as_float(r[0].y)), max_nan(__uint_as_float(r[0].z), __uint_as_float(r[0].w)));
+        if (N == 2) m = max_nan(m, max_nan(max_nan(__uint_as_float(r[N - 1].x), __uint_as_float(r[N - 1].y)), max_nan(__uint_as_float(r[N - 1].z), __uint_as_float(r[N - 1].w))));
+        return m;
     }
     static __device__ __forceinline__ float one(const uint4& r, int j) { return __uint_as_float(j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w); }
     static __device__ __forceinline__ void get(const uint4& r, float (&v)[4]) {
@@ -95,11 +98,15 @@ template <> struct Vec<float> {
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int W = 8;
-    static __device__ __forceinline__ float largest(const uint4& r) {             // in packed maxima
-        uint32_t m, n;
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t m;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+        return m;
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&r)[N]) {        // in packed maxima
+        uint32_t m = max2(max2(r[0].x, r[0].y), max2(r[0].z, r[0].w));
+        if (N == 2) m = max2(m, max2(max2(r[N - 1].x, r[N - 1].y), max2(r[N - 1].z, r[N - 1].w)));
         return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
     static __device__ __forceinline__ float one(const uint4& r, int j) {
@@ -117,11 +124,15 @@ template <> struct Vec<__nv_bfloat16> {
 };
 template <> struct Vec<__half> {
     static constexpr int W = 8;
-    static __device__ __forceinline__ float largest(const uint4& r) {             // in packed maxima
-        uint32_t m, n;
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t m;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+        return m;
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&r)[N]) {        // in packed maxima
+        uint32_t m = max2(max2(r[0].x, r[0].y), max2(r[0].z, r[0].w));
+        if (N == 2) m = max2(m, max2(max2(r[N - 1].x, r[N - 1].y), max2(r[N - 1].z, r[N - 1].w)));
         return max_nan(__half2float(__ushort_as_half(static_cast<unsigned short>(m))), __half2float(__ushort_as_half(static_cast<unsigned short>(m >> 16))));
     }
     static __device__ __forceinline__ float one(const uint4& r, int j) {
@@ -232,10 +243,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// CLUSTER > 1: so many blocks, the parts of a row, are a cluster, whose first joins them
+// CLUSTER > 1: so many blocks, the parts of a row, are a cluster, whose first joins them.  Blocks an SM of the small ones: f32 at ten would spill its
+// sums' registers (4096 rows of 49152: nine 132 us, ten 140, eight 146).
 template <typename T, int kThreads, int CLUSTER>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ? 2 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
-    constexpr int W = Vec<T>::W, UN = 2;
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? (sizeof(T) == 4 ? 9 : 10) : CLUSTER > 1 ? 2 : 3) logprobs_kernel(const LogprobArgs a, int splits, int part) {
+    constexpr int W = Vec<T>::W;
     __shared__ uint64_t found[kFound];
     __shared__ Sums warp_sums[kThreads / 32];
     __shared__ int count, warp_counts[kThreads / 32];
@@ -269,35 +281,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ?
             if (f > least) t.m = f;
             add(t, f, c, far);
         }
-        uint4 r[UN], ahead[UN];                                            // a step's loads and the next one's
-#pragma unroll
-        for (int i = 0; i < UN; ++i)
-            if (tid + i * kThreads < vecs) ahead[i] = xv[tid + i * kThreads];
-        for (int v = tid; v < vecs; v += UN * kThreads) {
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                r[i] = ahead[i];
-                if (v + (UN + i) * kThreads < vecs) ahead[i] = xv[v + (UN + i) * kThreads];
-            }
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                if (v + i * kThreads >= vecs) break;
-                const float m = Vec<T>::largest(r[i]);
-                top = max_nan(top, m);
-                // a thread's m stays until a logit is 2^60 times its weight: were it the running maximum, one of a warp's 32 would rise at almost
-                // every one of a row's few steps
-                if ((far ? c * (m - t.m) : fmaf(c, m, -(c * t.m))) > 60.f) rescale(t, m, c, far);
-                if (far) {
+        auto step = [&](const auto& r) {                                   // one or two vectors
+            constexpr int N = sizeof(r) / sizeof(uint4);
+            const float m = Vec<T>::largest(r);
+            top = max_nan(top, m);
+            // a thread's m stays until a logit is 2^60 times its weight: were it the running maximum, one of a warp's 32 would rise at almost
+            // every one of a row's few steps
+            if ((far ? c * (m - t.m) : fmaf(c, m, -(c * t.m))) > 60.f) rescale(t, m, c, far);
+            if (far) {
 #pragma unroll 1
-                    for (int j = 0; j < W; ++j) add(t, Vec<T>::one(r[i], j), c, true);
-                    continue;
-                }
-                // two sums side by side, packed
-                float f[W];
-                Vec<T>::get(r[i], f);
-                const float2 low = make_float2(-(c * t.m), -(c * t.m)), cc = make_float2(c, c);
-                float2 s2 = make_float2(0.f, 0.f), u2 = s2;
-                if (!hidden) {
+                for (int i = 0; i < N; ++i)
+#pragma unroll 1
+                    for (int j = 0; j < W; ++j) add(t, Vec<T>::one(i ? r[N - 1] : r[0], j), c, true);
+                return;
+            }
+            // two sums side by side, packed
+            const float2 low = make_float2(-(c * t.m), -(c * t.m)), cc = make_float2(c, c);
+            float2 s2 = make_float2(0.f, 0.f), u2 = s2;
+            if (!hidden) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float f[W];
+                    Vec<T>::get(r[i], f);
 #pragma unroll
                     for (int j = 0; j < W; j += 2) {
                         const float2 d = ffma2(cc, make_float2(f[j], f[j + 1]), low);
@@ -305,11 +310,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ?
                         s2 = fadd2(s2, e);
                         u2 = ffma2(e, d, u2);
                     }
-                    hidden = u2.x + u2.y != u2.x + u2.y;                   // 0 * inf
                 }
-                if (hidden) {
-                    // a logit of -inf has no weight; rows with one take this way from there on
-                    s2 = u2 = make_float2(0.f, 0.f);
+                hidden = u2.x + u2.y != u2.x + u2.y;                       // 0 * inf
+            }
+            if (hidden) {
+                // a logit of -inf has no weight; rows with one take this way from there on
+                s2 = u2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    float f[W];
+                    Vec<T>::get(r[i], f);
 #pragma unroll
                     for (int j = 0; j < W; j += 2) {
                         float2 d = ffma2(cc, make_float2(f[j], f[j + 1]), low);
@@ -319,9 +329,25 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : CLUSTER > 1 ?
                         u2 = ffma2(e, d, u2);
                     }
                 }
-                t.s += s2.x + s2.y;
-                t.u += u2.x + u2.y;
             }
+            t.s += s2.x + s2.y;
+            t.u += u2.x + u2.y;
+        };
+        // two vectors a step, whose loads are ahead by one; at most one is left
+        uint4 ahead[2];
+        int v = tid;
+        if (v < vecs) ahead[0] = xv[v];
+        if (v + kThreads < vecs) ahead[1] = xv[v + kThreads];
+#pragma unroll 2
+        for (; v + kThreads < vecs; v += 2 * kThreads) {
+            const uint4 r[2] = {ahead[0], ahead[1]};
+            if (v + 2 * kThreads < vecs) ahead[0] = xv[v + 2 * kThreads];
+            if (v + 3 * kThreads < vecs) ahead[1] = xv[v + 3 * kThreads];
+            step(r);
+        }
+        if (v < vecs) {
+            const uint4 r[1] = {ahead[0]};
+            step(r);
         }
         t = of_lanes<32>(t, c, far);
         if (lane == 0) warp_sums[warp] = t;
@@ -540,7 +566,7 @@ cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
         if (p.splits == 4) return launch(logprobs_kernel<T, 512, 4>, blocks, 512, 4, s, a, 4, part);
         return launch(logprobs_kernel<T, 512, 2>, blocks, 512, 2, s, a, 2, part);
     }
-    // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us; with a step's loads ahead 75); few: the most
+    // Many rows: four warps a block, as what a warp does once for a row then counts less (4096 bf16 rows of 49152: 95 -> 79 us; with a step's loads ahead and one check a step 74); few: the most
     // loads in flight for each.
     const cudaError_t e = blocks >= 152 * 8 ? launch(logprobs_kernel<T, 128, 1>, blocks, 128, 1, s, a, p.splits, part)
                                             : launch(logprobs_kernel<T, 512, 1>, blocks, 512, 1, s, a, p.splits, part);
