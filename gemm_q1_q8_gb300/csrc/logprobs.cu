@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, the entropy and the best alternatives of rows of logits.
 //
 //   p = softmax(scale * x);  in powers of two, c = scale * log2(e), t = c (x - max x), s = sum 2^t:
-//   logprob = (t[token] - log2 s) ln 2,  H = (log2 s - (sum 2^t t) / s) ln 2.
+//   logprob = scale (x[token] - max x) - log2(s) ln 2,  H = (log2 s - (sum 2^t t) / s) ln 2.
 // A thread block takes a row, or a part of one where there are few rows: one pass over the logits keeps the largest and the two sums a
 // thread (relative to one of its logits, exchanged where another is far above it).  The k best need no sorting: the k-th largest of the threads' own maxima bounds the
 // k-th largest logit from below, and a search over the bits of an order-preserving key finds it by 16 block-wide counts.  Only the threads whose maximum
@@ -47,9 +47,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 __device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return static_cast<uint64_t>(key) << 32 | (0xffffffffu - index); }
 
-// s = sum 2^t, u = sum 2^t t, m the largest logit or one near it.  Near: t = c x - r with r = c m rounded, one fma, while |r| < 2^20 (r is then off by at most
-// 1/32, the same in every term).  Far: t = c (x - m), for rows whose largest logit is further out, summed once more.
+// s = sum 2^t, u = sum 2^t t, t = c (x - m) with m the largest logit.  A thread first sums relative to a logit near its largest (kRise below).  Near: t = c x - r with
+// r = c m rounded, one fma, while |r| < 2^20 (r is then off by at most 1/32, the same in every term).  Far: t = c (x - m), for rows whose largest logit is further
+// out, summed once more.
 struct Sums { float m, s, u; };
+// A thread's m stays until a logit is further above it.  Were it the running maximum, one of a warp's 32 would rise at almost every one of a row's few
+// steps; but t is rounded relative to its size and u is a difference of what both signs of t give, so with m far below (60 here) what is left
+// of log2 s and the entropy of a row with one likely token is off by 2^-19.  With 8, t of what counts is off by 2^-22 at most.
+constexpr float kRise = 8.f;
 constexpr float kNear = 1048576.f;
 __device__ __forceinline__ bool is_far(float m, float c) { return !(fabsf(c * m) < kNear); }
 __device__ __forceinline__ float floor_of(float c) { return -1.0001f * kNear / c; }            // a first m that is far
@@ -66,13 +71,23 @@ __device__ __forceinline__ void add(Sums& a, float x, float c, bool far) {
     a.s += e;
     a.u = fmaf(e, t, a.u);
 }
+// A thread's sums relative to its largest logit `top`, whose own term is taken out as it was added and becomes exactly 1: with every t at most 0 then, log2 s is not below 0,
+// and a row of one allowed token gives 0.  Where no logit is above `least`, m is that.
+__device__ __forceinline__ void rebase(Sums& a, float top, float least, float c, bool far) {
+    if (top <= least) return;
+    const float t = power(top, a.m, c, far), e = exp2_fast(t), f = exp2_fast(-t);
+    const float s = a.s - e, u = a.u - e * t;                                      // the product as add rounds it for a first term
+    a.u = fmaf(-s, t, u) * f;
+    a.s = fmaf(s, f, 1.f);
+    a.m = top;
+}
 // The sums of a warp's lanes, or of a group's of N: the maximum first, so that each is rescaled once
 template <int N>
-__device__ __forceinline__ Sums of_lanes(Sums t, float c, bool far) {
+__device__ __forceinline__ Sums of_lanes(Sums t, float c) {
     float m = t.m;
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    rescale(t, m, c, far);
+    rescale(t, m, c, true);
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) {
         t.s += __shfl_xor_sync(0xffffffffu, t.s, o);
@@ -150,21 +165,23 @@ template <> struct Vec<__half> {
     }
 };
 
-__device__ __forceinline__ float logprob_of(float x, const Sums& a, float scale, float c) {
+__device__ __forceinline__ float logprob_of(float x, const Sums& a, float scale) {
     if (a.s == 0.f) return x != x ? x : __uint_as_float(0xff800000u);              // nothing has any weight
-    if (is_far(a.m, c) || is_far(x, c)) return scale * (x - a.m) - log2f(a.s) * kLn2;       // beside 2^20 the rounding of r is nothing
-    return (fmaf(c, x, -(c * a.m)) - log2f(a.s)) * kLn2;
+    return scale * (x - a.m) - log2f(a.s) * kLn2;
 }
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, const Sums& t, float c) {
-    if (a.entropy) a.entropy[row] = t.s == 0.f ? 0.f : (log2f(t.s) - t.u / t.s) * kLn2;
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, size_t row, const Sums& t) {
+    if (a.entropy) {
+        const float h = t.s == 0.f ? 0.f : (log2f(t.s) - t.u / t.s) * kLn2;
+        a.entropy[row] = h < 0.f ? 0.f : h;                                       // by its rounding; NaN stays
+    }
     if (a.logprob) {
         const int64_t tok = a.tokens[row];
         float r = 0.f;
         if (tok >= a.vocab) {
             r = __uint_as_float(0x7fffffffu);
             report_error(kErrIndex);
-        } else if (tok >= 0) r = logprob_of(to_f32(static_cast<const T*>(a.x)[row * a.stride + tok]), t, a.scale, c);
+        } else if (tok >= 0) r = logprob_of(to_f32(static_cast<const T*>(a.x)[row * a.stride + tok]), t, a.scale);
         a.logprob[row] = r;
     }
 }
@@ -183,18 +200,17 @@ __device__ __forceinline__ void join_row(const LogprobArgs& a, size_t row, int s
     for (int i = lane; i < splits; i += 32) most = max_nan(most, sums_of(i).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const bool far = is_far(most, c);
     Sums t = {most, 0.f, 0.f};
     for (int i = lane; i < splits; i += 32) {
-        const float4 p = sums_of(i);
-        // a near part's terms are relative to its rounded r
-        const float d = max_nan(power(p.x, most, c, far) - (is_far(p.x, c) ? 0.f : fmaf(c, p.x, -(c * p.x))), -1e4f), f = exp2_fast(d);
-        t.u += fmaf(p.y, d, p.z) * f;
-        t.s += p.y * f;
+        const float4 v = sums_of(i);
+        Sums p = {v.x, v.y, v.z};
+        rescale(p, most, c, true);
+        t.u += p.u;
+        t.s += p.s;
     }
-    t = of_lanes<32>(t, c, far);
+    t = of_lanes<32>(t, c);
     if (tid == 0) {
-        finish_row<T>(a, row, t, c);
+        finish_row<T>(a, row, t);
         *count = 0;
     }
     if (k == 0) return;
@@ -228,7 +244,7 @@ __device__ __forceinline__ void join_row(const LogprobArgs& a, size_t row, int s
         for (int j = 0; j < have; ++j) rank += found[j] > e;
         if (rank < k) {
             a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
-            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
+            a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
         }
     }
 }
@@ -285,9 +301,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? (sizeof(T) == 4 ? 
             constexpr int N = sizeof(r) / sizeof(uint4);
             const float m = Vec<T>::largest(r);
             top = max_nan(top, m);
-            // a thread's m stays until a logit is 2^60 times its weight: were it the running maximum, one of a warp's 32 would rise at almost
-            // every one of a row's few steps
-            if ((far ? c * (m - t.m) : fmaf(c, m, -(c * t.m))) > 60.f) rescale(t, m, c, far);
+            if ((far ? c * (m - t.m) : fmaf(c, m, -(c * t.m))) > kRise) rescale(t, m, c, far);
             if (far) {
 #pragma unroll 1
                 for (int i = 0; i < N; ++i)
@@ -349,11 +363,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? (sizeof(T) == 4 ? 
             const uint4 r[1] = {ahead[0]};
             step(r);
         }
-        t = of_lanes<32>(t, c, far);
+        rebase(t, top, least, c, far);
+        t = of_lanes<32>(t, c);
         if (lane == 0) warp_sums[warp] = t;
         if (tid == 0) count = 0;
         __syncthreads();
-        t = of_lanes<kThreads / 32>(warp_sums[lane % (kThreads / 32)], c, far);
+        t = of_lanes<kThreads / 32>(warp_sums[lane % (kThreads / 32)], c);
     };
     stream(false);
     if (is_far(t.m, c)) {                                                  // the same in every thread
@@ -363,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? (sizeof(T) == 4 ? 
     const uint32_t mine = key_of(top);
     if (tid == 0) {
         if (CLUSTER > 1) own_sums = make_float4(t.m, t.s, t.u, 0.f);
-        else if (splits == 1) finish_row<T>(a, row, t, c);
+        else if (splits == 1) finish_row<T>(a, row, t);
         else part_sums(a.workspace)[blockIdx.x] = make_float4(t.m, t.s, t.u, 0.f);
     }
     auto join = [&] {
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? (sizeof(T) == 4 ? 
             if (CLUSTER > 1) own_best[rank] = e;
             else if (splits == 1) {
                 a.top_ids[row * k + rank] = 0xffffffffu - static_cast<uint32_t>(e);
-                a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale, c);
+                a.top_values[row * k + rank] = logprob_of(value_of(static_cast<uint32_t>(e >> 32)), t, a.scale);
             } else part_best(a.workspace, gridDim.x)[static_cast<size_t>(blockIdx.x) * k + rank] = e;
         }
     }
