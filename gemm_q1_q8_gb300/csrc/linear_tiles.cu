@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (warp < 2) {
             // ---------------- MMAs: an issuer for each matrix
+            asm volatile("griddepcontrol.wait;" ::: "memory");         // the limit of a wait counts from here, not while earlier work runs
             const int m = warp;
             const uint32_t leader = elect_one();
             const uint32_t d = tmem + static_cast<uint32_t>(m * kDCols);
@@ -390,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tiles_kernel(const __grid_
                             for (int p = 0; p < 16; ++p) av[p] = ((word << (15 - p)) & 0x80008000u) ^ neg;
                         };
                         expand(words[2 * half]);
+                        // the first stages' weights go ahead of earlier work, as the packed weights are no part of it
+                        if (g == kStages) asm volatile("griddepcontrol.wait;" ::: "memory");
                         if (g >= kStages && !__all_sync(0xffffffffu, wait_or_abort_sleep(&bars->done[s], (g / kStages - 1) & 1u, abort))) {
                             live = false;
                             break;
