@@ -695,12 +695,12 @@ FUNCTIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh"
 
 
 def q1_q8_linear_workspace_bytes(rows: int, n: int, cols: int, dtype=torch.float32) -> int:
-    """Bytes of the workspace q1_q8_linear and q1_q8_glu need for these sizes (0: invalid)."""
+    """Bytes of the workspace q1_q8_linear and q1_q8_glu need for these sizes, and for fewer vectors (0: invalid)."""
     return lib().gq_q1_q8_linear_workspace_bytes(rows, n, cols, _TYPES.get(dtype, -1))
 
 
 def q1_q8_linear_workspace(rows: int, n: int, cols: int, dtype=torch.float32, device="cuda") -> torch.Tensor:
-    """A workspace for q1_q8_linear or q1_q8_glu, to be kept between calls (calls sharing it must not overlap)."""
+    """A workspace for q1_q8_linear or q1_q8_glu with up to `cols` vectors, to be kept between calls (calls sharing it must not overlap)."""
     need = q1_q8_linear_workspace_bytes(rows, n, cols, dtype)
     if need == 0:
         raise GQError("q1_q8_linear_workspace: invalid shape")

@@ -354,7 +354,7 @@ int gq_logprobs(const void* logits, long long stride, int type, int m, int vocab
 
 size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type) {
     if (rows < 1 || rows > kMaxRows || n < 128 || n % 128 != 0 || n > gq::kMaxN || cols < 1 || cols > kMaxCols || !type_bytes(type)) return 0;
-    return gq::linear_workspace_bytes(rows, n, cols, type);
+    return gq::linear_workspace_bytes(rows, n, cols);
 }
 
 int q1_q8_linear(const void* packed_w, const void* act, int rows, int n, int cols, const float* bias, int function,

@@ -13,6 +13,7 @@ namespace gq {
 namespace {
 
 constexpr int kBlockRows = 32;
+constexpr int kRowsAlways = 4;                    // tokens for which this kernel is taken: the faster one at every size that was measured
 
 // d = a . b (from zero), then d += a . b
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -227,7 +228,7 @@ cudaError_t launch_linear_rows(const LinearArgs& a, cudaStream_t s) {
 // 400 x 1024, 2560 x 2560, 2560 x 6912 and 14336 x 8192 and the pairs of 6912 x 2560 and 14336 x 4096, in microseconds.
 bool linear_by_rows(int rows, int n, int cols, bool pair, int parts) {
     if (cols > 32) return false;
-    if (cols <= 4) return true;                                               // at every size that was measured
+    if (cols <= kRowsAlways) return true;
     const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
     const float waves = static_cast<float>(((rows + kBlockRows - 1) / kBlockRows + 151) / 152);
     const float us = 1.7f + waves * (0.5f + n * 1e-3f * (0.25f + 0.08f * cols + (pair ? 0.7f : 0.25f) * nt));
@@ -239,13 +240,10 @@ cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s) {
     return pair ? launch_linear_rows<true>(a, s) : launch_linear_rows<false>(a, s);
 }
 
-size_t linear_workspace_bytes(int rows, int n, int cols, int type) {
-    // for either call; bf16 may take one part or, with Q8_0 outputs, two
-    size_t need = 16;
-    for (int pair = 0; pair < 2; ++pair)
-        for (int parts = type == GQ_BF16 ? 1 : 2; parts <= 2; ++parts)
-            if (!linear_by_rows(rows, n, cols, pair, parts)) need = std::max(need, linear_tiles_workspace_bytes(rows, n, cols, parts, pair));
-    return need;
+size_t linear_workspace_bytes(int rows, int n, int cols) {
+    // for either call, any outputs and any count of tokens up to this one
+    if (cols <= kRowsAlways) return 16;
+    return std::max(linear_tiles_workspace_bytes(rows, n, cols, false), linear_tiles_workspace_bytes(rows, n, cols, true));
 }
 
 }  // namespace gq

@@ -524,9 +524,10 @@ cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, cudaStream
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-constexpr int kSMs = 152;
+constexpr int kSMs = 152, kMaxTokens = 128;
 
 struct Shape { int bn; Plan p; float us; };
+int most_splits(int nb) { return std::min(16, std::max(1, nb / 2)); }
 struct Tile { int tokens; float once[2], stage[2]; };                      // once: linear, pair; a stage: of one part, of two
 // Tokens a tile and shares of n, by their cost in microseconds, fitted to calls of 16 to 517 tokens (2560 x 2560, 2560 x 6912, pairs of 6912 x 2560 and
 // 14336 x 4096): what a tile takes once (start, epilogue), its stages (two parts: the MMAs; one: the weights' way into tensor memory), more
@@ -541,7 +542,7 @@ Shape shape_of(int rows, int n, int cols, int parts, bool pair) {
         const float once = tile.once[pair], stage = tile.stage[parts - 1];
         const int row_tiles = pair ? tiles : (tiles + 1) / 2, tok_tiles = (cols + bn - 1) / bn;
         const long long all = static_cast<long long>(row_tiles) * tok_tiles;
-        for (int splits = 1; splits <= 16 && splits <= std::max(1, nb / 2); ++splits) {
+        for (int splits = 1; splits <= most_splits(nb); ++splits) {
             const long long units = all * splits, waves = (units + kSMs - 1) / kSMs;
             if (splits > 1 && units > kSMs) break;                         // shares are for SMs that would be idle
             const float sums = splits == 1 ? 0.f : 0.2f + static_cast<float>(splits) * cols * rows * (pair ? 2 : 1) * 4 * (1 / 2.4e6f);
@@ -595,9 +596,16 @@ cudaError_t tiles_by(const Shape& t, const LinearArgs& a, const void* parts, cud
 
 }  // namespace
 
-size_t linear_tiles_workspace_bytes(int rows, int n, int cols, int parts, bool pair) {
-    const Plan p = shape_of(rows, n, cols, parts, pair).p;
-    const size_t partial = p.splits > 1 ? static_cast<size_t>(p.splits) * (pair ? 2 : 1) * cols * p.pad_rows * 4 : 0;
+// Of a call of up to `cols` tokens: shares are taken for few tokens only, so that fewer tokens may need more than many do.  A call of s > 1 shares has at most
+// kSMs units, so tokens of at most kSMs / (s row_tiles) tiles of up to kMaxTokens.
+size_t linear_tiles_workspace_bytes(int rows, int n, int cols, bool pair) {
+    const long long tiles = (rows + BM - 1) / BM, row_tiles = pair ? tiles : (tiles + 1) / 2;
+    const size_t row_bytes = static_cast<size_t>(tiles) * BM * 4 * (pair ? 2 : 1);         // a token's sums of one share
+    size_t partial = 0;
+    for (int s = 2; s <= most_splits(n / 128) && s * row_tiles <= kSMs; ++s) {
+        const size_t tokens = std::min<long long>(cols, kSMs / (s * row_tiles) * kMaxTokens);
+        partial = std::max(partial, s * tokens * row_bytes);
+    }
     return parts_bytes(n, cols) + up(static_cast<size_t>(cols) * 4) + partial;
 }
 

@@ -447,8 +447,8 @@ enum gq_function {
  *   Outputs, either may be NULL: y_device [cols, rows] of `type`, rows y_stride elements apart (it may be residual_device with the same
  *   stride); blocks_device cols * rows/32 Q8_0 blocks, as the products and gq_dequantize_q8_0 take them, quantized in f32 by
  *   the rule stated at gq_quantize_q8_0 (a block with a NaN has a NaN scale).
- *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's sizes and type (both calls take the same), 16-byte aligned,
- *   overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
+ *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's rows, n and type and its cols or more (both calls take the same, and no
+ *   count of vectors needs more than a larger one), 16-byte aligned, overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
  * Precision: up to 32 tokens a kernel may be taken whose 32-block sums are exact.  The other, for more, holds activations in f16 parts: exact
  *   where they are not below 2^-20 of 128 times their vector's largest scale (there: off by at most 2^-39 of it); rounded to 12 bits where the only
  *   output is bf16.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 128 weights, of 65536 for bf16), everything after them
