@@ -772,7 +772,7 @@ LogProbs = collections.namedtuple("LogProbs", "logprob entropy top_ids top_logpr
 
 
 def logprobs_workspace_bytes(m: int, vocab: int, top: int = 0) -> int:
-    """Bytes of the workspace logprobs needs (0: invalid sizes)."""
+    """Bytes of the workspace logprobs needs for these sizes, and for fewer rows or alternatives (0: invalid sizes)."""
     return lib().gq_logprobs_workspace_bytes(m, vocab, top)
 
 
@@ -780,7 +780,7 @@ _logprobs_bytes = functools.lru_cache(maxsize=4096)(logprobs_workspace_bytes)
 
 
 def logprobs_workspace(m: int, vocab: int, top: int = 0, device="cuda") -> torch.Tensor:
-    """A workspace for logprobs, to be kept between calls (calls sharing it must not overlap)."""
+    """A workspace for logprobs with up to m rows and `top` alternatives, to be kept between calls (calls sharing it must not overlap)."""
     need = logprobs_workspace_bytes(m, vocab, top)
     if need == 0:
         raise GQError("logprobs_workspace: invalid shape")

@@ -547,10 +547,11 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join_kernel(const Logpr
 // Parts of a row, each a block: up to two blocks an SM, of at least 2048 logits.  Up to eight are a cluster and joined there (one launch instead of two: one row of
 // 49152 called from Python 22.7 -> 18.8 us); more, through the workspace, where eight would have long ways of their own on a GPU that is mostly idle.
 struct Parts { int splits; bool cluster; };
+constexpr int kMaxWideRows = 9;                   // rows that may go through the workspace
 Parts parts_of(int m, int vocab) {
     int n = 8;
     while (n > 1 && (m > 2 * 152 / n || vocab / n < 2048)) n /= 2;
-    if (n < 8 || vocab <= 8 * 32768 || m > 9) return {n, n > 1};
+    if (n < 8 || vocab <= 8 * 32768 || m > kMaxWideRows) return {n, n > 1};
     return {std::min(kMaxSplits, std::min(3 * 152 / m, vocab / 16384)), false};
 }
 
@@ -591,9 +592,14 @@ cudaError_t logprobs_type(const LogprobArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Of a call of up to m rows: few rows have more parts than many.
 size_t logprobs_workspace_bytes(int m, int vocab, int top) {
-    const Parts p = parts_of(m, vocab);
-    return p.splits == 1 || p.cluster ? 16 : static_cast<size_t>(m) * p.splits * (16 + 8 * static_cast<size_t>(top));
+    size_t parts = 0;
+    for (int rows = 1; rows <= std::min(m, kMaxWideRows); ++rows) {
+        const Parts p = parts_of(rows, vocab);
+        if (p.splits > 1 && !p.cluster) parts = std::max(parts, static_cast<size_t>(rows) * p.splits);
+    }
+    return parts ? parts * (16 + 8 * static_cast<size_t>(top)) : 16;
 }
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int type, cudaStream_t s) {

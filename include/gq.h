@@ -474,7 +474,7 @@ int q1_q8_glu(const void* packed_gate_device, const void* packed_up_device, cons
  *   logprob both or neither; entropy may be NULL.  A logit of -inf has no weight; a row of nothing else gives -inf for every token and
  *   entropy 0.  A row with NaN or +inf gives NaN (its alternatives in order, NaN first).  No other log probability is above 0 and no
  *   entropy below it; where one token has all the weight both are 0.
- *   workspace_device: gq_logprobs_workspace_bytes(m, vocab, top) bytes, 16-byte aligned, overwritten; calls that share it must not overlap
+ *   workspace_device: gq_logprobs_workspace_bytes(m or more, vocab, top or more) bytes, 16-byte aligned, overwritten; calls that share it must not overlap
  *   on the GPU.  The same inputs give the same bits.
  * Errors: GQ_EINVAL_SHAPE unless 1 <= m <= 2^24, 1 <= vocab <= 2^20, 0 <= top <= min(32, vocab), stride >= vocab, 0 < scale <=
  *         1e30; GQ_EUNSUPPORTED for another type; GQ_EINVAL_PTR for NULL or misaligned pointers or no output; GQ_ECUDA. */

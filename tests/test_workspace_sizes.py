@@ -18,3 +18,13 @@ def test_products(L, rows, n, type_):
     assert all(0 < a <= b for a, b in zip(sizes, sizes[1:]))
     # not much above what the activations' parts take
     assert all(s <= 4 * m * n + 4 * m + 512 + 152 * 2 * 128 * 128 * 4 for m, s in enumerate(sizes[:1299], 1))
+
+
+@pytest.mark.parametrize("vocab", [1, 33, 49152, 262144, 262145, 300001, 600000, 1 << 20])
+def test_log_probabilities(L, vocab):
+    most = min(vocab, 32)
+    tops = [[L.gq_logprobs_workspace_bytes(m, vocab, k) for m in list(range(1, 400)) + [4096, 1 << 24]] for k in range(most + 1)]
+    for sizes in tops:
+        assert all(16 <= a <= b for a, b in zip(sizes, sizes[1:]))
+    for fewer, more in zip(tops, tops[1:]):
+        assert all(a <= b for a, b in zip(fewer, more))
