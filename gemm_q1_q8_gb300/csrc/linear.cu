@@ -32,7 +32,7 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
 // Of a 128-block and 8 tokens: codes in [sub-block][lane][register], 2 KB; scales, [sub-block][token]; the tokens' bytes
 __host__ __device__ constexpr int block_bytes(int nt) { return nt * (2048 + 4 * 8 * 4 + 8 * 136); }
 // Blocks of a segment: up to 209 KB, a multiple of the shares
-__host__ __device__ constexpr int most_blocks(int nt) { return nt == 8 ? 8 : 64 / nt; }
+__host__ __device__ constexpr int most_blocks(int nt) { return 64 / nt; }
 
 template <int NT, bool PAIR, int kShares>
 __global__ void __launch_bounds__(64 * kShares, 8 / kShares) linear_rows_kernel(const LinearArgs a, int segment) {

@@ -384,7 +384,8 @@ cudaError_t block_norm_go(const BlockNormArgs& b, int m, int nt, bool vec, cudaS
     cfg.numAttrs = 1;
     // rows that fill their threads need no checks of bounds, and four blocks of 256 threads an SM (two of 512) then hold enough loads (the same case
     // 109 -> 97 us; three of them 109, 128 threads a row of 8 chunks 107; 8192 x 5120 without the read back 79 -> 73 us)
-    if (vec && nt <= 256 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 256>, b);
+    if constexpr (NV != 8)                                                 // eight chunks a thread are for rows of more than 512 threads
+        if (vec && nt <= 256 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 256>, b);
     if constexpr (NV == 4)
         if (vec && nt <= 512 && b.n.k == 4 * NV * nt) return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 2, 512>, b);
     return vec ? cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 1, 1024>, b) : cudaLaunchKernelEx(&cfg, block_norm_kernel<T, NV, 0, 1024>, b);
