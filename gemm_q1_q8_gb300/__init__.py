@@ -91,6 +91,7 @@ def lib():
             "gq_rmsnorm": (I, [P, LL, P, LL, P, F, I, I, I, P, P, P, P, P, P, P]),
             "gq_rmsnorm_block": (I, [P, LL, P, LL, P, P, LL, F, F, P, F, I, I, I, P, P, P, P, P, P, P]),
             "gq_q1_q8_linear_workspace_bytes": (S, [I, I, I, I]),
+            "gq_q1_q8_linear_plan": (I, [I, I, I, I, I, I]),
             "q1_q8_linear": (I, [P, P, I, I, I, P, I, P, LL, I, P, LL, P, P, P]),
             "q1_q8_glu": (I, [P, P, P, I, I, I, P, P, I, I, P, LL, P, P, P]),
             "gq_logprobs_workspace_bytes": (S, [I, I, I]),

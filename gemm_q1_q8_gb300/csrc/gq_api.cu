@@ -357,6 +357,11 @@ size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type) {
     return gq::linear_workspace_bytes(rows, n, cols);
 }
 
+int gq_q1_q8_linear_plan(int rows, int n, int cols, int type, int q8_0, int pair) {
+    if (!gq_q1_q8_linear_workspace_bytes(rows, n, cols, type)) return -1;
+    return gq::linear_plan(rows, n, cols, type == GQ_BF16 && !q8_0 ? 1 : 2, pair != 0);
+}
+
 int q1_q8_linear(const void* packed_w, const void* act, int rows, int n, int cols, const float* bias, int function,
                  const void* residual, long long residual_stride, int type, void* y, long long y_stride, void* blocks,
                  void* workspace, gq_stream_t stream) {

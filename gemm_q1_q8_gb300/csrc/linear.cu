@@ -240,6 +240,10 @@ cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s) {
     return pair ? launch_linear_rows<true>(a, s) : launch_linear_rows<false>(a, s);
 }
 
+int linear_plan(int rows, int n, int cols, int parts, bool pair) {
+    return linear_by_rows(rows, n, cols, pair, parts) ? 0 : linear_tiles_plan(rows, n, cols, parts, pair);
+}
+
 size_t linear_workspace_bytes(int rows, int n, int cols) {
     // for either call, any outputs and any count of tokens up to this one
     if (cols <= kRowsAlways) return 16;

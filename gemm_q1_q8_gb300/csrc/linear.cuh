@@ -34,6 +34,8 @@ struct LinearArgs {
 
 cudaError_t launch_linear(const LinearArgs& a, bool pair, cudaStream_t s);
 size_t linear_workspace_bytes(int rows, int n, int cols);
+int linear_plan(int rows, int n, int cols, int parts, bool pair);
+int linear_tiles_plan(int rows, int n, int cols, int parts, bool pair);
 cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s);
 size_t linear_tiles_workspace_bytes(int rows, int n, int cols, bool pair);
 float linear_tiles_us(int rows, int n, int cols, int parts, bool pair);

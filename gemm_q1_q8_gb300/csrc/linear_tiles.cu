@@ -609,6 +609,11 @@ size_t linear_tiles_workspace_bytes(int rows, int n, int cols, bool pair) {
     return parts_bytes(n, cols) + up(static_cast<size_t>(cols) * 4) + partial;
 }
 
+int linear_tiles_plan(int rows, int n, int cols, int parts, bool pair) {
+    const Shape t = shape_of(rows, n, cols, parts, pair);
+    return t.bn + 256 * t.p.splits;
+}
+
 float linear_tiles_us(int rows, int n, int cols, int parts, bool pair) { return shape_of(rows, n, cols, parts, pair).us; }
 
 cudaError_t launch_linear_tiles(const LinearArgs& a, bool pair, cudaStream_t s) {

@@ -458,6 +458,9 @@ enum gq_function {
  *         blocks_device with rows % 32 != 0; GQ_EUNSUPPORTED for another type or function; GQ_EINVAL_PTR for NULL or misaligned pointers (packed weights
  *         and workspace 16 bytes, others their elements), no output, or y_device = residual_device with another stride; GQ_ECUDA. */
 size_t gq_q1_q8_linear_workspace_bytes(int rows, int n, int cols, int type);   /* 0 for invalid sizes */
+/* The kernel that such a call takes, for tests and measurements: 0 the one for few vectors, otherwise vectors a tile + 256 * shares of n
+ * (-1 for invalid sizes).  q8_0: whether blocks_device is asked for; pair: whether the call is q1_q8_glu. */
+int gq_q1_q8_linear_plan(int rows, int n, int cols, int type, int q8_0, int pair);
 int q1_q8_linear(const void* packed_w_device, const void* act_device, int rows, int n, int cols, const float* bias_device,
                  int function, const void* residual_device, long long residual_stride, int type, void* y_device,
                  long long y_stride, void* blocks_device, void* workspace_device, gq_stream_t stream);
