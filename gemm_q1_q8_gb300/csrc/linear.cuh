@@ -45,7 +45,9 @@ namespace {
 // f16 parts that an activation takes
 __host__ __device__ __forceinline__ int linear_parts(const LinearArgs& a) { return a.type == GQ_BF16 && !a.blocks ? 1 : 2; }
 
-// 1 / (1 + e^-v); the exponential of 2^-v log2(e) and the reciprocal are off by two units each, and give 0 below 2^-126
+// 1 / (1 + e^-v); the exponential of 2^-v log2(e) and the reciprocal are off by two units each, and give 0 below 2^-126.  The exponent's product is rounded once and its
+// factor by a quarter of a unit, so e^-v is off by |v| 2^-23 of itself too: at -20, where the result is 2e-9, by 2e-6 of it (outputs of
+// 16 or 8 bits keep none of that, and a second term of the product would cost every value three instructions).
 __device__ __forceinline__ float sigmoid_of(float v) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504f));

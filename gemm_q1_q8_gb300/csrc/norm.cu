@@ -224,7 +224,7 @@ cudaError_t norm_type(const NormArgs& a, int m, cudaStream_t s) {
 // (formed as h = fma(residual_scale, x, y * (block_scale * rstd) * post * gate), a rounding a step).
 // One pass as above with two sums a row: y and then h stay in registers.  Bytes: y, x and the gate once, h and z once.
 // Bound by HBM for f32 rows (8192 x 4096 with a gate for each, h and the blocks out: 86 us, 6.6 TB/s), by the instructions and the chain of a row's loads,
-// two sums and outputs for 16 bits (56 us, 5.4 TB/s; with the read back 78 us).  A thread's four chunks are quantized together: 84.5 -> 77.6 us.
+// two sums and outputs for 16 bits (57 us, 5.3 TB/s; with the read back 76 to 78 us).  A thread's four chunks are quantized together: 84.5 -> 77.6 us.
 // --------------------------------------------------------------------------------------------
 struct BlockNormArgs {
     NormArgs n;                                       // x: the stream, h, y, act, ...: the outputs; r unused

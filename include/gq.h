@@ -447,13 +447,17 @@ enum gq_function {
  *   Outputs, either may be NULL: y_device [cols, rows] of `type`, rows y_stride elements apart (it may be residual_device with the same
  *   stride); blocks_device cols * rows/32 Q8_0 blocks, as the products and gq_dequantize_q8_0 take them, quantized in f32 by
  *   the rule stated at gq_quantize_q8_0 (a block with a NaN has a NaN scale).
- *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's rows, n and type and its cols or more (both calls take the same, and no
- *   count of vectors needs more than a larger one), 16-byte aligned, overwritten; calls that share it must not overlap on the GPU.  Nothing of it is kept between calls.
+ *   workspace_device: gq_q1_q8_linear_workspace_bytes(...) bytes for the call's rows, n and type and its cols or more (both calls take the same,
+ *   and no count of vectors needs more than a larger one), 16-byte aligned, overwritten; calls that share it must not overlap on the GPU.  Nothing
+ *   of it is kept between calls.
+ * For one vector without function and residual q1_q8_gemv is the faster call (2560 x 6912: 4.0 us, q1_q8_linear 5.8; 6912 x 2560: 3.0 and
+ *   4.8; two of them and q1_q8_glu: 5.9 and 7.6).
  * Precision: up to 32 tokens a kernel may be taken whose 32-block sums are exact.  The other, for more, holds activations in f16 parts: exact
  *   where they are not below 2^-20 of 128 times their vector's largest scale (there: off by at most 2^-39 of it); rounded to 12 bits where the only
  *   output is bf16.  Products are exact, sums f32 (the tensor cores truncate the sums of up to 128 weights, of 65536 for bf16), everything after them
- *   f32, rounded once.  The same inputs give the same bits.  A vector with a scale that is not finite gives no numbers, and leaves the others as
- *   they are.
+ *   f32, rounded once; SiLU and the tanh form of GELU are off by up to (4 + 2 |their exponent|) 2^-22 of themselves.  The same inputs give the same
+ *   bits.  A vector's last bits may change with the number of vectors, which chooses the kernel, its tile and its shares (where the only output is
+ *   bf16, by those 12 bits).  A vector with a scale that is not finite gives no numbers, and leaves the others as they are.
  * Errors: GQ_EINVAL_SHAPE if rows < 1, rows > 2^30, n < 128, n % 128 != 0, n > 2^20, cols < 1, cols > 2^20, a stride < rows or
  *         blocks_device with rows % 32 != 0; GQ_EUNSUPPORTED for another type or function; GQ_EINVAL_PTR for NULL or misaligned pointers (packed weights
  *         and workspace 16 bytes, others their elements), no output, or y_device = residual_device with another stride; GQ_ECUDA. */
